@@ -58,7 +58,7 @@ OUT_TYPE = {GEMM_F32: "f32", GEMM_F16_F32: "f32", GEMM_BF16_F32: "f32",
             GEMM_F16_F16: "f16", GEMM_BF16_BF16: "bf16"}
 
 EXPORTS = ("gemm", "gemm_ex", "gemm_host", "gemm_noalloc", "gemm_tune", "gemm_tune_reset",
-           "softmax_rows", "gemm_strerror", "gemm_check_device_error", "gemm_device_checks",
+           "softmax_rows", "gemm_grouped", "gemm_grouped_k", "gemm_lora", "gemm_strerror", "gemm_check_device_error", "gemm_device_checks",
            "gemm_release_workspace", "gemm_launch_count", "gemm_set_option", "gemm_get_option")
 
 _lock = threading.Lock()
@@ -94,6 +94,14 @@ def load(path: str = LIB_PATH):
         lib.gemm_tune_reset.restype, lib.gemm_tune_reset.argtypes = None, []
         lib.softmax_rows.restype = ci
         lib.softmax_rows.argtypes = [i64, i64, vp, i64, vp, i64, vp]
+        epi = ctypes.POINTER(GemmEpilogue)
+        lib.gemm_grouped.restype = ci
+        lib.gemm_grouped.argtypes = [i64] * 4 + [vp, vp, i64, vp, i64, i64, ci, vp, i64, ci, epi, vp]
+        lib.gemm_grouped_k.restype = ci
+        lib.gemm_grouped_k.argtypes = [i64] * 4 + [vp, vp, i64, vp, i64, vp, i64, i64, ci, epi, vp]
+        lib.gemm_lora.restype = ci
+        lib.gemm_lora.argtypes = [i64] * 5 + [vp, i64, vp, i64, ci, vp, vp, vp, vp, vp, i64, ci,
+                                              epi, vp]
         lib.gemm_strerror.restype, lib.gemm_strerror.argtypes = ctypes.c_char_p, [ci]
         lib.gemm_check_device_error.restype = ci
         lib.gemm_check_device_error.argtypes = [vp]
@@ -179,6 +187,35 @@ def gemm_tune_reset() -> None:
 def softmax_rows(M, N, x, ldx, y, ldy, stream=None) -> int:
     """Row softmax of an fp32 matrix over thread-block clusters; see gemm.h."""
     return load().softmax_rows(M, N, _ptr(x), ldx, _ptr(y), ldy, _stream(stream))
+
+
+def gemm_grouped(G, M, N, K, offsets, A, lda, B, ldb, strideb, b_major, C, ldc, dtype,
+                 alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE, stream=None) -> int:
+    """C[t] = act(alpha * A[t] B_g^T + beta * C[t] + bias[g]) for the rows t of each
+    group g (limits in the device array `offsets`); see include/gemm.h."""
+    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
+    return load().gemm_grouped(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, strideb,
+                               b_major, _ptr(C), ldc, dtype, ctypes.byref(epi), _stream(stream))
+
+
+def gemm_grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype,
+                   alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE, stream=None) -> int:
+    """C_g = act(alpha * sum over group g's rows t of A[t]^T B[t] + beta * C_g + bias[g])
+    (the weight gradient of gemm_grouped); see include/gemm.h."""
+    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
+    return load().gemm_grouped_k(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, _ptr(C),
+                                 ldc, stridec, dtype, ctypes.byref(epi), _stream(stream))
+
+
+def gemm_lora(M, N, K, L, R, A, lda, B, ldb, b_major, adapter, lora_a, lora_b, scale, C, ldc,
+              dtype, alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE,
+              stream=None) -> int:
+    """C = act(alpha * (A B^T + T LB_a) + beta * C + bias), T = scale[a] * A LA_a^T with
+    a = adapter[t] for each row t; see include/gemm.h."""
+    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
+    return load().gemm_lora(M, N, K, L, R, _ptr(A), lda, _ptr(B), ldb, b_major, _ptr(adapter),
+                            _ptr(lora_a), _ptr(lora_b), _ptr(scale), _ptr(C), ldc, dtype,
+                            ctypes.byref(epi), _stream(stream))
 
 
 def gemm_strerror(status: int) -> str:

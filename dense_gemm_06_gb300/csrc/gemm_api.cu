@@ -34,7 +34,7 @@ constexpr int kMaxDevices = 64;
 
 // Per-device error word written by kernels that give up on a wait (the
 // largest generation of a launch whose wait ran out; see internal.h).
-__device__ ErrWord g_err_word;
+__device__ ErrWord g_err_word[2];  // [0] timeouts, [1] bad values in device memory
 __device__ unsigned long long g_check_word;  // first failed device-side check (debug build)
 std::atomic<ErrWord> g_generation{1};
 
@@ -642,6 +642,13 @@ int check_word_address(unsigned long long** out) {
     return kOk;
 }
 
+int current_device_info(DeviceInfo** out, cudaMemPool_t* pool) {
+    return current_device(out, pool);
+}
+
+uint64_t option_wait_limit_ns() { return g_wait_limit_ns.load(); }
+int option_tc_fault_inject() { return g_fault_inject.load(); }
+
 ErrWord next_generation() { return g_generation.fetch_add(1, std::memory_order_relaxed); }
 
 TcLaunch resolve_tc_options(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -1061,18 +1068,18 @@ int gemm_check_device_error(void* stream) {
         cudaGetLastError();
         return kCuda;
     }
-    ErrWord word = 0;
-    if (cudaMemcpy(&word, dev->err_word, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    ErrWord word[2] = {0, 0};
+    if (cudaMemcpy(word, dev->err_word, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) {
         cudaGetLastError();
         return kCuda;
     }
-    if (word == 0) return kOk;
-    const ErrWord zero = 0;
-    if (cudaMemcpy(dev->err_word, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
+    if (word[0] == 0 && word[1] == 0) return kOk;
+    const ErrWord zero[2] = {0, 0};
+    if (cudaMemcpy(dev->err_word, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
         cudaGetLastError();
         return kCuda;
     }
-    return kTimeout;
+    return word[0] != 0 ? kTimeout : kInvalidArg;
 }
 
 int gemm_device_checks(void* stream, uint64_t* first) {

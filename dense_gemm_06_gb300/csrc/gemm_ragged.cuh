@@ -1,0 +1,1017 @@
+// gemm_ragged.cuh -- the tcgen05 kernel of the products whose sizes live in
+// device memory: gemm_grouped, gemm_grouped_k and the two launches of
+// gemm_lora (see gemm_ragged.cu for the mathematics and the design).
+//
+// One orientation serves all four: the MMA's M side (128 TMEM lanes per CTA)
+// is the feature side P -- the weights -- and its N side the row side Q -- the
+// tokens --, so that a unit of work is as wide as it has rows, in steps of 16
+// (32 for a CTA pair). A group of 40 rows costs 48 columns, not a 128-row tile.
+#pragma once
+
+#include "gemm_tc.cuh"
+
+namespace libgemm {
+
+enum RaggedMode {
+    kRagRows = 0,    // groups of rows, a weight matrix each        (gemm_grouped)
+    kRagDepth = 1,   // groups of the summed dimension              (gemm_grouped_k)
+    kRagShrink = 2,  // T = scale * X LA^T of a row tile's adapters (gemm_lora, 1st launch)
+    kRagLora = 3,    // X W^T + T LB                                (gemm_lora, 2nd launch)
+};
+
+// Tensor maps by use. P operands are 3-D (group or adapter number last).
+enum RaggedMap {
+    kMapP = 0,    // weights / B of the depth product / LA
+    kMapQ = 1,    // rows, a full unit's share per box
+    kMapQ16 = 2,  // rows, 16 per box (units narrower than the tile)
+    kMapP8 = 2, kMapQ8 = 3, kMapP1 = 4, kMapQ1 = 5,  // depth: 8- and 1-row boxes of the tail
+    kMapLB = 3,   // lora: LB
+    kMapT = 4, kMapT16 = 5,  // lora: T, as Q and Q16
+    kRaggedMaps = 6
+};
+
+struct RaggedParams {
+    CUtensorMap map[kRaggedMaps];
+    const int32_t* offsets;  // rows, depth: G + 1 group limits
+    int G;
+    int rows;       // rows of C (depth: of each C_g)
+    int feats;      // columns of C (shrink: of LB)
+    int depth;      // depth: rows of A and B, over which the groups are
+    int num_kb;     // 64-deep k-blocks (depth: per group, from the offsets)
+    int tile_w;     // rows of a full unit
+    int tiles_f;    // feature tiles
+    int tiles_r;    // row tiles (depth: per group; shrink: 128-row tiles)
+    int split;      // CTAs that share a unit's depth (a cluster; one CTA per unit side)
+    void* C;
+    int64_t ldc;
+    int64_t stridec;  // depth: between the C_g
+    EpiParams epi;
+    // gemm_lora
+    const int32_t* adapter;  // adapter number of each row
+    const float* scale;      // one factor per adapter, or null
+    const void* lora_b;      // LB as the kernels read it, row pitch ldlb
+    int64_t ldlb;
+    int L, R, slot;          // adapters, rank, lanes per adapter (16, 32, 64 or 128)
+    int list_w;              // rows that share one list of adapters (the expand's tile_w)
+    int chains;              // shrink: clusters that share a row tile's lists of lanes
+    int32_t* lists;          // per list tile: n, list_w adapter numbers, list_w slots, flags
+    int list_pitch, flags;
+    void* T;                 // hi | lo halves of T, 64 elements per 32 lanes
+    int64_t ldt;
+    int pdl;                 // host only
+    ErrWord* err;
+    unsigned long long* check;
+    ErrWord gen;
+    unsigned long long wait_limit_ns;
+    int fault_inject;
+};
+
+// Launchers, one per element type (gemm_ragged_<in>_<out>.cu, gemm_lora_<t>.cu).
+// cg: CTAs per unit; p_mn: the weights' features are contiguous.
+int launch_ragged_f16_f32(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                          const DeviceInfo& dev, cudaStream_t s);
+int launch_ragged_bf16_f32(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                           const DeviceInfo& dev, cudaStream_t s);
+int launch_ragged_f16_f16(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                          const DeviceInfo& dev, cudaStream_t s);
+int launch_ragged_bf16_bf16(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                            const DeviceInfo& dev, cudaStream_t s);
+int launch_lora_f16(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                    const DeviceInfo& dev, cudaStream_t s);
+int launch_lora_bf16(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                     const DeviceInfo& dev, cudaStream_t s);
+
+namespace {
+
+// The ring: 128 features and up to 128 rows of 64 k each per CTA and stage.
+struct RCfg {
+    static constexpr int P_BYTES = 128 * BK * 2;
+    static constexpr int Q_BYTES = 128 * BK * 2;
+    static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+    static constexpr int STAGES = 6;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    // shrink: ids[256], slots[256], first[256], warp sums[16] of the row tile's list
+    static constexpr int LIST_BYTES = 4096;
+    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts
+    static constexpr int NUM_BARS = 2 * STAGES + 8;
+    static constexpr int SMEM_BYTES = RING_BYTES + LIST_BYTES + NUM_BARS * 8 + 16 + 1024;
+    static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
+};
+constexpr int EXT_K = 32;  // lanes of T (rows of LB) per extension block: hi | lo fill 64
+
+// One unit of work: `width` rows of C from row0 (those before row_end are
+// stored) by 128 features per CTA from feat0.
+struct RUnit {
+    int g;           // group (weight matrix)
+    int row0, row_end;
+    int feat0;       // first feature of the unit (of the pair)
+    int width;       // MMA N: rows rounded up
+    int k0, nkb;     // depth: first k-row and k-blocks; else 0 and num_kb
+    int k_end;       // depth: the group's last k-row + 1
+    int tile;        // lora: list tile
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+__device__ __forceinline__ int round_width(int rows, int step, int most) {
+    return min(most, (rows + step - 1) / step * step);
+}
+
+// rows mode: finds the group, row tile and feature tile of unit u. The whole
+// warp takes part: a lane holds the limits of four consecutive groups, a scan
+// gives the units before each lane, and 128 groups are searched at a time.
+// Units are asked for in increasing order, so later chunks replace earlier
+// ones. Limits out of [0, M] are clamped and a decreasing pair is an empty
+// group, so no row outside A and C is ever addressed.
+struct RowWalk {
+    int g0, base, total, incl;
+    int off[5];
+
+    __device__ __forceinline__ int units(const RaggedParams& p, int i) const {
+        const int lane = threadIdx.x & 31;
+        const int rows = off[i + 1] - off[i];
+        return g0 + lane * 4 + i < p.G && rows > 0
+                   ? (rows + p.tile_w - 1) / p.tile_w * p.tiles_f : 0;
+    }
+    __device__ __forceinline__ void load(const RaggedParams& p) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int g = min(g0 + lane * 4 + i, p.G);
+            off[i] = clampi(__ldcg(p.offsets + g), 0, p.rows);
+        }
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += units(p, i);
+        incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    __device__ __forceinline__ void start(const RaggedParams& p) {
+        g0 = base = 0;
+        load(p);
+    }
+    template <int CG>
+    __device__ __forceinline__ bool find(const RaggedParams& p, int u, RUnit& un) {
+        while (u >= base + total) {
+            if (g0 + 128 >= p.G) return false;
+            base += total;
+            g0 += 128;
+            load(p);
+        }
+        const int lane = threadIdx.x & 31;
+        const int r = u - base;
+        const int who = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += units(p, i);
+        int rem = r - (incl - mine), g = g0 + lane * 4, lo = off[0], hi = off[1];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int n = units(p, i);
+            if (g == g0 + lane * 4 + i && rem >= n) {
+                rem -= n;
+                ++g;
+                lo = off[i + 1];
+                hi = off[i + 2];
+            }
+        }
+        un.g = __shfl_sync(0xffffffffu, g, who);
+        rem = __shfl_sync(0xffffffffu, rem, who);
+        lo = __shfl_sync(0xffffffffu, lo, who);
+        hi = __shfl_sync(0xffffffffu, hi, who);
+        const TileCoord tc = raster(rem, (hi - lo + p.tile_w - 1) / p.tile_w, p.tiles_f);
+        un.row0 = lo + tc.tm * p.tile_w;
+        un.row_end = hi;
+        un.feat0 = tc.tn * 128 * CG;
+        un.width = round_width(hi - un.row0, 16 * CG, p.tile_w);
+        un.k0 = 0;
+        un.k_end = 0;
+        un.nkb = p.num_kb;
+        un.tile = 0;
+        return true;
+    }
+};
+
+// The units of a role, in order: u = cluster, cluster + clusters, ...
+template <int CG, int MODE>
+struct Units {
+    RowWalk walk;
+    int u, step;
+
+    __device__ __forceinline__ Units(const RaggedParams& p, int cluster, int clusters)
+        : u(cluster), step(clusters) {
+        if constexpr (MODE == kRagRows) walk.start(p);
+    }
+    __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
+        const int t = u;
+        u += step;
+        if constexpr (MODE == kRagRows) {
+            return walk.template find<CG>(p, t, un);
+        } else if constexpr (MODE == kRagDepth) {
+            const int per = p.tiles_r * p.tiles_f;
+            if (t >= p.G * per) return false;
+            un.g = t / per;
+            const TileCoord tc = raster(t - un.g * per, p.tiles_r, p.tiles_f);
+            un.row0 = tc.tm * p.tile_w;
+            un.row_end = p.rows;
+            un.feat0 = tc.tn * 128 * CG;
+            un.width = round_width(p.rows - un.row0, 64 * CG, p.tile_w);
+            un.k0 = clampi(__ldcg(p.offsets + un.g), 0, p.depth);
+            un.k_end = clampi(__ldcg(p.offsets + un.g + 1), un.k0, p.depth);
+            un.nkb = (un.k_end - un.k0 + BK - 1) / BK;
+            un.tile = 0;
+            return true;
+        } else if constexpr (MODE == kRagLora) {
+            if (t >= p.tiles_r * p.tiles_f) return false;
+            const TileCoord tc = raster(t, p.tiles_r, p.tiles_f);
+            un.g = 0;
+            un.tile = tc.tm;
+            un.row0 = tc.tm * p.tile_w;
+            un.row_end = p.rows;
+            un.feat0 = tc.tn * 128 * CG;
+            un.width = round_width(p.rows - un.row0, 16 * CG, p.tile_w);
+            un.k0 = un.k_end = 0;
+            un.nkb = p.num_kb;
+            return true;
+        }
+        return false;
+    }
+};
+
+// shrink: the units of a cluster are the 128-lane parts sg = chain, chain +
+// chains, ... of its row tile's list (lane l of the list: rank index l % slot
+// of its l / slot-th adapter); un.g = sg.
+template <>
+struct Units<1, kRagShrink> {
+    int sg, parts, tile;
+    __device__ __forceinline__ Units(const RaggedParams& p, int cluster, int n)
+        : sg(cluster % p.chains), parts((n * p.slot + 127) / 128), tile(cluster / p.chains) {}
+    __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
+        if (sg >= parts || tile * 128 >= p.rows) return false;
+        un.g = sg;
+        sg += p.chains;
+        un.row0 = tile * 128;
+        un.row_end = p.rows;
+        un.feat0 = 0;
+        un.width = round_width(p.rows - un.row0, 16, p.tile_w);
+        un.k0 = un.k_end = 0;
+        un.nkb = p.num_kb;
+        un.tile = un.row0 / p.list_w;
+        return true;
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ bool nonfinite16(uint32_t w) {
+    constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// One element of C (feature f of row `row`), fused epilogue included.
+template <typename OutT>
+__device__ __forceinline__ void store_c(const RaggedParams& p, OutT* dst, float acc, float bias,
+                                        bool epi) {
+    float x = acc;
+    if (epi) {
+        x *= p.epi.alpha;
+        if (p.epi.beta != 0.f) x = fmaf(p.epi.beta, to_f32(*dst), x);
+        x = activate(x + bias, p.epi.act);
+    }
+    *dst = from_f32<OutT>(x);
+}
+
+// sum_r T[row][r] LB[id][r][f] for a row whose adapter is the s-th of its list
+// (the lanes of `t` are hi | lo halves in blocks of 32); lb points at LB[id][0][f].
+template <typename In>
+__device__ __noinline__ float adapter_part(const In* t, const In* lb, int64_t ldlb, int lane0,
+                                           int rank) {
+    float v = 0.f;
+    for (int r = 0; r < rank; ++r) {
+        const In* tt = t + (lane0 + r) / 32 * 64 + (lane0 + r) % 32;
+        v = fmaf(to_f32(tt[0]) + to_f32(tt[32]), to_f32(lb[r * ldlb]), v);
+    }
+    return v;
+}
+
+// The list of the distinct adapters of a row tile, in order of first use, by
+// all threads of the CTA: ids[list_w] the adapter or -1 of each row, then
+// slots[] each row's place in the list (-1: none), list[] the adapters.
+// Returns their number. (Quadratic in the tile's 256 rows at most: each row
+// looks for its first equal among the earlier ones in shared memory.)
+__device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* ids, int* slots,
+                                         int* list, int* sums) {
+    const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+    int id = -1;
+    if (i < p.list_w && row0 + i < p.rows) {
+        id = __ldcg(p.adapter + row0 + i);
+        if (id >= p.L) {
+            gen_record_timeout(p.err + 1, 1);  // flags the bad value (see internal.h)
+            id = -1;
+        }
+        if (id < 0) id = -1;
+    }
+    if (i < p.list_w) ids[i] = id;
+    __syncthreads();
+    int first = i;
+    if (id >= 0)
+        for (int j = 0; j < i; ++j)
+            if (ids[j] == id) {
+                first = j;
+                break;
+            }
+    const bool mine = id >= 0 && first == i;
+    const uint32_t b = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) sums[warp] = __popc(b);
+    __syncthreads();
+    int place = __popc(b & ((1u << lane) - 1)), n = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) place += sums[w];
+        n += sums[w];
+    }
+    if (mine) {
+        slots[i] = place;
+        list[place] = id;
+    }
+    __syncthreads();
+    int s = -1;
+    if (id >= 0) s = slots[first];
+    __syncthreads();
+    if (i < p.list_w) slots[i] = s;
+    __syncthreads();
+    return n;
+}
+
+// CG: CTAs per unit (a pair halves P's features and Q's rows between its
+// CTAs). P_MN: P's features are contiguous (weights N-major; always in the
+// depth product). With p.split > 1 (CG == 1) a cluster of `split` CTAs shares
+// each unit: every CTA sums its share of the k-blocks, and the partial sums
+// meet in the shared memory of the CTA that owns the row, in rank order.
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
+__global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
+    using C_ = RCfg;
+    using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr bool Q_MN = MODE == kRagDepth;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+
+    const uint32_t sP0 = base;
+    const uint32_t sQ0 = base + C_::STAGES * C_::P_BYTES;
+    const uint32_t bar0 = base + C_::RING_BYTES + C_::LIST_BYTES;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (C_::STAGES + s); };
+    auto accf_bar = [&](int a) { return bar0 + 8u * (2 * C_::STAGES + a); };
+    auto acce_bar = [&](int a) { return bar0 + 8u * (2 * C_::STAGES + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * C_::STAGES + 4);
+    const uint32_t never_bar = bar0 + 8u * (2 * C_::STAGES + 5);
+    const uint32_t free_bar = bar0 + 8u * (2 * C_::STAGES + 6);   // every CTA's ring is free
+    const uint32_t parts_bar = bar0 + 8u * (2 * C_::STAGES + 7);  // partial sums have arrived
+    int* sm_ids = reinterpret_cast<int*>(smem + C_::RING_BYTES);
+    int* sm_slots = sm_ids + 256;
+    int* sm_list = sm_ids + 512;
+    int* sm_sums = sm_ids + 768;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::RING_BYTES + C_::LIST_BYTES +
+                                                      8 * C_::NUM_BARS);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int S = CG == 1 ? p.split : 1;
+    const uint32_t crank = CG == 2 || S > 1 ? cluster_ctarank() : 0u;
+    const uint32_t rank = CG == 2 ? crank : 0u;   // side of the pair
+    const int part = S > 1 ? (int)crank : 0;      // share of the depth
+    const bool leader = rank == 0;
+    const int per_cluster = CG == 2 ? 2 : S;
+    const int cluster = (int)blockIdx.x / per_cluster;
+    const int nclusters = (int)gridDim.x / per_cluster;
+
+    if constexpr (MODE == kRagShrink) {
+        // Everything before this launch is complete past the wait, and the
+        // expand, which may then start, relies on that: it reads X and W
+        // without waiting for this grid.
+        pdl_wait();
+    }
+    pdl_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        if (MODE == kRagDepth ? p.depth > 0 : p.num_kb > 0) {  // no maps without a depth
+            tma_prefetch_desc(&p.map[kMapP]);
+            tma_prefetch_desc(&p.map[kMapQ]);
+        }
+        for (int s = 0; s < C_::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(accf_bar(a), 1);
+            mbar_init(acce_bar(a), CG * EPI_WARPS);
+        }
+        mbar_init(drain_bar, 1);
+        mbar_init(never_bar, 1);
+        mbar_init(free_bar, S);
+        mbar_init(parts_bar, S * EPI_WARPS);
+        fence_mbarrier_init_cluster();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    int n_list = 0;
+    if constexpr (MODE == kRagShrink) {
+        const int row0 = cluster / p.chains * 128;
+        const int list_tile = row0 / p.list_w;
+        n_list = make_list(p, list_tile * p.list_w, sm_ids, sm_slots, sm_list, sm_sums);
+        if (cluster % p.chains == 0 && part == 0 && row0 % p.list_w == 0) {
+            int32_t* out = p.lists + (int64_t)list_tile * p.list_pitch;
+            if (threadIdx.x == 0) out[0] = n_list;
+            if (threadIdx.x < n_list) out[1 + threadIdx.x] = sm_list[threadIdx.x];
+            if (threadIdx.x < p.list_w) out[1 + p.list_w + threadIdx.x] = sm_slots[threadIdx.x];
+        }
+    }
+    tc_fence_before_sync();
+    if (CG == 2 || S > 1) cluster_sync_all(); else __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+    bool aborted = false;
+    RUnit un;
+    // k-blocks [kb0, kb1) of a unit are this CTA's (all of them but for a split)
+    auto share = [&](int n, int& a, int& b) {
+        a = (int)((int64_t)n * part / S);
+        b = (int)((int64_t)n * (part + 1) / S);
+    };
+    // lora: extension blocks of a unit's list tile; 0 when its flags tell the
+    // epilogue to add the adapters' part itself. `ids`: its adapters.
+    auto ext_blocks = [&](int tile, int& n, const int32_t*& ids) {
+        const int32_t* l = p.lists + (int64_t)tile * p.list_pitch;
+        n = __ldcg(l);
+        ids = l + 1;
+        int bad = 0;
+        for (int i = lane; i < p.flags; i += 32) bad |= __ldcg(l + 1 + 2 * p.list_w + i);
+        if (__any_sync(0xffffffffu, bad != 0)) return 0;
+        return (n * p.slot + EXT_K - 1) / EXT_K;
+    };
+    const int list_arg = MODE == kRagShrink ? n_list : nclusters;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer --
+        if constexpr (MODE == kRagRows || MODE == kRagDepth) pdl_wait();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool waited = false;
+        Units<CG, MODE> units(p, cluster, list_arg);
+        while (units.next(p, un)) {
+            const int q_rows = un.width / CG;
+            const int q_row = un.row0 + (int)rank * q_rows;
+            const int f0 = un.feat0 + (int)rank * 128;
+            int kb0, kb1;
+            share(un.nkb, kb0, kb1);
+            // shrink: the adapters whose lanes this unit holds
+            const int spu = MODE == kRagShrink ? 128 / p.slot : 1;
+            const int s0 = MODE == kRagShrink ? un.g * spu : 0;
+            const int ns = MODE == kRagShrink ? min(spu, n_list - s0) : 1;
+            for (int kb = kb0; kb < kb1 && !aborted; ++kb) {
+                if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
+                const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+                const uint32_t sp = sP0 + stage * C_::P_BYTES;
+                const uint32_t sq = sQ0 + stage * C_::Q_BYTES;
+                if constexpr (MODE == kRagDepth) {
+                    const int k0 = un.k0 + kb * BK;
+                    const int tail = min(BK, un.k_end - k0);
+                    const int nq = q_rows / 64;  // 64-wide chunks of this CTA's rows
+                    if (tail == BK) {
+                        if (elect_one()) {
+                            if (leader)
+                                mbar_arrive_expect_tx(full_bar(stage),
+                                                      (uint32_t)(CG * (2 + nq) * 64 * BK * 2));
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_2d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], fb,
+                                                f0 + 64 * j, k0);
+                            for (int j = 0; j < nq; ++j)
+                                tma_load_2d<CG>(sq + j * 64 * BK * 2, &p.map[kMapQ], fb,
+                                                q_row + 64 * j, k0);
+                        }
+                    } else {
+                        // The group ends inside this block: its last k-rows come in
+                        // boxes of 8 and 1 rows, and the rows up to the next multiple
+                        // of 16 (one MMA step) are zeros, read past the end of the
+                        // matrix: another group's values, which may be infinite or
+                        // NaN, never meet a zero of this one's.
+                        const int n8 = tail / 8, n1 = tail % 8, z1 = n1 ? 8 - n1 : 0;
+                        const int rows16 = (tail + 15) / 16 * 16;
+                        const int pieces = n8 + n1 + z1 + (rows16 - (n8 * 8 + n1 + z1)) / 8;
+                        if (leader && lane == 0)
+                            mbar_arrive_expect_tx(full_bar(stage),
+                                                  (uint32_t)(CG * (2 + nq) * 64 * rows16 * 2));
+                        for (int i = lane; i < pieces * (2 + nq); i += 32) {
+                            const int piece = i % pieces, j = i / pieces;
+                            const bool one = piece >= n8 && piece < n8 + n1 + z1;
+                            const int r = piece < n8 ? piece * 8
+                                          : one      ? n8 * 8 + (piece - n8) : rows16 - 8;
+                            const int y = r < tail ? k0 + r : p.depth;
+                            const bool in_p = j < 2;
+                            const int jj = in_p ? j : j - 2;
+                            const uint32_t dst = (in_p ? sp : sq) +
+                                                 (uint32_t)(jj * 64 * BK * 2 + r * 128);
+                            const CUtensorMap* m = &p.map[in_p ? (one ? kMapP1 : kMapP8)
+                                                               : (one ? kMapQ1 : kMapQ8)];
+                            tma_load_2d<CG>(dst, m, fb, (in_p ? f0 : q_row) + 64 * jj, y);
+                        }
+                    }
+                } else {
+                    const int k0 = kb * BK;
+                    const bool x_ok = device_check(p.check, (k0 & 7) == 0 && (f0 & 7) == 0,
+                                                   kCheckTcTmaX, (unsigned long long)k0);
+                    if (x_ok && elect_one()) {
+                        const int p_bytes = MODE == kRagShrink ? ns * p.slot * BK * 2 : C_::P_BYTES;
+                        if (leader)
+                            mbar_arrive_expect_tx(full_bar(stage),
+                                                  (uint32_t)(CG * (p_bytes + q_rows * BK * 2)));
+                        if constexpr (MODE == kRagShrink) {
+                            for (int j = 0; j < ns; ++j)
+                                tma_load_3d<CG>(sp + j * p.slot * BK * 2, &p.map[kMapP], fb, k0, 0,
+                                                sm_list[s0 + j]);
+                        } else if constexpr (!P_MN) {
+                            tma_load_3d<CG>(sp, &p.map[kMapP], fb, k0, f0, un.g);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], fb,
+                                                f0 + 64 * j, k0, un.g);
+                        }
+                        if (un.width == p.tile_w) {
+                            tma_load_2d<CG>(sq, &p.map[kMapQ], fb, k0, q_row);
+                        } else {
+                            for (int r = 0; r < q_rows; r += 16)
+                                tma_load_2d<CG>(sq + r * 128, &p.map[kMapQ16], fb, k0, q_row + r);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if constexpr (MODE == kRagLora) {
+                // T and the lists are the first launch's: wait for it only here
+                if (!waited) pdl_wait();
+                waited = true;
+                int n;
+                const int32_t* ids;
+                const int ne = ext_blocks(un.tile, n, ids);
+                for (int e = part; e < ne && !aborted; e += S) {
+                    if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
+                    const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+                    const uint32_t sp = sP0 + stage * C_::P_BYTES;
+                    const uint32_t sq = sQ0 + stage * C_::Q_BYTES;
+                    const int k_rows = min(EXT_K, n * p.slot - e * EXT_K);
+                    const int box = min(p.slot, EXT_K);  // LB rows per copy
+                    const int pieces = k_rows / box;
+                    // every lane loads one adapter number, before the elected lane issues
+                    const int my_lane = e * EXT_K + lane * box;
+                    const int my_id = lane < pieces ? __ldcg(ids + my_lane / p.slot) : 0;
+                    const int id0 = __shfl_sync(0xffffffffu, my_id, 0);
+                    const int id1 = __shfl_sync(0xffffffffu, my_id, 1);
+                    if (elect_one()) {
+                        if (leader)
+                            mbar_arrive_expect_tx(
+                                full_bar(stage),
+                                (uint32_t)(CG * (k_rows * 128 * 2 + q_rows * BK * 2)));
+                        for (int i = 0; i < pieces; ++i)
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d<CG>(sp + j * 64 * BK * 2 + i * box * 128,
+                                                &p.map[kMapLB], fb, f0 + 64 * j,
+                                                (e * EXT_K + i * box) % p.slot, i ? id1 : id0);
+                        if (un.width == p.tile_w) {
+                            tma_load_2d<CG>(sq, &p.map[kMapT], fb, e * 64, q_row);
+                        } else {
+                            for (int r = 0; r < q_rows; r += 16)
+                                tma_load_2d<CG>(sq + r * 128, &p.map[kMapT16], fb, e * 64,
+                                                q_row + r);
+                        }
+                    }
+                    __syncwarp();
+                    if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (S > 1) cluster_sync_all();  // the ring held partial sums until here
+        }
+        if (aborted) grace_period_ns(200000);  // let issued copies land
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer --
+        if (leader) {
+            if constexpr (MODE == kRagRows || MODE == kRagDepth) pdl_wait();
+            constexpr uint32_t idesc0 =
+                make_idesc_f16(BF16, P_MN, Q_MN, (uint32_t)(128 * CG), 0u);
+            constexpr uint32_t idesc_ext0 =
+                make_idesc_f16(BF16, true, false, (uint32_t)(128 * CG), 0u);
+            const uint64_t p_mn0 = make_sdesc_sw128(sP0, 64 * BK * 2, 1024);
+            const uint64_t p_desc0 = P_MN ? p_mn0 : make_sdesc_sw128(sP0, 16, 1024);
+            const uint64_t q_desc0 = Q_MN ? make_sdesc_sw128(sQ0, 64 * BK * 2, 1024)
+                                          : make_sdesc_sw128(sQ0, 16, 1024);
+            constexpr int P_STEP = P_MN ? UMMA_K * 128 : UMMA_K * 2;
+            constexpr int Q_STEP = Q_MN ? UMMA_K * 128 : UMMA_K * 2;
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool waited = false;
+            Units<CG, MODE> units(p, cluster, list_arg);
+            while (units.next(p, un)) {
+                const uint32_t width_bits = (uint32_t)(un.width >> 3) << 17;
+                int kb0, kb1, n = 0, ne = 0;
+                share(un.nkb, kb0, kb1);
+                bool issued = false;  // the unit's first MMA overwrites the accumulator
+                bool acc_ready = false;
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+                auto get_acc = [&]() {  // the accumulator, once the unit needs it
+                    if (acc_ready) return true;
+                    acc_ready = true;
+                    if (!wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) return false;
+                    tc_fence_after_sync();
+                    return true;
+                };
+                for (int kb = kb0; kb < kb1 && !aborted; ++kb) {
+                    if (!get_acc() || !wait_bar_warp(full_bar(stage), phase, p)) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t pd = p_desc0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
+                    const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
+                    int steps = BK / UMMA_K;
+                    if constexpr (MODE == kRagDepth)
+                        steps = min(steps, (un.k_end - un.k0 - kb * BK + UMMA_K - 1) / UMMA_K);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < BK / UMMA_K; ++j)
+                            if (MODE != kRagDepth || j < steps)
+                                mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
+                                            qd + (uint64_t)(j * (Q_STEP >> 4)),
+                                            idesc0 | width_bits, issued || j != 0 ? 1u : 0u);
+                        mma_commit<CG>(empty_bar(stage));
+                    }
+                    issued = true;
+                    __syncwarp();
+                    if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if constexpr (MODE == kRagLora) {
+                    if (!waited) pdl_wait();
+                    waited = true;
+                    const int32_t* ids;
+                    ne = ext_blocks(un.tile, n, ids);
+                    for (int e = part; e < ne && !aborted; e += S) {
+                        if (!get_acc() || !wait_bar_warp(full_bar(stage), phase, p)) {
+                            aborted = true;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint64_t pd = p_mn0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
+                        const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
+                        const int steps = min(EXT_K, n * p.slot - e * EXT_K) / UMMA_K;
+                        if (elect_one()) {
+                            // both halves of T against the same rows of LB
+                            for (int j = 0; j < steps; ++j)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (UMMA_K * 128 >> 4)),
+                                                qd + (uint64_t)((j + 2 * h) * (UMMA_K * 2 >> 4)),
+                                                idesc_ext0 | width_bits,
+                                                issued || j + h != 0 ? 1u : 0u);
+                            mma_commit<CG>(empty_bar(stage));
+                        }
+                        issued = true;
+                        __syncwarp();
+                        if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                }
+                if (issued && !aborted) {
+                    if (elect_one()) mma_commit<CG>(accf_bar(acc));
+                    __syncwarp();
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                }
+                if (S > 1) cluster_sync_all();
+            }
+            // Drain: wait (bounded) until every MMA issued above has completed.
+            if (elect_one()) {
+                if constexpr (CG == 2) mma_commit_pair(drain_bar, (uint16_t)1);
+                else mma_commit_local(drain_bar);
+            }
+            __syncwarp();
+            uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp >= EPI_WARP0) {
+        // ------------------------------------------------------ epilogue --
+        const int q = (warp - EPI_WARP0) & 3;
+        const int half = (warp - EPI_WARP0) >> 2;
+        int acc = 0;
+        uint32_t acc_phase = 0, split_phase = 0;
+        pdl_wait();
+        if (p.fault_inject == 1) {
+            if (!__all_sync(0xffffffffu, wait_bar(never_bar, 0u, p))) aborted = true;
+        }
+        if constexpr (MODE == kRagShrink) {
+            // Does an adapter of the list hold an infinity or a NaN in LB? A
+            // zero of T times it would be NaN in the other adapters' rows of the
+            // tile, so the expand then adds this tile's adapters one by one.
+            // The CTAs of a list tile share the scan, which also brings LB into
+            // L2 for the expand.
+            const int subs = (p.list_w + 127) / 128;
+            const int me = ((cluster / p.chains % subs) * p.chains + cluster % p.chains) * S + part;
+            const int ctas = subs * p.chains * S;
+            const int vecs = (p.feats + 7) / 8;  // 16-byte groups per LB row
+            const int64_t total = (int64_t)n_list * p.R * vecs;
+            bool bad = false;
+            for (int64_t i = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32);
+                 i < total; i += (int64_t)ctas * (EPI_WARPS * 32)) {
+                const int v = (int)(i % vecs);
+                const int64_t lr = i / vecs;
+                const int id = sm_list[lr / p.R];
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.lora_b) +
+                    ((int64_t)id * p.R + lr % p.R) * p.ldlb + 8 * v));
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int left = p.feats - 8 * v - 2 * j;  // padding is not looked at
+                    if (left < 2) x[j] = left == 1 ? x[j] & 0xFFFFu : 0u;
+                    bad |= nonfinite16<BF16>(x[j]);
+                }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                int32_t* flag = p.lists + (int64_t)(cluster / p.chains * 128 / p.list_w) *
+                                              p.list_pitch + 1 + 2 * p.list_w;
+                flag[me * EPI_WARPS + (warp - EPI_WARP0)] = bad ? 1 : 0;
+            }
+        }
+        Units<CG, MODE> units(p, cluster, list_arg);
+        while (units.next(p, un)) {
+            int kb0, kb1, n = 0, ne = 0;
+            share(un.nkb, kb0, kb1);
+            bool issued = kb1 > kb0;
+            const int32_t* ids = nullptr;
+            if constexpr (MODE == kRagLora) {
+                ne = ext_blocks(un.tile, n, ids);
+                issued = issued || part < ne;
+            }
+            const bool by_hand = MODE == kRagLora && n > 0 && ne == 0;
+            if (!aborted && issued) {
+                if (!__all_sync(0xffffffffu, wait_bar(accf_bar(acc), acc_phase, p))) aborted = true;
+                tc_fence_after_sync();
+            }
+            const int l = q * 32 + lane;  // TMEM lane
+            const int f = un.feat0 + (int)rank * 128 + l;
+            const int n_rows = min(un.width, un.row_end - un.row0);
+            const bool epi = MODE != kRagShrink && p.epi.active;
+            const bool f_ok = f < p.feats;
+            float bias = 0.f;
+            if (MODE != kRagShrink && epi && p.epi.bias && f_ok)
+                bias = to_f32(static_cast<const OutT*>(p.epi.bias)[(int64_t)un.g * p.feats + f]);
+            OutT* c_col = nullptr;
+            if constexpr (MODE != kRagShrink)
+                c_col = static_cast<OutT*>(p.C) + (int64_t)un.row0 * p.ldc + f +
+                        (MODE == kRagDepth ? (int64_t)un.g * p.stridec : 0);
+            // shrink: this lane's adapter (place in the list, factor) and rank index
+            int slot = 0, r_idx = 0;
+            float factor = 1.f;
+            In* t_col = nullptr;
+            if constexpr (MODE == kRagShrink) {
+                const int ll = un.g * 128 + l;
+                slot = ll / p.slot;
+                r_idx = ll % p.slot;
+                if (slot < n_list && p.scale) factor = p.scale[sm_list[slot]];
+                t_col = static_cast<In*>(p.T) + (int64_t)un.row0 * p.ldt +
+                        (int64_t)(ll / 32) * 64 + lane;
+            }
+            // Row j of the unit, value v of this lane.
+            auto emit = [&](int j, float v) {
+                if constexpr (MODE == kRagShrink) {
+                    if (slot >= n_list) return;
+                    const bool own = sm_slots[un.row0 % p.list_w + j] == slot && r_idx < p.R;
+                    const float t = own ? v * factor : 0.f;
+                    const In hi = from_f32<In>(t);
+                    const float d = t - to_f32(hi);  // infinite or NaN: hi says it all
+                    In* dst = t_col + (int64_t)j * p.ldt;
+                    dst[0] = hi;
+                    dst[32] = from_f32<In>(isfinite(d) ? d : 0.f);
+                } else {
+                    if (!f_ok) return;
+                    if constexpr (MODE == kRagLora) {
+                        if (by_hand) {
+                            const int s = __ldcg(ids + p.list_w + j);
+                            if (s >= 0) {
+                                const int id = __ldcg(ids + s);
+                                v += adapter_part<In>(
+                                    static_cast<const In*>(p.T) + (int64_t)(un.row0 + j) * p.ldt,
+                                    static_cast<const In*>(p.lora_b) +
+                                        (int64_t)id * p.R * p.ldlb + f,
+                                    p.ldlb, s * p.slot, p.R);
+                            }
+                        }
+                    }
+                    OutT* dst = c_col + (int64_t)j * p.ldc;
+                    if (device_check(p.check, un.row0 + j >= 0 && un.row0 + j < p.rows,
+                                     kCheckTcStore, (unsigned long long)(uint32_t)un.row0))
+                        store_c<OutT>(p, dst, v, bias, epi);
+                }
+            };
+            const uint32_t taddr =
+                tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+            if (S == 1) {
+                if (!aborted) {
+#pragma unroll 1
+                    for (int c = half; c * 32 < un.width; c += 2) {
+                        uint32_t v[32];
+                        if (issued) {
+                            tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), v);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c * 32 + j < n_rows) emit(c * 32 + j, __uint_as_float(v[j]));
+                    }
+                }
+            } else {
+                // Tell the peers that this CTA's MMAs have read its ring, wait
+                // until all have, and give every CTA the partial sums of its rows.
+                const int own = un.width / S;  // rows per CTA
+                if (!aborted && warp == EPI_WARP0 && lane < S)
+                    mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
+                if (!aborted && !wait_bar_warp(free_bar, split_phase, p)) aborted = true;
+                if (!aborted) {
+#pragma unroll 1
+                    for (int c = half; c * 32 < un.width; c += 2) {
+                        uint32_t v[32];
+                        if (issued) {
+                            tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), v);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int col = c * 32 + j;
+                            if (col >= un.width) break;
+                            const int to = col / own;
+                            const uint32_t at =
+                                sP0 + (uint32_t)(((part * own + col - to * own) * 128 + l) * 4);
+                            st_cluster_f32(mapa_shared(at, (uint32_t)to),
+                                           issued ? __uint_as_float(v[j]) : 0.f);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane < S) mbar_arrive_cluster(mapa_shared(parts_bar, (uint32_t)lane));
+                    if (!wait_bar_warp(parts_bar, split_phase, p)) aborted = true;
+                }
+                if (!aborted) {
+                    for (int t = half; t < own; t += 2) {
+                        const int j = part * own + t;
+                        if (j >= n_rows) break;
+                        float v = 0.f;
+                        for (int r = 0; r < S; ++r)
+                            v += ld_shared_f32(sP0 + (uint32_t)(((r * own + t) * 128 + l) * 4));
+                        emit(j, v);
+                    }
+                }
+                split_phase ^= 1u;
+                fence_proxy_async_all();  // the next unit's copies write where the parts were
+            }
+            if (issued) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
+                    else mbar_arrive_local(acce_bar(acc));
+                }
+                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            }
+            if (S > 1) cluster_sync_all();
+        }
+        __syncwarp();
+    } else {
+        // Warp 3 of the first CTA looks over the group limits (the others clamp
+        // what is wrong with them); both idle warps keep the clusters' barrier.
+        if constexpr (MODE == kRagRows || MODE == kRagDepth) {
+            pdl_wait();
+            if (blockIdx.x == 0 && warp == 3) {
+                const int most = MODE == kRagRows ? p.rows : p.depth;
+                bool bad = false;
+                for (int g = lane; g < p.G; g += 32) {
+                    const int a = __ldcg(p.offsets + g), b = __ldcg(p.offsets + g + 1);
+                    bad |= a < 0 || b > most || b < a;
+                }
+                if (bad) gen_record_timeout(p.err + 1, 1);
+            }
+        }
+        __syncwarp();
+        if (S > 1) {
+            Units<CG, MODE> units(p, cluster, list_arg);
+            while (units.next(p, un)) cluster_sync_all();
+        }
+    }
+
+    // ------------------------------------------------------------ teardown --
+    tc_fence_before_sync();
+    if (CG == 2 || S > 1) cluster_sync_all(); else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+    }
+}
+
+// units: work units (an upper bound where only the device knows their number);
+// the grid holds as many clusters as fit the GPU at once, at most one per unit.
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
+int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev,
+                          cudaStream_t stream) {
+    auto kern = ragged_kernel<CG, MODE, P_MN, BF16, OutT>;
+    static std::mutex mu;
+    static uint64_t configured = 0;  // bit per device
+    static int pairs[64];
+    const int cl = CG == 2 ? 2 : rp.split;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = RCfg::SMEM_BYTES;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const uint64_t bit = 1ull << (dev.device & 63);
+        if (!(configured & bit)) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     RCfg::SMEM_BYTES) != cudaSuccess)
+                return kCuda;
+            int n = dev.sm_count / 2;
+            if (CG == 2) {
+                cfg.gridDim = dim3(2 * n);
+                int m = 0;
+                if (cudaOccupancyMaxActiveClusters(&m, kern, &cfg) == cudaSuccess && m > 0) n = m;
+                else cudaGetLastError();
+            }
+            pairs[dev.device & 63] = n;
+            configured |= bit;
+        }
+    }
+    int64_t clusters = units;
+    if (MODE != kRagShrink) {
+        const int64_t fit = CG == 2 ? pairs[dev.device & 63] : dev.sm_count / cl;
+        if (clusters > fit) clusters = fit;
+    }
+    if (clusters < 1) clusters = 1;
+    cfg.gridDim = dim3((unsigned)(clusters * cl));
+    if (rp.pdl) {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.stream = stream;
+    if (cudaLaunchKernelEx(&cfg, kern, rp) != cudaSuccess) {
+        cudaGetLastError();
+        return kCuda;
+    }
+    note_launch();
+    return kOk;
+}
+
+// The grouped products of one element type.
+template <bool BF16, typename OutT>
+int dispatch_ragged(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                    const DeviceInfo& dev, cudaStream_t s) {
+    if (mode == kRagDepth)
+        return cg == 2 ? launch_ragged_variant<2, kRagDepth, true, BF16, OutT>(rp, units, dev, s)
+                       : launch_ragged_variant<1, kRagDepth, true, BF16, OutT>(rp, units, dev, s);
+    if (cg == 2)
+        return p_mn ? launch_ragged_variant<2, kRagRows, true, BF16, OutT>(rp, units, dev, s)
+                    : launch_ragged_variant<2, kRagRows, false, BF16, OutT>(rp, units, dev, s);
+    return p_mn ? launch_ragged_variant<1, kRagRows, true, BF16, OutT>(rp, units, dev, s)
+                : launch_ragged_variant<1, kRagRows, false, BF16, OutT>(rp, units, dev, s);
+}
+
+// The two launches of gemm_lora of one element type.
+template <bool BF16, typename OutT>
+int dispatch_lora(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
+                  const DeviceInfo& dev, cudaStream_t s) {
+    if (mode == kRagShrink)
+        return launch_ragged_variant<1, kRagShrink, false, BF16, OutT>(rp, units, dev, s);
+    if (cg == 2)
+        return p_mn ? launch_ragged_variant<2, kRagLora, true, BF16, OutT>(rp, units, dev, s)
+                    : launch_ragged_variant<2, kRagLora, false, BF16, OutT>(rp, units, dev, s);
+    return p_mn ? launch_ragged_variant<1, kRagLora, true, BF16, OutT>(rp, units, dev, s)
+                : launch_ragged_variant<1, kRagLora, false, BF16, OutT>(rp, units, dev, s);
+}
+
+}  // namespace
+}  // namespace libgemm

@@ -72,10 +72,11 @@ bool get_encoder() {
     return g_encode != nullptr;
 }
 
-// The arguments of one 2-D tiled tensor map (zero fill outside the matrix).
+// The arguments of one tiled tensor map (zero fill outside the matrix). 2-D,
+// or, with mats > 0, 3-D: `mats` matrices mat_bytes apart, the box one of them.
 struct MapArgs {
     const void* ptr;
-    uint64_t inner, outer, stride_bytes;
+    uint64_t inner, outer, stride_bytes, mats, mat_bytes;
     uint32_t box_inner, box_outer;
     int32_t dtype, swizzle, promotion, pad;
 };
@@ -95,7 +96,8 @@ std::mutex g_map_mu;
 MapSlot g_maps[kMapSlots];
 
 uint64_t hash_args(const MapArgs& a) {
-    const uint64_t w[6] = {(uint64_t)(uintptr_t)a.ptr, a.inner, a.outer, a.stride_bytes,
+    const uint64_t w[8] = {(uint64_t)(uintptr_t)a.ptr, a.inner, a.outer, a.stride_bytes,
+                           a.mats, a.mat_bytes,
                            ((uint64_t)a.box_inner << 32) | a.box_outer,
                            ((uint64_t)(uint32_t)a.dtype << 40) ^ ((uint64_t)(uint32_t)a.swizzle << 20) ^
                                (uint64_t)(uint32_t)a.promotion};
@@ -117,11 +119,11 @@ bool encode_cached(CUtensorMap* out, const MapArgs& a) {
             return true;
         }
     }
-    const cuuint64_t dims[2] = {a.inner, a.outer};
-    const cuuint64_t strides[1] = {a.stride_bytes};
-    const cuuint32_t box[2] = {a.box_inner, a.box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    if (g_encode(out, (CUtensorMapDataType)a.dtype, 2, const_cast<void*>(a.ptr), dims, strides,
+    const cuuint64_t dims[3] = {a.inner, a.outer, a.mats};
+    const cuuint64_t strides[2] = {a.stride_bytes, a.mat_bytes};
+    const cuuint32_t box[3] = {a.box_inner, a.box_outer, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (g_encode(out, (CUtensorMapDataType)a.dtype, a.mats > 0 ? 3 : 2, const_cast<void*>(a.ptr), dims, strides,
                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, (CUtensorMapSwizzle)a.swizzle,
                  (CUtensorMapL2promotion)a.promotion,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -170,6 +172,18 @@ bool encode_tma_f32_2d(void* map, const float* ptr, uint64_t inner, uint64_t out
                          map_args(ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, inner, outer, ld * 4,
                                   box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B));
+}
+
+bool encode_tma_16(void* map, bool bf16, const void* ptr, uint64_t inner, uint64_t outer,
+                   uint64_t ld, uint64_t mats, uint64_t mat_stride, uint32_t box_inner,
+                   uint32_t box_outer) {
+    MapArgs a = map_args(ptr, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         inner, outer, ld * 2, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    a.mats = mats;
+    a.mat_bytes = mat_stride * 2;
+    return encode_cached(static_cast<CUtensorMap*>(map), a);
 }
 
 int launch_gemm_tc(const Problem& pr, const DeviceInfo& dev, const TcLaunch& o,

@@ -41,11 +41,16 @@ struct Problem {
 // not stop later ones.
 using ErrWord = unsigned long long;
 
+// The word after the error word: non-zero once a kernel met values in device
+// memory that its arguments' contract rules out (group offsets, adapter
+// numbers); it has clamped or skipped them. gemm_check_device_error() reads
+// and clears it too.
+
 struct DeviceInfo {
     int device;
     int sm_count;
     int cc_major, cc_minor;
-    ErrWord* err_word;  // device address of this device's error word
+    ErrWord* err_word;  // device address of this device's two error words
     unsigned long long* check_word;  // device address of its device-check word
 };
 
@@ -124,6 +129,14 @@ int launch_sgemm_f32(const Problem& p, const DeviceInfo& dev, int config, int sp
 // matrix. False when the driver's encoder is missing or rejects the map.
 bool encode_tma_f32_2d(void* map, const float* ptr, uint64_t inner, uint64_t outer, uint64_t ld,
                        uint32_t box_inner, uint32_t box_outer);
+// A TMA tensor map over 16-bit matrices of `outer` rows of `inner` contiguous
+// elements, `ld` elements apart: one matrix (mats == 0, 2-D) or `mats` of them
+// mat_stride elements apart (3-D, boxes of one matrix); box {box_inner,
+// box_outer}, 128-byte swizzle, zero fill outside a matrix. False when the
+// driver's encoder is missing or rejects the map.
+bool encode_tma_16(void* map, bool bf16, const void* ptr, uint64_t inner, uint64_t outer,
+                   uint64_t ld, uint64_t mats, uint64_t mat_stride, uint32_t box_inner,
+                   uint32_t box_outer);
 // dst[c * ldd + r] = src[r * lds + c] (fp32), rows x cols.
 int launch_transpose_f32(const float* src, int64_t lds, float* dst, int64_t ldd, int64_t rows,
                          int64_t cols, const DeviceInfo& dev, cudaStream_t stream);
@@ -157,6 +170,12 @@ void dispatch_log(const char* fmt, ...)
     __attribute__((format(printf, 1, 2)))
 #endif
     ;
+
+// The current device, resolved once (capability check, error word, scratch
+// pool); pool may be null. And two options as the tensor-core kernels take them.
+int current_device_info(DeviceInfo** out, cudaMemPool_t* pool);
+uint64_t option_wait_limit_ns();
+int option_tc_fault_inject();
 
 // Host-side argument checks and layout normalisation of gemm() (no CUDA calls),
 // and the current device's error-word address (cudaGetSymbolAddress only).

@@ -218,4 +218,66 @@ inline int64_t plan_tc_split(int64_t T, int64_t slots, int tile_n, int cta_group
     return T - r;
 }
 
+// How a product over ragged groups runs: CTAs per unit (a CTA pair takes 256
+// features, a single CTA 128), rows of a full unit, and CTAs that share a
+// unit's depth as a cluster (single CTAs only).
+struct RaggedShape {
+    int cta_group;
+    int tile_w;
+    int split;
+};
+
+// Largest power of two <= 8 that keeps units * split within the SMs and four
+// k-blocks for each CTA of the cluster.
+inline int plan_ragged_split(int64_t units, int64_t num_kb, int sm_count) {
+    int s = 1;
+    while (s < 8 && units * (2 * s) <= sm_count && num_kb >= 4 * (2 * s)) s *= 2;
+    return s;
+}
+
+// gemm_grouped: M rows in G groups (their sizes are known on the device only),
+// N features, num_kb k-blocks.
+inline RaggedShape plan_grouped(int64_t G, int64_t M, int64_t N, int64_t num_kb, int sm_count) {
+    const int64_t groups = G < M ? G : M;  // at most this many have rows
+    const int64_t avg = (M + groups - 1) / groups;
+    const int64_t pair_units = (groups + M / 256) * ((N + 255) / 256);
+    if (avg > 64 && pair_units * 2 > sm_count) return RaggedShape{2, 256, 1};
+    const int64_t units = (groups + M / 128) * ((N + 127) / 128);
+    return RaggedShape{1, 128, plan_ragged_split(units, num_kb, sm_count)};
+}
+
+// gemm_grouped_k: G results of M x N.
+inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count) {
+    const int64_t pair_units = G * ((M + 255) / 256) * ((N + 255) / 256);
+    if (pair_units * 2 > sm_count) return RaggedShape{2, 256, 1};
+    return RaggedShape{1, 128, 1};
+}
+
+// gemm_lora: the expand's shape, and the shrink's split and chains (clusters
+// that share the 128-lane parts of a row tile's list; parts: their largest
+// number).
+struct LoraShape {
+    RaggedShape expand;
+    int shrink_split, chains;
+};
+
+inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, int sm_count) {
+    LoraShape s{};
+    const int64_t pair_units = ((M + 255) / 256) * ((N + 255) / 256);
+    if (M > 128 && pair_units * 2 > sm_count) {
+        s.expand = RaggedShape{2, 256, 1};
+    } else {
+        int w = 16;
+        while (w < 128 && w < M) w *= 2;
+        const int64_t units = ((M + w - 1) / w) * ((N + 127) / 128);
+        s.expand = RaggedShape{1, w, plan_ragged_split(units, num_kb, sm_count)};
+    }
+    const int64_t tiles = (M + 127) / 128;
+    int64_t chains = sm_count / tiles;
+    chains = chains < 1 ? 1 : (chains > parts ? parts : chains);
+    s.chains = (int)chains;
+    s.shrink_split = plan_ragged_split(tiles * chains, num_kb, sm_count);
+    return s;
+}
+
 }  // namespace libgemm

@@ -145,6 +145,23 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint3
     }
 }
 
+// 3-D tiled TMA load; as tma_load_2d with a third coordinate.
+template <int CG>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+    if constexpr (CG == 2) {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];"
+            :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];"
+            :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    }
+}
+
 // 2-D tiled TMA load multicast to every CTA of `mask` (same shared-memory
 // offset in each). With .cta_group::2 the completion goes to the barrier at
 // the offset of `bar` in the pair leader (even rank) of each destination.
@@ -164,6 +181,17 @@ __device__ __forceinline__ void st_async_v2_f32(uint32_t addr, float a, float b,
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
         :: "r"(addr), "f"(a), "f"(b), "r"(remote_bar) : "memory");
+}
+
+// Stores a float at a shared::cluster address (own or peer CTA).
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(cluster_addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // ------------------------------------------------ cluster launch control --
@@ -224,6 +252,11 @@ __device__ __forceinline__ void bulk_wait_all() {
 // (TMA) reads of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The same for every state space (shared memory of cluster peers included).
+__device__ __forceinline__ void fence_proxy_async_all() {
+    asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05 --

@@ -259,13 +259,105 @@ void gemm_tune_reset(void);
 int softmax_rows(int64_t M, int64_t N, const float *x, int64_t ldx, float *y, int64_t ldy,
                  void *stream);
 
+/*
+ * gemm_grouped -- products over groups of rows with a matrix B_g of their own
+ * (the experts of a mixture-of-experts layer), in one launch:
+ *
+ *     C[t][n] = act(alpha * sum_k A[t][k] * B_g(n,k) + beta * C[t][n] + bias[g][n])
+ *               for offsets[g] <= t < offsets[g + 1],  0 <= g < G
+ *
+ * A is M x K, K-major (row pitch lda >= K), C is M x N, row-major (ldc >= N).
+ * B holds G matrices, strideb elements apart (for G > 1 at least one matrix's
+ * span), each K-major (B_g(n,k) = B[g*strideb + n*ldb + k], ldb >= K) or
+ * N-major (B[g*strideb + k*ldb + n], ldb >= N) by b_major: with the weights
+ * stored N x K, the forward product reads them K-major with (N, K) and the
+ * input gradient dA = dC * B reads the same memory N-major with N and K
+ * exchanged.
+ *
+ * `offsets` is a DEVICE array of G + 1 row numbers, not decreasing, within
+ * [0, M], 4-byte aligned; it is read by the kernel, never by the host, so the
+ * sizes may come from an earlier kernel of the stream and the call can be
+ * captured into a graph. Empty groups are allowed; rows of C outside
+ * [offsets[0], offsets[G]) are not written. Limits outside [0, M] are clamped
+ * and a decreasing pair counts as an empty group (no row outside A and C is
+ * ever touched); gemm_check_device_error() then reports
+ * GEMM_ERR_INVALID_ARG. M is the upper bound of the rows: the launch is sized
+ * by it.
+ *
+ * Types: the 16-bit dtypes (GEMM_F32 is GEMM_ERR_UNSUPPORTED). Accumulation
+ * is fp32, C is rounded once, and the sums do not depend on timing. epi as in
+ * gemm_ex (NULL: plain), with bias a DEVICE array of G x N elements of C's
+ * type. Operands whose rows are not 16-byte aligned (or with strideb no
+ * multiple of 8) are repacked into pool scratch first, B whole. G, M or N
+ * zero is a no-op, K zero leaves the epilogue of zero sums. Otherwise
+ * ownership, asynchrony and status codes are those of gemm().
+ */
+int gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets,
+                 const void *A, int64_t lda,
+                 const void *B, int64_t ldb, int64_t strideb, int b_major,
+                 void *C, int64_t ldc, int dtype, const gemm_epilogue *epi, void *stream);
+
+/*
+ * gemm_grouped_k -- the product whose summed dimension is in groups (the
+ * weight gradient of gemm_grouped), in one launch:
+ *
+ *     C_g[m][n] = act(alpha * sum_t A[t][m] * B[t][n] + beta * C_g[m][n] + bias[g][n])
+ *                 over offsets[g] <= t < offsets[g + 1],  0 <= g < G
+ *
+ * A is K x M and B is K x N (row pitches lda >= M, ldb >= N: M- and N-major),
+ * C holds G matrices of M x N, stridec elements apart (for G > 1 at least one
+ * matrix's span), row-major (ldc >= N). An empty group's sums are zero (its
+ * C_g is written). `offsets` as in gemm_grouped, within [0, K]. Values of
+ * other groups' rows never reach a sum, infinities and NaN included. With
+ * beta = 1 the call accumulates into C. Types, epilogue (bias: G x N),
+ * repacking, degenerate sizes and status codes as gemm_grouped.
+ */
+int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets,
+                   const void *A, int64_t lda, const void *B, int64_t ldb,
+                   void *C, int64_t ldc, int64_t stridec,
+                   int dtype, const gemm_epilogue *epi, void *stream);
+
+/*
+ * gemm_lora -- a projection that many requests share, each row with a
+ * low-rank adapter of its own:
+ *
+ *     C[t][n] = act(alpha * (sum_k A[t][k] * B(n,k) + sum_r T[t][r] * LB_a[r][n])
+ *                   + beta * C[t][n] + bias[n])
+ *     T[t][r] = scale[a] * sum_k A[t][k] * LA_a[r][k],   a = adapter[t]
+ *
+ * A is M x K, K-major; B is N x K, K- or N-major by b_major; C is M x N,
+ * row-major. lora_a holds L packed R x K matrices, lora_b L packed R x N
+ * matrices (the transpose of a usual N x R second factor), both of the
+ * operands' type, 1 <= R <= 128. `adapter` is a DEVICE array of M numbers:
+ * 0 .. L-1, or negative for a row without an adapter, in any order (rows of
+ * one adapter next to each other run fastest); a number >= L counts as none,
+ * and gemm_check_device_error() then reports GEMM_ERR_INVALID_ARG. scale is a
+ * DEVICE array of L floats, or NULL for ones.
+ *
+ * Types: GEMM_F16_F16 and GEMM_BF16_BF16 (others: GEMM_ERR_UNSUPPORTED).
+ * Sums are fp32; T is carried as two 16-bit numbers (2^-17 of its value in
+ * bf16, 2^-22 in fp16, and overflows where fp16 does); C is rounded once.
+ * Rows see their own adapter only: an infinity or NaN in another adapter does
+ * not reach them. Two launches: the second starts while the first still runs.
+ * Misaligned operands (rows of A, B, or K or N no multiple of 8 for the
+ * adapters) are repacked into pool scratch first. L or R zero: gemm_ex().
+ * epi as in gemm_ex. T takes at most 512 MiB of scratch (rows are processed
+ * in panels beyond). Otherwise as gemm().
+ */
+int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
+              const void *A, int64_t lda, const void *B, int64_t ldb, int b_major,
+              const int32_t *adapter, const void *lora_a, const void *lora_b, const float *scale,
+              void *C, int64_t ldc, int dtype, const gemm_epilogue *epi, void *stream);
+
 /* gemm_strerror -- a static, NUL-terminated description of a status code. */
 const char *gemm_strerror(int status);
 
 /*
  * gemm_check_device_error -- synchronises `stream`, then reads and clears the
- * current device's error word. Returns GEMM_OK, GEMM_ERR_TIMEOUT (a kernel
- * gave up on a barrier wait) or GEMM_ERR_CUDA (the synchronisation failed).
+ * current device's error words. Returns GEMM_OK, GEMM_ERR_TIMEOUT (a kernel
+ * gave up on a barrier wait), GEMM_ERR_INVALID_ARG (a kernel met group limits
+ * or adapter numbers out of range in device memory: gemm_grouped,
+ * gemm_grouped_k, gemm_lora) or GEMM_ERR_CUDA (the synchronisation failed).
  */
 int gemm_check_device_error(void *stream);
 

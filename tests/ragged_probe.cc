@@ -1,0 +1,34 @@
+// ragged_probe.cc -- prints the host-side choices of the grouped products and
+// of the adapters, compiled with a plain C++ compiler against the library's
+// own policy header (tests/test_ragged_policy.py drives it).
+//
+//   grouped   G M N num_kb sm_count    -> "cta_group tile_w split"
+//   grouped_k G M N sm_count           -> "cta_group tile_w split"
+//   lora M N num_kb parts sm_count     -> "cta_group tile_w split shrink_split chains"
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
+#include "policy.h"
+
+int main(int argc, char** argv) {
+    using namespace libgemm;
+    auto arg = [&](int i) { return i < argc ? std::atoll(argv[i]) : 0; };
+    if (argc == 7 && std::strcmp(argv[1], "grouped") == 0) {
+        const RaggedShape s = plan_grouped(arg(2), arg(3), arg(4), arg(5), (int)arg(6));
+        std::printf("%d %d %d\n", s.cta_group, s.tile_w, s.split);
+        return 0;
+    }
+    if (argc == 6 && std::strcmp(argv[1], "grouped_k") == 0) {
+        const RaggedShape s = plan_grouped_k(arg(2), arg(3), arg(4), (int)arg(5));
+        std::printf("%d %d %d\n", s.cta_group, s.tile_w, s.split);
+        return 0;
+    }
+    if (argc == 7 && std::strcmp(argv[1], "lora") == 0) {
+        const LoraShape s = plan_lora(arg(2), arg(3), arg(4), arg(5), (int)arg(6));
+        std::printf("%d %d %d %d %d\n", s.expand.cta_group, s.expand.tile_w, s.expand.split,
+                    s.shrink_split, s.chains);
+        return 0;
+    }
+    return 2;
+}
