@@ -85,36 +85,63 @@ struct Operand {
 struct RepackMats {
     const uint16_t* src;
     uint16_t* dst;
-    int64_t mats, mat_stride, outer, ld, inner, ldd;
+    int64_t rows;  // of all matrices
+    int64_t mat_stride, outer, ld, inner, ldd;
+};
+constexpr int kMaxRepacks = 4;
+struct RepackJobs {
+    RepackMats job[kMaxRepacks];
+    int n;
 };
 
-// Copies an operand whose rows TMA cannot read into 16-byte aligned rows,
-// matrix after matrix; a warp per row.
-__global__ void __launch_bounds__(256) repack16_mats_kernel(const RepackMats j) {
+// Copies operands whose rows TMA cannot read into 16-byte aligned rows, matrix
+// after matrix, their padding zero; a warp per row, all operands in one launch.
+__global__ void __launch_bounds__(256) repack16_mats_kernel(const __grid_constant__ RepackJobs jobs) {
     gemm_ptx::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32), rows = j.mats * j.outer;
-    for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows;
-         r += warps) {
-        const int64_t m = r / j.outer, o = r - m * j.outer;
-        repack16_row(j.src + m * j.mat_stride + o * j.ld, j.dst + r * j.ldd, j.inner, lane);
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
+    int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    for (int k = 0; k < jobs.n; ++k) {
+        const RepackMats& j = jobs.job[k];
+        for (; r < j.rows; r += warps) {
+            const int64_t m = r / j.outer, o = r - m * j.outer;
+            uint16_t* dst = j.dst + r * j.ldd;
+            repack16_row(j.src + m * j.mat_stride + o * j.ld, dst, j.inner, lane);
+            for (int64_t c = j.inner + lane; c < j.ldd; c += 32) dst[c] = 0;
+        }
+        r -= j.rows;
     }
 }
 
-// Replaces an operand that is not TMA-ready by its copy at *at (advanced).
-int repack(Operand& o, char*& at, const DeviceInfo& dev, cudaStream_t s) {
-    if (o.tma_ready()) return kOk;
-    RepackMats j{static_cast<const uint16_t*>(o.ptr), reinterpret_cast<uint16_t*>(at), o.mats,
-                 o.mat_stride, o.outer, o.ld, o.inner, o.packed_ld()};
-    repack16_mats_kernel<<<repack16_blocks(o.mats * o.outer, dev.sm_count), 256, 0, s>>>(j);
+// Scratch of the copies of those operands that are not TMA-ready.
+int64_t repack_bytes(Operand* const* ops, int n) {
+    int64_t bytes = 0;
+    for (int i = 0; i < n; ++i)
+        if (!ops[i]->tma_ready()) bytes += ops[i]->packed_bytes();
+    return bytes;
+}
+
+// Replaces the operands that are not TMA-ready by their copies at `at`.
+int repack(Operand* const* ops, int n, char* at, const DeviceInfo& dev, cudaStream_t s) {
+    RepackJobs jobs{};
+    int64_t rows = 0;
+    for (int i = 0; i < n; ++i) {
+        Operand& o = *ops[i];
+        if (o.tma_ready()) continue;
+        RepackMats& j = jobs.job[jobs.n++];
+        j = {static_cast<const uint16_t*>(o.ptr), reinterpret_cast<uint16_t*>(at),
+             o.mats * o.outer, o.mat_stride, o.outer, o.ld, o.inner, o.packed_ld()};
+        at += o.packed_bytes();
+        rows += j.rows;
+        o.ptr = j.dst;
+        o.ld = j.ldd;
+        o.mat_stride = o.outer * j.ldd;
+    }
+    if (jobs.n == 0) return kOk;
+    repack16_mats_kernel<<<repack16_blocks(rows, dev.sm_count), 256, 0, s>>>(jobs);
     if (cudaGetLastError() != cudaSuccess) return kCuda;
     note_launch();
-    dispatch_log("repack of a misaligned 16-bit operand: %lld x %lld x %lld", (long long)o.mats,
-                 (long long)o.outer, (long long)o.inner);
-    at += o.packed_bytes();
-    o.ptr = j.dst;
-    o.ld = j.ldd;
-    o.mat_stride = o.outer * j.ldd;
+    dispatch_log("repack of %d misaligned 16-bit operands, %lld rows", jobs.n, (long long)rows);
     return kOk;
 }
 
@@ -136,10 +163,13 @@ void common_params(RaggedParams& rp, const DeviceInfo& dev) {
     rp.gen = next_generation();
     rp.wait_limit_ns = option_wait_limit_ns();
     rp.fault_inject = option_tc_fault_inject();
-    rp.split = 1;
+    rp.split = 0;
     rp.chains = 1;
     rp.slot = 16;
     rp.list_w = 128;
+#ifdef LIBGEMM_TC_TRACE
+    rp.trace = trace_buffer();
+#endif
 }
 
 int launch(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units, int dtype,
@@ -151,6 +181,12 @@ int launch(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units, int dty
         case GEMM_BF16_BF16: return launch_ragged_bf16_bf16(rp, mode, cg, p_mn, units, dev, s);
         default: return kInvalidArg;
     }
+}
+
+int log2_of(int x) {
+    int n = 0;
+    while (x > 1) x /= 2, ++n;
+    return n;
 }
 
 int check_epilogue(const gemm_epilogue* e, int dtype) {
@@ -220,7 +256,7 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     rp.num_kb = (int)num_kb;
     rp.tile_w = shape.tile_w;
     rp.tiles_f = (int)((N + 128 * shape.cta_group - 1) / (128 * shape.cta_group));
-    rp.split = shape.split;
+    rp.split = log2_of(shape.split);
     rp.C = C;
     rp.ldc = ldc;
     rp.epi = epi_params(epi);
@@ -229,12 +265,13 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
 
     Scratch scratch{pool, s, dev->device};
     if (K > 0) {
-        const int64_t bytes = (a.tma_ready() ? 0 : a.packed_bytes()) +
-                              (b.tma_ready() ? 0 : b.packed_bytes());
-        char* at = nullptr;
-        if (bytes > 0 && !(at = static_cast<char*>(scratch.get((size_t)bytes)))) return kCuda;
-        rc = repack(a, at, *dev, s);
-        if (rc == kOk) rc = repack(b, at, *dev, s);
+        Operand* const ops[2] = {&a, &b};
+        const int64_t bytes = repack_bytes(ops, 2);
+        if (bytes > 0) {
+            char* at = static_cast<char*>(scratch.get((size_t)bytes));
+            if (!at) return kCuda;
+            rc = repack(ops, 2, at, *dev, s);
+        }
         if (rc == kOk &&
             !(map_3d(rp, kMapP, bf16, b, kmaj ? 128 : BK) &&
               map_2d(rp, kMapQ, bf16, a, (uint32_t)(shape.tile_w / shape.cta_group)) &&
@@ -294,7 +331,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rp.tile_w = shape.tile_w;
     rp.tiles_f = (int)((N + 128 * shape.cta_group - 1) / (128 * shape.cta_group));
     rp.tiles_r = (int)((M + shape.tile_w - 1) / shape.tile_w);
-    rp.split = shape.split;
+    rp.split = log2_of(shape.split);
     rp.C = C;
     rp.ldc = ldc;
     rp.stridec = stridec;
@@ -306,15 +343,14 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
 
     Scratch scratch{pool, s, dev->device};
     if (K > 0) {
-        const int64_t bytes = (a.tma_ready() ? 0 : a.packed_bytes()) +
-                              (b.tma_ready() ? 0 : b.packed_bytes());
-        char* at = nullptr;
-        if (bytes > 0 && !(at = static_cast<char*>(scratch.get((size_t)bytes)))) return kCuda;
-        rc = repack(a, at, *dev, s);
-        if (rc == kOk) rc = repack(b, at, *dev, s);
-        if (rc == kOk && !(map_2d(rp, kMapP, bf16, b, BK) && map_2d(rp, kMapQ, bf16, a, BK) &&
-                           map_2d(rp, kMapP8, bf16, b, 8) && map_2d(rp, kMapQ8, bf16, a, 8) &&
-                           map_2d(rp, kMapP1, bf16, b, 1) && map_2d(rp, kMapQ1, bf16, a, 1)))
+        Operand* const ops[2] = {&a, &b};
+        const int64_t bytes = repack_bytes(ops, 2);
+        if (bytes > 0) {
+            char* at = static_cast<char*>(scratch.get((size_t)bytes));
+            if (!at) return kCuda;
+            rc = repack(ops, 2, at, *dev, s);
+        }
+        if (rc == kOk && !(map_2d(rp, kMapP, bf16, b, BK) && map_2d(rp, kMapQ, bf16, a, BK)))
             rc = kCuda;
     }
     if (rc == kOk) rc = launch(rp, kRagDepth, shape.cta_group, true, units, dtype, *dev, s);
@@ -385,7 +421,7 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     const int W = ex.tile_w;
     const int64_t list_n = L < (M < W ? M : W) ? L : (M < W ? M : W);
     const int64_t ldt = up(list_n * slot, EXT_K) * 2;
-    const int subs = (W + 127) / 128;
+    const int subs = W / shape.shrink_w;
     const int flags = subs * shape.chains * shape.shrink_split * EPI_WARPS;
     const int list_pitch = 1 + 2 * W + flags;
 
@@ -395,9 +431,8 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     if (panel > M) panel = M;
     const int64_t t_bytes = up(panel * ldt * 2, 256);
     const int64_t list_bytes = up((panel + W - 1) / W * list_pitch * 4, 256);
-    int64_t bytes = t_bytes + list_bytes;
-    for (const Operand* o : {&x, &w, &la, &lb})
-        if (!o->tma_ready()) bytes += o->packed_bytes();
+    Operand* const ops[4] = {&x, &w, &la, &lb};
+    const int64_t bytes = t_bytes + list_bytes + repack_bytes(ops, 4);
     Scratch scratch{pool, s, dev->device};
     char* at = static_cast<char*>(scratch.get((size_t)bytes));
     if (!at) return kCuda;
@@ -405,8 +440,7 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     at += t_bytes;
     int32_t* lists = reinterpret_cast<int32_t*>(at);
     at += list_bytes;
-    for (Operand* o : {&x, &w, &la, &lb})
-        if (rc == kOk) rc = repack(*o, at, *dev, s);
+    rc = repack(ops, 4, at, *dev, s);
 
     for (int64_t m0 = 0; m0 < M && rc == kOk; m0 += panel) {
         const int64_t m = M - m0 < panel ? M - m0 : panel;
@@ -433,10 +467,12 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         rp.T = T;
         rp.ldt = ldt;
         RaggedParams sh = rp;  // the shrink
-        sh.tile_w = W < 128 ? W : 128;
-        sh.split = shape.shrink_split;
+        sh.tile_w = shape.shrink_w;
+        sh.split = log2_of(shape.shrink_split);
+#ifdef LIBGEMM_TC_TRACE
+        if (sh.trace) sh.trace += 64 * 1024;
+#endif
         const int64_t tiles = (m + W - 1) / W;
-        sh.tiles_r = (int)(tiles * subs);
         const int64_t clusters = tiles * subs * shape.chains;
         rp.C = static_cast<uint16_t*>(C) + m0 * ldc;
         rp.ldc = ldc;
@@ -444,7 +480,7 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         rp.tile_w = W;
         rp.tiles_r = (int)tiles;
         rp.tiles_f = (int)((N + 128 * ex.cta_group - 1) / (128 * ex.cta_group));
-        rp.split = ex.split;
+        rp.split = log2_of(ex.split);
         const int64_t units = tiles * rp.tiles_f;
         if (!units_fit(units, ex.cta_group * ex.split) ||
             !units_fit(clusters, shape.shrink_split)) {
@@ -468,10 +504,10 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     }
     scratch.release();
     if (rc == kOk)
-        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d chains, split %d; "
+        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d rows, %d chains, split %d; "
                      "expand %s, units of %d rows, split %d",
                      (long long)M, (long long)N, (long long)K, (long long)L, (long long)R,
-                     shape.chains, shape.shrink_split,
+                     shape.shrink_w, shape.chains, shape.shrink_split,
                      ex.cta_group == 2 ? "CTA pairs" : "one CTA per unit", W, ex.split);
     return rc;
 }

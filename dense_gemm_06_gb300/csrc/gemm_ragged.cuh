@@ -24,7 +24,6 @@ enum RaggedMap {
     kMapP = 0,    // weights / B of the depth product / LA
     kMapQ = 1,    // rows, a full unit's share per box
     kMapQ16 = 2,  // rows, 16 per box (units narrower than the tile)
-    kMapP8 = 2, kMapQ8 = 3, kMapP1 = 4, kMapQ1 = 5,  // depth: 8- and 1-row boxes of the tail
     kMapLB = 3,   // lora: LB
     kMapT = 4, kMapT16 = 5,  // lora: T, as Q and Q16
     kRaggedMaps = 6
@@ -38,10 +37,10 @@ struct RaggedParams {
     int feats;      // columns of C (shrink: of LB)
     int depth;      // depth: rows of A and B, over which the groups are
     int num_kb;     // 64-deep k-blocks (depth: per group, from the offsets)
-    int tile_w;     // rows of a full unit
+    int tile_w;     // rows of a full unit (shrink: divides list_w)
     int tiles_f;    // feature tiles
-    int tiles_r;    // row tiles (depth: per group; shrink: 128-row tiles)
-    int split;      // CTAs that share a unit's depth (a cluster; one CTA per unit side)
+    int tiles_r;    // row tiles (depth: per group)
+    int split;      // log2 of the CTAs that share a unit's depth (a cluster of single CTAs)
     void* C;
     int64_t ldc;
     int64_t stridec;  // depth: between the C_g
@@ -49,7 +48,7 @@ struct RaggedParams {
     // gemm_lora
     const int32_t* adapter;  // adapter number of each row
     const float* scale;      // one factor per adapter, or null
-    const void* lora_b;      // LB as the kernels read it, row pitch ldlb
+    const void* lora_b;      // LB as the kernels read it, row pitch ldlb (padding zero)
     int64_t ldlb;
     int L, R, slot;          // adapters, rank, lanes per adapter (16, 32, 64 or 128)
     int list_w;              // rows that share one list of adapters (the expand's tile_w)
@@ -64,7 +63,15 @@ struct RaggedParams {
     ErrWord gen;
     unsigned long long wait_limit_ns;
     int fault_inject;
+#ifdef LIBGEMM_TC_TRACE
+    unsigned long long* trace;  // trace build: 64 timestamps per CTA (the shrink's after
+                                // those of 1024 CTAs)
+#endif
 };
+
+#ifdef LIBGEMM_TC_TRACE
+unsigned long long* trace_buffer();  // the registered buffer (gemm_tc.cu)
+#endif
 
 // Launchers, one per element type (gemm_ragged_<in>_<out>.cu, gemm_lora_<t>.cu).
 // cg: CTAs per unit; p_mn: the weights' features are contiguous.
@@ -92,11 +99,18 @@ struct RCfg {
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     // shrink: ids[256], slots[256], first[256], warp sums[16] of the row tile's list
     static constexpr int LIST_BYTES = 4096;
-    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts
-    static constexpr int NUM_BARS = 2 * STAGES + 8;
+    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
+    // tail[S], tail_peer[S]
+    static constexpr int NUM_BARS = 4 * STAGES + 8;
     static constexpr int SMEM_BYTES = RING_BYTES + LIST_BYTES + NUM_BARS * 8 + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
+// fp32 results: depth summed in one accumulator, in k-blocks. The tensor core
+// cuts each addition to the accumulator off below 2^-23 of it, an error that
+// grows with the depth (measured: 1.3e-6 of the result's norm at a depth of
+// 1037, 3.5e-6 at a few thousand), so sums of 512 are added up in registers
+// with rounding. 16-bit results round off 2^-9 or 2^-12 anyway and sum whole.
+constexpr int FOLD_KB = 8;
 constexpr int EXT_K = 32;  // lanes of T (rows of LB) per extension block: hi | lo fill 64
 
 // One unit of work: `width` rows of C from row0 (those before row_end are
@@ -252,10 +266,10 @@ struct Units<1, kRagShrink> {
     __device__ __forceinline__ Units(const RaggedParams& p, int cluster, int n)
         : sg(cluster % p.chains), parts((n * p.slot + 127) / 128), tile(cluster / p.chains) {}
     __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
-        if (sg >= parts || tile * 128 >= p.rows) return false;
+        if (sg >= parts || tile * p.tile_w >= p.rows) return false;
         un.g = sg;
         sg += p.chains;
-        un.row0 = tile * 128;
+        un.row0 = tile * p.tile_w;
         un.row_end = p.rows;
         un.feat0 = 0;
         un.width = round_width(p.rows - un.row0, 16, p.tile_w);
@@ -285,6 +299,15 @@ __device__ __forceinline__ void store_c(const RaggedParams& p, OutT* dst, float 
     *dst = from_f32<OutT>(x);
 }
 
+// t as two 16-bit numbers, 32 elements apart.
+template <typename In>
+__device__ __forceinline__ void store_t(In* dst, float t) {
+    const In hi = from_f32<In>(t);
+    const float d = t - to_f32(hi);  // infinite or NaN where hi is: then hi says it all
+    dst[0] = hi;
+    dst[32] = from_f32<In>(isfinite(d) ? d : 0.f);
+}
+
 // sum_r T[row][r] LB[id][r][f] for a row whose adapter is the s-th of its list
 // (the lanes of `t` are hi | lo halves in blocks of 32); lb points at LB[id][0][f].
 template <typename In>
@@ -298,11 +321,38 @@ __device__ __noinline__ float adapter_part(const In* t, const In* lb, int64_t ld
     return v;
 }
 
+// wait_bar_warp without a call: the folding epilogue waits with its sums live,
+// and a call would spill them.
+__device__ __forceinline__ bool wait_bar_inline(uint32_t bar, uint32_t parity,
+                                                const RaggedParams& p) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t n = 1;; ++n) {
+            ok = mbar_try_wait(bar, parity);
+            if (ok || ((n & 31u) == 0 && gen_failed(p.err, p.gen))) break;
+            if ((n & 31u) == 0 && globaltimer_ns() - t0 > p.wait_limit_ns) {
+                gen_record_timeout(p.err, p.gen);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Debug build: true when element (row, f) lies inside C, else records it.
+__device__ __forceinline__ bool c_checked(const RaggedParams& p, int row, int f) {
+    return device_check(p.check, row >= 0 && row < p.rows && f >= 0 && f < p.feats, kCheckTcStore,
+                        ((unsigned long long)(uint32_t)row << 24) | (uint32_t)f);
+}
+
 // The list of the distinct adapters of a row tile, in order of first use, by
 // all threads of the CTA: ids[list_w] the adapter or -1 of each row, then
 // slots[] each row's place in the list (-1: none), list[] the adapters.
-// Returns their number. (Quadratic in the tile's 256 rows at most: each row
-// looks for its first equal among the earlier ones in shared memory.)
+// Returns their number. Rows of one warp find each other by match_any; the
+// first of each set then looks for its adapter among the earlier warps' rows
+// in shared memory (at most 224, four per load, no early exit: the loads
+// pipeline, where a scalar loop that stops at the first hit waits for each).
 __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* ids, int* slots,
                                          int* list, int* sums) {
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
@@ -315,23 +365,34 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
         }
         if (id < 0) id = -1;
     }
-    if (i < p.list_w) ids[i] = id;
+    if (i < 256) ids[i] = id;
     __syncthreads();
-    int first = i;
-    if (id >= 0)
-        for (int j = 0; j < i; ++j)
-            if (ids[j] == id) {
-                first = j;
-                break;
-            }
+    // the row's first equal within its warp, then (that row) among earlier warps
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    const int lead = __ffs(same) - 1;
+    int first = warp * 32 + lead;
+    if (id >= 0 && lead == lane && i < 256) {
+        const int4* v = reinterpret_cast<const int4*>(ids);
+#pragma unroll 8
+        for (int j = warp * 8 - 1; j >= 0; --j) {
+            const int4 x = v[j];
+            if (x.w == id) first = 4 * j + 3;
+            if (x.z == id) first = 4 * j + 2;
+            if (x.y == id) first = 4 * j + 1;
+            if (x.x == id) first = 4 * j;
+        }
+    }
     const bool mine = id >= 0 && first == i;
     const uint32_t b = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) sums[warp] = __popc(b);
+    first = __shfl_sync(0xffffffffu, first, lead);
     __syncthreads();
     int place = __popc(b & ((1u << lane) - 1)), n = 0;
+#pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) place += sums[w];
-        n += sums[w];
+        const int c = sums[w];
+        if (w < warp) place += c;
+        n += c;
     }
     if (mine) {
         slots[i] = place;
@@ -341,14 +402,14 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
     int s = -1;
     if (id >= 0) s = slots[first];
     __syncthreads();
-    if (i < p.list_w) slots[i] = s;
+    if (i < 256) slots[i] = s;
     __syncthreads();
     return n;
 }
 
 // CG: CTAs per unit (a pair halves P's features and Q's rows between its
 // CTAs). P_MN: P's features are contiguous (weights N-major; always in the
-// depth product). With p.split > 1 (CG == 1) a cluster of `split` CTAs shares
+// depth product). With p.split > 0 (CG == 1) a cluster of 2^split CTAs shares
 // each unit: every CTA sums its share of the k-blocks, and the partial sums
 // meet in the shared memory of the CTA that owns the row, in rank order.
 template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
@@ -356,6 +417,8 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     using C_ = RCfg;
     using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr bool Q_MN = MODE == kRagDepth;
+    constexpr bool FOLD = std::is_same_v<OutT, float> && MODE != kRagShrink;
+    constexpr int CHUNKS = CG == 2 ? 4 : 2;  // of 32 rows that an epilogue warp stores
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -372,6 +435,9 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     const uint32_t never_bar = bar0 + 8u * (2 * C_::STAGES + 5);
     const uint32_t free_bar = bar0 + 8u * (2 * C_::STAGES + 6);   // every CTA's ring is free
     const uint32_t parts_bar = bar0 + 8u * (2 * C_::STAGES + 7);  // partial sums have arrived
+    // depth: a group's last block in this CTA's ring / zeroed by the pair's other CTA
+    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * C_::STAGES + 8 + s); };
+    auto peer_bar = [&](int s) { return bar0 + 8u * (3 * C_::STAGES + 8 + s); };
     int* sm_ids = reinterpret_cast<int*>(smem + C_::RING_BYTES);
     int* sm_slots = sm_ids + 256;
     int* sm_list = sm_ids + 512;
@@ -381,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int S = CG == 1 ? p.split : 1;
+    const int S = CG == 1 ? 1 << p.split : 1;
     const uint32_t crank = CG == 2 || S > 1 ? cluster_ctarank() : 0u;
     const uint32_t rank = CG == 2 ? crank : 0u;   // side of the pair
     const int part = S > 1 ? (int)crank : 0;      // share of the depth
@@ -390,6 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     const int cluster = (int)blockIdx.x / per_cluster;
     const int nclusters = (int)gridDim.x / per_cluster;
 
+    if (threadIdx.x == 0) TC_TRACE(p, 0);
     if constexpr (MODE == kRagShrink) {
         // Everything before this launch is complete past the wait, and the
         // expand, which may then start, relies on that: it reads X and W
@@ -406,6 +473,8 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         for (int s = 0; s < C_::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(tail_bar(s), 1);
+            mbar_init(peer_bar(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar(a), 1);
@@ -423,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     }
     int n_list = 0;
     if constexpr (MODE == kRagShrink) {
-        const int row0 = cluster / p.chains * 128;
+        const int row0 = cluster / p.chains * p.tile_w;
         const int list_tile = row0 / p.list_w;
         n_list = make_list(p, list_tile * p.list_w, sm_ids, sm_slots, sm_list, sm_sums);
         if (cluster % p.chains == 0 && part == 0 && row0 % p.list_w == 0) {
@@ -437,13 +506,15 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     if (CG == 2 || S > 1) cluster_sync_all(); else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    if (threadIdx.x == 0) TC_TRACE(p, 1);
 
     bool aborted = false;
     RUnit un;
     // k-blocks [kb0, kb1) of a unit are this CTA's (all of them but for a split)
     auto share = [&](int n, int& a, int& b) {
-        a = (int)((int64_t)n * part / S);
-        b = (int)((int64_t)n * (part + 1) / S);
+        const int sh = CG == 1 ? p.split : 0;
+        a = (n >> sh) * part + (((n & (S - 1)) * part) >> sh);
+        b = (n >> sh) * (part + 1) + (((n & (S - 1)) * (part + 1)) >> sh);
     };
     // lora: extension blocks of a unit's list tile; 0 when its flags tell the
     // epilogue to add the adapters' part itself. `ids`: its adapters.
@@ -465,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         uint32_t phase = 0;
         bool waited = false;
         Units<CG, MODE> units(p, cluster, list_arg);
-        while (units.next(p, un)) {
+        for (bool more = units.next(p, un); more;) {
             const int q_rows = un.width / CG;
             const int q_row = un.row0 + (int)rank * q_rows;
             const int f0 = un.feat0 + (int)rank * 128;
@@ -484,49 +555,29 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     const int k0 = un.k0 + kb * BK;
                     const int tail = min(BK, un.k_end - k0);
                     const int nq = q_rows / 64;  // 64-wide chunks of this CTA's rows
-                    if (tail == BK) {
-                        if (elect_one()) {
-                            if (leader)
-                                mbar_arrive_expect_tx(full_bar(stage),
-                                                      (uint32_t)(CG * (2 + nq) * 64 * BK * 2));
-                            for (int j = 0; j < 2; ++j)
-                                tma_load_2d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], fb,
-                                                f0 + 64 * j, k0);
-                            for (int j = 0; j < nq; ++j)
-                                tma_load_2d<CG>(sq + j * 64 * BK * 2, &p.map[kMapQ], fb,
-                                                q_row + 64 * j, k0);
-                        }
-                    } else {
-                        // The group ends inside this block: its last k-rows come in
-                        // boxes of 8 and 1 rows, and the rows up to the next multiple
-                        // of 16 (one MMA step) are zeros, read past the end of the
-                        // matrix: another group's values, which may be infinite or
-                        // NaN, never meet a zero of this one's.
-                        const int n8 = tail / 8, n1 = tail % 8, z1 = n1 ? 8 - n1 : 0;
-                        const int rows16 = (tail + 15) / 16 * 16;
-                        const int pieces = n8 + n1 + z1 + (rows16 - (n8 * 8 + n1 + z1)) / 8;
-                        if (leader && lane == 0)
-                            mbar_arrive_expect_tx(full_bar(stage),
-                                                  (uint32_t)(CG * (2 + nq) * 64 * rows16 * 2));
-                        for (int i = lane; i < pieces * (2 + nq); i += 32) {
-                            const int piece = i % pieces, j = i / pieces;
-                            const bool one = piece >= n8 && piece < n8 + n1 + z1;
-                            const int r = piece < n8 ? piece * 8
-                                          : one      ? n8 * 8 + (piece - n8) : rows16 - 8;
-                            const int y = r < tail ? k0 + r : p.depth;
-                            const bool in_p = j < 2;
-                            const int jj = in_p ? j : j - 2;
-                            const uint32_t dst = (in_p ? sp : sq) +
-                                                 (uint32_t)(jj * 64 * BK * 2 + r * 128);
-                            const CUtensorMap* m = &p.map[in_p ? (one ? kMapP1 : kMapP8)
-                                                               : (one ? kMapQ1 : kMapQ8)];
-                            tma_load_2d<CG>(dst, m, fb, (in_p ? f0 : q_row) + 64 * jj, y);
-                        }
+                    // A group's last block also brings the next group's first rows;
+                    // warp 2 overwrites them with zeros before the MMA sees the stage.
+                    const bool whole = tail == BK;
+                    const uint32_t to = whole ? fb : tail_bar(stage);
+                    if (kb == kb0 && lane == 0) TC_TRACE(p, 2);
+                    if (kb == kb1 - 1 && lane == 0) TC_TRACE(p, 18);
+                    if (elect_one()) {
+                        if (leader || !whole)
+                            mbar_arrive_expect_tx(whole ? full_bar(stage) : tail_bar(stage),
+                                                  (uint32_t)((whole ? CG : 1) * (2 + nq) * 64 *
+                                                             BK * 2));
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], to, f0 + 64 * j,
+                                            k0);
+                        for (int j = 0; j < nq; ++j)
+                            tma_load_2d<CG>(sq + j * 64 * BK * 2, &p.map[kMapQ], to,
+                                            q_row + 64 * j, k0);
                     }
                 } else {
                     const int k0 = kb * BK;
                     const bool x_ok = device_check(p.check, (k0 & 7) == 0 && (f0 & 7) == 0,
                                                    kCheckTcTmaX, (unsigned long long)k0);
+                    if (kb == kb0 && lane == 0) TC_TRACE(p, 2);
                     if (x_ok && elect_one()) {
                         const int p_bytes = MODE == kRagShrink ? ns * p.slot * BK * 2 : C_::P_BYTES;
                         if (leader)
@@ -556,8 +607,10 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
             if constexpr (MODE == kRagLora) {
                 // T and the lists are the first launch's: wait for it only here
+                if (lane == 0) TC_TRACE(p, 3);
                 if (!waited) pdl_wait();
                 waited = true;
+                if (lane == 0) TC_TRACE(p, 4);
                 int n;
                 const int32_t* ids;
                 const int ne = ext_blocks(un.tile, n, ids);
@@ -596,7 +649,8 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
-            if (S > 1) cluster_sync_all();  // the ring held partial sums until here
+            more = units.next(p, un);
+            if (S > 1 && more) cluster_sync_all();  // the ring held partial sums until here
         }
         if (aborted) grace_period_ns(200000);  // let issued copies land
         __syncwarp();
@@ -620,13 +674,13 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             uint32_t acc_phase = 0;
             bool waited = false;
             Units<CG, MODE> units(p, cluster, list_arg);
-            while (units.next(p, un)) {
+            for (bool more = units.next(p, un); more;) {
                 const uint32_t width_bits = (uint32_t)(un.width >> 3) << 17;
                 int kb0, kb1, n = 0, ne = 0;
                 share(un.nkb, kb0, kb1);
                 bool issued = false;  // the unit's first MMA overwrites the accumulator
                 bool acc_ready = false;
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+                auto d_tmem = [&]() { return tmem_base + (uint32_t)(acc * ACC_COLS); };
                 auto get_acc = [&]() {  // the accumulator, once the unit needs it
                     if (acc_ready) return true;
                     acc_ready = true;
@@ -640,23 +694,36 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                         break;
                     }
                     tc_fence_after_sync();
+                    if (kb == kb0 && lane == 0) TC_TRACE(p, 5);
+                    if (kb == kb1 - 2 && lane == 0) TC_TRACE(p, 16);
+                    if (kb == kb1 - 1 && lane == 0) TC_TRACE(p, 17);
                     const uint64_t pd = p_desc0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
                     const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
-                    int steps = BK / UMMA_K;
-                    if constexpr (MODE == kRagDepth)
-                        steps = min(steps, (un.k_end - un.k0 - kb * BK + UMMA_K - 1) / UMMA_K);
+                    auto step = [&](int j) {
+                        mma_f16<CG>(d_tmem(), pd + (uint64_t)(j * (P_STEP >> 4)),
+                                    qd + (uint64_t)(j * (Q_STEP >> 4)), idesc0 | width_bits,
+                                    issued || j != 0 ? 1u : 0u);
+                    };
+                    const int left = MODE == kRagDepth ? un.k_end - un.k0 - kb * BK : BK;
                     if (elect_one()) {
+                        if (MODE != kRagDepth || left > BK - UMMA_K) {
 #pragma unroll
-                        for (int j = 0; j < BK / UMMA_K; ++j)
-                            if (MODE != kRagDepth || j < steps)
-                                mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
-                                            qd + (uint64_t)(j * (Q_STEP >> 4)),
-                                            idesc0 | width_bits, issued || j != 0 ? 1u : 0u);
+                            for (int j = 0; j < BK / UMMA_K; ++j) step(j);
+                        } else {  // a group's last block
+                            for (int j = 0; j * UMMA_K < left; ++j) step(j);
+                        }
                         mma_commit<CG>(empty_bar(stage));
                     }
                     issued = true;
                     __syncwarp();
                     if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
+                    if (FOLD && (kb - kb0) % FOLD_KB == FOLD_KB - 1 && kb + 1 < kb1) {
+                        // hand over this part of the sum, go on in the other accumulator
+                        if (elect_one()) mma_commit<CG>(accf_bar(acc));
+                        __syncwarp();
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                        issued = acc_ready = false;
+                    }
                 }
                 if constexpr (MODE == kRagLora) {
                     if (!waited) pdl_wait();
@@ -677,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                             for (int j = 0; j < steps; ++j)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
-                                    mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (UMMA_K * 128 >> 4)),
+                                    mma_f16<CG>(d_tmem(), pd + (uint64_t)(j * (UMMA_K * 128 >> 4)),
                                                 qd + (uint64_t)((j + 2 * h) * (UMMA_K * 2 >> 4)),
                                                 idesc_ext0 | width_bits,
                                                 issued || j + h != 0 ? 1u : 0u);
@@ -688,12 +755,14 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                         if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
                     }
                 }
+                if (lane == 0) TC_TRACE(p, 6);
                 if (issued && !aborted) {
                     if (elect_one()) mma_commit<CG>(accf_bar(acc));
                     __syncwarp();
                     if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
                 }
-                if (S > 1) cluster_sync_all();
+                more = units.next(p, un);
+                if (S > 1 && more) cluster_sync_all();
             }
             // Drain: wait (bounded) until every MMA issued above has completed.
             if (elect_one()) {
@@ -722,37 +791,36 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             // tile, so the expand then adds this tile's adapters one by one.
             // The CTAs of a list tile share the scan, which also brings LB into
             // L2 for the expand.
-            const int subs = (p.list_w + 127) / 128;
+            const int subs = p.list_w / p.tile_w;
             const int me = ((cluster / p.chains % subs) * p.chains + cluster % p.chains) * S + part;
             const int ctas = subs * p.chains * S;
-            const int vecs = (p.feats + 7) / 8;  // 16-byte groups per LB row
-            const int64_t total = (int64_t)n_list * p.R * vecs;
+            // 16-byte groups of one adapter's LB (its rows' padding is zero)
+            const int64_t vecs = (int64_t)p.R * p.ldlb / 8;
             bool bad = false;
-            for (int64_t i = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32);
-                 i < total; i += (int64_t)ctas * (EPI_WARPS * 32)) {
-                const int v = (int)(i % vecs);
-                const int64_t lr = i / vecs;
-                const int id = sm_list[lr / p.R];
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.lora_b) +
-                    ((int64_t)id * p.R + lr % p.R) * p.ldlb + 8 * v));
-                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            for (int64_t v = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32);
+                 v < vecs; v += (int64_t)ctas * (EPI_WARPS * 32)) {
+                const uint4* b = static_cast<const uint4*>(p.lora_b) + v;
+                for (int a = 0; a < n_list; a += 8) {  // eight loads in flight
+                    uint4 w[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int left = p.feats - 8 * v - 2 * j;  // padding is not looked at
-                    if (left < 2) x[j] = left == 1 ? x[j] & 0xFFFFu : 0u;
-                    bad |= nonfinite16<BF16>(x[j]);
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = __ldg(b + (int64_t)sm_list[min(a + j, n_list - 1)] * vecs);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        bad |= nonfinite16<BF16>(w[j].x) | nonfinite16<BF16>(w[j].y) |
+                               nonfinite16<BF16>(w[j].z) | nonfinite16<BF16>(w[j].w);
                 }
             }
             bad = __any_sync(0xffffffffu, bad);
+            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 7);
             if (lane == 0) {
-                int32_t* flag = p.lists + (int64_t)(cluster / p.chains * 128 / p.list_w) *
-                                              p.list_pitch + 1 + 2 * p.list_w;
+                int32_t* flag = p.lists + (int64_t)(cluster / p.chains / subs) * p.list_pitch +
+                                1 + 2 * p.list_w;
                 flag[me * EPI_WARPS + (warp - EPI_WARP0)] = bad ? 1 : 0;
             }
         }
         Units<CG, MODE> units(p, cluster, list_arg);
-        while (units.next(p, un)) {
+        for (bool more = units.next(p, un); more;) {
             int kb0, kb1, n = 0, ne = 0;
             share(un.nkb, kb0, kb1);
             bool issued = kb1 > kb0;
@@ -762,10 +830,6 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 issued = issued || part < ne;
             }
             const bool by_hand = MODE == kRagLora && n > 0 && ne == 0;
-            if (!aborted && issued) {
-                if (!__all_sync(0xffffffffu, wait_bar(accf_bar(acc), acc_phase, p))) aborted = true;
-                tc_fence_after_sync();
-            }
             const int l = q * 32 + lane;  // TMEM lane
             const int f = un.feat0 + (int)rank * 128 + l;
             const int n_rows = min(un.width, un.row_end - un.row0);
@@ -782,27 +846,24 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             int slot = 0, r_idx = 0;
             float factor = 1.f;
             In* t_col = nullptr;
+            const int* row_slot = nullptr;  // the rows' places in the list
+            int my_slot = 0;                // -2 for a lane past the rank: matches no row
             if constexpr (MODE == kRagShrink) {
                 const int ll = un.g * 128 + l;
                 slot = ll / p.slot;
                 r_idx = ll % p.slot;
                 if (slot < n_list && p.scale) factor = p.scale[sm_list[slot]];
+                my_slot = r_idx < p.R ? slot : -2;
+                row_slot = sm_slots + un.row0 % p.list_w;
                 t_col = static_cast<In*>(p.T) + (int64_t)un.row0 * p.ldt +
                         (int64_t)(ll / 32) * 64 + lane;
             }
             // Row j of the unit, value v of this lane.
             auto emit = [&](int j, float v) {
                 if constexpr (MODE == kRagShrink) {
-                    if (slot >= n_list) return;
-                    const bool own = sm_slots[un.row0 % p.list_w + j] == slot && r_idx < p.R;
-                    const float t = own ? v * factor : 0.f;
-                    const In hi = from_f32<In>(t);
-                    const float d = t - to_f32(hi);  // infinite or NaN: hi says it all
-                    In* dst = t_col + (int64_t)j * p.ldt;
-                    dst[0] = hi;
-                    dst[32] = from_f32<In>(isfinite(d) ? d : 0.f);
+                    if (slot < n_list) store_t<In>(t_col + (int64_t)j * p.ldt,
+                                                   row_slot[j] == my_slot ? v * factor : 0.f);
                 } else {
-                    if (!f_ok) return;
                     if constexpr (MODE == kRagLora) {
                         if (by_hand) {
                             const int s = __ldcg(ids + p.list_w + j);
@@ -816,75 +877,80 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                             }
                         }
                     }
-                    OutT* dst = c_col + (int64_t)j * p.ldc;
-                    if (device_check(p.check, un.row0 + j >= 0 && un.row0 + j < p.rows,
-                                     kCheckTcStore, (unsigned long long)(uint32_t)un.row0))
-                        store_c<OutT>(p, dst, v, bias, epi);
+                    if (c_checked(p, un.row0 + j, f))
+                        store_c<OutT>(p, c_col + (int64_t)j * p.ldc, v, bias, epi);
                 }
             };
-            const uint32_t taddr =
-                tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-            if (S == 1) {
-                if (!aborted) {
-#pragma unroll 1
-                    for (int c = half; c * 32 < un.width; c += 2) {
-                        uint32_t v[32];
-                        if (issued) {
-                            tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), v);
-                            tmem_wait_ld();
-                        } else {
+            // Rows 32 c .. of the unit, v[i] this lane's value of row 32 c + i.
+            auto emit_chunk = [&](int c, const float (&v)[32]) {
+                const int left = n_rows - c * 32;
+                if constexpr (MODE == kRagShrink) {
+                    if (slot >= n_list) return;
+                    In* dst = t_col + (int64_t)(c * 32) * p.ldt;
+                    int s[32];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = 0u;
-                        }
+                    for (int i = 0; i < 32; ++i) s[i] = row_slot[c * 32 + i];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c * 32 + j < n_rows) emit(c * 32 + j, __uint_as_float(v[j]));
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < left) store_t<In>(dst, s[i] == my_slot ? v[i] * factor : 0.f);
+                        dst += p.ldt;
                     }
+                    return;
                 }
-            } else {
-                // Tell the peers that this CTA's MMAs have read its ring, wait
-                // until all have, and give every CTA the partial sums of its rows.
-                const int own = un.width / S;  // rows per CTA
-                if (!aborted && warp == EPI_WARP0 && lane < S)
-                    mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
-                if (!aborted && !wait_bar_warp(free_bar, split_phase, p)) aborted = true;
-                if (!aborted) {
-#pragma unroll 1
-                    for (int c = half; c * 32 < un.width; c += 2) {
-                        uint32_t v[32];
-                        if (issued) {
-                            tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), v);
-                            tmem_wait_ld();
-                        }
+                if (!f_ok) return;
+                if (!epi && !by_hand) {
+                    // one store and one pointer step per row
+                    OutT* dst = c_col + (int64_t)(c * 32) * p.ldc;
+                    if (left >= 32) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int col = c * 32 + j;
-                            if (col >= un.width) break;
-                            const int to = col / own;
-                            const uint32_t at =
-                                sP0 + (uint32_t)(((part * own + col - to * own) * 128 + l) * 4);
-                            st_cluster_f32(mapa_shared(at, (uint32_t)to),
-                                           issued ? __uint_as_float(v[j]) : 0.f);
+                        for (int i = 0; i < 32; ++i) {
+                            if (c_checked(p, un.row0 + c * 32 + i, f)) *dst = from_f32<OutT>(v[i]);
+                            dst += p.ldc;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (i < left && c_checked(p, un.row0 + c * 32 + i, f))
+                                *dst = from_f32<OutT>(v[i]);
+                            dst += p.ldc;
                         }
                     }
-                    __syncwarp();
-                    if (lane < S) mbar_arrive_cluster(mapa_shared(parts_bar, (uint32_t)lane));
-                    if (!wait_bar_warp(parts_bar, split_phase, p)) aborted = true;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < left) emit(c * 32 + i, v[i]);
                 }
-                if (!aborted) {
-                    for (int t = half; t < own; t += 2) {
-                        const int j = part * own + t;
-                        if (j >= n_rows) break;
-                        float v = 0.f;
-                        for (int r = 0; r < S; ++r)
-                            v += ld_shared_f32(sP0 + (uint32_t)(((r * own + t) * 128 + l) * 4));
-                        emit(j, v);
-                    }
+            };
+            // Split depth: row j of the unit belongs to CTA j % S; this lane's
+            // partial sums of the chunk go there.
+            const int own = un.width >> (CG == 1 ? p.split : 0);  // rows per CTA
+            auto push_chunk = [&](int c, const float (&v)[32]) {
+                const uint32_t at = sP0 + (uint32_t)((part * own * 128 + l) * 4);
+                auto push = [&](int i) {
+                    st_cluster_f32(mapa_shared(at, (uint32_t)(i & (S - 1))) +
+                                       (uint32_t)(((c * 32 + i) >> p.split) * 512),
+                                   v[i]);
+                };
+#pragma unroll
+                for (int i = 0; i < 16; ++i) push(i);
+                if (c * 32 + 16 < un.width) {
+#pragma unroll
+                    for (int i = 16; i < 32; ++i) push(i);
                 }
-                split_phase ^= 1u;
-                fence_proxy_async_all();  // the next unit's copies write where the parts were
-            }
-            if (issued) {
+            };
+            const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
+            auto load_chunk = [&](int c, float (&v)[32]) {
+                uint32_t u[32];
+                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + c * 32), u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+            };
+            auto wait_acc = [&]() {
+                if (!aborted && !wait_bar_inline(accf_bar(acc), acc_phase, p)) aborted = true;
+                tc_fence_after_sync();
+            };
+            auto free_acc = [&]() {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -892,8 +958,108 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     else mbar_arrive_local(acce_bar(acc));
                 }
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            };
+            // The unit's sums: a folded depth's parts add up in registers; else
+            // the chunks are read from the accumulator as they are stored.
+            float sum[FOLD ? CHUNKS : 1][32];
+            if constexpr (FOLD) {
+#pragma unroll
+                for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[k][i] = 0.f;
+                for (int kb = kb0; kb < kb1; kb += FOLD_KB) {
+                    wait_acc();
+#pragma unroll
+                    for (int k = 0; k < CHUNKS; ++k) {
+                        const int c = half + 2 * k;
+                        if (!aborted && c * 32 < un.width) {
+                            // 16 columns at a time: the sums leave no registers for more
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t u[16];
+                                tmem_ld_32x32b_x16(
+                                    tlane + (uint32_t)(acc * ACC_COLS + c * 32 + h), u);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[k][h + i] += __uint_as_float(u[i]);
+                            }
+                        }
+                    }
+                    free_acc();
+                }
+            } else if (issued) {
+                wait_acc();
             }
-            if (S > 1) cluster_sync_all();
+            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 8);
+            auto each_chunk = [&](auto&& use) {
+                if constexpr (FOLD) {
+#pragma unroll
+                    for (int k = 0; k < CHUNKS; ++k)
+                        if ((half + 2 * k) * 32 < un.width) use(half + 2 * k, sum[k]);
+                } else {
+#pragma unroll 1
+                    for (int c = half; c * 32 < un.width; c += 2) {
+                        float v[32];
+                        if (issued) {
+                            load_chunk(c, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        }
+                        use(c, v);
+                    }
+                }
+            };
+            if (S == 1) {
+                if (!aborted) each_chunk(emit_chunk);
+            } else {
+                // Tell the peers that this CTA's MMAs have read its ring, wait
+                // until all have, and give every CTA the partial sums of its rows.
+                if (!aborted && warp == EPI_WARP0 && lane < S)
+                    mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
+                if (!aborted && !wait_bar_warp(free_bar, split_phase, p)) aborted = true;
+                if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 9);
+                if (!aborted) {
+                    each_chunk(push_chunk);
+                    __syncwarp();
+                    if (lane < S) mbar_arrive_cluster(mapa_shared(parts_bar, (uint32_t)lane));
+                    if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 10);
+                    if (!wait_bar_warp(parts_bar, split_phase, p)) aborted = true;
+                }
+                if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 11);
+                if (!aborted) {
+                    // add the parts in rank order, four rows at a time so that their
+                    // loads overlap
+                    const float* parts = reinterpret_cast<const float*>(smem) + l;
+                    for (int t0 = half; t0 < own; t0 += 8) {
+                        float v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            float x[8];
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                x[r] = r < S && t0 + 2 * u < own
+                                           ? parts[(r * own + t0 + 2 * u) * 128] : 0.f;
+                            v[u] = x[0];
+#pragma unroll
+                            for (int r = 1; r < 8; ++r) v[u] += x[r];
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int j = (t0 + 2 * u) * S + part;
+                            if (t0 + 2 * u < own && j < n_rows && (MODE == kRagShrink || f_ok))
+                                emit(j, v[u]);
+                        }
+                    }
+                }
+                split_phase ^= 1u;
+                fence_proxy_async_all();  // the next unit's copies write where the parts were
+            }
+            if (!FOLD && issued) free_acc();
+            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 12);
+            more = units.next(p, un);
+            if (S > 1 && more) cluster_sync_all();
         }
         __syncwarp();
     } else {
@@ -912,9 +1078,57 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         __syncwarp();
-        if (S > 1) {
+        if (MODE == kRagDepth && warp == 2) {
+            // A group's last block holds, past the group's end, rows of the next
+            // one: zeros up to the next multiple of 16 (one MMA step; the MMA
+            // stops there), in P and Q both, so that another group's values, which
+            // may be infinite or NaN, never meet a zero of this one's. Then the
+            // stage is full: the leader's warp says so, once its peer has zeroed
+            // its half too.
+            int block = 0;  // of this CTA's ring
+            uint32_t parity = 0;  // bit per stage
             Units<CG, MODE> units(p, cluster, list_arg);
-            while (units.next(p, un)) cluster_sync_all();
+            for (bool more = units.next(p, un); more;) {
+                int kb0, kb1;
+                share(un.nkb, kb0, kb1);
+                const int tail = (un.k_end - un.k0) % BK;
+                block += kb1 - kb0;
+                if (tail != 0 && kb1 == un.nkb && kb1 > kb0 && !aborted) {
+                    const int s = (block - 1) % C_::STAGES;
+                    const uint32_t bit = (parity >> s) & 1u;
+                    if (!wait_bar_warp(tail_bar(s), bit, p)) aborted = true;
+                    if (lane == 0) TC_TRACE(p, 14);
+                    const int rows16 = (tail + UMMA_K - 1) / UMMA_K * UMMA_K;
+                    const int nq = un.width / CG / 64;
+                    if (!aborted) {
+                        for (int j = 0; j < 2 + nq; ++j) {
+                            const uint32_t at =
+                                (j < 2 ? sP0 + s * C_::P_BYTES + j * 64 * BK * 2
+                                       : sQ0 + s * C_::Q_BYTES + (j - 2) * 64 * BK * 2);
+                            for (int i = tail * 8 + lane; i < rows16 * 8; i += 32)
+                                sts128(at + (uint32_t)i * 16u, 0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_all();  // before the MMA reads them
+                    }
+                    __syncwarp();
+                    if (lane == 0) TC_TRACE(p, 15);
+                    if (CG == 2 && leader && !aborted && !wait_bar_warp(peer_bar(s), bit, p))
+                        aborted = true;
+                    if (lane == 0 && !aborted) {
+                        if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
+                        else mbar_arrive_local(full_bar(s));
+                    }
+                    parity ^= 1u << s;
+                }
+                more = units.next(p, un);
+                if (S > 1 && more) cluster_sync_all();
+            }
+        } else if (S > 1) {
+            Units<CG, MODE> units(p, cluster, list_arg);
+            for (bool more = units.next(p, un); more;) {
+                more = units.next(p, un);
+                if (more) cluster_sync_all();
+            }
         }
     }
 
@@ -924,6 +1138,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+        if (lane == 0) TC_TRACE(p, 13);
     }
 }
 
@@ -936,7 +1151,7 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
     static std::mutex mu;
     static uint64_t configured = 0;  // bit per device
     static int pairs[64];
-    const int cl = CG == 2 ? 2 : rp.split;
+    const int cl = CG == 2 ? 2 : 1 << rp.split;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -166,6 +166,11 @@ bool encode_2d(CUtensorMap* map, bool bf16, const void* ptr, uint64_t inner, uin
 
 }  // namespace
 
+#ifdef LIBGEMM_TC_TRACE
+unsigned long long* trace_buffer();
+unsigned long long* trace_buffer() { return g_trace; }
+#endif
+
 bool encode_tma_f32_2d(void* map, const float* ptr, uint64_t inner, uint64_t outer, uint64_t ld,
                        uint32_t box_inner, uint32_t box_outer) {
     return encode_cached(static_cast<CUtensorMap*>(map),

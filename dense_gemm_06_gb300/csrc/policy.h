@@ -253,12 +253,13 @@ inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count)
     return RaggedShape{1, 128, 1};
 }
 
-// gemm_lora: the expand's shape, and the shrink's split and chains (clusters
-// that share the 128-lane parts of a row tile's list; parts: their largest
-// number).
+// gemm_lora: the expand's shape, and the shrink's rows per tile, split and
+// chains (clusters that share the 128-lane parts of a row tile's list; parts:
+// their largest number, which only decides where tiles and split leave SMs
+// idle).
 struct LoraShape {
     RaggedShape expand;
-    int shrink_split, chains;
+    int shrink_w, shrink_split, chains;
 };
 
 inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, int sm_count) {
@@ -272,11 +273,12 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, 
         const int64_t units = ((M + w - 1) / w) * ((N + 127) / 128);
         s.expand = RaggedShape{1, w, plan_ragged_split(units, num_kb, sm_count)};
     }
-    const int64_t tiles = (M + 127) / 128;
-    int64_t chains = sm_count / tiles;
-    chains = chains < 1 ? 1 : (chains > parts ? parts : chains);
-    s.chains = (int)chains;
-    s.shrink_split = plan_ragged_split(tiles * chains, num_kb, sm_count);
+    s.shrink_w = s.expand.tile_w < 128 ? s.expand.tile_w : 128;
+    if (M > 128 && (M + 127) / 128 * 2 <= sm_count) s.shrink_w = 64;
+    const int64_t tiles = (M + s.shrink_w - 1) / s.shrink_w;
+    s.shrink_split = plan_ragged_split(tiles, num_kb, sm_count);
+    const int64_t chains = sm_count / (tiles * s.shrink_split);
+    s.chains = (int)(chains < 1 ? 1 : (chains > parts ? parts : chains));
     return s;
 }
 
