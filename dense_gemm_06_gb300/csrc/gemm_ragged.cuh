@@ -32,6 +32,7 @@ enum RaggedMap {
 struct RaggedParams {
     CUtensorMap map[kRaggedMaps];
     const int32_t* offsets;  // rows, depth: G + 1 group limits
+    const CUtensorMap* gmaps;  // depth: P's and Q's map of each group (device memory)
     int G;
     int rows;       // rows of C (depth: of each C_g)
     int feats;      // columns of C (shrink: of LB)
@@ -99,9 +100,8 @@ struct RCfg {
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     // shrink: ids[256], slots[256], first[256], warp sums[16] of the row tile's list
     static constexpr int LIST_BYTES = 4096;
-    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
-    // tail[S], tail_peer[S]
-    static constexpr int NUM_BARS = 4 * STAGES + 8;
+    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts
+    static constexpr int NUM_BARS = 2 * STAGES + 8;
     static constexpr int SMEM_BYTES = RING_BYTES + LIST_BYTES + NUM_BARS * 8 + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
@@ -435,9 +435,6 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     const uint32_t never_bar = bar0 + 8u * (2 * C_::STAGES + 5);
     const uint32_t free_bar = bar0 + 8u * (2 * C_::STAGES + 6);   // every CTA's ring is free
     const uint32_t parts_bar = bar0 + 8u * (2 * C_::STAGES + 7);  // partial sums have arrived
-    // depth: a group's last block in this CTA's ring / zeroed by the pair's other CTA
-    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * C_::STAGES + 8 + s); };
-    auto peer_bar = [&](int s) { return bar0 + 8u * (3 * C_::STAGES + 8 + s); };
     int* sm_ids = reinterpret_cast<int*>(smem + C_::RING_BYTES);
     int* sm_slots = sm_ids + 256;
     int* sm_list = sm_ids + 512;
@@ -466,15 +463,13 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
-        if (MODE == kRagDepth ? p.depth > 0 : p.num_kb > 0) {  // no maps without a depth
+        if (MODE != kRagDepth && p.num_kb > 0) {  // no maps without a depth
             tma_prefetch_desc(&p.map[kMapP]);
             tma_prefetch_desc(&p.map[kMapQ]);
         }
         for (int s = 0; s < C_::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
-            mbar_init(tail_bar(s), 1);
-            mbar_init(peer_bar(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar(a), 1);
@@ -535,6 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         int stage = 0;
         uint32_t phase = 0;
         bool waited = false;
+        int map_group = -1;
         Units<CG, MODE> units(p, cluster, list_arg);
         for (bool more = units.next(p, un); more;) {
             const int q_rows = un.width / CG;
@@ -542,6 +538,18 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             const int f0 = un.feat0 + (int)rank * 128;
             int kb0, kb1;
             share(un.nkb, kb0, kb1);
+            const CUtensorMap* gmaps = nullptr;
+            if constexpr (MODE == kRagDepth) {
+                gmaps = p.gmaps + 2 * (int64_t)un.g;
+                if (un.nkb > 0 && un.g != map_group) {  // once per group, by the issuing lane
+                    if (elect_one()) {
+                        tma_desc_acquire(gmaps);
+                        tma_desc_acquire(gmaps + 1);
+                    }
+                    __syncwarp();
+                    map_group = un.g;
+                }
+            }
             // shrink: the adapters whose lanes this unit holds
             const int spu = MODE == kRagShrink ? 128 / p.slot : 1;
             const int s0 = MODE == kRagShrink ? un.g * spu : 0;
@@ -553,25 +561,19 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 const uint32_t sq = sQ0 + stage * C_::Q_BYTES;
                 if constexpr (MODE == kRagDepth) {
                     const int k0 = un.k0 + kb * BK;
-                    const int tail = min(BK, un.k_end - k0);
                     const int nq = q_rows / 64;  // 64-wide chunks of this CTA's rows
-                    // A group's last block also brings the next group's first rows;
-                    // warp 2 overwrites them with zeros before the MMA sees the stage.
-                    const bool whole = tail == BK;
-                    const uint32_t to = whole ? fb : tail_bar(stage);
                     if (kb == kb0 && lane == 0) TC_TRACE(p, 2);
-                    if (kb == kb1 - 1 && lane == 0) TC_TRACE(p, 18);
                     if (elect_one()) {
-                        if (leader || !whole)
-                            mbar_arrive_expect_tx(whole ? full_bar(stage) : tail_bar(stage),
-                                                  (uint32_t)((whole ? CG : 1) * (2 + nq) * 64 *
-                                                             BK * 2));
+                        if (leader)
+                            mbar_arrive_expect_tx(full_bar(stage),
+                                                  (uint32_t)(CG * (2 + nq) * 64 * BK * 2));
+                        // the group's own maps end at its last row: what its last
+                        // block takes beyond is zeros, never another group's values
                         for (int j = 0; j < 2; ++j)
-                            tma_load_2d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], to, f0 + 64 * j,
-                                            k0);
+                            tma_load_2d<CG>(sp + j * 64 * BK * 2, gmaps, fb, f0 + 64 * j, k0);
                         for (int j = 0; j < nq; ++j)
-                            tma_load_2d<CG>(sq + j * 64 * BK * 2, &p.map[kMapQ], to,
-                                            q_row + 64 * j, k0);
+                            tma_load_2d<CG>(sq + j * 64 * BK * 2, gmaps + 1, fb, q_row + 64 * j,
+                                            k0);
                     }
                 } else {
                     const int k0 = kb * BK;
@@ -678,51 +680,47 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 const uint32_t width_bits = (uint32_t)(un.width >> 3) << 17;
                 int kb0, kb1, n = 0, ne = 0;
                 share(un.nkb, kb0, kb1);
-                bool issued = false;  // the unit's first MMA overwrites the accumulator
-                bool acc_ready = false;
-                auto d_tmem = [&]() { return tmem_base + (uint32_t)(acc * ACC_COLS); };
-                auto get_acc = [&]() {  // the accumulator, once the unit needs it
-                    if (acc_ready) return true;
-                    acc_ready = true;
-                    if (!wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) return false;
+                bool issued = false;  // into the accumulator acc: else the first MMA overwrites
+                const uint32_t idesc = idesc0 | width_bits;
+                for (int kb = kb0; kb < kb1 && !aborted;) {
+                    if (!wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
                     tc_fence_after_sync();
-                    return true;
-                };
-                for (int kb = kb0; kb < kb1 && !aborted; ++kb) {
-                    if (!get_acc() || !wait_bar_warp(full_bar(stage), phase, p)) {
-                        aborted = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    if (kb == kb0 && lane == 0) TC_TRACE(p, 5);
-                    if (kb == kb1 - 2 && lane == 0) TC_TRACE(p, 16);
-                    if (kb == kb1 - 1 && lane == 0) TC_TRACE(p, 17);
-                    const uint64_t pd = p_desc0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
-                    const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
-                    auto step = [&](int j) {
-                        mma_f16<CG>(d_tmem(), pd + (uint64_t)(j * (P_STEP >> 4)),
-                                    qd + (uint64_t)(j * (Q_STEP >> 4)), idesc0 | width_bits,
-                                    issued || j != 0 ? 1u : 0u);
-                    };
-                    const int left = MODE == kRagDepth ? un.k_end - un.k0 - kb * BK : BK;
-                    if (elect_one()) {
-                        if (MODE != kRagDepth || left > BK - UMMA_K) {
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+                    const int first = kb;
+                    const int last = FOLD ? min(kb + FOLD_KB, kb1) : kb1;
+                    for (; kb < last; ++kb) {
+                        if (!wait_bar_warp(full_bar(stage), phase, p)) { aborted = true; break; }
+                        tc_fence_after_sync();
+                        if (kb == kb0 && lane == 0) TC_TRACE(p, 5);
+                        const uint64_t pd = p_desc0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
+                        const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
+                        // depth: a group's last block stops at its last 16-deep step
+                        const int left = MODE == kRagDepth ? un.k_end - un.k0 - kb * BK : BK;
+                        if (elect_one()) {
+                            if (MODE != kRagDepth || left > BK - UMMA_K) {
 #pragma unroll
-                            for (int j = 0; j < BK / UMMA_K; ++j) step(j);
-                        } else {  // a group's last block
-                            for (int j = 0; j * UMMA_K < left; ++j) step(j);
+                                for (int j = 0; j < BK / UMMA_K; ++j)
+                                    mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
+                                                qd + (uint64_t)(j * (Q_STEP >> 4)), idesc,
+                                                ((kb - first) | j) != 0 ? 1u : 0u);
+                            } else {
+                                for (int j = 0; j * UMMA_K < left; ++j)
+                                    mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
+                                                qd + (uint64_t)(j * (Q_STEP >> 4)), idesc,
+                                                ((kb - first) | j) != 0 ? 1u : 0u);
+                            }
+                            mma_commit<CG>(empty_bar(stage));
                         }
-                        mma_commit<CG>(empty_bar(stage));
+                        __syncwarp();
+                        if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
                     }
                     issued = true;
-                    __syncwarp();
-                    if (++stage == C_::STAGES) { stage = 0; phase ^= 1u; }
-                    if (FOLD && (kb - kb0) % FOLD_KB == FOLD_KB - 1 && kb + 1 < kb1) {
+                    if (FOLD && kb < kb1 && !aborted) {
                         // hand over this part of the sum, go on in the other accumulator
                         if (elect_one()) mma_commit<CG>(accf_bar(acc));
                         __syncwarp();
                         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-                        issued = acc_ready = false;
+                        issued = false;
                     }
                 }
                 if constexpr (MODE == kRagLora) {
@@ -731,11 +729,13 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     const int32_t* ids;
                     ne = ext_blocks(un.tile, n, ids);
                     for (int e = part; e < ne && !aborted; e += S) {
-                        if (!get_acc() || !wait_bar_warp(full_bar(stage), phase, p)) {
+                        if (!issued && !wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) {
                             aborted = true;
                             break;
                         }
+                        if (!wait_bar_warp(full_bar(stage), phase, p)) { aborted = true; break; }
                         tc_fence_after_sync();
+                        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
                         const uint64_t pd = p_mn0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
                         const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
                         const int steps = min(EXT_K, n * p.slot - e * EXT_K) / UMMA_K;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                             for (int j = 0; j < steps; ++j)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
-                                    mma_f16<CG>(d_tmem(), pd + (uint64_t)(j * (UMMA_K * 128 >> 4)),
+                                    mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (UMMA_K * 128 >> 4)),
                                                 qd + (uint64_t)((j + 2 * h) * (UMMA_K * 2 >> 4)),
                                                 idesc_ext0 | width_bits,
                                                 issued || j + h != 0 ? 1u : 0u);
@@ -1078,52 +1078,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         __syncwarp();
-        if (MODE == kRagDepth && warp == 2) {
-            // A group's last block holds, past the group's end, rows of the next
-            // one: zeros up to the next multiple of 16 (one MMA step; the MMA
-            // stops there), in P and Q both, so that another group's values, which
-            // may be infinite or NaN, never meet a zero of this one's. Then the
-            // stage is full: the leader's warp says so, once its peer has zeroed
-            // its half too.
-            int block = 0;  // of this CTA's ring
-            uint32_t parity = 0;  // bit per stage
-            Units<CG, MODE> units(p, cluster, list_arg);
-            for (bool more = units.next(p, un); more;) {
-                int kb0, kb1;
-                share(un.nkb, kb0, kb1);
-                const int tail = (un.k_end - un.k0) % BK;
-                block += kb1 - kb0;
-                if (tail != 0 && kb1 == un.nkb && kb1 > kb0 && !aborted) {
-                    const int s = (block - 1) % C_::STAGES;
-                    const uint32_t bit = (parity >> s) & 1u;
-                    if (!wait_bar_warp(tail_bar(s), bit, p)) aborted = true;
-                    if (lane == 0) TC_TRACE(p, 14);
-                    const int rows16 = (tail + UMMA_K - 1) / UMMA_K * UMMA_K;
-                    const int nq = un.width / CG / 64;
-                    if (!aborted) {
-                        for (int j = 0; j < 2 + nq; ++j) {
-                            const uint32_t at =
-                                (j < 2 ? sP0 + s * C_::P_BYTES + j * 64 * BK * 2
-                                       : sQ0 + s * C_::Q_BYTES + (j - 2) * 64 * BK * 2);
-                            for (int i = tail * 8 + lane; i < rows16 * 8; i += 32)
-                                sts128(at + (uint32_t)i * 16u, 0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_all();  // before the MMA reads them
-                    }
-                    __syncwarp();
-                    if (lane == 0) TC_TRACE(p, 15);
-                    if (CG == 2 && leader && !aborted && !wait_bar_warp(peer_bar(s), bit, p))
-                        aborted = true;
-                    if (lane == 0 && !aborted) {
-                        if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(peer_bar(s), 0));
-                        else mbar_arrive_local(full_bar(s));
-                    }
-                    parity ^= 1u << s;
-                }
-                more = units.next(p, un);
-                if (S > 1 && more) cluster_sync_all();
-            }
-        } else if (S > 1) {
+        if (S > 1) {
             Units<CG, MODE> units(p, cluster, list_arg);
             for (bool more = units.next(p, un); more;) {
                 more = units.next(p, un);

@@ -126,6 +126,26 @@ __device__ __forceinline__ void tma_prefetch_desc(const void* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
 }
 
+// A tensor map in shared memory (128-byte aligned): sets the size of its
+// dimension 1 (rows of a 2-D map).
+__device__ __forceinline__ void tma_desc_set_rows(uint32_t smem_map, uint32_t rows) {
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
+                 :: "r"(smem_map), "r"(rows) : "memory");
+}
+
+// Copies a tensor map from shared to global memory (both 128-byte aligned) and
+// releases it for use by TMA; the whole warp calls it.
+__device__ __forceinline__ void tma_desc_publish(void* map, uint32_t smem_map) {
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
+        " [%0], [%1], 128;" :: "l"(map), "r"(smem_map) : "memory");
+}
+
+// Before this thread's first TMA copy through a map that tma_desc_publish wrote.
+__device__ __forceinline__ void tma_desc_acquire(const void* map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" :: "l"(map) : "memory");
+}
+
 // 2-D tiled TMA load into this CTA's shared memory, completing on the
 // mbarrier at `bar` (a shared::cluster address). With CG == 2 the barrier may
 // live in the peer CTA of the pair (.cta_group::2).
