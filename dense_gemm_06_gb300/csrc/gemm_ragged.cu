@@ -183,6 +183,20 @@ bool map_3d(RaggedParams& rp, int i, bool bf16, const Operand& o, uint32_t box_o
                          (uint64_t)o.ld, (uint64_t)o.mats, (uint64_t)stride, 64, box_outer);
 }
 
+// C by TMA where its rows (and matrices) are 16-byte aligned and nothing is
+// fused: a box is one staging tile, 32 features by as many rows as 2 KB hold.
+void map_c(RaggedParams& rp, int dtype, void* C, int64_t mats, int64_t stride, int64_t rows,
+           int64_t cols, int64_t ld) {
+    const int es = c_bytes(dtype);
+    if (rp.epi.active || !aligned_to(C, 16) || ld * es % 16 || (mats > 1 && stride * es % 16))
+        return;
+    rp.c_tma = encode_tma_c(&rp.map[kMapC], es == 4, is_bf16(dtype), C, (uint64_t)cols,
+                            (uint64_t)rows, (uint64_t)ld, (uint64_t)mats,
+                            (uint64_t)(mats == 1 ? rows * ld : stride), 32,
+                            (uint32_t)(RCfg::TILE_BYTES / (32 * es)))
+                   ? 1 : 0;
+}
+
 void common_params(RaggedParams& rp, const DeviceInfo& dev) {
     rp.pdl = 1;
     rp.err = dev.err_word;
@@ -287,6 +301,7 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     rp.C = C;
     rp.ldc = ldc;
     rp.epi = epi_params(epi);
+    map_c(rp, dtype, C, 0, 0, M, N, ldc);
     const int64_t units = ((G < M ? G : M) + M / shape.tile_w) * rp.tiles_f;
     if (!units_fit(units, shape.cta_group * shape.split)) return kUnsupported;
 
@@ -363,6 +378,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rp.ldc = ldc;
     rp.stridec = stridec;
     rp.epi = epi_params(epi);
+    map_c(rp, dtype, C, G, stridec, M, N, ldc);
     const int64_t units = G * rp.tiles_f * rp.tiles_r;
     if ((int64_t)rp.tiles_f * rp.tiles_r > INT32_MAX / G ||
         !units_fit(units, shape.cta_group * shape.split))
@@ -510,6 +526,7 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         rp.C = static_cast<uint16_t*>(C) + m0 * ldc;
         rp.ldc = ldc;
         rp.epi = epi_params(epi);
+        map_c(rp, dtype, rp.C, 0, 0, m, N, ldc);
         rp.tile_w = W;
         rp.tiles_r = (int)tiles;
         rp.tiles_f = (int)((N + 128 * ex.cta_group - 1) / (128 * ex.cta_group));

@@ -26,7 +26,8 @@ enum RaggedMap {
     kMapQ16 = 2,  // rows, 16 per box (units narrower than the tile)
     kMapLB = 3,   // lora: LB
     kMapT = 4, kMapT16 = 5,  // lora: T, as Q and Q16
-    kRaggedMaps = 6
+    kMapC = 6,    // C, a staging tile per box (depth: 3-D), where c_tma
+    kRaggedMaps = 7
 };
 
 struct RaggedParams {
@@ -43,6 +44,7 @@ struct RaggedParams {
     int tiles_r;    // row tiles (depth: per group)
     int split;      // log2 of the CTAs that share a unit's depth (a cluster of single CTAs)
     void* C;
+    int c_tma;        // C's rows are 16-byte aligned: whole pieces go out by TMA
     int64_t ldc;
     int64_t stridec;  // depth: between the C_g
     EpiParams epi;
@@ -98,11 +100,16 @@ struct RCfg {
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
     static constexpr int STAGES = 6;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-    // shrink: ids[256], slots[256], first[256], warp sums[16] of the row tile's list
-    static constexpr int LIST_BYTES = 4096;
-    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts
-    static constexpr int NUM_BARS = 2 * STAGES + 8;
-    static constexpr int SMEM_BYTES = RING_BYTES + LIST_BYTES + NUM_BARS * 8 + 16 + 1024;
+    // Two 2 KB staging tiles per epilogue warp (shrink: its list instead --
+    // ids[256], slots[256], list[256], warp sums[16])
+    static constexpr int TILE_BYTES = 2048;
+    static constexpr int EXTRA_BYTES = EPI_WARPS * 2 * TILE_BYTES;
+    // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
+    // unit_ready[UNITS], unit_read[UNITS]; then the TMEM address and the units
+    static constexpr int UNITS = 4;
+    static constexpr int NUM_BARS = 2 * STAGES + 8 + 2 * UNITS;
+    static constexpr int UNIT_OFFSET = NUM_BARS * 8 + 16;
+    static constexpr int SMEM_BYTES = RING_BYTES + EXTRA_BYTES + UNIT_OFFSET + UNITS * 48 + 1024;
     static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
 // fp32 results: depth summed in one accumulator, in k-blocks. The tensor core
@@ -280,6 +287,54 @@ struct Units<1, kRagShrink> {
     }
 };
 
+// A unit passed through shared memory, 48 bytes per slot.
+__device__ __forceinline__ void put_unit(uint32_t at, const RUnit& un, bool more) {
+    sts128(at, (uint32_t)un.g, (uint32_t)un.row0, (uint32_t)un.row_end, (uint32_t)un.feat0);
+    sts128(at + 16, (uint32_t)un.width, (uint32_t)un.k0, (uint32_t)un.nkb, (uint32_t)un.k_end);
+    sts128(at + 32, (uint32_t)un.tile, more ? 1u : 0u, 0u, 0u);
+}
+__device__ __forceinline__ bool get_unit(uint32_t at, RUnit& un) {
+    const uint4 a = lds128(at), b = lds128(at + 16), c = lds128(at + 32);
+    un.g = (int)a.x; un.row0 = (int)a.y; un.row_end = (int)a.z; un.feat0 = (int)a.w;
+    un.width = (int)b.x; un.k0 = (int)b.y; un.nkb = (int)b.z; un.k_end = (int)b.w;
+    un.tile = (int)c.x;
+    return c.y != 0;
+}
+
+// A wait on the unit slots. It outlasts a timeout of another wait of the
+// launch: every role goes on taking units after one, so that the clusters'
+// barriers stay in step, and the slots keep moving.
+__device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity, const RaggedParams& p) {
+    if (!mbar_try_wait(bar, parity)) {
+        const uint64_t t0 = globaltimer_ns(), limit = 2 * p.wait_limit_ns + 1000000000ull;
+        while (!mbar_try_wait(bar, parity))
+            if (globaltimer_ns() - t0 > limit) {
+                gen_record_timeout(p.err, p.gen);
+                return false;
+            }
+    }
+    return true;
+}
+
+// The units of a role, in order, as warp 2 finds them (finding one takes 0.5
+// to 1.4 us of searches, divisions and reads of the limits, which the MMA
+// would otherwise wait for at every unit).
+struct Feed {
+    uint32_t ready, slots;  // the first ready barrier and slot
+    int j;
+    __device__ __forceinline__ Feed(uint32_t r, uint32_t s) : ready(r), slots(s), j(0) {}
+    __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
+        const int s = j % RCfg::UNITS;
+        if (!__all_sync(0xffffffffu, wait_unit(ready + 8u * s, (uint32_t)(j / RCfg::UNITS) & 1u, p)))
+            return false;
+        const bool more = get_unit(slots + 48u * s, un);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_local(ready + 8u * (RCfg::UNITS + s));
+        ++j;
+        return more;
+    }
+};
+
 template <bool BF16>
 __device__ __forceinline__ bool nonfinite16(uint32_t w) {
     constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
@@ -297,6 +352,17 @@ __device__ __forceinline__ void store_c(const RaggedParams& p, OutT* dst, float 
         x = activate(x + bias, p.epi.act);
     }
     *dst = from_f32<OutT>(x);
+}
+
+// x, rounded to T, into shared memory.
+template <typename T>
+__device__ __forceinline__ void sts_as(uint32_t addr, float x) {
+    const T t = from_f32<T>(x);
+    if constexpr (sizeof(T) == 4)
+        asm volatile("st.shared.f32 [%0], %1;" :: "r"(addr), "f"(t) : "memory");
+    else
+        asm volatile("st.shared.b16 [%0], %1;"
+                     :: "r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&t)) : "memory");
 }
 
 // t as two 16-bit numbers, 32 elements apart.
@@ -426,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
 
     const uint32_t sP0 = base;
     const uint32_t sQ0 = base + C_::STAGES * C_::P_BYTES;
-    const uint32_t bar0 = base + C_::RING_BYTES + C_::LIST_BYTES;
+    const uint32_t bar0 = base + C_::RING_BYTES + C_::EXTRA_BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (C_::STAGES + s); };
     auto accf_bar = [&](int a) { return bar0 + 8u * (2 * C_::STAGES + a); };
@@ -435,11 +501,13 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     const uint32_t never_bar = bar0 + 8u * (2 * C_::STAGES + 5);
     const uint32_t free_bar = bar0 + 8u * (2 * C_::STAGES + 6);   // every CTA's ring is free
     const uint32_t parts_bar = bar0 + 8u * (2 * C_::STAGES + 7);  // partial sums have arrived
+    const uint32_t ready_bar = bar0 + 8u * (2 * C_::STAGES + 8);  // [UNITS], then read[UNITS]
+    const uint32_t unit_slots = bar0 + (uint32_t)C_::UNIT_OFFSET;
     int* sm_ids = reinterpret_cast<int*>(smem + C_::RING_BYTES);
     int* sm_slots = sm_ids + 256;
     int* sm_list = sm_ids + 512;
     int* sm_sums = sm_ids + 768;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::RING_BYTES + C_::LIST_BYTES +
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::RING_BYTES + C_::EXTRA_BYTES +
                                                       8 * C_::NUM_BARS);
 
     const int warp = threadIdx.x >> 5;
@@ -479,6 +547,11 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         mbar_init(never_bar, 1);
         mbar_init(free_bar, S);
         mbar_init(parts_bar, S * EPI_WARPS);
+        for (int i = 0; i < C_::UNITS; ++i) {
+            mbar_init(ready_bar + 8u * i, 1);
+            // read by the producer, the epilogue warps and the leader's MMA warp
+            mbar_init(ready_bar + 8u * (C_::UNITS + i), 1 + EPI_WARPS + (leader ? 1 : 0));
+        }
         fence_mbarrier_init_cluster();
     }
     if (warp == 1) {
@@ -531,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         uint32_t phase = 0;
         bool waited = false;
         int map_group = -1;
-        Units<CG, MODE> units(p, cluster, list_arg);
+        Feed units(ready_bar, unit_slots);
         for (bool more = units.next(p, un); more;) {
             const int q_rows = un.width / CG;
             const int q_row = un.row0 + (int)rank * q_rows;
@@ -675,16 +748,19 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             int acc = 0;
             uint32_t acc_phase = 0;
             bool waited = false;
-            Units<CG, MODE> units(p, cluster, list_arg);
+            int nt = 0;  // units issued (trace slots)
+            Feed units(ready_bar, unit_slots);
             for (bool more = units.next(p, un); more;) {
                 const uint32_t width_bits = (uint32_t)(un.width >> 3) << 17;
                 int kb0, kb1, n = 0, ne = 0;
                 share(un.nkb, kb0, kb1);
                 bool issued = false;  // into the accumulator acc: else the first MMA overwrites
+                if (lane == 0) TC_TRACE(p, 20 + 4 * nt);
                 const uint32_t idesc = idesc0 | width_bits;
                 for (int kb = kb0; kb < kb1 && !aborted;) {
                     if (!wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
                     tc_fence_after_sync();
+                    if (kb == kb0 && lane == 0) TC_TRACE(p, 21 + 4 * nt);
                     const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
                     const int first = kb;
                     const int last = FOLD ? min(kb + FOLD_KB, kb1) : kb1;
@@ -692,6 +768,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                         if (!wait_bar_warp(full_bar(stage), phase, p)) { aborted = true; break; }
                         tc_fence_after_sync();
                         if (kb == kb0 && lane == 0) TC_TRACE(p, 5);
+                        if (kb == kb0 && lane == 0) TC_TRACE(p, 22 + 4 * nt);
                         const uint64_t pd = p_desc0 + (uint64_t)(stage * (C_::P_BYTES >> 4));
                         const uint64_t qd = q_desc0 + (uint64_t)(stage * (C_::Q_BYTES >> 4));
                         // depth: a group's last block stops at its last 16-deep step
@@ -756,6 +833,8 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     }
                 }
                 if (lane == 0) TC_TRACE(p, 6);
+                if (lane == 0) TC_TRACE(p, 23 + 4 * nt);
+                ++nt;
                 if (issued && !aborted) {
                     if (elect_one()) mma_commit<CG>(accf_bar(acc));
                     __syncwarp();
@@ -781,6 +860,10 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         const int half = (warp - EPI_WARP0) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0, split_phase = 0;
+        constexpr int PIECE = C_::TILE_BYTES / (32 * (int)sizeof(OutT));
+        const uint32_t tiles =
+            base + C_::RING_BYTES + (uint32_t)((warp - EPI_WARP0) * 2 * C_::TILE_BYTES);
+        int tile_i = 0;
         pdl_wait();
         if (p.fault_inject == 1) {
             if (!__all_sync(0xffffffffu, wait_bar(never_bar, 0u, p))) aborted = true;
@@ -819,7 +902,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 flag[me * EPI_WARPS + (warp - EPI_WARP0)] = bad ? 1 : 0;
             }
         }
-        Units<CG, MODE> units(p, cluster, list_arg);
+        Feed units(ready_bar, unit_slots);
         for (bool more = units.next(p, un); more;) {
             int kb0, kb1, n = 0, ne = 0;
             share(un.nkb, kb0, kb1);
@@ -894,6 +977,42 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     for (int i = 0; i < 32; ++i) {
                         if (i < left) store_t<In>(dst, s[i] == my_slot ? v[i] * factor : 0.f);
                         dst += p.ldt;
+                    }
+                    return;
+                }
+                if (!epi && !by_hand && p.c_tma && f - lane + 32 <= p.feats) {
+                    // Pieces of PIECE rows by 32 features through the warp's staging
+                    // tiles, one being written while TMA reads the other; a piece
+                    // with rows past the group's end is stored row by row.
+#pragma unroll
+                    for (int r = 0; r < 32; r += PIECE) {
+                        const int row = un.row0 + c * 32 + r;
+                        if (r + PIECE <= left) {
+                            const uint32_t tile = tiles + (uint32_t)(tile_i * C_::TILE_BYTES);
+                            tile_i ^= 1;
+                            if (lane == 0) bulk_wait_read_1();
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < PIECE; ++i)
+                                sts_as<OutT>(tile + (uint32_t)((i * 32 + lane) * sizeof(OutT)),
+                                             v[r + i]);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && c_checked(p, row, f) &&
+                                c_checked(p, row + PIECE - 1, f + 31)) {
+                                if constexpr (MODE == kRagDepth)
+                                    tma_store_3d(&p.map[kMapC], tile, f, row, un.g);
+                                else
+                                    tma_store_2d(&p.map[kMapC], tile, f, row);
+                                bulk_commit_group();
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < PIECE; ++i)
+                                if (r + i < left && c_checked(p, row + i, f))
+                                    c_col[(int64_t)(c * 32 + r + i) * p.ldc] =
+                                        from_f32<OutT>(v[r + i]);
+                        }
                     }
                     return;
                 }
@@ -1061,12 +1180,14 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             more = units.next(p, un);
             if (S > 1 && more) cluster_sync_all();
         }
+        if (MODE != kRagShrink && p.c_tma && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
-        // Warp 3 of the first CTA looks over the group limits (the others clamp
-        // what is wrong with them); both idle warps keep the clusters' barrier.
+        // Warp 2 finds the units and passes them on, up to UNITS ahead; warp 3 of
+        // the first CTA looks over the group limits (the others clamp what is wrong
+        // with them). Both take part in the barrier between a split's units.
+        if constexpr (MODE == kRagRows || MODE == kRagDepth) pdl_wait();
         if constexpr (MODE == kRagRows || MODE == kRagDepth) {
-            pdl_wait();
             if (blockIdx.x == 0 && warp == 3) {
                 const int most = MODE == kRagRows ? p.rows : p.depth;
                 bool bad = false;
@@ -1078,11 +1199,24 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         __syncwarp();
-        if (S > 1) {
+        if (warp == 2 || S > 1) {
             Units<CG, MODE> units(p, cluster, list_arg);
-            for (bool more = units.next(p, un); more;) {
+            bool more = true;
+            for (int j = 0; more; ++j) {
                 more = units.next(p, un);
-                if (more) cluster_sync_all();
+                if (warp == 2) {
+                    const int s = j % C_::UNITS;
+                    if (j >= C_::UNITS &&
+                        !wait_unit(ready_bar + 8u * (C_::UNITS + s),
+                                   (uint32_t)(j / C_::UNITS - 1) & 1u, p))
+                        break;
+                    if (lane == 0) {
+                        put_unit(unit_slots + 48u * s, un, more);
+                        mbar_arrive_local(ready_bar + 8u * s);
+                    }
+                    __syncwarp();
+                }
+                if (S > 1 && j > 0 && more) cluster_sync_all();
             }
         }
     }

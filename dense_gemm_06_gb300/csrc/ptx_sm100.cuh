@@ -254,6 +254,13 @@ __device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int3
                  :: "l"(map), "r"(x), "r"(y), "r"(src) : "memory");
 }
 
+// 3-D tiled TMA store.
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int32_t x, int32_t y,
+                                             int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 :: "l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -261,6 +268,11 @@ __device__ __forceinline__ void bulk_commit_group() {
 // Wait until every committed bulk store has finished READING shared memory.
 __device__ __forceinline__ void bulk_wait_read_all() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// Wait until all but the last committed bulk store have finished reading.
+__device__ __forceinline__ void bulk_wait_read_1() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
 // Wait until every committed bulk store has completed.
