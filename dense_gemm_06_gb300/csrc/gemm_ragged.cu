@@ -114,14 +114,17 @@ __global__ void __launch_bounds__(256) repack16_mats_kernel(const __grid_constan
 }
 
 // gemm_grouped_k: the two operands' tensor maps once per group, cut off at the
-// group's last row, so that TMA fills its last block with zeros. A warp per
-// group. (Zeroing the block in shared memory instead put a hand-over of 1-2 us
+// group's last row, so that TMA fills its last block with zeros; the order of
+// the groups, the longest first (for up to kMaxSorted groups: each warp ranks
+// its group among all), so that the units handed out last are short ones; and
+// the count of units taken. A warp per group. (Zeroing the block in shared memory instead put a hand-over of 1-2 us
 // between the copy and the MMA of every unit: 64 groups of 769 rows took
 // 536 us that way, 389 this way, 64 of 768, which need no zeros, 351.)
-constexpr int kMapWarps = 4;
+constexpr int kMapWarps = 4, kMaxSorted = 4096;
 __global__ void __launch_bounds__(32 * kMapWarps)
     depth_maps_kernel(const __grid_constant__ CUtensorMap pm, const __grid_constant__ CUtensorMap qm,
-                      const int32_t* offsets, int G, int depth, CUtensorMap* out) {
+                      const int32_t* offsets, int G, int depth, CUtensorMap* out, int32_t* order,
+                      unsigned int* ticket) {
     gemm_ptx::pdl_launch_dependents();
     __shared__ __align__(128) uint32_t maps[kMapWarps][2][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,6 +134,17 @@ __global__ void __launch_bounds__(32 * kMapWarps)
     maps[w][1][lane] = reinterpret_cast<const uint32_t*>(&qm)[lane];
     const int lo = clampi(offsets[g], 0, depth);
     const int hi = clampi(offsets[g + 1], lo, depth);
+    if (g == 0 && lane == 0) *ticket = 0;
+    int rank = 0;
+    if (G <= kMaxSorted)
+        for (int h = lane; h < G; h += 32) {
+            const int a = clampi(offsets[h], 0, depth);
+            const int n = clampi(offsets[h + 1], a, depth) - a;
+            rank += n > hi - lo || (n == hi - lo && h < g);
+        }
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    if (lane == 0) order[G <= kMaxSorted ? rank : g] = g;
+    if (depth == 0) return;  // no maps, and no use of them
     __syncwarp();
     for (int i = 0; i < 2; ++i) {
         const uint32_t at = gemm_ptx::smem_u32(&maps[w][i][0]);
@@ -183,17 +197,16 @@ bool map_3d(RaggedParams& rp, int i, bool bf16, const Operand& o, uint32_t box_o
                          (uint64_t)o.ld, (uint64_t)o.mats, (uint64_t)stride, 64, box_outer);
 }
 
-// C by TMA where its rows (and matrices) are 16-byte aligned and nothing is
-// fused: a box is one staging tile, 32 features by as many rows as 2 KB hold.
+// A 16-bit C by TMA where its rows (and matrices) are 16-byte aligned and
+// nothing is fused: a box is one staging tile, 32 features by 32 rows.
 void map_c(RaggedParams& rp, int dtype, void* C, int64_t mats, int64_t stride, int64_t rows,
            int64_t cols, int64_t ld) {
-    const int es = c_bytes(dtype);
-    if (rp.epi.active || !aligned_to(C, 16) || ld * es % 16 || (mats > 1 && stride * es % 16))
+    if (c_bytes(dtype) != 2 || rp.epi.active || !aligned_to(C, 16) || ld % 8 ||
+        (mats > 1 && stride % 8))
         return;
-    rp.c_tma = encode_tma_c(&rp.map[kMapC], es == 4, is_bf16(dtype), C, (uint64_t)cols,
-                            (uint64_t)rows, (uint64_t)ld, (uint64_t)mats,
-                            (uint64_t)(mats == 1 ? rows * ld : stride), 32,
-                            (uint32_t)(RCfg::TILE_BYTES / (32 * es)))
+    rp.c_tma = encode_tma_c16(&rp.map[kMapC], is_bf16(dtype), C, (uint64_t)cols, (uint64_t)rows,
+                              (uint64_t)ld, (uint64_t)mats,
+                              (uint64_t)(mats == 1 ? rows * ld : stride), 32, 32)
                    ? 1 : 0;
 }
 
@@ -385,22 +398,28 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
         return kUnsupported;
 
     Scratch scratch{pool, s, dev->device};
+    Operand* const ops[2] = {&a, &b};
+    const int64_t map_bytes = G * 2 * (int64_t)sizeof(CUtensorMap);
+    const int64_t plan_bytes = up(map_bytes + (G + 1) * 4, 256);
+    char* at = static_cast<char*>(
+        scratch.get((size_t)(plan_bytes + (K > 0 ? repack_bytes(ops, 2) : 0))));
+    if (!at) return kCuda;
+    CUtensorMap* gmaps = reinterpret_cast<CUtensorMap*>(at);
+    int32_t* order = reinterpret_cast<int32_t*>(at + map_bytes);
+    unsigned int* ticket = reinterpret_cast<unsigned int*>(order + G);
+    rp.gmaps = gmaps;
+    rp.order = order;
+    rp.ticket = ticket;
     if (K > 0) {
-        Operand* const ops[2] = {&a, &b};
-        const int64_t map_bytes = up(G * 2 * (int64_t)sizeof(CUtensorMap), 256);
-        char* at = static_cast<char*>(scratch.get((size_t)(map_bytes + repack_bytes(ops, 2))));
-        if (!at) return kCuda;
-        CUtensorMap* gmaps = reinterpret_cast<CUtensorMap*>(at);
-        rp.gmaps = gmaps;
-        rc = repack(ops, 2, at + map_bytes, *dev, s);
+        rc = repack(ops, 2, at + plan_bytes, *dev, s);
         if (rc == kOk && !(map_2d(rp, kMapP, bf16, b, BK) && map_2d(rp, kMapQ, bf16, a, BK)))
             rc = kCuda;
-        if (rc == kOk) {
-            depth_maps_kernel<<<(int)((G + kMapWarps - 1) / kMapWarps), 32 * kMapWarps, 0, s>>>(
-                rp.map[kMapP], rp.map[kMapQ], offsets, (int)G, (int)K, gmaps);
-            if (cudaGetLastError() != cudaSuccess) rc = kCuda;
-            else note_launch();
-        }
+    }
+    if (rc == kOk) {
+        depth_maps_kernel<<<(int)((G + kMapWarps - 1) / kMapWarps), 32 * kMapWarps, 0, s>>>(
+            rp.map[kMapP], rp.map[kMapQ], offsets, (int)G, (int)K, gmaps, order, ticket);
+        if (cudaGetLastError() != cudaSuccess) rc = kCuda;
+        else note_launch();
     }
     if (rc == kOk) rc = launch(rp, kRagDepth, shape.cta_group, true, units, dtype, *dev, s);
     scratch.release();

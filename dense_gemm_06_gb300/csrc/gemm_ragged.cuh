@@ -33,7 +33,11 @@ enum RaggedMap {
 struct RaggedParams {
     CUtensorMap map[kRaggedMaps];
     const int32_t* offsets;  // rows, depth: G + 1 group limits
-    const CUtensorMap* gmaps;  // depth: P's and Q's map of each group (device memory)
+    // depth, in device memory: P's and Q's map of each group, the order of the
+    // groups and the count of units taken
+    const CUtensorMap* gmaps;
+    const int32_t* order;
+    unsigned int* ticket;
     int G;
     int rows;       // rows of C (depth: of each C_g)
     int feats;      // columns of C (shrink: of LB)
@@ -44,7 +48,7 @@ struct RaggedParams {
     int tiles_r;    // row tiles (depth: per group)
     int split;      // log2 of the CTAs that share a unit's depth (a cluster of single CTAs)
     void* C;
-    int c_tma;        // C's rows are 16-byte aligned: whole pieces go out by TMA
+    int c_tma;        // a 16-bit C with 16-byte aligned rows: whole pieces go out by TMA
     int64_t ldc;
     int64_t stridec;  // depth: between the C_g
     EpiParams epi;
@@ -105,9 +109,10 @@ struct RCfg {
     static constexpr int TILE_BYTES = 2048;
     static constexpr int EXTRA_BYTES = EPI_WARPS * 2 * TILE_BYTES;
     // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
-    // unit_ready[UNITS], unit_read[UNITS]; then the TMEM address and the units
+    // unit_ready[UNITS], unit_read[UNITS], unit_read_by_peer[UNITS]; then the TMEM
+    // address and the units
     static constexpr int UNITS = 4;
-    static constexpr int NUM_BARS = 2 * STAGES + 8 + 2 * UNITS;
+    static constexpr int NUM_BARS = 2 * STAGES + 8 + 3 * UNITS;
     static constexpr int UNIT_OFFSET = NUM_BARS * 8 + 16;
     static constexpr int SMEM_BYTES = RING_BYTES + EXTRA_BYTES + UNIT_OFFSET + UNITS * 48 + 1024;
     static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
@@ -223,21 +228,33 @@ template <int CG, int MODE>
 struct Units {
     RowWalk walk;
     int u, step;
+    bool started;
 
     __device__ __forceinline__ Units(const RaggedParams& p, int cluster, int clusters)
-        : u(cluster), step(clusters) {
+        : u(cluster), step(clusters), started(false) {
         if constexpr (MODE == kRagRows) walk.start(p);
     }
     __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
-        const int t = u;
+        int t = u;
         u += step;
+        if constexpr (MODE == kRagDepth) {
+            // After its first unit a cluster takes the next one that nobody has:
+            // the groups, and so the units, are of any size (see depth_maps_kernel
+            // for the order).
+            if (started) {
+                if ((threadIdx.x & 31) == 0) t = step + (int)atomicAdd(p.ticket, 1u);
+                t = __shfl_sync(0xffffffffu, t, 0);
+            }
+            started = true;
+        }
         if constexpr (MODE == kRagRows) {
             return walk.template find<CG>(p, t, un);
         } else if constexpr (MODE == kRagDepth) {
             const int per = p.tiles_r * p.tiles_f;
             if (t >= p.G * per) return false;
-            un.g = t / per;
-            const TileCoord tc = raster(t - un.g * per, p.tiles_r, p.tiles_f);
+            const int nth = t / per;
+            un.g = __ldcg(p.order + nth);
+            const TileCoord tc = raster(t - nth * per, p.tiles_r, p.tiles_f);
             un.row0 = tc.tm * p.tile_w;
             un.row_end = p.rows;
             un.feat0 = tc.tn * 128 * CG;
@@ -287,11 +304,14 @@ struct Units<1, kRagShrink> {
     }
 };
 
-// A unit passed through shared memory, 48 bytes per slot.
+// A unit passed through shared memory (a shared::cluster address), 48 bytes per
+// slot.
 __device__ __forceinline__ void put_unit(uint32_t at, const RUnit& un, bool more) {
-    sts128(at, (uint32_t)un.g, (uint32_t)un.row0, (uint32_t)un.row_end, (uint32_t)un.feat0);
-    sts128(at + 16, (uint32_t)un.width, (uint32_t)un.k0, (uint32_t)un.nkb, (uint32_t)un.k_end);
-    sts128(at + 32, (uint32_t)un.tile, more ? 1u : 0u, 0u, 0u);
+    st_cluster_v4(at, (uint32_t)un.g, (uint32_t)un.row0, (uint32_t)un.row_end,
+                  (uint32_t)un.feat0);
+    st_cluster_v4(at + 16, (uint32_t)un.width, (uint32_t)un.k0, (uint32_t)un.nkb,
+                  (uint32_t)un.k_end);
+    st_cluster_v4(at + 32, (uint32_t)un.tile, more ? 1u : 0u, 0u, 0u);
 }
 __device__ __forceinline__ bool get_unit(uint32_t at, RUnit& un) {
     const uint4 a = lds128(at), b = lds128(at + 16), c = lds128(at + 32);
@@ -316,9 +336,11 @@ __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity, const R
     return true;
 }
 
-// The units of a role, in order, as warp 2 finds them (finding one takes 0.5
-// to 1.4 us of searches, divisions and reads of the limits, which the MMA
-// would otherwise wait for at every unit).
+// The units of a role, in order, as warp 2 (a pair's leader's) finds them:
+// finding one takes 0.5 to 1.4 us of searches, divisions and reads of the
+// limits, which the MMA would otherwise wait for at every unit.
+// (Each arrival here is local and of CTA scope: a release at cluster scope
+// waits for the warp's outstanding stores of C, 1 to 2 us per unit.)
 struct Feed {
     uint32_t ready, slots;  // the first ready barrier and slot
     int j;
@@ -354,15 +376,12 @@ __device__ __forceinline__ void store_c(const RaggedParams& p, OutT* dst, float 
     *dst = from_f32<OutT>(x);
 }
 
-// x, rounded to T, into shared memory.
+// x, rounded to a 16-bit T, into shared memory.
 template <typename T>
 __device__ __forceinline__ void sts_as(uint32_t addr, float x) {
     const T t = from_f32<T>(x);
-    if constexpr (sizeof(T) == 4)
-        asm volatile("st.shared.f32 [%0], %1;" :: "r"(addr), "f"(t) : "memory");
-    else
-        asm volatile("st.shared.b16 [%0], %1;"
-                     :: "r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&t)) : "memory");
+    asm volatile("st.shared.b16 [%0], %1;"
+                 :: "r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&t)) : "memory");
 }
 
 // t as two 16-bit numbers, 32 elements apart.
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int S = CG == 1 ? 1 << p.split : 1;
+    const int S = CG == 1 && MODE != kRagDepth ? 1 << p.split : 1;  // depth: units by ticket
     const uint32_t crank = CG == 2 || S > 1 ? cluster_ctarank() : 0u;
     const uint32_t rank = CG == 2 ? crank : 0u;   // side of the pair
     const int part = S > 1 ? (int)crank : 0;      // share of the depth
@@ -551,6 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             mbar_init(ready_bar + 8u * i, 1);
             // read by the producer, the epilogue warps and the leader's MMA warp
             mbar_init(ready_bar + 8u * (C_::UNITS + i), 1 + EPI_WARPS + (leader ? 1 : 0));
+            mbar_init(ready_bar + 8u * (2 * C_::UNITS + i), 1);  // read in the pair's other CTA
         }
         fence_mbarrier_init_cluster();
     }
@@ -580,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
     RUnit un;
     // k-blocks [kb0, kb1) of a unit are this CTA's (all of them but for a split)
     auto share = [&](int n, int& a, int& b) {
-        const int sh = CG == 1 ? p.split : 0;
+        const int sh = CG == 1 && MODE != kRagDepth ? p.split : 0;
         a = (n >> sh) * part + (((n & (S - 1)) * part) >> sh);
         b = (n >> sh) * (part + 1) + (((n & (S - 1)) * (part + 1)) >> sh);
     };
@@ -860,10 +880,15 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         const int half = (warp - EPI_WARP0) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0, split_phase = 0;
-        constexpr int PIECE = C_::TILE_BYTES / (32 * (int)sizeof(OutT));
+        // 16-bit results leave in 32 x 32 chunks by TMA (rows K-major at a depth of
+        // 2048: 323 us against 337 us by st.global, whose 64-byte rows take the
+        // shared-memory port that the operands need); fp32 ones, with 128-byte rows,
+        // row by row (2.4 us per unit against 3.0 us through staging tiles).
+        constexpr bool BY_TMA = MODE != kRagShrink && sizeof(OutT) == 2;
         const uint32_t tiles =
             base + C_::RING_BYTES + (uint32_t)((warp - EPI_WARP0) * 2 * C_::TILE_BYTES);
         int tile_i = 0;
+        int nt = 0;  // units stored (trace slots)
         pdl_wait();
         if (p.fault_inject == 1) {
             if (!__all_sync(0xffffffffu, wait_bar(never_bar, 0u, p))) aborted = true;
@@ -980,41 +1005,29 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     }
                     return;
                 }
-                if (!epi && !by_hand && p.c_tma && f - lane + 32 <= p.feats) {
-                    // Pieces of PIECE rows by 32 features through the warp's staging
-                    // tiles, one being written while TMA reads the other; a piece
-                    // with rows past the group's end is stored row by row.
+                if constexpr (BY_TMA) {
+                    if (!epi && !by_hand && p.c_tma && left >= 32 && f - lane + 32 <= p.feats) {
+                        // A whole chunk goes through one of the warp's two staging
+                        // tiles, written while TMA still reads the other.
+                        const uint32_t tile = tiles + (uint32_t)(tile_i * C_::TILE_BYTES);
+                        const int row = un.row0 + c * 32;
+                        tile_i ^= 1;
+                        if (lane == 0) bulk_wait_read_1();
+                        __syncwarp();
 #pragma unroll
-                    for (int r = 0; r < 32; r += PIECE) {
-                        const int row = un.row0 + c * 32 + r;
-                        if (r + PIECE <= left) {
-                            const uint32_t tile = tiles + (uint32_t)(tile_i * C_::TILE_BYTES);
-                            tile_i ^= 1;
-                            if (lane == 0) bulk_wait_read_1();
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < PIECE; ++i)
-                                sts_as<OutT>(tile + (uint32_t)((i * 32 + lane) * sizeof(OutT)),
-                                             v[r + i]);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0 && c_checked(p, row, f) &&
-                                c_checked(p, row + PIECE - 1, f + 31)) {
-                                if constexpr (MODE == kRagDepth)
-                                    tma_store_3d(&p.map[kMapC], tile, f, row, un.g);
-                                else
-                                    tma_store_2d(&p.map[kMapC], tile, f, row);
-                                bulk_commit_group();
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < PIECE; ++i)
-                                if (r + i < left && c_checked(p, row + i, f))
-                                    c_col[(int64_t)(c * 32 + r + i) * p.ldc] =
-                                        from_f32<OutT>(v[r + i]);
+                        for (int i = 0; i < 32; ++i)
+                            sts_as<OutT>(tile + (uint32_t)((i * 32 + lane) * 2), v[i]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && c_checked(p, row, f) && c_checked(p, row + 31, f + 31)) {
+                            if constexpr (MODE == kRagDepth)
+                                tma_store_3d(&p.map[kMapC], tile, f, row, un.g);
+                            else
+                                tma_store_2d(&p.map[kMapC], tile, f, row);
+                            bulk_commit_group();
                         }
+                        return;
                     }
-                    return;
                 }
                 if (!f_ok) return;
                 if (!epi && !by_hand) {
@@ -1057,6 +1070,9 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     for (int i = 16; i < 32; ++i) push(i);
                 }
             };
+            // pair units' timeline (the leader's slots hold its MMA warp's)
+            const bool stamp = CG == 2 && !leader && warp == EPI_WARP0 && lane == 0;
+            if (stamp) TC_TRACE(p, 20 + 4 * nt);
             const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
             auto load_chunk = [&](int c, float (&v)[32]) {
                 uint32_t u[32];
@@ -1069,65 +1085,83 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 if (!aborted && !wait_bar_inline(accf_bar(acc), acc_phase, p)) aborted = true;
                 tc_fence_after_sync();
             };
+            // Relaxed: the accumulator's reads are complete (wait::ld) and nothing else
+            // is handed over, so the arrival need not wait for the stores of C.
+            bool held = false;
             auto free_acc = [&]() {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
-                    else mbar_arrive_local(acce_bar(acc));
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster_relaxed(mapa_shared(acce_bar(acc), 0));
+                    else
+                        mbar_arrive_local(acce_bar(acc));
                 }
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                held = false;
             };
-            // The unit's sums: a folded depth's parts add up in registers; else
-            // the chunks are read from the accumulator as they are stored.
+            // The unit's sums: the parts of a folded depth before the last add up
+            // in registers; the last one (or the only one) is read from its
+            // accumulator as the chunks are stored.
             float sum[FOLD ? CHUNKS : 1][32];
-            if constexpr (FOLD) {
+            bool folded = false;
+            auto add_chunk = [&](int k) {
+                // 16 columns at a time: the sums leave no registers for more
 #pragma unroll
-                for (int k = 0; k < CHUNKS; ++k)
+                for (int h = 0; h < 32; h += 16) {
+                    uint32_t u[16];
+                    tmem_ld_32x32b_x16(
+                        tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32 + h), u);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[k][i] = 0.f;
-                for (int kb = kb0; kb < kb1; kb += FOLD_KB) {
-                    wait_acc();
-#pragma unroll
-                    for (int k = 0; k < CHUNKS; ++k) {
-                        const int c = half + 2 * k;
-                        if (!aborted && c * 32 < un.width) {
-                            // 16 columns at a time: the sums leave no registers for more
-#pragma unroll
-                            for (int h = 0; h < 32; h += 16) {
-                                uint32_t u[16];
-                                tmem_ld_32x32b_x16(
-                                    tlane + (uint32_t)(acc * ACC_COLS + c * 32 + h), u);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    sum[k][h + i] += __uint_as_float(u[i]);
-                            }
-                        }
-                    }
-                    free_acc();
+                    for (int i = 0; i < 16; ++i) sum[k][h + i] += __uint_as_float(u[i]);
                 }
-            } else if (issued) {
-                wait_acc();
-            }
-            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 8);
-            auto each_chunk = [&](auto&& use) {
-                if constexpr (FOLD) {
+            };
+            if constexpr (FOLD) {
+                if (kb1 - kb0 > FOLD_KB) {
+                    folded = true;
 #pragma unroll
                     for (int k = 0; k < CHUNKS; ++k)
-                        if ((half + 2 * k) * 32 < un.width) use(half + 2 * k, sum[k]);
-                } else {
-#pragma unroll 1
-                    for (int c = half; c * 32 < un.width; c += 2) {
-                        float v[32];
-                        if (issued) {
-                            load_chunk(c, v);
-                        } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                        }
-                        use(c, v);
+                        for (int i = 0; i < 32; ++i) sum[k][i] = 0.f;
+                    int kb = kb0;
+                    for (; kb + FOLD_KB < kb1; kb += FOLD_KB) {
+                        wait_acc();
+#pragma unroll
+                        for (int k = 0; k < CHUNKS; ++k)
+                            if (!aborted && (half + 2 * k) * 32 < un.width) add_chunk(k);
+                        free_acc();
                     }
+                }
+            }
+            if (issued) wait_acc();
+            held = issued;
+            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 8);
+            if (stamp) TC_TRACE(p, 22 + 4 * nt);
+            auto each_chunk = [&](auto&& use) {
+                if constexpr (FOLD) {
+                    if (folded) {
+#pragma unroll
+                        for (int k = 0; k < CHUNKS; ++k)
+                            if ((half + 2 * k) * 32 < un.width) {
+                                add_chunk(k);
+                                if (k == CHUNKS - 1) free_acc();
+                                use(half + 2 * k, sum[k]);
+                            }
+                        return;
+                    }
+                }
+#pragma unroll 1
+                for (int c = half; c * 32 < un.width; c += 2) {
+                    float v[32];
+                    if (issued) {
+                        load_chunk(c, v);
+                        if ((c + 2) * 32 >= un.width) free_acc();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+                    use(c, v);
                 }
             };
             if (S == 1) {
@@ -1175,12 +1209,14 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 split_phase ^= 1u;
                 fence_proxy_async_all();  // the next unit's copies write where the parts were
             }
-            if (!FOLD && issued) free_acc();
+            if (held) free_acc();
             if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 12);
+            if (stamp) TC_TRACE(p, 23 + 4 * nt);
+            ++nt;
             more = units.next(p, un);
             if (S > 1 && more) cluster_sync_all();
         }
-        if (MODE != kRagShrink && p.c_tma && lane == 0) bulk_wait_all();
+        if (BY_TMA && p.c_tma && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
         // Warp 2 finds the units and passes them on, up to UNITS ahead; warp 3 of
@@ -1199,20 +1235,39 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         __syncwarp();
-        if (warp == 2 || S > 1) {
+        if (warp == 2 && !leader) {
+            // tells the leader's warp 2 that this CTA has read a unit
+            bool more = true;
+            for (int j = 0; more; ++j) {
+                const int s = j % C_::UNITS;
+                const uint32_t parity = (uint32_t)(j / C_::UNITS) & 1u;
+                if (!__all_sync(0xffffffffu, wait_unit(ready_bar + 8u * s, parity, p))) break;
+                more = get_unit(unit_slots + 48u * s, un);
+                if (!__all_sync(0xffffffffu,
+                                wait_unit(ready_bar + 8u * (C_::UNITS + s), parity, p)))
+                    break;
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (2 * C_::UNITS + s), 0));
+                __syncwarp();
+            }
+        } else if (warp == 2 || S > 1) {
             Units<CG, MODE> units(p, cluster, list_arg);
             bool more = true;
             for (int j = 0; more; ++j) {
                 more = units.next(p, un);
                 if (warp == 2) {
                     const int s = j % C_::UNITS;
-                    if (j >= C_::UNITS &&
-                        !wait_unit(ready_bar + 8u * (C_::UNITS + s),
-                                   (uint32_t)(j / C_::UNITS - 1) & 1u, p))
-                        break;
-                    if (lane == 0) {
-                        put_unit(unit_slots + 48u * s, un, more);
-                        mbar_arrive_local(ready_bar + 8u * s);
+                    const uint32_t parity = (uint32_t)(j / C_::UNITS - 1) & 1u;
+                    if (j >= C_::UNITS) {
+                        bool ok = wait_unit(ready_bar + 8u * (C_::UNITS + s), parity, p);
+                        if (CG == 2)
+                            ok = ok && wait_unit(ready_bar + 8u * (2 * C_::UNITS + s), parity, p);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                    }
+                    if (lane < CG) {  // to each CTA of the pair
+                        const uint32_t to = CG == 2 ? (uint32_t)lane : crank;
+                        put_unit(mapa_shared(unit_slots + 48u * s, to), un, more);
+                        mbar_arrive_cluster(mapa_shared(ready_bar + 8u * s, to));
                     }
                     __syncwarp();
                 }

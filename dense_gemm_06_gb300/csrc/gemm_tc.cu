@@ -191,17 +191,14 @@ bool encode_tma_16(void* map, bool bf16, const void* ptr, uint64_t inner, uint64
     return encode_cached(static_cast<CUtensorMap*>(map), a);
 }
 
-bool encode_tma_c(void* map, bool f32, bool bf16, void* ptr, uint64_t inner, uint64_t outer,
-                  uint64_t ld, uint64_t mats, uint64_t mat_stride, uint32_t box_inner,
-                  uint32_t box_outer) {
-    const uint64_t es = f32 ? 4 : 2;
-    MapArgs a = map_args(ptr, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                  : (bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
-                         inner, outer, ld * es, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE,
+bool encode_tma_c16(void* map, bool bf16, void* ptr, uint64_t inner, uint64_t outer, uint64_t ld,
+                    uint64_t mats, uint64_t mat_stride, uint32_t box_inner, uint32_t box_outer) {
+    MapArgs a = map_args(ptr, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         inner, outer, ld * 2, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE,
                          CU_TENSOR_MAP_L2_PROMOTION_NONE);
     a.mats = mats;
-    a.mat_bytes = mat_stride * es;
+    a.mat_bytes = mat_stride * 2;
     return encode_cached(static_cast<CUtensorMap*>(map), a);
 }
 

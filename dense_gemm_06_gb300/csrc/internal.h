@@ -137,10 +137,9 @@ bool encode_tma_f32_2d(void* map, const float* ptr, uint64_t inner, uint64_t out
 bool encode_tma_16(void* map, bool bf16, const void* ptr, uint64_t inner, uint64_t outer,
                    uint64_t ld, uint64_t mats, uint64_t mat_stride, uint32_t box_inner,
                    uint32_t box_outer);
-// The same for storing to a C of fp32, fp16 or bf16, without swizzle.
-bool encode_tma_c(void* map, bool f32, bool bf16, void* ptr, uint64_t inner, uint64_t outer,
-                  uint64_t ld, uint64_t mats, uint64_t mat_stride, uint32_t box_inner,
-                  uint32_t box_outer);
+// The same for storing to a 16-bit C, without swizzle.
+bool encode_tma_c16(void* map, bool bf16, void* ptr, uint64_t inner, uint64_t outer, uint64_t ld,
+                    uint64_t mats, uint64_t mat_stride, uint32_t box_inner, uint32_t box_outer);
 // dst[c * ldd + r] = src[r * lds + c] (fp32), rows x cols.
 int launch_transpose_f32(const float* src, int64_t lds, float* dst, int64_t ldd, int64_t rows,
                          int64_t cols, const DeviceInfo& dev, cudaStream_t stream);

@@ -96,6 +96,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                  :: "r"(cluster_bar) : "memory");
 }
 
+// The same without ordering this thread's memory accesses.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+                 :: "r"(cluster_bar) : "memory");
+}
+
 // One non-blocking probe of the phase with the given parity (cluster-scope
 // acquire, so arrivals released by the peer CTA are ordered before us).
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
@@ -208,10 +214,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(cluster_addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// Four words at a 16-byte aligned shared::cluster address.
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t x, uint32_t y,
+                                              uint32_t z, uint32_t w) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(cluster_addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // ------------------------------------------------ cluster launch control --
