@@ -346,14 +346,22 @@ struct Feed {
     int j;
     __device__ __forceinline__ Feed(uint32_t r, uint32_t s) : ready(r), slots(s), j(0) {}
     __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
+        const bool more = peek(p, un);
+        done();
+        return more;
+    }
+    // The next unit / its slot may be used again.
+    __device__ __forceinline__ bool peek(const RaggedParams& p, RUnit& un) {
         const int s = j % RCfg::UNITS;
         if (!__all_sync(0xffffffffu, wait_unit(ready + 8u * s, (uint32_t)(j / RCfg::UNITS) & 1u, p)))
             return false;
-        const bool more = get_unit(slots + 48u * s, un);
+        return get_unit(slots + 48u * s, un);
+    }
+    __device__ __forceinline__ void done() {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive_local(ready + 8u * (RCfg::UNITS + s));
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive_local(ready + 8u * (RCfg::UNITS + j % RCfg::UNITS));
         ++j;
-        return more;
     }
 };
 
@@ -928,7 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         Feed units(ready_bar, unit_slots);
-        for (bool more = units.next(p, un); more;) {
+        for (bool more = units.peek(p, un); more;) {
             int kb0, kb1, n = 0, ne = 0;
             share(un.nkb, kb0, kb1);
             bool issued = kb1 > kb0;
@@ -1106,16 +1114,11 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             float sum[FOLD ? CHUNKS : 1][32];
             bool folded = false;
             auto add_chunk = [&](int k) {
-                // 16 columns at a time: the sums leave no registers for more
+                uint32_t u[32];
+                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32), u);
+                tmem_wait_ld();
 #pragma unroll
-                for (int h = 0; h < 32; h += 16) {
-                    uint32_t u[16];
-                    tmem_ld_32x32b_x16(
-                        tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32 + h), u);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[k][h + i] += __uint_as_float(u[i]);
-                }
+                for (int i = 0; i < 32; ++i) sum[k][i] += __uint_as_float(u[i]);
             };
             if constexpr (FOLD) {
                 if (kb1 - kb0 > FOLD_KB) {
@@ -1136,6 +1139,9 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
             if (issued) wait_acc();
             held = issued;
+            // Here, before this unit's stores and well after the last one's: even a
+            // CTA-scope release waits for stores just issued.
+            units.done();
             if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 8);
             if (stamp) TC_TRACE(p, 22 + 4 * nt);
             auto each_chunk = [&](auto&& use) {
@@ -1213,9 +1219,10 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 12);
             if (stamp) TC_TRACE(p, 23 + 4 * nt);
             ++nt;
-            more = units.next(p, un);
+            more = units.peek(p, un);
             if (S > 1 && more) cluster_sync_all();
         }
+        units.done();
         if (BY_TMA && p.c_tma && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
