@@ -117,6 +117,9 @@ struct RCfg {
     static constexpr int SMEM_BYTES = RING_BYTES + EXTRA_BYTES + UNIT_OFFSET + UNITS * 48 + 1024;
     static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
+// Warps: 0 copies, 1 MMA, 2 units, 3 .. 10 epilogue.
+constexpr int REPI_WARP0 = 3;
+constexpr int RTHREADS = 32 * (REPI_WARP0 + EPI_WARPS);
 // fp32 results: depth summed in one accumulator, in k-blocks. The tensor core
 // cuts each addition to the accumulator off below 2^-23 of it, an error that
 // grows with the depth (measured: 1.3e-6 of the result's norm at a depth of
@@ -482,7 +485,7 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
     __syncthreads();
     int place = __popc(b & ((1u << lane) - 1)), n = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < RTHREADS / 32; ++w) {
         const int c = sums[w];
         if (w < warp) place += c;
         n += c;
@@ -506,7 +509,7 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
 // each unit: every CTA sums its share of the k-blocks, and the partial sums
 // meet in the shared memory of the CTA that owns the row, in rank order.
 template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
-__global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
+__global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
     using C_ = RCfg;
     using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr bool Q_MN = MODE == kRagDepth;
@@ -882,10 +885,10 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             }
         }
         __syncwarp();
-    } else if (warp >= EPI_WARP0) {
+    } else if (warp >= REPI_WARP0) {
         // ------------------------------------------------------ epilogue --
-        const int q = (warp - EPI_WARP0) & 3;
-        const int half = (warp - EPI_WARP0) >> 2;
+        const int q = warp & 3;  // TMEM lane quarter (hardware: warp % 4)
+        const int half = (warp - REPI_WARP0) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0, split_phase = 0;
         // 16-bit results leave in 32 x 32 chunks by TMA (rows K-major at a depth of
@@ -894,7 +897,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         // row by row (2.4 us per unit against 3.0 us through staging tiles).
         constexpr bool BY_TMA = MODE != kRagShrink && sizeof(OutT) == 2;
         const uint32_t tiles =
-            base + C_::RING_BYTES + (uint32_t)((warp - EPI_WARP0) * 2 * C_::TILE_BYTES);
+            base + C_::RING_BYTES + (uint32_t)((warp - REPI_WARP0) * 2 * C_::TILE_BYTES);
         int tile_i = 0;
         int nt = 0;  // units stored (trace slots)
         pdl_wait();
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             // 16-byte groups of one adapter's LB (its rows' padding is zero)
             const int64_t vecs = (int64_t)p.R * p.ldlb / 8;
             bool bad = false;
-            for (int64_t v = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32);
+            for (int64_t v = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - REPI_WARP0 * 32);
                  v < vecs; v += (int64_t)ctas * (EPI_WARPS * 32)) {
                 const uint4* b = static_cast<const uint4*>(p.lora_b) + v;
                 for (int a = 0; a < n_list; a += 8) {  // eight loads in flight
@@ -928,11 +931,11 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 }
             }
             bad = __any_sync(0xffffffffu, bad);
-            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 7);
+            if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 7);
             if (lane == 0) {
                 int32_t* flag = p.lists + (int64_t)(cluster / p.chains / subs) * p.list_pitch +
                                 1 + 2 * p.list_w;
-                flag[me * EPI_WARPS + (warp - EPI_WARP0)] = bad ? 1 : 0;
+                flag[me * EPI_WARPS + (warp - REPI_WARP0)] = bad ? 1 : 0;
             }
         }
         Feed units(ready_bar, unit_slots);
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             const bool epi = MODE != kRagShrink && p.epi.active;
             const bool f_ok = f < p.feats;
             float bias = 0.f;
-            if (MODE != kRagShrink && epi && p.epi.bias && f_ok)
+            if (epi && p.epi.bias && f_ok)
                 bias = to_f32(static_cast<const OutT*>(p.epi.bias)[(int64_t)un.g * p.feats + f]);
             OutT* c_col = nullptr;
             if constexpr (MODE != kRagShrink)
@@ -1079,16 +1082,13 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 }
             };
             // pair units' timeline (the leader's slots hold its MMA warp's)
-            const bool stamp = CG == 2 && !leader && warp == EPI_WARP0 && lane == 0;
+            const bool stamp = CG == 2 && !leader && warp == REPI_WARP0 && lane == 0;
             if (stamp) TC_TRACE(p, 20 + 4 * nt);
             const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-            auto load_chunk = [&](int c, float (&v)[32]) {
-                uint32_t u[32];
-                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + c * 32), u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+            auto read_chunk = [&](int k, uint32_t (&u)[32]) {
+                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32), u);
             };
+            auto has = [&](int k) { return k < CHUNKS && (half + 2 * k) * 32 < un.width; };
             auto wait_acc = [&]() {
                 if (!aborted && !wait_bar_inline(accf_bar(acc), acc_phase, p)) aborted = true;
                 tc_fence_after_sync();
@@ -1115,8 +1115,8 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             bool folded = false;
             auto add_chunk = [&](int k) {
                 uint32_t u[32];
-                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32), u);
-                tmem_wait_ld();
+                read_chunk(k, u);
+                tmem_wait_ld(u);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[k][i] += __uint_as_float(u[i]);
             };
@@ -1127,12 +1127,11 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sum[k][i] = 0.f;
-                    int kb = kb0;
-                    for (; kb + FOLD_KB < kb1; kb += FOLD_KB) {
+                    for (int kb = kb0; kb + FOLD_KB < kb1; kb += FOLD_KB) {
                         wait_acc();
 #pragma unroll
                         for (int k = 0; k < CHUNKS; ++k)
-                            if (!aborted && (half + 2 * k) * 32 < un.width) add_chunk(k);
+                            if (has(k)) add_chunk(k);
                         free_acc();
                     }
                 }
@@ -1142,32 +1141,36 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             // Here, before this unit's stores and well after the last one's: even a
             // CTA-scope release waits for stores just issued.
             units.done();
-            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 8);
+            if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 8);
             if (stamp) TC_TRACE(p, 22 + 4 * nt);
             auto each_chunk = [&](auto&& use) {
                 if constexpr (FOLD) {
                     if (folded) {
 #pragma unroll
                         for (int k = 0; k < CHUNKS; ++k)
-                            if ((half + 2 * k) * 32 < un.width) {
+                            if (has(k)) {
                                 add_chunk(k);
-                                if (k == CHUNKS - 1) free_acc();
+                                if (!has(k + 1)) free_acc();
                                 use(half + 2 * k, sum[k]);
                             }
                         return;
                     }
                 }
 #pragma unroll 1
-                for (int c = half; c * 32 < un.width; c += 2) {
+                for (int k = 0; has(k); ++k) {
                     float v[32];
                     if (issued) {
-                        load_chunk(c, v);
-                        if ((c + 2) * 32 >= un.width) free_acc();
+                        uint32_t u[32];
+                        read_chunk(k, u);
+                        tmem_wait_ld(u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                        if (!has(k + 1)) free_acc();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
-                    use(c, v);
+                    use(half + 2 * k, v);
                 }
             };
             if (S == 1) {
@@ -1175,18 +1178,18 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
             } else {
                 // Tell the peers that this CTA's MMAs have read its ring, wait
                 // until all have, and give every CTA the partial sums of its rows.
-                if (!aborted && warp == EPI_WARP0 && lane < S)
+                if (!aborted && warp == REPI_WARP0 && lane < S)
                     mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
                 if (!aborted && !wait_bar_warp(free_bar, split_phase, p)) aborted = true;
-                if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 9);
+                if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 9);
                 if (!aborted) {
                     each_chunk(push_chunk);
                     __syncwarp();
                     if (lane < S) mbar_arrive_cluster(mapa_shared(parts_bar, (uint32_t)lane));
-                    if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 10);
+                    if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 10);
                     if (!wait_bar_warp(parts_bar, split_phase, p)) aborted = true;
                 }
-                if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 11);
+                if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 11);
                 if (!aborted) {
                     // add the parts in rank order, four rows at a time so that their
                     // loads overlap
@@ -1216,7 +1219,7 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 fence_proxy_async_all();  // the next unit's copies write where the parts were
             }
             if (held) free_acc();
-            if (warp == EPI_WARP0 && lane == 0) TC_TRACE(p, 12);
+            if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 12);
             if (stamp) TC_TRACE(p, 23 + 4 * nt);
             ++nt;
             more = units.peek(p, un);
@@ -1226,12 +1229,12 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
         if (BY_TMA && p.c_tma && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
-        // Warp 2 finds the units and passes them on, up to UNITS ahead; warp 3 of
-        // the first CTA looks over the group limits (the others clamp what is wrong
-        // with them). Both take part in the barrier between a split's units.
-        if constexpr (MODE == kRagRows || MODE == kRagDepth) pdl_wait();
+        // Warp 2 finds the units and passes them on, up to UNITS ahead, and takes
+        // part in the barrier between a split's units. The first CTA's looks over
+        // the group limits too (all clamp what is wrong with them).
         if constexpr (MODE == kRagRows || MODE == kRagDepth) {
-            if (blockIdx.x == 0 && warp == 3) {
+            pdl_wait();
+            if (blockIdx.x == 0) {
                 const int most = MODE == kRagRows ? p.rows : p.depth;
                 bool bad = false;
                 for (int g = lane; g < p.G; g += 32) {
@@ -1240,9 +1243,9 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                 }
                 if (bad) gen_record_timeout(p.err + 1, 1);
             }
+            __syncwarp();
         }
-        __syncwarp();
-        if (warp == 2 && !leader) {
+        if (!leader) {
             // tells the leader's warp 2 that this CTA has read a unit
             bool more = true;
             for (int j = 0; more; ++j) {
@@ -1257,27 +1260,25 @@ __global__ void __launch_bounds__(THREADS, 1) ragged_kernel(const __grid_constan
                     mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (2 * C_::UNITS + s), 0));
                 __syncwarp();
             }
-        } else if (warp == 2 || S > 1) {
+        } else {
             Units<CG, MODE> units(p, cluster, list_arg);
             bool more = true;
             for (int j = 0; more; ++j) {
                 more = units.next(p, un);
-                if (warp == 2) {
-                    const int s = j % C_::UNITS;
-                    const uint32_t parity = (uint32_t)(j / C_::UNITS - 1) & 1u;
-                    if (j >= C_::UNITS) {
-                        bool ok = wait_unit(ready_bar + 8u * (C_::UNITS + s), parity, p);
-                        if (CG == 2)
-                            ok = ok && wait_unit(ready_bar + 8u * (2 * C_::UNITS + s), parity, p);
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                    }
-                    if (lane < CG) {  // to each CTA of the pair
-                        const uint32_t to = CG == 2 ? (uint32_t)lane : crank;
-                        put_unit(mapa_shared(unit_slots + 48u * s, to), un, more);
-                        mbar_arrive_cluster(mapa_shared(ready_bar + 8u * s, to));
-                    }
-                    __syncwarp();
+                const int s = j % C_::UNITS;
+                const uint32_t parity = (uint32_t)(j / C_::UNITS - 1) & 1u;
+                if (j >= C_::UNITS) {
+                    bool ok = wait_unit(ready_bar + 8u * (C_::UNITS + s), parity, p);
+                    if (CG == 2)
+                        ok = ok && wait_unit(ready_bar + 8u * (2 * C_::UNITS + s), parity, p);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                 }
+                if (lane < CG) {  // to each CTA of the pair
+                    const uint32_t to = CG == 2 ? (uint32_t)lane : crank;
+                    put_unit(mapa_shared(unit_slots + 48u * s, to), un, more);
+                    mbar_arrive_cluster(mapa_shared(ready_bar + 8u * s, to));
+                }
+                __syncwarp();
                 if (S > 1 && j > 0 && more) cluster_sync_all();
             }
         }
@@ -1309,7 +1310,7 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
     attr[0].val.clusterDim.x = cl;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(RTHREADS);
     cfg.dynamicSmemBytes = RCfg::SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
