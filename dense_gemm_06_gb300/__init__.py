@@ -74,6 +74,8 @@ class GemmError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load libgemm.so (built by ``__graft_entry__.build()``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -127,15 +129,40 @@ def _ptr(x) -> int:
     raise TypeError(f"cannot take a pointer of {type(x).__name__}")
 
 
-def _stream(s) -> int:
-    if s is None:
+_raw_stream = None  # the current torch stream's handle, once torch has a device
+
+
+def _current_stream() -> int:
+    global _raw_stream
+    if _raw_stream is None:
         try:
             import torch
-            if torch.cuda.is_available():
-                return int(torch.cuda.current_stream().cuda_stream)
         except ImportError:
-            pass
-        return 0
+            return 0
+        if not torch.cuda.is_available():
+            return 0
+        # the handle without a Stream object (3 us of every call), where this
+        # torch has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        if raw is not None and device is not None:
+            _raw_stream = lambda: int(raw(device()))
+        else:
+            _raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
+def _epilogue(alpha, beta, bias, activation):
+    """A gemm_epilogue argument; None (plain) where nothing is asked for."""
+    if alpha == 1.0 and beta == 0.0 and bias is None and activation == GEMM_ACT_NONE:
+        return None
+    return ctypes.byref(GemmEpilogue(alpha, beta, _ptr(bias) or None, activation))
+
+
+def _stream(s) -> int:
+    if s is None:
+        return _current_stream()
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
@@ -193,18 +220,16 @@ def gemm_grouped(G, M, N, K, offsets, A, lda, B, ldb, strideb, b_major, C, ldc, 
                  alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE, stream=None) -> int:
     """C[t] = act(alpha * A[t] B_g^T + beta * C[t] + bias[g]) for the rows t of each
     group g (limits in the device array `offsets`); see include/gemm.h."""
-    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
     return load().gemm_grouped(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, strideb,
-                               b_major, _ptr(C), ldc, dtype, ctypes.byref(epi), _stream(stream))
+                               b_major, _ptr(C), ldc, dtype, _epilogue(alpha, beta, bias, activation), _stream(stream))
 
 
 def gemm_grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype,
                    alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE, stream=None) -> int:
     """C_g = act(alpha * sum over group g's rows t of A[t]^T B[t] + beta * C_g + bias[g])
     (the weight gradient of gemm_grouped); see include/gemm.h."""
-    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
     return load().gemm_grouped_k(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, _ptr(C),
-                                 ldc, stridec, dtype, ctypes.byref(epi), _stream(stream))
+                                 ldc, stridec, dtype, _epilogue(alpha, beta, bias, activation), _stream(stream))
 
 
 def gemm_lora(M, N, K, L, R, A, lda, B, ldb, b_major, adapter, lora_a, lora_b, scale, C, ldc,
@@ -212,10 +237,9 @@ def gemm_lora(M, N, K, L, R, A, lda, B, ldb, b_major, adapter, lora_a, lora_b, s
               stream=None) -> int:
     """C = act(alpha * (A B^T + T LB_a) + beta * C + bias), T = scale[a] * A LA_a^T with
     a = adapter[t] for each row t; see include/gemm.h."""
-    epi = GemmEpilogue(alpha, beta, _ptr(bias) or None, activation)
     return load().gemm_lora(M, N, K, L, R, _ptr(A), lda, _ptr(B), ldb, b_major, _ptr(adapter),
                             _ptr(lora_a), _ptr(lora_b), _ptr(scale), _ptr(C), ldc, dtype,
-                            ctypes.byref(epi), _stream(stream))
+                            _epilogue(alpha, beta, bias, activation), _stream(stream))
 
 
 def gemm_strerror(status: int) -> str:

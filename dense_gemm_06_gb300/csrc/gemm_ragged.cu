@@ -484,14 +484,19 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     // rows; the tile is 256 rows wide at most.
     const int64_t most = M < 256 ? M : 256;
     const int64_t parts = ((L < most ? L : most) * slot + 127) / 128;
-    const LoraShape shape = plan_lora(M, N, num_kb, parts, dev->sm_count);
+    const LoraShape shape = plan_lora(M, N, num_kb, parts, slot, dev->sm_count);
     const RaggedShape& ex = shape.expand;
     const int W = ex.tile_w;
     const int64_t list_n = L < (M < W ? M : W) ? L : (M < W ? M : W);
     const int64_t ldt = up(list_n * slot, EXT_K) * 2;
     const int subs = W / shape.shrink_w;
-    const int flags = subs * shape.chains * shape.shrink_split * EPI_WARPS;
+    const int flags = shape.rows_blocks > 0
+                          ? shape.scan_blocks
+                          : subs * shape.chains * shape.shrink_split * EPI_WARPS;
     const int list_pitch = 1 + 2 * W + flags;
+
+    // the kernels count the 16-byte groups of a list's LBs in 32 bits
+    if (list_n * R * (lb.packed_ld() / 8) > INT32_MAX) return kUnsupported;
 
     // Row panels bound T; each is a whole number of tiles.
     int64_t panel = kMaxTBytes / (ldt * 2) / W * W;
@@ -522,6 +527,11 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         rp.num_kb = (int)num_kb;
         rp.adapter = adapter + m0;
         rp.scale = scale;
+        rp.x = xp.ptr;
+        rp.ldx = xp.ld;
+        rp.lora_a = la.ptr;
+        rp.ldla = la.ld;
+        rp.depth = (int)K;
         rp.lora_b = lb.ptr;
         rp.ldlb = lb.ld;
         rp.L = (int)L;
@@ -568,15 +578,21 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
             break;
         }
         auto run = bf16 ? launch_lora_bf16 : launch_lora_f16;
-        rc = run(sh, kRagShrink, 1, false, clusters, *dev, s);
+        if (shape.rows_blocks > 0) {
+            sh.chains = shape.rows_blocks;
+            rc = run(sh, kRagShrinkRows, 1, false, shape.rows_blocks + shape.scan_blocks, *dev, s);
+        } else {
+            rc = run(sh, kRagShrink, 1, false, clusters, *dev, s);
+        }
         if (rc == kOk) rc = run(rp, kRagLora, ex.cta_group, !kmaj, units, *dev, s);
     }
     scratch.release();
     if (rc == kOk)
-        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d rows, %d chains, split %d; "
+        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d blocks of dot products or "
+                     "%d rows, %d chains, split %d; "
                      "expand %s, units of %d rows, split %d",
                      (long long)M, (long long)N, (long long)K, (long long)L, (long long)R,
-                     shape.shrink_w, shape.chains, shape.shrink_split,
+                     shape.rows_blocks, shape.shrink_w, shape.chains, shape.shrink_split,
                      ex.cta_group == 2 ? "CTA pairs" : "one CTA per unit", W, ex.split);
     return rc;
 }

@@ -17,6 +17,7 @@ enum RaggedMode {
     kRagDepth = 1,   // groups of the summed dimension              (gemm_grouped_k)
     kRagShrink = 2,  // T = scale * X LA^T of a row tile's adapters (gemm_lora, 1st launch)
     kRagLora = 3,    // X W^T + T LB                                (gemm_lora, 2nd launch)
+    kRagShrinkRows = 4,  // kRagShrink for few rows, by plain dot products
 };
 
 // Tensor maps by use. P operands are 3-D (group or adapter number last).
@@ -41,7 +42,7 @@ struct RaggedParams {
     int G;
     int rows;       // rows of C (depth: of each C_g)
     int feats;      // columns of C (shrink: of LB)
-    int depth;      // depth: rows of A and B, over which the groups are
+    int depth;      // depth: rows of A and B, over which the groups are (kRagShrinkRows: K)
     int num_kb;     // 64-deep k-blocks (depth: per group, from the offsets)
     int tile_w;     // rows of a full unit (shrink: divides list_w)
     int tiles_f;    // feature tiles
@@ -55,11 +56,15 @@ struct RaggedParams {
     // gemm_lora
     const int32_t* adapter;  // adapter number of each row
     const float* scale;      // one factor per adapter, or null
+    const void* x;           // kRagShrinkRows: X and LA, row pitches ldx and ldla
+    const void* lora_a;
+    int64_t ldx, ldla;
     const void* lora_b;      // LB as the kernels read it, row pitch ldlb (padding zero)
     int64_t ldlb;
     int L, R, slot;          // adapters, rank, lanes per adapter (16, 32, 64 or 128)
     int list_w;              // rows that share one list of adapters (the expand's tile_w)
     int chains;              // shrink: clusters that share a row tile's lists of lanes
+                             // (kRagShrinkRows: blocks of dot products)
     int32_t* lists;          // per list tile: n, list_w adapter numbers, list_w slots, flags
     int list_pitch, flags;
     void* T;                 // hi | lo halves of T, 64 elements per 32 lanes
@@ -108,6 +113,9 @@ struct RCfg {
     // ids[256], slots[256], list[256], warp sums[16])
     static constexpr int TILE_BYTES = 2048;
     static constexpr int EXTRA_BYTES = EPI_WARPS * 2 * TILE_BYTES;
+    // Partial sums of a split unit of up to PARTS_ROWS rows: behind the list.
+    static constexpr int PARTS_OFFSET = 4096;
+    static constexpr int PARTS_ROWS = (EXTRA_BYTES - PARTS_OFFSET) / 512;
     // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
     // unit_ready[UNITS], unit_read[UNITS], unit_read_by_peer[UNITS]; then the TMEM
     // address and the units
@@ -374,6 +382,15 @@ __device__ __forceinline__ bool nonfinite16(uint32_t w) {
     return (w & e) == e || ((w >> 16) & e) == e;
 }
 
+// Two packed 16-bit numbers.
+template <bool BF16>
+__device__ __forceinline__ float2 to_f32x2(uint32_t w) {
+    if constexpr (BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // One element of C (feature f of row `row`), fused epilogue included.
 template <typename OutT>
 __device__ __forceinline__ void store_c(const RaggedParams& p, OutT* dst, float acc, float bias,
@@ -449,6 +466,7 @@ __device__ __forceinline__ bool c_checked(const RaggedParams& p, int row, int f)
 // first of each set then looks for its adapter among the earlier warps' rows
 // in shared memory (at most 224, four per load, no early exit: the loads
 // pipeline, where a scalar loop that stops at the first hit waits for each).
+template <int NTHREADS>
 __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* ids, int* slots,
                                          int* list, int* sums) {
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
@@ -485,7 +503,7 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
     __syncthreads();
     int place = __popc(b & ((1u << lane) - 1)), n = 0;
 #pragma unroll
-    for (int w = 0; w < RTHREADS / 32; ++w) {
+    for (int w = 0; w < NTHREADS / 32; ++w) {
         const int c = sums[w];
         if (w < warp) place += c;
         n += c;
@@ -501,6 +519,147 @@ __device__ __forceinline__ int make_list(const RaggedParams& p, int row0, int* i
     if (i < 256) slots[i] = s;
     __syncthreads();
     return n;
+}
+
+// Does the LB of a listed adapter hold an infinity or a NaN, in this thread's
+// share (16-byte groups i, i + step, ... of the listed LBs one after the other;
+// their rows' padding is zero)? Eight loads in flight.
+template <bool BF16>
+__device__ __forceinline__ bool scan_lb(const RaggedParams& p, const int* list, int n, uint32_t i,
+                                        uint32_t step) {
+    const uint32_t vecs = (uint32_t)((int64_t)p.R * p.ldlb / 8);
+    const uint64_t total = (uint64_t)n * vecs;
+    const uint4* lb = static_cast<const uint4*>(p.lora_b);
+    bool bad = false;
+    for (uint64_t at = i; at < total; at += 8ull * step) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint64_t x = at + (uint64_t)j * step;
+            w[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (x < total) {
+                const uint32_t a = (uint32_t)x / vecs;  // total < 2^32: see lora()
+                w[j] = __ldg(lb + (int64_t)list[a] * vecs + ((uint32_t)x - a * vecs));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            bad |= nonfinite16<BF16>(w[j].x) | nonfinite16<BF16>(w[j].y) |
+                   nonfinite16<BF16>(w[j].z) | nonfinite16<BF16>(w[j].w);
+    }
+    return bad;
+}
+
+// kRagShrinkRows: T of few rows without tensor cores. A block computes ROW_RANKS
+// of a row's dot products sum_k x[k] LA_a[r][k], each of its 8 warps an eighth
+// of K for all of them, straight from memory, and writes them (zeros for the
+// list's other adapters). Little is read twice in a decoding batch, so there is
+// nothing to tile; what counts is the chain of latencies: the row's adapter
+// number, then all loads in flight at once while the list is made, then a
+// shuffle and one exchange through shared memory -- where the tensor-core form
+// goes through a ring, a cluster's exchange and its barriers (10.7 us for one
+// row of 4096, 14 us for 48). The blocks past p.chains scan LB meanwhile, one
+// flag each.
+constexpr int kRowsThreads = 256, ROW_RANKS = 4;
+template <bool BF16>
+__global__ void __launch_bounds__(kRowsThreads) lora_rows_kernel(const __grid_constant__ RaggedParams p) {
+    using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int WARPS = kRowsThreads / 32;
+    __shared__ __align__(16) int ids[256], slots[256], list[256], sums[16];
+    __shared__ float partial[WARPS][ROW_RANKS];
+    __shared__ int any_bad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) any_bad = 0;
+    pdl_wait();  // and the expand relies on it, as after kRagShrink
+    pdl_launch_dependents();
+    if ((int)blockIdx.x >= p.chains) {
+        const int n = make_list<kRowsThreads>(p, 0, ids, slots, list, sums);
+        const int me = (int)blockIdx.x - p.chains;
+        const bool bad = scan_lb<BF16>(p, list, n, (uint32_t)(me * kRowsThreads + threadIdx.x),
+                                       (uint32_t)(p.flags * kRowsThreads));
+        if (__any_sync(0xffffffffu, bad) && lane == 0) any_bad = 1;
+        __syncthreads();
+        if (threadIdx.x == 0) p.lists[1 + 2 * p.list_w + me] = any_bad;
+        return;
+    }
+    const int per_row = p.slot / ROW_RANKS;  // blocks per row
+    const int row = (int)blockIdx.x / per_row;
+    const int r0 = (int)blockIdx.x % per_row * ROW_RANKS;
+    const int a = __ldcg(p.adapter + row);
+    const bool some = a >= 0 && a < p.L && r0 < p.R;
+    float t[ROW_RANKS] = {};
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const In*>(p.x) +
+                                                    (int64_t)row * p.ldx);
+    const uint4* la[ROW_RANKS];
+#pragma unroll
+    for (int i = 0; i < ROW_RANKS; ++i)  // a rank past the last reads the last's row
+        la[i] = reinterpret_cast<const uint4*>(
+            static_cast<const In*>(p.lora_a) +
+            ((int64_t)(some ? a : 0) * p.R + min(r0 + i, p.R - 1)) * p.ldla);
+    const int vecs = p.depth / 8, rest = p.depth % 8;
+    // vectors v, v + 32 and those of the other ranks, in flight across the list
+    constexpr int U = 2, STEP = WARPS * 32;
+    uint4 xv[U], av[U][ROW_RANKS];
+    auto load = [&](int v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = some && v + u * STEP < vecs;
+            xv[u] = in ? __ldg(x + v + u * STEP) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < ROW_RANKS; ++i)
+                av[u][i] = in ? __ldg(la[i] + v + u * STEP) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto dot = [](float acc, const uint4& u, const uint4& v) {
+        const uint32_t a4[4] = {u.x, u.y, u.z, u.w}, b4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = to_f32x2<BF16>(a4[i]), g = to_f32x2<BF16>(b4[i]);
+            acc = fmaf(f.x, g.x, acc);
+            acc = fmaf(f.y, g.y, acc);
+        }
+        return acc;
+    };
+    int v = warp * 32 + lane;
+    load(v);
+    const int n = make_list<kRowsThreads>(p, 0, ids, slots, list, sums);
+    for (; v - lane - warp * 32 < vecs; v += U * STEP) {
+        if (v - lane - warp * 32 != 0) load(v);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < ROW_RANKS; ++i) t[i] = dot(t[i], xv[u], av[u][i]);
+    }
+    if (some && warp == 0 && lane < rest)
+#pragma unroll
+        for (int i = 0; i < ROW_RANKS; ++i)
+            t[i] = fmaf(to_f32(reinterpret_cast<const In*>(x)[8 * vecs + lane]),
+                        to_f32(reinterpret_cast<const In*>(la[i])[8 * vecs + lane]), t[i]);
+#pragma unroll
+    for (int i = 0; i < ROW_RANKS; ++i) {
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) t[i] += __shfl_xor_sync(0xffffffffu, t[i], d);
+        if (lane == 0) partial[warp][i] = t[i];
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) p.lists[0] = n;
+        if (threadIdx.x < n) p.lists[1 + threadIdx.x] = list[threadIdx.x];
+        if (threadIdx.x < p.list_w) p.lists[1 + p.list_w + threadIdx.x] = slots[threadIdx.x];
+    }
+    const int s = slots[row];
+    In* out = static_cast<In*>(p.T) + (int64_t)row * p.ldt;
+    for (int k = threadIdx.x; k < n * ROW_RANKS; k += kRowsThreads) {
+        const int j = k / ROW_RANKS, i = k % ROW_RANKS;
+        float sum = 0.f;
+        if (j == s && r0 + i < p.R) {
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) sum += partial[w][i];
+            if (p.scale) sum *= p.scale[a];
+        }
+        const int ll = j * p.slot + r0 + i;
+        store_t<In>(out + ll / 32 * 64 + ll % 32, sum);
+    }
 }
 
 // CG: CTAs per unit (a pair halves P's features and Q's rows between its
@@ -593,7 +752,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
     if constexpr (MODE == kRagShrink) {
         const int row0 = cluster / p.chains * p.tile_w;
         const int list_tile = row0 / p.list_w;
-        n_list = make_list(p, list_tile * p.list_w, sm_ids, sm_slots, sm_list, sm_sums);
+        n_list = make_list<RTHREADS>(p, list_tile * p.list_w, sm_ids, sm_slots, sm_list, sm_sums);
         if (cluster % p.chains == 0 && part == 0 && row0 % p.list_w == 0) {
             int32_t* out = p.lists + (int64_t)list_tile * p.list_pitch;
             if (threadIdx.x == 0) out[0] = n_list;
@@ -890,7 +1049,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
         const int q = warp & 3;  // TMEM lane quarter (hardware: warp % 4)
         const int half = (warp - REPI_WARP0) >> 2;
         int acc = 0;
-        uint32_t acc_phase = 0, split_phase = 0;
+        uint32_t acc_phase = 0, split_phase = 0, free_phase = 0;
         // 16-bit results leave in 32 x 32 chunks by TMA (rows K-major at a depth of
         // 2048: 323 us against 337 us by st.global, whose 64-byte rows take the
         // shared-memory port that the operands need); fp32 ones, with 128-byte rows,
@@ -913,23 +1072,10 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             const int subs = p.list_w / p.tile_w;
             const int me = ((cluster / p.chains % subs) * p.chains + cluster % p.chains) * S + part;
             const int ctas = subs * p.chains * S;
-            // 16-byte groups of one adapter's LB (its rows' padding is zero)
-            const int64_t vecs = (int64_t)p.R * p.ldlb / 8;
-            bool bad = false;
-            for (int64_t v = (int64_t)me * (EPI_WARPS * 32) + (threadIdx.x - REPI_WARP0 * 32);
-                 v < vecs; v += (int64_t)ctas * (EPI_WARPS * 32)) {
-                const uint4* b = static_cast<const uint4*>(p.lora_b) + v;
-                for (int a = 0; a < n_list; a += 8) {  // eight loads in flight
-                    uint4 w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = __ldg(b + (int64_t)sm_list[min(a + j, n_list - 1)] * vecs);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        bad |= nonfinite16<BF16>(w[j].x) | nonfinite16<BF16>(w[j].y) |
-                               nonfinite16<BF16>(w[j].z) | nonfinite16<BF16>(w[j].w);
-                }
-            }
+            bool bad = scan_lb<BF16>(p, sm_list, n_list,
+                                     (uint32_t)(me * (EPI_WARPS * 32) + threadIdx.x -
+                                                REPI_WARP0 * 32),
+                                     (uint32_t)(ctas * (EPI_WARPS * 32)));
             bad = __any_sync(0xffffffffu, bad);
             if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 7);
             if (lane == 0) {
@@ -1067,8 +1213,13 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             // Split depth: row j of the unit belongs to CTA j % S; this lane's
             // partial sums of the chunk go there.
             const int own = un.width >> (CG == 1 ? p.split : 0);  // rows per CTA
+            // Up to PARTS_ROWS rows fit beside the ring; more take the ring itself,
+            // once every CTA's MMAs have read theirs.
+            const bool beside = un.width <= C_::PARTS_ROWS;
+            const uint32_t parts_at =
+                beside ? (uint32_t)(C_::RING_BYTES + C_::PARTS_OFFSET) : 0u;
             auto push_chunk = [&](int c, const float (&v)[32]) {
-                const uint32_t at = sP0 + (uint32_t)((part * own * 128 + l) * 4);
+                const uint32_t at = base + parts_at + (uint32_t)((part * own * 128 + l) * 4);
                 auto push = [&](int i) {
                     st_cluster_f32(mapa_shared(at, (uint32_t)(i & (S - 1))) +
                                        (uint32_t)(((c * 32 + i) >> p.split) * 512),
@@ -1176,11 +1327,15 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             if (S == 1) {
                 if (!aborted) each_chunk(emit_chunk);
             } else {
-                // Tell the peers that this CTA's MMAs have read its ring, wait
-                // until all have, and give every CTA the partial sums of its rows.
-                if (!aborted && warp == REPI_WARP0 && lane < S)
-                    mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
-                if (!aborted && !wait_bar_warp(free_bar, split_phase, p)) aborted = true;
+                // Give every CTA the partial sums of its rows (through the ring: after
+                // telling the peers that this CTA's MMAs have read it, and hearing
+                // the same of theirs).
+                if (!beside) {
+                    if (!aborted && warp == REPI_WARP0 && lane < S)
+                        mbar_arrive_cluster(mapa_shared(free_bar, (uint32_t)lane));
+                    if (!aborted && !wait_bar_warp(free_bar, free_phase, p)) aborted = true;
+                    free_phase ^= 1u;
+                }
                 if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 9);
                 if (!aborted) {
                     each_chunk(push_chunk);
@@ -1191,27 +1346,23 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 }
                 if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 11);
                 if (!aborted) {
-                    // add the parts in rank order, four rows at a time so that their
-                    // loads overlap
-                    const float* parts = reinterpret_cast<const float*>(smem) + l;
-                    for (int t0 = half; t0 < own; t0 += 8) {
-                        float v[4];
+                    // add the parts in rank order, eight rows at a time so that
+                    // their loads overlap
+                    const float* parts = reinterpret_cast<const float*>(smem + parts_at) + l;
+                    for (int t0 = half; t0 < own && t0 * S + part < n_rows; t0 += 16) {
+                        float v[8];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            float x[8];
+                        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+#pragma unroll 1
+                        for (int r = 0; r < S; ++r)
 #pragma unroll
-                            for (int r = 0; r < 8; ++r)
-                                x[r] = r < S && t0 + 2 * u < own
-                                           ? parts[(r * own + t0 + 2 * u) * 128] : 0.f;
-                            v[u] = x[0];
+                            for (int u = 0; u < 8; ++u)
+                                if (t0 + 2 * u < own) v[u] += parts[(r * own + t0 + 2 * u) * 128];
+                        if (MODE != kRagShrink && !f_ok) continue;
 #pragma unroll
-                            for (int r = 1; r < 8; ++r) v[u] += x[r];
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 8; ++u) {
                             const int j = (t0 + 2 * u) * S + part;
-                            if (t0 + 2 * u < own && j < n_rows && (MODE == kRagShrink || f_ok))
-                                emit(j, v[u]);
+                            if (t0 + 2 * u < own && j < n_rows) emit(j, v[u]);
                         }
                     }
                 }
@@ -1285,8 +1436,16 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
     }
 
     // ------------------------------------------------------------ teardown --
+    // (Relaxed: no CTA reads what another wrote after this; it only must not
+    // exit, or free its TMEM, while a peer still uses its memory.)
     tc_fence_before_sync();
-    if (CG == 2 || S > 1) cluster_sync_all(); else __syncthreads();
+    if (CG == 2 || S > 1) {
+        __syncwarp();
+        cluster_arrive_relaxed();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, TMEM_COLS);
@@ -1367,10 +1526,30 @@ int dispatch_ragged(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units
                 : launch_ragged_variant<1, kRagRows, false, BF16, OutT>(rp, units, dev, s);
 }
 
+template <bool BF16>
+int launch_lora_rows(RaggedParams& rp, int64_t blocks, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    if (cudaLaunchKernelEx(&cfg, lora_rows_kernel<BF16>, rp) != cudaSuccess) {
+        cudaGetLastError();
+        return kCuda;
+    }
+    note_launch();
+    return kOk;
+}
+
 // The two launches of gemm_lora of one element type.
 template <bool BF16, typename OutT>
 int dispatch_lora(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
                   const DeviceInfo& dev, cudaStream_t s) {
+    if (mode == kRagShrinkRows) return launch_lora_rows<BF16>(rp, units, s);
     if (mode == kRagShrink)
         return launch_ragged_variant<1, kRagShrink, false, BF16, OutT>(rp, units, dev, s);
     if (cg == 2)

@@ -253,16 +253,20 @@ inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count)
     return RaggedShape{1, 128, 1};
 }
 
-// gemm_lora: the expand's shape, and the shrink's rows per tile, split and
-// chains (clusters that share the 128-lane parts of a row tile's list; parts:
-// their largest number, which only decides where tiles and split leave SMs
-// idle).
+// gemm_lora: the expand's shape, and the shrink's: rows_blocks > 0 -- few rows,
+// plain dot products in that many blocks, beside scan_blocks that look over LB
+// --, else rows per tile, split
+// and chains (clusters that share the 128-lane parts of a row tile's list;
+// parts: their largest number, which only decides where tiles and split leave
+// SMs idle). slot: lanes per adapter.
 struct LoraShape {
     RaggedShape expand;
+    int rows_blocks, scan_blocks;
     int shrink_w, shrink_split, chains;
 };
 
-inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, int sm_count) {
+inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, int slot,
+                           int sm_count) {
     LoraShape s{};
     const int64_t pair_units = ((M + 255) / 256) * ((N + 255) / 256);
     if (M > 128 && pair_units * 2 > sm_count) {
@@ -270,6 +274,8 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, 
     } else {
         int w = 16;
         while (w < 128 && w < M) w *= 2;
+        // more rows than a unit: narrower units before a split of the depth
+        if (M > 128 && ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count) w = 64;
         const int64_t units = ((M + w - 1) / w) * ((N + 127) / 128);
         s.expand = RaggedShape{1, w, plan_ragged_split(units, num_kb, sm_count)};
     }
@@ -279,6 +285,10 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, 
     s.shrink_split = plan_ragged_split(tiles, num_kb, sm_count);
     const int64_t chains = sm_count / (tiles * s.shrink_split);
     s.chains = (int)(chains < 1 ? 1 : (chains > parts ? parts : chains));
+    if (M <= 64) {
+        s.rows_blocks = (int)(M * (slot / 4));
+        s.scan_blocks = M < 32 ? 16 : 64;
+    }
     return s;
 }
 
