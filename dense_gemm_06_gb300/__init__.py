@@ -221,7 +221,8 @@ def gemm_grouped(G, M, N, K, offsets, A, lda, B, ldb, strideb, b_major, C, ldc, 
     """C[t] = act(alpha * A[t] B_g^T + beta * C[t] + bias[g]) for the rows t of each
     group g (limits in the device array `offsets`); see include/gemm.h."""
     return load().gemm_grouped(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, strideb,
-                               b_major, _ptr(C), ldc, dtype, _epilogue(alpha, beta, bias, activation), _stream(stream))
+                               b_major, _ptr(C), ldc, dtype,
+                               _epilogue(alpha, beta, bias, activation), _stream(stream))
 
 
 def gemm_grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype,
@@ -229,7 +230,8 @@ def gemm_grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype,
     """C_g = act(alpha * sum over group g's rows t of A[t]^T B[t] + beta * C_g + bias[g])
     (the weight gradient of gemm_grouped); see include/gemm.h."""
     return load().gemm_grouped_k(G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, _ptr(C),
-                                 ldc, stridec, dtype, _epilogue(alpha, beta, bias, activation), _stream(stream))
+                                 ldc, stridec, dtype, _epilogue(alpha, beta, bias, activation),
+                                 _stream(stream))
 
 
 def gemm_lora(M, N, K, L, R, A, lda, B, ldb, b_major, adapter, lora_a, lora_b, scale, C, ldc,

@@ -723,6 +723,12 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
         if (MODE != kRagDepth && p.num_kb > 0) {  // no maps without a depth
             tma_prefetch_desc(&p.map[kMapP]);
             tma_prefetch_desc(&p.map[kMapQ]);
+            tma_prefetch_desc(&p.map[kMapQ16]);
+            if (MODE == kRagLora) {
+                tma_prefetch_desc(&p.map[kMapLB]);
+                tma_prefetch_desc(&p.map[kMapT]);
+                tma_prefetch_desc(&p.map[kMapT16]);
+            }
         }
         for (int s = 0; s < C_::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
@@ -776,10 +782,12 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
     };
     // lora: extension blocks of a unit's list tile; 0 when its flags tell the
     // epilogue to add the adapters' part itself. `ids`: its adapters.
-    auto ext_blocks = [&](int tile, int& n, const int32_t*& ids) {
+    // `id`: this lane's entry of the list, read with the rest (one latency).
+    auto ext_blocks = [&](int tile, int& n, const int32_t*& ids, int& id) {
         const int32_t* l = p.lists + (int64_t)tile * p.list_pitch;
         n = __ldcg(l);
         ids = l + 1;
+        id = __ldcg(ids + (lane & (p.list_w - 1)));
         int bad = 0;
         for (int i = lane; i < p.flags; i += 32) bad |= __ldcg(l + 1 + 2 * p.list_w + i);
         if (__any_sync(0xffffffffu, bad != 0)) return 0;
@@ -878,7 +886,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 if (lane == 0) TC_TRACE(p, 4);
                 int n;
                 const int32_t* ids;
-                const int ne = ext_blocks(un.tile, n, ids);
+                int lane_id;
+                const int ne = ext_blocks(un.tile, n, ids, lane_id);
                 for (int e = part; e < ne && !aborted; e += S) {
                     if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
                     const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
@@ -887,11 +896,12 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     const int k_rows = min(EXT_K, n * p.slot - e * EXT_K);
                     const int box = min(p.slot, EXT_K);  // LB rows per copy
                     const int pieces = k_rows / box;
-                    // every lane loads one adapter number, before the elected lane issues
-                    const int my_lane = e * EXT_K + lane * box;
-                    const int my_id = lane < pieces ? __ldcg(ids + my_lane / p.slot) : 0;
-                    const int id0 = __shfl_sync(0xffffffffu, my_id, 0);
-                    const int id1 = __shfl_sync(0xffffffffu, my_id, 1);
+                    // the (one or two) adapters' numbers, for the lane that issues
+                    const int at0 = e * EXT_K / p.slot, at1 = at0 + 1;
+                    int id0 = __shfl_sync(0xffffffffu, lane_id, at0 & 31);
+                    int id1 = __shfl_sync(0xffffffffu, lane_id, at1 & 31);
+                    if (at0 >= 32) id0 = __ldcg(ids + at0);
+                    if (at1 >= 32 && at1 < n) id1 = __ldcg(ids + at1);
                     if (elect_one()) {
                         if (leader)
                             mbar_arrive_expect_tx(
@@ -994,7 +1004,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     if (!waited) pdl_wait();
                     waited = true;
                     const int32_t* ids;
-                    ne = ext_blocks(un.tile, n, ids);
+                    int lane_id;
+                    ne = ext_blocks(un.tile, n, ids, lane_id);
                     for (int e = part; e < ne && !aborted; e += S) {
                         if (!issued && !wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) {
                             aborted = true;
@@ -1091,7 +1102,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             bool issued = kb1 > kb0;
             const int32_t* ids = nullptr;
             if constexpr (MODE == kRagLora) {
-                ne = ext_blocks(un.tile, n, ids);
+                int lane_id;
+                ne = ext_blocks(un.tile, n, ids, lane_id);
                 issued = issued || part < ne;
             }
             const bool by_hand = MODE == kRagLora && n > 0 && ne == 0;
@@ -1236,10 +1248,9 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             const bool stamp = CG == 2 && !leader && warp == REPI_WARP0 && lane == 0;
             if (stamp) TC_TRACE(p, 20 + 4 * nt);
             const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-            auto read_chunk = [&](int k, uint32_t (&u)[32]) {
-                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + (half + 2 * k) * 32), u);
+            auto read_chunk = [&](int c, uint32_t (&u)[32]) {
+                tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + c * 32), u);
             };
-            auto has = [&](int k) { return k < CHUNKS && (half + 2 * k) * 32 < un.width; };
             auto wait_acc = [&]() {
                 if (!aborted && !wait_bar_inline(accf_bar(acc), acc_phase, p)) aborted = true;
                 tc_fence_after_sync();
@@ -1266,8 +1277,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             bool folded = false;
             auto add_chunk = [&](int k) {
                 uint32_t u[32];
-                read_chunk(k, u);
-                tmem_wait_ld(u);
+                read_chunk(half + 2 * k, u);
+                tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[k][i] += __uint_as_float(u[i]);
             };
@@ -1282,7 +1293,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                         wait_acc();
 #pragma unroll
                         for (int k = 0; k < CHUNKS; ++k)
-                            if (has(k)) add_chunk(k);
+                            if (!aborted && (half + 2 * k) * 32 < un.width) add_chunk(k);
                         free_acc();
                     }
                 }
@@ -1299,31 +1310,32 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     if (folded) {
 #pragma unroll
                         for (int k = 0; k < CHUNKS; ++k)
-                            if (has(k)) {
+                            if ((half + 2 * k) * 32 < un.width) {
                                 add_chunk(k);
-                                if (!has(k + 1)) free_acc();
+                                if (k == CHUNKS - 1) free_acc();
                                 use(half + 2 * k, sum[k]);
                             }
                         return;
                     }
                 }
 #pragma unroll 1
-                for (int k = 0; has(k); ++k) {
+                for (int c = half; c * 32 < un.width; c += 2) {
                     float v[32];
                     if (issued) {
                         uint32_t u[32];
-                        read_chunk(k, u);
-                        tmem_wait_ld(u);
+                        read_chunk(c, u);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                        if (!has(k + 1)) free_acc();
+                        if ((c + 2) * 32 >= un.width) free_acc();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
-                    use(half + 2 * k, v);
+                    use(c, v);
                 }
             };
+
             if (S == 1) {
                 if (!aborted) each_chunk(emit_chunk);
             } else {
@@ -1346,24 +1358,21 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 }
                 if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 11);
                 if (!aborted) {
-                    // add the parts in rank order, eight rows at a time so that
-                    // their loads overlap
+                    // add the parts in rank order (a short loop: it runs once per call
+                    // when decoding, and code that is not in the instruction cache
+                    // costs more than the loads' latency)
                     const float* parts = reinterpret_cast<const float*>(smem + parts_at) + l;
-                    for (int t0 = half; t0 < own && t0 * S + part < n_rows; t0 += 16) {
-                        float v[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = 0.f;
 #pragma unroll 1
-                        for (int r = 0; r < S; ++r)
+                    for (int t = half; t < own; t += 2) {
+                        const int j = t * S + part;
+                        if (j >= n_rows) break;
+                        float x[8], v = 0.f;
 #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (t0 + 2 * u < own) v[u] += parts[(r * own + t0 + 2 * u) * 128];
-                        if (MODE != kRagShrink && !f_ok) continue;
+                        for (int r = 0; r < 8; ++r)
+                            x[r] = r < S ? parts[(r * own + t) * 128] : 0.f;
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const int j = (t0 + 2 * u) * S + part;
-                            if (t0 + 2 * u < own && j < n_rows) emit(j, v[u]);
-                        }
+                        for (int r = 0; r < 8; ++r) v += x[r];
+                        if (MODE == kRagShrink || f_ok) emit(j, v);
                     }
                 }
                 split_phase ^= 1u;
