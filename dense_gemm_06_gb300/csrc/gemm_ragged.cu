@@ -219,6 +219,7 @@ void common_params(RaggedParams& rp, const DeviceInfo& dev) {
     rp.fault_inject = option_tc_fault_inject();
     rp.split = 0;
     rp.chains = 1;
+    rp.lanes = 128;
     rp.slot = 16;
     rp.list_w = 128;
 #ifdef LIBGEMM_TC_TRACE
@@ -483,8 +484,8 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     // The list of a row tile holds at most as many adapters as the tile has
     // rows; the tile is 256 rows wide at most.
     const int64_t most = M < 256 ? M : 256;
-    const int64_t parts = ((L < most ? L : most) * slot + 127) / 128;
-    const LoraShape shape = plan_lora(M, N, num_kb, parts, slot, dev->sm_count);
+    const LoraShape shape =
+        plan_lora(M, N, num_kb, L < most ? L : most, slot, dev->sm_count);
     const RaggedShape& ex = shape.expand;
     const int W = ex.tile_w;
     const int64_t list_n = L < (M < W ? M : W) ? L : (M < W ? M : W);
@@ -545,6 +546,7 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         rp.T = T;
         rp.ldt = ldt;
         RaggedParams sh = rp;  // the shrink
+        sh.lanes = shape.lanes;
         sh.tile_w = shape.shrink_w;
         sh.split = log2_of(shape.shrink_split);
 #ifdef LIBGEMM_TC_TRACE
@@ -589,10 +591,10 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     scratch.release();
     if (rc == kOk)
         dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d blocks of dot products or "
-                     "%d rows, %d chains, split %d; "
+                     "%d lanes x %d rows, %d chains, split %d; "
                      "expand %s, units of %d rows, split %d",
                      (long long)M, (long long)N, (long long)K, (long long)L, (long long)R,
-                     shape.rows_blocks, shape.shrink_w, shape.chains, shape.shrink_split,
+                     shape.rows_blocks, shape.lanes, shape.shrink_w, shape.chains, shape.shrink_split,
                      ex.cta_group == 2 ? "CTA pairs" : "one CTA per unit", W, ex.split);
     return rc;
 }

@@ -63,6 +63,7 @@ struct RaggedParams {
     int64_t ldlb;
     int L, R, slot;          // adapters, rank, lanes per adapter (16, 32, 64 or 128)
     int list_w;              // rows that share one list of adapters (the expand's tile_w)
+    int lanes;               // shrink: lanes per unit, 64 (narrow) or 128
     int chains;              // shrink: clusters that share a row tile's lists of lanes
                              // (kRagShrinkRows: blocks of dot products)
     int32_t* lists;          // per list tile: n, list_w adapter numbers, list_w slots, flags
@@ -102,10 +103,21 @@ int launch_lora_bf16(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t unit
 
 namespace {
 
+constexpr int UNIT_SLOTS = 4;  // units found ahead
+
 // The ring: 128 features and up to 128 rows of 64 k each per CTA and stage.
+// NARROW (the shrink of ranks up to 32): 64 of both, two k-blocks to a stage.
+// With so little work in a block the loops' own latency (a wait, an election,
+// a commit: 0.22 us) is what bounds it, not the bytes: 8192 rows of 4096 took
+// 22 us with one block per stage however many stages there were. The MMA's
+// other 64 lanes read whatever lies behind and are never stored.
+template <bool NARROW>
 struct RCfg {
-    static constexpr int P_BYTES = 128 * BK * 2;
-    static constexpr int Q_BYTES = 128 * BK * 2;
+    static constexpr int LANES = NARROW ? 64 : 128;
+    static constexpr int SUB = NARROW ? 2 : 1;  // k-blocks per stage
+    static constexpr int BLOCK_BYTES = LANES * BK * 2;
+    static constexpr int P_BYTES = SUB * BLOCK_BYTES;
+    static constexpr int Q_BYTES = SUB * BLOCK_BYTES;
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
     static constexpr int STAGES = 6;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -119,7 +131,7 @@ struct RCfg {
     // full[S], empty[S], acc_full[2], acc_empty[2], drain, never, ring_free, parts,
     // unit_ready[UNITS], unit_read[UNITS], unit_read_by_peer[UNITS]; then the TMEM
     // address and the units
-    static constexpr int UNITS = 4;
+    static constexpr int UNITS = UNIT_SLOTS;
     static constexpr int NUM_BARS = 2 * STAGES + 8 + 3 * UNITS;
     static constexpr int UNIT_OFFSET = NUM_BARS * 8 + 16;
     static constexpr int SMEM_BYTES = RING_BYTES + EXTRA_BYTES + UNIT_OFFSET + UNITS * 48 + 1024;
@@ -292,14 +304,15 @@ struct Units {
     }
 };
 
-// shrink: the units of a cluster are the 128-lane parts sg = chain, chain +
+// shrink: the units of a cluster are the lane parts (`lanes` each) sg = chain, chain +
 // chains, ... of its row tile's list (lane l of the list: rank index l % slot
 // of its l / slot-th adapter); un.g = sg.
 template <>
 struct Units<1, kRagShrink> {
     int sg, parts, tile;
     __device__ __forceinline__ Units(const RaggedParams& p, int cluster, int n)
-        : sg(cluster % p.chains), parts((n * p.slot + 127) / 128), tile(cluster / p.chains) {}
+        : sg(cluster % p.chains), parts((n * p.slot + p.lanes - 1) / p.lanes),
+          tile(cluster / p.chains) {}
     __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
         if (sg >= parts || tile * p.tile_w >= p.rows) return false;
         un.g = sg;
@@ -363,15 +376,15 @@ struct Feed {
     }
     // The next unit / its slot may be used again.
     __device__ __forceinline__ bool peek(const RaggedParams& p, RUnit& un) {
-        const int s = j % RCfg::UNITS;
-        if (!__all_sync(0xffffffffu, wait_unit(ready + 8u * s, (uint32_t)(j / RCfg::UNITS) & 1u, p)))
+        const int s = j % UNIT_SLOTS;
+        if (!__all_sync(0xffffffffu, wait_unit(ready + 8u * s, (uint32_t)(j / UNIT_SLOTS) & 1u, p)))
             return false;
         return get_unit(slots + 48u * s, un);
     }
     __device__ __forceinline__ void done() {
         __syncwarp();
         if ((threadIdx.x & 31) == 0)
-            mbar_arrive_local(ready + 8u * (RCfg::UNITS + j % RCfg::UNITS));
+            mbar_arrive_local(ready + 8u * (UNIT_SLOTS + j % UNIT_SLOTS));
         ++j;
     }
 };
@@ -664,12 +677,15 @@ __global__ void __launch_bounds__(kRowsThreads) lora_rows_kernel(const __grid_co
 
 // CG: CTAs per unit (a pair halves P's features and Q's rows between its
 // CTAs). P_MN: P's features are contiguous (weights N-major; always in the
-// depth product). With p.split > 0 (CG == 1) a cluster of 2^split CTAs shares
+// depth product); the shrink, whose P is always K-major, runs its narrow ring
+// with it. With p.split > 0 (CG == 1) a cluster of 2^split CTAs shares
 // each unit: every CTA sums its share of the k-blocks, and the partial sums
 // meet in the shared memory of the CTA that owns the row, in rank order.
 template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
 __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
-    using C_ = RCfg;
+    constexpr bool NARROW = MODE == kRagShrink && P_MN;
+    constexpr bool PF_MN = P_MN && MODE != kRagShrink;  // P's features are contiguous
+    using C_ = RCfg<NARROW>;
     using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr bool Q_MN = MODE == kRagDepth;
     constexpr bool FOLD = std::is_same_v<OutT, float> && MODE != kRagShrink;
@@ -822,10 +838,10 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 }
             }
             // shrink: the adapters whose lanes this unit holds
-            const int spu = MODE == kRagShrink ? 128 / p.slot : 1;
+            const int spu = MODE == kRagShrink ? C_::LANES / p.slot : 1;
             const int s0 = MODE == kRagShrink ? un.g * spu : 0;
             const int ns = MODE == kRagShrink ? min(spu, n_list - s0) : 1;
-            for (int kb = kb0; kb < kb1 && !aborted; ++kb) {
+            for (int kb = kb0; kb < kb1 && !aborted; kb += C_::SUB) {
                 if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
                 const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
                 const uint32_t sp = sP0 + stage * C_::P_BYTES;
@@ -853,13 +869,17 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     if (kb == kb0 && lane == 0) TC_TRACE(p, 2);
                     if (x_ok && elect_one()) {
                         const int p_bytes = MODE == kRagShrink ? ns * p.slot * BK * 2 : C_::P_BYTES;
+                        const int subs = NARROW ? min(C_::SUB, kb1 - kb) : 1;
                         if (leader)
-                            mbar_arrive_expect_tx(full_bar(stage),
-                                                  (uint32_t)(CG * (p_bytes + q_rows * BK * 2)));
+                            mbar_arrive_expect_tx(
+                                full_bar(stage),
+                                (uint32_t)(subs * CG * (p_bytes + q_rows * BK * 2)));
                         if constexpr (MODE == kRagShrink) {
                             for (int j = 0; j < ns; ++j)
-                                tma_load_3d<CG>(sp + j * p.slot * BK * 2, &p.map[kMapP], fb, k0, 0,
-                                                sm_list[s0 + j]);
+                                for (int b = 0; b < subs; ++b)
+                                    tma_load_3d<CG>(
+                                        sp + b * C_::BLOCK_BYTES + j * p.slot * BK * 2,
+                                        &p.map[kMapP], fb, k0 + b * BK, 0, sm_list[s0 + j]);
                         } else if constexpr (!P_MN) {
                             tma_load_3d<CG>(sp, &p.map[kMapP], fb, k0, f0, un.g);
                         } else {
@@ -867,11 +887,15 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                                 tma_load_3d<CG>(sp + j * 64 * BK * 2, &p.map[kMapP], fb,
                                                 f0 + 64 * j, k0, un.g);
                         }
-                        if (un.width == p.tile_w) {
-                            tma_load_2d<CG>(sq, &p.map[kMapQ], fb, k0, q_row);
-                        } else {
-                            for (int r = 0; r < q_rows; r += 16)
-                                tma_load_2d<CG>(sq + r * 128, &p.map[kMapQ16], fb, k0, q_row + r);
+                        for (int b = 0; b < subs; ++b) {
+                            const uint32_t dst = sq + (uint32_t)(b * C_::BLOCK_BYTES);
+                            if (un.width == p.tile_w) {
+                                tma_load_2d<CG>(dst, &p.map[kMapQ], fb, k0 + b * BK, q_row);
+                            } else {
+                                for (int r = 0; r < q_rows; r += 16)
+                                    tma_load_2d<CG>(dst + r * 128, &p.map[kMapQ16], fb, k0 + b * BK,
+                                                    q_row + r);
+                            }
                         }
                     }
                 }
@@ -934,14 +958,14 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
         if (leader) {
             if constexpr (MODE == kRagRows || MODE == kRagDepth) pdl_wait();
             constexpr uint32_t idesc0 =
-                make_idesc_f16(BF16, P_MN, Q_MN, (uint32_t)(128 * CG), 0u);
+                make_idesc_f16(BF16, PF_MN, Q_MN, (uint32_t)(128 * CG), 0u);
             constexpr uint32_t idesc_ext0 =
                 make_idesc_f16(BF16, true, false, (uint32_t)(128 * CG), 0u);
             const uint64_t p_mn0 = make_sdesc_sw128(sP0, 64 * BK * 2, 1024);
-            const uint64_t p_desc0 = P_MN ? p_mn0 : make_sdesc_sw128(sP0, 16, 1024);
+            const uint64_t p_desc0 = PF_MN ? p_mn0 : make_sdesc_sw128(sP0, 16, 1024);
             const uint64_t q_desc0 = Q_MN ? make_sdesc_sw128(sQ0, 64 * BK * 2, 1024)
                                           : make_sdesc_sw128(sQ0, 16, 1024);
-            constexpr int P_STEP = P_MN ? UMMA_K * 128 : UMMA_K * 2;
+            constexpr int P_STEP = PF_MN ? UMMA_K * 128 : UMMA_K * 2;
             constexpr int Q_STEP = Q_MN ? UMMA_K * 128 : UMMA_K * 2;
             int stage = 0;
             uint32_t phase = 0;
@@ -964,7 +988,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
                     const int first = kb;
                     const int last = FOLD ? min(kb + FOLD_KB, kb1) : kb1;
-                    for (; kb < last; ++kb) {
+                    for (; kb < last; kb += C_::SUB) {
                         if (!wait_bar_warp(full_bar(stage), phase, p)) { aborted = true; break; }
                         tc_fence_after_sync();
                         if (kb == kb0 && lane == 0) TC_TRACE(p, 5);
@@ -980,6 +1004,14 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                                     mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
                                                 qd + (uint64_t)(j * (Q_STEP >> 4)), idesc,
                                                 ((kb - first) | j) != 0 ? 1u : 0u);
+                                if (NARROW && kb + 1 < last) {  // the stage's second block
+#pragma unroll
+                                    for (int j = 0; j < BK / UMMA_K; ++j)
+                                        mma_f16<CG>(d_tmem,
+                                                    pd + (uint64_t)((C_::BLOCK_BYTES + j * P_STEP) >> 4),
+                                                    qd + (uint64_t)((C_::BLOCK_BYTES + j * Q_STEP) >> 4),
+                                                    idesc, 1u);
+                                }
                             } else {
                                 for (int j = 0; j * UMMA_K < left; ++j)
                                     mma_f16<CG>(d_tmem, pd + (uint64_t)(j * (P_STEP >> 4)),
@@ -1126,8 +1158,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             const int* row_slot = nullptr;  // the rows' places in the list
             int my_slot = 0;                // -2 for a lane past the rank: matches no row
             if constexpr (MODE == kRagShrink) {
-                const int ll = un.g * 128 + l;
-                slot = ll / p.slot;
+                const int ll = un.g * C_::LANES + l;
+                slot = l < C_::LANES ? ll / p.slot : n_list;  // n_list: nothing to store
                 r_idx = ll % p.slot;
                 if (slot < n_list && p.scale) factor = p.scale[sm_list[slot]];
                 my_slot = r_idx < p.R ? slot : -2;
@@ -1479,7 +1511,7 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.blockDim = dim3(RTHREADS);
-    cfg.dynamicSmemBytes = RCfg::SMEM_BYTES;
+    cfg.dynamicSmemBytes = RCfg<MODE == kRagShrink && P_MN>::SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     {
@@ -1487,7 +1519,7 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
         const uint64_t bit = 1ull << (dev.device & 63);
         if (!(configured & bit)) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     RCfg::SMEM_BYTES) != cudaSuccess)
+                                     RCfg<MODE == kRagShrink && P_MN>::SMEM_BYTES) != cudaSuccess)
                 return kCuda;
             int n = dev.sm_count / 2;
             if (CG == 2) {
@@ -1560,7 +1592,9 @@ int dispatch_lora(RaggedParams& rp, int mode, int cg, bool p_mn, int64_t units,
                   const DeviceInfo& dev, cudaStream_t s) {
     if (mode == kRagShrinkRows) return launch_lora_rows<BF16>(rp, units, s);
     if (mode == kRagShrink)
-        return launch_ragged_variant<1, kRagShrink, false, BF16, OutT>(rp, units, dev, s);
+        return rp.lanes == 64
+                   ? launch_ragged_variant<1, kRagShrink, true, BF16, OutT>(rp, units, dev, s)
+                   : launch_ragged_variant<1, kRagShrink, false, BF16, OutT>(rp, units, dev, s);
     if (cg == 2)
         return p_mn ? launch_ragged_variant<2, kRagLora, true, BF16, OutT>(rp, units, dev, s)
                     : launch_ragged_variant<2, kRagLora, false, BF16, OutT>(rp, units, dev, s);

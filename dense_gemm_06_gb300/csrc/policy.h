@@ -255,17 +255,19 @@ inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count)
 
 // gemm_lora: the expand's shape, and the shrink's: rows_blocks > 0 -- few rows,
 // plain dot products in that many blocks, beside scan_blocks that look over LB
-// --, else rows per tile, split
-// and chains (clusters that share the 128-lane parts of a row tile's list;
-// parts: their largest number, which only decides where tiles and split leave
-// SMs idle). slot: lanes per adapter.
+// --, else lanes per unit, rows per tile, split and chains (clusters that share
+// the parts of a row tile's list). slot: lanes per adapter; ranks up to 32 run
+// the narrow ring (64 lanes and rows, twice the stages: a tile of requests one
+// after the other seldom has more than two adapters). listed: most adapters of
+// a list.
 struct LoraShape {
     RaggedShape expand;
+    int lanes;
     int rows_blocks, scan_blocks;
     int shrink_w, shrink_split, chains;
 };
 
-inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, int slot,
+inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed, int slot,
                            int sm_count) {
     LoraShape s{};
     const int64_t pair_units = ((M + 255) / 256) * ((N + 255) / 256);
@@ -279,8 +281,10 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t parts, 
         const int64_t units = ((M + w - 1) / w) * ((N + 127) / 128);
         s.expand = RaggedShape{1, w, plan_ragged_split(units, num_kb, sm_count)};
     }
-    s.shrink_w = s.expand.tile_w < 128 ? s.expand.tile_w : 128;
+    s.lanes = slot <= 32 ? 64 : 128;
+    s.shrink_w = s.expand.tile_w < s.lanes ? s.expand.tile_w : s.lanes;
     if (M > 128 && (M + 127) / 128 * 2 <= sm_count) s.shrink_w = 64;
+    const int64_t parts = (listed * slot + s.lanes - 1) / s.lanes;
     const int64_t tiles = (M + s.shrink_w - 1) / s.shrink_w;
     s.shrink_split = plan_ragged_split(tiles, num_kb, sm_count);
     const int64_t chains = sm_count / (tiles * s.shrink_split);

@@ -4,8 +4,8 @@
 //
 //   grouped   G M N num_kb sm_count    -> "cta_group tile_w split"
 //   grouped_k G M N sm_count           -> "cta_group tile_w split"
-//   lora M N num_kb parts slot sm_count
-//       -> "cta_group tile_w split rows_blocks scan_blocks shrink_w shrink_split chains"
+//   lora M N num_kb listed slot sm_count
+//       -> "cta_group tile_w split rows_blocks scan_blocks lanes shrink_w shrink_split chains"
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -28,8 +28,8 @@ int main(int argc, char** argv) {
     if (argc == 8 && std::strcmp(argv[1], "lora") == 0) {
         const LoraShape s =
             plan_lora(arg(2), arg(3), arg(4), arg(5), (int)arg(6), (int)arg(7));
-        std::printf("%d %d %d %d %d %d %d %d\n", s.expand.cta_group, s.expand.tile_w,
-                    s.expand.split, s.rows_blocks, s.scan_blocks, s.shrink_w, s.shrink_split, s.chains);
+        std::printf("%d %d %d %d %d %d %d %d %d\n", s.expand.cta_group, s.expand.tile_w,
+                    s.expand.split, s.rows_blocks, s.scan_blocks, s.lanes, s.shrink_w, s.shrink_split, s.chains);
         return 0;
     }
     return 2;
