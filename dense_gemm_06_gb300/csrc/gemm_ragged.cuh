@@ -142,10 +142,12 @@ constexpr int REPI_WARP0 = 3;
 constexpr int RTHREADS = 32 * (REPI_WARP0 + EPI_WARPS);
 // fp32 results: depth summed in one accumulator, in k-blocks. The tensor core
 // cuts each addition to the accumulator off below 2^-23 of it, an error that
-// grows with the depth (measured: 1.3e-6 of the result's norm at a depth of
-// 1037, 3.5e-6 at a few thousand), so sums of 512 are added up in registers
-// with rounding. 16-bit results round off 2^-9 or 2^-12 anyway and sum whole.
-constexpr int FOLD_KB = 8;
+// grows with the depth (measured against 64 bits, 2-norm: 1.3e-6 of the result
+// at a depth of 1037, 3.5e-6 at a few thousand), so sums of 704 are added up in
+// registers with rounding (6e-7 at any depth; plain fp32 sums: 2.5e-7 to
+// 5e-7). 16-bit results round off 2^-9 or 2^-12 anyway and sum whole. Sums of
+// 512, 768 or 1024 take the same time (476-483 us, 64 gradients of 2816 x 2048).
+constexpr int FOLD_KB = 11;
 constexpr int EXT_K = 32;  // lanes of T (rows of LB) per extension block: hi | lo fill 64
 
 // One unit of work: `width` rows of C from row0 (those before row_end are
