@@ -197,11 +197,11 @@ bool map_3d(RaggedParams& rp, int i, bool bf16, const Operand& o, uint32_t box_o
                          (uint64_t)o.ld, (uint64_t)o.mats, (uint64_t)stride, 64, box_outer);
 }
 
-// A 16-bit C by TMA where its rows (and matrices) are 16-byte aligned and
-// nothing is fused: a box is one staging tile, 32 features by 32 rows.
+// A 16-bit C by TMA where its rows (and matrices) are 16-byte aligned: a box is
+// one staging tile, 32 features by 32 rows.
 void map_c(RaggedParams& rp, int dtype, void* C, int64_t mats, int64_t stride, int64_t rows,
            int64_t cols, int64_t ld) {
-    if (c_bytes(dtype) != 2 || rp.epi.active || !aligned_to(C, 16) || ld % 8 ||
+    if (c_bytes(dtype) != 2 || !aligned_to(C, 16) || ld % 8 ||
         (mats > 1 && stride % 8))
         return;
     rp.c_tma = encode_tma_c16(&rp.map[kMapC], is_bf16(dtype), C, (uint64_t)cols, (uint64_t)rows,

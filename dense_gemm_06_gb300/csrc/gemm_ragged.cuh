@@ -1149,6 +1149,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             float bias = 0.f;
             if (epi && p.epi.bias && f_ok)
                 bias = to_f32(static_cast<const OutT*>(p.epi.bias)[(int64_t)un.g * p.feats + f]);
+            const bool accumulates = epi && p.epi.beta == 1.f && !p.epi.bias && p.epi.act == 0;
             OutT* c_col = nullptr;
             if constexpr (MODE != kRagShrink)
                 c_col = static_cast<OutT*>(p.C) + (int64_t)un.row0 * p.ldc + f +
@@ -1169,31 +1170,29 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 t_col = static_cast<In*>(p.T) + (int64_t)un.row0 * p.ldt +
                         (int64_t)(ll / 32) * 64 + lane;
             }
-            // Row j of the unit, value v of this lane.
+            // lora, by hand: what row j's adapter adds to this lane's feature.
+            auto adapters = [&](int j) {
+                const int s = __ldcg(ids + p.list_w + j);
+                if (s < 0) return 0.f;
+                const int id = __ldcg(ids + s);
+                return adapter_part<In>(
+                    static_cast<const In*>(p.T) + (int64_t)(un.row0 + j) * p.ldt,
+                    static_cast<const In*>(p.lora_b) + (int64_t)id * p.R * p.ldlb + f, p.ldlb,
+                    s * p.slot, p.R);
+            };
+            // One row j of the unit, value v of this lane (split depths).
             auto emit = [&](int j, float v) {
                 if constexpr (MODE == kRagShrink) {
                     if (slot < n_list) store_t<In>(t_col + (int64_t)j * p.ldt,
                                                    row_slot[j] == my_slot ? v * factor : 0.f);
-                } else {
-                    if constexpr (MODE == kRagLora) {
-                        if (by_hand) {
-                            const int s = __ldcg(ids + p.list_w + j);
-                            if (s >= 0) {
-                                const int id = __ldcg(ids + s);
-                                v += adapter_part<In>(
-                                    static_cast<const In*>(p.T) + (int64_t)(un.row0 + j) * p.ldt,
-                                    static_cast<const In*>(p.lora_b) +
-                                        (int64_t)id * p.R * p.ldlb + f,
-                                    p.ldlb, s * p.slot, p.R);
-                            }
-                        }
-                    }
-                    if (c_checked(p, un.row0 + j, f))
-                        store_c<OutT>(p, c_col + (int64_t)j * p.ldc, v, bias, epi);
+                } else if (f_ok && c_checked(p, un.row0 + j, f)) {
+                    if (MODE == kRagLora && by_hand) v += adapters(j);
+                    store_c<OutT>(p, c_col + (int64_t)j * p.ldc, v, bias, epi);
                 }
             };
-            // Rows 32 c .. of the unit, v[i] this lane's value of row 32 c + i.
-            auto emit_chunk = [&](int c, const float (&v)[32]) {
+            // Rows 32 c .. of the unit, v[i] this lane's value of row 32 c + i (the
+            // fused epilogue works in place).
+            auto emit_chunk = [&](int c, float (&v)[32]) {
                 const int left = n_rows - c * 32;
                 if constexpr (MODE == kRagShrink) {
                     if (slot >= n_list) return;
@@ -1208,12 +1207,59 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     }
                     return;
                 }
+                OutT* dst = c_col + (int64_t)(c * 32) * p.ldc;
+                const int row = un.row0 + c * 32;
+                if constexpr (MODE == kRagLora) {
+                    if (by_hand && f_ok) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < left) v[i] += adapters(c * 32 + i);
+                    }
+                }
+                if constexpr (std::is_same_v<OutT, float>) {
+                    if (accumulates) {
+                        // C += alpha * sum, added in L2: nothing to wait for (each
+                        // element gets one addition, so its order is no question)
+                        if (!f_ok) return;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (i < left && c_checked(p, row + i, f))
+                                red_add_f32(dst, p.epi.alpha * v[i]);
+                            dst += p.ldc;
+                        }
+                        return;
+                    }
+                }
+                if (epi && f_ok) {
+                    // the incoming C of OLD rows at a time: one latency for all of them
+                    constexpr int OLD = FOLD ? 8 : 32;
+#pragma unroll
+                    for (int r = 0; r < 32; r += OLD) {
+                        float old[OLD];
+#pragma unroll
+                        for (int i = 0; i < OLD; ++i)
+                            old[i] = p.epi.beta != 0.f && r + i < left
+                                         ? to_f32(dst[(int64_t)(r + i) * p.ldc]) : 0.f;
+#pragma unroll
+                        for (int i = 0; i < OLD; ++i) {
+                            v[r + i] *= p.epi.alpha;
+                            if (p.epi.beta != 0.f) v[r + i] = fmaf(p.epi.beta, old[i], v[r + i]);
+                            v[r + i] += bias;
+                        }
+                    }
+                    if (p.epi.act == 1) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], 1);
+                    } else if (p.epi.act == 2) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], 2);
+                    }
+                }
                 if constexpr (BY_TMA) {
-                    if (!epi && !by_hand && p.c_tma && left >= 32 && f - lane + 32 <= p.feats) {
+                    if (p.c_tma && left >= 32 && f - lane + 32 <= p.feats) {
                         // A whole chunk goes through one of the warp's two staging
                         // tiles, written while TMA still reads the other.
                         const uint32_t tile = tiles + (uint32_t)(tile_i * C_::TILE_BYTES);
-                        const int row = un.row0 + c * 32;
                         tile_i ^= 1;
                         if (lane == 0) bulk_wait_read_1();
                         __syncwarp();
@@ -1233,27 +1279,19 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                     }
                 }
                 if (!f_ok) return;
-                if (!epi && !by_hand) {
-                    // one store and one pointer step per row
-                    OutT* dst = c_col + (int64_t)(c * 32) * p.ldc;
-                    if (left >= 32) {
+                // one store and one pointer step per row
+                if (left >= 32) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (c_checked(p, un.row0 + c * 32 + i, f)) *dst = from_f32<OutT>(v[i]);
-                            dst += p.ldc;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (i < left && c_checked(p, un.row0 + c * 32 + i, f))
-                                *dst = from_f32<OutT>(v[i]);
-                            dst += p.ldc;
-                        }
+                    for (int i = 0; i < 32; ++i) {
+                        if (c_checked(p, row + i, f)) *dst = from_f32<OutT>(v[i]);
+                        dst += p.ldc;
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < left) emit(c * 32 + i, v[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < left && c_checked(p, row + i, f)) *dst = from_f32<OutT>(v[i]);
+                        dst += p.ldc;
+                    }
                 }
             };
             // Split depth: row j of the unit belongs to CTA j % S; this lane's
@@ -1406,7 +1444,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                             x[r] = r < S ? parts[(r * own + t) * 128] : 0.f;
 #pragma unroll
                         for (int r = 0; r < 8; ++r) v += x[r];
-                        if (MODE == kRagShrink || f_ok) emit(j, v);
+                        emit(j, v);
                     }
                 }
                 split_phase ^= 1u;

@@ -214,6 +214,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(cluster_addr), "f"(v) : "memory");
 }
 
+// *p += v in global memory, rounded to nearest; nothing comes back.
+__device__ __forceinline__ void red_add_f32(float* p, float v) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" :: "l"(p), "f"(v) : "memory");
+}
+
 // Four words at a 16-byte aligned shared::cluster address.
 __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t x, uint32_t y,
                                               uint32_t z, uint32_t w) {
