@@ -683,7 +683,11 @@ __global__ void __launch_bounds__(kRowsThreads) lora_rows_kernel(const __grid_co
 // with it. With p.split > 0 (CG == 1) a cluster of 2^split CTAs shares
 // each unit: every CTA sums its share of the k-blocks, and the partial sums
 // meet in the shared memory of the CTA that owns the row, in rank order.
-template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
+// EPI: the launch has a fused epilogue. A template argument where fp32 sums are
+// folded (else always true): the 128 sums leave the plain kernel no registers
+// for code that it does not run (511 us against 477 us, 64 weight gradients of
+// 2816 x 2048).
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, bool EPI>
 __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
     constexpr bool NARROW = MODE == kRagShrink && P_MN;
     constexpr bool PF_MN = P_MN && MODE != kRagShrink;  // P's features are contiguous
@@ -1144,7 +1148,7 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
             const int l = q * 32 + lane;  // TMEM lane
             const int f = un.feat0 + (int)rank * 128 + l;
             const int n_rows = min(un.width, un.row_end - un.row0);
-            const bool epi = MODE != kRagShrink && p.epi.active;
+            const bool epi = EPI && MODE != kRagShrink && p.epi.active;
             const bool f_ok = f < p.feats;
             float bias = 0.f;
             if (epi && p.epi.bias && f_ok)
@@ -1536,10 +1540,13 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
 
 // units: work units (an upper bound where only the device knows their number);
 // the grid holds as many clusters as fit the GPU at once, at most one per unit.
-template <int CG, int MODE, bool P_MN, bool BF16, typename OutT>
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, bool EPI = true>
 int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev,
                           cudaStream_t stream) {
-    auto kern = ragged_kernel<CG, MODE, P_MN, BF16, OutT>;
+    if constexpr (EPI && std::is_same_v<OutT, float> && MODE != kRagShrink)
+        if (!rp.epi.active)
+            return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, false>(rp, units, dev, stream);
+    auto kern = ragged_kernel<CG, MODE, P_MN, BF16, OutT, EPI>;
     static std::mutex mu;
     static uint64_t configured = 0;  // bit per device
     static int pairs[64];
