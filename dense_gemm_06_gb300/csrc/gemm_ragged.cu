@@ -320,14 +320,21 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     if (!units_fit(units, shape.cta_group * shape.split)) return kUnsupported;
 
     Scratch scratch{pool, s, dev->device};
-    if (K > 0) {
-        Operand* const ops[2] = {&a, &b};
-        const int64_t bytes = repack_bytes(ops, 2);
-        if (bytes > 0) {
-            char* at = static_cast<char*>(scratch.get((size_t)bytes));
-            if (!at) return kCuda;
-            rc = repack(ops, 2, at, *dev, s);
+    Operand* const ops[2] = {&a, &b};
+    const int64_t ticket_bytes =
+        plan_grouped_ticket(shape, M, N, num_kb, dev->sm_count) ? 256 : 0;
+    const int64_t bytes = ticket_bytes + (K > 0 ? repack_bytes(ops, 2) : 0);
+    char* at = nullptr;
+    if (bytes > 0 && !(at = static_cast<char*>(scratch.get((size_t)bytes)))) return kCuda;
+    if (ticket_bytes > 0) {
+        rp.ticket = reinterpret_cast<unsigned int*>(at);
+        if (cudaMemsetAsync(rp.ticket, 0, sizeof(unsigned int), s) != cudaSuccess) {
+            cudaGetLastError();
+            rc = kCuda;
         }
+    }
+    if (K > 0 && rc == kOk) {
+        rc = repack(ops, 2, at + ticket_bytes, *dev, s);
         if (rc == kOk &&
             !(map_3d(rp, kMapP, bf16, b, kmaj ? 128 : BK) &&
               map_2d(rp, kMapQ, bf16, a, (uint32_t)(shape.tile_w / shape.cta_group)) &&

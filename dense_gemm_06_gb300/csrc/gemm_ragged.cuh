@@ -34,8 +34,8 @@ enum RaggedMap {
 struct RaggedParams {
     CUtensorMap map[kRaggedMaps];
     const int32_t* offsets;  // rows, depth: G + 1 group limits
-    // depth, in device memory: P's and Q's map of each group, the order of the
-    // groups and the count of units taken
+    // in device memory; depth: P's and Q's map of each group and the order of the
+    // groups; depth, and rows where units are many: the count of units taken
     const CUtensorMap* gmaps;
     const int32_t* order;
     unsigned int* ticket;
@@ -262,11 +262,11 @@ struct Units {
     __device__ __forceinline__ bool next(const RaggedParams& p, RUnit& un) {
         int t = u;
         u += step;
-        if constexpr (MODE == kRagDepth) {
+        if constexpr (MODE == kRagDepth || MODE == kRagRows) {
             // After its first unit a cluster takes the next one that nobody has:
             // the groups, and so the units, are of any size (see depth_maps_kernel
-            // for the order).
-            if (started) {
+            // for their order in the depth product).
+            if (started && (MODE == kRagDepth || p.ticket)) {
                 if ((threadIdx.x & 31) == 0) t = step + (int)atomicAdd(p.ticket, 1u);
                 t = __shfl_sync(0xffffffffu, t, 0);
             }

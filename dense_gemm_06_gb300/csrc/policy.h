@@ -246,6 +246,18 @@ inline RaggedShape plan_grouped(int64_t G, int64_t M, int64_t N, int64_t num_kb,
     return RaggedShape{1, 128, plan_ragged_split(units, num_kb, sm_count)};
 }
 
+// gemm_grouped: whether CTA pairs count the units taken instead of walking every
+// n-th one. The units' widths differ, so a fixed walk ends up to about a unit
+// late; the count costs a 4-byte memset before the launch and the launch's
+// overlap with what precedes it. Measured: units of 224 k-blocks (8 groups,
+// 16384 rows, 4096 x 14336) 1034 us against 1073 us, units of 32 (64 groups,
+// 49152 rows, 2816 x 2048) 348 us against 345 us; so from 64 k-blocks on, with
+// two rounds of units at least.
+inline bool plan_grouped_ticket(const RaggedShape& s, int64_t M, int64_t N, int64_t num_kb,
+                                int sm_count) {
+    return s.cta_group == 2 && num_kb >= 64 && (M / 256) * ((N + 255) / 256) >= sm_count;
+}
+
 // gemm_grouped_k: G results of M x N.
 inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count) {
     const int64_t pair_units = G * ((M + 255) / 256) * ((N + 255) / 256);

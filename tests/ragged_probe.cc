@@ -3,6 +3,7 @@
 // own policy header (tests/test_ragged_policy.py drives it).
 //
 //   grouped   G M N num_kb sm_count    -> "cta_group tile_w split"
+//   ticket G M N num_kb sm_count       -> "0" or "1"
 //   grouped_k G M N sm_count           -> "cta_group tile_w split"
 //   lora M N num_kb listed slot sm_count
 //       -> "cta_group tile_w split rows_blocks scan_blocks lanes shrink_w shrink_split chains"
@@ -18,6 +19,11 @@ int main(int argc, char** argv) {
     if (argc == 7 && std::strcmp(argv[1], "grouped") == 0) {
         const RaggedShape s = plan_grouped(arg(2), arg(3), arg(4), arg(5), (int)arg(6));
         std::printf("%d %d %d\n", s.cta_group, s.tile_w, s.split);
+        return 0;
+    }
+    if (argc == 7 && std::strcmp(argv[1], "ticket") == 0) {
+        const RaggedShape s = plan_grouped(arg(2), arg(3), arg(4), arg(5), (int)arg(6));
+        std::printf("%d\n", plan_grouped_ticket(s, arg(3), arg(4), arg(5), (int)arg(6)) ? 1 : 0);
         return 0;
     }
     if (argc == 6 && std::strcmp(argv[1], "grouped_k") == 0) {

@@ -71,6 +71,7 @@ def test_rows_exact(dtype, major, sizes, N, K):
     ([600, 1, 900, 33], 2500, 72, K_MAJOR),
     ([(i * 7) % 5 for i in range(300)], 192, 96, K_MAJOR),     # three chunks of groups
     ([0] * 290 + [3, 0, 200], 130, 64, K_MAJOR),
+    ([5000, 2000, 0, 300, 2900, 9], 2048, 4104, MN_MAJOR),     # pairs that count their units
     ([2, 1], 256, 8192, K_MAJOR),                              # a cluster shares the depth
     ([9], 1024, 4096, MN_MAJOR),
     ([33, 90], 128, 2048, K_MAJOR),

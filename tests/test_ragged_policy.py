@@ -47,6 +47,16 @@ def test_grouped_shape(probe, G, M, N, num_kb, want):
     assert probe("grouped", G, M, N, num_kb, SMS) == want
 
 
+@pytest.mark.parametrize("G,M,N,num_kb,want", [
+    (8, 16384, 4096, 224, 1), (8, 16384, 4096, 64, 1), (8, 16384, 4096, 63, 0),
+    (64, 49152, 2816, 32, 0),
+    (8, 2560, 4096, 224, 1), (8, 2048, 4096, 224, 0),  # 160 and 128 whole units on 76 pairs
+    (64, 512, 4096, 224, 0),                           # single CTAs
+])
+def test_grouped_counts_its_units(probe, G, M, N, num_kb, want):
+    assert probe("ticket", G, M, N, num_kb, SMS) == (want,)
+
+
 @pytest.mark.parametrize("G,M,N,want", [
     (64, 2816, 2048, (2, 256, 1)), (24, 776, 520, (2, 256, 1)), (4, 256, 256, (1, 128, 1)),
     (77, 256, 256, (2, 256, 1)), (76, 256, 256, (1, 128, 1)),
