@@ -5,6 +5,8 @@
     python -m dense_gemm_06_gb300.profile_case --case f16skinny --reps 3
     python -m dense_gemm_06_gb300.profile_case --case f16small --reps 3
     python -m dense_gemm_06_gb300.profile_case --case every
+    python -m dense_gemm_06_gb300.profile_case --case grouped --reps 3   (or grouped_decode,
+                                                                    grouped_k, lora, lora_decode)
     python -m dense_gemm_06_gb300.profile_case --case bf16 --vendor --reps 2
     python -m dense_gemm_06_gb300.profile_case --case f16skinny --dtype 3 --bm 0 --vendor --reps 2
 
@@ -112,6 +114,62 @@ def run_every():
     lg.check(lg.gemm_check_device_error(), "device error word")
 
 
+# groups, rows, N, K of the ragged products (lora: adapters, rows, N, K; rank 32)
+RAGGED = {"grouped": (16, 12288, 2816, 2048), "grouped_decode": (64, 512, 1536, 2048),
+          "grouped_k": (16, 12288, 2048, 2816), "lora": (32, 4096, 4096, 4096),
+          "lora_decode": (32, 48, 4096, 4096)}
+
+
+def run_ragged(case, reps):
+    """One ragged product, bf16 (grouped_k: fp32 results), uneven groups."""
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+
+    G, M, N, K = RAGGED[case]
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+    if case.startswith("lora"):
+        run = M // G if M >= G * 16 else 1
+        ids = ((torch.arange(M, device="cuda") // run) % G).int()
+        x, w, la, lb = normal(M, K), normal(N, K), normal(G, 32, K), normal(G, 32, N)
+        C = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        flops = 2 * M * N * K + 2 * M * 32 * (N + K)
+
+        def call():
+            return lg.gemm_lora(M, N, K, G, 32, x, K, w, K, lg.GEMM_MAJOR_K, ids, la, lb, None, C,
+                                N, lg.GEMM_BF16_BF16)
+    else:
+        cuts = torch.linspace(0, 1, G + 1, device="cuda") ** 1.5  # sizes grow along the groups
+        off = (cuts * M).round().int()
+        flops = 2 * M * N * K
+        if case == "grouped_k":
+            x, y = normal(M, K), normal(M, N)
+            C = torch.empty(G, K, N, device="cuda")
+
+            def call():
+                return lg.gemm_grouped_k(G, K, N, M, off, x, K, y, N, C, N, K * N,
+                                         lg.GEMM_BF16_F32)
+        else:
+            x, w = normal(M, K), normal(G, N, K)
+            C = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+
+            def call():
+                return lg.gemm_grouped(G, M, N, K, off, x, K, w, K, N * K, lg.GEMM_MAJOR_K, C, N,
+                                       lg.GEMM_BF16_BF16)
+    for r in range(reps):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        lg.check(call(), case)
+        e1.record()
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1)
+        print(f"{case} rep {r}: {ms:.4f} ms, {flops / (ms * 1e-3) / 1e12:.1f} TFLOP/s")
+    lg.check(lg.gemm_check_device_error(), "device error words")
+
+
 def main(argv=None):
     import torch
 
@@ -122,6 +180,14 @@ def main(argv=None):
         argv = sys.argv[1:]
     if "--case" in argv and argv[argv.index("--case") + 1:argv.index("--case") + 2] == ["every"]:
         run_every()
+        return
+    if "--case" in argv and argv[argv.index("--case") + 1:][:1] and \
+            argv[argv.index("--case") + 1] in RAGGED:
+        ap = argparse.ArgumentParser()
+        ap.add_argument("--case", choices=sorted(RAGGED))
+        ap.add_argument("--reps", type=int, default=3)
+        a = ap.parse_args(argv)
+        run_ragged(a.case, a.reps)
         return
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", choices=sorted(CASES) + ["every"], required=True)
