@@ -16,6 +16,7 @@
 #pragma once
 
 #include "gemm_tc.cuh"
+#include "ptx_ragged.cuh"
 
 namespace libgemm {
 
@@ -336,6 +337,16 @@ struct Units<1, kRagShrink> {
         return true;
     }
 };
+
+// Bounded waits as in gemm_tc.cuh, for this kernel's parameters.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const RaggedParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, p.err, p.gen, p.wait_limit_ns);
+}
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity,
+                                              const RaggedParams& p) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, p));
+}
 
 // A unit passed through shared memory (a shared::cluster address), 48 bytes per
 // slot.

@@ -149,9 +149,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, ErrWord* e
     }
 }
 
-// P: a kernel's parameter block (err, gen, wait_limit_ns).
-template <typename P>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const P& p) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const TcParams& p) {
     if (mbar_try_wait(bar, parity)) return true;
     return wait_slow(bar, parity, p.err, p.gen, p.wait_limit_ns);
 }
@@ -170,8 +168,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Bounded wait taken by every lane of a warp; the outcome is warp-uniform.
-template <typename P>
-__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const P& p) {
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const TcParams& p) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, p));
 }
 
