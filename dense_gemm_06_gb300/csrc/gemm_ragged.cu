@@ -108,7 +108,8 @@ struct RepackJobs {
 
 // Copies operands whose rows TMA cannot read into 16-byte aligned rows, matrix
 // after matrix, their padding zero; a warp per row, all operands in one launch.
-__global__ void __launch_bounds__(256) repack16_mats_kernel(const __grid_constant__ RepackJobs jobs) {
+__global__ void __launch_bounds__(256)
+    repack16_mats_kernel(const __grid_constant__ RepackJobs jobs) {
     gemm_ptx::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
@@ -129,14 +130,15 @@ __global__ void __launch_bounds__(256) repack16_mats_kernel(const __grid_constan
 // group's last row, so that TMA fills its last block with zeros; the order of
 // the groups, the longest first (for up to kMaxSorted groups: each warp ranks
 // its group among all), so that the units handed out last are short ones; and
-// the count of units taken. A warp per group. (Zeroing the block in shared memory instead put a hand-over of 1-2 us
-// between the copy and the MMA of every unit: 64 groups of 769 rows took
-// 536 us that way, 389 this way, 64 of 768, which need no zeros, 351.)
+// the count of units taken. A warp per group. (Zeroing the block in shared
+// memory instead put a hand-over of 1-2 us between the copy and the MMA of every
+// unit: 64 groups of 769 rows took 536 us that way, 389 this way, 64 of 768,
+// which need no zeros, 351.)
 constexpr int kMapWarps = 4, kMaxSorted = 4096;
 __global__ void __launch_bounds__(32 * kMapWarps)
-    depth_maps_kernel(const __grid_constant__ CUtensorMap pm, const __grid_constant__ CUtensorMap qm,
-                      const int32_t* offsets, int G, int depth, CUtensorMap* out, int32_t* order,
-                      unsigned int* ticket) {
+    depth_maps_kernel(const __grid_constant__ CUtensorMap pm,
+                      const __grid_constant__ CUtensorMap qm, const int32_t* offsets, int G,
+                      int depth, CUtensorMap* out, int32_t* order, unsigned int* ticket) {
     gemm_ptx::pdl_launch_dependents();
     __shared__ __align__(128) uint32_t maps[kMapWarps][2][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -609,12 +611,13 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     }
     scratch.release();
     if (rc == kOk)
-        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d blocks of dot products or "
-                     "%d lanes x %d rows, %d chains, split %d; "
-                     "expand %s, units of %d rows, split %d",
+        dispatch_log("lora %lldx%lldx%lld, %lld adapters of rank %lld: shrink %d blocks of dot "
+                     "products or %d lanes x %d rows, %d chains, split %d; expand %s, units of "
+                     "%d rows, split %d",
                      (long long)M, (long long)N, (long long)K, (long long)L, (long long)R,
-                     shape.rows_blocks, shape.lanes, shape.shrink_w, shape.chains, shape.shrink_split,
-                     ex.cta_group == 2 ? "CTA pairs" : "one CTA per unit", W, ex.split);
+                     shape.rows_blocks, shape.lanes, shape.shrink_w, shape.chains,
+                     shape.shrink_split, ex.cta_group == 2 ? "CTA pairs" : "one CTA per unit", W,
+                     ex.split);
     return rc;
 }
 

@@ -180,10 +180,12 @@ __device__ __forceinline__ int round_width(int rows, int step, int most) {
 // warp takes part: a lane holds the limits of four consecutive groups, a scan
 // gives the units before each lane, and 128 groups are searched at a time.
 // Units are asked for in increasing order, so later chunks replace earlier
-// ones. Limits out of [0, M] are clamped and a decreasing pair is an empty
-// group, so no row outside A and C is ever addressed.
+// ones. Limits are clamped to [0, M] and to the largest before them, so that
+// whatever they hold, the groups do not overlap, no row outside A and C is ever
+// addressed and there are no more units than the launch was sized for.
 struct RowWalk {
     int g0, base, total, incl;
+    int top;  // the largest limit before the chunk
     int off[5];
 
     __device__ __forceinline__ int units(const RaggedParams& p, int i) const {
@@ -199,6 +201,17 @@ struct RowWalk {
             const int g = min(g0 + lane * 4 + i, p.G);
             off[i] = clampi(__ldcg(p.offsets + g), 0, p.rows);
         }
+        int most = max(max(off[0], off[1]), max(off[2], off[3]));
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, most, d);
+            if (lane >= d) most = max(most, o);
+        }
+        int before = __shfl_up_sync(0xffffffffu, most, 1);
+        before = lane > 0 ? max(before, top) : top;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) before = off[i] = max(off[i], before);
+        top = __shfl_sync(0xffffffffu, off[4], 31);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine += units(p, i);
@@ -211,7 +224,7 @@ struct RowWalk {
         total = __shfl_sync(0xffffffffu, incl, 31);
     }
     __device__ __forceinline__ void start(const RaggedParams& p) {
-        g0 = base = 0;
+        g0 = base = top = 0;
         load(p);
     }
     template <int CG>
@@ -595,7 +608,8 @@ __device__ __forceinline__ bool scan_lb(const RaggedParams& p, const int* list, 
 // flag each.
 constexpr int kRowsThreads = 256, ROW_RANKS = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(kRowsThreads) lora_rows_kernel(const __grid_constant__ RaggedParams p) {
+__global__ void __launch_bounds__(kRowsThreads)
+    lora_rows_kernel(const __grid_constant__ RaggedParams p) {
     using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr int WARPS = kRowsThreads / 32;
     __shared__ __align__(16) int ids[256], slots[256], list[256], sums[16];
@@ -706,7 +720,8 @@ __global__ void __launch_bounds__(kRowsThreads) lora_rows_kernel(const __grid_co
 // for code that it does not run (511 us against 477 us, 64 weight gradients of
 // 2816 x 2048).
 template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, bool EPI>
-__global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_constant__ RaggedParams p) {
+__global__ void __launch_bounds__(RTHREADS, 1)
+    ragged_kernel(const __grid_constant__ RaggedParams p) {
     constexpr bool NARROW = MODE == kRagShrink && P_MN;
     constexpr bool PF_MN = P_MN && MODE != kRagShrink;  // P's features are contiguous
     using C_ = RCfg<NARROW>;
@@ -1030,11 +1045,13 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                                                 ((kb - first) | j) != 0 ? 1u : 0u);
                                 if (NARROW && kb + 1 < last) {  // the stage's second block
 #pragma unroll
-                                    for (int j = 0; j < BK / UMMA_K; ++j)
+                                    for (int j = 0; j < BK / UMMA_K; ++j) {
+                                        constexpr int at = C_::BLOCK_BYTES;
                                         mma_f16<CG>(d_tmem,
-                                                    pd + (uint64_t)((C_::BLOCK_BYTES + j * P_STEP) >> 4),
-                                                    qd + (uint64_t)((C_::BLOCK_BYTES + j * Q_STEP) >> 4),
+                                                    pd + (uint64_t)((at + j * P_STEP) >> 4),
+                                                    qd + (uint64_t)((at + j * Q_STEP) >> 4),
                                                     idesc, 1u);
+                                    }
                                 }
                             } else {
                                 for (int j = 0; j * UMMA_K < left; ++j)
@@ -1241,7 +1258,8 @@ __global__ void __launch_bounds__(RTHREADS, 1) ragged_kernel(const __grid_consta
                 if constexpr (std::is_same_v<OutT, float>) {
                     if (accumulates) {
                         // C += alpha * sum, added in L2: nothing to wait for (each
-                        // element gets one addition, so its order is no question)
+                        // element gets one addition, so its order is no question).
+                        // That addition takes numbers below 2^-126 as zero.
                         if (!f_ok) return;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {

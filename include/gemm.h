@@ -278,11 +278,12 @@ int softmax_rows(int64_t M, int64_t N, const float *x, int64_t ldx, float *y, in
  * [0, M], 4-byte aligned; it is read by the kernel, never by the host, so the
  * sizes may come from an earlier kernel of the stream and the call can be
  * captured into a graph. Empty groups are allowed; rows of C outside
- * [offsets[0], offsets[G]) are not written. Limits outside [0, M] are clamped
- * and a decreasing pair counts as an empty group (no row outside A and C is
- * ever touched); gemm_check_device_error() then reports
+ * [offsets[0], offsets[G]) are not written. Limits outside [0, M] are clamped,
+ * one below an earlier one counts as that one (no row outside A and C is ever
+ * touched, none belongs to two groups); gemm_check_device_error() then reports
  * GEMM_ERR_INVALID_ARG. M is the upper bound of the rows: the launch is sized
- * by it.
+ * by it. Of the options, GEMM_OPT_WAIT_LIMIT_NS and the timeout test hook
+ * GEMM_OPT_TC_FAULT_INJECT apply.
  *
  * Types: the 16-bit dtypes (GEMM_F32 is GEMM_ERR_UNSUPPORTED). Accumulation
  * is fp32, C is rounded once, and the sums do not depend on timing. epi as in
@@ -308,8 +309,10 @@ int gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offs
  * C holds G matrices of M x N, stridec elements apart (for G > 1 at least one
  * matrix's span), row-major (ldc >= N). An empty group's sums are zero (its
  * C_g is written). `offsets` as in gemm_grouped, within [0, K]. Values of
- * other groups' rows never reach a sum, infinities and NaN included. With
- * beta = 1 the call accumulates into C. Types, epilogue (bias: G x N),
+ * other groups' rows never reach a sum, infinities and NaN included (of wrong
+ * limits each pair is clamped by itself, a decreasing one empty). With beta = 1
+ * the call accumulates into C (an fp32 one through global additions, which
+ * take numbers below 2^-126 as zero). It takes 260 bytes of scratch per group. Types, epilogue (bias: G x N),
  * repacking, degenerate sizes and status codes as gemm_grouped.
  */
 int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets,

@@ -189,8 +189,28 @@ def test_bad_limits_are_clamped_and_reported(offsets, errors, call):
         hi = min(max(offsets[g + 1], lo), M)
         if call == "depth":
             assert_exact(got[g], A[lo:hi].double().T @ X[lo:hi].double())
-        elif hi > lo and not (offsets[1] > offsets[2]):
+        else:  # never below an earlier limit
+            lo, hi = (min(max(max(offsets[:i + 1]), 0), M) for i in (g, g + 1))
             assert_exact(got[0][lo:hi], A[lo:hi].double() @ B[g].double().T)
+
+
+def test_many_wrong_limits():
+    """Limits that go up and down over several chunks of groups."""
+    G, M, N, K = 700, 300, 64, 64
+    limits = [(g * 97) % 331 - 15 for g in range(G + 1)]
+    off = torch.tensor(limits, dtype=torch.int32, device="cuda")
+    A, B = rand((M, K), torch.bfloat16, 1), rand((G, N, K), torch.bfloat16, 2)
+    C = Result(1, M, N, torch.bfloat16)
+    lg.check(lg.gemm_grouped(G, M, N, K, off, A, K, B, K, N * K, 0, C.ptr, N, BF))
+    assert lg.gemm_check_device_error() == lg.GEMM_ERR_INVALID_ARG
+    got, top = C.read()[0], 0
+    first = min(max(limits[0], 0), M)
+    for g in range(G):
+        lo = min(max(top, limits[g], 0), M)
+        top = max(top, limits[g])
+        hi = min(max(top, limits[g + 1], 0), M)
+        assert_exact(got[lo:hi], A[lo:hi].double() @ B[g].double().T)
+    assert bool((got[:first] == ru.CANARY).all())
 
 
 def ref_depth(A, B, ends):
