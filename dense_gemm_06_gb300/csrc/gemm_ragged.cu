@@ -41,7 +41,7 @@
 //   * T is carried as two 16-bit numbers, hi = rn(t) and lo = rn(t - hi), both
 //     multiplied: one 16-bit T would add a rounding of the adapter's part as
 //     large as C's own, two leave 2^-17 (bf16) or 2^-22 (fp16) of it.
-//   * Up to 64 rows the shrink is plain dot products (kRagShrinkRows).
+//   * For few rows the shrink is plain dot products (kRagShrinkRows).
 //   * A zero of T against an infinite or NaN LB of another row's adapter would
 //     be NaN. The shrink scans the listed LBs (bringing them into L2 for the
 //     expand); a tile with such an adapter adds the adapters' part per row in
