@@ -227,14 +227,18 @@ struct RaggedShape {
     int split;
 };
 
-// Largest power of two <= 8 that keeps units * split within the SMs and eight
-// k-blocks for each CTA of the cluster. Measured against no split: one row of
-// 4096 x 4096 9.0 us and 17.7 us, 4 groups of 2 rows of 512 x 7168 17.0 and 28.0,
-// 100 rows of 2048 x 4096 20.3 and 22.7; with four k-blocks each, 2 groups of 30
-// rows of 1024 x 2048 took 13.5 and 11.9.
+// Largest power of two <= 8 that keeps units * split within the SMs (half of them
+// for clusters of 8: a GPC holds few of those, and 16 no longer run at once) and
+// six k-blocks for each CTA of the cluster. Measured, with and without a split:
+// one row of 4096 x 4096 9.0 us and 17.7 us, 4 groups of 2 rows of 512 x 7168
+// 11.7 and 28.0, 2 of 30 rows of 1024 x 2048 7.9 and 11.9. Clusters of 8 and of
+// 4: 20 rows of 1024 x 4096 (8 units) 7.8 and 9.4, 8 groups of one row of 256 x
+// 4096 (16 units) 14.5 and 9.2.
 inline int plan_ragged_split(int64_t units, int64_t num_kb, int sm_count) {
     int s = 1;
-    while (s < 8 && units * (2 * s) <= sm_count && num_kb >= 8 * (2 * s)) s *= 2;
+    while (s < 8 && units * (2 * s) <= (s == 4 ? sm_count / 2 : sm_count) &&
+           num_kb >= 6 * (2 * s))
+        s *= 2;
     return s;
 }
 
@@ -310,7 +314,8 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
     const int64_t parts = (listed * slot + s.lanes - 1) / s.lanes;
     const int64_t tiles = (M + s.shrink_w - 1) / s.shrink_w;
     s.shrink_split = plan_ragged_split(tiles, num_kb, sm_count);
-    const int64_t chains = sm_count / (tiles * s.shrink_split);
+    const int64_t room = s.shrink_split == 8 ? sm_count / 2 : sm_count;  // as for a split
+    const int64_t chains = room / (tiles * s.shrink_split);
     s.chains = (int)(chains < 1 ? 1 : (chains > parts ? parts : chains));
     if (M <= 128 && M * slot <= 4096) {
         s.rows_blocks = (int)(M * (slot / 4));
