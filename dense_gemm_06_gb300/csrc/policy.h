@@ -314,8 +314,7 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
     const int64_t parts = (listed * slot + s.lanes - 1) / s.lanes;
     const int64_t tiles = (M + s.shrink_w - 1) / s.shrink_w;
     s.shrink_split = plan_ragged_split(tiles, num_kb, sm_count);
-    const int64_t room = s.shrink_split == 8 ? sm_count / 2 : sm_count;  // as for a split
-    const int64_t chains = room / (tiles * s.shrink_split);
+    const int64_t chains = sm_count / (tiles * s.shrink_split);
     s.chains = (int)(chains < 1 ? 1 : (chains > parts ? parts : chains));
     if (M <= 128 && M * slot <= 4096) {
         s.rows_blocks = (int)(M * (slot / 4));

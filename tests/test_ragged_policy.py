@@ -71,11 +71,11 @@ def test_grouped_k_shape(probe, G, M, N, want):
     # cta_group tile_w split | rows_blocks scan_blocks | lanes shrink_w split chains
     (1, 4096, 64, 1, 16, (1, 16, 4, 4, 16, 64, 16, 8, 1)),
     (48, 4096, 64, 32, 16, (1, 64, 4, 192, 64, 64, 64, 8, 8)),
-    (64, 4096, 64, 64, 64, (1, 64, 4, 1024, 64, 128, 64, 8, 9)),
+    (64, 4096, 64, 64, 64, (1, 64, 4, 1024, 64, 128, 64, 8, 19)),
     (128, 4096, 64, 64, 32, (1, 128, 4, 1024, 64, 64, 64, 8, 9)),
     # more rows or ranks than the dot products take: the tensor cores' shrink
     (129, 4096, 64, 4, 16, (1, 64, 1, 0, 0, 64, 64, 8, 1)),
-    (64, 4096, 64, 64, 128, (1, 64, 4, 0, 0, 128, 64, 8, 9)),
+    (64, 4096, 64, 64, 128, (1, 64, 4, 0, 0, 128, 64, 8, 19)),
     (100, 4096, 64, 4, 64, (1, 128, 4, 0, 0, 128, 128, 8, 2)),
     # five tiles of 128 by 15 would leave half the SMs idle: tiles of 64
     (611, 1804, 25, 16, 32, (1, 64, 1, 0, 0, 64, 64, 4, 3)),
