@@ -5,7 +5,7 @@
 // What bounds it (see gemm_ragged.cu for the cases): few rows per group, HBM --
 // the weights stream through the ring once (1024 rows in 128 groups of 1536 x
 // 2048: 119 us, 6.5 TB/s); many, the tensor pipe and its feed from L2 (one group
-// of 8192^3: 556 us, 1.98 PFLOP/s, gemm() 548 us on the same box); the smallest
+// of 8192^3: 556 us, 1.98 PFLOP/s, gemm() 548 us on the same GPU); the smallest
 // calls, the chain of latencies from launch to last store (one row against 4096 x
 // 4096 with an adapter: 12 us, of which the weights take 5).
 //

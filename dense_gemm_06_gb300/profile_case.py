@@ -111,6 +111,17 @@ def run_every():
         y = torch.empty_like(x)
         lg.check(lg.softmax_rows(M, N, x, N, y, N), "softmax_rows")
         print(f"every: softmax_rows {M} x {N}", flush=True)
+    from dense_gemm_06_gb300 import experts_demo
+    for tokens, rank, what in ((37, 16, "dot products"), (300, 16, "narrow"), (300, 64, "wide")):
+        experts_demo.step(experts_demo.make(tokens, 8, 256, 384, 3, rank), 2)
+        print(f"every: experts and adapters, {tokens} rows, rank {rank} (shrink: {what})", flush=True)
+    off = torch.tensor([0, 40, 100], dtype=torch.int32, device="cuda")
+    A = torch.randn(100, 133, device="cuda").half()
+    W = torch.randn(2, 65, 133, device="cuda").half()
+    Y = torch.empty(100, 65, device="cuda")
+    lg.check(lg.gemm_grouped(2, 100, 65, 133, off, A, 133, W, 133, 65 * 133, 0, Y, 65,
+                             lg.GEMM_F16_F32), "gemm_grouped")
+    print("every: gemm_grouped with its repack, misaligned fp16", flush=True)
     lg.check(lg.gemm_check_device_error(), "device error word")
 
 

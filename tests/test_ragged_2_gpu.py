@@ -263,6 +263,19 @@ def test_depth_pitches_and_bases(pads, shifts):
     assert_exact(C, ref_depth(A, B, ends))
 
 
+@pytest.mark.parametrize("gap", [64, 13])
+@pytest.mark.parametrize("dtype", [BF, lg.GEMM_F16_F32])
+def test_depth_results_further_apart_than_they_span(gap, dtype):
+    sizes, M, N = [40, 0, 3, 300], 136, 264
+    ends, off = offsets_of(sizes)
+    A, B = rand((343, M), IN[dtype], 1), rand((343, N), IN[dtype], 2)
+    C = torch.full((4, M * N + gap), ru.CANARY, dtype=OUT[dtype], device="cuda")
+    lg.check(lg.gemm_grouped_k(4, M, N, 343, off, A, M, B, N, C, N, M * N + gap, dtype))
+    check()
+    assert_exact(C[:, :M * N].reshape(4, M, N), ref_depth(A, B, ends))
+    assert bool((C[:, M * N:] == ru.CANARY).all())
+
+
 @pytest.mark.parametrize("M,N", [(136, 200), (1032, 1288)])
 def test_depth_other_groups_values_never_meet(M, N):
     sizes = [17, 0, 30, 1, 70, 64, 5]
