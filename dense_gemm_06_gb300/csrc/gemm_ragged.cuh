@@ -16,6 +16,7 @@
 #pragma once
 
 #include "gemm_tc.cuh"
+#include "policy.h"
 #include "ptx_ragged.cuh"
 
 namespace libgemm {
@@ -172,10 +173,6 @@ struct RUnit {
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-__device__ __forceinline__ int round_width(int rows, int step, int most) {
-    return min(most, (rows + step - 1) / step * step);
-}
-
 // rows mode: finds the group, row tile and feature tile of unit u. The whole
 // warp takes part: a lane holds the limits of four consecutive groups, a scan
 // gives the units before each lane, and 128 groups are searched at a time.
@@ -191,14 +188,13 @@ struct RowWalk {
     __device__ __forceinline__ int units(const RaggedParams& p, int i) const {
         const int lane = threadIdx.x & 31;
         const int rows = off[i + 1] - off[i];
-        return g0 + lane * 4 + i < p.G && rows > 0
-                   ? (rows + p.tile_w - 1) / p.tile_w * p.tiles_f : 0;
+        return lane * 4 + i < p.G - g0 && rows > 0 ? ragged_units(rows, p.tile_w) * p.tiles_f : 0;
     }
     __device__ __forceinline__ void load(const RaggedParams& p) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
-            const int g = min(g0 + lane * 4 + i, p.G);
+            const int g = g0 + min(lane * 4 + i, p.G - g0);
             off[i] = clampi(__ldcg(p.offsets + g), 0, p.rows);
         }
         int most = max(max(off[0], off[1]), max(off[2], off[3]));
@@ -230,7 +226,7 @@ struct RowWalk {
     template <int CG>
     __device__ __forceinline__ bool find(const RaggedParams& p, int u, RUnit& un) {
         while (u >= base + total) {
-            if (g0 + 128 >= p.G) return false;
+            if (p.G - g0 <= 128) return false;
             base += total;
             g0 += 128;
             load(p);
@@ -256,11 +252,11 @@ struct RowWalk {
         rem = __shfl_sync(0xffffffffu, rem, who);
         lo = __shfl_sync(0xffffffffu, lo, who);
         hi = __shfl_sync(0xffffffffu, hi, who);
-        const TileCoord tc = raster(rem, (hi - lo + p.tile_w - 1) / p.tile_w, p.tiles_f);
+        const TileCoord tc = raster(rem, ragged_units(hi - lo, p.tile_w), p.tiles_f);
         un.row0 = lo + tc.tm * p.tile_w;
         un.row_end = hi;
         un.feat0 = tc.tn * 128 * CG;
-        un.width = round_width(hi - un.row0, 16 * CG, p.tile_w);
+        un.width = ragged_width(hi - un.row0, 16 * CG, p.tile_w);
         un.k0 = 0;
         un.k_end = 0;
         un.nkb = p.num_kb;
@@ -304,10 +300,10 @@ struct Units {
             un.row0 = tc.tm * p.tile_w;
             un.row_end = p.rows;
             un.feat0 = tc.tn * 128 * CG;
-            un.width = round_width(p.rows - un.row0, 64 * CG, p.tile_w);
+            un.width = ragged_width(p.rows - un.row0, 64 * CG, p.tile_w);
             un.k0 = clampi(__ldcg(p.offsets + un.g), 0, p.depth);
             un.k_end = clampi(__ldcg(p.offsets + un.g + 1), un.k0, p.depth);
-            un.nkb = (un.k_end - un.k0 + BK - 1) / BK;
+            un.nkb = ragged_blocks(un.k0, un.k_end);
             un.tile = 0;
             return true;
         } else if constexpr (MODE == kRagLora) {
@@ -318,7 +314,7 @@ struct Units {
             un.row0 = tc.tm * p.tile_w;
             un.row_end = p.rows;
             un.feat0 = tc.tn * 128 * CG;
-            un.width = round_width(p.rows - un.row0, 16 * CG, p.tile_w);
+            un.width = ragged_width(p.rows - un.row0, 16 * CG, p.tile_w);
             un.k0 = un.k_end = 0;
             un.nkb = p.num_kb;
             return true;
@@ -343,7 +339,7 @@ struct Units<1, kRagShrink> {
         un.row0 = tile * p.tile_w;
         un.row_end = p.rows;
         un.feat0 = 0;
-        un.width = round_width(p.rows - un.row0, 16, p.tile_w);
+        un.width = ragged_width(p.rows - un.row0, 16, p.tile_w);
         un.k0 = un.k_end = 0;
         un.nkb = p.num_kb;
         un.tile = un.row0 / p.list_w;
@@ -1296,7 +1292,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                     }
                 }
                 if constexpr (BY_TMA) {
-                    if (p.c_tma && left >= 32 && f - lane + 32 <= p.feats) {
+                    if (p.c_tma && left >= 32 && p.feats - (f - lane) >= 32) {
                         // A whole chunk goes through one of the warp's two staging
                         // tiles, written while TMA still reads the other.
                         const uint32_t tile = tiles + (uint32_t)(tile_i * C_::TILE_BYTES);
@@ -1509,7 +1505,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             if (blockIdx.x == 0) {
                 const int most = MODE == kRagRows ? p.rows : p.depth;
                 bool bad = false;
-                for (int g = lane; g < p.G; g += 32) {
+                for (unsigned g = lane; g < (unsigned)p.G; g += 32) {
                     const int a = __ldcg(p.offsets + g), b = __ldcg(p.offsets + g + 1);
                     bad |= a < 0 || b > most || b < a;
                 }

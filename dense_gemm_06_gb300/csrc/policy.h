@@ -9,6 +9,12 @@
 #include <cstdint>
 #include <numeric>
 
+#ifdef __CUDACC__
+#define LIBGEMM_BOTH __host__ __device__ __forceinline__
+#else
+#define LIBGEMM_BOTH inline
+#endif
+
 namespace libgemm {
 
 // K-split of the FFMA kernel's tail. Tiles 0 .. dp_tiles-1 (raster order) run
@@ -226,6 +232,21 @@ struct RaggedShape {
     int tile_w;
     int split;
 };
+
+// The kernels' round-ups, in unsigned numbers: a group may have up to 2^31 - 1
+// rows, whose round-up no longer fits an int. Units of a group of `rows` rows;
+// rows that a unit spans when `rows` of its group are left; 64-deep blocks of
+// the summed rows [k0, k_end).
+LIBGEMM_BOTH int ragged_units(int rows, int tile_w) {
+    return (int)(((unsigned)rows + (unsigned)tile_w - 1u) / (unsigned)tile_w);
+}
+LIBGEMM_BOTH int ragged_width(int rows, int step, int most) {
+    const unsigned up = ((unsigned)rows + (unsigned)step - 1u) / (unsigned)step * (unsigned)step;
+    return (int)(up < (unsigned)most ? up : (unsigned)most);
+}
+LIBGEMM_BOTH int ragged_blocks(int k0, int k_end) {
+    return (int)(((unsigned)(k_end - k0) + 63u) / 64u);
+}
 
 // Largest power of two <= 8 that keeps units * split within the SMs (half of them
 // for clusters of 8: a GPC holds few of those, and 16 no longer run at once) and
