@@ -300,6 +300,7 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
         if (!A || !B || !aligned_to(A, 2) || !aligned_to(B, 2)) return kInvalidArg;
         if (lda < a.inner || ldb < b.inner) return kInvalidArg;
         if (!span_fits(1, 0, a.outer, a.inner, lda, 2)) return kInvalidArg;
+        if (!span_fits(1, 0, b.outer, b.inner, ldb, 2)) return kInvalidArg;  // so the next sum fits
         if (G > 1 && strideb < (b.outer - 1) * ldb + b.inner) return kInvalidArg;
         if (!span_fits(G, strideb, b.outer, b.inner, ldb, 2)) return kInvalidArg;
     }

@@ -44,6 +44,21 @@ def test_round_ups(probe, rows):
         assert probe("blocks", k0, rows) == -(-(rows - k0) // 64)
 
 
+@pytest.mark.parametrize("ld", [1 << 60, 3 << 60, 1 << 61, 1 << 62, (1 << 63) - 1])
+@pytest.mark.parametrize("stride", [128, 1 << 60, (1 << 63) - 1])
+def test_matrices_whose_span_passes_64_bits_are_refused(ld, stride):
+    import dense_gemm_06_gb300 as lg
+    from dense_gemm_06_gb300 import _build
+    _build.build()
+    p = 0x10000  # a fake, aligned address: the checks never dereference
+    bf = lg.GEMM_BF16_BF16
+    for major in (lg.GEMM_MAJOR_K, lg.GEMM_MAJOR_MN):
+        assert lg.gemm_grouped(3, 10, 8, 16, p, p, 16, p, ld, stride, major, p, 8, bf,
+                               stream=0) == lg.GEMM_ERR_INVALID_ARG
+    assert lg.gemm_grouped_k(3, 10, 8, 16, p, p, 10, p, 8, p, ld, stride, bf,
+                             stream=0) == lg.GEMM_ERR_INVALID_ARG
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("groups", [1, 2])
 def test_rows_up_to_the_last(groups):
