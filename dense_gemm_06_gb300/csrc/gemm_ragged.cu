@@ -40,7 +40,9 @@
 //     any adapter order share the tile.
 //   * T is carried as two 16-bit numbers, hi = rn(t) and lo = rn(t - hi), both
 //     multiplied: one 16-bit T would add a rounding of the adapter's part as
-//     large as C's own, two leave 2^-17 (bf16) or 2^-22 (fp16) of it.
+//     large as C's own, two leave 2^-17 (bf16) or 2^-22 (fp16) of it; small T in
+//     fp16, where the second runs out of exponents, takes two more (see T_SMALL
+//     in gemm_ragged.cuh).
 //   * For few rows the shrink is plain dot products (kRagShrinkRows).
 //   * A zero of T against an infinite or NaN LB of another row's adapter would
 //     be NaN. The shrink scans the listed LBs (bringing them into L2 for the
@@ -511,10 +513,11 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
     const RaggedShape& ex = shape.expand;
     const int W = ex.tile_w;
     const int64_t list_n = L < (M < W ? M : W) ? L : (M < W ? M : W);
-    const int64_t ldt = up(list_n * slot, EXT_K) * 2;
+    const int64_t ldt =
+        up(list_n * slot, EXT_K) / EXT_K * (bf16 ? T_BLOCK<__nv_bfloat16> : T_BLOCK<__half>);
     const int subs = W / shape.shrink_w;
     const int flags = shape.rows_blocks > 0
-                          ? shape.scan_blocks
+                          ? shape.scan_blocks + (bf16 ? 0 : shape.rows_blocks)
                           : subs * shape.chains * shape.shrink_split * EPI_WARPS;
     const int list_pitch = 1 + 2 * W + flags;
 

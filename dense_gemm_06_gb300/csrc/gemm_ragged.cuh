@@ -76,8 +76,8 @@ struct RaggedParams {
     int chains;              // shrink: clusters that share a row tile's lists of lanes
                              // (kRagShrinkRows: blocks of dot products)
     int32_t* lists;          // per list tile: n, list_w adapter numbers, list_w slots, flags
-    int list_pitch, flags;
-    void* T;                 // hi | lo halves of T, 64 elements per 32 lanes
+    int list_pitch, flags;   // flags: of a list, one per warp (block) that looked
+    void* T;                 // halves of T: 64 elements per 32 lanes, fp16: 128
     int64_t ldt;
     int pdl;                 // host only
     ErrWord* err;
@@ -158,6 +158,24 @@ constexpr int RTHREADS = 32 * (REPI_WARP0 + EPI_WARPS);
 // 512, 768 or 1024 take the same time (476-483 us, 64 gradients of 2816 x 2048).
 constexpr int FOLD_KB = 11;
 constexpr int EXT_K = 32;  // lanes of T (rows of LB) per extension block: hi | lo fill 64
+// T in fp16. Below 2^-3 its low half runs out of exponents (its last step is
+// 2^-24), so what hi + lo leave of t is kept too, times 2^24 and again as two
+// halves: t = hi + lo + 2^-24 (hi2 + lo2), to 2^-22 of t down to 2^-25 and
+// 2^-49 below. In a tile where some row's neighbouring ranks (a warp's 32, four
+// in the dot products) are all below T_SMALL, the expand sums hi2 and lo2 into
+// the other accumulator and the epilogue joins the two. Elsewhere hi + lo leave
+// 2^-25, at most 2^-19 of the row's largest t nearby: 1/128 of C's own rounding.
+// (bf16 has fp32's exponents: hi + lo do.) Measured, 48 rows and 24 adapters of
+// 4096 x 4096: 16.3 us with hi and lo only, 16.6 us so, 18.1 us where the second
+// accumulator is used; 8192 rows 179, 184 and 205 us. Rank 16, T about 1e-6, LB
+// about 1e3: the adapters' part was off by 1.7e-2 with hi and lo only.
+constexpr float T_SMALL = 0x1p-6f, T_UP = 0x1p24f, T_DOWN = 0x1p-24f;
+// Elements of T per 32 lanes.
+template <typename In>
+constexpr int T_BLOCK = std::is_same_v<In, __half> ? 128 : 64;
+// Bits of a list's flags.
+constexpr int kListNonfinite = 1;  // an infinity or NaN in a listed LB
+constexpr int kListSmallT = 2;     // small T: hi2 and lo2 count
 
 // One unit of work: `width` rows of C from row0 (those before row_end are
 // stored) by 128 features per CTA from feat0.
@@ -454,24 +472,42 @@ __device__ __forceinline__ void sts_as(uint32_t addr, float x) {
                  :: "r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&t)) : "memory");
 }
 
-// t as two 16-bit numbers, 32 elements apart.
+// t as two 16-bit numbers, 32 elements apart; fp16: and what they leave of it
+// as two more.
 template <typename In>
 __device__ __forceinline__ void store_t(In* dst, float t) {
     const In hi = from_f32<In>(t);
     const float d = t - to_f32(hi);  // infinite or NaN where hi is: then hi says it all
+    const In lo = from_f32<In>(isfinite(d) ? d : 0.f);
     dst[0] = hi;
-    dst[32] = from_f32<In>(isfinite(d) ? d : 0.f);
+    dst[32] = lo;
+    if constexpr (std::is_same_v<In, __half>) {
+        // (a large t leaves more than fp16 holds, and needs none of it)
+        const float left = (d - to_f32(lo)) * T_UP, small = fabsf(left) < 1.f ? left : 0.f;
+        const In hi2 = from_f32<In>(small);
+        dst[64] = hi2;
+        dst[96] = from_f32<In>(small - to_f32(hi2));
+    }
+}
+
+// Is the largest of these numbers' magnitudes, given as bits, small but not zero?
+__device__ __forceinline__ bool small_t(uint32_t largest) {
+    return largest != 0u && largest < __float_as_uint(T_SMALL);
 }
 
 // sum_r T[row][r] LB[id][r][f] for a row whose adapter is the s-th of its list
-// (the lanes of `t` are hi | lo halves in blocks of 32); lb points at LB[id][0][f].
+// (the lanes of `t` in blocks of 32, as store_t leaves them); lb points at
+// LB[id][0][f].
 template <typename In>
 __device__ __noinline__ float adapter_part(const In* t, const In* lb, int64_t ldlb, int lane0,
                                            int rank) {
     float v = 0.f;
     for (int r = 0; r < rank; ++r) {
-        const In* tt = t + (lane0 + r) / 32 * 64 + (lane0 + r) % 32;
-        v = fmaf(to_f32(tt[0]) + to_f32(tt[32]), to_f32(lb[r * ldlb]), v);
+        const In* tt = t + (lane0 + r) / 32 * T_BLOCK<In> + (lane0 + r) % 32;
+        float x = to_f32(tt[0]) + to_f32(tt[32]);
+        if constexpr (std::is_same_v<In, __half>)
+            x = fmaf(T_DOWN, to_f32(tt[64]) + to_f32(tt[96]), x);
+        v = fmaf(x, to_f32(lb[r * ldlb]), v);
     }
     return v;
 }
@@ -618,11 +654,12 @@ __global__ void __launch_bounds__(kRowsThreads)
     if ((int)blockIdx.x >= p.chains) {
         const int n = make_list<kRowsThreads>(p, 0, ids, slots, list, sums);
         const int me = (int)blockIdx.x - p.chains;
+        const int scans = (int)gridDim.x - p.chains;
         const bool bad = scan_lb<BF16>(p, list, n, (uint32_t)(me * kRowsThreads + threadIdx.x),
-                                       (uint32_t)(p.flags * kRowsThreads));
+                                       (uint32_t)(scans * kRowsThreads));
         if (__any_sync(0xffffffffu, bad) && lane == 0) any_bad = 1;
         __syncthreads();
-        if (threadIdx.x == 0) p.lists[1 + 2 * p.list_w + me] = any_bad;
+        if (threadIdx.x == 0) p.lists[1 + 2 * p.list_w + me] = any_bad ? kListNonfinite : 0;
         return;
     }
     const int per_row = p.slot / ROW_RANKS;  // blocks per row
@@ -690,6 +727,19 @@ __global__ void __launch_bounds__(kRowsThreads)
         if (threadIdx.x < n) p.lists[1 + threadIdx.x] = list[threadIdx.x];
         if (threadIdx.x < p.list_w) p.lists[1 + p.list_w + threadIdx.x] = slots[threadIdx.x];
     }
+    if (!BF16 && threadIdx.x == 0) {  // this block's flag: behind those of the scan
+        uint32_t largest = 0u;
+#pragma unroll
+        for (int i = 0; i < ROW_RANKS; ++i) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) sum += partial[w][i];
+            if (p.scale && some) sum *= p.scale[a];
+            if (some && r0 + i < p.R) largest = max(largest, __float_as_uint(fabsf(sum)));
+        }
+        p.lists[1 + 2 * p.list_w + (int)gridDim.x - p.chains + (int)blockIdx.x] =
+            small_t(largest) ? kListSmallT : 0;
+    }
     const int s = slots[row];
     In* out = static_cast<In*>(p.T) + (int64_t)row * p.ldt;
     for (int k = threadIdx.x; k < n * ROW_RANKS; k += kRowsThreads) {
@@ -701,7 +751,7 @@ __global__ void __launch_bounds__(kRowsThreads)
             if (p.scale) sum *= p.scale[a];
         }
         const int ll = j * p.slot + r0 + i;
-        store_t<In>(out + ll / 32 * 64 + ll % 32, sum);
+        store_t<In>(out + ll / 32 * T_BLOCK<In> + ll % 32, sum);
     }
 }
 
@@ -723,6 +773,8 @@ __global__ void __launch_bounds__(RTHREADS, 1)
     using C_ = RCfg<NARROW>;
     using In = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr bool Q_MN = MODE == kRagDepth;
+    // T in fp16 may need the second accumulator (see T_SMALL)
+    constexpr bool SMALL_T = MODE == kRagLora && !BF16;
     constexpr bool FOLD = std::is_same_v<OutT, float> && MODE != kRagShrink;
     constexpr int CHUNKS = CG == 2 ? 4 : 2;  // of 32 rows that an epilogue warp stores
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -831,17 +883,24 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         a = (n >> sh) * part + (((n & (S - 1)) * part) >> sh);
         b = (n >> sh) * (part + 1) + (((n & (S - 1)) * (part + 1)) >> sh);
     };
+    // lora: those of n extension blocks that this CTA takes.
+    auto blocks_of = [&](int n) {
+        const int sh = CG == 1 ? p.split : 0;
+        return part < n ? ((n - 1 - part) >> sh) + 1 : 0;
+    };
     // lora: extension blocks of a unit's list tile; 0 when its flags tell the
     // epilogue to add the adapters' part itself. `ids`: its adapters.
     // `id`: this lane's entry of the list, read with the rest (one latency).
-    auto ext_blocks = [&](int tile, int& n, const int32_t*& ids, int& id) {
+    // `two`: whether hi2 and lo2 count (fp16).
+    auto ext_blocks = [&](int tile, int& n, const int32_t*& ids, int& id, bool& two) {
         const int32_t* l = p.lists + (int64_t)tile * p.list_pitch;
         n = __ldcg(l);
         ids = l + 1;
         id = __ldcg(ids + (lane & (p.list_w - 1)));
         int bad = 0;
         for (int i = lane; i < p.flags; i += 32) bad |= __ldcg(l + 1 + 2 * p.list_w + i);
-        if (__any_sync(0xffffffffu, bad != 0)) return 0;
+        two = SMALL_T && __any_sync(0xffffffffu, (bad & kListSmallT) != 0);
+        if (__any_sync(0xffffffffu, (bad & kListNonfinite) != 0)) return 0;
         return (n * p.slot + EXT_K - 1) / EXT_K;
     };
     const int list_arg = MODE == kRagShrink ? n_list : nclusters;
@@ -946,9 +1005,14 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 int n;
                 const int32_t* ids;
                 int lane_id;
-                const int ne = ext_blocks(un.tile, n, ids, lane_id);
-                for (int e = part; e < ne && !aborted; e += S) {
+                bool two;
+                const int ne = ext_blocks(un.tile, n, ids, lane_id, two);
+                // hi and lo of all adapters, then hi2 and lo2
+                const int mine = blocks_of(ne);
+                for (int nth = 0; nth < (two ? 2 * mine : mine) && !aborted; ++nth) {
                     if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
+                    const int e = part + (two && nth >= mine ? nth - mine : nth) * S;
+                    const int x = e * T_BLOCK<In> + (nth < mine ? 0 : 64);  // T's elements
                     const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
                     const uint32_t sp = sP0 + stage * C_::P_BYTES;
                     const uint32_t sq = sQ0 + stage * C_::Q_BYTES;
@@ -972,11 +1036,10 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                                                 &p.map[kMapLB], fb, f0 + 64 * j,
                                                 (e * EXT_K + i * box) % p.slot, i ? id1 : id0);
                         if (un.width == p.tile_w) {
-                            tma_load_2d<CG>(sq, &p.map[kMapT], fb, e * 64, q_row);
+                            tma_load_2d<CG>(sq, &p.map[kMapT], fb, x, q_row);
                         } else {
                             for (int r = 0; r < q_rows; r += 16)
-                                tma_load_2d<CG>(sq + r * 128, &p.map[kMapT16], fb, e * 64,
-                                                q_row + r);
+                                tma_load_2d<CG>(sq + r * 128, &p.map[kMapT16], fb, x, q_row + r);
                         }
                     }
                     __syncwarp();
@@ -1074,8 +1137,17 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                     waited = true;
                     const int32_t* ids;
                     int lane_id;
-                    ne = ext_blocks(un.tile, n, ids, lane_id);
-                    for (int e = part; e < ne && !aborted; e += S) {
+                    bool two;
+                    ne = ext_blocks(un.tile, n, ids, lane_id, two);
+                    const int mine = blocks_of(ne);
+                    for (int nth = 0; nth < (two ? 2 * mine : mine) && !aborted; ++nth) {
+                        const int e = part + (two && nth >= mine ? nth - mine : nth) * S;
+                        if (two && nth == mine) {  // hi2 and lo2 go into the other accumulator
+                            if (elect_one()) mma_commit<CG>(accf_bar(acc));
+                            __syncwarp();
+                            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                            issued = false;
+                        }
                         if (!issued && !wait_bar_warp(acce_bar(acc), acc_phase ^ 1u, p)) {
                             aborted = true;
                             break;
@@ -1143,6 +1215,8 @@ __global__ void __launch_bounds__(RTHREADS, 1)
         if (p.fault_inject == 1) {
             if (!__all_sync(0xffffffffu, wait_bar(never_bar, 0u, p))) aborted = true;
         }
+        int list_flags = 0;       // shrink: what this warp saw, written at its end
+        int32_t* flag = nullptr;
         if constexpr (MODE == kRagShrink) {
             // Does an adapter of the list hold an infinity or a NaN in LB? A
             // zero of T times it would be NaN in the other adapters' rows of the
@@ -1156,13 +1230,10 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                                      (uint32_t)(me * (EPI_WARPS * 32) + threadIdx.x -
                                                 REPI_WARP0 * 32),
                                      (uint32_t)(ctas * (EPI_WARPS * 32)));
-            bad = __any_sync(0xffffffffu, bad);
+            if (__any_sync(0xffffffffu, bad)) list_flags = kListNonfinite;
+            flag = p.lists + (int64_t)(cluster / p.chains / subs) * p.list_pitch + 1 +
+                   2 * p.list_w + me * EPI_WARPS + (warp - REPI_WARP0);
             if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 7);
-            if (lane == 0) {
-                int32_t* flag = p.lists + (int64_t)(cluster / p.chains / subs) * p.list_pitch +
-                                1 + 2 * p.list_w;
-                flag[me * EPI_WARPS + (warp - REPI_WARP0)] = bad ? 1 : 0;
-            }
         }
         Feed units(ready_bar, unit_slots);
         for (bool more = units.peek(p, un); more;) {
@@ -1170,9 +1241,11 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             share(un.nkb, kb0, kb1);
             bool issued = kb1 > kb0;
             const int32_t* ids = nullptr;
+            bool two = false;  // a second accumulator holds the sums of hi2 and lo2
             if constexpr (MODE == kRagLora) {
                 int lane_id;
-                ne = ext_blocks(un.tile, n, ids, lane_id);
+                ne = ext_blocks(un.tile, n, ids, lane_id, two);
+                two = two && part < ne;
                 issued = issued || part < ne;
             }
             const bool by_hand = MODE == kRagLora && n > 0 && ne == 0;
@@ -1203,8 +1276,14 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 my_slot = r_idx < p.R ? slot : -2;
                 row_slot = sm_slots + un.row0 % p.list_w;
                 t_col = static_cast<In*>(p.T) + (int64_t)un.row0 * p.ldt +
-                        (int64_t)(ll / 32) * 64 + lane;
+                        (int64_t)(ll / 32) * T_BLOCK<In> + lane;
             }
+            // shrink, fp16: notes a row of small T (all lanes of the warp).
+            auto note_t = [&](float t) {
+                if (MODE == kRagShrink && !BF16 &&
+                    small_t(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(t)))))
+                    list_flags |= kListSmallT;
+            };
             // lora, by hand: what row j's adapter adds to this lane's feature.
             auto adapters = [&](int j) {
                 const int s = __ldcg(ids + p.list_w + j);
@@ -1218,8 +1297,9 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             // One row j of the unit, value v of this lane (split depths).
             auto emit = [&](int j, float v) {
                 if constexpr (MODE == kRagShrink) {
-                    if (slot < n_list) store_t<In>(t_col + (int64_t)j * p.ldt,
-                                                   row_slot[j] == my_slot ? v * factor : 0.f);
+                    const float t = slot < n_list && row_slot[j] == my_slot ? v * factor : 0.f;
+                    note_t(t);
+                    if (slot < n_list) store_t<In>(t_col + (int64_t)j * p.ldt, t);
                 } else if (f_ok && c_checked(p, un.row0 + j, f)) {
                     if (MODE == kRagLora && by_hand) v += adapters(j);
                     store_c<OutT>(p, c_col + (int64_t)j * p.ldc, v, bias, epi);
@@ -1230,14 +1310,18 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             auto emit_chunk = [&](int c, float (&v)[32]) {
                 const int left = n_rows - c * 32;
                 if constexpr (MODE == kRagShrink) {
-                    if (slot >= n_list) return;
+                    if (BF16 && slot >= n_list) return;
                     In* dst = t_col + (int64_t)(c * 32) * p.ldt;
                     int s[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[i] = row_slot[c * 32 + i];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (i < left) store_t<In>(dst, s[i] == my_slot ? v[i] * factor : 0.f);
+                        const float t = slot < n_list && s[i] == my_slot ? v[i] * factor : 0.f;
+                        if (i < left) {
+                            note_t(t);
+                            if (BF16 || slot < n_list) store_t<In>(dst, t);
+                        }
                         dst += p.ldt;
                     }
                     return;
@@ -1359,8 +1443,14 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             auto read_chunk = [&](int c, uint32_t (&u)[32]) {
                 tmem_ld_32x32b_x32(tlane + (uint32_t)(acc * ACC_COLS + c * 32), u);
             };
+            auto read_second = [&](int c, uint32_t (&u)[32]) {
+                tmem_ld_32x32b_x32(tlane + (uint32_t)((acc ^ 1) * ACC_COLS + c * 32), u);
+            };
             auto wait_acc = [&]() {
                 if (!aborted && !wait_bar_inline(accf_bar(acc), acc_phase, p)) aborted = true;
+                if (SMALL_T && two && !aborted &&
+                    !wait_bar_inline(accf_bar(acc ^ 1), acc_phase ^ (uint32_t)acc, p))
+                    aborted = true;
                 tc_fence_after_sync();
             };
             // Relaxed: the accumulator's reads are complete (wait::ld) and nothing else
@@ -1377,6 +1467,10 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 }
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
                 held = false;
+            };
+            auto free_accs = [&]() {
+                free_acc();
+                if (SMALL_T && two) free_acc();
             };
             // The unit's sums: the parts of a folded depth before the last add up
             // in registers; the last one (or the only one) is read from its
@@ -1435,7 +1529,14 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                        if ((c + 2) * 32 >= un.width) free_acc();
+                        if (SMALL_T && two) {
+                            read_second(c, u);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = fmaf(T_DOWN, __uint_as_float(u[i]), v[i]);
+                        }
+                        if ((c + 2) * 32 >= un.width) free_accs();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -1486,7 +1587,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 split_phase ^= 1u;
                 fence_proxy_async_all();  // the next unit's copies write where the parts were
             }
-            if (held) free_acc();
+            if (held) free_accs();
             if (warp == REPI_WARP0 && lane == 0) TC_TRACE(p, 12);
             if (stamp) TC_TRACE(p, 23 + 4 * nt);
             ++nt;
@@ -1494,6 +1595,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             if (S > 1 && more) cluster_sync_all();
         }
         units.done();
+        if (MODE == kRagShrink && lane == 0) *flag = list_flags;
         if (BY_TMA && p.c_tma && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {

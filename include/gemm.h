@@ -338,8 +338,10 @@ int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *of
  * DEVICE array of L floats, or NULL for ones.
  *
  * Types: GEMM_F16_F16 and GEMM_BF16_BF16 (others: GEMM_ERR_UNSUPPORTED).
- * Sums are fp32; T is carried as two 16-bit numbers (2^-17 of its value in
- * bf16, 2^-22 in fp16, and overflows where fp16 does); C is rounded once.
+ * Sums are fp32; C is rounded once. T is carried as two 16-bit numbers: bf16
+ * leaves 2^-17 of its value. fp16 leaves 2^-22, or 2^-19 of the largest T among
+ * the row's neighbouring ranks where T is small beside that one, or 2^-49; it
+ * overflows where fp16 does (65504).
  * Rows see their own adapter only: an infinity or NaN in another adapter does
  * not reach them. Two launches: the second starts while the first still runs.
  * Misaligned operands (rows of A, B, or K or N no multiple of 8 for the
