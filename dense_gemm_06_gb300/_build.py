@@ -10,8 +10,8 @@ build(checks=True) compiles the debug build with device-side checks
 addresses checked in the kernels, see gemm_device_checks in gemm.h) into
 _build_checks/ and libgemm_checks.so; build(trace=True) the phase-trace
 build of the tensor-core kernel (-DLIBGEMM_TC_TRACE: %globaltimer stamps at
-fixed points of every role, 64 per CTA, into a device buffer registered with
-the extra export libgemm_tc_trace_buffer(void*)) into _build_trace/ and
+fixed points of every role, 64 for each of 1024 CTAs, into a device buffer
+registered with the extra export libgemm_tc_trace_buffer(void*)) into _build_trace/ and
 libgemm_trace.so. The default build has neither.
 """
 

@@ -240,6 +240,7 @@ void common_params(RaggedParams& rp, const DeviceInfo& dev) {
     rp.list_w = 128;
 #ifdef LIBGEMM_TC_TRACE
     rp.trace = trace_buffer();
+    rp.trace_ctas = kTraceCtas;
 #endif
 }
 
@@ -575,7 +576,8 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
         sh.tile_w = shape.shrink_w;
         sh.split = log2_of(shape.shrink_split);
 #ifdef LIBGEMM_TC_TRACE
-        if (sh.trace) sh.trace += 64 * 1024;
+        rp.trace_ctas = sh.trace_ctas = kTraceCtas / 2;  // the buffer's lower and upper half
+        if (sh.trace) sh.trace += 64 * (kTraceCtas / 2);
 #endif
         const int64_t tiles = (m + W - 1) / W;
         const int64_t clusters = tiles * subs * shape.chains;

@@ -86,8 +86,8 @@ struct RaggedParams {
     unsigned long long wait_limit_ns;
     int fault_inject;
 #ifdef LIBGEMM_TC_TRACE
-    unsigned long long* trace;  // trace build: 64 timestamps per CTA (the shrink's after
-                                // those of 1024 CTAs)
+    unsigned long long* trace;  // trace build: 64 timestamps for each of trace_ctas CTAs
+    unsigned trace_ctas;
 #endif
 };
 

@@ -274,6 +274,7 @@ int launch_gemm_tc(const Problem& pr, const DeviceInfo& dev, const TcLaunch& o,
     tp.clc = o.clc && !mc ? 1 : 0;  // the multicast variant keeps the static schedule
 #ifdef LIBGEMM_TC_TRACE
     tp.trace = g_trace;
+    tp.trace_ctas = kTraceCtas;
 #endif
     // units (at most twice the tiles) x CTAs must fit the grid's int range
     if ((int64_t)tp.tiles_m * tp.tiles_n * 2 * CG > 0x7fffffffLL) return kUnsupported;
@@ -306,8 +307,10 @@ int launch_gemm_tc(const Problem& pr, const DeviceInfo& dev, const TcLaunch& o,
 }  // namespace libgemm
 
 #ifdef LIBGEMM_TC_TRACE
-// Debug build only: device buffer of 64 timestamps per CTA for the next
-// launches of the tensor-core kernel (NULL: no tracing).
+// Debug build only: device buffer of 64 timestamps (8 bytes each) for each of
+// 1024 CTAs, for the next launches of the tensor-core kernels (NULL: no
+// tracing). gemm_lora's first launch takes the upper half, its second the
+// lower. CTAs past the buffer are not stamped.
 extern "C" void libgemm_tc_trace_buffer(void* dev_ptr) {
     libgemm::g_trace = static_cast<unsigned long long*>(dev_ptr);
 }

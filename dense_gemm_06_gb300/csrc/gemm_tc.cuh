@@ -47,6 +47,7 @@ struct TcParams {
     EpiParams epi;             // fused epilogue (inactive for a plain GEMM)
 #ifdef LIBGEMM_TC_TRACE
     unsigned long long* trace;  // debug build: per-CTA phase timestamps (64 per CTA)
+    unsigned trace_ctas;        // of this many CTAs
 #endif
 };
 
@@ -54,9 +55,10 @@ struct TcParams {
 // fixed points of every role, 64 slots per CTA, for reading the kernel's
 // timeline on the host. Compiled out of the library.
 #ifdef LIBGEMM_TC_TRACE
+constexpr unsigned kTraceCtas = 1024;  // that the registered buffer has room for
 #define TC_TRACE(p, slot)                                                              \
     do {                                                                               \
-        if ((p).trace && (slot) < 64)                                                  \
+        if ((p).trace && (slot) < 64 && blockIdx.x < (p).trace_ctas)                   \
             (p).trace[(size_t)blockIdx.x * 64 + (slot)] = gemm_ptx::globaltimer_ns();  \
     } while (0)
 #else
