@@ -11,8 +11,10 @@ micro-batches (beta = 1) as fp32:
 
     dW2_e += dy^T h   dh = dy W2_e   dW1_e += (dh masked)^T x   dx = (dh masked) W1_e
 
-Nothing of it copies the experts' sizes to the host: the limits come from
-torch.bincount and cumsum on the stream that the products run on.
+Nothing of it copies the experts' sizes to the host: the limits are searched
+for in the sorted experts of the rows, on the stream that the products run on
+(torch.bincount would read its input's range back), so block() can be captured
+into a graph.
 
     python -m dense_gemm_06_gb300.experts_demo [--tokens T] [--experts E] [--top K]
         [--hidden D] [--inner F] [--requests Q] [--rank R]
@@ -76,10 +78,9 @@ def route(x, router, top):
     lg.check(lg.softmax_rows(x.shape[0], router.shape[0], logits, router.shape[0], logits,
                              router.shape[0]))
     weight, expert = logits.topk(top, dim=1)
-    order = expert.flatten().argsort(stable=True)
-    sizes = torch.bincount(expert.flatten(), minlength=router.shape[0])
-    offsets = torch.zeros(router.shape[0] + 1, dtype=torch.int32, device=x.device)
-    offsets[1:] = sizes.cumsum(0)
+    by_expert, order = expert.flatten().sort(stable=True)
+    offsets = torch.searchsorted(by_expert, torch.arange(router.shape[0] + 1, device=x.device),
+                                 out_int32=True)
     return offsets, order // top, weight.flatten()[order]
 
 
@@ -100,8 +101,9 @@ def make(tokens, n_experts, hidden, inner, requests, rank, seed=0):
         dout=normal(tokens, hidden))
 
 
-def step(s, top, timed=lambda name, f: f()):
-    """The block's forward and the experts' backward pass; a dict of results."""
+def block(s, top, timed=lambda name, f: f()):
+    """The block's forward and the experts' backward pass; a dict of results.
+    Everything is enqueued on the current stream, nothing waits for it."""
     import torch
     x = timed("lora projection", lambda: lora(s["x"], s["w"], s["adapter"], s["la"], s["lb"],
                                               s["scale"]))
@@ -117,9 +119,15 @@ def step(s, top, timed=lambda name, f: f()):
     dh = timed("down input gradient", lambda: experts_input_grad(dy, s["w2"], offsets)) * (h > 0)
     timed("up weight gradient", lambda: experts_weight_grad(dh, xs, offsets, dw1))
     dxs = timed("up input gradient", lambda: experts_input_grad(dh, s["w1"], offsets))
-    lg.check(lg.gemm_check_device_error())
     return dict(x=x, offsets=offsets, token=token, weight=weight, out=out, dy=dy, dw1=dw1, dw2=dw2,
                 dxs=dxs)
+
+
+def step(s, top, timed=lambda name, f: f()):
+    """block(), and a check of the device's error words."""
+    r = block(s, top, timed)
+    lg.check(lg.gemm_check_device_error())
+    return r
 
 
 def reference(s, r):
