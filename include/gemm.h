@@ -288,7 +288,9 @@ int softmax_rows(int64_t M, int64_t N, const float *x, int64_t ldx, float *y, in
  * Types: the 16-bit dtypes (GEMM_F32 is GEMM_ERR_UNSUPPORTED). Accumulation
  * is fp32, C is rounded once, and the sums do not depend on timing. epi as in
  * gemm_ex (NULL: plain), with bias a DEVICE array of G x N elements of C's
- * type. Operands whose rows are not 16-byte aligned (or with strideb no
+ * type. An fp32 C with beta = 1 and neither bias nor activation is added to by
+ * global additions (unless CTAs share the depth): they take numbers below
+ * 2^-126, of C and of the product, as zero. Operands whose rows are not 16-byte aligned (or with strideb no
  * multiple of 8) are repacked into pool scratch first, B whole. G, M or N
  * zero is a no-op, K zero leaves the epilogue of zero sums. Otherwise
  * ownership, asynchrony and status codes are those of gemm().
@@ -311,9 +313,9 @@ int gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offs
  * C_g is written). `offsets` as in gemm_grouped, within [0, K]. Values of
  * other groups' rows never reach a sum, infinities and NaN included (of wrong
  * limits each pair is clamped by itself, a decreasing one empty). With beta = 1
- * the call accumulates into C (an fp32 one through global additions, which
- * take numbers below 2^-126 as zero). It takes 260 bytes of scratch per group. Types, epilogue (bias: G x N),
- * repacking, degenerate sizes and status codes as gemm_grouped.
+ * the call accumulates into C (fp32: see gemm_grouped). It takes 260 bytes of
+ * scratch per group. Types, epilogue (bias: G x N), repacking, degenerate sizes
+ * and status codes as gemm_grouped.
  */
 int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets,
                    const void *A, int64_t lda, const void *B, int64_t ldb,
@@ -347,7 +349,15 @@ int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *of
  * Misaligned operands (rows of A, B, or K or N no multiple of 8 for the
  * adapters) are repacked into pool scratch first. L or R zero: gemm_ex().
  * epi as in gemm_ex. T takes at most 512 MiB of scratch (rows are processed
- * in panels beyond). Otherwise as gemm().
+ * in panels beyond). Adapters of a row tile (up to 256 rows) whose lora_b have
+ * 2^34 elements or more between them are GEMM_ERR_UNSUPPORTED. Otherwise as
+ * gemm().
+ *
+ * Backward: the input gradient is the same call on dC with lora_a and lora_b
+ * exchanged and B read along its other side (M, K, N; b_major exchanged). The
+ * adapters' own gradients, of rows sorted by adapter, are grouped products:
+ * U = dC LB^T and T = A LA^T by gemm_grouped (N = R), then dLA = U^T A and
+ * dLB = T^T dC by gemm_grouped_k, times scale.
  */
 int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
               const void *A, int64_t lda, const void *B, int64_t ldb, int b_major,
