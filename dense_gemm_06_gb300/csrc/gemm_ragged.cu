@@ -399,7 +399,13 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rc = check_device_pointers(ptrs, 5, dev->device);
     if (rc != kOk) return rc;
 
-    const RaggedShape shape = plan_grouped_k(G, M, N, dev->sm_count);
+    const EpiParams ep = epi_params(epi);
+    const bool reads = ep.active && ep.beta != 0.f;
+    const RaggedOut out = oe == 2              ? (reads ? kOut16Reads : kOut16)
+                          : !ep.active         ? kOut32
+                          : reads && !adds(ep) ? kOut32Reads
+                                               : kOut32Epilogue;
+    const RaggedShape shape = plan_grouped_k(G, M, N, dev->sm_count, out, K / G);
     const bool bf16 = is_bf16(dtype);
     RaggedParams rp;
     std::memset(&rp, 0, sizeof(rp));
@@ -416,7 +422,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rp.C = C;
     rp.ldc = ldc;
     rp.stridec = stridec;
-    rp.epi = epi_params(epi);
+    rp.epi = ep;
     map_c(rp, dtype, C, G, stridec, M, N, ldc);
     const int64_t units = G * rp.tiles_f * rp.tiles_r;
     if ((int64_t)rp.tiles_f * rp.tiles_r > INT32_MAX / G ||

@@ -189,6 +189,12 @@ struct RUnit {
     int tile;        // lora: list tile
 };
 
+// An active epilogue that adds to C and does nothing else: an fp32 C takes it as
+// global additions.
+__host__ __device__ __forceinline__ bool adds(const EpiParams& e) {
+    return e.beta == 1.f && !e.bias && e.act == 0;
+}
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 // rows mode: finds the group, row tile and feature tile of unit u. The whole
@@ -1257,7 +1263,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             float bias = 0.f;
             if (epi && p.epi.bias && f_ok)
                 bias = to_f32(static_cast<const OutT*>(p.epi.bias)[(int64_t)un.g * p.feats + f]);
-            const bool accumulates = epi && p.epi.beta == 1.f && !p.epi.bias && p.epi.act == 0;
+            const bool accumulates = epi && adds(p.epi);
             OutT* c_col = nullptr;
             if constexpr (MODE != kRagShrink)
                 c_col = static_cast<OutT*>(p.C) + (int64_t)un.row0 * p.ldc + f +

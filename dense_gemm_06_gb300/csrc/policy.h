@@ -289,13 +289,45 @@ inline bool plan_grouped_ticket(const RaggedShape& s, int64_t M, int64_t N, int6
     return s.cta_group == 2 && num_kb >= 64 && (M / 256) * ((N + 255) / 256) >= sm_count;
 }
 
-// gemm_grouped_k: G results of M x N. Pairs where their units fill the SMs;
-// measured, single CTAs and pairs: 13 results of 1600 x 2752 47.6 and 33.8 us, 22
-// of 2598 x 1152 64.5 and 52.2, 8 fp32 ones of 1536 x 1664 30.5 and 33.9.
-inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count) {
+// What gemm_grouped_k's epilogue does to C.
+enum RaggedOut {
+    kOut16,          // 16-bit, written
+    kOut16Reads,     // 16-bit, read first (beta)
+    kOut32,          // fp32, written as it is summed
+    kOut32Epilogue,  // fp32, added to by global additions, or bias / activation, beta 0
+    kOut32Reads,     // fp32, read first (any other beta)
+};
+
+// gemm_grouped_k: G results of M x N, `avg` summed rows each on average. Pairs
+// move fewer operands per product; single CTAs store a result with half the
+// columns per epilogue warp, which counts where C is read or the sums are short.
+// Measured, single CTAs and pairs (us; rounds: pair units per pair):
+//   kOut16          8 of 1536 x 1664, 64 to 1000 rows 20.4 to 46.5, 17.3 to 38.5; 77
+//                   of 256 x 256 9.9 to 29.1, 10.3 to 30.5
+//   kOut16Reads     3 rounds 44 and 55, 7 69 and 91, 16 275 and 308, 20 225 and
+//                   270, 40 713 and 719, 74 1459 and 1444
+//   kOut32          300 rows, 1 round 15.4 and 17.1, 3 24.4 and 28.2, 4 28.3 and
+//                   30.2, 6 41.5 and 39.4, 13 68.8 and 60.8; 800 rows, 1 round 21.6
+//                   and 22.5, 3 36.3 and 31.0, 4 43.2 and 41.1
+//   kOut32Epilogue  beta 1, 40 rounds, 64, 300, 768 and 1500 rows 266 and 276, 285
+//                   and 295, 365 and 336, 585 and 465; 768 rows, 13 rounds 126 and
+//                   124, 7 73 and 78, 3 50 and 58. ReLU alike: 768 rows, 13 rounds
+//                   107 and 102, 300 rows 73 and 86
+//   kOut32Reads     74 rounds, 64, 768 and 1500 rows 765 and 1293, 849 and 1267,
+//                   1146 and 1369; 3 rounds, 64 rows 30 and 51
+inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count,
+                                  RaggedOut out = kOut16, int64_t avg = 0) {
+    const RaggedShape pairs{2, 256, 1}, single{1, 128, 1};
     const int64_t pair_units = G * ((M + 255) / 256) * ((N + 255) / 256);
-    if (pair_units * 2 > sm_count) return RaggedShape{2, 256, 1};
-    return RaggedShape{1, 128, 1};
+    if (pair_units * 2 <= sm_count) return single;
+    const int64_t rounds = pair_units * 2 / sm_count;
+    switch (out) {
+        case kOut16: return pairs;
+        case kOut16Reads: return rounds >= 32 ? pairs : single;
+        case kOut32: return rounds >= 5 || (rounds >= 3 && avg >= 512) ? pairs : single;
+        case kOut32Epilogue: return rounds >= 8 && avg >= 704 ? pairs : single;
+        default: return single;
+    }
 }
 
 // gemm_lora: the expand's shape, and the shrink's: rows_blocks > 0 -- few rows,

@@ -27,6 +27,10 @@ ROWS_PAIRS_COUNTED = [([5000, 2000, 0, 300, 2900, 9], 2048, 4104)]
 ROWS_SINGLE = [([50, 0, 49, 3] * 12, 520, 1000), ([40, 64, 1] * 10, 776, 136)]  # whole depth
 ROWS_SPLIT = [([9], 1024, 16384, 8), ([2, 20], 264, 9000, 8), ([60], 520, 2048, 4)]
 
-# gemm_grouped_k: (sizes, M, N)
+# gemm_grouped_k: (sizes, M, N). Pairs for 16-bit results that are written, for
+# 16-bit results that are read (beta), and for fp32 ones, plain or with an
+# epilogue; fp32 results that are read never get pairs.
 DEPTH_PAIRS = [([1500, 0, 705, 704, 40], 1032, 1288), ([1, 3000, 63], 1040, 1800)]
+DEPTH_PAIRS_READ = [([i * 7 % 61 for i in range(200)], 776, 776)]
+DEPTH_PAIRS_F32 = [([1500, 0, 705, 704, 640], 2568, 2824)]
 DEPTH_SINGLE = [([1500, 0, 705, 704, 40], 264, 328), ([2111], 136, 264)]

@@ -22,7 +22,7 @@ K_MAJOR, MN_MAJOR = lg.GEMM_MAJOR_K, lg.GEMM_MAJOR_MN
 # alpha, beta, bias, activation; integers and quarters, so that every result
 # before the last rounding is exact in fp32
 EPILOGUES = [(1.0, 1.0, False, 0), (0.25, 1.0, False, 0), (0.25, 0.5, True, lg.GEMM_ACT_RELU),
-             (1.0, 0.0, True, 0), (-0.5, 2.0, False, lg.GEMM_ACT_RELU),
+             (1.0, 0.0, True, 0), (0.25, 0.0, True, lg.GEMM_ACT_RELU), (-0.5, 2.0, False, lg.GEMM_ACT_RELU),
              (0.25, 0.5, True, lg.GEMM_ACT_GELU)]
 
 
@@ -93,7 +93,7 @@ def test_rows_pairs_leave_other_rows_alone():
 # ----------------------------------------------------------- gemm_grouped_k --
 
 @pytest.mark.parametrize("dtype", [BF, HF, F32, lg.GEMM_F16_F32])
-@pytest.mark.parametrize("sizes,M,N", rs.DEPTH_PAIRS + rs.DEPTH_SINGLE)
+@pytest.mark.parametrize("sizes,M,N", rs.DEPTH_PAIRS + rs.DEPTH_SINGLE + rs.DEPTH_PAIRS_F32)
 def test_depth_exact(dtype, sizes, M, N):
     C, A, B, ends = run_depth(sizes, M, N, dtype)
     assert_exact(C, ref_depth(A, B, ends))
@@ -101,7 +101,8 @@ def test_depth_exact(dtype, sizes, M, N):
 
 @pytest.mark.parametrize("epi", EPILOGUES)
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("sizes,M,N", rs.DEPTH_PAIRS + rs.DEPTH_SINGLE)
+@pytest.mark.parametrize("sizes,M,N", rs.DEPTH_PAIRS + rs.DEPTH_SINGLE + rs.DEPTH_PAIRS_F32 +
+                         rs.DEPTH_PAIRS_READ)
 def test_depth_epilogue(epi, dtype, sizes, M, N):
     G = len(sizes)
     old, bias, args = epi_args(epi, (G, M, N), (G, N), dtype)
@@ -231,7 +232,7 @@ def test_rows_fp32_accuracy_does_not_fall_with_the_depth(dtype, sizes, N):
 
 
 @pytest.mark.parametrize("dtype", [F32, lg.GEMM_F16_F32])
-@pytest.mark.parametrize("M,N", [(1032, 1288), (264, 328)])
+@pytest.mark.parametrize("M,N", [(1032, 1288), (264, 328), (2568, 2824)])
 def test_depth_fp32_accuracy_does_not_fall_with_the_depth(dtype, M, N):
     C, A, B, ends = run_depth([6000, 9000, 704, 7000], M, N, dtype, ints=False)
     assert relative(C, ref_depth(A, B, ends)) < FOLDED

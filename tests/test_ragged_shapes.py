@@ -4,6 +4,7 @@
 import pytest
 
 import ragged_shapes as rs
+from test_ragged_limits import probe as limits  # noqa: F401 (a fixture)
 from test_ragged_policy import SMS, probe  # noqa: F401 (a fixture)
 
 FOLD = 11  # k-blocks that fp32 results sum in one accumulator
@@ -53,8 +54,38 @@ def test_rows(probe):  # noqa: F811
     assert any(blocks(s[2]) > FOLD * s[3] for s in rs.ROWS_SPLIT)
 
 
-def test_depth(probe):  # noqa: F811
-    for shapes, cg in ((rs.DEPTH_PAIRS, 2), (rs.DEPTH_SINGLE, 1)):
-        for sizes, M, N in shapes:
-            assert probe("grouped_k", len(sizes), M, N, SMS)[0] == cg
-            assert max(sizes) > 64 * FOLD
+W16, R16, W32, E32, R32 = range(5)  # RaggedOut
+
+
+def depth(limits, sizes, M, N, out):  # noqa: F811
+    return limits("depth", len(sizes), M, N, SMS, out, sum(sizes) // len(sizes))
+
+
+def test_depth(limits):  # noqa: F811
+    for s in rs.DEPTH_PAIRS:
+        assert depth(limits, *s, W16) == 2
+    for s in rs.DEPTH_PAIRS_READ:
+        assert depth(limits, *s, W16) == depth(limits, *s, R16) == 2
+    for s in rs.DEPTH_PAIRS_F32:
+        assert depth(limits, *s, W32) == depth(limits, *s, E32) == 2
+        assert max(s[0]) > 64 * FOLD
+    for s in rs.DEPTH_SINGLE + rs.DEPTH_PAIRS + rs.DEPTH_PAIRS_READ + rs.DEPTH_PAIRS_F32:
+        assert depth(limits, *s, R32) == 1
+    for s in rs.DEPTH_SINGLE:
+        assert {depth(limits, *s, out) for out in range(5)} == {1}
+        assert max(s[0]) > 64 * FOLD
+
+
+@pytest.mark.parametrize("G,M,N,avg,want", [
+    # where single CTAs were measured faster by 3% or more, or pairs (CTAs per
+    # unit, by what the epilogue does to C; None: within 3%)
+    (8, 1536, 1664, 300, (2, None, 1, None, 1)), (8, 1536, 1664, 1000, (2, None, 2, None, 1)),
+    (24, 776, 520, 64, (2, 1, 1, 1, 1)), (24, 776, 520, 768, (2, 1, None, 1, 1)),
+    (13, 1600, 2752, 300, (2, 1, 2, 1, 1)), (13, 1600, 2752, 768, (2, 1, 2, 2, 1)),
+    (64, 2816, 2048, 64, (2, None, 2, 1, 1)), (64, 2816, 2048, 768, (2, 2, 2, 2, 1)),
+    (64, 520, 520, 64, (2, 1, None, 1, 1)), (160, 256, 256, 300, (None, None, 1, None, None)),
+    (16, 256, 512, 300, (1, 1, 1, 1, 1)), (40, 256, 256, 1000, (1, 1, 1, 1, 1)),
+])
+def test_depth_takes_what_was_faster(limits, G, M, N, avg, want):  # noqa: F811
+    for out, cg in enumerate(want):
+        assert cg in (None, limits("depth", G, M, N, SMS, out, avg)), out
