@@ -371,7 +371,12 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
     s.chains = (int)(chains < 1 ? 1 : (chains > parts ? parts : chains));
     if (M <= 128 && M * slot <= 4096) {
         s.rows_blocks = (int)(M * (slot / 4));
-        s.scan_blocks = M < 32 ? 16 : 64;
+        // 16 blocks look over 512 KB of LB in one pass of their loads. Measured, 16
+        // and 64 blocks (us): 1 row of rank 16 and 4096 features (128 KB) 13.1 and
+        // 13.4, 1 of rank 128 (1 MB) 12.5 and 11.1, 16 of rank 16 (2 MB) 13.0 and
+        // 12.4, 24 (3 MB) 16.9 and 14.1, 16 of rank 128 (16 MB) 58.9 and 29.6; 16 of
+        // rank 16 and 1024 features (512 KB) 9.3 and 9.6, 24 (768 KB) 10.4 and 10.6
+        s.scan_blocks = listed * slot * N * 2 < (1 << 20) ? 16 : 64;
     }
     return s;
 }

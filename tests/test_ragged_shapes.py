@@ -89,3 +89,14 @@ def test_depth(limits):  # noqa: F811
 def test_depth_takes_what_was_faster(limits, G, M, N, avg, want):  # noqa: F811
     for out, cg in enumerate(want):
         assert cg in (None, limits("depth", G, M, N, SMS, out, avg)), out
+
+
+@pytest.mark.parametrize("M,R,N,want", [
+    # blocks that look over LB, where one of 16 and 64 was measured faster by 3% or more
+    (1, 16, 1024, 16), (8, 64, 4096, 64), (16, 16, 1024, 16), (16, 16, 4096, 64),
+    (24, 16, 4096, 64), (32, 16, 4096, 64), (1, 128, 4096, 64), (1, 128, 1024, 16),
+    (16, 128, 1024, 64), (16, 128, 4096, 64), (32, 64, 1024, 64), (128, 16, 4096, 64),
+])
+def test_lora_scan_goes_by_the_size_of_lb(probe, M, R, N, want):  # noqa: F811
+    plan, _ = lora(probe, M, N, 4096, R, 24)
+    assert plan[3] > 0 and plan[4] == want
