@@ -280,10 +280,13 @@ inline RaggedShape plan_grouped(int64_t G, int64_t M, int64_t N, int64_t num_kb,
 // gemm_grouped: whether CTA pairs count the units taken instead of walking every
 // n-th one. The units' widths differ, so a fixed walk ends up to about a unit
 // late; the count costs a 4-byte memset before the launch and the launch's
-// overlap with what precedes it. Measured: units of 224 k-blocks (8 groups,
-// 16384 rows, 4096 x 14336) 1034 us against 1073 us, units of 32 (64 groups,
-// 49152 rows, 2816 x 2048) 348 us against 345 us; so from 64 k-blocks on, with
-// two rounds of units at least.
+// overlap with what precedes it, 3 us in all. Measured, walked and counted, by
+// k-blocks per unit: 64 groups, 49152 rows, 2816 features 16 203 and 207 us, 32
+// 387 and 386, 64 804 and 795, 128 1567 and 1522, 224 2920 and 2790; 8 groups,
+// 16384 rows, 4096 features 16 84 and 87, 64 320 and 321, 128 660 and 648, 224
+// 1172 and 1164; 16 groups, 12288 rows, 2048 features 32 71 and 75, 64 132 and
+// 136, 128 259 and 262, 224 501 and 486. So from 64 k-blocks on, with two rounds
+// of units at least; between 64 and 128 neither is ahead by more than 3%.
 inline bool plan_grouped_ticket(const RaggedShape& s, int64_t M, int64_t N, int64_t num_kb,
                                 int sm_count) {
     return s.cta_group == 2 && num_kb >= 64 && (M / 256) * ((N + 255) / 256) >= sm_count;
@@ -334,11 +337,11 @@ inline RaggedShape plan_grouped_k(int64_t G, int64_t M, int64_t N, int sm_count,
 // plain dot products in that many blocks, beside scan_blocks that look over LB
 // (whole calls on 4096 x 4096 with 24 adapters, dot products and tensor cores:
 // 48 rows of rank 16 16.3 and 23.1 us, 128 rows of rank 16 21.1 and 28.3, 64
-// rows of rank 64 31.2 and 31.5) --, else lanes per unit, rows per tile, split and chains (clusters that share
-// the parts of a row tile's list). slot: lanes per adapter; ranks up to 32 run
-// the narrow ring (64 lanes and rows, twice the stages: a tile of requests one
-// after the other seldom has more than two adapters). listed: most adapters of
-// a list.
+// rows of rank 64 31.2 and 31.5) --, else lanes per unit, rows per tile, split
+// and chains (clusters that share the parts of a row tile's list). slot: lanes
+// per adapter; ranks up to 32 run the narrow ring (64 lanes and rows, two
+// k-blocks per stage: a tile of requests one after the other seldom has more
+// than two adapters). listed: most adapters of a list.
 struct LoraShape {
     RaggedShape expand;
     int lanes;
@@ -355,8 +358,14 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
     } else {
         int w = 16;
         while (w < 128 && w < M) w *= 2;
-        // more rows than a unit: narrower units before a split of the depth (611
-        // rows of 1804 x 1544 26.5 us, split 31.5; 400 of 1024 x 4096 26.8 and 25.6)
+        // More rows than a unit: narrower units before a split of the depth. Which
+        // is faster hangs on the rows' adapters, which only the device knows.
+        // Requests one after the other (19 rows each, rank 24), units of 64 and of
+        // 128 rows: 47 shapes of 129 to 900 rows, 46 of them faster with 64, by 5 to
+        // 40% (611 rows of 1804 x 1544 26.2 and 37.4 us, 400 of 1024 x 4096 26.2 and
+        // 30.6; 200 of 1804 x 4096 28.9 and 27.8). Another adapter in every row, 8
+        // adapters of rank 16: 26.5 and 31.4, 26.9 and 25.3, 29.2 and 27.3; 40
+        // adapters: 60.0 and 56.5, 57.9 and 54.1, 46.7 and 45.1.
         if (M > 128 && ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count) w = 64;
         const int64_t units = ((M + w - 1) / w) * ((N + 127) / 128);
         s.expand = RaggedShape{1, w, plan_ragged_split(units, num_kb, sm_count)};
