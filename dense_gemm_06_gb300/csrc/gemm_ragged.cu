@@ -52,8 +52,13 @@
 //     depth; partial sums go through distributed shared memory to the CTA that
 //     owns the row and are added in rank order, so results do not depend on
 //     timing.
-//   * The expand is a programmatic dependent of the shrink and starts on X and
-//     W at once; it waits for the shrink only before its first block of T.
+//   * The expand is a programmatic dependent of the shrink: where it runs it
+//     starts on X and W at once and waits for the shrink only before its first
+//     block of T. It runs on an SM once the shrink's blocks there are done: its
+//     CTA takes 226 KB of shared memory, and not even a block of dot products
+//     (4 KB, 16384 registers) fits beside it. One token's shrink is 20 blocks, so
+//     most of the expand overlaps it; 48 rows of rank 16 are 256 blocks, on every
+//     SM, and the overlap is the shrink's last round.
 #include <cuda_runtime.h>
 
 #include <cstdint>

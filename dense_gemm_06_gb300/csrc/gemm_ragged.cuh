@@ -7,7 +7,10 @@
 // 2048: 119 us, 6.5 TB/s); many, the tensor pipe and its feed from L2 (one group
 // of 8192^3: 556 us, 1.98 PFLOP/s, gemm() 548 us on the same GPU); the smallest
 // calls, the chain of latencies from launch to last store (one row against 4096 x
-// 4096 with an adapter: 12 us, of which the weights take 5).
+// 4096 with an adapter: 11 us, of which the weights take 5).
+//
+// Times in these files are of short runs. In runs of seconds the large calls settle
+// at the power limit's clocks and take 12 to 18% longer (cuBLAS: 10%).
 //
 // One orientation serves all four: the MMA's M side (128 TMEM lanes per CTA)
 // is the feature side P -- the weights -- and its N side the row side Q -- the

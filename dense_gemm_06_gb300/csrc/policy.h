@@ -361,8 +361,8 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
         // More rows than a unit: narrower units before a split of the depth. Which
         // is faster hangs on the rows' adapters, which only the device knows.
         // Requests one after the other (19 rows each, rank 24), units of 64 and of
-        // 128 rows: 47 shapes of 129 to 900 rows, 46 of them faster with 64, by 5 to
-        // 40% (611 rows of 1804 x 1544 26.2 and 37.4 us, 400 of 1024 x 4096 26.2 and
+        // 128 rows: 66 shapes of 129 to 900 rows, 65 of them faster with 64, by 4 to
+        // 72% (611 rows of 1804 x 1544 26.2 and 37.4 us, 400 of 1024 x 4096 26.2 and
         // 30.6; 200 of 1804 x 4096 28.9 and 27.8). Another adapter in every row, 8
         // adapters of rank 16: 26.5 and 31.4, 26.9 and 25.3, 29.2 and 27.3; 40
         // adapters: 60.0 and 56.5, 57.9 and 54.1, 46.7 and 45.1.

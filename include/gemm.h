@@ -345,7 +345,7 @@ int gemm_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *of
  * the row's neighbouring ranks where T is small beside that one, or 2^-49; it
  * overflows where fp16 does (65504).
  * Rows see their own adapter only: an infinity or NaN in another adapter does
- * not reach them. Two launches: the second starts while the first still runs.
+ * not reach them. Two launches; the second starts on an SM as the first leaves it.
  * Misaligned operands (rows of A, B, or K or N no multiple of 8 for the
  * adapters) are repacked into pool scratch first. L or R zero: gemm_ex().
  * epi as in gemm_ex. T takes at most 512 MiB of scratch (rows are processed
