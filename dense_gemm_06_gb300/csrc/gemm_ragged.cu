@@ -279,6 +279,13 @@ EpiParams epi_params(const gemm_epilogue* e) {
     return EpiParams{1, e->alpha, e->beta, e->bias, 0, e->activation};
 }
 
+RaggedOut ragged_out(const EpiParams& e, int dtype) {
+    const bool reads = e.active && e.beta != 0.f;
+    if (c_bytes(dtype) == 2) return reads ? kOut16Reads : kOut16;
+    if (!e.active) return kOut32;
+    return reads && !adds(e) ? kOut32Reads : kOut32Epilogue;
+}
+
 bool sizes_ok(int64_t a, int64_t b, int64_t c, int64_t d) {
     for (int64_t x : {a, b, c, d})
         if (x < 0 || x > INT32_MAX) return false;
@@ -322,7 +329,9 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     if (rc != kOk) return rc;
 
     const int64_t num_kb = (K + BK - 1) / BK;
-    const RaggedShape shape = plan_grouped(G, M, N, num_kb, dev->sm_count);
+    const EpiParams ep = epi_params(epi);
+    const RaggedShape shape =
+        plan_grouped(G, M, N, num_kb, dev->sm_count, ragged_out(ep, dtype));
     const bool bf16 = is_bf16(dtype);
     RaggedParams rp;
     std::memset(&rp, 0, sizeof(rp));
@@ -337,7 +346,7 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     rp.split = log2_of(shape.split);
     rp.C = C;
     rp.ldc = ldc;
-    rp.epi = epi_params(epi);
+    rp.epi = ep;
     map_c(rp, dtype, C, 0, 0, M, N, ldc);
     const int64_t units = ((G < M ? G : M) + M / shape.tile_w) * rp.tiles_f;
     if (!units_fit(units, shape.cta_group * shape.split)) return kUnsupported;
@@ -405,12 +414,8 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     if (rc != kOk) return rc;
 
     const EpiParams ep = epi_params(epi);
-    const bool reads = ep.active && ep.beta != 0.f;
-    const RaggedOut out = oe == 2              ? (reads ? kOut16Reads : kOut16)
-                          : !ep.active         ? kOut32
-                          : reads && !adds(ep) ? kOut32Reads
-                                               : kOut32Epilogue;
-    const RaggedShape shape = plan_grouped_k(G, M, N, dev->sm_count, out, K / G);
+    const RaggedShape shape =
+        plan_grouped_k(G, M, N, dev->sm_count, ragged_out(ep, dtype), K / G);
     const bool bf16 = is_bf16(dtype);
     RaggedParams rp;
     std::memset(&rp, 0, sizeof(rp));

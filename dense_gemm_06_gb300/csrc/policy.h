@@ -263,16 +263,37 @@ inline int plan_ragged_split(int64_t units, int64_t num_kb, int sm_count) {
     return s;
 }
 
+// What the epilogue of a grouped product does to C.
+enum RaggedOut {
+    kOut16,          // 16-bit, written
+    kOut16Reads,     // 16-bit, read first (beta)
+    kOut32,          // fp32, written as it is summed
+    kOut32Epilogue,  // fp32, added to by global additions, or bias / activation, beta 0
+    kOut32Reads,     // fp32, read first (any other beta)
+};
+
 // gemm_grouped: M rows in G groups (their sizes are known on the device only),
 // N features, num_kb k-blocks. Pairs where a group has more than 64 rows on
 // average and their units fill the SMs. Measured, 64 groups of 1536 x 2048,
 // single CTAs and pairs: 8 rows each 70.2 and 71.4 us, 64 rows 75.0 and 75.4, 96
-// rows 78.9 and 78.3, 256 rows 103.7 and 92.0.
-inline RaggedShape plan_grouped(int64_t G, int64_t M, int64_t N, int64_t num_kb, int sm_count) {
+// rows 78.9 and 78.3, 256 rows 103.7 and 92.0. A fused epilogue on fp32 results
+// takes a pair's warps, with twice the columns each, longer than it saves unless
+// many rounds of units (and with C read first, a long depth) hide it: 3 rounds,
+// 22 k-blocks (16 groups, 4096 rows, 2048 features) beta 1 41.0 and 51.6 us, other
+// beta 43.1 and 71.6, bias and GELU 40.2 and 64.1; 7 rounds, 32 k-blocks 83.2 and
+// 92.6, 85.3 and 115.1, 85.4 and 110.2; 15 rounds, 64 k-blocks 505 and 372, 513 and
+// 473, 526 and 442; 37 rounds, 32 k-blocks 533 and 457, 578 and 688, 630 and 574.
+// (16-bit results with the same epilogues: pairs at most 3% slower, up to 36%
+// faster.)
+inline RaggedShape plan_grouped(int64_t G, int64_t M, int64_t N, int64_t num_kb, int sm_count,
+                                RaggedOut out = kOut16) {
     const int64_t groups = G < M ? G : M;  // at most this many have rows
     const int64_t avg = (M + groups - 1) / groups;
     const int64_t pair_units = (groups + M / 256) * ((N + 255) / 256);
-    if (avg > 64 && pair_units * 2 > sm_count) return RaggedShape{2, 256, 1};
+    bool pairs = avg > 64 && pair_units * 2 > sm_count;
+    if (out == kOut32Epilogue || out == kOut32Reads)
+        pairs = pairs && pair_units * 2 / sm_count >= 12 && (out != kOut32Reads || num_kb >= 64);
+    if (pairs) return RaggedShape{2, 256, 1};
     const int64_t units = (groups + M / 128) * ((N + 127) / 128);
     return RaggedShape{1, 128, plan_ragged_split(units, num_kb, sm_count)};
 }
@@ -291,15 +312,6 @@ inline bool plan_grouped_ticket(const RaggedShape& s, int64_t M, int64_t N, int6
                                 int sm_count) {
     return s.cta_group == 2 && num_kb >= 64 && (M / 256) * ((N + 255) / 256) >= sm_count;
 }
-
-// What gemm_grouped_k's epilogue does to C.
-enum RaggedOut {
-    kOut16,          // 16-bit, written
-    kOut16Reads,     // 16-bit, read first (beta)
-    kOut32,          // fp32, written as it is summed
-    kOut32Epilogue,  // fp32, added to by global additions, or bias / activation, beta 0
-    kOut32Reads,     // fp32, read first (any other beta)
-};
 
 // gemm_grouped_k: G results of M x N, `avg` summed rows each on average. Pairs
 // move fewer operands per product; single CTAs store a result with half the

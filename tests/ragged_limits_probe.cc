@@ -6,6 +6,7 @@
 //   units ROWS TILE_W            -> units of a group of ROWS rows
 //   width ROWS STEP MOST         -> rows that a unit of ROWS rows left spans
 //   blocks K0 K_END              -> 64-deep blocks of a depth group
+//   rows G M N NUM_KB SMS OUT    -> CTAs per unit of gemm_grouped (OUT: RaggedOut)
 //   depth G M N SMS OUT AVG      -> CTAs per unit of gemm_grouped_k (OUT: RaggedOut)
 #include <cstdio>
 #include <cstdlib>
@@ -22,6 +23,9 @@ int main(int argc, char** argv) {
         std::printf("%d\n", ragged_width(arg(2), arg(3), arg(4)));
     else if (argc == 4 && std::strcmp(argv[1], "blocks") == 0)
         std::printf("%d\n", ragged_blocks(arg(2), arg(3)));
+    else if (argc == 8 && std::strcmp(argv[1], "rows") == 0)
+        std::printf("%d\n", plan_grouped(arg(2), arg(3), arg(4), arg(5), arg(6),
+                                         (RaggedOut)arg(7)).cta_group);
     else if (argc == 8 && std::strcmp(argv[1], "depth") == 0)
         std::printf("%d\n", plan_grouped_k(arg(2), arg(3), arg(4), arg(5), (RaggedOut)arg(6),
                                            arg(7)).cta_group);

@@ -23,6 +23,9 @@ ROWS_PAIRS = [
     ([700, 30, 0, 1100, 256, 513], 2048, 328), ([900, 300, 0, 0, 1500], 2088, 776),
     ([600, 1, 900, 33], 2503, 1032),
 ]
+# fp32 results with a fused epilogue in pairs: the second and third with any beta
+ROWS_PAIRS_F32 = [([7000, 300, 0, 6000], 4400, 776), ([7000, 300, 0, 6000], 4400, 4104),
+                  ([4100, 1, 8500], 4567, 4100)]
 ROWS_PAIRS_COUNTED = [([5000, 2000, 0, 300, 2900, 9], 2048, 4104)]
 ROWS_SINGLE = [([50, 0, 49, 3] * 12, 520, 1000), ([40, 64, 1] * 10, 776, 136)]  # whole depth
 ROWS_SPLIT = [([9], 1024, 16384, 8), ([2, 20], 264, 9000, 8), ([60], 520, 2048, 4)]

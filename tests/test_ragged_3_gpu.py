@@ -69,19 +69,20 @@ def test_rows_epilogue(epi, dtype, sizes, N, K):
     assert_epilogue(C, ref, epi[3])
 
 
-@pytest.mark.parametrize("epi", [EPILOGUES[2]])
-@pytest.mark.parametrize("sizes,N,K", rs.ROWS_PAIRS_COUNTED)
-def test_rows_counted_pairs_epilogue(epi, sizes, N, K):
+@pytest.mark.parametrize("epi", EPILOGUES)
+@pytest.mark.parametrize("sizes,N,K", rs.ROWS_PAIRS_F32)
+def test_rows_fp32_pairs_epilogue(epi, sizes, N, K):
     old, bias, args = epi_args(epi, (sum(sizes), N), (len(sizes), N), F32)
     C, A, B, ends = run_rows(sizes, N, K, F32, fill=old, **args)
     ref = epi[0] * ref_rows(A, B, ends, len(sizes), N) + epi[1] * old.double()
-    for g, (lo, hi) in enumerate(zip(ends, ends[1:])):
-        ref[lo:hi] += bias[g].double()
+    if bias is not None:
+        for g, (lo, hi) in enumerate(zip(ends, ends[1:])):
+            ref[lo:hi] += bias[g].double()
     assert_epilogue(C, ref, epi[3])
 
 
-def test_rows_pairs_leave_other_rows_alone():
-    sizes, N, K = rs.ROWS_PAIRS[1]
+@pytest.mark.parametrize("sizes,N,K", [rs.ROWS_PAIRS[1], rs.ROWS_PAIRS_F32[0]])
+def test_rows_leave_other_rows_alone(sizes, N, K):
     M = 7 + sum(sizes) + 300
     old = rand((M, N), torch.float32, 9)
     C, A, B, ends = run_rows(sizes, N, K, F32, start=7, extra=300, fill=old, beta=1.0)

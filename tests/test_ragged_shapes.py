@@ -35,7 +35,14 @@ def test_lora_panels(probe, shape, bf16, f16):  # noqa: F811
         assert -(-M // rows) == want
 
 
-def test_rows(probe):  # noqa: F811
+W16, R16, W32, E32, R32 = range(5)  # RaggedOut
+
+
+def rows(limits, sizes, N, K, out):  # noqa: F811
+    return limits("rows", len(sizes), sum(sizes), N, blocks(K), SMS, out)
+
+
+def test_rows(probe, limits):  # noqa: F811
     def plan(sizes, N, K):
         return probe("grouped", len(sizes), sum(sizes), N, blocks(K), SMS)
 
@@ -49,12 +56,16 @@ def test_rows(probe):  # noqa: F811
     for s in rs.ROWS_SINGLE:
         assert plan(*s) == (1, 128, 1)
     assert any(blocks(s[2]) > FOLD for s in rs.ROWS_SINGLE)
+    for s in rs.ROWS_PAIRS_F32:
+        assert rows(limits, *s, W32) == rows(limits, *s, E32) == 2 and blocks(s[2]) > FOLD
+    for s in rs.ROWS_PAIRS_F32[1:]:
+        assert rows(limits, *s, R32) == 2
+    assert rows(limits, *rs.ROWS_PAIRS_F32[0], R32) == 1
+    for s in rs.ROWS_PAIRS:
+        assert [rows(limits, *s, out) for out in range(5)] == [2, 2, 2, 1, 1]
     for sizes, N, K, split in rs.ROWS_SPLIT:
         assert plan(sizes, N, K) == (1, 128, split)
     assert any(blocks(s[2]) > FOLD * s[3] for s in rs.ROWS_SPLIT)
-
-
-W16, R16, W32, E32, R32 = range(5)  # RaggedOut
 
 
 def depth(limits, sizes, M, N, out):  # noqa: F811
@@ -74,6 +85,16 @@ def test_depth(limits):  # noqa: F811
     for s in rs.DEPTH_SINGLE:
         assert {depth(limits, *s, out) for out in range(5)} == {1}
         assert max(s[0]) > 64 * FOLD
+
+
+@pytest.mark.parametrize("G,M,N,num_kb,want", [
+    # as below, for gemm_grouped
+    (64, 49152, 2816, 32, (2, 2, 2, 2, 1)), (8, 16384, 4096, 64, (2, 2, 2, 2, 2)),
+    (16, 4096, 2048, 22, (2, 2, None, 1, 1)), (64, 8192, 1408, 32, (None, 2, None, 1, 1)),
+])
+def test_rows_take_what_was_faster(limits, G, M, N, num_kb, want):  # noqa: F811
+    for out, cg in enumerate(want):
+        assert cg in (None, limits("rows", G, M, N, num_kb, SMS, out)), out
 
 
 @pytest.mark.parametrize("G,M,N,avg,want", [
