@@ -58,7 +58,10 @@ OUT_TYPE = {GEMM_F32: "f32", GEMM_F16_F32: "f32", GEMM_BF16_F32: "f32",
             GEMM_F16_F16: "f16", GEMM_BF16_BF16: "bf16"}
 
 EXPORTS = ("gemm", "gemm_ex", "gemm_host", "gemm_noalloc", "gemm_tune", "gemm_tune_reset",
-           "softmax_rows", "gemm_grouped", "gemm_grouped_k", "gemm_lora", "gemm_strerror", "gemm_check_device_error", "gemm_device_checks",
+           "softmax_rows", "gemm_grouped", "gemm_grouped_k", "gemm_lora",
+           "gemm_xent", "gemm_xent_grad", "layernorm_rows", "layernorm_rows_grad", "embed_rows",
+           "embed_rows_grad", "router_balance", "router_balance_grad",
+           "gemm_strerror", "gemm_check_device_error", "gemm_device_checks",
            "gemm_release_workspace", "gemm_launch_count", "gemm_set_option", "gemm_get_option")
 
 _lock = threading.Lock()
@@ -104,6 +107,21 @@ def load(path: str = LIB_PATH):
         lib.gemm_lora.restype = ci
         lib.gemm_lora.argtypes = [i64] * 5 + [vp, i64, vp, i64, ci, vp, vp, vp, vp, vp, i64, ci,
                                               epi, vp]
+        f32 = ctypes.c_float
+        for name, types in (
+                ("gemm_xent", [i64] * 3 + [vp, i64, vp, i64, vp, vp, vp, ci, vp]),
+                ("gemm_xent_grad", [i64] * 3 + [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64,
+                                                f32, f32, ci, vp]),
+                ("layernorm_rows", [i64] * 2 + [vp, i64, vp, vp, f32, vp, i64, vp, vp, ci, vp]),
+                ("layernorm_rows_grad", [i64] * 2 + [vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp,
+                                                     f32, ci, vp]),
+                ("embed_rows", [i64] * 3 + [vp, vp, i64, f32, vp, i64, ci, vp]),
+                ("embed_rows_grad", [i64] * 3 + [vp, vp, i64, f32, vp, i64, f32, ci, vp]),
+                ("router_balance", [i64] * 3 + [vp, i64, vp, vp, vp, vp, vp, ci, vp]),
+                ("router_balance_grad", [i64] * 3 + [vp, i64, vp, vp, vp, vp, i64, f32, f32, ci,
+                                                     vp])):
+            f = getattr(lib, name)
+            f.restype, f.argtypes = ci, types
         lib.gemm_strerror.restype, lib.gemm_strerror.argtypes = ctypes.c_char_p, [ci]
         lib.gemm_check_device_error.restype = ci
         lib.gemm_check_device_error.argtypes = [vp]
@@ -242,6 +260,68 @@ def gemm_lora(M, N, K, L, R, A, lda, B, ldb, b_major, adapter, lora_a, lora_b, s
     return load().gemm_lora(M, N, K, L, R, _ptr(A), lda, _ptr(B), ldb, b_major, _ptr(adapter),
                             _ptr(lora_a), _ptr(lora_b), _ptr(scale), _ptr(C), ldc, dtype,
                             _epilogue(alpha, beta, bias, activation), _stream(stream))
+
+
+def gemm_xent(M, N, K, X, ldx, W, ldw, target, loss, lse, dtype, stream=None) -> int:
+    """loss[t] = lse[t] - (X W^T)[t][target[t]] with lse = log sum exp over the N columns,
+    which are never stored; see include/gemm.h."""
+    return load().gemm_xent(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _ptr(target), _ptr(loss),
+                            _ptr(lse), dtype, _stream(stream))
+
+
+def gemm_xent_grad(M, N, K, X, ldx, W, ldw, target, lse, dloss, dX, lddx, dW, lddw, dtype,
+                   alpha=1.0, beta=0.0, stream=None) -> int:
+    """dX = G W, dW = beta * dW + G^T X with G = alpha * dloss[t] * (softmax - one at the
+    target), from gemm_xent's lse; see include/gemm.h."""
+    return load().gemm_xent_grad(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _ptr(target), _ptr(lse),
+                                 _ptr(dloss), _ptr(dX), lddx, _ptr(dW), lddw, alpha, beta, dtype,
+                                 _stream(stream))
+
+
+def layernorm_rows(M, N, x, ldx, weight, bias, eps, y, ldy, mean, rstd, dtype,
+                   stream=None) -> int:
+    """y = (x - mean) * rstd * weight + bias of every row; see include/gemm.h."""
+    return load().layernorm_rows(M, N, _ptr(x), ldx, _ptr(weight), _ptr(bias), eps, _ptr(y), ldy,
+                                 _ptr(mean), _ptr(rstd), dtype, _stream(stream))
+
+
+def layernorm_rows_grad(M, N, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, dweight, dbias,
+                        dtype, beta=0.0, stream=None) -> int:
+    """layernorm_rows' dx, and beta * (dweight, dbias) plus theirs; see include/gemm.h."""
+    return load().layernorm_rows_grad(M, N, _ptr(x), ldx, _ptr(weight), _ptr(mean), _ptr(rstd),
+                                      _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dweight), _ptr(dbias),
+                                      beta, dtype, _stream(stream))
+
+
+def embed_rows(M, V, K, ids, table, ldt, y, ldy, dtype, scale=1.0, stream=None) -> int:
+    """y[t] = scale * table[ids[t]], zeros where ids[t] is negative; see include/gemm.h."""
+    return load().embed_rows(M, V, K, _ptr(ids), _ptr(table), ldt, scale, _ptr(y), ldy, dtype,
+                             _stream(stream))
+
+
+def embed_rows_grad(M, V, K, ids, dy, lddy, dtable, lddt, dtype, scale=1.0, beta=0.0,
+                    stream=None) -> int:
+    """dtable[v] = beta * dtable[v] + scale * the sum of dy[t] over ids[t] == v; see
+    include/gemm.h."""
+    return load().embed_rows_grad(M, V, K, _ptr(ids), _ptr(dy), lddy, scale, _ptr(dtable), lddt,
+                                  beta, dtype, _stream(stream))
+
+
+def router_balance(T, E, top, logits, ldl, expert, counts, offsets, prob, loss, dtype,
+                   stream=None) -> int:
+    """The experts' counts and group limits, mean probabilities and balance loss of a
+    router's choices; see include/gemm.h."""
+    return load().router_balance(T, E, top, _ptr(logits), ldl, _ptr(expert), _ptr(counts),
+                                 _ptr(offsets), _ptr(prob), _ptr(loss), dtype, _stream(stream))
+
+
+def router_balance_grad(T, E, top, logits, ldl, expert, counts, dloss, dlogits, lddl, dtype,
+                        alpha=1.0, beta=0.0, stream=None) -> int:
+    """dlogits = beta * dlogits + alpha * dloss times the balance loss's gradient; see
+    include/gemm.h."""
+    return load().router_balance_grad(T, E, top, _ptr(logits), ldl, _ptr(expert), _ptr(counts),
+                                      _ptr(dloss), _ptr(dlogits), lddl, alpha, beta, dtype,
+                                      _stream(stream))
 
 
 def gemm_strerror(status: int) -> str:

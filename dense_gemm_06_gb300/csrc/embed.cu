@@ -1,0 +1,585 @@
+// embed.cu -- embed_rows() and embed_rows_grad().
+//
+//   y_t = scale table[id_t]           (zeros where id_t is negative)
+//   dtable_v = beta dtable_v + scale sum over the t with id_t = v of dy_t
+//
+// Both are bound by memory. The gradient sorts the tokens (a row of the table is
+// then one run of the sorted list), so that every row of the table is written
+// once, by one block, and its terms are added in the order of t: no atomics, and
+// results that do not depend on timing.
+//
+// Sort: the 64-bit number (token, t) is unique, so its place in the sorted list is
+// a count of smaller ones. Blocks sort 2048 numbers each in shared memory; then
+// eight runs at a time are merged, every number finding its place among the seven
+// other runs by binary search. 65536 tokens take three launches.
+//
+// Sums: the sorted list is cut into chunks of equal length, so that a frequent
+// token's rows are shared by many blocks. A block adds up the runs within its
+// chunk; a run that crosses chunks leaves one partial sum in each, which a last
+// kernel adds in the order of the chunks.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm.h"
+#include "internal.h"
+#include "policy.h"
+#include "rows.cuh"
+
+namespace libgemm {
+namespace {
+
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// G elements of a row, from any alignment: the one or two aligned 16-byte (or
+// smaller) pieces that hold them, shifted together. The second piece is read only
+// when it holds one of them.
+template <typename T, int G>
+__device__ __forceinline__ void load_group(const T* p, float (&out)[G]) {
+    constexpr int BYTES = G * (int)sizeof(T);  // 4, 8 or 16
+    constexpr int WORDS = BYTES / 4;
+    static_assert(BYTES == 8 || BYTES == 16, "whole words");
+    struct alignas(BYTES) Piece { uint32_t w[WORDS]; };
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t off = (uint32_t)(at % BYTES);
+    const Piece* from = reinterpret_cast<const Piece*>(at - off);
+    uint32_t w[2 * WORDS];
+    const Piece a = from[0];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = a.w[i];
+    if (off) {
+        const Piece b = from[1];
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[WORDS + i] = b.w[i];
+        uint32_t r[WORDS];
+        const uint32_t skip = off / 4, bits = off % 4 * 8;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) {
+                if (skip == (uint32_t)k) lo = w[i + k];
+                if (skip == (uint32_t)k && i + k + 1 < 2 * WORDS) hi = w[i + k + 1];
+            }
+            r[i] = __funnelshift_r(lo, hi, bits);
+        }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = r[i];
+    }
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) out[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const uint16_t h = (uint16_t)(w[i / 2] >> (i % 2 * 16));
+            out[i] = to_f32(*reinterpret_cast<const T*>(&h));
+        }
+    }
+}
+
+// G elements to a row at `p`, in one store where that is aligned.
+template <typename T, int G>
+__device__ __forceinline__ void store_group(T* p, const float (&v)[G]) {
+    alignas(16) T o[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) o[i] = from_f32<T>(v[i]);
+    constexpr int BYTES = G * (int)sizeof(T);
+    if (reinterpret_cast<uintptr_t>(p) % (BYTES < 16 ? BYTES : 16) == 0) {
+        if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(o);
+#pragma unroll
+        for (int j = 0; j < BYTES / 16; ++j)
+            reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<uint4*>(o)[j];
+    } else {
+#pragma unroll
+        for (int i = 0; i < G; ++i) p[i] = o[i];
+    }
+}
+
+struct EmbedArgs {
+    int64_t M, V, K;
+    const int32_t* ids;
+    const void* table;
+    int64_t ldt;
+    float scale;
+    void* y;
+    int64_t ldy;
+    ErrWord* err;
+};
+
+// One row for each `threads` threads of a block; a thread takes groups of G
+// elements that are aligned in y, and the first threads the row's loose ends.
+constexpr int kEmbedRows = 4;  // rows in flight in a thread
+template <typename T, typename O>
+__global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int threads) {
+    gemm_ptx::pdl_launch_dependents();
+    constexpr int G = 16 / (int)sizeof(O) < 16 / (int)sizeof(T) ? 16 / (int)sizeof(O)
+                                                                : 16 / (int)sizeof(T);
+    const int lanes = blockDim.x / threads;
+    const int tid = threadIdx.x % threads;
+    const int64_t step = (int64_t)gridDim.x * lanes;
+    gemm_ptx::pdl_wait();
+    for (int64_t t0 = (int64_t)blockIdx.x * lanes + threadIdx.x / threads; t0 < a.M;
+         t0 += step * kEmbedRows) {
+        const T* from[kEmbedRows];
+        O* to[kEmbedRows];
+        int head[kEmbedRows];
+#pragma unroll
+        for (int j = 0; j < kEmbedRows; ++j) {
+            const int64_t t = t0 + j * step;
+            from[j] = nullptr;
+            to[j] = nullptr;
+            head[j] = 0;
+            if (t >= a.M) continue;
+            const int id = a.ids[t];
+            if (id >= a.V && tid == 0) report_bad_value(a.err);
+            if (id >= 0 && id < a.V) from[j] = static_cast<const T*>(a.table) + id * a.ldt;
+            to[j] = static_cast<O*>(a.y) + t * a.ldy;
+            const int past = (int)(reinterpret_cast<uintptr_t>(to[j]) % (G * sizeof(O))) /
+                             (int)sizeof(O);
+            head[j] = past ? G - past : 0;
+            if (head[j] > a.K) head[j] = (int)a.K;
+        }
+        for (int64_t c = (int64_t)tid * G; c < a.K; c += (int64_t)threads * G) {
+            float v[kEmbedRows][G];
+#pragma unroll
+            for (int j = 0; j < kEmbedRows; ++j) {
+#pragma unroll
+                for (int e = 0; e < G; ++e) v[j][e] = 0.f;
+                if (from[j] && c + head[j] + G <= a.K) load_group<T, G>(from[j] + c + head[j], v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kEmbedRows; ++j) {
+                if (!to[j] || c + head[j] + G > a.K) continue;
+#pragma unroll
+                for (int e = 0; e < G; ++e) v[j][e] *= a.scale;
+                store_group<O, G>(to[j] + c + head[j], v[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kEmbedRows; ++j) {
+            if (!to[j]) continue;
+            const int64_t tail = head[j] + (a.K - head[j]) / G * G;
+            for (int64_t i = tid; i < head[j] + (a.K - tail); i += threads) {
+                const int64_t c = i < head[j] ? i : tail + (i - head[j]);
+                to[j][c] = from_f32<O>(from[j] ? a.scale * to_f32(from[j][c]) : 0.f);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ sort --
+// The number of a token: its row of the table above its place in the list;
+// tokens that do not count come last.
+constexpr int kTile = 2048;      // numbers that a block sorts
+constexpr int kMerge = 8;        // runs merged in one pass
+constexpr uint32_t kNone = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t token_of(uint64_t x) { return (uint32_t)(x >> 32); }
+
+__global__ void __launch_bounds__(1024)
+    sort_tiles_kernel(const int32_t* __restrict__ ids, int64_t M, int64_t V,
+                      uint64_t* __restrict__ out, ErrWord* err) {
+    gemm_ptx::pdl_launch_dependents();
+    __shared__ uint64_t x[kTile];
+    gemm_ptx::pdl_wait();
+    const int64_t base = (int64_t)blockIdx.x * kTile;
+    const int n = M - base < kTile ? (int)(M - base) : kTile;
+    for (int i = threadIdx.x; i < kTile; i += 1024) {
+        uint64_t v = ~0ull;
+        if (i < n) {
+            const int id = ids[base + i];
+            if (id >= V) report_bad_value(err);
+            v = ((uint64_t)(id >= 0 && id < V ? (uint32_t)id : kNone) << 32) | (uint32_t)(base + i);
+        }
+        x[i] = v;
+    }
+    int size = 2;
+    while (size < n) size *= 2;  // of the numbers to sort
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            __syncthreads();
+            const int i = threadIdx.x;  // a pair for each thread
+            const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+            if (hi < size) {
+                const uint64_t a = x[lo], b = x[hi];
+                if ((a > b) == ((lo & k) == 0)) {
+                    x[lo] = b;
+                    x[hi] = a;
+                }
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 1024) out[base + i] = x[i];
+}
+
+__global__ void __launch_bounds__(256)
+    sort_merge_kernel(const uint64_t* __restrict__ in, uint64_t* __restrict__ out, int64_t M,
+                      int64_t run) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M) return;
+    const uint64_t x = in[i];
+    const int64_t own = i / run, first = own / kMerge * kMerge;
+    int64_t lo[kMerge], hi[kMerge];
+#pragma unroll
+    for (int r = 0; r < kMerge; ++r) {
+        lo[r] = (first + r) * run;
+        hi[r] = lo[r] + run;
+        if (lo[r] > M) lo[r] = M;
+        if (hi[r] > M) hi[r] = M;
+        if (first + r == own) lo[r] = hi[r] = i;  // its place in its own run
+    }
+    // The binary searches step by step side by side.
+    for (int64_t width = run; width > 0; width /= 2)
+#pragma unroll
+        for (int r = 0; r < kMerge; ++r)
+            if (lo[r] < hi[r]) {
+                const int64_t mid = lo[r] + (hi[r] - lo[r]) / 2;
+                if (in[mid] < x) lo[r] = mid + 1;
+                else hi[r] = mid;
+            }
+    int64_t at = first * run;
+#pragma unroll
+    for (int r = 0; r < kMerge; ++r) {
+        const int64_t begin = (first + r) * run;
+        if (begin < M) at += lo[r] - begin;
+    }
+    out[at] = x;
+}
+
+// ------------------------------------------------------------------ sums --
+struct EmbedGradArgs {
+    int64_t M, V, K;
+    const uint64_t* sorted;
+    const void* dy;
+    int64_t lddy;
+    float scale, beta;
+    void* dtable;
+    int64_t lddt;
+    float* part;      // chunks x 2 x kp: a crossing run's sum at the chunk's begin, and at its end
+    int64_t kp;       // K rounded up to whole groups
+    int chunk;        // sorted numbers of a chunk
+    int chunks;
+    int col_blocks;   // blocks that share a chunk's columns
+    int64_t sum_blocks;
+};
+
+constexpr int kSumThreads = 128;
+constexpr int kFillRows = 32;     // rows of the table that a block looks after
+
+// The first place of the sorted list whose token is not below `token`.
+__device__ __forceinline__ int64_t first_at(const uint64_t* sorted, int64_t M, uint64_t token) {
+    int64_t lo = 0, hi = M;
+    const uint64_t x = token << 32;
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (sorted[mid] < x) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <typename O, int G>
+__device__ __forceinline__ void write_sum(const EmbedGradArgs& a, uint32_t token, int64_t c,
+                                          const float (&sum)[G]) {
+    O* at = static_cast<O*>(a.dtable) + (int64_t)token * a.lddt + c;
+    if (c + G <= a.K) {
+        float v[G];
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+            v[e] = a.beta != 0.f ? fmaf(a.beta, to_f32(at[e]), a.scale * sum[e])
+                                 : a.scale * sum[e];
+        store_group<O, G>(at, v);
+    } else {
+        for (int e = 0; e < G; ++e)
+            if (c + e < a.K)
+                at[e] = from_f32<O>(a.beta != 0.f
+                                        ? fmaf(a.beta, to_f32(at[e]), a.scale * sum[e])
+                                        : a.scale * sum[e]);
+    }
+}
+
+// The first a.sum_blocks blocks add up chunks; the others look after the rows of
+// the table that no token names (zeros, or beta times what they hold).
+template <typename T, typename O>
+__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    constexpr int G = 16 / (int)sizeof(T);
+    __shared__ uint32_t named;
+    __shared__ int64_t range[2];
+    gemm_ptx::pdl_wait();
+    if (blockIdx.x < a.sum_blocks) {
+        const int64_t chunk = blockIdx.x / a.col_blocks;
+        const int64_t c = ((int64_t)(blockIdx.x % a.col_blocks) * kSumThreads + threadIdx.x) * G;
+        if (c >= a.K) return;
+        const int64_t p0 = chunk * a.chunk;
+        const int64_t p1 = p0 + a.chunk < a.M ? p0 + a.chunk : a.M;
+        const uint32_t before = p0 > 0 ? token_of(a.sorted[p0 - 1]) : kNone;
+        const uint32_t after = p1 < a.M ? token_of(a.sorted[p1]) : kNone;
+        const bool whole = c + G <= a.K;
+        float sum[G] = {};
+        uint32_t token = token_of(a.sorted[p0]);
+        bool crossing = p0 > 0 && before == token;  // the run began in an earlier chunk
+        constexpr int AHEAD = 4;
+        for (int64_t p = p0; p < p1; p += AHEAD) {
+            uint32_t tok[AHEAD];
+            float v[AHEAD][G];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                tok[j] = kNone;
+                if (p + j >= p1) continue;
+                const uint64_t x = a.sorted[p + j];
+                tok[j] = token_of(x);
+                if (tok[j] == kNone) continue;
+                const T* row = static_cast<const T*>(a.dy) + (int64_t)(uint32_t)x * a.lddy + c;
+                if (whole) {
+                    load_group<T, G>(row, v[j]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < G; ++e) v[j][e] = c + e < a.K ? to_f32(row[e]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                if (p + j >= p1) continue;
+                if (tok[j] != token) {  // the run before ends here
+                    if (token != kNone) {
+                        if (crossing) {
+                            float* to = a.part + chunk * 2 * a.kp + c;
+#pragma unroll
+                            for (int e = 0; e < G; ++e) to[e] = sum[e];
+                        } else {
+                            write_sum<O, G>(a, token, c, sum);
+                        }
+                    }
+                    token = tok[j];
+                    crossing = false;
+#pragma unroll
+                    for (int e = 0; e < G; ++e) sum[e] = 0.f;
+                }
+                if (token != kNone) {
+#pragma unroll
+                    for (int e = 0; e < G; ++e) sum[e] += v[j][e];
+                }
+            }
+        }
+        if (token == kNone) return;
+        const bool goes_on = p1 < a.M && after == token;
+        if (crossing || goes_on) {
+            float* to = a.part + (chunk * 2 + (crossing ? 0 : 1)) * a.kp + c;
+#pragma unroll
+            for (int e = 0; e < G; ++e) to[e] = sum[e];
+        } else {
+            write_sum<O, G>(a, token, c, sum);
+        }
+        return;
+    }
+    // Rows without a token: which of these kFillRows have one stands in the sorted
+    // list between the places of the first and the last.
+    const int64_t v0 = (int64_t)(blockIdx.x - a.sum_blocks) * kFillRows;
+    const int rows = a.V - v0 < kFillRows ? (int)(a.V - v0) : kFillRows;
+    if (threadIdx.x == 0) named = 0;
+    if (threadIdx.x < 2) range[threadIdx.x] = first_at(a.sorted, a.M, v0 + threadIdx.x * rows);
+    __syncthreads();
+    for (int64_t p = range[0] + threadIdx.x; p < range[1]; p += kSumThreads) {
+        const uint32_t bit = 1u << (token_of(a.sorted[p]) - (uint32_t)v0);
+        if (!(named & bit)) atomicOr(&named, bit);
+    }
+    __syncthreads();
+    constexpr int GO = 16 / (int)sizeof(O);
+    for (int r = 0; r < rows; ++r) {
+        if (named >> r & 1) continue;
+        O* row = static_cast<O*>(a.dtable) + (v0 + r) * a.lddt;
+        if (a.beta != 0.f) {
+            for (int64_t c = threadIdx.x; c < a.K; c += kSumThreads)
+                row[c] = from_f32<O>(a.beta * to_f32(row[c]));
+            continue;
+        }
+        const int past = (int)(reinterpret_cast<uintptr_t>(row) % 16) / (int)sizeof(O);
+        int64_t head = past ? GO - past : 0;
+        if (head > a.K) head = a.K;
+        const int64_t tail = head + (a.K - head) / GO * GO;
+        for (int64_t c = head + (int64_t)threadIdx.x * GO; c < tail; c += kSumThreads * GO)
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+        for (int64_t i = threadIdx.x; i < head + (a.K - tail); i += kSumThreads)
+            row[i < head ? i : tail + (i - head)] = from_f32<O>(0.f);
+    }
+}
+
+// A run that crosses chunks: the block of the chunk where it begins adds its
+// partial sums in order.
+template <typename T, typename O>
+__global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGradArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    constexpr int G = 16 / (int)sizeof(T);
+    gemm_ptx::pdl_wait();
+    const int64_t chunk = blockIdx.x / a.col_blocks;
+    const int64_t c = ((int64_t)(blockIdx.x % a.col_blocks) * kSumThreads + threadIdx.x) * G;
+    const int64_t p0 = chunk * a.chunk, p1 = p0 + a.chunk;
+    if (c >= a.K || p1 >= a.M) return;
+    const uint32_t token = token_of(a.sorted[p1 - 1]);
+    if (token == kNone || token_of(a.sorted[p1]) != token) return;   // no run goes on
+    if (p0 > 0 && token_of(a.sorted[p0 - 1]) == token &&
+        token_of(a.sorted[p0]) == token) return;                     // it began earlier
+    const int64_t end = first_at(a.sorted, a.M, (uint64_t)token + 1);
+    const int64_t last = (end - 1) / a.chunk;
+    float sum[G];
+    const float* from = a.part + (chunk * 2 + 1) * a.kp + c;
+#pragma unroll
+    for (int e = 0; e < G; ++e) sum[e] = from[e];
+#pragma unroll 4
+    for (int64_t k = chunk + 1; k <= last; ++k) {
+        const float* more = a.part + k * 2 * a.kp + c;
+#pragma unroll
+        for (int e = 0; e < G; ++e) sum[e] += more[e];
+    }
+    write_sum<O, G>(a, token, c, sum);
+}
+
+bool rows_ok(const void* p, int64_t rows, int64_t K, int64_t ld, int es) {
+    return p && aligned_to(p, es) && ld >= K &&
+           (__int128)(rows - 1) * ld + K <= (__int128)(INT64_MAX / es);
+}
+
+int embed(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* table, int64_t ldt,
+          float scale, void* y, int64_t ldy, int dtype, cudaStream_t s) {
+    if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
+    if (M < 0 || V < 0 || K < 0 || M > INT32_MAX || V > INT32_MAX || K > INT32_MAX)
+        return kInvalidArg;
+    if (M == 0 || K == 0) return kOk;
+    const int ts = dtype == GEMM_F32 ? 4 : 2, os = dtype <= GEMM_BF16_F32 ? 4 : 2;
+    if (!ids || !aligned_to(ids, 4) || !rows_ok(y, M, K, ldy, os)) return kInvalidArg;
+    if (V > 0 && !rows_ok(table, V, K, ldt, ts)) return kInvalidArg;
+    DeviceInfo* dev = nullptr;
+    int rc = current_device_info(&dev, nullptr);
+    if (rc != kOk) return rc;
+    const void* ptrs[3] = {ids, V > 0 ? table : nullptr, y};
+    rc = check_device_pointers(ptrs, 3, dev->device);
+    if (rc != kOk) return rc;
+    const EmbedArgs a{M, V, K, ids, table, ldt, scale, y, ldy, dev->err_word};
+    int threads = 32;  // of a row: 8 elements each, as near as a block has
+    while (threads < 256 && threads * 8 < K) threads *= 2;
+    const int64_t blocks = (M + 256 / threads - 1) / (256 / threads);
+    const int64_t most = (int64_t)dev->sm_count * 8;
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    auto run = [&](auto kern) { return launch_dependent(kern, grid, dim3(256), 0, s, a, threads); };
+    switch (dtype) {
+        case GEMM_F32: return run(embed_kernel<float, float>);
+        case GEMM_F16_F32: return run(embed_kernel<__half, float>);
+        case GEMM_BF16_F32: return run(embed_kernel<__nv_bfloat16, float>);
+        case GEMM_F16_F16: return run(embed_kernel<__half, __half>);
+        default: return run(embed_kernel<__nv_bfloat16, __nv_bfloat16>);
+    }
+}
+
+int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* dy, int64_t lddy,
+               float scale, void* dtable, int64_t lddt, float beta, int dtype, cudaStream_t s) {
+    if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
+    if (M < 0 || V < 0 || K < 0 || M > INT32_MAX || V > INT32_MAX || K > INT32_MAX)
+        return kInvalidArg;
+    if (V == 0 || K == 0) return kOk;
+    const int ts = dtype == GEMM_F32 ? 4 : 2, os = dtype <= GEMM_BF16_F32 ? 4 : 2;
+    if (!rows_ok(dtable, V, K, lddt, os)) return kInvalidArg;
+    if (M > 0 && (!ids || !aligned_to(ids, 4) || !rows_ok(dy, M, K, lddy, ts))) return kInvalidArg;
+    if (M == 0 && beta == 1.f) return kOk;
+    DeviceInfo* dev = nullptr;
+    cudaMemPool_t pool = nullptr;
+    int rc = current_device_info(&dev, &pool);
+    if (rc != kOk) return rc;
+    const void* ptrs[3] = {M > 0 ? ids : nullptr, M > 0 ? dy : nullptr, dtable};
+    rc = check_device_pointers(ptrs, 3, dev->device);
+    if (rc != kOk) return rc;
+
+    EmbedGradArgs a{};
+    a.M = M;
+    a.V = V;
+    a.K = K;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.scale = scale;
+    a.beta = beta;
+    a.dtable = dtable;
+    a.lddt = lddt;
+    const int group = 16 / ts;
+    a.kp = up(K, 16);
+    a.chunk = embed_chunk(M);
+    a.chunks = (int)((M + a.chunk - 1) / a.chunk);
+    a.col_blocks = (int)((K + (int64_t)group * kSumThreads - 1) / ((int64_t)group * kSumThreads));
+    a.sum_blocks = (int64_t)a.chunks * a.col_blocks;
+    const int64_t fill = beta == 1.f ? 0 : (V + kFillRows - 1) / kFillRows;
+    if (a.sum_blocks + fill > INT32_MAX) return kUnsupported;
+    Scratch scratch{pool, s, dev->device};
+    const int64_t list = up(M * 8, 256);
+    char* mem = nullptr;
+    if (M > 0) {
+        mem = static_cast<char*>(scratch.get((size_t)(2 * list + (int64_t)a.chunks * 2 * a.kp * 4)));
+        if (!mem) return kCuda;
+        uint64_t* in = reinterpret_cast<uint64_t*>(mem);
+        uint64_t* out = reinterpret_cast<uint64_t*>(mem + list);
+        rc = launch_dependent(sort_tiles_kernel, dim3((unsigned)((M + kTile - 1) / kTile)),
+                              dim3(1024), 0, s, ids, M, V, in, dev->err_word);
+        for (int64_t run = kTile; rc == kOk && run < M; run *= kMerge) {
+            rc = launch_dependent(sort_merge_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256),
+                                  0, s, (const uint64_t*)in, out, M, run);
+            std::swap(in, out);
+        }
+        a.sorted = in;
+        a.part = reinterpret_cast<float*>(mem + 2 * list);
+    }
+    auto run = [&](auto sum, auto cross) {
+        int r = rc;
+        if (r == kOk && a.sum_blocks + fill > 0)
+            r = launch_dependent(sum, dim3((unsigned)(a.sum_blocks + fill)), dim3(kSumThreads), 0,
+                                 s, a);
+        if (r == kOk && a.chunks > 1)
+            r = launch_dependent(cross, dim3((unsigned)a.sum_blocks), dim3(kSumThreads), 0, s, a);
+        return r;
+    };
+    switch (dtype) {
+        case GEMM_F32: rc = run(embed_sum_kernel<float, float>, embed_cross_kernel<float, float>); break;
+        case GEMM_F16_F32: rc = run(embed_sum_kernel<__half, float>, embed_cross_kernel<__half, float>); break;
+        case GEMM_BF16_F32:
+            rc = run(embed_sum_kernel<__nv_bfloat16, float>, embed_cross_kernel<__nv_bfloat16, float>);
+            break;
+        case GEMM_F16_F16: rc = run(embed_sum_kernel<__half, __half>, embed_cross_kernel<__half, __half>); break;
+        default:
+            rc = run(embed_sum_kernel<__nv_bfloat16, __nv_bfloat16>,
+                     embed_cross_kernel<__nv_bfloat16, __nv_bfloat16>);
+            break;
+    }
+    scratch.release();
+    return rc;
+}
+
+}  // namespace
+}  // namespace libgemm
+
+using namespace libgemm;
+
+extern "C" {
+
+int embed_rows(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* table, int64_t ldt,
+               float scale, void* y, int64_t ldy, int dtype, void* stream) {
+    try {
+        return embed(M, V, K, ids, table, ldt, scale, y, ldy, dtype,
+                     static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+int embed_rows_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* dy,
+                    int64_t lddy, float scale, void* dtable, int64_t lddt, float beta, int dtype,
+                    void* stream) {
+    try {
+        return embed_grad(M, V, K, ids, dy, lddy, scale, dtable, lddt, beta, dtype,
+                          static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,606 @@
+// layernorm.cu -- layernorm_rows() and layernorm_rows_grad().
+//
+//   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+//   xhat = (x - mean) rstd,  y = xhat weight + bias
+//   g = dy weight,  dx = rstd (g - sum g / N - xhat sum (g xhat) / N)
+//   dweight = sum over rows of dy xhat,  dbias = sum over rows of dy
+//
+// Both are bound by memory. Forward: a row sits in the registers of one warp (or
+// 4 or 16 warps), so x is read once, and the squares are summed around the mean,
+// not as a difference of large sums. Backward: a thread owns 16 columns and walks
+// down the rows of its block with 32 running sums in registers, so x and dy are
+// read once for dx, dweight and dbias together; the blocks' sums, N numbers each,
+// are added by a second kernel in the order of the blocks, so results do not
+// depend on timing.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm.h"
+#include "internal.h"
+#include "policy.h"
+#include "rows.cuh"
+
+namespace libgemm {
+namespace {
+
+// VEC elements at once (16 bytes of them, or one).
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+// VEC numbers from `p` (VEC > 1: 16-byte aligned), or `other` where p is null.
+template <typename W, int VEC>
+__device__ __forceinline__ void load_weights(const W* p, int64_t at, float other,
+                                             float (&out)[VEC]) {
+    constexpr int PER = VEC == 1 ? 1 : 16 / (int)sizeof(W);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = other;
+    if (!p) return;
+#pragma unroll
+    for (int j = 0; j < VEC; j += PER) {
+        const Pack<W, PER> k = *reinterpret_cast<const Pack<W, PER>*>(p + at + j);
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (j + e < VEC) out[j + e] = to_f32(k.v[e]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums over the WARPS warps that share a row (a whole block when WARPS > 1);
+// `slots` holds WARPS x K numbers, and every use of it is one barrier apart from
+// the next use of the same half.
+template <int WARPS, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float* slots) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+    if constexpr (WARPS > 1) {
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) slots[w * K + k] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float t = lane < WARPS ? slots[lane * K + k] : 0.f;
+#pragma unroll
+            for (int o = (WARPS > 16 ? 32 : WARPS) / 2; o; o >>= 1)
+                t += __shfl_xor_sync(0xffffffffu, t, o);
+            v[k] = __shfl_sync(0xffffffffu, t, 0);
+        }
+    }
+}
+
+struct NormArgs {
+    int64_t M;
+    int N;
+    const void* x;
+    int64_t ldx;
+    const void* weight;  // null: ones
+    const void* bias;    // null: zeros
+    float eps;
+    void* y;
+    int64_t ldy;
+    float* mean;  // null: not kept
+    float* rstd;
+};
+
+// A row for each WARPS warps; NV vectors of VEC elements in each thread. Blocks
+// of BLOCK threads hold BLOCK / (32 WARPS) rows.
+template <typename T, typename W, int WARPS, int NV, int VEC, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) norm_kernel(const NormArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    constexpr int TR = 32 * WARPS;  // threads of a row
+    __shared__ float slots[2][WARPS > 1 ? WARPS : 1];
+    const int tid = threadIdx.x % TR;
+    const int64_t row = (int64_t)blockIdx.x * (BLOCK / TR) + threadIdx.x / TR;
+    gemm_ptx::pdl_wait();
+    if (row >= a.M) return;  // a whole warp, or (WARPS > 1) a whole block
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    Pack<T, VEC> v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TR + tid) * VEC;
+        if (c < a.N) v[i] = *reinterpret_cast<const Pack<T, VEC>*>(x + c);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((i * TR + tid) * VEC < a.N) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[0] += to_f32(v[i].v[e]);
+        }
+    row_sum<WARPS, 1>(s, slots[0]);
+    const float mean = s[0] / (float)a.N;
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((i * TR + tid) * VEC < a.N) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float d = to_f32(v[i].v[e]) - mean;
+                s[0] = fmaf(d, d, s[0]);
+            }
+        }
+    row_sum<WARPS, 1>(s, slots[1]);
+    const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+    if (tid == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+    const W* weight = static_cast<const W*>(a.weight);
+    const W* bias = static_cast<const W*>(a.bias);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TR + tid) * VEC;
+        if (c >= a.N) continue;
+        float w[VEC], b[VEC];
+        load_weights<W, VEC>(weight, c, 1.f, w);
+        load_weights<W, VEC>(bias, c, 0.f, b);
+        Pack<T, VEC> o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            o.v[e] = from_f32<T>(fmaf((to_f32(v[i].v[e]) - mean) * rstd, w[e], b[e]));
+        *reinterpret_cast<Pack<T, VEC>*>(y + c) = o;
+    }
+}
+
+// Rows too long for the registers of a block: x is read three times (from L2
+// after the first).
+template <typename T, typename W>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    __shared__ float slots[2][32];
+    gemm_ptx::pdl_wait();
+    const W* weight = static_cast<const W*>(a.weight);
+    const W* bias = static_cast<const W*>(a.bias);
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+        T* y = static_cast<T*>(a.y) + row * a.ldy;
+        float s[1] = {0.f};
+        for (int64_t c = threadIdx.x; c < a.N; c += 1024) s[0] += to_f32(x[c]);
+        row_sum<32, 1>(s, slots[0]);
+        const float mean = s[0] / (float)a.N;
+        s[0] = 0.f;
+        for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
+            const float d = to_f32(x[c]) - mean;
+            s[0] = fmaf(d, d, s[0]);
+        }
+        row_sum<32, 1>(s, slots[1]);
+        const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
+            const float h = (to_f32(x[c]) - mean) * rstd;
+            const float w = weight ? to_f32(weight[c]) : 1.f;
+            y[c] = from_f32<T>(fmaf(h, w, bias ? to_f32(bias[c]) : 0.f));
+        }
+    }
+}
+
+struct NormGradArgs {
+    int64_t M;
+    int N;
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    const void* dy;
+    int64_t lddy;
+    void* dx;  // null: not wanted
+    int64_t lddx;
+    float* part;  // blocks x 2 x N sums, or null: not wanted
+};
+
+constexpr int kOwn = 16;  // columns of a thread in the backward kernel
+
+// A block of WARPS x LANES warps: LANES rows at a time, each on WARPS warps
+// (LANES > 1 only with one warp a row). Thread tid of a row owns the columns
+// (i TR + tid) VEC + e, i < kOwn / VEC.
+template <typename T, typename W, int WARPS, int LANES, int VEC>
+__global__ void __launch_bounds__(32 * WARPS * LANES)
+    norm_grad_kernel(const NormGradArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    constexpr int TR = 32 * WARPS, NV = kOwn / VEC;
+    __shared__ float slots[2][2 * WARPS];
+    __shared__ float merge[LANES > 1 ? (LANES - 1) * TR * 2 : 1];
+    const int tid = threadIdx.x % TR, sub = threadIdx.x / TR;
+    gemm_ptx::pdl_wait();
+    float w[kOwn];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = (i * TR + tid) * VEC + e;
+            w[i * VEC + e] =
+                c < a.N && a.weight ? to_f32(static_cast<const W*>(a.weight)[c]) : 1.f;
+        }
+    float dw[kOwn] = {}, db[kOwn] = {};
+    const float inv = 1.f / (float)a.N;
+    const int64_t step = (int64_t)gridDim.x * LANES;
+    int64_t row = (int64_t)blockIdx.x * LANES + sub;
+    Pack<T, VEC> xv[NV], gv[NV];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+        const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+        mean = a.mean[r];
+        rstd = a.rstd[r];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TR + tid) * VEC;
+            if (c < a.N) {
+                xv[i] = *reinterpret_cast<const Pack<T, VEC>*>(x + c);
+                gv[i] = *reinterpret_cast<const Pack<T, VEC>*>(dy + c);
+            }
+        }
+    };
+    if (row < a.M) fetch(row);
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+        float h[kOwn], g[kOwn], s[2] = {0.f, 0.f};
+        const float r = rstd;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (i * TR + tid) * VEC < a.N;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int k = i * VEC + e;
+                h[k] = in ? (to_f32(xv[i].v[e]) - mean) * r : 0.f;
+                const float d = in ? to_f32(gv[i].v[e]) : 0.f;
+                dw[k] = fmaf(d, h[k], dw[k]);
+                db[k] += d;
+                g[k] = d * w[k];
+                s[0] += g[k];
+                s[1] = fmaf(g[k], h[k], s[1]);
+            }
+        }
+        if (row + step < a.M) fetch(row + step);  // the next row's reads beside this one's sums
+        if (a.dx) {
+            row_sum<WARPS, 2>(s, slots[turn]);
+            const float c0 = s[0] * inv, c1 = s[1] * inv;
+            T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TR + tid) * VEC;
+                if (c >= a.N) continue;
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int k = i * VEC + e;
+                    o.v[e] = from_f32<T>(r * (g[k] - c0 - h[k] * c1));
+                }
+                *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o;
+            }
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = (i * TR + tid) * VEC + e;
+            float u = dw[i * VEC + e], v = db[i * VEC + e];
+            if constexpr (LANES > 1) {  // the block's rows, in the order of its warps
+                __syncthreads();
+                if (sub > 0) {
+                    merge[((sub - 1) * TR + tid) * 2] = u;
+                    merge[((sub - 1) * TR + tid) * 2 + 1] = v;
+                }
+                __syncthreads();
+                if (sub > 0) continue;
+#pragma unroll 1
+                for (int o = 0; o < LANES - 1; ++o) {
+                    u += merge[(o * TR + tid) * 2];
+                    v += merge[(o * TR + tid) * 2 + 1];
+                }
+            }
+            if (c < a.N) {
+                part[c] = u;
+                part[a.N + c] = v;
+            }
+        }
+}
+
+// Long rows, first pass: dx of a row per block; x and dy are read twice.
+template <typename T, typename W>
+__global__ void __launch_bounds__(1024) norm_grad_long_kernel(const NormGradArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    __shared__ float slots[2][64];
+    gemm_ptx::pdl_wait();
+    const W* weight = static_cast<const W*>(a.weight);
+    const float inv = 1.f / (float)a.N;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+        const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+        T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+        const float mean = a.mean[row], r = a.rstd[row];
+        float s[2] = {0.f, 0.f};
+        for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
+            const float g = to_f32(dy[c]) * (weight ? to_f32(weight[c]) : 1.f);
+            s[0] += g;
+            s[1] = fmaf(g, (to_f32(x[c]) - mean) * r, s[1]);
+        }
+        row_sum<32, 2>(s, slots[turn]);
+        for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
+            const float g = to_f32(dy[c]) * (weight ? to_f32(weight[c]) : 1.f);
+            const float h = (to_f32(x[c]) - mean) * r;
+            dx[c] = from_f32<T>(r * (g - s[0] * inv - h * (s[1] * inv)));
+        }
+    }
+}
+
+// Long rows, second pass: a block's 256 columns over its share of the rows.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_grad_long_sums_kernel(const NormGradArgs a) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.N) return;
+    float u = 0.f, v = 0.f;
+    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+        const float d = to_f32(static_cast<const T*>(a.dy)[row * a.lddy + c]);
+        const float x = to_f32(static_cast<const T*>(a.x)[row * a.ldx + c]);
+        u = fmaf(d, (x - a.mean[row]) * a.rstd[row], u);
+        v += d;
+    }
+    float* part = a.part + (int64_t)blockIdx.y * 2 * a.N;
+    part[c] = u;
+    part[a.N + c] = v;
+}
+
+// dweight and dbias: the blocks' sums, added in their order within 8 shares.
+constexpr int kShares = 8;
+template <typename W>
+__global__ void __launch_bounds__(32 * kShares)
+    norm_join_kernel(const float* __restrict__ part, int blocks, int N, W* __restrict__ dweight,
+                     W* __restrict__ dbias, float beta) {
+    gemm_ptx::pdl_launch_dependents();
+    __shared__ float got[kShares][32];
+    gemm_ptx::pdl_wait();
+    const int share = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // of 2 N: dweight, then dbias
+    float s = 0.f;
+    if (c < 2 * (int64_t)N) {
+#pragma unroll 8
+        for (int b = share; b < blocks; b += kShares) s += part[(int64_t)b * 2 * N + c];
+    }
+    got[share][lane] = s;
+    __syncthreads();
+    if (share > 0 || c >= 2 * (int64_t)N) return;
+    for (int i = 1; i < kShares; ++i) s += got[i][lane];
+    W* out = c < N ? dweight : dbias;
+    if (!out) return;
+    W* at = out + (c < N ? c : c - N);
+    *at = from_f32<W>(beta != 0.f ? fmaf(beta, to_f32(*at), s) : s);
+}
+
+int row_bytes(int dtype) { return dtype == GEMM_F32 ? 4 : 2; }
+int weight_bytes(int dtype) { return dtype <= GEMM_BF16_F32 ? 4 : 2; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool rows_ok(const void* p, int64_t M, int64_t N, int64_t ld, int es) {
+    return p && aligned_to(p, es) && ld >= N &&
+           (__int128)(M - 1) * ld + N <= (__int128)(INT64_MAX / es);
+}
+bool vec_ready(const void* p, int64_t ld, int es) {
+    return aligned_to(p, 16) && ld * es % 16 == 0;
+}
+
+template <typename T, typename W, int VEC>
+int norm_dispatch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+    auto run = [&](auto warps, auto nv, auto block) {
+        constexpr int WARPS = decltype(warps)::value, NV = decltype(nv)::value;
+        constexpr int BLOCK = decltype(block)::value, ROWS = BLOCK / (32 * WARPS);
+        return launch_dependent(norm_kernel<T, W, WARPS, NV, VEC, BLOCK>,
+                                dim3((unsigned)((a.M + ROWS - 1) / ROWS)), dim3(BLOCK), 0, s, a);
+    };
+    using std::integral_constant;
+#define NORM_RUN(WARPS, NV, BLOCK)                                                     \
+    return run(integral_constant<int, WARPS>{}, integral_constant<int, NV>{},          \
+               integral_constant<int, BLOCK>{})
+    // vectors of a thread: 8 at most by 16 bytes, 32 single elements
+    constexpr int MOST = VEC == 1 ? 32 : 8;
+    const int64_t vecs = (a.N + VEC - 1) / VEC;
+    if (a.M >= dev.sm_count * 8 || vecs <= 32) {  // enough rows for a warp each
+        if (vecs <= 32) NORM_RUN(1, 1, 128);
+        if (vecs <= 32 * (MOST / 2)) NORM_RUN(1, MOST / 2, 128);
+        if (vecs <= 32 * MOST) NORM_RUN(1, MOST, 128);
+    }
+    if (vecs <= 128 * (MOST / 4)) NORM_RUN(4, MOST / 4, 128);
+    if (vecs <= 128 * MOST) NORM_RUN(4, MOST, 128);
+    if (vecs <= 512 * (MOST / 2)) NORM_RUN(16, MOST / 2, 512);
+    if (vecs <= 512 * MOST) NORM_RUN(16, MOST, 512);
+#undef NORM_RUN
+    return launch_dependent(norm_long_kernel<T, W>,
+                            dim3((unsigned)(a.M < dev.sm_count * 2 ? a.M : dev.sm_count * 2)),
+                            dim3(1024), 0, s, a);
+}
+
+template <typename T, typename W>
+int norm_forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+    const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.y, a.ldy, sizeof(T)) &&
+                     a.N % (16 / sizeof(T)) == 0 && aligned_to(a.weight, 16) &&
+                     aligned_to(a.bias, 16);
+    return vec ? norm_dispatch<T, W, 16 / sizeof(T)>(a, dev, s) : norm_dispatch<T, W, 1>(a, dev, s);
+}
+
+// The backward kernel's blocks (its sums' parts) for rows of N columns: 0 where
+// the rows are too long for it.
+struct GradPlan {
+    int warps, lanes, blocks;
+};
+GradPlan grad_plan(int64_t M, int64_t N, int sm_count) {
+    GradPlan g{16, 1, 0};
+    for (int w : {1, 2, 4, 8, 16})
+        if (N <= 32 * w * kOwn) {
+            g.warps = w;
+            break;
+        }
+    if (N > 32 * 16 * kOwn) return g;
+    g.lanes = g.warps == 1 ? 4 : 1;
+    const int64_t rows = (M + g.lanes - 1) / g.lanes;
+    const int64_t most = (int64_t)sm_count * (16 / (g.warps * g.lanes));
+    g.blocks = (int)(rows < most ? rows : most);
+    return g;
+}
+constexpr int kLongShares = 32;
+
+template <typename T, typename W>
+int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const DeviceInfo& dev,
+                  cudaMemPool_t pool, cudaStream_t s) {
+    const bool sums = dweight || dbias;
+    int rc = kOk;
+    const GradPlan g = grad_plan(a.M, a.N, dev.sm_count);
+    const int parts = g.blocks > 0 ? g.blocks : (int)(a.M < kLongShares ? a.M : kLongShares);
+    Scratch scratch{pool, s, dev.device};
+    if (sums && a.M > 0) {
+        a.part = static_cast<float*>(scratch.get((size_t)parts * 2 * a.N * 4));
+        if (!a.part) return kCuda;
+    }
+    const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.dy, a.lddy, sizeof(T)) &&
+                     (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) && a.N % (16 / sizeof(T)) == 0;
+    if (a.M > 0 && g.blocks > 0) {
+#define NORM_GRAD_RUN(WARPS, LANES)                                                            \
+    rc = vec ? launch_dependent(norm_grad_kernel<T, W, WARPS, LANES, 16 / (int)sizeof(T)>,     \
+                                dim3(g.blocks), dim3(32 * WARPS * LANES), 0, s, a)             \
+             : launch_dependent(norm_grad_kernel<T, W, WARPS, LANES, 1>, dim3(g.blocks),       \
+                                dim3(32 * WARPS * LANES), 0, s, a)
+        switch (g.warps) {
+            case 1: NORM_GRAD_RUN(1, 4); break;
+            case 2: NORM_GRAD_RUN(2, 1); break;
+            case 4: NORM_GRAD_RUN(4, 1); break;
+            case 8: NORM_GRAD_RUN(8, 1); break;
+            default: NORM_GRAD_RUN(16, 1); break;
+        }
+#undef NORM_GRAD_RUN
+    } else if (a.M > 0) {
+        // the sums first: dx may be written over x or dy
+        if (sums)
+            rc = launch_dependent(norm_grad_long_sums_kernel<T>,
+                                  dim3((unsigned)((a.N + 255) / 256), (unsigned)parts), dim3(256),
+                                  0, s, a);
+        if (rc == kOk && a.dx)
+            rc = launch_dependent(norm_grad_long_kernel<T, W>,
+                                  dim3((unsigned)(a.M < dev.sm_count * 2 ? a.M
+                                                                         : dev.sm_count * 2)),
+                                  dim3(1024), 0, s, a);
+    }
+    if (rc == kOk && sums)
+        rc = launch_dependent(norm_join_kernel<W>, dim3((unsigned)((2 * (int64_t)a.N + 31) / 32)),
+                              dim3(32 * kShares), 0, s, (const float*)a.part,
+                              a.M > 0 ? parts : 0, a.N, dweight, dbias, beta);
+    scratch.release();
+    return rc;
+}
+
+int layernorm(int64_t M, int64_t N, const void* x, int64_t ldx, const void* weight,
+              const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+              int dtype, cudaStream_t s) {
+    if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
+    if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX || !(eps >= 0.f)) return kInvalidArg;
+    if (M == 0 || N == 0) return kOk;
+    const int es = row_bytes(dtype), ws = weight_bytes(dtype);
+    if (!rows_ok(x, M, N, ldx, es) || !rows_ok(y, M, N, ldy, es)) return kInvalidArg;
+    if (!aligned_to(weight, ws) || !aligned_to(bias, ws) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4))
+        return kInvalidArg;
+    DeviceInfo* dev = nullptr;
+    int rc = current_device_info(&dev, nullptr);
+    if (rc != kOk) return rc;
+    const void* ptrs[6] = {x, y, weight, bias, mean, rstd};
+    rc = check_device_pointers(ptrs, 6, dev->device);
+    if (rc != kOk) return rc;
+    const NormArgs a{M, (int)N, x, ldx, weight, bias, eps, y, ldy, mean, rstd};
+    switch (dtype) {
+        case GEMM_F32: return norm_forward<float, float>(a, *dev, s);
+        case GEMM_F16_F32: return norm_forward<__half, float>(a, *dev, s);
+        case GEMM_BF16_F32: return norm_forward<__nv_bfloat16, float>(a, *dev, s);
+        case GEMM_F16_F16: return norm_forward<__half, __half>(a, *dev, s);
+        default: return norm_forward<__nv_bfloat16, __nv_bfloat16>(a, *dev, s);
+    }
+}
+
+int layernorm_grad(int64_t M, int64_t N, const void* x, int64_t ldx, const void* weight,
+                   const float* mean, const float* rstd, const void* dy, int64_t lddy, void* dx,
+                   int64_t lddx, void* dweight, void* dbias, float beta, int dtype,
+                   cudaStream_t s) {
+    if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
+    if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX) return kInvalidArg;
+    const int es = row_bytes(dtype), ws = weight_bytes(dtype);
+    if (!aligned_to(weight, ws) || !aligned_to(dweight, ws) || !aligned_to(dbias, ws))
+        return kInvalidArg;
+    if (N == 0 || (!dx && !dweight && !dbias) || (M == 0 && !dweight && !dbias)) return kOk;
+    if (M > 0) {
+        if (!rows_ok(x, M, N, ldx, es) || !rows_ok(dy, M, N, lddy, es) || !mean || !rstd ||
+            !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+            return kInvalidArg;
+        if (dx && !rows_ok(dx, M, N, lddx, es)) return kInvalidArg;
+    }
+    DeviceInfo* dev = nullptr;
+    cudaMemPool_t pool = nullptr;
+    int rc = current_device_info(&dev, &pool);
+    if (rc != kOk) return rc;
+    const void* ptrs[8] = {M ? x : nullptr,  M ? weight : nullptr, M ? mean : nullptr,
+                           M ? rstd : nullptr, M ? dy : nullptr,   M ? dx : nullptr,
+                           dweight, dbias};
+    rc = check_device_pointers(ptrs, 8, dev->device);
+    if (rc != kOk) return rc;
+    const NormGradArgs a{M, (int)N, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, nullptr};
+    auto run = [&](auto t, auto w) {
+        using T = decltype(t);
+        using W = decltype(w);
+        return norm_backward<T, W>(a, static_cast<W*>(dweight), static_cast<W*>(dbias), beta, *dev,
+                                   pool, s);
+    };
+    switch (dtype) {
+        case GEMM_F32: return run(float{}, float{});
+        case GEMM_F16_F32: return run(__half{}, float{});
+        case GEMM_BF16_F32: return run(__nv_bfloat16{}, float{});
+        case GEMM_F16_F16: return run(__half{}, __half{});
+        default: return run(__nv_bfloat16{}, __nv_bfloat16{});
+    }
+}
+
+}  // namespace
+}  // namespace libgemm
+
+using namespace libgemm;
+
+extern "C" {
+
+int layernorm_rows(int64_t M, int64_t N, const void* x, int64_t ldx, const void* weight,
+                   const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                   int dtype, void* stream) {
+    try {
+        return layernorm(M, N, x, ldx, weight, bias, eps, y, ldy, mean, rstd, dtype,
+                         static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+int layernorm_rows_grad(int64_t M, int64_t N, const void* x, int64_t ldx, const void* weight,
+                        const float* mean, const float* rstd, const void* dy, int64_t lddy,
+                        void* dx, int64_t lddx, void* dweight, void* dbias, float beta, int dtype,
+                        void* stream) {
+    try {
+        return layernorm_grad(M, N, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, dweight, dbias,
+                              beta, dtype, static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+}  // extern "C"

@@ -402,4 +402,50 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
     return s;
 }
 
+// gemm_xent, gemm_xent_grad: tiles of the logits (M rows, N columns of a piece of
+// the vocabulary). CTA pairs on 256 x 256, but single CTAs on 128 rows where at
+// most 128 rows make half of a pair's tile padding, or where pairs would leave
+// more than half of the SMs idle; these take 64 columns if all tiles then still
+// run at once, else 128.
+constexpr int64_t kXentMaxVocab = 1 << 24;
+struct XentShape {
+    int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
+    int tile_n;
+};
+inline XentShape plan_xent(int64_t M, int64_t N, int sm_count) {
+    const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
+    if (M > 128 && pairs * 4 >= sm_count) return XentShape{2, 256};
+    return XentShape{1, ((M + 127) / 128) * ((N + 63) / 64) <= sm_count ? 64 : 128};
+}
+
+// Rows of gemm_xent that run together: a whole number of tiles whose partial
+// maxima and sums (16 bytes for every row and tile of 64 columns or more) stay
+// within 256 MB.
+inline int64_t xent_panel_rows(int64_t M, int64_t N, int tile_n) {
+    const int64_t per_row = (N + tile_n - 1) / tile_n * 16;
+    const int64_t rows = (256ll << 20) / per_row / 256 * 256;
+    return rows < 256 ? 256 : (rows < M ? rows : M);
+}
+
+// Columns of the vocabulary that gemm_xent_grad holds G of at one time: all of
+// them if `parts` numbers of 16 bits for each of `rows` rows stay within 512 MB,
+// else pieces of equal width (in whole tiles) that do, of 4096 columns at least:
+// every piece adds its part of dX to an fp32 sum, which a narrow one would spend
+// its time on.
+inline int64_t xent_piece_cols(int64_t rows, int64_t N, int parts) {
+    int64_t most = (512ll << 20) / (rows * 2 * parts) / 256 * 256;
+    if (most < 4096) most = 4096;
+    if (N <= most) return N;
+    const int64_t pieces = (N + most - 1) / most;
+    return ((N + pieces - 1) / pieces + 255) / 256 * 256;
+}
+
+// embed_rows_grad: sorted tokens of a chunk, which a block (for each share of the
+// columns) adds up: 16, longer for so many tokens that there would be more than
+// 8192 chunks.
+inline int embed_chunk(int64_t M) {
+    const int64_t n = (M + 8191) / 8192;
+    return (int)(n < 16 ? 16 : n);
+}
+
 }  // namespace libgemm

@@ -1,0 +1,503 @@
+// xent.cu -- gemm_xent() and gemm_xent_grad(): the softmax cross entropy of a
+// projection onto a large vocabulary, and its gradients, without keeping the
+// logits.
+//
+//   z_tv   = sum_k X[t][k] W[v][k]
+//   lse_t  = log sum_v exp(z_tv),     loss_t = lse_t - z_t,target
+//   G_tv   = alpha dloss_t (exp(z_tv - lse_t) - [v = target_t])
+//   dX     = G W,                     dW = beta dW + G^T X
+//
+// Forward: the kernel of xent.cuh leaves a (maximum, sum of exponentials) pair
+// for every row and 128 columns (a half tile), which a second kernel joins:
+// exp(m_i - m) s_i summed over the pairs, the online softmax identity. The logits
+// are never stored, only 1/16 of their bytes.
+//
+// Backward: piece by piece of the vocabulary the same kernel computes the logits
+// again and writes G as 16-bit numbers; the dense kernel of gemm() multiplies it
+// with the piece's rows of W (dX, summed over the pieces in fp32) and with X (the
+// piece's rows of dW, complete). G takes at most 512 MB, or 4096 columns.
+//
+// Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
+// relative 2^-9 (bf16) is below the rounding of a 16-bit result. An fp32 dW would
+// show it, so for that G is two numbers, hi + lo (2^-17 of g), and X is multiplied
+// with both in one product of twice the depth, hi below lo. fp16 has the exponents
+// for that only near 1: G is scaled by a power of two that brings the largest
+// |alpha dloss| to 2^12, its small probabilities then reach down to 2^-36 of it,
+// and the products go through fp32 scratch from which they are scaled back.
+//
+// Rows whose target does not count are zero in G, and zero in the copy of X that
+// dW is multiplied from (0 times an infinity would be NaN).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/gemm.h"
+#include "internal.h"
+#include "policy.h"
+#include "repack16.cuh"
+#include "rows.cuh"
+#include "xent.cuh"
+
+namespace libgemm {
+namespace {
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool is_bf16(int dtype) { return dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16; }
+bool tma_ready(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
+
+// `rows` rows of `cols` elements, ld apart, stay addressable.
+bool span_fits(int64_t rows, int64_t cols, int64_t ld, int esize) {
+    if (rows <= 0 || cols <= 0) return true;
+    return (__int128)(rows - 1) * ld + cols <= (__int128)(INT64_MAX / esize);
+}
+
+// Joins the pairs of a row: warps take every 8th half tile, lanes a row each.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    xent_join_kernel(const float2* __restrict__ part, int64_t ld, int parts, int M,
+                     const float* __restrict__ picked, const int32_t* __restrict__ target,
+                     int vocab, float* __restrict__ loss, float* __restrict__ lse) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    __shared__ float2 got[kJoinWarps][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.f;
+    auto join = [&](float2 o) {
+        const float nm = fmaxf(m, o.x);
+        const float from = nm == -INFINITY ? 0.f : nm;
+        s = s * ex2((m - from) * kLog2e) + o.y * ex2((o.x - from) * kLog2e);
+        m = nm;
+    };
+    if (row < M) {
+        const float2* at = part + row;
+        int i = w;
+        for (; i + 3 * kJoinWarps < parts; i += 4 * kJoinWarps) {
+            float2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = at[(int64_t)(i + j * kJoinWarps) * ld];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) join(v[j]);
+        }
+        for (; i < parts; i += kJoinWarps) join(at[(int64_t)i * ld]);
+    }
+    got[w][lane] = make_float2(m, s);
+    __syncthreads();
+    if (w != 0 || row >= M) return;
+    for (int i = 1; i < kJoinWarps; ++i) join(got[i][lane]);
+    const float l = m + logf(s);
+    if (lse) lse[row] = l;
+    const int t = target[row];
+    loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.f;
+}
+
+// K == 0: every logit is zero.
+__global__ void xent_uniform_kernel(int M, int vocab, const int32_t* target, float* loss,
+                                    float* lse, ErrWord* err) {
+    const float l = (float)log((double)vocab);
+    for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < M; r += gridDim.x * blockDim.x) {
+        const int t = target[r];
+        if (t >= vocab) report_bad_value(err);
+        if (lse) lse[r] = l;
+        loss[r] = t >= 0 && t < vocab ? l : 0.f;
+    }
+}
+
+// The rows of X that count, in rows of TMA's alignment; the others, and those
+// from M to `rows`, zero. With copies == 2 the same again below. A warp per row.
+__global__ void __launch_bounds__(256)
+    xent_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, int M, int64_t K,
+                     const int32_t* __restrict__ target, int vocab, uint16_t* __restrict__ out,
+                     int64_t ldo, int rows, int copies) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
+    for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+         r < (int64_t)rows * copies; r += warps) {
+        const int64_t t = r % rows;
+        uint16_t* dst = out + r * ldo;
+        const int v = t < M ? target[t] : -1;
+        if (v >= 0 && v < vocab) {
+            repack16_row(X + t * ldx, dst, K, lane);
+            for (int64_t c = K + lane; c < ldo; c += 32) dst[c] = 0;
+        } else {
+            for (int64_t c = lane * 8; c < ldo; c += 256)
+                *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// scale[0]: the power of two that brings the largest finite |alpha dloss_t| of
+// the rows that count into [2^12, 2^13); scale[1]: its inverse. One block.
+__global__ void __launch_bounds__(1024)
+    xent_scale_kernel(int M, const int32_t* __restrict__ target, int vocab,
+                      const float* __restrict__ dloss, float alpha, float* __restrict__ scale) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    __shared__ float most[32];
+    float top = 0.f;
+    for (int r = threadIdx.x; r < M; r += blockDim.x) {
+        const int t = target[r];
+        const float d = fabsf(dloss ? alpha * dloss[r] : alpha);
+        if (t >= 0 && t < vocab && d < INFINITY) top = fmaxf(top, d);
+    }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, most[i]);
+    int e = top > 0.f ? 12 - ilogbf(top) : 0;
+    e = min(max(e, -100), 100);
+    scale[0] = ldexpf(1.f, e);
+    scale[1] = ldexpf(1.f, -e);
+}
+
+// out = scale * sum + beta * out, rounded once; rows x cols, four columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    xent_finish_kernel(const float* __restrict__ sum, int64_t lds, T* __restrict__ out, int64_t ldo,
+                       int64_t rows, int64_t cols, const float* __restrict__ scale, float beta) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    const float by = scale ? *scale : 1.f;
+    const int64_t quads = (cols + 3) / 4;
+    const bool whole = ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * quads; i += step) {
+        const int64_t r = i / quads, c = (i - r * quads) * 4;
+        const float4 v = *reinterpret_cast<const float4*>(sum + r * lds + c);  // lds % 4 == 0
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        T* dst = out + r * ldo + c;
+        const int n = cols - c < 4 ? (int)(cols - c) : 4;
+        alignas(16) T o[4];
+        for (int e = 0; e < 4; ++e)
+            if (e < n) o[e] = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(dst[e]), by * f[e])
+                                                      : by * f[e]);
+        if (whole && n == 4) {
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+            else
+                *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+        } else {
+            for (int e = 0; e < n; ++e) dst[e] = o[e];
+        }
+    }
+}
+
+int finish(const float* sum, int64_t lds, void* out, int64_t ldo, int64_t rows, int64_t cols,
+           const float* scale, float beta, int esize, bool bf16, const DeviceInfo& dev,
+           cudaStream_t s) {
+    const int64_t blocks = (rows * ((cols + 3) / 4) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < dev.sm_count * 16 ? blocks : dev.sm_count * 16));
+    if (esize == 4)
+        return launch_dependent(xent_finish_kernel<float>, grid, dim3(256), 0, s, sum, lds,
+                                static_cast<float*>(out), ldo, rows, cols, scale, beta);
+    if (bf16)
+        return launch_dependent(xent_finish_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, sum, lds,
+                                static_cast<__nv_bfloat16*>(out), ldo, rows, cols, scale, beta);
+    return launch_dependent(xent_finish_kernel<__half>, grid, dim3(256), 0, s, sum, lds,
+                            static_cast<__half*>(out), ldo, rows, cols, scale, beta);
+}
+
+// Checks of X, W and target that both calls make; no CUDA calls.
+int check_inputs(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+                 int64_t ldw, const int32_t* target, int dtype) {
+    if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
+    if (M < 0 || N < 1 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+        return kInvalidArg;
+    if (dtype == GEMM_F32 || N > kXentMaxVocab) return kUnsupported;
+    if (M == 0) return kOk;
+    if (!target || !aligned_to(target, 4)) return kInvalidArg;
+    if (K == 0) return kOk;
+    if (!X || !W || !aligned_to(X, 2) || !aligned_to(W, 2) || ldx < K || ldw < K)
+        return kInvalidArg;
+    if (!span_fits(M, K, ldx, 2) || !span_fits(N, K, ldw, 2)) return kInvalidArg;
+    return kOk;
+}
+
+// The parts of one scratch buffer, 256-byte aligned.
+struct Parts {
+    int64_t bytes = 0;
+    int64_t add(int64_t n) {
+        const int64_t at = bytes;
+        bytes += up(n, 256);
+        return at;
+    }
+};
+
+// Copies an operand whose rows TMA cannot read (offset `at` of the scratch).
+int repack_one(const void*& p, int64_t& ld, int64_t rows, int64_t cols, char* to,
+               const DeviceInfo& dev, cudaStream_t s) {
+    Repack16 job{static_cast<const uint16_t*>(p), reinterpret_cast<uint16_t*>(to), ld, up(cols, 8),
+                 rows, cols};
+    repack16_kernel<<<repack16_blocks(rows, dev.sm_count), 256, 0, s>>>(job, Repack16{});
+    if (cudaGetLastError() != cudaSuccess) return kCuda;
+    note_launch();
+    dispatch_log("repack of a misaligned 16-bit operand, %lld x %lld", (long long)rows,
+                 (long long)cols);
+    p = job.dst;
+    ld = job.ldd;
+    return kOk;
+}
+
+void xent_params(XentParams& xp, int64_t M, int64_t N, int64_t K, const XentShape& shape,
+                 int64_t vocab, const int32_t* target, const DeviceInfo& dev) {
+    std::memset(&xp, 0, sizeof(xp));
+    xp.M = (int)M;
+    xp.N = (int)N;
+    xp.num_kb = (int)((K + XBK - 1) / XBK);
+    xp.tile_n = shape.tile_n;
+    xp.tiles_m = (int)((M + XROWS * shape.cta_group - 1) / (XROWS * shape.cta_group));
+    xp.tiles_n = (int)((N + shape.tile_n - 1) / shape.tile_n);
+    xp.band = 8;
+    xp.vocab = (int)vocab;
+    xp.target = target;
+    xp.alpha = 1.f;
+    xp.err = dev.err_word;
+    xp.gen = next_generation();
+    xp.wait_limit_ns = option_wait_limit_ns();
+    xp.fault_inject = option_tc_fault_inject();
+}
+
+bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void* W, int64_t ldw,
+               int64_t K, const XentShape& shape) {
+    return encode_tma_16(&xp.map_x, bf16, X, (uint64_t)K, (uint64_t)xp.M, (uint64_t)ldx, 0, 0, XBK,
+                         XROWS) &&
+           encode_tma_16(&xp.map_w, bf16, W, (uint64_t)K, (uint64_t)xp.N, (uint64_t)ldw, 0, 0, XBK,
+                         (uint32_t)(shape.tile_n / shape.cta_group));
+}
+
+int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const DeviceInfo& dev,
+           cudaStream_t s) {
+    if ((int64_t)xp.tiles_m * xp.tiles_n * 2 > INT32_MAX) return kUnsupported;
+    const int rc = bf16 ? launch_xent_bf16(xp, mode, shape.cta_group, dev, s)
+                        : launch_xent_f16(xp, mode, shape.cta_group, dev, s);
+    dispatch_log("cross entropy %s %dx%d, %d k-blocks: %s, %d x %d tiles of %d columns",
+                 mode == kXentStats ? "logits" : "gradient's logits", xp.M, xp.N, xp.num_kb,
+                 shape.cta_group == 2 ? "CTA pairs" : "one CTA per tile", xp.tiles_m, xp.tiles_n,
+                 xp.tile_n);
+    return rc;
+}
+
+int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+            int64_t ldw, const int32_t* target, float* loss, float* lse, int dtype,
+            cudaStream_t s) {
+    int rc = check_inputs(M, N, K, X, ldx, W, ldw, target, dtype);
+    if (rc != kOk || M == 0) return rc;
+    if (!loss || !aligned_to(loss, 4) || !aligned_to(lse, 4)) return kInvalidArg;
+    DeviceInfo* dev = nullptr;
+    cudaMemPool_t pool = nullptr;
+    rc = current_device_info(&dev, &pool);
+    if (rc != kOk) return rc;
+    const void* ptrs[5] = {K > 0 ? X : nullptr, K > 0 ? W : nullptr, target, loss, lse};
+    rc = check_device_pointers(ptrs, 5, dev->device);
+    if (rc != kOk) return rc;
+    if (K == 0) {
+        const int64_t blocks = (M + 255) / 256;
+        xent_uniform_kernel<<<(unsigned)(blocks < dev->sm_count ? blocks : dev->sm_count), 256, 0,
+                              s>>>((int)M, (int)N, target, loss, lse, dev->err_word);
+        if (cudaGetLastError() != cudaSuccess) return kCuda;
+        note_launch();
+        return kOk;
+    }
+    const bool bf16 = is_bf16(dtype);
+    const XentShape shape = plan_xent(M, N, dev->sm_count);
+    const int64_t panel = xent_panel_rows(M, N, shape.tile_n);
+    const int64_t parts = (N + shape.tile_n - 1) / shape.tile_n * 2;
+    Parts at;
+    const int64_t part_at = at.add(parts * up(panel, 32) * 8);
+    const int64_t picked_at = at.add(panel * 4);
+    const int64_t x_at = tma_ready(X, ldx) ? -1 : at.add(M * up(K, 8) * 2);
+    const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * up(K, 8) * 2);
+    Scratch scratch{pool, s, dev->device};
+    char* mem = static_cast<char*>(scratch.get((size_t)at.bytes));
+    if (!mem) return kCuda;
+    if (x_at >= 0) rc = repack_one(X, ldx, M, K, mem + x_at, *dev, s);
+    if (rc == kOk && w_at >= 0) rc = repack_one(W, ldw, N, K, mem + w_at, *dev, s);
+    for (int64_t r0 = 0; r0 < M && rc == kOk; r0 += panel) {
+        const int64_t m = M - r0 < panel ? M - r0 : panel;
+        XentParams xp;
+        xent_params(xp, m, N, K, shape, N, target + r0, *dev);
+        if (!xent_maps(xp, bf16, static_cast<const uint16_t*>(X) + r0 * ldx, ldx, W, ldw, K,
+                       shape)) {
+            rc = kCuda;
+            break;
+        }
+        xp.part = reinterpret_cast<float2*>(mem + part_at);
+        xp.part_ld = up(panel, 32);
+        xp.picked = reinterpret_cast<float*>(mem + picked_at);
+        rc = launch(xp, kXentStats, bf16, shape, *dev, s);
+        if (rc != kOk) break;
+        rc = launch_dependent(xent_join_kernel, dim3((unsigned)((m + 31) / 32)),
+                              dim3(32 * kJoinWarps), 0, s, (const float2*)xp.part, xp.part_ld,
+                              (int)parts, (int)m, (const float*)xp.picked, target + r0, (int)N,
+                              loss + r0, lse ? lse + r0 : nullptr);
+    }
+    scratch.release();
+    return rc;
+}
+
+// C = alpha A B^T + beta C on the dense kernel.
+int product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, int a_major,
+            const void* B, int64_t ldb, int b_major, void* C, int64_t ldc, int dtype, float beta,
+            const DeviceInfo& dev, cudaStream_t s) {
+    Problem p{M, N, K, A, lda, a_major == GEMM_MAJOR_K, B, ldb, b_major == GEMM_MAJOR_K, C, ldc,
+              dtype, EpiParams{}};
+    if (beta != 0.f) p.epi = EpiParams{1, 1.f, beta, nullptr, 0, GEMM_ACT_NONE};
+    return launch_gemm_tc(p, dev,
+                          resolve_tc_options(M, N, K, A, lda, a_major, B, ldb, b_major, C, ldc,
+                                             GEMM_MAJOR_MN, dtype),
+                          s);
+}
+
+int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+             int64_t ldw, const int32_t* target, const float* lse, const float* dloss, void* dX,
+             int64_t lddx, void* dW, int64_t lddw, float alpha, float beta, int dtype,
+             cudaStream_t s) {
+    int rc = check_inputs(M, N, K, X, ldx, W, ldw, target, dtype);
+    if (rc != kOk) return rc;
+    const int we = dtype <= GEMM_BF16_F32 ? 4 : 2;
+    if (!aligned_to(dX, 2) || !aligned_to(dW, we)) return kInvalidArg;
+    if (K > 0 && ((dX && M > 0 && lddx < K) || (dW && lddw < K))) return kInvalidArg;
+    if ((dX && !span_fits(M, K, lddx, 2)) || (dW && !span_fits(N, K, lddw, we)))
+        return kInvalidArg;
+    if (M > 0 && K > 0 && (dX || dW) &&
+        (!lse || !aligned_to(lse, 4) || !aligned_to(dloss, 4)))
+        return kInvalidArg;
+    if (K == 0 || (!dX && !dW) || (M == 0 && !dW)) return kOk;
+    DeviceInfo* dev = nullptr;
+    cudaMemPool_t pool = nullptr;
+    rc = current_device_info(&dev, &pool);
+    if (rc != kOk) return rc;
+    const bool bf16 = is_bf16(dtype);
+    if (M == 0) {  // no rows: dW = beta dW
+        rc = check_device_pointers(&dW, 1, dev->device);
+        if (rc != kOk) return rc;
+        Problem p{N, K, 0, nullptr, 0, true, nullptr, 0, true, dW, lddw, dtype,
+                  EpiParams{1, 1.f, beta, nullptr, 0, GEMM_ACT_NONE}};
+        return launch_epilogue_only(p, *dev, s);
+    }
+    const void* ptrs[7] = {X, W, target, lse, dloss, dX, dW};
+    rc = check_device_pointers(ptrs, 7, dev->device);
+    if (rc != kOk) return rc;
+
+    const int parts = dW && we == 4 ? 2 : 1;  // numbers that hold an entry of G
+    const bool scaled = !bf16;
+    const int64_t piece = xent_piece_cols(up(M, 256), N, parts);
+    const XentShape shape = plan_xent(M, piece, dev->sm_count);  // of every piece
+    const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
+    const int64_t pieces = (N + piece - 1) / piece;
+    const bool sum_dx = dX && (pieces > 1 || scaled);
+    const int64_t ldg = up(piece, 256), ldk = up(K, 8);
+    Parts at;
+    const int64_t g_at = at.add(ldg * rows * parts * 2);
+    const bool copy_x = dW || !tma_ready(X, ldx);
+    const int64_t x_at = copy_x ? at.add(ldk * rows * parts * 2) : -1;
+    const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * ldk * 2);
+    const int64_t dx_at = sum_dx ? at.add(M * up(K, 4) * 4) : -1;
+    const int64_t dw_at = dW && scaled ? at.add(piece * up(K, 4) * 4) : -1;
+    const int64_t scale_at = scaled ? at.add(8) : -1;
+    Scratch scratch{pool, s, dev->device};
+    char* mem = static_cast<char*>(scratch.get((size_t)at.bytes));
+    if (!mem) return kCuda;
+    float* scale = scaled ? reinterpret_cast<float*>(mem + scale_at) : nullptr;
+    float* dx_sum = sum_dx ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
+    float* dw_sum = dw_at >= 0 ? reinterpret_cast<float*>(mem + dw_at) : nullptr;
+    char* g = mem + g_at;
+
+    const void* xc = X;  // rows that count, aligned
+    int64_t ldxc = ldx;
+    if (copy_x) {
+        const int64_t blocks = ((int64_t)rows * parts + 7) / 8;
+        rc = launch_dependent(xent_rows_kernel,
+                              dim3((unsigned)(blocks < dev->sm_count * 8 ? blocks
+                                                                         : dev->sm_count * 8)),
+                              dim3(256), 0, s, static_cast<const uint16_t*>(X), ldx, (int)M, K,
+                              target, (int)N, reinterpret_cast<uint16_t*>(mem + x_at), ldk, rows,
+                              parts);
+        xc = mem + x_at;
+        ldxc = ldk;
+    }
+    if (rc == kOk && w_at >= 0) rc = repack_one(W, ldw, N, K, mem + w_at, *dev, s);
+    if (rc == kOk && scaled)
+        rc = launch_dependent(xent_scale_kernel, dim3(1), dim3(1024), 0, s, (int)M, target, (int)N,
+                              dloss, alpha, scale);
+    const int f32 = bf16 ? GEMM_BF16_F32 : GEMM_F16_F32;
+    const int same = bf16 ? GEMM_BF16_BF16 : GEMM_F16_F16;
+    for (int64_t v0 = 0; v0 < N && rc == kOk; v0 += piece) {
+        const int64_t n = N - v0 < piece ? N - v0 : piece;
+        const void* wp = static_cast<const uint16_t*>(W) + v0 * ldw;
+        XentParams xp;
+        xent_params(xp, M, n, K, shape, N, target, *dev);
+        xp.col0 = (int)v0;
+        xp.lo_row = rows;
+        xp.lse = lse;
+        xp.dloss = dloss;
+        xp.alpha = alpha;
+        xp.scale = scale;
+        if (!xent_maps(xp, bf16, xc, ldxc, wp, ldw, K, shape) ||
+            !encode_tma_16(&xp.map_g, bf16, g, (uint64_t)ldg, (uint64_t)rows * parts,
+                           (uint64_t)ldg, 0, 0, 64, 32)) {
+            rc = kCuda;
+            break;
+        }
+        rc = launch(xp, parts == 2 ? kXentGrad2 : kXentGrad, bf16, shape, *dev, s);
+        if (rc == kOk && dX)
+            rc = sum_dx ? product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dx_sum,
+                                  up(K, 4), f32, v0 > 0 ? 1.f : 0.f, *dev, s)
+                        : product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dX, lddx,
+                                  same, 0.f, *dev, s);
+        if (rc != kOk || !dW) continue;
+        void* dst = static_cast<char*>(dW) + v0 * lddw * we;
+        const int64_t depth = (int64_t)rows * parts;
+        if (!scaled) {
+            rc = product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dst, lddw,
+                         dtype, beta, *dev, s);
+        } else {
+            rc = product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dw_sum,
+                         up(K, 4), f32, 0.f, *dev, s);
+            if (rc == kOk)
+                rc = finish(dw_sum, up(K, 4), dst, lddw, n, K, scale + 1, beta, we, bf16, *dev, s);
+        }
+    }
+    if (rc == kOk && sum_dx)
+        rc = finish(dx_sum, up(K, 4), dX, lddx, M, K, scaled ? scale + 1 : nullptr, 0.f, 2, bf16,
+                    *dev, s);
+    scratch.release();
+    return rc;
+}
+
+}  // namespace
+}  // namespace libgemm
+
+using namespace libgemm;
+
+extern "C" {
+
+int gemm_xent(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+              int64_t ldw, const int32_t* target, float* loss, float* lse, int dtype,
+              void* stream) {
+    try {
+        return forward(M, N, K, X, ldx, W, ldw, target, loss, lse, dtype,
+                       static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+int gemm_xent_grad(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+                   int64_t ldw, const int32_t* target, const float* lse, const float* dloss,
+                   void* dX, int64_t lddx, void* dW, int64_t lddw, float alpha, float beta,
+                   int dtype, void* stream) {
+    try {
+        return backward(M, N, K, X, ldx, W, ldw, target, lse, dloss, dX, lddx, dW, lddw, alpha,
+                        beta, dtype, static_cast<cudaStream_t>(stream));
+    } catch (...) {
+        return kCuda;
+    }
+}
+
+}  // extern "C"

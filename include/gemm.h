@@ -364,15 +364,175 @@ int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
               const int32_t *adapter, const void *lora_a, const void *lora_b, const float *scale,
               void *C, int64_t ldc, int dtype, const gemm_epilogue *epi, void *stream);
 
+/*
+ * gemm_xent -- the softmax cross entropy of a projection onto a large vocabulary,
+ * without keeping the logits:
+ *
+ *     z[t][v] = sum_k X[t][k] * W[v][k],   lse[t] = log sum_v exp(z[t][v])
+ *     loss[t] = lse[t] - z[t][target[t]]   (0 where target[t] < 0)
+ *
+ * X is M x K and W is N x K, both K-major (ldx, ldw >= K; W as an embedding table
+ * is stored). target is a DEVICE array of M numbers: 0 .. N-1, or negative for a
+ * row that does not count (a prompt's token, padding); a number >= N counts as
+ * negative, and gemm_check_device_error() then reports GEMM_ERR_INVALID_ARG. loss
+ * and lse are DEVICE arrays of M floats; lse may be NULL, and is written for every
+ * row. Types: the 16-bit dtypes (the result's type is not used; GEMM_F32 is
+ * GEMM_ERR_UNSUPPORTED). Logits and sums are fp32; infinite or NaN logits make
+ * their row's lse NaN. N is 1 .. 2^24 (more: GEMM_ERR_UNSUPPORTED). The rows' results
+ * do not depend on each other. Scratch: 16 bytes for each row and 64 to 256
+ * columns, for as many rows at a time as stay within 256 MB, and copies of X or W
+ * where their rows are not 16-byte aligned. M zero is a no-op, K zero gives
+ * lse = log N. Otherwise ownership, asynchrony and status codes are gemm()'s.
+ */
+int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+              const void *W, int64_t ldw, const int32_t *target, float *loss, float *lse,
+              int dtype, void *stream);
+
+/*
+ * gemm_xent_grad -- the gradients of gemm_xent, from its lse:
+ *
+ *     G[t][v] = alpha * dloss[t] * (exp(z[t][v] - lse[t]) - (v == target[t]))
+ *     dX = G * W,   dW = beta * dW + G^T * X
+ *
+ * with G zero for rows that do not count; of them nothing but target is used (X,
+ * lse and dloss may hold anything there). dloss is a DEVICE array of M floats, or
+ * NULL for ones (the mean of M tokens: alpha = 1 / M). dX is M x K (lddx >= K) of
+ * the operands' type, dW is N x K (lddw >= K) of the dtype's result type: fp32 for
+ * master gradients, which beta = 1 accumulates over micro-batches, or 16-bit.
+ * Either may be NULL. dX and dW overlap neither each other nor X and W.
+ *
+ * The logits are computed again, a piece of the vocabulary at a time. G is held as
+ * 16-bit numbers, for an fp32 dW as two that leave 2^-17 (bf16) or 2^-22 (fp16) of
+ * it; fp16 numbers are scaled by a power of two that brings the largest
+ * |alpha * dloss[t]| into [2^12, 2^13), so that G reaches down to 2^-36 of that.
+ * Probabilities below 2^-126 count as zero.
+ * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, or
+ * 4096 columns), a copy of X (two for an fp32 dW), an fp32 dX where the
+ * vocabulary takes more than one piece or the type is fp16, and for fp16 the
+ * piece of dW in fp32. With M zero dW = beta * dW; K zero is a no-op. Otherwise
+ * as gemm_xent.
+ */
+int gemm_xent_grad(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                   const void *W, int64_t ldw, const int32_t *target, const float *lse,
+                   const float *dloss, void *dX, int64_t lddx, void *dW, int64_t lddw,
+                   float alpha, float beta, int dtype, void *stream);
+
+/*
+ * layernorm_rows -- of every row of an M x N matrix x (row pitch ldx >= N):
+ *
+ *     mean = sum_n x[n] / N,   rstd = 1 / sqrt(sum_n (x[n] - mean)^2 / N + eps)
+ *     y[n] = (x[n] - mean) * rstd * weight[n] + bias[n]
+ *
+ * The dtype's first type is that of x and y, its second that of weight and bias
+ * (GEMM_BF16_F32: bf16 rows, fp32 weights; GEMM_F32: all fp32). weight (NULL:
+ * ones) and bias (NULL: zeros) are DEVICE vectors of N elements. mean and rstd
+ * are DEVICE arrays of M floats for the backward pass, or NULL. Statistics are
+ * fp32, y is rounded once. y may be x itself (ldy == ldx). Any N; rows that are
+ * 16-byte aligned, of a whole number of 16-byte pieces, run fastest. eps < 0 or
+ * NaN is GEMM_ERR_INVALID_ARG. M or N zero is a no-op. Otherwise as gemm().
+ */
+int layernorm_rows(int64_t M, int64_t N, const void *x, int64_t ldx, const void *weight,
+                   const void *bias, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                   int dtype, void *stream);
+
+/*
+ * layernorm_rows_grad -- the gradients of layernorm_rows, from its mean and rstd:
+ *
+ *     xhat = (x - mean) * rstd,   g = dy * weight
+ *     dx = rstd * (g - sum_n g / N - xhat * (sum_n g * xhat) / N)
+ *     dweight = beta * dweight + sum over the rows of dy * xhat
+ *     dbias   = beta * dbias   + sum over the rows of dy
+ *
+ * dy and dx have x's type (row pitches lddy, lddx >= N), dweight and dbias the
+ * weights' type. dx, dweight and dbias may each be NULL; dx may be dy or x itself
+ * (with its pitch). Sums are fp32 and do not depend on timing. With M zero dweight
+ * and dbias are beta times themselves. Otherwise as layernorm_rows.
+ */
+int layernorm_rows_grad(int64_t M, int64_t N, const void *x, int64_t ldx, const void *weight,
+                        const float *mean, const float *rstd, const void *dy, int64_t lddy,
+                        void *dx, int64_t lddx, void *dweight, void *dbias, float beta,
+                        int dtype, void *stream);
+
+/*
+ * embed_rows -- y[t] = scale * table[ids[t]] for M rows t: a token embedding.
+ * table is V x K (row pitch ldt >= K), y is M x K (ldy >= K); the dtype's first
+ * type is the table's, its second y's. ids is a DEVICE array of M numbers: 0 ..
+ * V-1, or negative for a row of zeros (padding); a number >= V counts as negative,
+ * and gemm_check_device_error() then reports GEMM_ERR_INVALID_ARG. y is rounded
+ * once. M or K zero is a no-op. Otherwise as gemm().
+ */
+int embed_rows(int64_t M, int64_t V, int64_t K, const int32_t *ids, const void *table,
+               int64_t ldt, float scale, void *y, int64_t ldy, int dtype, void *stream);
+
+/*
+ * embed_rows_grad -- the table's gradient of embed_rows:
+ *
+ *     dtable[v] = beta * dtable[v] + scale * sum over the t with ids[t] == v of dy[t]
+ *
+ * The dtype's first type is dy's (M x K, lddy >= K), its second dtable's (V x K,
+ * lddt >= K). With beta = 1 only the rows that a token names are touched (an
+ * embedding tied to gemm_xent's W adds to its dW this way); else the whole table is
+ * written. ids as in embed_rows; dy of rows that do not count may hold anything.
+ * Sums are fp32 in an order that M alone fixes, rounded once. Scratch: 16 bytes a
+ * token, and 2 K floats for each 16 tokens (at most 8192 times). Otherwise as
+ * embed_rows.
+ */
+int embed_rows_grad(int64_t M, int64_t V, int64_t K, const int32_t *ids, const void *dy,
+                    int64_t lddy, float scale, void *dtable, int64_t lddt, float beta, int dtype,
+                    void *stream);
+
+/*
+ * router_balance -- of a router's choice of `top` of E experts for T tokens, the
+ * experts' counts, their group limits, and the balance loss:
+ *
+ *     p[t] = softmax(logits[t])             of the tokens that count, n of them
+ *     counts[e] = how often expert[t][k] == e,   counts[E] = n
+ *     offsets[0] = 0,   offsets[e + 1] = offsets[e] + counts[e]
+ *     prob[e] = sum_t p[t][e] / n
+ *     *loss = E * sum_e counts[e] / (top * n) * prob[e]   (1 when balanced)
+ *
+ * logits is T x E (ldl >= E) of the dtype's first type. expert is a DEVICE array
+ * of T x top numbers: 0 .. E-1, or negative for a choice that was dropped; a token
+ * whose first number is negative does not count (padding), and nothing else of it
+ * is used. A number >= E is left out, and gemm_check_device_error() then reports
+ * GEMM_ERR_INVALID_ARG. counts (E + 1 numbers), offsets (E + 1, or NULL), prob (E
+ * floats) and loss (one float) are DEVICE arrays; offsets are the limits that
+ * gemm_grouped takes for rows sorted by expert. Sums are fp32 and do not depend on
+ * timing. E is 1 .. 1024 (more: GEMM_ERR_UNSUPPORTED), T * top at most 2^31 - 1. T
+ * zero (or n zero) gives zeros. Otherwise as gemm().
+ */
+int router_balance(int64_t T, int64_t E, int64_t top, const void *logits, int64_t ldl,
+                   const int32_t *expert, int32_t *counts, int32_t *offsets, float *prob,
+                   float *loss, int dtype, void *stream);
+
+/*
+ * router_balance_grad -- the gradient of router_balance's loss (the counts are
+ * constants), from its counts:
+ *
+ *     f[e] = counts[e] / (top * n)
+ *     dlogits[t][e] = alpha * *dloss * E / n * p[t][e] * (f[e] - sum_j f[j] * p[t][j])
+ *                     + beta * dlogits[t][e]
+ *
+ * zero (plus beta times what is there) for tokens that do not count. dlogits is
+ * T x E (lddl >= E) of the dtype's second type and may be logits itself where the
+ * types and pitches are the same and beta is 0. dloss is a DEVICE float, or NULL
+ * for 1. T zero is a no-op. Otherwise as router_balance.
+ */
+int router_balance_grad(int64_t T, int64_t E, int64_t top, const void *logits, int64_t ldl,
+                        const int32_t *expert, const int32_t *counts, const float *dloss,
+                        void *dlogits, int64_t lddl, float alpha, float beta, int dtype,
+                        void *stream);
+
 /* gemm_strerror -- a static, NUL-terminated description of a status code. */
 const char *gemm_strerror(int status);
 
 /*
  * gemm_check_device_error -- synchronises `stream`, then reads and clears the
  * current device's error words. Returns GEMM_OK, GEMM_ERR_TIMEOUT (a kernel
- * gave up on a barrier wait), GEMM_ERR_INVALID_ARG (a kernel met group limits
- * or adapter numbers out of range in device memory: gemm_grouped,
- * gemm_grouped_k, gemm_lora) or GEMM_ERR_CUDA (the synchronisation failed).
+ * gave up on a barrier wait), GEMM_ERR_INVALID_ARG (a kernel met group limits,
+ * adapter numbers, targets, token or expert numbers out of range in device memory:
+ * gemm_grouped, gemm_grouped_k, gemm_lora, gemm_xent, embed_rows, router_balance and
+ * their gradients) or GEMM_ERR_CUDA (the synchronisation failed).
  */
 int gemm_check_device_error(void *stream);
 
