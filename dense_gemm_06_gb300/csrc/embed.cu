@@ -9,9 +9,9 @@
 // results that do not depend on timing.
 //
 // Sort: the 64-bit number (token, t) is unique, so its place in the sorted list is
-// a count of smaller ones. Blocks sort 2048 numbers each in shared memory; then
-// eight runs at a time are merged, every number finding its place among the seven
-// other runs by binary search. 65536 tokens take three launches.
+// a count of smaller ones. Blocks sort 512 numbers each; then 16 runs at a time are
+// merged, every number finding its place among the 15 other runs by binary
+// search. 8192 tokens take two launches, 131072 three.
 //
 // Sums: the sorted list is cut into chunks of equal length, so that a frequent
 // token's rows are shared by many blocks. A block adds up the runs within its
@@ -108,144 +108,147 @@ struct EmbedArgs {
     ErrWord* err;
 };
 
-// One row for each `threads` threads of a block; a thread takes groups of G
-// elements that are aligned in y, and the first threads the row's loose ends.
-constexpr int kEmbedRows = 4;  // rows in flight in a thread
+// A warp takes a piece of a row: kPieces groups of G elements in each lane, all in
+// flight at once (2 KB of a 16-bit row). Groups are aligned in y; the elements
+// before the first and after the last whole group are copied one by one.
+constexpr int kPieces = 4;
 template <typename T, typename O>
-__global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int threads) {
+__global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int pieces) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int G = 16 / (int)sizeof(O) < 16 / (int)sizeof(T) ? 16 / (int)sizeof(O)
                                                                 : 16 / (int)sizeof(T);
-    const int lanes = blockDim.x / threads;
-    const int tid = threadIdx.x % threads;
-    const int64_t step = (int64_t)gridDim.x * lanes;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    const int64_t t = unit / pieces, piece = unit - t * pieces;
     gemm_ptx::pdl_wait();
-    for (int64_t t0 = (int64_t)blockIdx.x * lanes + threadIdx.x / threads; t0 < a.M;
-         t0 += step * kEmbedRows) {
-        const T* from[kEmbedRows];
-        O* to[kEmbedRows];
-        int head[kEmbedRows];
+    if (t >= a.M) return;
+    const int id = a.ids[t];
+    if (id >= a.V && lane == 0) report_bad_value(a.err);
+    const bool named = id >= 0 && id < a.V;
+    const T* from = static_cast<const T*>(a.table) + (named ? (int64_t)id * a.ldt : 0);
+    O* to = static_cast<O*>(a.y) + t * a.ldy;
+    const int past = (int)(reinterpret_cast<uintptr_t>(to) % (G * sizeof(O))) / (int)sizeof(O);
+    int64_t head = past ? G - past : 0;
+    if (head > a.K) head = a.K;
+    const int64_t tail = head + (a.K - head) / G * G;
+    const int64_t c0 = head + (piece * kPieces * 32 + lane) * G;
+    float v[kPieces][G];
 #pragma unroll
-        for (int j = 0; j < kEmbedRows; ++j) {
-            const int64_t t = t0 + j * step;
-            from[j] = nullptr;
-            to[j] = nullptr;
-            head[j] = 0;
-            if (t >= a.M) continue;
-            const int id = a.ids[t];
-            if (id >= a.V && tid == 0) report_bad_value(a.err);
-            if (id >= 0 && id < a.V) from[j] = static_cast<const T*>(a.table) + id * a.ldt;
-            to[j] = static_cast<O*>(a.y) + t * a.ldy;
-            const int past = (int)(reinterpret_cast<uintptr_t>(to[j]) % (G * sizeof(O))) /
-                             (int)sizeof(O);
-            head[j] = past ? G - past : 0;
-            if (head[j] > a.K) head[j] = (int)a.K;
-        }
-        for (int64_t c = (int64_t)tid * G; c < a.K; c += (int64_t)threads * G) {
-            float v[kEmbedRows][G];
+    for (int j = 0; j < kPieces; ++j) {
 #pragma unroll
-            for (int j = 0; j < kEmbedRows; ++j) {
-#pragma unroll
-                for (int e = 0; e < G; ++e) v[j][e] = 0.f;
-                if (from[j] && c + head[j] + G <= a.K) load_group<T, G>(from[j] + c + head[j], v[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < kEmbedRows; ++j) {
-                if (!to[j] || c + head[j] + G > a.K) continue;
-#pragma unroll
-                for (int e = 0; e < G; ++e) v[j][e] *= a.scale;
-                store_group<O, G>(to[j] + c + head[j], v[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kEmbedRows; ++j) {
-            if (!to[j]) continue;
-            const int64_t tail = head[j] + (a.K - head[j]) / G * G;
-            for (int64_t i = tid; i < head[j] + (a.K - tail); i += threads) {
-                const int64_t c = i < head[j] ? i : tail + (i - head[j]);
-                to[j][c] = from_f32<O>(from[j] ? a.scale * to_f32(from[j][c]) : 0.f);
-            }
-        }
+        for (int e = 0; e < G; ++e) v[j][e] = 0.f;
+        if (named && c0 + j * 32 * G < tail) load_group<T, G>(from + c0 + j * 32 * G, v[j]);
     }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+        if (c0 + j * 32 * G >= tail) continue;
+#pragma unroll
+        for (int e = 0; e < G; ++e) v[j][e] *= a.scale;
+        store_group<O, G>(to + c0 + j * 32 * G, v[j]);
+    }
+    if (piece == 0)
+        for (int64_t i = lane; i < head + (a.K - tail); i += 32) {
+            const int64_t c = i < head ? i : tail + (i - head);
+            to[c] = from_f32<O>(named ? a.scale * to_f32(from[c]) : 0.f);
+        }
 }
 
 // ------------------------------------------------------------------ sort --
 // The number of a token: its row of the table above its place in the list;
 // tokens that do not count come last.
-constexpr int kTile = 2048;      // numbers that a block sorts
-constexpr int kMerge = 8;        // runs merged in one pass
+constexpr int kTile = 512;       // numbers that a block sorts
+constexpr int kMerge = 16;       // runs merged in one pass
 constexpr uint32_t kNone = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t token_of(uint64_t x) { return (uint32_t)(x >> 32); }
 
-__global__ void __launch_bounds__(1024)
+// Bitonic: a thread holds numbers i and i + kTile / 2; partners nearer than a warp
+// are exchanged by shuffles, the others through shared memory.
+__global__ void __launch_bounds__(kTile / 2)
     sort_tiles_kernel(const int32_t* __restrict__ ids, int64_t M, int64_t V,
                       uint64_t* __restrict__ out, ErrWord* err) {
     gemm_ptx::pdl_launch_dependents();
+    constexpr int HALF = kTile / 2;
     __shared__ uint64_t x[kTile];
     gemm_ptx::pdl_wait();
     const int64_t base = (int64_t)blockIdx.x * kTile;
-    const int n = M - base < kTile ? (int)(M - base) : kTile;
-    for (int i = threadIdx.x; i < kTile; i += 1024) {
-        uint64_t v = ~0ull;
-        if (i < n) {
-            const int id = ids[base + i];
-            if (id >= V) report_bad_value(err);
-            v = ((uint64_t)(id >= 0 && id < V ? (uint32_t)id : kNone) << 32) | (uint32_t)(base + i);
-        }
-        x[i] = v;
+    const int i0 = threadIdx.x;
+    uint64_t v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t t = base + i0 + h * HALF;
+        v[h] = ~0ull;  // past the list: after every number
+        if (t >= M) continue;
+        const int id = ids[t];
+        if (id >= V) report_bad_value(err);
+        v[h] = ((uint64_t)(id >= 0 && id < V ? (uint32_t)id : kNone) << 32) | (uint32_t)t;
     }
-    int size = 2;
-    while (size < n) size *= 2;  // of the numbers to sort
-    for (int k = 2; k <= size; k *= 2)
+#pragma unroll
+    for (int k = 2; k <= kTile; k *= 2) {
+#pragma unroll
         for (int j = k / 2; j > 0; j /= 2) {
-            __syncthreads();
-            const int i = threadIdx.x;  // a pair for each thread
-            const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-            if (hi < size) {
-                const uint64_t a = x[lo], b = x[hi];
-                if ((a > b) == ((lo & k) == 0)) {
-                    x[lo] = b;
-                    x[hi] = a;
-                }
+            if (j == HALF) {  // the thread's own two (k == kTile: ascending)
+                const uint64_t lo = v[0] < v[1] ? v[0] : v[1];
+                v[1] = v[0] < v[1] ? v[1] : v[0];
+                v[0] = lo;
+                continue;
+            }
+            uint64_t other[2];
+            if (j < 32) {
+                other[0] = __shfl_xor_sync(0xffffffffu, v[0], j);
+                other[1] = __shfl_xor_sync(0xffffffffu, v[1], j);
+            } else {
+                __syncthreads();
+                x[i0] = v[0];
+                x[i0 + HALF] = v[1];
+                __syncthreads();
+                other[0] = x[i0 ^ j];
+                other[1] = x[(i0 ^ j) + HALF];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = i0 + h * HALF;
+                const bool small = ((i & j) == 0) == ((i & k) == 0);  // keeps the smaller
+                if (small ? other[h] < v[h] : other[h] > v[h]) v[h] = other[h];
             }
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += 1024) out[base + i] = x[i];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (base + i0 + h * HALF < M) out[base + i0 + h * HALF] = v[h];
 }
 
 __global__ void __launch_bounds__(256)
     sort_merge_kernel(const uint64_t* __restrict__ in, uint64_t* __restrict__ out, int64_t M,
-                      int64_t run) {
+                      uint32_t run) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= M) return;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, n = (uint32_t)M;
+    if (i >= n) return;
     const uint64_t x = in[i];
-    const int64_t own = i / run, first = own / kMerge * kMerge;
-    int64_t lo[kMerge], hi[kMerge];
+    const uint32_t own = i / run, first = own / kMerge * kMerge;
+    // how many numbers of each run are below x: binary searches side by side
+    uint32_t lo[kMerge], hi[kMerge];
 #pragma unroll
     for (int r = 0; r < kMerge; ++r) {
-        lo[r] = (first + r) * run;
-        hi[r] = lo[r] + run;
-        if (lo[r] > M) lo[r] = M;
-        if (hi[r] > M) hi[r] = M;
+        const uint64_t begin = (uint64_t)(first + r) * run;
+        lo[r] = begin < n ? (uint32_t)begin : n;
+        hi[r] = begin + run < n ? (uint32_t)(begin + run) : n;
         if (first + r == own) lo[r] = hi[r] = i;  // its place in its own run
     }
-    // The binary searches step by step side by side.
-    for (int64_t width = run; width > 0; width /= 2)
+    for (uint32_t width = run; width > 0; width /= 2)
 #pragma unroll
         for (int r = 0; r < kMerge; ++r)
             if (lo[r] < hi[r]) {
-                const int64_t mid = lo[r] + (hi[r] - lo[r]) / 2;
+                const uint32_t mid = lo[r] + (hi[r] - lo[r]) / 2;
                 if (in[mid] < x) lo[r] = mid + 1;
                 else hi[r] = mid;
             }
-    int64_t at = first * run;
+    uint64_t at = (uint64_t)first * run;
 #pragma unroll
     for (int r = 0; r < kMerge; ++r) {
-        const int64_t begin = (first + r) * run;
-        if (begin < M) at += lo[r] - begin;
+        const uint64_t begin = (uint64_t)(first + r) * run;
+        if (begin < n) at += lo[r] - begin;
     }
     out[at] = x;
 }
@@ -430,11 +433,27 @@ __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGra
     const float* from = a.part + (chunk * 2 + 1) * a.kp + c;
 #pragma unroll
     for (int e = 0; e < G; ++e) sum[e] = from[e];
-#pragma unroll 4
-    for (int64_t k = chunk + 1; k <= last; ++k) {
-        const float* more = a.part + k * 2 * a.kp + c;
+    constexpr int AHEAD = 64 / G;
+    for (int64_t k = chunk + 1; k <= last; k += AHEAD) {
+        float4 more[AHEAD][G / 4];
 #pragma unroll
-        for (int e = 0; e < G; ++e) sum[e] += more[e];
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q)
+                if (k + j <= last)
+                    more[j][q] =
+                        reinterpret_cast<const float4*>(a.part + (k + j) * 2 * a.kp + c)[q];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (k + j <= last) {
+#pragma unroll
+                for (int q = 0; q < G / 4; ++q) {
+                    sum[4 * q] += more[j][q].x;
+                    sum[4 * q + 1] += more[j][q].y;
+                    sum[4 * q + 2] += more[j][q].z;
+                    sum[4 * q + 3] += more[j][q].w;
+                }
+            }
     }
     write_sum<O, G>(a, token, c, sum);
 }
@@ -460,12 +479,13 @@ int embed(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* table
     rc = check_device_pointers(ptrs, 3, dev->device);
     if (rc != kOk) return rc;
     const EmbedArgs a{M, V, K, ids, table, ldt, scale, y, ldy, dev->err_word};
-    int threads = 32;  // of a row: 8 elements each, as near as a block has
-    while (threads < 256 && threads * 8 < K) threads *= 2;
-    const int64_t blocks = (M + 256 / threads - 1) / (256 / threads);
-    const int64_t most = (int64_t)dev->sm_count * 8;
-    const dim3 grid((unsigned)(blocks < most ? blocks : most));
-    auto run = [&](auto kern) { return launch_dependent(kern, grid, dim3(256), 0, s, a, threads); };
+    const int64_t group = 16 / (os > ts ? os : ts);
+    const int64_t pieces = (K + group * 32 * kPieces - 1) / (group * 32 * kPieces);
+    if (M * pieces > (int64_t)INT32_MAX * 8) return kUnsupported;
+    const dim3 grid((unsigned)((M * pieces + 7) / 8));
+    auto run = [&](auto kern) {
+        return launch_dependent(kern, grid, dim3(256), 0, s, a, (int)pieces);
+    };
     switch (dtype) {
         case GEMM_F32: return run(embed_kernel<float, float>);
         case GEMM_F16_F32: return run(embed_kernel<__half, float>);
@@ -520,10 +540,10 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
         uint64_t* in = reinterpret_cast<uint64_t*>(mem);
         uint64_t* out = reinterpret_cast<uint64_t*>(mem + list);
         rc = launch_dependent(sort_tiles_kernel, dim3((unsigned)((M + kTile - 1) / kTile)),
-                              dim3(1024), 0, s, ids, M, V, in, dev->err_word);
+                              dim3(kTile / 2), 0, s, ids, M, V, in, dev->err_word);
         for (int64_t run = kTile; rc == kOk && run < M; run *= kMerge) {
             rc = launch_dependent(sort_merge_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256),
-                                  0, s, (const uint64_t*)in, out, M, run);
+                                  0, s, (const uint64_t*)in, out, M, (uint32_t)run);
             std::swap(in, out);
         }
         a.sorted = in;

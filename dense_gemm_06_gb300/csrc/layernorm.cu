@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/gemm.h"
 #include "internal.h"
@@ -205,14 +206,35 @@ struct NormGradArgs {
 
 constexpr int kOwn = 16;  // columns of a thread in the backward kernel
 
-// A block of WARPS x LANES warps: LANES rows at a time, each on WARPS warps
+// A copy of BYTES (4, 8 or 16) into shared memory that this thread waits for itself.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"(gemm_ptx::smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                     :: "r"(gemm_ptx::smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
+// Rows on their way to a thread, the one that it works on included. With 16-bit
+// rows of 2048, 128 threads and three blocks on an SM that is 96 KB in flight.
+template <typename T> constexpr int kNormStages = sizeof(T) == 2 ? 4 : 3;
+
+// A block of WARPS x LANES warps: LANES rows side by side, each on WARPS warps
 // (LANES > 1 only with one warp a row). Thread tid of a row owns the columns
-// (i TR + tid) VEC + e, i < kOwn / VEC.
+// (i TR + tid) VEC + e, i < kOwn / VEC. It copies its own parts of the next rows
+// into its own shared memory (single 16-bit elements, which the copies do not
+// take, into registers), so that the copies need no barrier.
 template <typename T, typename W, int WARPS, int LANES, int VEC>
 __global__ void __launch_bounds__(32 * WARPS * LANES)
     norm_grad_kernel(const NormGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
-    constexpr int TR = 32 * WARPS, NV = kOwn / VEC;
+    constexpr int TR = 32 * WARPS, NV = kOwn / VEC, THREADS = TR * LANES;
+    constexpr int BYTES = VEC * (int)sizeof(T), STAGES = kNormStages<T>;
+    constexpr bool RING = BYTES >= 4;
+    using V = Pack<T, VEC>;
+    extern __shared__ __align__(16) uint8_t ring[];  // STAGES x (x, dy) x NV x THREADS vectors
     __shared__ float slots[2][2 * WARPS];
     __shared__ float merge[LANES > 1 ? (LANES - 1) * TR * 2 : 1];
     const int tid = threadIdx.x % TR, sub = threadIdx.x / TR;
@@ -229,34 +251,56 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
     float dw[kOwn] = {}, db[kOwn] = {};
     const float inv = 1.f / (float)a.N;
     const int64_t step = (int64_t)gridDim.x * LANES;
-    int64_t row = (int64_t)blockIdx.x * LANES + sub;
-    Pack<T, VEC> xv[NV], gv[NV];
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&](int64_t r) {
-        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-        const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
-        mean = a.mean[r];
-        rstd = a.rstd[r];
+    const int64_t row0 = (int64_t)blockIdx.x * LANES + sub;
+    auto slot = [&](int stage, int which, int i) {
+        return reinterpret_cast<V*>(ring) + ((stage * 2 + which) * NV + i) * THREADS + threadIdx.x;
+    };
+    V xv[NV], gv[NV];
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.M) {
+            const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+            const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TR + tid) * VEC;
-            if (c < a.N) {
-                xv[i] = *reinterpret_cast<const Pack<T, VEC>*>(x + c);
-                gv[i] = *reinterpret_cast<const Pack<T, VEC>*>(dy + c);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TR + tid) * VEC;
+                if (c >= a.N) continue;
+                if constexpr (RING) {
+                    copy_async<BYTES>(slot(stage, 0, i), x + c);
+                    copy_async<BYTES>(slot(stage, 1, i), dy + c);
+                } else {
+                    xv[i] = *reinterpret_cast<const V*>(x + c);
+                    gv[i] = *reinterpret_cast<const V*>(dy + c);
+                }
             }
         }
+        if constexpr (RING) asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (row < a.M) fetch(row);
-    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+    if constexpr (RING) {
+        for (int k = 0; k < STAGES - 1; ++k) fetch(row0 + k * step, k);
+    } else {
+        fetch(row0, 0);
+    }
+    float mean = 0.f, rstd = 0.f;
+    if (row0 < a.M) mean = a.mean[row0], rstd = a.rstd[row0];
+    int turn = 0, stage = 0;
+    for (int64_t row = row0; row < a.M; row += step, turn ^= 1) {
         float h[kOwn], g[kOwn], s[2] = {0.f, 0.f};
-        const float r = rstd;
+        const float r = rstd, m = mean;
+        if constexpr (RING) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 2) : "memory");
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                xv[i] = *slot(stage, 0, i);
+                gv[i] = *slot(stage, 1, i);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const bool in = (i * TR + tid) * VEC < a.N;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int k = i * VEC + e;
-                h[k] = in ? (to_f32(xv[i].v[e]) - mean) * r : 0.f;
+                h[k] = in ? (to_f32(xv[i].v[e]) - m) * r : 0.f;
                 const float d = in ? to_f32(gv[i].v[e]) : 0.f;
                 dw[k] = fmaf(d, h[k], dw[k]);
                 db[k] += d;
@@ -265,7 +309,12 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
                 s[1] = fmaf(g[k], h[k], s[1]);
             }
         }
-        if (row + step < a.M) fetch(row + step);  // the next row's reads beside this one's sums
+        // the next rows' reads beside this one's sums (the stage that was read the
+        // round before)
+        if constexpr (RING) fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+        else fetch(row + step, 0);
+        if (row + step < a.M) mean = a.mean[row + step], rstd = a.rstd[row + step];
+        if (++stage == STAGES) stage = 0;
         if (a.dx) {
             row_sum<WARPS, 2>(s, slots[turn]);
             const float c0 = s[0] * inv, c1 = s[1] * inv;
@@ -274,16 +323,17 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TR + tid) * VEC;
                 if (c >= a.N) continue;
-                Pack<T, VEC> o;
+                V o;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int k = i * VEC + e;
                     o.v[e] = from_f32<T>(r * (g[k] - c0 - h[k] * c1));
                 }
-                *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o;
+                *reinterpret_cast<V*>(dx + c) = o;
             }
         }
     }
+    if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.N;
 #pragma unroll
@@ -361,8 +411,8 @@ __global__ void __launch_bounds__(256) norm_grad_long_sums_kernel(const NormGrad
     part[a.N + c] = v;
 }
 
-// dweight and dbias: the blocks' sums, added in their order within 8 shares.
-constexpr int kShares = 8;
+// dweight and dbias: the blocks' sums, added in their order within 32 shares.
+constexpr int kShares = 32;
 template <typename W>
 __global__ void __launch_bounds__(32 * kShares)
     norm_join_kernel(const float* __restrict__ part, int blocks, int N, W* __restrict__ dweight,
@@ -379,8 +429,12 @@ __global__ void __launch_bounds__(32 * kShares)
     }
     got[share][lane] = s;
     __syncthreads();
+    for (int o = kShares / 2; o; o /= 2) {
+        if (share < o) got[share][lane] += got[share + o][lane];
+        __syncthreads();
+    }
     if (share > 0 || c >= 2 * (int64_t)N) return;
-    for (int i = 1; i < kShares; ++i) s += got[i][lane];
+    s = got[0][lane];
     W* out = c < N ? dweight : dbias;
     if (!out) return;
     W* at = out + (c < N ? c : c - N);
@@ -451,11 +505,32 @@ GradPlan grad_plan(int64_t M, int64_t N, int sm_count) {
     if (N > 32 * 16 * kOwn) return g;
     g.lanes = g.warps == 1 ? 4 : 1;
     const int64_t rows = (M + g.lanes - 1) / g.lanes;
-    const int64_t most = (int64_t)sm_count * (16 / (g.warps * g.lanes));
+    const int64_t most = (int64_t)sm_count * (12 / (g.warps * g.lanes) < 1 ? 1 : 12 / (g.warps * g.lanes));
     g.blocks = (int)(rows < most ? rows : most);
     return g;
 }
 constexpr int kLongShares = 32;
+
+template <typename T, typename W, int WARPS, int LANES, int VEC>
+int run_norm_grad(const NormGradArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t s) {
+    constexpr int THREADS = 32 * WARPS * LANES;
+    constexpr int SMEM = VEC * sizeof(T) >= 4 ? kNormStages<T> * 2 * kOwn * (int)sizeof(T) * THREADS
+                                              : 0;
+    auto kern = norm_grad_kernel<T, W, WARPS, LANES, VEC>;
+    if constexpr (SMEM > 40 * 1024) {
+        static std::mutex mu;
+        static uint64_t configured = 0;  // bit per device
+        std::lock_guard<std::mutex> lock(mu);
+        const uint64_t bit = 1ull << (dev.device & 63);
+        if (!(configured & bit)) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
+                cudaSuccess)
+                return kCuda;
+            configured |= bit;
+        }
+    }
+    return launch_dependent(kern, dim3(blocks), dim3(THREADS), SMEM, s, a);
+}
 
 template <typename T, typename W>
 int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const DeviceInfo& dev,
@@ -472,11 +547,9 @@ int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const Device
     const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.dy, a.lddy, sizeof(T)) &&
                      (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) && a.N % (16 / sizeof(T)) == 0;
     if (a.M > 0 && g.blocks > 0) {
-#define NORM_GRAD_RUN(WARPS, LANES)                                                            \
-    rc = vec ? launch_dependent(norm_grad_kernel<T, W, WARPS, LANES, 16 / (int)sizeof(T)>,     \
-                                dim3(g.blocks), dim3(32 * WARPS * LANES), 0, s, a)             \
-             : launch_dependent(norm_grad_kernel<T, W, WARPS, LANES, 1>, dim3(g.blocks),       \
-                                dim3(32 * WARPS * LANES), 0, s, a)
+#define NORM_GRAD_RUN(WARPS, LANES)                                                        \
+    rc = vec ? run_norm_grad<T, W, WARPS, LANES, 16 / (int)sizeof(T)>(a, g.blocks, dev, s) \
+             : run_norm_grad<T, W, WARPS, LANES, 1>(a, g.blocks, dev, s)
         switch (g.warps) {
             case 1: NORM_GRAD_RUN(1, 4); break;
             case 2: NORM_GRAD_RUN(2, 1); break;

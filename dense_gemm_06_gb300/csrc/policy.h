@@ -406,20 +406,27 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
 // the vocabulary). CTA pairs on 256 x 256, but single CTAs on 128 rows where at
 // most 128 rows make half of a pair's tile padding, or where pairs would leave
 // more than half of the SMs idle; these take 64 columns if all tiles then still
-// run at once, else 128.
+// run at once, else 128. The forward pass of at most 128 rows is bound by reading
+// W, so its tiles divide the columns evenly over whole rounds of the SMs (32000
+// columns on 152 SMs: 2 rounds of 112).
 constexpr int64_t kXentMaxVocab = 1 << 24;
 struct XentShape {
     int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
     int tile_n;
 };
-inline XentShape plan_xent(int64_t M, int64_t N, int sm_count) {
+inline XentShape plan_xent(int64_t M, int64_t N, int sm_count, bool forward) {
     const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
     if (M > 128 && pairs * 4 >= sm_count) return XentShape{2, 256};
+    if (forward && M <= 128) {
+        const int64_t rounds = (N + 128 * (int64_t)sm_count - 1) / (128 * (int64_t)sm_count);
+        const int64_t each = (N + rounds * sm_count - 1) / (rounds * sm_count);
+        return XentShape{1, each <= 32 ? 32 : (int)((each + 15) / 16 * 16)};
+    }
     return XentShape{1, ((M + 127) / 128) * ((N + 63) / 64) <= sm_count ? 64 : 128};
 }
 
 // Rows of gemm_xent that run together: a whole number of tiles whose partial
-// maxima and sums (16 bytes for every row and tile of 64 columns or more) stay
+// maxima and sums (16 bytes for every row and tile of 32 columns or more) stay
 // within 256 MB.
 inline int64_t xent_panel_rows(int64_t M, int64_t N, int tile_n) {
     const int64_t per_row = (N + tile_n - 1) / tile_n * 16;
@@ -441,11 +448,11 @@ inline int64_t xent_piece_cols(int64_t rows, int64_t N, int parts) {
 }
 
 // embed_rows_grad: sorted tokens of a chunk, which a block (for each share of the
-// columns) adds up: 16, longer for so many tokens that there would be more than
-// 8192 chunks.
+// columns) adds up: 16, up to 64 for so many tokens that there would be more than
+// 1024 chunks, and longer where there would be more than 8192.
 inline int embed_chunk(int64_t M) {
-    const int64_t n = (M + 8191) / 8192;
-    return (int)(n < 16 ? 16 : n);
+    const int64_t n = (M + 1023) / 1024, most = (M + 8191) / 8192;
+    return (int)(most > 64 ? most : n < 16 ? 16 : n > 64 ? 64 : n);
 }
 
 }  // namespace libgemm

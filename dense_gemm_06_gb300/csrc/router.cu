@@ -40,6 +40,18 @@ __device__ __forceinline__ float max32(float v) {
     return v;
 }
 
+// *p of the block `rank` of the cluster.
+template <typename T>
+__device__ __forceinline__ T ld_cluster(const T* p, int rank) {
+    static_assert(sizeof(T) == 4, "words");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];"
+                 : "=r"(v)
+                 : "r"(gemm_ptx::mapa_shared(gemm_ptx::smem_u32(p), (uint32_t)rank))
+                 : "memory");
+    return *reinterpret_cast<T*>(&v);
+}
+
 // A row's probabilities: NE of them in each lane, expert lane + 32 i.
 template <int NE>
 __device__ __forceinline__ void softmax_row(float (&v)[NE]) {
@@ -80,24 +92,33 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs 
     gemm_ptx::pdl_wait();
     float total[NE] = {};
     int rows = 0;
+    auto count = [&](int e) {
+        if (e >= a.E) report_bad_value(a.err);
+        else if (e >= 0) atomicAdd(&counts[e], 1);
+    };
     const int64_t step = (int64_t)gridDim.x * kWarps;
     for (int64_t t0 = (int64_t)blockIdx.x * kWarps + warp; t0 < a.T; t0 += ROWS * step) {
         float v[ROWS][NE];
+        int first[ROWS];
         bool in[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int64_t t = t0 + r * step;
-            in[r] = t < a.T && a.expert[t * a.top] >= 0;
             const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
+            // read whether the row counts or not, so that one latency covers both
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                v[r][i] = in[r] && lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : -INFINITY;
-            if (in[r])
-                for (int k = lane; k < a.top; k += 32) {
-                    const int e = a.expert[t * a.top + k];
-                    if (e >= a.E) report_bad_value(a.err);
-                    else if (e >= 0) atomicAdd(&counts[e], 1);
-                }
+                v[r][i] = t < a.T && lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : -INFINITY;
+            first[r] = -1;
+            if (t < a.T && lane < a.top) first[r] = a.expert[t * a.top + lane];
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            in[r] = __shfl_sync(0xffffffffu, first[r], 0) >= 0;
+            if (!in[r]) continue;
+            count(first[r]);
+            for (int k = lane + 32; k < a.top; k += 32)
+                count(a.expert[(t0 + r * step) * a.top + k]);
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
@@ -122,28 +143,37 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs 
     }
 }
 
-// One block: the blocks' sums and counts, the limits and the loss. `shares`
-// threads an expert (a power of two), each a share of the blocks.
-__global__ void __launch_bounds__(1024)
+// A cluster of kJoin blocks: each adds up its share of the blocks' sums and
+// counts, the first one the shares, and writes the limits and the loss. `shares`
+// threads an expert (a power of two), each a share of the block's.
+constexpr int kJoin = 8;
+__global__ void __cluster_dims__(kJoin, 1, 1) __launch_bounds__(1024)
     balance_join_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_n,
                         int blocks, int E, int top, int shares, int32_t* __restrict__ counts,
                         int32_t* __restrict__ offsets, float* __restrict__ prob,
                         float* __restrict__ loss) {
     gemm_ptx::pdl_launch_dependents();
     __shared__ float p[1024];
-    __shared__ int32_t c[1025], rows_of[1024];
+    __shared__ int32_t c[1024], warp_n[32];
+    __shared__ float warp_f[32];
+    __shared__ int32_t all_rows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)gemm_ptx::cluster_ctarank();
     gemm_ptx::pdl_wait();
-    // the rows that count
-    int n = 0;
-    for (int b = threadIdx.x; b < blocks; b += 1024) n += part_n[(int64_t)b * (E + 1) + E];
-    rows_of[threadIdx.x] = n;
+    const int b0 = (int)((int64_t)blocks * rank / kJoin);
+    const int b1 = (int)((int64_t)blocks * (rank + 1) / kJoin);
+    int n = 0;  // rows that count
+    for (int b = b0 + threadIdx.x; b < b1; b += 1024) n += part_n[(int64_t)b * (E + 1) + E];
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) warp_n[warp] = n;
     // an expert's shares lie a whole number of experts apart
-    const int e = threadIdx.x % (1024 / shares), share = threadIdx.x / (1024 / shares);
+    const int wide = 1024 / shares;
+    const int e = threadIdx.x % wide, share = threadIdx.x / wide;
     float s = 0.f;
     int32_t k = 0;
     if (e < E) {
 #pragma unroll 8
-        for (int b = share; b < blocks; b += shares) {
+        for (int b = b0 + share; b < b1; b += shares) {
             s += part_p[(int64_t)b * E + e];
             k += part_n[(int64_t)b * (E + 1) + e];
         }
@@ -151,49 +181,65 @@ __global__ void __launch_bounds__(1024)
     p[threadIdx.x] = s;
     c[threadIdx.x] = k;
     __syncthreads();
-    for (int o = 512; o; o /= 2) {
-        if (threadIdx.x < o) rows_of[threadIdx.x] += rows_of[threadIdx.x + o];
-        __syncthreads();
-    }
-    n = rows_of[0];
     for (int o = shares / 2; o; o /= 2) {
         if (share < o) {
-            p[threadIdx.x] += p[threadIdx.x + o * (1024 / shares)];
-            c[threadIdx.x] += c[threadIdx.x + o * (1024 / shares)];
+            p[threadIdx.x] += p[threadIdx.x + o * wide];
+            c[threadIdx.x] += c[threadIdx.x + o * wide];
         }
         __syncthreads();
     }
+    if (warp == 0) {
+        n = __reduce_add_sync(0xffffffffu, warp_n[lane]);
+        if (lane == 0) all_rows = n;
+    }
+    gemm_ptx::cluster_sync_all();
+    const bool mine = rank == 0 && threadIdx.x < E;
+    int32_t own = 0;
+    s = 0.f;
+    n = 0;
+    if (rank == 0) {
+        for (int r = 0; r < kJoin; ++r) {
+            n += ld_cluster(&all_rows, r);
+            if (mine) {
+                s += ld_cluster(&p[threadIdx.x], r);
+                own += ld_cluster(&c[threadIdx.x], r);
+            }
+        }
+    }
+    gemm_ptx::cluster_sync_all();  // no block leaves, or writes, while its sums are read
+    if (rank != 0) return;
     const int m = n > 0 ? n : 1;
     float term = 0.f;
-    const bool mine = threadIdx.x < E;  // share 0
     if (mine) {
-        const float mean = p[threadIdx.x] / (float)m;
-        counts[threadIdx.x] = c[threadIdx.x];
+        const float mean = s / (float)m;
+        counts[threadIdx.x] = own;
         prob[threadIdx.x] = mean;
-        term = (float)((double)c[threadIdx.x] / ((double)top * m)) * mean;
+        term = (float)((double)own / ((double)top * m)) * mean;
     }
-    if (threadIdx.x == 0) counts[E] = n;
-    const int32_t own = mine ? c[threadIdx.x] : 0;
+    // the limits: a sum up to each expert; the loss: a sum in a fixed order
+    int32_t upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t add = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += add;
+    }
+    term = sum32(term);
+    if (lane == 31) warp_n[warp] = upto;
+    if (lane == 0) warp_f[warp] = term;
     __syncthreads();
-    // the limits: an inclusive sum over the experts; the loss: a sum in a fixed order
-    p[threadIdx.x] = term;
-    c[threadIdx.x] = own;
-    __syncthreads();
-    for (int o = 1; o < 1024; o *= 2) {
-        const int32_t add = threadIdx.x >= o ? c[threadIdx.x - o] : 0;
-        __syncthreads();
-        c[threadIdx.x] += add;
-        __syncthreads();
-    }
-    for (int o = 512; o; o /= 2) {
-        if (threadIdx.x < o) p[threadIdx.x] += p[threadIdx.x + o];
-        __syncthreads();
-    }
     if (offsets) {
-        if (mine) offsets[threadIdx.x + 1] = c[threadIdx.x];
+        int32_t before = lane < warp ? warp_n[lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (mine) offsets[threadIdx.x + 1] = before + upto;
         if (threadIdx.x == 0) offsets[0] = 0;
     }
-    if (threadIdx.x == 0) *loss = (float)E * p[0];
+    if (warp == 0) {
+        term = sum32(warp_f[lane]);
+        if (lane == 0) {
+            *loss = (float)E * term;
+            counts[E] = n;
+        }
+    }
 }
 
 struct BalanceGradArgs {
@@ -232,7 +278,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_grad_kernel(const Balance
             const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                v[r][i] = in[r] && lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : -INFINITY;
+                v[r][i] = t < a.T && lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : -INFINITY;
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
@@ -263,15 +309,16 @@ bool rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int es) {
 }
 
 // Calls f with an integral constant NE (numbers of a lane) and ROWS (rows in
-// flight: 16 numbers a lane at most, and four rows).
+// flight: 32 numbers a lane at most, and four rows).
 template <typename F>
 int with_lanes(int E, F&& f) {
     using std::integral_constant;
     if (E <= 32) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
     if (E <= 64) return f(integral_constant<int, 2>{}, integral_constant<int, 4>{});
     if (E <= 128) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-    if (E <= 256) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-    if (E <= 512) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    if (E <= 192) return f(integral_constant<int, 6>{}, integral_constant<int, 4>{});
+    if (E <= 256) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    if (E <= 512) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
     return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
 }
 
@@ -330,7 +377,7 @@ int balance(int64_t T, int64_t E, int64_t top, const void* logits, int64_t ldl,
     if (rc == kOk) {
         int shares = 1;
         while (shares * 2 * E <= 1024) shares *= 2;
-        rc = launch_dependent(balance_join_kernel, dim3(1), dim3(1024), 0, s,
+        rc = launch_dependent(balance_join_kernel, dim3(kJoin), dim3(1024), 0, s,
                               (const float*)a.part_p, (const int32_t*)a.part_n, (int)blocks,
                               (int)E, (int)top, shares, counts, offsets, prob, loss);
     }

@@ -20,7 +20,8 @@
 // Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
 // relative 2^-9 (bf16) is below the rounding of a 16-bit result. An fp32 dW would
 // show it, so for that G is two numbers, hi + lo (2^-17 of g), and X is multiplied
-// with both in one product of twice the depth, hi below lo. fp16 has the exponents
+// with both in one product of twice the depth, on gemm_grouped_k's kernel, which
+// adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384). fp16 has the exponents
 // for that only near 1: G is scaled by a power of two that brings the largest
 // |alpha dloss| to 2^12, its small probabilities then reach down to 2^-36 of it,
 // and the products go through fp32 scratch from which they are scaled back.
@@ -53,17 +54,20 @@ bool span_fits(int64_t rows, int64_t cols, int64_t ld, int esize) {
     return (__int128)(rows - 1) * ld + cols <= (__int128)(INT64_MAX / esize);
 }
 
-// Joins the pairs of a row: warps take every 8th half tile, lanes a row each.
-constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(32 * kJoinWarps)
+// Joins the pairs of a row: a block takes ROWS rows, its threads a row and every
+// (kJoinThreads / ROWS)th half tile of it each.
+constexpr int kJoinThreads = 512;
+template <int ROWS>
+__global__ void __launch_bounds__(kJoinThreads)
     xent_join_kernel(const float2* __restrict__ part, int64_t ld, int parts, int M,
                      const float* __restrict__ picked, const int32_t* __restrict__ target,
                      int vocab, float* __restrict__ loss, float* __restrict__ lse) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
-    __shared__ float2 got[kJoinWarps][32];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 32 + lane;
+    constexpr int SHARES = kJoinThreads / ROWS, AHEAD = 8;
+    __shared__ float2 got[SHARES][ROWS];
+    const int share = threadIdx.x / ROWS, r = threadIdx.x % ROWS;
+    const int row = blockIdx.x * ROWS + r;
     float m = -INFINITY, s = 0.f;
     auto join = [&](float2 o) {
         const float nm = fmaxf(m, o.x);
@@ -73,20 +77,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     };
     if (row < M) {
         const float2* at = part + row;
-        int i = w;
-        for (; i + 3 * kJoinWarps < parts; i += 4 * kJoinWarps) {
-            float2 v[4];
+        for (int i = share; i < parts; i += AHEAD * SHARES) {
+            float2 v[AHEAD];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = at[(int64_t)(i + j * kJoinWarps) * ld];
+            for (int j = 0; j < AHEAD; ++j)
+                v[j] = i + j * SHARES < parts ? at[(int64_t)(i + j * SHARES) * ld]
+                                              : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) join(v[j]);
+            for (int j = 0; j < AHEAD; ++j) join(v[j]);
         }
-        for (; i < parts; i += kJoinWarps) join(at[(int64_t)i * ld]);
     }
-    got[w][lane] = make_float2(m, s);
-    __syncthreads();
-    if (w != 0 || row >= M) return;
-    for (int i = 1; i < kJoinWarps; ++i) join(got[i][lane]);
+    got[share][r] = make_float2(m, s);
+    for (int o = SHARES / 2; o; o /= 2) {
+        __syncthreads();
+        if (share < o) {
+            join(got[share + o][r]);
+            got[share][r] = make_float2(m, s);
+        }
+    }
+    if (share != 0 || row >= M) return;
     const float l = m + logf(s);
     if (lse) lse[row] = l;
     const int t = target[row];
@@ -107,12 +116,17 @@ __global__ void xent_uniform_kernel(int M, int vocab, const int32_t* target, flo
 
 // The rows of X that count, in rows of TMA's alignment; the others, and those
 // from M to `rows`, zero. With copies == 2 the same again below. A warp per row.
+// limits: {0, rows * copies}, the depth of dW's product.
 __global__ void __launch_bounds__(256)
     xent_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, int M, int64_t K,
                      const int32_t* __restrict__ target, int vocab, uint16_t* __restrict__ out,
-                     int64_t ldo, int rows, int copies) {
+                     int64_t ldo, int rows, int copies, int32_t* __restrict__ limits) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        limits[0] = 0;
+        limits[1] = rows * copies;
+    }
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
     for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
@@ -249,9 +263,13 @@ void xent_params(XentParams& xp, int64_t M, int64_t N, int64_t K, const XentShap
     xp.M = (int)M;
     xp.N = (int)N;
     xp.num_kb = (int)((K + XBK - 1) / XBK);
+    const int parts = (xp.num_kb + kXentFold - 1) / kXentFold;
+    xp.part_kb = (xp.num_kb + parts - 1) / parts;
     xp.tile_n = shape.tile_n;
     xp.tiles_m = (int)((M + XROWS * shape.cta_group - 1) / (XROWS * shape.cta_group));
     xp.tiles_n = (int)((N + shape.tile_n - 1) / shape.tile_n);
+    xp.x_rows = M < XROWS ? (int)up(M, 8) : XROWS;
+    xp.stage_bytes = (xp.x_rows + shape.tile_n) * XBK * 2;
     xp.band = 8;
     xp.vocab = (int)vocab;
     xp.target = target;
@@ -262,10 +280,17 @@ void xent_params(XentParams& xp, int64_t M, int64_t N, int64_t K, const XentShap
     xp.fault_inject = option_tc_fault_inject();
 }
 
+// The stages that fit the ring of a mode.
+int stages_of(const XentParams& xp, int mode) {
+    const int ring = mode == kXentGrad2 ? XentCfg<kXentGrad2>::RING : XentCfg<kXentGrad>::RING;
+    const int n = ring / xp.stage_bytes;
+    return n < XentCfg<kXentStats>::MOST ? n : XentCfg<kXentStats>::MOST;
+}
+
 bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void* W, int64_t ldw,
                int64_t K, const XentShape& shape) {
     return encode_tma_16(&xp.map_x, bf16, X, (uint64_t)K, (uint64_t)xp.M, (uint64_t)ldx, 0, 0, XBK,
-                         XROWS) &&
+                         shape.cta_group == 2 ? XROWS : (uint32_t)xp.x_rows) &&
            encode_tma_16(&xp.map_w, bf16, W, (uint64_t)K, (uint64_t)xp.N, (uint64_t)ldw, 0, 0, XBK,
                          (uint32_t)(shape.tile_n / shape.cta_group));
 }
@@ -273,6 +298,7 @@ bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void
 int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const DeviceInfo& dev,
            cudaStream_t s) {
     if ((int64_t)xp.tiles_m * xp.tiles_n * 2 > INT32_MAX) return kUnsupported;
+    xp.stages = stages_of(xp, mode);
     const int rc = bf16 ? launch_xent_bf16(xp, mode, shape.cta_group, dev, s)
                         : launch_xent_f16(xp, mode, shape.cta_group, dev, s);
     dispatch_log("cross entropy %s %dx%d, %d k-blocks: %s, %d x %d tiles of %d columns",
@@ -304,7 +330,7 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
         return kOk;
     }
     const bool bf16 = is_bf16(dtype);
-    const XentShape shape = plan_xent(M, N, dev->sm_count);
+    const XentShape shape = plan_xent(M, N, dev->sm_count, true);
     const int64_t panel = xent_panel_rows(M, N, shape.tile_n);
     const int64_t parts = (N + shape.tile_n - 1) / shape.tile_n * 2;
     Parts at;
@@ -331,10 +357,16 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
         xp.picked = reinterpret_cast<float*>(mem + picked_at);
         rc = launch(xp, kXentStats, bf16, shape, *dev, s);
         if (rc != kOk) break;
-        rc = launch_dependent(xent_join_kernel, dim3((unsigned)((m + 31) / 32)),
-                              dim3(32 * kJoinWarps), 0, s, (const float2*)xp.part, xp.part_ld,
-                              (int)parts, (int)m, (const float*)xp.picked, target + r0, (int)N,
-                              loss + r0, lse ? lse + r0 : nullptr);
+        // few rows: more threads for each
+        const int rows = m <= 2 * dev->sm_count ? 2 : m <= 8 * dev->sm_count ? 8 : 32;
+        auto join = [&](auto kern) {
+            return launch_dependent(kern, dim3((unsigned)((m + rows - 1) / rows)),
+                                    dim3(kJoinThreads), 0, s, (const float2*)xp.part, xp.part_ld,
+                                    (int)parts, (int)m, (const float*)xp.picked, target + r0,
+                                    (int)N, loss + r0, lse ? lse + r0 : nullptr);
+        };
+        rc = rows == 2 ? join(xent_join_kernel<2>)
+                       : rows == 8 ? join(xent_join_kernel<8>) : join(xent_join_kernel<32>);
     }
     scratch.release();
     return rc;
@@ -351,6 +383,17 @@ int product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, int a_m
                           resolve_tc_options(M, N, K, A, lda, a_major, B, ldb, b_major, C, ldc,
                                              GEMM_MAJOR_MN, dtype),
                           s);
+}
+
+// The same for fp32 results of a depth that the tensor core's cut-off additions
+// would show in: sum over t of A[t][m] B[t][n] on the product that folds its sums.
+// limits: {0, depth} in device memory.
+int product_folded(int64_t M, int64_t N, int64_t depth, const void* A, int64_t lda, const void* B,
+                   int64_t ldb, float* C, int64_t ldc, int dtype, float beta,
+                   const int32_t* limits, cudaStream_t s) {
+    const gemm_epilogue epi{1.f, beta, nullptr, GEMM_ACT_NONE};
+    return gemm_grouped_k(1, M, N, depth, limits, A, lda, B, ldb, C, ldc, M * ldc, dtype,
+                          beta != 0.f ? &epi : nullptr, s);
 }
 
 int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
@@ -387,7 +430,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const int parts = dW && we == 4 ? 2 : 1;  // numbers that hold an entry of G
     const bool scaled = !bf16;
     const int64_t piece = xent_piece_cols(up(M, 256), N, parts);
-    const XentShape shape = plan_xent(M, piece, dev->sm_count);  // of every piece
+    const XentShape shape = plan_xent(M, piece, dev->sm_count, false);  // of every piece
     const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
     const int64_t pieces = (N + piece - 1) / piece;
     const bool sum_dx = dX && (pieces > 1 || scaled);
@@ -400,12 +443,14 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const int64_t dx_at = sum_dx ? at.add(M * up(K, 4) * 4) : -1;
     const int64_t dw_at = dW && scaled ? at.add(piece * up(K, 4) * 4) : -1;
     const int64_t scale_at = scaled ? at.add(8) : -1;
+    const int64_t limits_at = at.add(8);
     Scratch scratch{pool, s, dev->device};
     char* mem = static_cast<char*>(scratch.get((size_t)at.bytes));
     if (!mem) return kCuda;
     float* scale = scaled ? reinterpret_cast<float*>(mem + scale_at) : nullptr;
     float* dx_sum = sum_dx ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
     float* dw_sum = dw_at >= 0 ? reinterpret_cast<float*>(mem + dw_at) : nullptr;
+    int32_t* limits = reinterpret_cast<int32_t*>(mem + limits_at);
     char* g = mem + g_at;
 
     const void* xc = X;  // rows that count, aligned
@@ -417,7 +462,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
                                                                          : dev->sm_count * 8)),
                               dim3(256), 0, s, static_cast<const uint16_t*>(X), ldx, (int)M, K,
                               target, (int)N, reinterpret_cast<uint16_t*>(mem + x_at), ldk, rows,
-                              parts);
+                              parts, limits);
         xc = mem + x_at;
         ldxc = ldk;
     }
@@ -454,11 +499,15 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
         const int64_t depth = (int64_t)rows * parts;
         if (!scaled) {
-            rc = product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dst, lddw,
-                         dtype, beta, *dev, s);
+            rc = parts == 2 ? product_folded(n, K, depth, g, ldg, xc, ldxc,
+                                             static_cast<float*>(dst), lddw, f32, beta, limits, s)
+                            : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN,
+                                      dst, lddw, same, beta, *dev, s);
         } else {
-            rc = product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dw_sum,
-                         up(K, 4), f32, 0.f, *dev, s);
+            rc = parts == 2 ? product_folded(n, K, depth, g, ldg, xc, ldxc, dw_sum, up(K, 4), f32,
+                                             0.f, limits, s)
+                            : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN,
+                                      dw_sum, up(K, 4), f32, 0.f, *dev, s);
             if (rc == kOk)
                 rc = finish(dw_sum, up(K, 4), dst, lddw, n, K, scale + 1, beta, we, bf16, *dev, s);
         }

@@ -10,10 +10,17 @@
 //
 // The pipeline is the dense kernel's: warp 0 copies 64-deep blocks of X and W by
 // TMA into a ring, warp 1 issues the MMAs (a CTA pair on 256 x 256 tiles, or one
-// CTA on 128 rows by 64 or 128 columns) into one of two TMEM accumulators, and
+// CTA on 128 rows by up to 128 columns) into one of two TMEM accumulators, and
 // eight warps read the other one. A tile row is one TMEM lane, so one thread sees
 // 64 columns of a row at a time: the softmax needs no exchange between threads,
-// and per element one maximum, one fma, one ex2 and one addition. With K = 2048
+// and per element one maximum, one fma, one ex2 and one addition.
+//
+// The tensor core cuts off what an addition shifts below its last bits, so a long
+// sum of products drifts towards zero by about half a step for every 16 of depth:
+// losses of K = 2048 were off by 6e-6 of themselves. So an accumulator takes at
+// most kXentFold blocks of depth, and the epilogue warps add up those parts in
+// registers, rounded to nearest (128 numbers a thread; the warps that only issue
+// copies and MMAs hand over registers for them).  With K = 2048
 // these take about 1,100 of the 8,192 cycles that a tile's MMAs take, and they
 // run beside the next tile's MMAs: the tensor pipe bounds the kernel.
 #pragma once
@@ -35,12 +42,16 @@ namespace libgemm {
 enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2 };
 
 struct XentParams {
-    CUtensorMap map_x;   // M x K: boxes of 64 x 128 rows
+    CUtensorMap map_x;   // M x K: boxes of 64 x 128 (one CTA a tile: x_rows) rows
     CUtensorMap map_w;   // the piece's N x K: boxes of 64 x (tile_n / CG) rows
     CUtensorMap map_g;   // kGrad, kGrad2: G, boxes of 64 columns x 32 rows
     int M, N;            // rows, and columns of this piece of the vocabulary
     int num_kb;          // 64-deep blocks of K
+    int part_kb;         // blocks whose sums one accumulator takes (see kXentFold)
     int tiles_m, tiles_n, tile_n;
+    int x_rows;          // one CTA a tile: rows of X in a stage; the MMA reads on into what
+                         // follows, which only rows past M see
+    int stage_bytes, stages;  // one CTA a tile: the ring, as deep as its stages are small
     int band;            // tile rows of a raster band
     int col0;            // the piece's first vocabulary number
     int vocab;           // the whole vocabulary: targets at or past it do not count
@@ -69,15 +80,22 @@ using namespace gemm_ptx;
 constexpr int XBK = 64;            // depth of a stage: one 128-byte swizzled row
 constexpr int XROWS = 128;         // rows of X in a CTA (TMEM lanes)
 constexpr int XSTAGE = 2 * XROWS * XBK * 2;  // X and at most 128 rows of W: 32 KB
+constexpr int kXentFold = 11;      // 704 of depth, as in the ragged products
 constexpr int XEPI_WARP0 = 4, XEPI_WARPS = 8;
+constexpr int XREGS = 168;         // of a thread at launch: 65536 / 384, in steps of 8
+constexpr int XREGS_ISSUE = 56, XREGS_EPI = 224;
 constexpr int XTHREADS = 32 * (XEPI_WARP0 + XEPI_WARPS);
+static_assert(XEPI_WARP0 * XREGS_ISSUE + XEPI_WARPS * XREGS_EPI <=
+                  (XEPI_WARP0 + XEPI_WARPS) * XREGS,
+              "setmaxnreg hands out what the block was launched with");
 
 template <int MODE> struct XentCfg {
     static constexpr int BOXES = MODE == kXentGrad2 ? 2 : 1;  // 64 x 32 boxes of G per warp
     static constexpr int STAGES = MODE == kXentGrad2 ? 5 : 6;
     static constexpr int RING = STAGES * XSTAGE;
     static constexpr int STAGING = XEPI_WARPS * BOXES * 32 * 128;
-    static constexpr int BARS = 2 * STAGES + 6;
+    static constexpr int MOST = 16;  // stages of one CTA's ring
+    static constexpr int BARS = 2 * MOST + 6;
     static constexpr int SMEM = RING + STAGING + BARS * 8 + 16 + 1024;  // + alignment
     static_assert(SMEM <= 232448, "over the 227 KB of shared memory a CTA may use");
 };
@@ -102,6 +120,26 @@ __device__ __noinline__ bool xent_wait_slow(uint32_t bar, uint32_t parity, ErrWo
 __device__ __forceinline__ bool xent_wait(uint32_t bar, uint32_t parity, const XentParams& p) {
     const bool ok = mbar_try_wait(bar, parity) ||
                     xent_wait_slow(bar, parity, p.err, p.gen, p.wait_limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The same without a call: the epilogue waits with 128 sums in its registers.
+__device__ __forceinline__ bool xent_wait_inline(uint32_t bar, uint32_t parity,
+                                                 const XentParams& p) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t t0 = globaltimer_ns();
+        uint32_t n = 0;
+        while (!ok) {
+            ok = mbar_try_wait(bar, parity);
+            if (ok || (++n & 31u)) continue;
+            if (gen_failed(p.err, p.gen)) break;
+            if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+                gen_record_timeout(p.err, p.gen);
+                break;
+            }
+        }
+    }
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -147,6 +185,11 @@ __device__ __forceinline__ float2 unpack16(uint32_t u) {
     }
 }
 
+// All four warps of the issuing warp group call it.
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(XREGS_ISSUE));
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Tiles in raster order: bands of `band` tile rows, column after column, every
@@ -165,7 +208,10 @@ __device__ __forceinline__ int2 xent_tile(int t, const XentParams& p) {
 template <int MODE, int CG, bool BF16>
 __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant__ XentParams p) {
     using C_ = XentCfg<MODE>;
-    constexpr int XSTAGES = C_::STAGES;
+    constexpr int MOST = C_::MOST;
+    const int stages = CG == 2 ? C_::STAGES : p.stages;
+    const int stage_bytes = CG == 2 ? XSTAGE : p.stage_bytes;
+    const int x_bytes = CG == 2 ? XROWS * XBK * 2 : p.x_rows * XBK * 2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024 bytes
@@ -173,11 +219,11 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
     const uint32_t staging0 = base + C_::RING;
     const uint32_t bar0 = staging0 + C_::STAGING;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (XSTAGES + s); };
-    auto accf_bar = [&](int a) { return bar0 + 8u * (2 * XSTAGES + a); };
-    auto acce_bar = [&](int a) { return bar0 + 8u * (2 * XSTAGES + 2 + a); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * XSTAGES + 4);
-    const uint32_t never_bar = bar0 + 8u * (2 * XSTAGES + 5);
+    auto empty_bar = [&](int s) { return bar0 + 8u * (MOST + s); };
+    auto accf_bar = [&](int a) { return bar0 + 8u * (2 * MOST + a); };
+    auto acce_bar = [&](int a) { return bar0 + 8u * (2 * MOST + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * MOST + 4);
+    const uint32_t never_bar = bar0 + 8u * (2 * MOST + 5);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C_::RING + C_::STAGING + 8 * C_::BARS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -191,7 +237,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&p.map_x);
         tma_prefetch_desc(&p.map_w);
-        for (int s = 0; s < XSTAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
@@ -215,11 +261,12 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
+        give_registers();
         pdl_wait();
         int stage = 0;
         uint32_t phase = 0;
         const int b_rows = p.tile_n / CG;
-        const uint32_t bytes = (uint32_t)(CG * (XROWS + b_rows) * XBK * 2);
+        const uint32_t bytes = (uint32_t)(CG * (x_bytes + b_rows * XBK * 2));
         for (int t = cluster; t < total && !aborted; t += nclusters) {
             const int2 tile = xent_tile(t, p);
             const int x_row = (tile.x * CG + (int)rank) * XROWS;
@@ -227,14 +274,14 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             for (int kb = 0; kb < p.num_kb; ++kb) {
                 if (!xent_wait(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
                 const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
-                const uint32_t at = base + stage * XSTAGE;
+                const uint32_t at = base + stage * stage_bytes;
                 if (xent_elect()) {
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), bytes);
                     tma_load_2d<CG>(at, &p.map_x, fb, kb * XBK, x_row);
-                    tma_load_2d<CG>(at + XROWS * XBK * 2, &p.map_w, fb, kb * XBK, w_row);
+                    tma_load_2d<CG>(at + x_bytes, &p.map_w, fb, kb * XBK, w_row);
                 }
                 __syncwarp();
-                if (++stage == XSTAGES) { stage = 0; phase ^= 1u; }
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
         }
         if (aborted) {  // let issued copies land
@@ -245,36 +292,42 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer --
+        give_registers();
         if (rank == 0) {
             const uint32_t idesc = make_idesc_f16(BF16, false, false, (uint32_t)(XROWS * CG),
                                                   (uint32_t)p.tile_n);
             const uint64_t x_desc0 = make_sdesc_sw128(base, 16, 1024);
-            const uint64_t w_desc0 = make_sdesc_sw128(base + XROWS * XBK * 2, 16, 1024);
+            const uint64_t w_desc0 = make_sdesc_sw128(base + x_bytes, 16, 1024);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             for (int t = cluster; t < total && !aborted; t += nclusters) {
-                if (!xent_wait(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!xent_wait(full_bar(stage), phase, p)) { aborted = true; break; }
+                for (int kb = 0; kb < p.num_kb && !aborted;) {
+                    if (!xent_wait(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
                     tc_fence_after_sync();
-                    const uint64_t xd = x_desc0 + (uint64_t)(stage * (XSTAGE >> 4));
-                    const uint64_t wd = w_desc0 + (uint64_t)(stage * (XSTAGE >> 4));
-                    if (xent_elect()) {
+                    const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+                    const int end = min(kb + p.part_kb, p.num_kb);
+                    uint32_t add = 0;
+                    for (; kb < end; ++kb) {
+                        if (!xent_wait(full_bar(stage), phase, p)) { aborted = true; break; }
+                        tc_fence_after_sync();
+                        const uint64_t xd = x_desc0 + (uint64_t)(stage * (stage_bytes >> 4));
+                        const uint64_t wd = w_desc0 + (uint64_t)(stage * (stage_bytes >> 4));
+                        if (xent_elect()) {
 #pragma unroll
-                        for (int j = 0; j < XBK / 16; ++j)
-                            mma_f16<CG>(d, xd + (uint64_t)(2 * j), wd + (uint64_t)(2 * j), idesc,
-                                        (kb | j) != 0 ? 1u : 0u);
-                        mma_commit<CG>(empty_bar(stage));
+                            for (int j = 0; j < XBK / 16; ++j)
+                                mma_f16<CG>(d, xd + (uint64_t)(2 * j), wd + (uint64_t)(2 * j),
+                                            idesc, j > 0 ? 1u : add);
+                            mma_commit<CG>(empty_bar(stage));
+                        }
+                        __syncwarp();
+                        add = 1;
+                        if (++stage == stages) { stage = 0; phase ^= 1u; }
                     }
+                    if (aborted) break;
+                    if (xent_elect()) mma_commit<CG>(accf_bar(acc));
                     __syncwarp();
-                    if (++stage == XSTAGES) { stage = 0; phase ^= 1u; }
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
                 }
-                if (aborted) break;
-                if (xent_elect()) mma_commit<CG>(accf_bar(acc));
-                __syncwarp();
-                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             }
             // every MMA issued above has completed before the CTA lets go of its memory
             if (xent_elect()) {
@@ -289,17 +342,28 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         __syncwarp();
     } else if (warp >= XEPI_WARP0) {
         // ------------------------------------------------------ epilogue --
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(XREGS_EPI));
         const int q = (warp - XEPI_WARP0) & 3;      // TMEM lane quarter
         const int half = (warp - XEPI_WARP0) >> 2;  // even or odd 64-column blocks
+        constexpr int BLOCKS = CG;                  // of a tile, at most, in a warp
         const uint32_t staging =
             staging0 + (uint32_t)((warp - XEPI_WARP0) * C_::BOXES * 32 * 128);
         const uint32_t my_row = staging + (uint32_t)lane * 128u;
         int acc = 0;
         uint32_t acc_phase = 0;
+        // the accumulator has been read: the MMAs may write it again
+        auto release = [&](int a) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(acce_bar(a), 0));
+                else mbar_arrive_local(acce_bar(a));
+            }
+        };
         pdl_wait();
         float alpha = p.alpha;
         if (MODE != kXentStats && p.scale) alpha *= *p.scale;
-        if (p.fault_inject == 1 && !xent_wait(never_bar, 0u, p)) aborted = true;
+        if (p.fault_inject == 1 && !xent_wait_inline(never_bar, 0u, p)) aborted = true;
         for (int t = cluster; t < total && !aborted; t += nclusters) {
             const int2 tile = xent_tile(t, p);
             const int row0 = (tile.x * CG + (int)rank) * XROWS + q * 32;
@@ -319,14 +383,41 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             }
             const bool counts = target >= 0;
             const int rel = target - p.col0;  // the target's column in this piece
-            if (!xent_wait(accf_bar(acc), acc_phase, p)) { aborted = true; break; }
+            // the parts of the depth before the last, added up
+            const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+            float parts[BLOCKS * 64];
+#pragma unroll
+            for (int i = 0; i < BLOCKS * 64; ++i) parts[i] = 0.f;
+            for (int kb = p.part_kb; kb < p.num_kb; kb += p.part_kb) {
+                if (!xent_wait_inline(accf_bar(acc), acc_phase, p)) { aborted = true; break; }
+                tc_fence_after_sync();
+#pragma unroll
+                for (int j = 0; j < BLOCKS; ++j) {
+                    const int b = half + 2 * j;
+                    if (CG == 1 && b * 64 >= p.tile_n) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(lanes + (uint32_t)(acc * ACC_COLS + b * 64 + h * 32), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            parts[j * 64 + h * 32 + i] += __uint_as_float(v[i]);
+                    }
+                }
+                release(acc);
+                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            }
+            if (aborted) break;
+            if (!xent_wait_inline(accf_bar(acc), acc_phase, p)) { aborted = true; break; }
             tc_fence_after_sync();
-            const uint32_t taddr =
-                tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-            const int c0 = tile.y * p.tile_n;
+            const uint32_t taddr = lanes + (uint32_t)(acc * ACC_COLS);
+            const int c0 = tile.y * p.tile_n, end = min(c0 + p.tile_n, p.N);
             float m = -INFINITY, sum = 0.f;
-#pragma unroll 1
-            for (int b = half; b < p.tile_n / 64; b += 2) {
+#pragma unroll
+            for (int j = 0; j < BLOCKS; ++j) {
+                const int b = half + 2 * j;
+                if (CG == 1 && b * 64 >= p.tile_n) continue;
                 const int col = c0 + b * 64;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -334,13 +425,16 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                     __syncwarp();
                     tmem_ld_32x32b_x32(taddr + (uint32_t)(b * 64 + h * 32), v);
                     tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __float_as_uint(parts[j * 64 + h * 32 + i] + __uint_as_float(v[i]));
                     const int first = col + h * 32;
-                    const int at = counts ? rel - first : -1;  // the target's place in v
+                    const int at = counts && rel < end ? rel - first : -1;  // the target's place in v
                     if constexpr (MODE == kXentStats) {
-                        if (p.N - first < 32) {
+                        if (end - first < 32) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (first + i >= p.N) v[i] = 0xff800000u;  // -infinity
+                                if (first + i >= end) v[i] = 0xff800000u;  // -infinity
                         }
                         float top = __uint_as_float(v[0]);
 #pragma unroll
@@ -421,16 +515,13 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             if constexpr (MODE == kXentStats)
                 if (row < p.M)
                     p.part[(int64_t)(tile.y * 2 + half) * p.part_ld + row] = make_float2(m, sum);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
-                else mbar_arrive_local(acce_bar(acc));
-            }
+            release(acc);
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
         if (MODE != kXentStats && lane == 0) bulk_wait_all();
         __syncwarp();
+    } else {
+        give_registers();
     }
 
     // ------------------------------------------------------------ teardown --
@@ -463,6 +554,10 @@ int launch_xent_variant(XentParams& xp, const DeviceInfo& dev, cudaStream_t stre
         std::lock_guard<std::mutex> lock(mu);
         const uint64_t bit = 1ull << (dev.device & 63);
         if (!(configured & bit)) {
+            // the epilogue's registers come out of what the block is launched with
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != XREGS)
+                return kCuda;
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
                 cudaSuccess)
                 return kCuda;

@@ -379,7 +379,7 @@ int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
  * row. Types: the 16-bit dtypes (the result's type is not used; GEMM_F32 is
  * GEMM_ERR_UNSUPPORTED). Logits and sums are fp32; infinite or NaN logits make
  * their row's lse NaN. N is 1 .. 2^24 (more: GEMM_ERR_UNSUPPORTED). The rows' results
- * do not depend on each other. Scratch: 16 bytes for each row and 64 to 256
+ * do not depend on each other. Scratch: 16 bytes for each row and 32 to 256
  * columns, for as many rows at a time as stay within 256 MB, and copies of X or W
  * where their rows are not 16-byte aligned. M zero is a no-op, K zero gives
  * lse = log N. Otherwise ownership, asynchrony and status codes are gemm()'s.
