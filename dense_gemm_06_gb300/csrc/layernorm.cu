@@ -206,15 +206,10 @@ struct NormGradArgs {
 
 constexpr int kOwn = 16;  // columns of a thread in the backward kernel
 
-// A copy of BYTES (4, 8 or 16) into shared memory that this thread waits for itself.
-template <int BYTES>
+// A copy of 16 bytes into shared memory that this thread waits for itself.
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                     :: "r"(gemm_ptx::smem_u32(to)), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
-                     :: "r"(gemm_ptx::smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(gemm_ptx::smem_u32(to)), "l"(from) : "memory");
 }
 
 // Rows on their way to a thread, the one that it works on included. With 16-bit
@@ -224,15 +219,16 @@ template <typename T> constexpr int kNormStages = sizeof(T) == 2 ? 4 : 3;
 // A block of WARPS x LANES warps: LANES rows side by side, each on WARPS warps
 // (LANES > 1 only with one warp a row). Thread tid of a row owns the columns
 // (i TR + tid) VEC + e, i < kOwn / VEC. It copies its own parts of the next rows
-// into its own shared memory (single 16-bit elements, which the copies do not
-// take, into registers), so that the copies need no barrier.
+// into its own shared memory, so that the copies need no barrier. (Single elements
+// go to registers, one row ahead: 4-byte copies of 10007 rows of 8191 took 222 us,
+// loads 166.)
 template <typename T, typename W, int WARPS, int LANES, int VEC>
 __global__ void __launch_bounds__(32 * WARPS * LANES)
     norm_grad_kernel(const NormGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int TR = 32 * WARPS, NV = kOwn / VEC, THREADS = TR * LANES;
     constexpr int BYTES = VEC * (int)sizeof(T), STAGES = kNormStages<T>;
-    constexpr bool RING = BYTES >= 4;
+    constexpr bool RING = BYTES == 16;
     using V = Pack<T, VEC>;
     extern __shared__ __align__(16) uint8_t ring[];  // STAGES x (x, dy) x NV x THREADS vectors
     __shared__ float slots[2][2 * WARPS];
@@ -265,8 +261,8 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
                 const int c = (i * TR + tid) * VEC;
                 if (c >= a.N) continue;
                 if constexpr (RING) {
-                    copy_async<BYTES>(slot(stage, 0, i), x + c);
-                    copy_async<BYTES>(slot(stage, 1, i), dy + c);
+                    copy_async(slot(stage, 0, i), x + c);
+                    copy_async(slot(stage, 1, i), dy + c);
                 } else {
                     xv[i] = *reinterpret_cast<const V*>(x + c);
                     gv[i] = *reinterpret_cast<const V*>(dy + c);
@@ -514,7 +510,7 @@ constexpr int kLongShares = 32;
 template <typename T, typename W, int WARPS, int LANES, int VEC>
 int run_norm_grad(const NormGradArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int THREADS = 32 * WARPS * LANES;
-    constexpr int SMEM = VEC * sizeof(T) >= 4 ? kNormStages<T> * 2 * kOwn * (int)sizeof(T) * THREADS
+    constexpr int SMEM = VEC * sizeof(T) == 16 ? kNormStages<T> * 2 * kOwn * (int)sizeof(T) * THREADS
                                               : 0;
     auto kern = norm_grad_kernel<T, W, WARPS, LANES, VEC>;
     if constexpr (SMEM > 40 * 1024) {
