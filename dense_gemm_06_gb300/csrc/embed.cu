@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kTile / 2)
             for (int h = 0; h < 2; ++h) {
                 const int i = i0 + h * HALF;
                 const bool small = ((i & j) == 0) == ((i & k) == 0);  // keeps the smaller
-                if (small ? other[h] < v[h] : other[h] > v[h]) v[h] = other[h];
+                v[h] = (other[h] < v[h]) == small ? other[h] : v[h];
             }
         }
     }
@@ -218,42 +218,59 @@ __global__ void __launch_bounds__(kTile / 2)
         if (base + i0 + h * HALF < M) out[base + i0 + h * HALF] = v[h];
 }
 
-__global__ void __launch_bounds__(256)
+// Each number finds its place in the 16 runs by binary searches side by side: first
+// among a part of the run in shared memory (all of it up to kSamples numbers, else
+// every (run / kFew)th), then, of long runs, in what lies between. In global memory
+// alone, where every block starts at the same few numbers, 8192 numbers took 26 us.
+constexpr int kMergeThreads = 128;
+constexpr int kSamples = kTile, kFew = 128;
+__global__ void __launch_bounds__(kMergeThreads)
     sort_merge_kernel(const uint64_t* __restrict__ in, uint64_t* __restrict__ out, int64_t M,
                       uint32_t run) {
     gemm_ptx::pdl_launch_dependents();
+    extern __shared__ uint64_t sample[];  // kMerge x samples of a run
     gemm_ptx::pdl_wait();
-    const uint32_t i = blockIdx.x * 256 + threadIdx.x, n = (uint32_t)M;
+    const uint32_t n = (uint32_t)M;
+    const uint64_t group = (uint64_t)run * kMerge;
+    const uint64_t i = (uint64_t)blockIdx.x * kMergeThreads + threadIdx.x;
+    const uint64_t base = (uint64_t)blockIdx.x * kMergeThreads / group * group;
+    const uint32_t each = run <= kSamples ? run : kFew, stride = run / each;
+    // the last of each `stride` numbers, as if the list went on with larger ones
+    for (uint32_t k = threadIdx.x; k < kMerge * each; k += kMergeThreads) {
+        const uint64_t at = base + (uint64_t)k * stride + stride - 1;
+        sample[k] = at < n ? in[at] : ~0ull;
+    }
+    __syncthreads();
     if (i >= n) return;
     const uint64_t x = in[i];
-    const uint32_t own = i / run, first = own / kMerge * kMerge;
-    // How many numbers of each run are below x: binary searches side by side, their
-    // loads issued together (with branches around them they came one by one: 28 us
-    // for 8192 numbers, 16 runs).
-    uint32_t begin[kMerge], len[kMerge], pos[kMerge];
+    uint32_t pos[kMerge];  // samples of each run that are below x
+#pragma unroll
+    for (int r = 0; r < kMerge; ++r) pos[r] = 0;
+    for (uint32_t w = each / 2; w > 0; w /= 2)
+#pragma unroll
+        for (int r = 0; r < kMerge; ++r)
+            if (sample[r * each + pos[r] + w - 1] < x) pos[r] += w;
+    uint64_t at = base;
 #pragma unroll
     for (int r = 0; r < kMerge; ++r) {
-        const uint64_t at = (uint64_t)(first + r) * run;
-        begin[r] = at < n ? (uint32_t)at : n;
-        len[r] = n - begin[r] < run ? n - begin[r] : run;
-        pos[r] = 0;
-        if (first + r == own) begin[r] = i, len[r] = 0;  // counted below
+        if (sample[r * each + pos[r]] < x) ++pos[r];
+        pos[r] *= stride;
     }
-    for (uint32_t w = run / 2; w > 0; w /= 2) {
+    // fewer than `stride` numbers more (none where a run's samples are all below)
+    for (uint32_t w = stride / 2; w > 0; w /= 2) {
         uint64_t got[kMerge];
 #pragma unroll
         for (int r = 0; r < kMerge; ++r) {
-            const uint32_t at = pos[r] + w - 1;
-            got[r] = at < len[r] ? in[begin[r] + at] : ~0ull;
+            const uint64_t p = base + (uint64_t)r * run + pos[r] + w - 1;
+            got[r] = in[p < n ? p : n - 1];
         }
 #pragma unroll
         for (int r = 0; r < kMerge; ++r)
-            if (got[r] < x) pos[r] += w;
+            if (pos[r] < run && base + (uint64_t)r * run + pos[r] + w - 1 < n && got[r] < x)
+                pos[r] += w;
     }
-    uint64_t at = (uint64_t)first * run + (i - own * run);
 #pragma unroll
-    for (int r = 0; r < kMerge; ++r)
-        at += pos[r] + (pos[r] < len[r] && in[begin[r] + pos[r]] < x ? 1 : 0);
+    for (int r = 0; r < kMerge; ++r) at += pos[r];
     out[at] = x;
 }
 
@@ -294,24 +311,75 @@ __device__ __forceinline__ int64_t first_at(const uint64_t* sorted, int64_t M, u
     return lo;
 }
 
+// G elements of a row from column c on, held by each lane of a warp one group after
+// the other (the whole warp calls it, lanes past the row's end too). Where the row
+// starts on no 16-byte boundary, lanes hand the beginning of their groups to the
+// lane before, so that all but the warp's first and last elements still leave in
+// 16-byte stores (2-byte stores of rows of 1803 took two thirds of the kernel).
+template <typename O, int G>
+__device__ __forceinline__ void store_row(O* row, int64_t K, int64_t c, const float (&v)[G]) {
+    constexpr int ES = (int)sizeof(O), WORDS = G * ES / 4, PER = 16 / ES;
+    static_assert(WORDS % 4 == 0, "whole 16-byte pieces");
+    alignas(16) O o[G];
+#pragma unroll
+    for (int e = 0; e < G; ++e) o[e] = from_f32<O>(v[e]);
+    uint32_t w[WORDS + 4];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<uint32_t*>(o)[i];
+    const int lane = threadIdx.x & 31;
+    // bytes up to the next 16-byte boundary: the same for every lane
+    const uint32_t skip = (uint32_t)(-(intptr_t)reinterpret_cast<uintptr_t>(row + c)) & 15u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+    const uint32_t words = skip / 4, bits = skip % 4 * 8;
+    uint32_t s[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (words == (uint32_t)k) {
+                lo = w[i + k];
+                if (i + k + 1 < WORDS + 4) hi = w[i + k + 1];
+            }
+        s[i] = __funnelshift_r(lo, hi, bits);
+    }
+    const int ahead = (int)skip / ES;  // elements that the lane before takes
+#pragma unroll
+    for (int g = 0; g < WORDS / 4; ++g) {
+        const int64_t c0 = c + ahead + g * PER;  // the piece's first element
+        // of the last lane's last piece the next warp has the rest
+        const int have = lane == 31 && g == WORDS / 4 - 1 ? PER - ahead : PER;
+        if (c0 + PER <= K && have == PER) {
+            *reinterpret_cast<uint4*>(row + c0) =
+                make_uint4(s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]);
+        } else {
+            const O* piece = reinterpret_cast<const O*>(s + 4 * g);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (e < have && c0 + e < K) row[c0 + e] = piece[e];
+        }
+    }
+    if (lane == 0) {  // no lane before
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (e < ahead && c + e < K) row[c + e] = o[e];
+    }
+}
+
 template <typename O, int G>
 __device__ __forceinline__ void write_sum(const EmbedGradArgs& a, uint32_t token, int64_t c,
                                           const float (&sum)[G]) {
-    O* at = static_cast<O*>(a.dtable) + (int64_t)token * a.lddt + c;
-    if (c + G <= a.K) {
-        float v[G];
+    O* row = static_cast<O*>(a.dtable) + (int64_t)token * a.lddt;
+    float v[G];
 #pragma unroll
-        for (int e = 0; e < G; ++e)
-            v[e] = a.beta != 0.f ? fmaf(a.beta, to_f32(at[e]), a.scale * sum[e])
-                                 : a.scale * sum[e];
-        store_group<O, G>(at, v);
-    } else {
-        for (int e = 0; e < G; ++e)
-            if (c + e < a.K)
-                at[e] = from_f32<O>(a.beta != 0.f
-                                        ? fmaf(a.beta, to_f32(at[e]), a.scale * sum[e])
-                                        : a.scale * sum[e]);
+    for (int e = 0; e < G; ++e) {
+        v[e] = a.scale * sum[e];
+        if (a.beta != 0.f && c + e < a.K) v[e] = fmaf(a.beta, to_f32(row[c + e]), v[e]);
     }
+    __syncwarp();  // every lane has read what it adds to
+    store_row<O, G>(row, a.K, c, v);
 }
 
 // The first a.sum_blocks blocks add up chunks; the others look after the rows of
@@ -326,7 +394,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
     if (blockIdx.x < a.sum_blocks) {
         const int64_t chunk = blockIdx.x / a.col_blocks;
         const int64_t c = ((int64_t)(blockIdx.x % a.col_blocks) * kSumThreads + threadIdx.x) * G;
-        if (c >= a.K) return;
+        const bool out = c >= a.K;  // such lanes only take part in the stores
+        if (__all_sync(0xffffffffu, out)) return;
         const int64_t p0 = chunk * a.chunk;
         const int64_t p1 = p0 + a.chunk < a.M ? p0 + a.chunk : a.M;
         const uint32_t before = p0 > 0 ? token_of(a.sorted[p0 - 1]) : kNone;
@@ -347,7 +416,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
                 tok[j] = token_of(x);
                 if (tok[j] == kNone) continue;
                 const T* row = static_cast<const T*>(a.dy) + (int64_t)(uint32_t)x * a.lddy + c;
-                if (whole) {
+                if (out) {
+#pragma unroll
+                    for (int e = 0; e < G; ++e) v[j][e] = 0.f;
+                } else if (whole) {
                     load_group<T, G>(row, v[j]);
                 } else {
 #pragma unroll
@@ -361,8 +433,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
                     if (token != kNone) {
                         if (crossing) {
                             float* to = a.part + chunk * 2 * a.kp + c;
+                            if (!out)
 #pragma unroll
-                            for (int e = 0; e < G; ++e) to[e] = sum[e];
+                                for (int e = 0; e < G; ++e) to[e] = sum[e];
                         } else {
                             write_sum<O, G>(a, token, c, sum);
                         }
@@ -382,8 +455,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
         const bool goes_on = p1 < a.M && after == token;
         if (crossing || goes_on) {
             float* to = a.part + (chunk * 2 + (crossing ? 0 : 1)) * a.kp + c;
+            if (!out)
 #pragma unroll
-            for (int e = 0; e < G; ++e) to[e] = sum[e];
+                for (int e = 0; e < G; ++e) to[e] = sum[e];
         } else {
             write_sum<O, G>(a, token, c, sum);
         }
@@ -409,18 +483,22 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
     for (int r = 0; r < rows; ++r) {
         if (named >> r & 1) continue;
         O* row = static_cast<O*>(a.dtable) + (v0 + r) * a.lddt;
+        int64_t count = a.K;
+        if (a.lddt == a.K)  // rows without gaps between them: as one
+            for (; r + 1 < rows && !(named >> (r + 1) & 1); ++r) count += a.K;
         if (a.beta != 0.f) {
-            for (int64_t c = threadIdx.x; c < a.K; c += kSumThreads)
+            for (int64_t c = threadIdx.x; c < count; c += kSumThreads)
                 row[c] = from_f32<O>(a.beta * to_f32(row[c]));
             continue;
         }
         const int past = (int)(reinterpret_cast<uintptr_t>(row) % 16) / (int)sizeof(O);
         int64_t head = past ? GO - past : 0;
-        if (head > a.K) head = a.K;
-        const int64_t tail = head + (a.K - head) / GO * GO;
+        if (head > count) head = count;
+        const int64_t tail = head + (count - head) / GO * GO;
+#pragma unroll 4
         for (int64_t c = head + (int64_t)threadIdx.x * GO; c < tail; c += kSumThreads * GO)
             *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
-        for (int64_t i = threadIdx.x; i < head + (a.K - tail); i += kSumThreads)
+        for (int64_t i = threadIdx.x; i < head + (count - tail); i += kSumThreads)
             row[i < head ? i : tail + (i - head)] = from_f32<O>(0.f);
     }
 }
@@ -441,12 +519,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGra
     if (p0 > 0 && token_of(a.sorted[p0 - 1]) == token &&
         token_of(a.sorted[p0]) == token) return;                     // it began earlier
     const int64_t end = first_at(a.sorted, a.M, (uint64_t)token + 1);
-    if (c >= a.K) return;
+    const bool out = c >= a.K;
+    if (__all_sync(0xffffffffu, out)) return;
     const int64_t last = (end - 1) / a.chunk;
     float sum[G];
     const float* from = a.part + (chunk * 2 + 1) * a.kp + c;
 #pragma unroll
-    for (int e = 0; e < G; ++e) sum[e] = from[e];
+    for (int e = 0; e < G; ++e) sum[e] = out ? 0.f : from[e];
     constexpr int AHEAD = 64 / G;
     for (int64_t k = chunk + 1; k <= last; k += AHEAD) {
         float4 more[AHEAD][G / 4];
@@ -454,12 +533,12 @@ __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGra
         for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
             for (int q = 0; q < G / 4; ++q)
-                if (k + j <= last)
+                if (k + j <= last && !out)
                     more[j][q] =
                         reinterpret_cast<const float4*>(a.part + (k + j) * 2 * a.kp + c)[q];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (k + j <= last) {
+            if (k + j <= last && !out) {
 #pragma unroll
                 for (int q = 0; q < G / 4; ++q) {
                     sum[4 * q] += more[j][q].x;
@@ -556,8 +635,13 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
         rc = launch_dependent(sort_tiles_kernel, dim3((unsigned)((M + kTile - 1) / kTile)),
                               dim3(kTile / 2), 0, s, ids, M, V, in, dev->err_word);
         for (int64_t run = kTile; rc == kOk && run < M; run *= kMerge) {
-            rc = launch_dependent(sort_merge_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256),
-                                  0, s, (const uint64_t*)in, out, M, (uint32_t)run);
+            const int smem = kMerge * (run <= kSamples ? (int)run : kFew) * 8;
+            rc = allow_smem(sort_merge_kernel, kMerge * kSamples * 8, *dev);
+            if (rc == kOk)
+                rc = launch_dependent(sort_merge_kernel,
+                                      dim3((unsigned)((M + kMergeThreads - 1) / kMergeThreads)),
+                                      dim3(kMergeThreads), smem, s, (const uint64_t*)in, out, M,
+                                      (uint32_t)run);
             std::swap(in, out);
         }
         a.sorted = in;

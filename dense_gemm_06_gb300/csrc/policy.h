@@ -449,9 +449,10 @@ inline int64_t xent_piece_cols(int64_t rows, int64_t N, int parts) {
 
 // embed_rows_grad: sorted tokens of a chunk, which a block (for each share of the
 // columns) adds up: 16, up to 64 for so many tokens that there would be more than
-// 1024 chunks, and longer where there would be more than 8192.
+// 256 chunks (a frequent token's chunks are added up one after the other), and
+// longer where there would be more than 8192.
 inline int embed_chunk(int64_t M) {
-    const int64_t n = (M + 1023) / 1024, most = (M + 8191) / 8192;
+    const int64_t n = (M + 255) / 256, most = (M + 8191) / 8192;
     return (int)(most > 64 ? most : n < 16 ? 16 : n > 64 ? 64 : n);
 }
 

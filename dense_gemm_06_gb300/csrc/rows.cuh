@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
+#include <set>
 #include <type_traits>
 #include <utility>
 
@@ -43,6 +45,24 @@ int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cud
         return kCuda;
     }
     note_launch();
+    return kOk;
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory on this device.
+template <typename K>
+int allow_smem(K kern, int bytes, const DeviceInfo& dev) {
+    if (bytes <= 40 * 1024) return kOk;
+    static std::mutex mu;
+    static std::set<std::pair<const void*, int>> allowed;
+    std::lock_guard<std::mutex> lock(mu);
+    const std::pair<const void*, int> key(reinterpret_cast<const void*>(kern), dev.device);
+    if (allowed.count(key)) return kOk;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return kCuda;
+    }
+    allowed.insert(key);
     return kOk;
 }
 
