@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const uint64_t base = (uint64_t)blockIdx.x * kMergeThreads / group * group;
     const uint32_t each = run <= kSamples ? run : kFew, stride = run / each;
     // the last of each `stride` numbers, as if the list went on with larger ones
+#pragma unroll 16
     for (uint32_t k = threadIdx.x; k < kMerge * each; k += kMergeThreads) {
         const uint64_t at = base + (uint64_t)k * stride + stride - 1;
         sample[k] = at < n ? in[at] : ~0ull;
@@ -292,7 +293,8 @@ struct EmbedGradArgs {
 };
 
 constexpr int kSumThreads = 128;
-constexpr int kFillRows = 32;     // rows of the table that a block looks after
+constexpr int kFillRows = 8;      // rows of the table that a block looks after: small pieces,
+                                  // so that the last blocks end together
 
 // The first place of the sorted list whose token is not below `token`; the whole
 // warp calls it (32 places at a time: 4 steps for 2^20 numbers).

@@ -518,10 +518,18 @@ __global__ void __launch_bounds__(32 * kShares)
     const int share = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // of 2 N: dweight, then dbias
     float s = 0.f;
-    if (c < 2 * (int64_t)N) {
-#pragma unroll 8
-        for (int b = share; b < blocks; b += kShares) s += part[(int64_t)b * 2 * N + c];
-    }
+    constexpr int AHEAD = 10;  // reads in flight
+    if (c < 2 * (int64_t)N)
+        for (int b = share; b < blocks; b += AHEAD * kShares) {
+            float v[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int64_t at = b + j * kShares;
+                v[j] = at < blocks ? part[at * 2 * N + c] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) s += v[j];
+        }
     got[share][lane] = s;
     __syncthreads();
     for (int o = kShares / 2; o; o /= 2) {

@@ -85,12 +85,9 @@ struct BalanceArgs {
 
 // A row on LANES lanes, expert sub + LANES i in lane sub; a warp takes 32 / LANES
 // rows at a time, ROWS times over with their reads in flight together.
-// Clusters of CLUSTER blocks (for many rows) add up their sums before they write
-// them, so that there are few to join.
 constexpr int kWarps = 8;
-template <typename T, int LANES, int NE, int ROWS, int CLUSTER>
-__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(32 * kWarps)
-    balance_kernel(const BalanceArgs a) {
+template <typename T, int LANES, int NE, int ROWS>
+__global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int SIDE = 32 / LANES;  // rows of a warp side by side
     extern __shared__ int32_t counts[];  // E + 1, then kWarps x E sums
@@ -145,62 +142,59 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(32 * kWarps)
         if (side == 0 && sub + LANES * i < a.E) sums[warp * a.E + sub + LANES * i] = total[i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) {
+    for (int e = threadIdx.x; e <= a.E; e += 32 * kWarps) {
+        a.part_n[(int64_t)blockIdx.x * (a.E + 1) + e] = counts[e];
+        if (e == a.E) continue;
         float s = 0.f;
         for (int w = 0; w < kWarps; ++w) s += sums[w * a.E + e];
-        sums[e] = s;  // warp 0's own, which no other thread reads
+        a.part_p[(int64_t)blockIdx.x * a.E + e] = s;
     }
-    if constexpr (CLUSTER > 1) gemm_ptx::cluster_sync_all();
-    else __syncthreads();
-    if (CLUSTER == 1 || gemm_ptx::cluster_ctarank() == 0) {
-        const int64_t part = blockIdx.x / CLUSTER;
-        for (int e = threadIdx.x; e <= a.E; e += 32 * kWarps) {
-            int32_t n[CLUSTER];
-            float s[CLUSTER];
-#pragma unroll
-            for (int r = 0; r < CLUSTER; ++r) {
-                n[r] = CLUSTER == 1 ? counts[e] : ld_cluster(&counts[e], r);
-                s[r] = e == a.E ? 0.f : CLUSTER == 1 ? sums[e] : ld_cluster(&sums[e], r);
-            }
-#pragma unroll
-            for (int r = 1; r < CLUSTER; ++r) {
-                n[0] += n[r];
-                s[0] += s[r];
-            }
-            a.part_n[part * (a.E + 1) + e] = n[0];
-            if (e < a.E) a.part_p[part * a.E + e] = s[0];
-        }
-    }
-    if constexpr (CLUSTER > 1) gemm_ptx::cluster_sync_all();  // no block leaves before
 }
 
-// One block: the sums and counts, the limits and the loss. `shares` threads an
-// expert (a power of two), each a share of the parts.
-__global__ void __launch_bounds__(1024)
+// One cluster of JOIN blocks (one where there is little to add up): each adds up
+// its share of the parts, the first one the shares, and writes the limits and the
+// loss. `shares` threads an expert (a power of two), each a share of the block's
+// parts, whose reads are in flight together.
+template <int JOIN>
+__global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(1024)
     balance_join_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_n,
                         int parts, int E, int top, int shares, int32_t* __restrict__ counts,
                         int32_t* __restrict__ offsets, float* __restrict__ prob,
                         float* __restrict__ loss) {
     gemm_ptx::pdl_launch_dependents();
+    constexpr int AHEAD = 8;
     __shared__ float p[1024];
     __shared__ int32_t c[1024], warp_n[32], warp_c[32];
     __shared__ float warp_f[32];
+    __shared__ int32_t block_n;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = JOIN == 1 ? 0 : (int)gemm_ptx::cluster_ctarank();
     gemm_ptx::pdl_wait();
+    const int b0 = (int)((int64_t)parts * rank / JOIN);
+    const int b1 = (int)((int64_t)parts * (rank + 1) / JOIN);
     int n = 0;  // rows that count
-    for (int b = threadIdx.x; b < parts; b += 1024) n += part_n[(int64_t)b * (E + 1) + E];
+    for (int b = b0 + threadIdx.x; b < b1; b += 1024) n += part_n[(int64_t)b * (E + 1) + E];
     // an expert's shares lie a whole number of experts apart
     const int wide = 1024 / shares;
     const int e = threadIdx.x % wide, share = threadIdx.x / wide;
     float s = 0.f;
     int32_t k = 0;
-    if (e < E) {
-#pragma unroll 16
-        for (int b = share; b < parts; b += shares) {
-            s += part_p[(int64_t)b * E + e];
-            k += part_n[(int64_t)b * (E + 1) + e];
+    if (e < E)
+        for (int b = b0 + share; b < b1; b += AHEAD * shares) {
+            float ps[AHEAD];
+            int32_t ns[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int64_t at = b + j * shares;
+                ps[j] = at < b1 ? part_p[at * E + e] : 0.f;
+                ns[j] = at < b1 ? part_n[at * (E + 1) + e] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                s += ps[j];
+                k += ns[j];
+            }
         }
-    }
     p[threadIdx.x] = s;
     c[threadIdx.x] = k;
     n = __reduce_add_sync(0xffffffffu, n);
@@ -215,11 +209,37 @@ __global__ void __launch_bounds__(1024)
     }
     n = __reduce_add_sync(0xffffffffu, warp_n[lane]);
     const bool mine = threadIdx.x < E;
-    const int32_t own = mine ? c[threadIdx.x] : 0;
+    int32_t own = c[threadIdx.x];
+    s = p[threadIdx.x];
+    if constexpr (JOIN > 1) {
+        if (threadIdx.x == 0) block_n = n;
+        gemm_ptx::cluster_sync_all();
+        if (rank == 0) {
+            int32_t rn[JOIN], rc[JOIN];
+            float rp[JOIN];
+#pragma unroll
+            for (int r = 0; r < JOIN; ++r) {
+                rn[r] = ld_cluster(&block_n, r);
+                rp[r] = ld_cluster(&p[threadIdx.x], r);
+                rc[r] = ld_cluster(&c[threadIdx.x], r);
+            }
+            n = own = 0;
+            s = 0.f;
+#pragma unroll
+            for (int r = 0; r < JOIN; ++r) {
+                n += rn[r];
+                own += rc[r];
+                s += rp[r];
+            }
+        }
+        gemm_ptx::cluster_sync_all();  // no block leaves while its sums are read
+        if (rank != 0) return;
+    }
+    if (!mine) own = 0;
     const int m = n > 0 ? n : 1;
     float term = 0.f;
     if (mine) {
-        const float mean = p[threadIdx.x] / (float)m;
+        const float mean = s / (float)m;
         counts[threadIdx.x] = own;
         prob[threadIdx.x] = mean;
         term = (float)((double)own / ((double)top * m)) * mean;
@@ -371,18 +391,15 @@ int balance(int64_t T, int64_t E, int64_t top, const void* logits, int64_t ldl,
     if (rc != kOk) return rc;
     const int each = kWarps * (E <= 256 ? 4 : 1);  // rows of a block at a time
     int64_t blocks = (T + each - 1) / each;
-    const int64_t most = (int64_t)dev->sm_count * 3 / 8 * 8;
+    const int64_t most = (int64_t)dev->sm_count * 3;
     if (blocks > most) blocks = most;
-    const bool clusters = blocks >= 64;
-    if (clusters) blocks = blocks / 8 * 8;
-    const int64_t parts = clusters ? blocks / 8 : blocks;
     Scratch scratch{pool, s, dev->device};
     BalanceArgs a{T, (int)E, (int)top, logits, ldl, expert, nullptr, nullptr, dev->err_word};
     if (blocks > 0) {
-        char* mem = static_cast<char*>(scratch.get((size_t)(parts * (2 * E + 1) * 4)));
+        char* mem = static_cast<char*>(scratch.get((size_t)(blocks * (2 * E + 1) * 4)));
         if (!mem) return kCuda;
         a.part_p = reinterpret_cast<float*>(mem);
-        a.part_n = reinterpret_cast<int32_t*>(mem + parts * E * 4);
+        a.part_n = reinterpret_cast<int32_t*>(mem + blocks * E * 4);
         const size_t smem = (size_t)(E + 1 + kWarps * E) * 4;
         const dim3 grid((unsigned)blocks), block(32 * kWarps);
         rc = with_lanes((int)E, [&](auto lanes, auto ne, auto rows) {
@@ -390,9 +407,8 @@ int balance(int64_t T, int64_t E, int64_t top, const void* logits, int64_t ldl,
             constexpr int NE = decltype(ne)::value, ROWS = decltype(rows)::value;
             auto run = [&](auto t) {
                 using L = decltype(t);
-                return launch_dependent(clusters ? balance_kernel<L, LANES, NE, ROWS, 8>
-                                                 : balance_kernel<L, LANES, NE, ROWS, 1>,
-                                        grid, block, smem, s, a);
+                return launch_dependent(balance_kernel<L, LANES, NE, ROWS>, grid, block, smem, s,
+                                        a);
             };
             if (dtype == GEMM_F32) return run(float{});
             if (dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16) return run(__nv_bfloat16{});
@@ -402,9 +418,12 @@ int balance(int64_t T, int64_t E, int64_t top, const void* logits, int64_t ldl,
     if (rc == kOk) {
         int shares = 1;
         while (shares * 2 * E <= 1024) shares *= 2;
-        rc = launch_dependent(balance_join_kernel, dim3(1), dim3(1024), 0, s,
-                              (const float*)a.part_p, (const int32_t*)a.part_n, (int)parts, (int)E,
-                              (int)top, shares, counts, offsets, prob, loss);
+        // more than one round of reads for each thread: eight blocks share them
+        const bool wide = blocks > 8 * shares;
+        rc = launch_dependent(wide ? balance_join_kernel<8> : balance_join_kernel<1>,
+                              dim3(wide ? 8 : 1), dim3(1024), 0, s, (const float*)a.part_p,
+                              (const int32_t*)a.part_n, (int)blocks, (int)E, (int)top, shares,
+                              counts, offsets, prob, loss);
     }
     scratch.release();
     return rc;
