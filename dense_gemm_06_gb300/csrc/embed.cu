@@ -14,9 +14,8 @@
 // search. 8192 tokens take two launches, 131072 three.
 //
 // Sums: the sorted list is cut into chunks of equal length, so that a frequent
-// token's rows are shared by many blocks. A block adds up the runs within its
-// chunk; a run that crosses chunks leaves one partial sum in each, which a last
-// kernel adds in the order of the chunks.
+// token's rows are shared by many blocks. A run that crosses chunks leaves one
+// partial sum in each, which a last kernel adds in the order of the chunks.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -32,52 +31,78 @@ namespace {
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// G elements of a row, from any alignment: the one or two aligned 16-byte (or
-// smaller) pieces that hold them, shifted together. The second piece is read only
-// when it holds one of them.
-template <typename T, int G>
-__device__ __forceinline__ void load_group(const T* p, float (&out)[G]) {
-    constexpr int BYTES = G * (int)sizeof(T);  // 4, 8 or 16
-    constexpr int WORDS = BYTES / 4;
-    static_assert(BYTES == 8 || BYTES == 16, "whole words");
-    struct alignas(BYTES) Piece { uint32_t w[WORDS]; };
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint32_t off = (uint32_t)(at % BYTES);
-    const Piece* from = reinterpret_cast<const Piece*>(at - off);
-    uint32_t w[2 * WORDS];
-    const Piece a = from[0];
+// r = the words from byte `off` (below 4 WORDS_OFF) of w on. `off` is the same in
+// every lane, so that the cases are branches and not selections.
+template <int WORDS, int WORDS_OFF, int HAVE>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[HAVE], uint32_t off,
+                                            uint32_t (&r)[WORDS]) {
+    const uint32_t bits = off % 4 * 8;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) w[i] = a.w[i];
-    if (off) {
-        const Piece b = from[1];
+    for (int k = 0; k < WORDS_OFF; ++k)
+        if (off / 4 == (uint32_t)k) {
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[WORDS + i] = b.w[i];
-        uint32_t r[WORDS];
-        const uint32_t skip = off / 4, bits = off % 4 * 8;
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            uint32_t lo = 0, hi = 0;
-#pragma unroll
-            for (int k = 0; k < WORDS; ++k) {
-                if (skip == (uint32_t)k) lo = w[i + k];
-                if (skip == (uint32_t)k && i + k + 1 < 2 * WORDS) hi = w[i + k + 1];
-            }
-            r[i] = __funnelshift_r(lo, hi, bits);
+            for (int i = 0; i < WORDS; ++i)
+                r[i] = __funnelshift_r(w[i + k], i + k + 1 < HAVE ? w[i + k + 1] : 0u, bits);
         }
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = r[i];
-    }
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) out[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const uint16_t h = (uint16_t)(w[i / 2] >> (i % 2 * 16));
-            out[i] = to_f32(*reinterpret_cast<const T*>(&h));
-        }
-    }
 }
+
+// G elements of a row on their way: the aligned piece that begins with them, or
+// (ALIGNED false) the one or two aligned pieces that hold them. The second one is
+// read only where it holds one of them, else the first again, so that the reads of
+// several groups are in flight together, without branches between them.
+template <int BYTES>
+struct alignas(BYTES) Piece {
+    uint32_t w[BYTES / 4];
+};
+template <typename T, int G, bool ALIGNED>
+struct Group {
+    static constexpr int BYTES = G * (int)sizeof(T), WORDS = BYTES / 4;
+    static_assert(BYTES == 8 || BYTES == 16, "whole words");
+    Piece<BYTES> a, b;
+
+    __device__ __forceinline__ void load(const T* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint32_t off = ALIGNED ? 0 : (uint32_t)(at % BYTES);
+        const Piece<BYTES>* from = reinterpret_cast<const Piece<BYTES>*>(at - off);
+        a = from[0];
+        if constexpr (!ALIGNED) b = from[off ? 1 : 0];
+    }
+    // The elements; p as in load().
+    __device__ __forceinline__ void values(const T* p, float (&out)[G]) const {
+        uint32_t r[WORDS];
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) r[i] = a.w[i];
+        } else {
+            uint32_t w[2 * WORDS];
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = a.w[i], w[WORDS + i] = b.w[i];
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) % BYTES);
+            // selections, not branches: the groups of several pieces interleave
+            const uint32_t skip = off / 4, bits = off % 4 * 8;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                uint32_t lo = 0, hi = 0;
+#pragma unroll
+                for (int k = 0; k < WORDS; ++k) {
+                    if (skip == (uint32_t)k) lo = w[i + k];
+                    if (skip == (uint32_t)k && i + k + 1 < 2 * WORDS) hi = w[i + k + 1];
+                }
+                r[i] = __funnelshift_r(lo, hi, bits);
+            }
+        }
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) out[i] = __uint_as_float(r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const uint16_t h = (uint16_t)(r[i / 2] >> (i % 2 * 16));
+                out[i] = to_f32(*reinterpret_cast<const T*>(&h));
+            }
+        }
+    }
+};
 
 // G elements to a row at `p`, in one store where that is aligned.
 template <typename T, int G>
@@ -112,7 +137,7 @@ struct EmbedArgs {
 // flight at once (2 KB of a 16-bit row). Groups are aligned in y; the elements
 // before the first and after the last whole group are copied one by one.
 constexpr int kPieces = 4;
-template <typename T, typename O>
+template <typename T, typename O, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int pieces) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int G = 16 / (int)sizeof(O) < 16 / (int)sizeof(T) ? 16 / (int)sizeof(O)
@@ -132,19 +157,18 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int piece
     if (head > a.K) head = a.K;
     const int64_t tail = head + (a.K - head) / G * G;
     const int64_t c0 = head + (piece * kPieces * 32 + lane) * G;
-    float v[kPieces][G];
+    Group<T, G, ALIGNED> v[kPieces];
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-#pragma unroll
-        for (int e = 0; e < G; ++e) v[j][e] = 0.f;
-        if (named && c0 + j * 32 * G < tail) load_group<T, G>(from + c0 + j * 32 * G, v[j]);
-    }
+    for (int j = 0; j < kPieces; ++j)
+        if (named && c0 + j * 32 * G < tail) v[j].load(from + c0 + j * 32 * G);
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
         if (c0 + j * 32 * G >= tail) continue;
+        float f[G] = {};
+        if (named) v[j].values(from + c0 + j * 32 * G, f);
 #pragma unroll
-        for (int e = 0; e < G; ++e) v[j][e] *= a.scale;
-        store_group<O, G>(to + c0 + j * 32 * G, v[j]);
+        for (int e = 0; e < G; ++e) f[e] *= a.scale;
+        store_group<O, G>(to + c0 + j * 32 * G, f);
     }
     if (piece == 0)
         for (int64_t i = lane; i < head + (a.K - tail); i += 32) {
@@ -166,11 +190,12 @@ __device__ __forceinline__ uint32_t token_of(uint64_t x) { return (uint32_t)(x >
 // are exchanged by shuffles, the others through shared memory.
 __global__ void __launch_bounds__(kTile / 2)
     sort_tiles_kernel(const int32_t* __restrict__ ids, int64_t M, int64_t V,
-                      uint64_t* __restrict__ out, ErrWord* err) {
+                      uint64_t* __restrict__ out, uint32_t* __restrict__ count, ErrWord* err) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int HALF = kTile / 2;
     __shared__ uint64_t x[kTile];
     gemm_ptx::pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *count = 0;  // of the pieces, counted later
     const int64_t base = (int64_t)blockIdx.x * kTile;
     const int i0 = threadIdx.x;
     uint64_t v[2];
@@ -288,11 +313,14 @@ struct EmbedGradArgs {
     int64_t kp;       // K rounded up to whole groups
     int chunk;        // sorted numbers of a chunk
     int chunks;
-    int col_blocks;   // blocks that share a chunk's columns
+    int col_warps;    // warps that share a row's columns in the last kernel
+    int col_blocks;   // and blocks (of 128 groups) before that
+    const struct RunPiece* pieces;
+    const uint32_t* count;  // of the pieces
     int64_t sum_blocks;
 };
 
-constexpr int kSumThreads = 128;
+constexpr int kSumThreads = 128, kSumWarps = kSumThreads / 32;
 constexpr int kFillRows = 8;      // rows of the table that a block looks after: small pieces,
                                   // so that the last blocks end together
 
@@ -331,22 +359,24 @@ __device__ __forceinline__ void store_row(O* row, int64_t K, int64_t c, const fl
     const int lane = threadIdx.x & 31;
     // bytes up to the next 16-byte boundary: the same for every lane
     const uint32_t skip = (uint32_t)(-(intptr_t)reinterpret_cast<uintptr_t>(row + c)) & 15u;
+    if (skip == 0) {
+        if (c + G <= K) {
+#pragma unroll
+            for (int g = 0; g < WORDS / 4; ++g)
+                reinterpret_cast<uint4*>(row + c)[g] =
+                    make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+                if (c + e < K) row[c + e] = o[e];
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-    const uint32_t words = skip / 4, bits = skip % 4 * 8;
     uint32_t s[WORDS];
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (words == (uint32_t)k) {
-                lo = w[i + k];
-                if (i + k + 1 < WORDS + 4) hi = w[i + k + 1];
-            }
-        s[i] = __funnelshift_r(lo, hi, bits);
-    }
+    shift_words<WORDS, 4>(w, skip, s);
     const int ahead = (int)skip / ES;  // elements that the lane before takes
 #pragma unroll
     for (int g = 0; g < WORDS / 4; ++g) {
@@ -370,104 +400,158 @@ __device__ __forceinline__ void store_row(O* row, int64_t K, int64_t c, const fl
     }
 }
 
+// G sums of a run to its row of the table; the whole warp calls it.
 template <typename O, int G>
 __device__ __forceinline__ void write_sum(const EmbedGradArgs& a, uint32_t token, int64_t c,
                                           const float (&sum)[G]) {
     O* row = static_cast<O*>(a.dtable) + (int64_t)token * a.lddt;
     float v[G];
 #pragma unroll
-    for (int e = 0; e < G; ++e) {
-        v[e] = a.scale * sum[e];
-        if (a.beta != 0.f && c + e < a.K) v[e] = fmaf(a.beta, to_f32(row[c + e]), v[e]);
+    for (int e = 0; e < G; ++e) v[e] = a.scale * sum[e];
+    if (a.beta != 0.f) {
+        constexpr int PER = 16 / (int)sizeof(O);
+        if (reinterpret_cast<uintptr_t>(row + c) % 16 == 0 && c + G <= a.K) {
+#pragma unroll
+            for (int j = 0; j < G; j += PER) {
+                const Piece<16> old = *reinterpret_cast<const Piece<16>*>(row + c + j);
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    v[j + e] = fmaf(a.beta, to_f32(reinterpret_cast<const O*>(&old)[e]), v[j + e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+                if (c + e < a.K) v[e] = fmaf(a.beta, to_f32(row[c + e]), v[e]);
+        }
+        __syncwarp();  // every lane has read what it adds to
     }
-    __syncwarp();  // every lane has read what it adds to
     store_row<O, G>(row, a.K, c, v);
 }
 
-// The first a.sum_blocks blocks add up chunks; the others look after the rows of
-// the table that no token names (zeros, or beta times what they hold).
-template <typename T, typename O>
+// The list of the pieces: runs of one token within a chunk, in any order (they are
+// summed apart from each other, so results do not depend on it).
+struct RunPiece {
+    uint32_t token, row;    // row: of the piece's first number
+    uint32_t at;            // its place in the sorted list
+    uint32_t count_begins;  // numbers << 2 | goes on after the chunk << 1 | begins here
+};
+
+__global__ void __launch_bounds__(256)
+    embed_pieces_kernel(const uint64_t* __restrict__ sorted, int64_t M, int chunk,
+                        RunPiece* __restrict__ pieces, uint32_t* __restrict__ count) {
+    gemm_ptx::pdl_launch_dependents();
+    __shared__ uint32_t first[9];
+    gemm_ptx::pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint64_t x = p < M ? sorted[p] : ~0ull;
+    const uint32_t token = token_of(x);
+    const bool begins = token != kNone && (p == 0 || token_of(sorted[p - 1]) != token);
+    const bool piece = token != kNone && (begins || p % chunk == 0);
+    const uint32_t mask = __ballot_sync(0xffffffffu, piece);
+    if (lane == 0) first[w] = __popc(mask);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t sum = 0;
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t n = first[i];
+            first[i] = sum;
+            sum += n;
+        }
+        const uint32_t base = sum ? atomicAdd(count, sum) : 0;
+        for (int i = 0; i < 8; ++i) first[i] += base;
+    }
+    __syncthreads();
+    if (!piece) return;
+    // the piece's end: the last number of the chunk that is not above the token's
+    int64_t end = (p / chunk + 1) * chunk;
+    if (end > M) end = M;
+    int64_t lo = p + 1, hi = end;
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (token_of(sorted[mid]) == token) lo = mid + 1;
+        else hi = mid;
+    }
+    const bool goes_on = lo == end && end < M && token_of(sorted[end]) == token;
+    pieces[first[w] + __popc(mask & ((1u << lane) - 1))] =
+        RunPiece{token, (uint32_t)x, (uint32_t)p,
+                 (uint32_t)(lo - p) << 2 | (goes_on ? 2u : 0u) | (begins ? 1u : 0u)};
+}
+
+// Two roles, side by side.
+//
+// Sums (the first a.sum_blocks blocks): a block takes a piece of the list and 128
+// groups of columns at a time, every sum_blocks'th; it reads the next one's entry
+// beside this one's rows. Few registers and little code, so that many pieces are
+// in flight: most have a row or two. (A warp that walked through a chunk and wrote
+// wherever a run ended took three times as long.)
+//
+// The others: the rows of the table that no token names become zeros, or beta times
+// what they hold.
+template <typename T, typename O, bool ALIGNED>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
-    constexpr int G = 16 / (int)sizeof(T);
+    constexpr int G = 16 / (int)sizeof(T), AHEAD = ALIGNED ? 4 : 2;  // rows in flight
     __shared__ uint32_t named;
     __shared__ int64_t range[2];
     gemm_ptx::pdl_wait();
     if (blockIdx.x < a.sum_blocks) {
-        const int64_t chunk = blockIdx.x / a.col_blocks;
-        const int64_t c = ((int64_t)(blockIdx.x % a.col_blocks) * kSumThreads + threadIdx.x) * G;
-        const bool out = c >= a.K;  // such lanes only take part in the stores
-        if (__all_sync(0xffffffffu, out)) return;
-        const int64_t p0 = chunk * a.chunk;
-        const int64_t p1 = p0 + a.chunk < a.M ? p0 + a.chunk : a.M;
-        const uint32_t before = p0 > 0 ? token_of(a.sorted[p0 - 1]) : kNone;
-        const uint32_t after = p1 < a.M ? token_of(a.sorted[p1]) : kNone;
+        // every `stride`th piece, and always the same columns
+        const uint32_t pieces = *a.count, stride = (uint32_t)a.sum_blocks / a.col_blocks;
+        const int64_t c =
+            ((int64_t)(blockIdx.x % (uint32_t)a.col_blocks) * kSumThreads + threadIdx.x) * G;
         const bool whole = c + G <= a.K;
-        float sum[G] = {};
-        uint32_t token = token_of(a.sorted[p0]);
-        bool crossing = p0 > 0 && before == token;  // the run began in an earlier chunk
-        constexpr int AHEAD = 4;
-        for (int64_t p = p0; p < p1; p += AHEAD) {
-            uint32_t tok[AHEAD];
-            float v[AHEAD][G];
+        uint32_t at = blockIdx.x / (uint32_t)a.col_blocks;
+        RunPiece next{};
+        if (at < pieces) next = a.pieces[at];
+        for (; at < pieces; at += stride) {
+            const RunPiece piece = next;
+            if (at + stride < pieces) next = a.pieces[at + stride];
+            const int count = (int)(piece.count_begins >> 2);
+            const bool begins = piece.count_begins & 1u, goes_on = piece.count_begins & 2u;
+            float sum[G] = {};
+            for (int j0 = 0; j0 < count; j0 += AHEAD) {
+                Group<T, G, ALIGNED> v[AHEAD];
+                const T* from[AHEAD];
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                tok[j] = kNone;
-                if (p + j >= p1) continue;
-                const uint64_t x = a.sorted[p + j];
-                tok[j] = token_of(x);
-                if (tok[j] == kNone) continue;
-                const T* row = static_cast<const T*>(a.dy) + (int64_t)(uint32_t)x * a.lddy + c;
-                if (out) {
-#pragma unroll
-                    for (int e = 0; e < G; ++e) v[j][e] = 0.f;
-                } else if (whole) {
-                    load_group<T, G>(row, v[j]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < G; ++e) v[j][e] = c + e < a.K ? to_f32(row[e]) : 0.f;
+                for (int j = 0; j < AHEAD; ++j) {
+                    if (j0 + j >= count) continue;
+                    const uint32_t row = j0 + j == 0 ? piece.row
+                                                     : (uint32_t)a.sorted[piece.at + j0 + j];
+                    from[j] = static_cast<const T*>(a.dy) + (int64_t)row * a.lddy + c;
+                    if (whole) v[j].load(from[j]);
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                if (p + j >= p1) continue;
-                if (tok[j] != token) {  // the run before ends here
-                    if (token != kNone) {
-                        if (crossing) {
-                            float* to = a.part + chunk * 2 * a.kp + c;
-                            if (!out)
-#pragma unroll
-                                for (int e = 0; e < G; ++e) to[e] = sum[e];
-                        } else {
-                            write_sum<O, G>(a, token, c, sum);
-                        }
+                for (int j = 0; j < AHEAD; ++j) {
+                    if (j0 + j >= count) continue;
+                    float f[G] = {};
+                    if (whole) {
+                        v[j].values(from[j], f);
+                    } else {  // a group that the row's end cuts
+                        for (int e = 0; e < G; ++e)
+                            if (c + e < a.K) f[e] = to_f32(from[j][e]);
                     }
-                    token = tok[j];
-                    crossing = false;
 #pragma unroll
-                    for (int e = 0; e < G; ++e) sum[e] = 0.f;
-                }
-                if (token != kNone) {
-#pragma unroll
-                    for (int e = 0; e < G; ++e) sum[e] += v[j][e];
+                    for (int e = 0; e < G; ++e) sum[e] += f[e];
                 }
             }
-        }
-        if (token == kNone) return;
-        const bool goes_on = p1 < a.M && after == token;
-        if (crossing || goes_on) {
-            float* to = a.part + (chunk * 2 + (crossing ? 0 : 1)) * a.kp + c;
-            if (!out)
+            if (begins && !goes_on) {
+                write_sum<O, G>(a, piece.token, c, sum);
+            } else if (c < a.K) {
+                const int64_t chunk = piece.at / (uint32_t)a.chunk;
+                float4* to =
+                    reinterpret_cast<float4*>(a.part + (chunk * 2 + (begins ? 1 : 0)) * a.kp + c);
 #pragma unroll
-                for (int e = 0; e < G; ++e) to[e] = sum[e];
-        } else {
-            write_sum<O, G>(a, token, c, sum);
+                for (int k = 0; k < G / 4; ++k)
+                    to[k] = make_float4(sum[4 * k], sum[4 * k + 1], sum[4 * k + 2],
+                                        sum[4 * k + 3]);
+            }
         }
         return;
     }
     // Rows without a token: which of these kFillRows have one stands in the sorted
     // list between the places of the first and the last.
-    const int64_t v0 = (int64_t)(blockIdx.x - a.sum_blocks) * kFillRows;
+    const int64_t v0 = (blockIdx.x - a.sum_blocks) * kFillRows;
     const int rows = a.V - v0 < kFillRows ? (int)(a.V - v0) : kFillRows;
     if (threadIdx.x == 0) named = 0;
     if (threadIdx.x < 64) {
@@ -506,49 +590,70 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
 }
 
 // A run that crosses chunks: the block of the chunk where it begins adds its
-// partial sums in order.
+// partial sums, each warp a quarter of the chunks in order, and then the quarters.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
-    constexpr int G = 16 / (int)sizeof(T);
+    constexpr int G = 16 / (int)sizeof(T), AHEAD = 64 / G;
+    __shared__ float4 quarter[kSumWarps - 1][G / 4][32];
     gemm_ptx::pdl_wait();
-    const int64_t chunk = blockIdx.x / a.col_blocks;
-    const int64_t c = ((int64_t)(blockIdx.x % a.col_blocks) * kSumThreads + threadIdx.x) * G;
-    const int64_t p0 = chunk * a.chunk, p1 = p0 + a.chunk;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const uint32_t chunk = blockIdx.x / (uint32_t)a.col_warps;
+    const int64_t c = ((int64_t)(blockIdx.x - chunk * (uint32_t)a.col_warps) * 32 + lane) * G;
+    const int64_t p0 = (int64_t)chunk * a.chunk, p1 = p0 + a.chunk;
     if (p1 >= a.M) return;
     const uint32_t token = token_of(a.sorted[p1 - 1]);
     if (token == kNone || token_of(a.sorted[p1]) != token) return;   // no run goes on
     if (p0 > 0 && token_of(a.sorted[p0 - 1]) == token &&
         token_of(a.sorted[p0]) == token) return;                     // it began earlier
     const int64_t end = first_at(a.sorted, a.M, (uint64_t)token + 1);
-    const bool out = c >= a.K;
-    if (__all_sync(0xffffffffu, out)) return;
-    const int64_t last = (end - 1) / a.chunk;
-    float sum[G];
-    const float* from = a.part + (chunk * 2 + 1) * a.kp + c;
+    const bool in = c < a.K;  // the other lanes only take part in the stores
+    // chunk's own sum is its second one; those of the chunks after it their first
+    const int64_t more = (end - 1) / a.chunk - chunk;
+    const int64_t k0 = chunk + 1 + more * w / kSumWarps, k1 = chunk + 1 + more * (w + 1) / kSumWarps;
+    float sum[G] = {};
+    auto add = [&](const float4 (&v)[G / 4]) {
 #pragma unroll
-    for (int e = 0; e < G; ++e) sum[e] = out ? 0.f : from[e];
-    constexpr int AHEAD = 64 / G;
-    for (int64_t k = chunk + 1; k <= last; k += AHEAD) {
-        float4 more[AHEAD][G / 4];
+        for (int q = 0; q < G / 4; ++q) {
+            sum[4 * q] += v[q].x;
+            sum[4 * q + 1] += v[q].y;
+            sum[4 * q + 2] += v[q].z;
+            sum[4 * q + 3] += v[q].w;
+        }
+    };
+    auto load = [&](float4 (&v)[G / 4], int64_t slot) {
+#pragma unroll
+        for (int q = 0; q < G / 4; ++q)
+            v[q] = in ? reinterpret_cast<const float4*>(a.part + slot * a.kp + c)[q]
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (w == 0) {
+        float4 v[G / 4];
+        load(v, (int64_t)chunk * 2 + 1);
+        add(v);
+    }
+    for (int64_t k = k0; k < k1; k += AHEAD) {
+        float4 v[AHEAD][G / 4];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-#pragma unroll
-            for (int q = 0; q < G / 4; ++q)
-                if (k + j <= last && !out)
-                    more[j][q] =
-                        reinterpret_cast<const float4*>(a.part + (k + j) * 2 * a.kp + c)[q];
+            if (k + j < k1) load(v[j], (k + j) * 2);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (k + j <= last && !out) {
+            if (k + j < k1) add(v[j]);
+    }
+    if (w > 0) {
 #pragma unroll
-                for (int q = 0; q < G / 4; ++q) {
-                    sum[4 * q] += more[j][q].x;
-                    sum[4 * q + 1] += more[j][q].y;
-                    sum[4 * q + 2] += more[j][q].z;
-                    sum[4 * q + 3] += more[j][q].w;
-                }
-            }
+        for (int q = 0; q < G / 4; ++q)
+            quarter[w - 1][q][lane] =
+                make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
+    }
+    __syncthreads();
+    if (w > 0) return;
+    for (int o = 0; o < kSumWarps - 1; ++o) {
+        float4 v[G / 4];
+#pragma unroll
+        for (int q = 0; q < G / 4; ++q) v[q] = quarter[o][q][lane];
+        add(v);
     }
     write_sum<O, G>(a, token, c, sum);
 }
@@ -556,6 +661,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGra
 bool rows_ok(const void* p, int64_t rows, int64_t K, int64_t ld, int es) {
     return p && aligned_to(p, es) && ld >= K &&
            (__int128)(rows - 1) * ld + K <= (__int128)(INT64_MAX / es);
+}
+
+bool rows_aligned(const void* p, int64_t ld, int es) {
+    return aligned_to(p, 16) && ld * es % 16 == 0;
 }
 
 int embed(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* table, int64_t ldt,
@@ -578,15 +687,20 @@ int embed(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* table
     const int64_t pieces = (K + group * 32 * kPieces - 1) / (group * 32 * kPieces);
     if (M * pieces > (int64_t)INT32_MAX * 8) return kUnsupported;
     const dim3 grid((unsigned)((M * pieces + 7) / 8));
-    auto run = [&](auto kern) {
-        return launch_dependent(kern, grid, dim3(256), 0, s, a, (int)pieces);
+    // groups start on 16-byte boundaries in both
+    const bool aligned = rows_aligned(table, ldt, ts) && rows_aligned(y, ldy, os);
+    auto run = [&](auto t, auto o) {
+        using T = decltype(t);
+        using O = decltype(o);
+        return launch_dependent(aligned ? embed_kernel<T, O, true> : embed_kernel<T, O, false>,
+                                grid, dim3(256), 0, s, a, (int)pieces);
     };
     switch (dtype) {
-        case GEMM_F32: return run(embed_kernel<float, float>);
-        case GEMM_F16_F32: return run(embed_kernel<__half, float>);
-        case GEMM_BF16_F32: return run(embed_kernel<__nv_bfloat16, float>);
-        case GEMM_F16_F16: return run(embed_kernel<__half, __half>);
-        default: return run(embed_kernel<__nv_bfloat16, __nv_bfloat16>);
+        case GEMM_F32: return run(float{}, float{});
+        case GEMM_F16_F32: return run(__half{}, float{});
+        case GEMM_BF16_F32: return run(__nv_bfloat16{}, float{});
+        case GEMM_F16_F16: return run(__half{}, __half{});
+        default: return run(__nv_bfloat16{}, __nv_bfloat16{});
     }
 }
 
@@ -622,20 +736,26 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
     a.kp = up(K, 16);
     a.chunk = embed_chunk(M);
     a.chunks = (int)((M + a.chunk - 1) / a.chunk);
-    a.col_blocks = (int)((K + (int64_t)group * kSumThreads - 1) / ((int64_t)group * kSumThreads));
-    a.sum_blocks = (int64_t)a.chunks * a.col_blocks;
+    a.col_warps = (int)((K + (int64_t)group * 32 - 1) / ((int64_t)group * 32));
+    a.col_blocks = (a.col_warps + kSumWarps - 1) / kSumWarps;
+    // eight on an SM, where there may be as many pieces; as many for each of the columns
+    const int64_t stride = (dev->sm_count * 8 + a.col_blocks - 1) / a.col_blocks;
+    a.sum_blocks = (M < stride ? M : stride) * a.col_blocks;
+    const int64_t cross_blocks = (int64_t)a.chunks * a.col_warps;
     const int64_t fill = beta == 1.f ? 0 : (V + kFillRows - 1) / kFillRows;
-    if (a.sum_blocks + fill > INT32_MAX) return kUnsupported;
+    if (a.sum_blocks + fill > INT32_MAX || cross_blocks > INT32_MAX) return kUnsupported;
     Scratch scratch{pool, s, dev->device};
     const int64_t list = up(M * 8, 256);
     char* mem = nullptr;
     if (M > 0) {
-        mem = static_cast<char*>(scratch.get((size_t)(2 * list + (int64_t)a.chunks * 2 * a.kp * 4)));
+        const int64_t part = up((int64_t)a.chunks * 2 * a.kp * 4, 256);
+        mem = static_cast<char*>(scratch.get((size_t)(4 * list + part + 4)));
         if (!mem) return kCuda;
         uint64_t* in = reinterpret_cast<uint64_t*>(mem);
         uint64_t* out = reinterpret_cast<uint64_t*>(mem + list);
+        uint32_t* count = reinterpret_cast<uint32_t*>(mem + 4 * list + part);
         rc = launch_dependent(sort_tiles_kernel, dim3((unsigned)((M + kTile - 1) / kTile)),
-                              dim3(kTile / 2), 0, s, ids, M, V, in, dev->err_word);
+                              dim3(kTile / 2), 0, s, ids, M, V, in, count, dev->err_word);
         for (int64_t run = kTile; rc == kOk && run < M; run *= kMerge) {
             const int smem = kMerge * (run <= kSamples ? (int)run : kFew) * 8;
             rc = allow_smem(sort_merge_kernel, kMerge * kSamples * 8, *dev);
@@ -647,28 +767,34 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
             std::swap(in, out);
         }
         a.sorted = in;
-        a.part = reinterpret_cast<float*>(mem + 2 * list);
+        RunPiece* pieces = reinterpret_cast<RunPiece*>(mem + 2 * list);
+        if (rc == kOk)
+            rc = launch_dependent(embed_pieces_kernel, dim3((unsigned)((M + 255) / 256)),
+                                  dim3(256), 0, s, a.sorted, M, a.chunk, pieces, count);
+        a.pieces = pieces;
+        a.count = count;
+        a.part = reinterpret_cast<float*>(mem + 4 * list);
     }
-    auto run = [&](auto sum, auto cross) {
+    const bool aligned = rows_aligned(dy, lddy, ts);
+    auto run = [&](auto t, auto o) {
+        using T = decltype(t);
+        using O = decltype(o);
         int r = rc;
         if (r == kOk && a.sum_blocks + fill > 0)
-            r = launch_dependent(sum, dim3((unsigned)(a.sum_blocks + fill)), dim3(kSumThreads), 0,
-                                 s, a);
+            r = launch_dependent(aligned ? embed_sum_kernel<T, O, true>
+                                         : embed_sum_kernel<T, O, false>,
+                                 dim3((unsigned)(a.sum_blocks + fill)), dim3(kSumThreads), 0, s, a);
         if (r == kOk && a.chunks > 1)
-            r = launch_dependent(cross, dim3((unsigned)a.sum_blocks), dim3(kSumThreads), 0, s, a);
+            r = launch_dependent(embed_cross_kernel<T, O>, dim3((unsigned)cross_blocks),
+                                 dim3(kSumThreads), 0, s, a);
         return r;
     };
     switch (dtype) {
-        case GEMM_F32: rc = run(embed_sum_kernel<float, float>, embed_cross_kernel<float, float>); break;
-        case GEMM_F16_F32: rc = run(embed_sum_kernel<__half, float>, embed_cross_kernel<__half, float>); break;
-        case GEMM_BF16_F32:
-            rc = run(embed_sum_kernel<__nv_bfloat16, float>, embed_cross_kernel<__nv_bfloat16, float>);
-            break;
-        case GEMM_F16_F16: rc = run(embed_sum_kernel<__half, __half>, embed_cross_kernel<__half, __half>); break;
-        default:
-            rc = run(embed_sum_kernel<__nv_bfloat16, __nv_bfloat16>,
-                     embed_cross_kernel<__nv_bfloat16, __nv_bfloat16>);
-            break;
+        case GEMM_F32: rc = run(float{}, float{}); break;
+        case GEMM_F16_F32: rc = run(__half{}, float{}); break;
+        case GEMM_BF16_F32: rc = run(__nv_bfloat16{}, float{}); break;
+        case GEMM_F16_F16: rc = run(__half{}, __half{}); break;
+        default: rc = run(__nv_bfloat16{}, __nv_bfloat16{}); break;
     }
     scratch.release();
     return rc;

@@ -447,13 +447,12 @@ inline int64_t xent_piece_cols(int64_t rows, int64_t N, int parts) {
     return ((N + pieces - 1) / pieces + 255) / 256 * 256;
 }
 
-// embed_rows_grad: sorted tokens of a chunk, which a block (for each share of the
-// columns) adds up: 16, up to 64 for so many tokens that there would be more than
-// 256 chunks (a frequent token's chunks are added up one after the other), and
-// longer where there would be more than 8192.
+// embed_rows_grad: sorted tokens of a chunk, within which a run is added up by one
+// warp (for each share of the columns): 32, a multiple of that where there would be
+// more than 8192 chunks.
 inline int embed_chunk(int64_t M) {
-    const int64_t n = (M + 255) / 256, most = (M + 8191) / 8192;
-    return (int)(most > 64 ? most : n < 16 ? 16 : n > 64 ? 64 : n);
+    const int64_t n = (M + 8191) / 8192;
+    return n <= 32 ? 32 : (int)((n + 31) / 32 * 32);
 }
 
 }  // namespace libgemm
