@@ -425,6 +425,33 @@ inline XentShape plan_xent(int64_t M, int64_t N, int sm_count, bool forward) {
     return XentShape{1, ((M + 127) / 128) * ((N + 63) / 64) <= sm_count ? 64 : 128};
 }
 
+// gemm_xent_grad: how dX (M x K, the depth the `n` columns of a piece of the
+// vocabulary) runs when its tiles alone would leave SMs idle: so many shares of the
+// depth (splits; 1: gemm()'s kernel), of at least 512 columns, that the rounds of
+// units times the length of one is least, and the fewest such (each leaves an fp32
+// part of dX to add up). Tiles as in plan_xent; at most 128 rows are bound by
+// reading W.
+struct XentSumPlan {
+    XentShape shape;
+    int splits;
+    int64_t each(int64_t n) const { return ((n + 63) / 64 + splits - 1) / splits; }  // blocks
+    int used(int64_t n) const { return (int)(((n + 63) / 64 + each(n) - 1) / each(n)); }
+};
+inline XentSumPlan plan_xent_sum(int64_t M, int64_t K, int64_t n, int sm_count) {
+    XentSumPlan plan{M > 128 ? XentShape{2, 256} : XentShape{1, 128}, 1};
+    const int rows = 128 * plan.shape.cta_group, slots = sm_count / plan.shape.cta_group;
+    const int64_t tiles = ((M + rows - 1) / rows) *
+                          ((K + plan.shape.tile_n - 1) / plan.shape.tile_n);
+    if (tiles * 2 > slots) return plan;
+    const int64_t most = n / 512 < 64 ? n / 512 : 64;
+    double best = 1.0;  // one round of whole tiles
+    for (int s = 2; s <= most; ++s) {
+        const double t = (double)((tiles * s + slots - 1) / slots) / s;
+        if (t < best * 0.97) best = t, plan.splits = s;
+    }
+    return plan;
+}
+
 // Rows of gemm_xent that run together: a whole number of tiles whose partial
 // maxima and sums (16 bytes for every row and tile of 32 columns or more) stay
 // within 256 MB.

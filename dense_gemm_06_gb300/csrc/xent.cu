@@ -169,51 +169,78 @@ __global__ void __launch_bounds__(1024)
     scale[1] = ldexpf(1.f, -e);
 }
 
-// out = scale * sum + beta * out, rounded once; rows x cols, four columns a thread.
+// out = scale * (the sum of `parts` matrices, part_rows rows apart) + beta * out,
+// rounded once; rows x cols, four columns a thread, blocks of 1024 columns by rows.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    xent_finish_kernel(const float* __restrict__ sum, int64_t lds, T* __restrict__ out, int64_t ldo,
-                       int64_t rows, int64_t cols, const float* __restrict__ scale, float beta) {
+    xent_finish_kernel(const float* __restrict__ sum, int64_t lds, int parts, int64_t part_rows,
+                       T* __restrict__ out, int64_t ldo, int64_t rows, int cols,
+                       const float* __restrict__ scale, float beta) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
+    constexpr int AHEAD = 4;  // rows in flight
     const float by = scale ? *scale : 1.f;
-    const int64_t quads = (cols + 3) / 4;
-    const bool whole = ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * quads; i += step) {
-        const int64_t r = i / quads, c = (i - r * quads) * 4;
-        const float4 v = *reinterpret_cast<const float4*>(sum + r * lds + c);  // lds % 4 == 0
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        T* dst = out + r * ldo + c;
-        const int n = cols - c < 4 ? (int)(cols - c) : 4;
-        alignas(16) T o[4];
-        for (int e = 0; e < 4; ++e)
-            if (e < n) o[e] = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(dst[e]), by * f[e])
-                                                      : by * f[e]);
-        if (whole && n == 4) {
-            if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
-            else
-                *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
-        } else {
-            for (int e = 0; e < n; ++e) dst[e] = o[e];
+    const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (c >= cols) return;
+    const bool whole =
+        c + 4 <= cols && ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
+    for (int64_t r0 = blockIdx.x; r0 < rows; r0 += (int64_t)AHEAD * gridDim.x) {
+        float4 v[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t r = r0 + j * (int64_t)gridDim.x;
+            if (r < rows) v[j] = *reinterpret_cast<const float4*>(sum + r * lds + c);  // lds % 4 == 0
+        }
+        for (int p = 1; p < parts; ++p) {
+            float4 more[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int64_t r = r0 + j * (int64_t)gridDim.x;
+                if (r < rows)
+                    more[j] = *reinterpret_cast<const float4*>(sum + (p * part_rows + r) * lds + c);
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                v[j].x += more[j].x, v[j].y += more[j].y, v[j].z += more[j].z, v[j].w += more[j].w;
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t r = r0 + j * (int64_t)gridDim.x;
+            if (r >= rows) continue;
+            T* dst = out + r * ldo + c;
+            const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            alignas(16) T o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols)
+                    o[e] = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(dst[e]), by * f[e])
+                                                   : by * f[e]);
+            if (whole) {
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+                else
+                    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) dst[e] = o[e];
+            }
         }
     }
 }
 
-int finish(const float* sum, int64_t lds, void* out, int64_t ldo, int64_t rows, int64_t cols,
-           const float* scale, float beta, int esize, bool bf16, const DeviceInfo& dev,
-           cudaStream_t s) {
-    const int64_t blocks = (rows * ((cols + 3) / 4) + 255) / 256;
-    const dim3 grid((unsigned)(blocks < dev.sm_count * 16 ? blocks : dev.sm_count * 16));
-    if (esize == 4)
-        return launch_dependent(xent_finish_kernel<float>, grid, dim3(256), 0, s, sum, lds,
-                                static_cast<float*>(out), ldo, rows, cols, scale, beta);
-    if (bf16)
-        return launch_dependent(xent_finish_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, sum, lds,
-                                static_cast<__nv_bfloat16*>(out), ldo, rows, cols, scale, beta);
-    return launch_dependent(xent_finish_kernel<__half>, grid, dim3(256), 0, s, sum, lds,
-                            static_cast<__half*>(out), ldo, rows, cols, scale, beta);
+int finish(const float* sum, int64_t lds, int parts, int64_t part_rows, void* out, int64_t ldo,
+           int64_t rows, int64_t cols, const float* scale, float beta, int esize, bool bf16,
+           const DeviceInfo& dev, cudaStream_t s) {
+    const int64_t wide = (cols + 1023) / 1024, most = (dev.sm_count * 16 + wide - 1) / wide;
+    const dim3 grid((unsigned)(rows < most ? rows : most), (unsigned)wide);
+    auto run = [&](auto t) {
+        using T = decltype(t);
+        return launch_dependent(xent_finish_kernel<T>, grid, dim3(256), 0, s, sum, lds, parts,
+                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, scale, beta);
+    };
+    if (esize == 4) return run(float{});
+    return bf16 ? run(__nv_bfloat16{}) : run(__half{});
 }
 
 // Checks of X, W and target that both calls make; no CUDA calls.
@@ -257,14 +284,22 @@ int repack_one(const void*& p, int64_t& ld, int64_t rows, int64_t cols, char* to
     return kOk;
 }
 
+int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const DeviceInfo& dev,
+           cudaStream_t s);
+
+// The depth that one accumulator takes: equal parts of at most kXentFold blocks.
+void fold_depth(XentParams& xp) {
+    const int parts = (xp.num_kb + kXentFold - 1) / kXentFold;
+    xp.part_kb = parts > 0 ? (xp.num_kb + parts - 1) / parts : 1;
+}
+
 void xent_params(XentParams& xp, int64_t M, int64_t N, int64_t K, const XentShape& shape,
                  int64_t vocab, const int32_t* target, const DeviceInfo& dev) {
     std::memset(&xp, 0, sizeof(xp));
     xp.M = (int)M;
     xp.N = (int)N;
     xp.num_kb = (int)((K + XBK - 1) / XBK);
-    const int parts = (xp.num_kb + kXentFold - 1) / kXentFold;
-    xp.part_kb = (xp.num_kb + parts - 1) / parts;
+    fold_depth(xp);
     xp.tile_n = shape.tile_n;
     xp.tiles_m = (int)((M + XROWS * shape.cta_group - 1) / (XROWS * shape.cta_group));
     xp.tiles_n = (int)((N + shape.tile_n - 1) / shape.tile_n);
@@ -295,14 +330,37 @@ bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void
                          (uint32_t)(shape.tile_n / shape.cta_group));
 }
 
+// dX's part of a piece (n columns, in a vocabulary cut into pieces of `piece`) in
+// shares of the depth that are the same for every piece: sums (+)= G W.
+int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int64_t n,
+               const void* g, int64_t ldg, const void* W, int64_t ldw, float* sums, int64_t sum_rows, bool add,
+               bool bf16, const DeviceInfo& dev, cudaStream_t s) {
+    XentParams xp;
+    xent_params(xp, M, K, 0, plan.shape, 0, nullptr, dev);
+    xp.all_kb = (int)((n + XBK - 1) / XBK);
+    xp.num_kb = (int)plan.each(piece);
+    xp.splits = (xp.all_kb + xp.num_kb - 1) / xp.num_kb;
+    fold_depth(xp);
+    xp.sums = sums;
+    xp.sum_ld = up(K, 4);
+    xp.sum_rows = sum_rows;
+    xp.add = add ? 1 : 0;
+    if (!encode_tma_16(&xp.map_x, bf16, g, (uint64_t)n, (uint64_t)M, (uint64_t)ldg, 0, 0, XBK,
+                       plan.shape.cta_group == 2 ? XROWS : (uint32_t)xp.x_rows) ||
+        !encode_tma_16(&xp.map_w, bf16, W, (uint64_t)K, (uint64_t)n, (uint64_t)ldw, 0, 0, 64, XBK))
+        return kCuda;
+    return launch(xp, kXentSum, bf16, plan.shape, dev, s);
+}
+
 int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const DeviceInfo& dev,
            cudaStream_t s) {
-    if ((int64_t)xp.tiles_m * xp.tiles_n * 2 > INT32_MAX) return kUnsupported;
+    const int64_t units = (int64_t)xp.tiles_m * xp.tiles_n * (mode == kXentSum ? xp.splits : 1);
+    if (units * 2 > INT32_MAX) return kUnsupported;
     xp.stages = stages_of(xp, mode);
     const int rc = bf16 ? launch_xent_bf16(xp, mode, shape.cta_group, dev, s)
                         : launch_xent_f16(xp, mode, shape.cta_group, dev, s);
     dispatch_log("cross entropy %s %dx%d, %d k-blocks: %s, %d x %d tiles of %d columns",
-                 mode == kXentStats ? "logits" : "gradient's logits", xp.M, xp.N, xp.num_kb,
+                 mode == kXentStats ? "logits" : mode == kXentSum ? "dX" : "gradient's logits", xp.M, xp.N, xp.num_kb,
                  shape.cta_group == 2 ? "CTA pairs" : "one CTA per tile", xp.tiles_m, xp.tiles_n,
                  xp.tile_n);
     return rc;
@@ -358,7 +416,7 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
         rc = launch(xp, kXentStats, bf16, shape, *dev, s);
         if (rc != kOk) break;
         // few rows: more threads for each
-        const int rows = m <= 2 * dev->sm_count ? 2 : m <= 8 * dev->sm_count ? 8 : 32;
+        const int rows = m <= 4 * dev->sm_count ? 2 : m <= 24 * dev->sm_count ? 8 : 32;
         auto join = [&](auto kern) {
             return launch_dependent(kern, dim3((unsigned)((m + rows - 1) / rows)),
                                     dim3(kJoinThreads), 0, s, (const float2*)xp.part, xp.part_ld,
@@ -433,14 +491,17 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const XentShape shape = plan_xent(M, piece, dev->sm_count, false);  // of every piece
     const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
     const int64_t pieces = (N + piece - 1) / piece;
-    const bool sum_dx = dX && (pieces > 1 || scaled);
+    // dX by shares of the depth where its tiles are few, else through gemm()'s kernel
+    const XentSumPlan plan = plan_xent_sum(M, K, piece, dev->sm_count);
+    const bool split_dx = dX && plan.splits > 1;
+    const bool sum_dx = dX && (pieces > 1 || scaled || split_dx);
     const int64_t ldg = up(piece, 256), ldk = up(K, 8);
     Parts at;
     const int64_t g_at = at.add(ldg * rows * parts * 2);
     const bool copy_x = dW || !tma_ready(X, ldx);
     const int64_t x_at = copy_x ? at.add(ldk * rows * parts * 2) : -1;
     const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * ldk * 2);
-    const int64_t dx_at = sum_dx ? at.add(M * up(K, 4) * 4) : -1;
+    const int64_t dx_at = sum_dx ? at.add(plan.splits * M * up(K, 4) * 4) : -1;
     const int64_t dw_at = dW && scaled ? at.add(piece * up(K, 4) * 4) : -1;
     const int64_t scale_at = scaled ? at.add(8) : -1;
     const int64_t limits_at = at.add(8);
@@ -490,7 +551,9 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
             break;
         }
         rc = launch(xp, parts == 2 ? kXentGrad2 : kXentGrad, bf16, shape, *dev, s);
-        if (rc == kOk && dX)
+        if (rc == kOk && split_dx)
+            rc = launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, bf16, *dev, s);
+        else if (rc == kOk && dX)
             rc = sum_dx ? product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dx_sum,
                                   up(K, 4), f32, v0 > 0 ? 1.f : 0.f, *dev, s)
                         : product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dX, lddx,
@@ -509,12 +572,12 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
                             : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN,
                                       dw_sum, up(K, 4), f32, 0.f, *dev, s);
             if (rc == kOk)
-                rc = finish(dw_sum, up(K, 4), dst, lddw, n, K, scale + 1, beta, we, bf16, *dev, s);
+                rc = finish(dw_sum, up(K, 4), 1, 0, dst, lddw, n, K, scale + 1, beta, we, bf16, *dev, s);
         }
     }
     if (rc == kOk && sum_dx)
-        rc = finish(dx_sum, up(K, 4), dX, lddx, M, K, scaled ? scale + 1 : nullptr, 0.f, 2, bf16,
-                    *dev, s);
+        rc = finish(dx_sum, up(K, 4), split_dx ? plan.used(piece) : 1, M, dX, lddx, M, K,
+                    scaled ? scale + 1 : nullptr, 0.f, 2, bf16, *dev, s);
     scratch.release();
     return rc;
 }

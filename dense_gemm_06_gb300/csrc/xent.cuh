@@ -6,7 +6,11 @@
 //   kGrad   G = d (exp(z - lse) - [v = target]) rounded to 16 bits, for the
 //           products dX = G W and dW = G^T X (16-bit results);
 //   kGrad2  the same as two 16-bit numbers, hi = rn(g) and lo = rn(g - hi), for
-//           an fp32 dW.
+//           an fp32 dW;
+//   kSum    dX = G W where its tiles are few: the depth (the piece's columns of
+//           the vocabulary) is shared by several CTAs or pairs a tile, each of
+//           which leaves an fp32 part (1531 rows of 1037 from 50001 columns: 220 us
+//           with a CTA for each of 108 whole tiles, 100 us so).
 //
 // The pipeline is the dense kernel's: warp 0 copies 64-deep blocks of X and W by
 // TMA into a ring, warp 1 issues the MMAs (a CTA pair on 256 x 256 tiles, or one
@@ -39,9 +43,11 @@
 
 namespace libgemm {
 
-enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2 };
+enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2, kXentSum = 3 };
 
 struct XentParams {
+    // kSum: X is G (rows of the piece's columns), W its rows of W read N-major, M x N
+    // the rows and columns of dX, num_kb the blocks of one share of the depth.
     CUtensorMap map_x;   // M x K: boxes of 64 x 128 (one CTA a tile: x_rows) rows
     CUtensorMap map_w;   // the piece's N x K: boxes of 64 x (tile_n / CG) rows
     CUtensorMap map_g;   // kGrad, kGrad2: G, boxes of 64 columns x 32 rows
@@ -60,6 +66,10 @@ struct XentParams {
     float2* part;        // kStats: (maximum, sum) of each row, half tile by half tile
     int64_t part_ld;     // rows of a half tile in `part`
     float* picked;       // kStats: each row's target logit
+    float* sums;         // kSum: splits x sum_rows x sum_ld
+    int64_t sum_ld, sum_rows;
+    int splits, all_kb;  // shares of the depth, and the blocks of all of them
+    int add;             // kSum: add to what `sums` holds
     const float* lse;
     const float* dloss;  // null: ones
     const float* scale;  // null: 1; a power of two that keeps fp16 numbers in range
@@ -231,8 +241,13 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
     const int cluster = CG == 2 ? (int)cluster_id_x() : (int)blockIdx.x;
     const int nclusters = CG == 2 ? (int)num_clusters_x() : (int)gridDim.x;
-    const int total = p.tiles_m * p.tiles_n;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int total = MODE == kXentSum ? tiles * p.splits : tiles;
     constexpr int ACC_COLS = CG == 2 ? 256 : 128;  // TMEM columns of an accumulator
+    // depth blocks of a unit (kSum: the last share may be shorter)
+    auto blocks_of = [&](int split) {
+        return MODE == kXentSum ? min(p.num_kb, p.all_kb - split * p.num_kb) : p.num_kb;
+    };
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&p.map_x);
@@ -268,17 +283,25 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         const int b_rows = p.tile_n / CG;
         const uint32_t bytes = (uint32_t)(CG * (x_bytes + b_rows * XBK * 2));
         for (int t = cluster; t < total && !aborted; t += nclusters) {
-            const int2 tile = xent_tile(t, p);
+            const int split = MODE == kXentSum ? t / tiles : 0;
+            const int2 tile = xent_tile(MODE == kXentSum ? t - split * tiles : t, p);
             const int x_row = (tile.x * CG + (int)rank) * XROWS;
             const int w_row = tile.y * p.tile_n + (int)rank * b_rows;
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            const int kb0 = split * p.num_kb, kbs = blocks_of(split);
+            for (int kb = 0; kb < kbs; ++kb) {
                 if (!xent_wait(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
                 const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
                 const uint32_t at = base + stage * stage_bytes;
                 if (xent_elect()) {
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), bytes);
-                    tma_load_2d<CG>(at, &p.map_x, fb, kb * XBK, x_row);
-                    tma_load_2d<CG>(at + x_bytes, &p.map_w, fb, kb * XBK, w_row);
+                    tma_load_2d<CG>(at, &p.map_x, fb, (kb0 + kb) * XBK, x_row);
+                    if constexpr (MODE == kXentSum) {
+                        for (int j = 0; j < b_rows / 64; ++j)  // boxes of 64 columns
+                            tma_load_2d<CG>(at + x_bytes + j * 64 * XBK * 2, &p.map_w, fb,
+                                            w_row + 64 * j, (kb0 + kb) * XBK);
+                    } else {
+                        tma_load_2d<CG>(at + x_bytes, &p.map_w, fb, kb * XBK, w_row);
+                    }
                 }
                 __syncwarp();
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -294,18 +317,23 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         // ---------------------------------------------------- MMA issuer --
         give_registers();
         if (rank == 0) {
-            const uint32_t idesc = make_idesc_f16(BF16, false, false, (uint32_t)(XROWS * CG),
+            // W is K-major, 32 bytes a step of 16 deep, or (kSum) N-major, 16 rows of 128
+            constexpr bool W_MN = MODE == kXentSum;
+            constexpr uint64_t W_STEP = W_MN ? 16 * 128 >> 4 : 32 >> 4;
+            const uint32_t idesc = make_idesc_f16(BF16, false, W_MN, (uint32_t)(XROWS * CG),
                                                   (uint32_t)p.tile_n);
             const uint64_t x_desc0 = make_sdesc_sw128(base, 16, 1024);
-            const uint64_t w_desc0 = make_sdesc_sw128(base + x_bytes, 16, 1024);
+            const uint64_t w_desc0 =
+                make_sdesc_sw128(base + x_bytes, W_MN ? 64 * XBK * 2 : 16, 1024);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             for (int t = cluster; t < total && !aborted; t += nclusters) {
-                for (int kb = 0; kb < p.num_kb && !aborted;) {
+                const int kbs = blocks_of(MODE == kXentSum ? t / tiles : 0);
+                for (int kb = 0; kb < kbs && !aborted;) {
                     if (!xent_wait(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
                     tc_fence_after_sync();
                     const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
-                    const int end = min(kb + p.part_kb, p.num_kb);
+                    const int end = min(kb + p.part_kb, kbs);
                     uint32_t add = 0;
                     for (; kb < end; ++kb) {
                         if (!xent_wait(full_bar(stage), phase, p)) { aborted = true; break; }
@@ -315,8 +343,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                         if (xent_elect()) {
 #pragma unroll
                             for (int j = 0; j < XBK / 16; ++j)
-                                mma_f16<CG>(d, xd + (uint64_t)(2 * j), wd + (uint64_t)(2 * j),
-                                            idesc, j > 0 ? 1u : add);
+                                mma_f16<CG>(d, xd + (uint64_t)(2 * j), wd + W_STEP * (uint64_t)j, idesc,
+                                            j > 0 ? 1u : add);
                             mma_commit<CG>(empty_bar(stage));
                         }
                         __syncwarp();
@@ -365,12 +393,14 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         if (MODE != kXentStats && p.scale) alpha *= *p.scale;
         if (p.fault_inject == 1 && !xent_wait_inline(never_bar, 0u, p)) aborted = true;
         for (int t = cluster; t < total && !aborted; t += nclusters) {
-            const int2 tile = xent_tile(t, p);
+            const int split = MODE == kXentSum ? t / tiles : 0;
+            const int2 tile = xent_tile(MODE == kXentSum ? t - split * tiles : t, p);
+            const int kbs = blocks_of(split);
             const int row0 = (tile.x * CG + (int)rank) * XROWS + q * 32;
             const int row = row0 + lane;
             int target = -1;
             float lse2 = 0.f, d = 0.f;
-            if (row < p.M) {
+            if (MODE != kXentSum && row < p.M) {
                 const int v = p.target[row];
                 if (v >= 0 && v < p.vocab) target = v;
                 if (v >= p.vocab) report_bad_value(p.err);
@@ -388,7 +418,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             float parts[BLOCKS * 64];
 #pragma unroll
             for (int i = 0; i < BLOCKS * 64; ++i) parts[i] = 0.f;
-            for (int kb = p.part_kb; kb < p.num_kb; kb += p.part_kb) {
+            for (int kb = p.part_kb; kb < kbs; kb += p.part_kb) {
                 if (!xent_wait_inline(accf_bar(acc), acc_phase, p)) { aborted = true; break; }
                 tc_fence_after_sync();
 #pragma unroll
@@ -430,7 +460,23 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                         v[i] = __float_as_uint(parts[j * 64 + h * 32 + i] + __uint_as_float(v[i]));
                     const int first = col + h * 32;
                     const int at = counts && rel < end ? rel - first : -1;  // the target's place in v
-                    if constexpr (MODE == kXentStats) {
+                    if constexpr (MODE == kXentSum) {
+                        if (row < p.M) {
+                            float* to = p.sums + (split * p.sum_rows + row) * p.sum_ld + first;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                if (first + i >= p.sum_ld) continue;  // sum_ld % 4 == 0
+                                float4 o = make_float4(
+                                    __uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                    __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                                if (p.add) {
+                                    const float4 old = *reinterpret_cast<const float4*>(to + i);
+                                    o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
+                                }
+                                *reinterpret_cast<float4*>(to + i) = o;
+                            }
+                        }
+                    } else if constexpr (MODE == kXentStats) {
                         if (end - first < 32) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -518,7 +564,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             release(acc);
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (MODE != kXentStats && lane == 0) bulk_wait_all();
+        if ((MODE == kXentGrad || MODE == kXentGrad2) && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
         give_registers();
@@ -574,7 +620,7 @@ int launch_xent_variant(XentParams& xp, const DeviceInfo& dev, cudaStream_t stre
             configured |= bit;
         }
     }
-    const int64_t tiles = (int64_t)xp.tiles_m * xp.tiles_n;
+    const int64_t tiles = (int64_t)xp.tiles_m * xp.tiles_n * (MODE == kXentSum ? xp.splits : 1);
     int n = resident[dev.device & 63];
     if (n > tiles) n = (int)tiles;
     cfg.gridDim = dim3(CG * n);
@@ -595,8 +641,11 @@ int launch_xent(XentParams& xp, int mode, int cg, const DeviceInfo& dev, cudaStr
     if (mode == kXentGrad)
         return cg == 2 ? launch_xent_variant<kXentGrad, 2, BF16>(xp, dev, s)
                        : launch_xent_variant<kXentGrad, 1, BF16>(xp, dev, s);
-    return cg == 2 ? launch_xent_variant<kXentGrad2, 2, BF16>(xp, dev, s)
-                   : launch_xent_variant<kXentGrad2, 1, BF16>(xp, dev, s);
+    if (mode == kXentGrad2)
+        return cg == 2 ? launch_xent_variant<kXentGrad2, 2, BF16>(xp, dev, s)
+                       : launch_xent_variant<kXentGrad2, 1, BF16>(xp, dev, s);
+    return cg == 2 ? launch_xent_variant<kXentSum, 2, BF16>(xp, dev, s)
+                   : launch_xent_variant<kXentSum, 1, BF16>(xp, dev, s);
 }
 
 }  // namespace

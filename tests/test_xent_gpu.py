@@ -183,6 +183,19 @@ def test_pieces_of_the_vocabulary(dtype):
     compare(65700, 5000, 16, dtype, out=0.5)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 2000, 40), (7, 33000, 130), (130, 20000, 264),
+                                   (600, 9001, 1037), (1531, 12007, 776)])
+def test_dx_by_shares_of_the_vocabulary(M, N, K, dtype):
+    """Few tiles of dX: its depth is shared out."""
+    compare(M, N, K, dtype)
+
+
+def test_dx_by_shares_in_pieces():
+    """The shares add up over pieces of the vocabulary, the last one shorter."""
+    compare(300, 900001, 16, BF, out=0.1)
+
+
 def test_panels_of_rows():
     M, N, K = 4200, 1 << 20, 8
     X, W, target, _ = inputs(M, N, K, BF)
