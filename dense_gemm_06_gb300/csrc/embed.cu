@@ -31,29 +31,10 @@ namespace {
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// r = the words from byte `off` (below 4 WORDS_OFF) of w on. `off` is the same in
-// every lane, so that the cases are branches and not selections.
-template <int WORDS, int WORDS_OFF, int HAVE>
-__device__ __forceinline__ void shift_words(const uint32_t (&w)[HAVE], uint32_t off,
-                                            uint32_t (&r)[WORDS]) {
-    const uint32_t bits = off % 4 * 8;
-#pragma unroll
-    for (int k = 0; k < WORDS_OFF; ++k)
-        if (off / 4 == (uint32_t)k) {
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i)
-                r[i] = __funnelshift_r(w[i + k], i + k + 1 < HAVE ? w[i + k + 1] : 0u, bits);
-        }
-}
-
 // G elements of a row on their way: the aligned piece that begins with them, or
 // (ALIGNED false) the one or two aligned pieces that hold them. The second one is
 // read only where it holds one of them, else the first again, so that the reads of
 // several groups are in flight together, without branches between them.
-template <int BYTES>
-struct alignas(BYTES) Piece {
-    uint32_t w[BYTES / 4];
-};
 template <typename T, int G, bool ALIGNED>
 struct Group {
     static constexpr int BYTES = G * (int)sizeof(T), WORDS = BYTES / 4;
@@ -190,12 +171,12 @@ __device__ __forceinline__ uint32_t token_of(uint64_t x) { return (uint32_t)(x >
 // are exchanged by shuffles, the others through shared memory.
 __global__ void __launch_bounds__(kTile / 2)
     sort_tiles_kernel(const int32_t* __restrict__ ids, int64_t M, int64_t V,
-                      uint64_t* __restrict__ out, uint32_t* __restrict__ count, ErrWord* err) {
+                      uint64_t* __restrict__ out, uint32_t* __restrict__ counts, ErrWord* err) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int HALF = kTile / 2;
     __shared__ uint64_t x[kTile];
     gemm_ptx::pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *count = 0;  // of the pieces, counted later
+    if (blockIdx.x == 0 && threadIdx.x < 2) counts[threadIdx.x] = 0;  // for a later kernel
     const int64_t base = (int64_t)blockIdx.x * kTile;
     const int i0 = threadIdx.x;
     uint64_t v[2];
@@ -316,7 +297,8 @@ struct EmbedGradArgs {
     int col_warps;    // warps that share a row's columns in the last kernel
     int col_blocks;   // and blocks (of 128 groups) before that
     const struct RunPiece* pieces;
-    const uint32_t* count;  // of the pieces
+    const uint32_t* crossing;
+    const uint32_t* counts;  // of pieces and crossing
     int64_t sum_blocks;
 };
 
@@ -341,65 +323,6 @@ __device__ __forceinline__ int64_t first_at(const uint64_t* sorted, int64_t M, u
     return lo;
 }
 
-// G elements of a row from column c on, held by each lane of a warp one group after
-// the other (the whole warp calls it, lanes past the row's end too). Where the row
-// starts on no 16-byte boundary, lanes hand the beginning of their groups to the
-// lane before, so that all but the warp's first and last elements still leave in
-// 16-byte stores (2-byte stores of rows of 1803 took two thirds of the kernel).
-template <typename O, int G>
-__device__ __forceinline__ void store_row(O* row, int64_t K, int64_t c, const float (&v)[G]) {
-    constexpr int ES = (int)sizeof(O), WORDS = G * ES / 4, PER = 16 / ES;
-    static_assert(WORDS % 4 == 0, "whole 16-byte pieces");
-    alignas(16) O o[G];
-#pragma unroll
-    for (int e = 0; e < G; ++e) o[e] = from_f32<O>(v[e]);
-    uint32_t w[WORDS + 4];
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<uint32_t*>(o)[i];
-    const int lane = threadIdx.x & 31;
-    // bytes up to the next 16-byte boundary: the same for every lane
-    const uint32_t skip = (uint32_t)(-(intptr_t)reinterpret_cast<uintptr_t>(row + c)) & 15u;
-    if (skip == 0) {
-        if (c + G <= K) {
-#pragma unroll
-            for (int g = 0; g < WORDS / 4; ++g)
-                reinterpret_cast<uint4*>(row + c)[g] =
-                    make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-                if (c + e < K) row[c + e] = o[e];
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-    uint32_t s[WORDS];
-    shift_words<WORDS, 4>(w, skip, s);
-    const int ahead = (int)skip / ES;  // elements that the lane before takes
-#pragma unroll
-    for (int g = 0; g < WORDS / 4; ++g) {
-        const int64_t c0 = c + ahead + g * PER;  // the piece's first element
-        // of the last lane's last piece the next warp has the rest
-        const int have = lane == 31 && g == WORDS / 4 - 1 ? PER - ahead : PER;
-        if (c0 + PER <= K && have == PER) {
-            *reinterpret_cast<uint4*>(row + c0) =
-                make_uint4(s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]);
-        } else {
-            const O* piece = reinterpret_cast<const O*>(s + 4 * g);
-#pragma unroll
-            for (int e = 0; e < PER; ++e)
-                if (e < have && c0 + e < K) row[c0 + e] = piece[e];
-        }
-    }
-    if (lane == 0) {  // no lane before
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-            if (e < ahead && c + e < K) row[c + e] = o[e];
-    }
-}
-
 // G sums of a run to its row of the table; the whole warp calls it.
 template <typename O, int G>
 __device__ __forceinline__ void write_sum(const EmbedGradArgs& a, uint32_t token, int64_t c,
@@ -408,23 +331,7 @@ __device__ __forceinline__ void write_sum(const EmbedGradArgs& a, uint32_t token
     float v[G];
 #pragma unroll
     for (int e = 0; e < G; ++e) v[e] = a.scale * sum[e];
-    if (a.beta != 0.f) {
-        constexpr int PER = 16 / (int)sizeof(O);
-        if (reinterpret_cast<uintptr_t>(row + c) % 16 == 0 && c + G <= a.K) {
-#pragma unroll
-            for (int j = 0; j < G; j += PER) {
-                const Piece<16> old = *reinterpret_cast<const Piece<16>*>(row + c + j);
-#pragma unroll
-                for (int e = 0; e < PER; ++e)
-                    v[j + e] = fmaf(a.beta, to_f32(reinterpret_cast<const O*>(&old)[e]), v[j + e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-                if (c + e < a.K) v[e] = fmaf(a.beta, to_f32(row[c + e]), v[e]);
-        }
-        __syncwarp();  // every lane has read what it adds to
-    }
+    if (a.beta != 0.f) add_row<O, G>(row, a.K, c, a.beta, v);
     store_row<O, G>(row, a.K, c, v);
 }
 
@@ -436,9 +343,12 @@ struct RunPiece {
     uint32_t count_begins;  // numbers << 2 | goes on after the chunk << 1 | begins here
 };
 
+// counts: of the pieces, and of `crossing`, the chunks in which a run begins that
+// goes on in the next one (one at most in a chunk).
 __global__ void __launch_bounds__(256)
     embed_pieces_kernel(const uint64_t* __restrict__ sorted, int64_t M, int chunk,
-                        RunPiece* __restrict__ pieces, uint32_t* __restrict__ count) {
+                        RunPiece* __restrict__ pieces, uint32_t* __restrict__ crossing,
+                        uint32_t* __restrict__ counts) {
     gemm_ptx::pdl_launch_dependents();
     __shared__ uint32_t first[9];
     gemm_ptx::pdl_wait();
@@ -458,7 +368,7 @@ __global__ void __launch_bounds__(256)
             first[i] = sum;
             sum += n;
         }
-        const uint32_t base = sum ? atomicAdd(count, sum) : 0;
+        const uint32_t base = sum ? atomicAdd(counts, sum) : 0;
         for (int i = 0; i < 8; ++i) first[i] += base;
     }
     __syncthreads();
@@ -473,6 +383,7 @@ __global__ void __launch_bounds__(256)
         else hi = mid;
     }
     const bool goes_on = lo == end && end < M && token_of(sorted[end]) == token;
+    if (begins && goes_on) crossing[atomicAdd(counts + 1, 1u)] = (uint32_t)(p / chunk);
     pieces[first[w] + __popc(mask & ((1u << lane) - 1))] =
         RunPiece{token, (uint32_t)x, (uint32_t)p,
                  (uint32_t)(lo - p) << 2 | (goes_on ? 2u : 0u) | (begins ? 1u : 0u)};
@@ -497,7 +408,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
     gemm_ptx::pdl_wait();
     if (blockIdx.x < a.sum_blocks) {
         // every `stride`th piece, and always the same columns
-        const uint32_t pieces = *a.count, stride = (uint32_t)a.sum_blocks / a.col_blocks;
+        const uint32_t pieces = a.counts[0], stride = (uint32_t)a.sum_blocks / a.col_blocks;
         const int64_t c =
             ((int64_t)(blockIdx.x % (uint32_t)a.col_blocks) * kSumThreads + threadIdx.x) * G;
         const bool whole = c + G <= a.K;
@@ -589,7 +500,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedGradA
     }
 }
 
-// A run that crosses chunks: the block of the chunk where it begins adds its
+// A run that crosses chunks: a block for each 32 groups of its columns adds its
 // partial sums, each warp a quarter of the chunks in order, and then the quarters.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGradArgs a) {
@@ -598,64 +509,65 @@ __global__ void __launch_bounds__(kSumThreads) embed_cross_kernel(const EmbedGra
     __shared__ float4 quarter[kSumWarps - 1][G / 4][32];
     gemm_ptx::pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const uint32_t chunk = blockIdx.x / (uint32_t)a.col_warps;
-    const int64_t c = ((int64_t)(blockIdx.x - chunk * (uint32_t)a.col_warps) * 32 + lane) * G;
-    const int64_t p0 = (int64_t)chunk * a.chunk, p1 = p0 + a.chunk;
-    if (p1 >= a.M) return;
-    const uint32_t token = token_of(a.sorted[p1 - 1]);
-    if (token == kNone || token_of(a.sorted[p1]) != token) return;   // no run goes on
-    if (p0 > 0 && token_of(a.sorted[p0 - 1]) == token &&
-        token_of(a.sorted[p0]) == token) return;                     // it began earlier
-    const int64_t end = first_at(a.sorted, a.M, (uint64_t)token + 1);
-    const bool in = c < a.K;  // the other lanes only take part in the stores
-    // chunk's own sum is its second one; those of the chunks after it their first
-    const int64_t more = (end - 1) / a.chunk - chunk;
-    const int64_t k0 = chunk + 1 + more * w / kSumWarps, k1 = chunk + 1 + more * (w + 1) / kSumWarps;
-    float sum[G] = {};
-    auto add = [&](const float4 (&v)[G / 4]) {
+    const uint32_t runs = a.counts[1], stride = gridDim.x / (uint32_t)a.col_warps;
+    const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.col_warps) * 32 + lane) * G;
+    for (uint32_t at = blockIdx.x / (uint32_t)a.col_warps; at < runs; at += stride) {
+        const int64_t chunk = a.crossing[at];
+        const uint32_t token = token_of(a.sorted[(chunk + 1) * a.chunk]);
+        const int64_t end = first_at(a.sorted, a.M, (uint64_t)token + 1);
+        const bool in = c < a.K;  // the other lanes only take part in the stores
+        // chunk's own sum is its second one; those of the chunks after it their first
+        const int64_t more = (end - 1) / a.chunk - chunk;
+        const int64_t k0 = chunk + 1 + more * w / kSumWarps;
+        const int64_t k1 = chunk + 1 + more * (w + 1) / kSumWarps;
+        float sum[G] = {};
+        auto add = [&](const float4 (&v)[G / 4]) {
 #pragma unroll
-        for (int q = 0; q < G / 4; ++q) {
-            sum[4 * q] += v[q].x;
-            sum[4 * q + 1] += v[q].y;
-            sum[4 * q + 2] += v[q].z;
-            sum[4 * q + 3] += v[q].w;
+            for (int q = 0; q < G / 4; ++q) {
+                sum[4 * q] += v[q].x;
+                sum[4 * q + 1] += v[q].y;
+                sum[4 * q + 2] += v[q].z;
+                sum[4 * q + 3] += v[q].w;
+            }
+        };
+        auto load = [&](float4 (&v)[G / 4], int64_t slot) {
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q)
+                v[q] = in ? reinterpret_cast<const float4*>(a.part + slot * a.kp + c)[q]
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        if (w == 0) {
+            float4 v[G / 4];
+            load(v, chunk * 2 + 1);
+            add(v);
         }
-    };
-    auto load = [&](float4 (&v)[G / 4], int64_t slot) {
+        for (int64_t k = k0; k < k1; k += AHEAD) {
+            float4 v[AHEAD][G / 4];
 #pragma unroll
-        for (int q = 0; q < G / 4; ++q)
-            v[q] = in ? reinterpret_cast<const float4*>(a.part + slot * a.kp + c)[q]
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    if (w == 0) {
-        float4 v[G / 4];
-        load(v, (int64_t)chunk * 2 + 1);
-        add(v);
+            for (int j = 0; j < AHEAD; ++j)
+                if (k + j < k1) load(v[j], (k + j) * 2);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                if (k + j < k1) add(v[j]);
+        }
+        if (w > 0) {
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q)
+                quarter[w - 1][q][lane] =
+                    make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
+        }
+        __syncthreads();
+        if (w == 0) {
+            for (int o = 0; o < kSumWarps - 1; ++o) {
+                float4 v[G / 4];
+#pragma unroll
+                for (int q = 0; q < G / 4; ++q) v[q] = quarter[o][q][lane];
+                add(v);
+            }
+            write_sum<O, G>(a, token, c, sum);
+        }
+        __syncthreads();  // the next run's quarters go to the same place
     }
-    for (int64_t k = k0; k < k1; k += AHEAD) {
-        float4 v[AHEAD][G / 4];
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j)
-            if (k + j < k1) load(v[j], (k + j) * 2);
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j)
-            if (k + j < k1) add(v[j]);
-    }
-    if (w > 0) {
-#pragma unroll
-        for (int q = 0; q < G / 4; ++q)
-            quarter[w - 1][q][lane] =
-                make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
-    }
-    __syncthreads();
-    if (w > 0) return;
-    for (int o = 0; o < kSumWarps - 1; ++o) {
-        float4 v[G / 4];
-#pragma unroll
-        for (int q = 0; q < G / 4; ++q) v[q] = quarter[o][q][lane];
-        add(v);
-    }
-    write_sum<O, G>(a, token, c, sum);
 }
 
 bool rows_ok(const void* p, int64_t rows, int64_t K, int64_t ld, int es) {
@@ -741,7 +653,9 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
     // eight on an SM, where there may be as many pieces; as many for each of the columns
     const int64_t stride = (dev->sm_count * 8 + a.col_blocks - 1) / a.col_blocks;
     a.sum_blocks = (M < stride ? M : stride) * a.col_blocks;
-    const int64_t cross_blocks = (int64_t)a.chunks * a.col_warps;
+    // of chunks, one run at most goes on from each
+    const int64_t cross = (dev->sm_count * 8 + a.col_warps - 1) / a.col_warps;
+    const int64_t cross_blocks = (a.chunks < cross ? a.chunks : cross) * a.col_warps;
     const int64_t fill = beta == 1.f ? 0 : (V + kFillRows - 1) / kFillRows;
     if (a.sum_blocks + fill > INT32_MAX || cross_blocks > INT32_MAX) return kUnsupported;
     Scratch scratch{pool, s, dev->device};
@@ -749,13 +663,13 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
     char* mem = nullptr;
     if (M > 0) {
         const int64_t part = up((int64_t)a.chunks * 2 * a.kp * 4, 256);
-        mem = static_cast<char*>(scratch.get((size_t)(4 * list + part + 4)));
+        mem = static_cast<char*>(scratch.get((size_t)(4 * list + part + 8 + (int64_t)a.chunks * 4)));
         if (!mem) return kCuda;
         uint64_t* in = reinterpret_cast<uint64_t*>(mem);
         uint64_t* out = reinterpret_cast<uint64_t*>(mem + list);
-        uint32_t* count = reinterpret_cast<uint32_t*>(mem + 4 * list + part);
+        uint32_t* counts = reinterpret_cast<uint32_t*>(mem + 4 * list + part);
         rc = launch_dependent(sort_tiles_kernel, dim3((unsigned)((M + kTile - 1) / kTile)),
-                              dim3(kTile / 2), 0, s, ids, M, V, in, count, dev->err_word);
+                              dim3(kTile / 2), 0, s, ids, M, V, in, counts, dev->err_word);
         for (int64_t run = kTile; rc == kOk && run < M; run *= kMerge) {
             const int smem = kMerge * (run <= kSamples ? (int)run : kFew) * 8;
             rc = allow_smem(sort_merge_kernel, kMerge * kSamples * 8, *dev);
@@ -770,9 +684,11 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
         RunPiece* pieces = reinterpret_cast<RunPiece*>(mem + 2 * list);
         if (rc == kOk)
             rc = launch_dependent(embed_pieces_kernel, dim3((unsigned)((M + 255) / 256)),
-                                  dim3(256), 0, s, a.sorted, M, a.chunk, pieces, count);
+                                  dim3(256), 0, s, a.sorted, M, a.chunk, pieces, counts + 2,
+                                  counts);
         a.pieces = pieces;
-        a.count = count;
+        a.crossing = counts + 2;
+        a.counts = counts;
         a.part = reinterpret_cast<float*>(mem + 4 * list);
     }
     const bool aligned = rows_aligned(dy, lddy, ts);

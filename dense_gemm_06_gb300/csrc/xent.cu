@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out = scale * (the sum of `parts` matrices, part_rows rows apart) + beta * out,
-// rounded once; rows x cols, four columns a thread, blocks of 1024 columns by rows.
+// rounded once; rows x cols. A warp takes 32 groups of 16 bytes of two rows at a
+// time, and stores them in 16-byte pieces whatever out's alignment.
 template <typename T>
 __global__ void __launch_bounds__(256)
     xent_finish_kernel(const float* __restrict__ sum, int64_t lds, int parts, int64_t part_rows,
@@ -178,53 +179,31 @@ __global__ void __launch_bounds__(256)
                        const float* __restrict__ scale, float beta) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
-    constexpr int AHEAD = 4;  // rows in flight
+    constexpr int ROWS = 2, G = 16 / (int)sizeof(T);
     const float by = scale ? *scale : 1.f;
-    const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
-    if (c >= cols) return;
-    const bool whole =
-        c + 4 <= cols && ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
-    for (int64_t r0 = blockIdx.x; r0 < rows; r0 += (int64_t)AHEAD * gridDim.x) {
-        float4 v[AHEAD];
+    const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * G;
+    const int64_t warps = (int64_t)gridDim.x * 8;
+    for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS; r0 < rows;
+         r0 += warps * ROWS) {
+        float v[ROWS][G] = {};
+        const float* from = sum + r0 * lds + c;
+        for (int p = 0; p < parts; ++p, from += part_rows * lds)
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            const int64_t r = r0 + j * (int64_t)gridDim.x;
-            if (r < rows) v[j] = *reinterpret_cast<const float4*>(sum + r * lds + c);  // lds % 4 == 0
-        }
-        for (int p = 1; p < parts; ++p) {
-            float4 more[AHEAD];
+            for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int64_t r = r0 + j * (int64_t)gridDim.x;
-                if (r < rows)
-                    more[j] = *reinterpret_cast<const float4*>(sum + (p * part_rows + r) * lds + c);
-            }
+                for (int q = 0; q < G; q += 4) {
+                    if (r0 + j >= rows || c + q >= lds) continue;  // lds % 4 == 0
+                    const float4 f = *reinterpret_cast<const float4*>(from + j * lds + q);
+                    v[j][q] += f.x, v[j][q + 1] += f.y, v[j][q + 2] += f.z, v[j][q + 3] += f.w;
+                }
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j)
-                v[j].x += more[j].x, v[j].y += more[j].y, v[j].z += more[j].z, v[j].w += more[j].w;
-        }
+        for (int j = 0; j < ROWS; ++j) {
+            if (r0 + j >= rows) continue;
+            T* row = out + (r0 + j) * ldo;
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            const int64_t r = r0 + j * (int64_t)gridDim.x;
-            if (r >= rows) continue;
-            T* dst = out + r * ldo + c;
-            const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-            alignas(16) T o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < cols)
-                    o[e] = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(dst[e]), by * f[e])
-                                                   : by * f[e]);
-            if (whole) {
-                if constexpr (sizeof(T) == 4)
-                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
-                else
-                    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < cols) dst[e] = o[e];
-            }
+            for (int e = 0; e < G; ++e) v[j][e] *= by;
+            if (beta != 0.f) add_row<T, G>(row, cols, c, beta, v[j]);
+            store_row<T, G>(row, cols, c, v[j]);
         }
     }
 }
@@ -232,8 +211,9 @@ __global__ void __launch_bounds__(256)
 int finish(const float* sum, int64_t lds, int parts, int64_t part_rows, void* out, int64_t ldo,
            int64_t rows, int64_t cols, const float* scale, float beta, int esize, bool bf16,
            const DeviceInfo& dev, cudaStream_t s) {
-    const int64_t wide = (cols + 1023) / 1024, most = (dev.sm_count * 16 + wide - 1) / wide;
-    const dim3 grid((unsigned)(rows < most ? rows : most), (unsigned)wide);
+    const int64_t across = (cols * esize + 511) / 512;  // warps for a row
+    const int64_t turns = (rows + 15) / 16, most = (dev.sm_count * 8 + across - 1) / across;
+    const dim3 grid((unsigned)(turns < most ? turns : most), (unsigned)across);
     auto run = [&](auto t) {
         using T = decltype(t);
         return launch_dependent(xent_finish_kernel<T>, grid, dim3(256), 0, s, sum, lds, parts,
