@@ -383,9 +383,12 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
     return rc;
 }
 
+// scratch_args: arguments that are the library's own scratch, for which the device
+// check does not hold (memory that a stream capture allocates has no attributes yet);
+// the caller has checked the others.
 int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, const void* A,
               int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc, int64_t stridec,
-              int dtype, const gemm_epilogue* epi, cudaStream_t s) {
+              int dtype, const gemm_epilogue* epi, cudaStream_t s, bool scratch_args = false) {
     if (dtype == GEMM_F32) return kUnsupported;
     if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
     if (!sizes_ok(G, M, N, K)) return kInvalidArg;
@@ -410,7 +413,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     if (rc != kOk) return rc;
     const void* ptrs[5] = {K > 0 ? A : nullptr, K > 0 ? B : nullptr, C, offsets,
                            epi ? epi->bias : nullptr};
-    rc = check_device_pointers(ptrs, 5, dev->device);
+    if (!scratch_args) rc = check_device_pointers(ptrs, 5, dev->device);
     if (rc != kOk) return rc;
 
     const EpiParams ep = epi_params(epi);
@@ -644,6 +647,14 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
 }
 
 }  // namespace
+
+int launch_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
+                     const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc,
+                     int64_t stridec, int dtype, float beta, cudaStream_t s) {
+    const gemm_epilogue epi{1.f, beta, nullptr, GEMM_ACT_NONE};
+    return grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype, &epi, s, true);
+}
+
 }  // namespace libgemm
 
 using namespace libgemm;

@@ -429,9 +429,8 @@ int product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, int a_m
 int product_folded(int64_t M, int64_t N, int64_t depth, const void* A, int64_t lda, const void* B,
                    int64_t ldb, float* C, int64_t ldc, int dtype, float beta,
                    const int32_t* limits, cudaStream_t s) {
-    const gemm_epilogue epi{1.f, beta, nullptr, GEMM_ACT_NONE};
-    return gemm_grouped_k(1, M, N, depth, limits, A, lda, B, ldb, C, ldc, M * ldc, dtype,
-                          beta != 0.f ? &epi : nullptr, s);
+    return launch_grouped_k(1, M, N, depth, limits, A, lda, B, ldb, C, ldc, M * ldc, dtype, beta,
+                            s);
 }
 
 int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,

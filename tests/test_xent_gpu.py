@@ -332,6 +332,35 @@ def test_against_differences():
         assert abs(diff - slope) <= lim, (which, diff, slope, lim)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [128, 121])
+def test_every_path_can_be_captured(dtype, K):
+    """Few tiles and many, aligned rows and not, one number of G and two."""
+    for M, N in ((130, 3000), (1100, 9984)):
+        X, W, target, dloss = inputs(M, N, K, dtype)
+        loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        dX = torch.empty(M, K, dtype=IN[dtype], device="cuda")
+        dW = torch.zeros(N, K, dtype=OUT[dtype], device="cuda")
+
+        def step():
+            lg.check(lg.gemm_xent(M, N, K, X, K, W, K, target, loss, lse, dtype))
+            lg.check(lg.gemm_xent_grad(M, N, K, X, K, W, K, target, lse, dloss, dX, K, dW, K,
+                                       dtype, beta=1.0))
+        step()
+        want = [t.clone() for t in (loss, lse, dX, dW)]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for t in (loss, lse, dX, dW):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((loss, lse, dX, dW), want))
+        del graph
+    check()
+
+
 def test_repeats_on_other_streams_and_in_graphs():
     """The same bits on any stream, beside another call, and from a graph that follows
     new inputs; two graphs and an eager call keep their own workspaces."""
