@@ -388,7 +388,8 @@ int grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, 
 // the caller has checked the others.
 int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets, const void* A,
               int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc, int64_t stridec,
-              int dtype, const gemm_epilogue* epi, cudaStream_t s, bool scratch_args = false) {
+              int dtype, const gemm_epilogue* epi, cudaStream_t s, bool scratch_args = false,
+              const float* scale = nullptr) {
     if (dtype == GEMM_F32) return kUnsupported;
     if (dtype < GEMM_F32 || dtype > GEMM_BF16_BF16) return kInvalidArg;
     if (!sizes_ok(G, M, N, K)) return kInvalidArg;
@@ -416,7 +417,8 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     if (!scratch_args) rc = check_device_pointers(ptrs, 5, dev->device);
     if (rc != kOk) return rc;
 
-    const EpiParams ep = epi_params(epi);
+    EpiParams ep = epi_params(epi);
+    if (scale) ep.active = 1;  // a factor in device memory, on alpha
     const RaggedShape shape =
         plan_grouped_k(G, M, N, dev->sm_count, ragged_out(ep, dtype), K / G);
     const bool bf16 = is_bf16(dtype);
@@ -436,6 +438,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rp.ldc = ldc;
     rp.stridec = stridec;
     rp.epi = ep;
+    rp.scale = scale;
     map_c(rp, dtype, C, G, stridec, M, N, ldc);
     const int64_t units = G * rp.tiles_f * rp.tiles_r;
     if ((int64_t)rp.tiles_f * rp.tiles_r > INT32_MAX / G ||
@@ -650,9 +653,10 @@ int lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* A, i
 
 int launch_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                      const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc,
-                     int64_t stridec, int dtype, float beta, cudaStream_t s) {
+                     int64_t stridec, int dtype, float beta, const float* scale, cudaStream_t s) {
     const gemm_epilogue epi{1.f, beta, nullptr, GEMM_ACT_NONE};
-    return grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype, &epi, s, true);
+    return grouped_k(G, M, N, K, offsets, A, lda, B, ldb, C, ldc, stridec, dtype, &epi, s, true,
+                     scale);
 }
 
 }  // namespace libgemm

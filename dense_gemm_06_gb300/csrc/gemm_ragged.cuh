@@ -67,7 +67,8 @@ struct RaggedParams {
     EpiParams epi;
     // gemm_lora
     const int32_t* adapter;  // adapter number of each row
-    const float* scale;      // one factor per adapter, or null
+    const float* scale;      // one factor per adapter, or null (depth: null, or one factor
+                             // on alpha: gemm_xent_grad's scaling back of fp16 sums)
     const void* x;           // kRagShrinkRows: X and LA, row pitches ldx and ldla
     const void* lora_a;
     int64_t ldx, ldla;
@@ -1267,6 +1268,10 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             if (epi && p.epi.bias && f_ok)
                 bias = to_f32(static_cast<const OutT*>(p.epi.bias)[(int64_t)un.g * p.feats + f]);
             const bool accumulates = epi && adds(p.epi);
+            // read where it is used: the folded sums leave it no register
+            auto alpha = [&]() {
+                return MODE == kRagDepth && p.scale ? p.epi.alpha * *p.scale : p.epi.alpha;
+            };
             OutT* c_col = nullptr;
             if constexpr (MODE != kRagShrink)
                 c_col = static_cast<OutT*>(p.C) + (int64_t)un.row0 * p.ldc + f +
@@ -1350,10 +1355,11 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                         // element gets one addition, so its order is no question).
                         // That addition takes numbers below 2^-126 as zero.
                         if (!f_ok) return;
+                        const float by = alpha();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             if (i < left && c_checked(p, row + i, f))
-                                red_add_f32(dst, p.epi.alpha * v[i]);
+                                red_add_f32(dst, by * v[i]);
                             dst += p.ldc;
                         }
                         return;
@@ -1362,6 +1368,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 if (epi && f_ok) {
                     // the incoming C of OLD rows at a time: one latency for all of them
                     constexpr int OLD = FOLD ? 8 : 32;
+                    const float by = alpha();
 #pragma unroll
                     for (int r = 0; r < 32; r += OLD) {
                         float old[OLD];
@@ -1371,7 +1378,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                                          ? to_f32(dst[(int64_t)(r + i) * p.ldc]) : 0.f;
 #pragma unroll
                         for (int i = 0; i < OLD; ++i) {
-                            v[r + i] *= p.epi.alpha;
+                            v[r + i] *= by;
                             if (p.epi.beta != 0.f) v[r + i] = fmaf(p.epi.beta, old[i], v[r + i]);
                             v[r + i] += bias;
                         }

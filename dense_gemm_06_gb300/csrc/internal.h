@@ -204,10 +204,11 @@ TcLaunch resolve_tc_options(int64_t M, int64_t N, int64_t K, const void* A, int6
                             int64_t ldc, int c_major, int dtype);
 
 // gemm_grouped_k() on buffers that may be the library's own scratch: the caller has
-// checked the arguments that are not.
+// checked the arguments that are not. scale: null, or a factor of the products in
+// device memory.
 int launch_grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                      const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc,
-                     int64_t stridec, int dtype, float beta, cudaStream_t s);
+                     int64_t stridec, int dtype, float beta, const float* scale, cudaStream_t s);
 
 // Row softmax over thread-block clusters (softmax_cluster.cu); rows longer
 // than softmax_max_cols() are not supported.

@@ -410,6 +410,7 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
 // W, so its tiles divide the columns evenly over whole rounds of the SMs (32000
 // columns on 152 SMs: 2 rounds of 112).
 constexpr int64_t kXentMaxVocab = 1 << 24;
+constexpr int64_t kXentMaxDepth = 1 << 20;  // K of gemm_xent_grad
 struct XentShape {
     int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
     int tile_n;

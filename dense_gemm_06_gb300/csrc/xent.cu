@@ -23,8 +23,8 @@
 // with both in one product of twice the depth, on gemm_grouped_k's kernel, which
 // adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384). fp16 has the exponents
 // for that only near 1: G is scaled by a power of two that brings the largest
-// |alpha dloss| to 2^12, its small probabilities then reach down to 2^-36 of it,
-// and the products go through fp32 scratch from which they are scaled back.
+// |alpha dloss| to 2^12, its small probabilities then reach down to 2^-36 of it, and
+// the products are scaled back in fp32 before they are rounded.
 //
 // Rows whose target does not count are zero in G, and zero in the copy of X that
 // dW is multiplied from (0 times an infinity would be NaN).
@@ -169,17 +169,17 @@ __global__ void __launch_bounds__(1024)
     scale[1] = ldexpf(1.f, -e);
 }
 
-// out = scale * (the sum of `parts` matrices, part_rows rows apart) + beta * out,
-// rounded once; rows x cols. A warp takes 32 groups of 16 bytes of two rows at a
-// time, and stores them in 16-byte pieces whatever out's alignment.
+// dX = scale * (the sum of `parts` matrices, part_rows rows apart), rounded once;
+// rows x cols. A warp takes 32 groups of 8 columns of two rows at a time, and stores
+// them in 16-byte pieces whatever dX's alignment.
 template <typename T>
 __global__ void __launch_bounds__(256)
     xent_finish_kernel(const float* __restrict__ sum, int64_t lds, int parts, int64_t part_rows,
                        T* __restrict__ out, int64_t ldo, int64_t rows, int cols,
-                       const float* __restrict__ scale, float beta) {
+                       const float* __restrict__ scale) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
-    constexpr int ROWS = 2, G = 16 / (int)sizeof(T);
+    constexpr int ROWS = 2, G = 8;
     const float by = scale ? *scale : 1.f;
     const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * G;
     const int64_t warps = (int64_t)gridDim.x * 8;
@@ -199,27 +199,24 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             if (r0 + j >= rows) continue;
-            T* row = out + (r0 + j) * ldo;
 #pragma unroll
             for (int e = 0; e < G; ++e) v[j][e] *= by;
-            if (beta != 0.f) add_row<T, G>(row, cols, c, beta, v[j]);
-            store_row<T, G>(row, cols, c, v[j]);
+            store_row<T, G>(out + (r0 + j) * ldo, cols, c, v[j]);
         }
     }
 }
 
 int finish(const float* sum, int64_t lds, int parts, int64_t part_rows, void* out, int64_t ldo,
-           int64_t rows, int64_t cols, const float* scale, float beta, int esize, bool bf16,
-           const DeviceInfo& dev, cudaStream_t s) {
-    const int64_t across = (cols * esize + 511) / 512;  // warps for a row
+           int64_t rows, int64_t cols, const float* scale, bool bf16, const DeviceInfo& dev,
+           cudaStream_t s) {
+    const int64_t across = (cols + 255) / 256;  // warps for a row
     const int64_t turns = (rows + 15) / 16, most = (dev.sm_count * 8 + across - 1) / across;
     const dim3 grid((unsigned)(turns < most ? turns : most), (unsigned)across);
     auto run = [&](auto t) {
         using T = decltype(t);
         return launch_dependent(xent_finish_kernel<T>, grid, dim3(256), 0, s, sum, lds, parts,
-                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, scale, beta);
+                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, scale);
     };
-    if (esize == 4) return run(float{});
     return bf16 ? run(__nv_bfloat16{}) : run(__half{});
 }
 
@@ -423,14 +420,14 @@ int product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, int a_m
                           s);
 }
 
-// The same for fp32 results of a depth that the tensor core's cut-off additions
-// would show in: sum over t of A[t][m] B[t][n] on the product that folds its sums.
-// limits: {0, depth} in device memory.
-int product_folded(int64_t M, int64_t N, int64_t depth, const void* A, int64_t lda, const void* B,
-                   int64_t ldb, float* C, int64_t ldc, int dtype, float beta,
-                   const int32_t* limits, cudaStream_t s) {
+// dW = beta dW + scale G^T X on the product over the rows of one group, {0, depth}
+// in `limits`: it adds up fp32 sums in parts of the depth (the tensor core's cut-off
+// additions would show in an fp32 dW), and takes the factor from device memory.
+int product_rows(int64_t M, int64_t N, int64_t depth, const void* A, int64_t lda, const void* B,
+                 int64_t ldb, void* C, int64_t ldc, int dtype, float beta, const float* scale,
+                 const int32_t* limits, cudaStream_t s) {
     return launch_grouped_k(1, M, N, depth, limits, A, lda, B, ldb, C, ldc, M * ldc, dtype, beta,
-                            s);
+                            scale, s);
 }
 
 int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
@@ -439,6 +436,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
              cudaStream_t s) {
     int rc = check_inputs(M, N, K, X, ldx, W, ldw, target, dtype);
     if (rc != kOk) return rc;
+    if (K > kXentMaxDepth) return kUnsupported;
     const int we = dtype <= GEMM_BF16_F32 ? 4 : 2;
     if (!aligned_to(dX, 2) || !aligned_to(dW, we)) return kInvalidArg;
     if (K > 0 && ((dX && M > 0 && lddx < K) || (dW && lddw < K))) return kInvalidArg;
@@ -481,7 +479,6 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const int64_t x_at = copy_x ? at.add(ldk * rows * parts * 2) : -1;
     const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * ldk * 2);
     const int64_t dx_at = sum_dx ? at.add(plan.splits * M * up(K, 4) * 4) : -1;
-    const int64_t dw_at = dW && scaled ? at.add(piece * up(K, 4) * 4) : -1;
     const int64_t scale_at = scaled ? at.add(8) : -1;
     const int64_t limits_at = at.add(8);
     Scratch scratch{pool, s, dev->device};
@@ -489,7 +486,6 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     if (!mem) return kCuda;
     float* scale = scaled ? reinterpret_cast<float*>(mem + scale_at) : nullptr;
     float* dx_sum = sum_dx ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
-    float* dw_sum = dw_at >= 0 ? reinterpret_cast<float*>(mem + dw_at) : nullptr;
     int32_t* limits = reinterpret_cast<int32_t*>(mem + limits_at);
     char* g = mem + g_at;
 
@@ -540,23 +536,15 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
         if (rc != kOk || !dW) continue;
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
         const int64_t depth = (int64_t)rows * parts;
-        if (!scaled) {
-            rc = parts == 2 ? product_folded(n, K, depth, g, ldg, xc, ldxc,
-                                             static_cast<float*>(dst), lddw, f32, beta, limits, s)
-                            : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN,
-                                      dst, lddw, same, beta, *dev, s);
-        } else {
-            rc = parts == 2 ? product_folded(n, K, depth, g, ldg, xc, ldxc, dw_sum, up(K, 4), f32,
-                                             0.f, limits, s)
-                            : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN,
-                                      dw_sum, up(K, 4), f32, 0.f, *dev, s);
-            if (rc == kOk)
-                rc = finish(dw_sum, up(K, 4), 1, 0, dst, lddw, n, K, scale + 1, beta, we, bf16, *dev, s);
-        }
+        rc = parts == 2 || scaled
+                 ? product_rows(n, K, depth, g, ldg, xc, ldxc, dst, lddw, dtype, beta,
+                                scaled ? scale + 1 : nullptr, limits, s)
+                 : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dst, lddw,
+                           dtype, beta, *dev, s);
     }
     if (rc == kOk && sum_dx)
         rc = finish(dx_sum, up(K, 4), split_dx ? plan.used(piece) : 1, M, dX, lddx, M, K,
-                    scaled ? scale + 1 : nullptr, 0.f, 2, bf16, *dev, s);
+                    scaled ? scale + 1 : nullptr, bf16, *dev, s);
     scratch.release();
     return rc;
 }
