@@ -47,6 +47,70 @@ __device__ __forceinline__ void load_weights(const W* p, int64_t at, float other
     }
 }
 
+// Two fp32 numbers that one instruction works on (each rounded as by itself): the
+// kernels that walk down the rows are bound by instructions as much as by memory.
+struct Two {
+    unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 apart(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(Two a) {
+    const float2 f = apart(a);
+    return f.x + f.y;
+}
+
+// A vector's elements in pairs, and back.
+template <typename T, int VEC>
+__device__ __forceinline__ void to_pairs(const Pack<T, VEC>& p, Two (&out)[VEC / 2]) {
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
+            out[j] = two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+            out[j] = two(to_f32(p.v[2 * j]), to_f32(p.v[2 * j + 1]));
+        }
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> from_pairs(const Two (&in)[VEC / 2]) {
+    Pack<T, VEC> p;
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        const float2 f = apart(in[j]);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            reinterpret_cast<__nv_bfloat162*>(&p)[j] = __floats2bfloat162_rn(f.x, f.y);
+        else if constexpr (std::is_same<T, __half>::value)
+            reinterpret_cast<__half2*>(&p)[j] = __floats2half2_rn(f.x, f.y);
+        else
+            p.v[2 * j] = f.x, p.v[2 * j + 1] = f.y;
+    }
+    return p;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -130,7 +194,7 @@ __global__ void __launch_bounds__(BLOCK) norm_kernel(const NormArgs a) {
             }
         }
     row_sum<WARPS, 1>(s, slots[1]);
-    const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+    const float rstd = rsqrtf(s[0] / (float)a.N + a.eps);
     if (tid == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
@@ -178,13 +242,19 @@ __global__ void __launch_bounds__(32 * WARPS * LANES) norm_walk_kernel(const Nor
     __shared__ float slots[2][WARPS];
     const int tid = threadIdx.x % TR;
     gemm_ptx::pdl_wait();
-    float w[NV][VEC], b[NV][VEC];
+    constexpr int P = VEC / 2;  // pairs of a vector
+    Two w[NV][P], b[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TR + tid) * VEC;
         const bool in = c < a.N;
-        load_weights<W, VEC>(in ? static_cast<const W*>(a.weight) : nullptr, c, 1.f, w[i]);
-        load_weights<W, VEC>(in ? static_cast<const W*>(a.bias) : nullptr, c, 0.f, b[i]);
+        float f[VEC];
+        load_weights<W, VEC>(in ? static_cast<const W*>(a.weight) : nullptr, c, 1.f, f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) w[i][j] = two(f[2 * j], f[2 * j + 1]);
+        load_weights<W, VEC>(in ? static_cast<const W*>(a.bias) : nullptr, c, 0.f, f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) b[i][j] = two(f[2 * j], f[2 * j + 1]);
     }
     const int64_t step = (int64_t)gridDim.x * LANES;
     const int64_t row0 = (int64_t)blockIdx.x * LANES + threadIdx.x / TR;
@@ -203,50 +273,50 @@ __global__ void __launch_bounds__(32 * WARPS * LANES) norm_walk_kernel(const Nor
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int k = 0; k < STAGES - 1; ++k) fetch(row0 + k * step, k);
+    const float inv = 1.f / (float)a.N;
     int stage = 0;
     for (int64_t row = row0; row < a.M; row += step) {
-        float v[NV][VEC], s[1] = {0.f};
+        Two v[NV][P], t = two(0.f, 0.f);
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 2) : "memory");
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if ((i * TR + tid) * VEC >= a.N) continue;
-            const V got = *slot(stage, i);
+            to_pairs<T, VEC>(*slot(stage, i), v[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] = to_f32(got.v[e]);
-                s[0] += v[i][e];
-            }
+            for (int j = 0; j < P; ++j) t = add2(t, v[i][j]);
         }
         fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
         if (++stage == STAGES) stage = 0;
+        float s[1] = {sum2(t)};
         row_sum<WARPS, 1>(s, slots[0]);
         const float mean = s[0] / (float)a.N;
-        s[0] = 0.f;
+        const Two off = two(-mean, -mean);
+        t = two(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if ((i * TR + tid) * VEC >= a.N) continue;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] -= mean;
-                s[0] = fmaf(v[i][e], v[i][e], s[0]);
+            for (int j = 0; j < P; ++j) {
+                v[i][j] = add2(v[i][j], off);
+                t = fma2(v[i][j], v[i][j], t);
             }
         }
+        s[0] = sum2(t);
         row_sum<WARPS, 1>(s, slots[1]);
-        const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+        const float rstd = rsqrtf(s[0] * inv + a.eps);
         if (tid == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
+        const Two by = two(rstd, rstd);
         T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TR + tid) * VEC;
             if (c >= a.N) continue;
-            V o;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                o.v[e] = from_f32<T>(fmaf(v[i][e] * rstd, w[i][e], b[i][e]));
-            *reinterpret_cast<V*>(y + c) = o;
+            for (int j = 0; j < P; ++j) v[i][j] = fma2(mul2(v[i][j], by), w[i][j], b[i][j]);
+            *reinterpret_cast<V*>(y + c) = from_pairs<T, VEC>(v[i]);
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -274,7 +344,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
             s[0] = fmaf(d, d, s[0]);
         }
         row_sum<32, 1>(s, slots[1]);
-        const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+        const float rstd = rsqrtf(s[0] / (float)a.N + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -329,13 +399,13 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
     gemm_ptx::pdl_wait();
     float w[kOwn];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TR + tid) * VEC;
+        float f[VEC];
+        load_weights<W, VEC>(c < a.N ? static_cast<const W*>(a.weight) : nullptr, c, 1.f, f);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int c = (i * TR + tid) * VEC + e;
-            w[i * VEC + e] =
-                c < a.N && a.weight ? to_f32(static_cast<const W*>(a.weight)[c]) : 1.f;
-        }
+        for (int e = 0; e < VEC; ++e) w[i * VEC + e] = f[e];
+    }
     float dw[kOwn] = {}, db[kOwn] = {};
     const float inv = 1.f / (float)a.N;
     const int64_t step = (int64_t)gridDim.x * LANES;
@@ -430,32 +500,45 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
     }
     if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.part) return;
-    float* part = a.part + (int64_t)blockIdx.x * 2 * a.N;
+    if constexpr (LANES > 1) {  // the block's rows, in the order of its warps
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int c = (i * TR + tid) * VEC + e;
-            float u = dw[i * VEC + e], v = db[i * VEC + e];
-            if constexpr (LANES > 1) {  // the block's rows, in the order of its warps
-                __syncthreads();
-                if (sub > 0) {
-                    merge[((sub - 1) * TR + tid) * 2] = u;
-                    merge[((sub - 1) * TR + tid) * 2 + 1] = v;
-                }
-                __syncthreads();
-                if (sub > 0) continue;
-#pragma unroll 1
-                for (int o = 0; o < LANES - 1; ++o) {
-                    u += merge[(o * TR + tid) * 2];
-                    v += merge[(o * TR + tid) * 2 + 1];
-                }
+        for (int k = 0; k < kOwn; ++k) {
+            __syncthreads();
+            if (sub > 0) {
+                merge[((sub - 1) * TR + tid) * 2] = dw[k];
+                merge[((sub - 1) * TR + tid) * 2 + 1] = db[k];
             }
-            if (c < a.N) {
-                part[c] = u;
-                part[a.N + c] = v;
+            __syncthreads();
+            if (sub > 0) continue;
+#pragma unroll 1
+            for (int o = 0; o < LANES - 1; ++o) {
+                dw[k] += merge[(o * TR + tid) * 2];
+                db[k] += merge[(o * TR + tid) * 2 + 1];
             }
         }
+        if (sub > 0) return;
+    }
+    // whole vectors at once: single stores of 608 blocks' sums of 2048 columns took a
+    // third of the kernel
+    constexpr int PER = VEC == 1 ? 1 : 4;
+    struct alignas(4 * PER) Out { float v[PER]; };
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TR + tid) * VEC;
+        if (c >= a.N) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; e += PER) {
+            Out u, v;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                u.v[k] = dw[i * VEC + e + k];
+                v.v[k] = db[i * VEC + e + k];
+            }
+            *reinterpret_cast<Out*>(part + c + e) = u;
+            *reinterpret_cast<Out*>(part + a.N + c + e) = v;
+        }
+    }
 }
 
 // Long rows, first pass: dx of a row per block; x and dy are read twice.
@@ -617,12 +700,12 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t M, int64_t N, int sm_count) {
     GradPlan g{16, 1, 0};
+    if (N > 32 * 16 * kOwn) return g;
     for (int w : {1, 2, 4, 8, 16})
         if (N <= 32 * w * kOwn) {
             g.warps = w;
             break;
         }
-    if (N > 32 * 16 * kOwn) return g;
     g.lanes = g.warps == 1 ? 4 : 1;
     const int64_t rows = (M + g.lanes - 1) / g.lanes;
     const int64_t most = (int64_t)sm_count * (kGradWarps / (g.warps * g.lanes));
@@ -655,7 +738,8 @@ int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const Device
         if (!a.part) return kCuda;
     }
     const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.dy, a.lddy, sizeof(T)) &&
-                     (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) && a.N % (16 / sizeof(T)) == 0;
+                     (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) &&
+                     a.N % (16 / sizeof(T)) == 0 && aligned_to(a.weight, 16);
     if (a.M > 0 && g.blocks > 0) {
 #define NORM_GRAD_RUN(WARPS, LANES)                                                        \
     rc = vec ? run_norm_grad<T, W, WARPS, LANES, 16 / (int)sizeof(T)>(a, g.blocks, dev, s) \
