@@ -232,74 +232,104 @@ constexpr int kOwn = 16;  // columns of a thread in the kernels that walk down t
 // memory, so that the copies need no barrier. (A row a warp, the weights read from
 // L1 for each: 8192 rows of 2048, bf16 with fp32 weights, 19 us.)
 constexpr int kWalkStages = 4;
-template <typename T, typename W, int WARPS, int LANES>
+template <typename T, typename W, int WARPS, int LANES, int VEC>
 __global__ void __launch_bounds__(32 * WARPS * LANES) norm_walk_kernel(const NormArgs a) {
     gemm_ptx::pdl_launch_dependents();
-    constexpr int VEC = 16 / (int)sizeof(T), TR = 32 * WARPS, NV = kOwn / VEC;
+    constexpr int TR = 32 * WARPS, NV = kOwn / VEC, P = kOwn / 2;
     constexpr int THREADS = TR * LANES, STAGES = kWalkStages;
+    constexpr bool RING = VEC > 1;  // single elements: the next row in registers
     using V = Pack<T, VEC>;
     extern __shared__ __align__(16) uint8_t ring[];  // STAGES x NV x THREADS vectors
     __shared__ float slots[2][WARPS];
     const int tid = threadIdx.x % TR;
+    // the column of a thread's number k
+    auto column = [&](int k) { return (k / VEC * TR + tid) * VEC + k % VEC; };
     gemm_ptx::pdl_wait();
-    constexpr int P = VEC / 2;  // pairs of a vector
-    Two w[NV][P], b[NV][P];
+    Two w[P], b[P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TR + tid) * VEC;
+        const int c = column(i * VEC);
         const bool in = c < a.N;
-        float f[VEC];
+        float f[VEC], g[VEC];
         load_weights<W, VEC>(in ? static_cast<const W*>(a.weight) : nullptr, c, 1.f, f);
+        load_weights<W, VEC>(in ? static_cast<const W*>(a.bias) : nullptr, c, 0.f, g);
+        if constexpr (VEC > 1) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) w[i][j] = two(f[2 * j], f[2 * j + 1]);
-        load_weights<W, VEC>(in ? static_cast<const W*>(a.bias) : nullptr, c, 0.f, f);
-#pragma unroll
-        for (int j = 0; j < P; ++j) b[i][j] = two(f[2 * j], f[2 * j + 1]);
+            for (int j = 0; j < VEC / 2; ++j) {
+                w[i * VEC / 2 + j] = two(f[2 * j], f[2 * j + 1]);
+                b[i * VEC / 2 + j] = two(g[2 * j], g[2 * j + 1]);
+            }
+        } else if (i % 2 == 0) {
+            w[i / 2] = two(f[0], 0.f);
+            b[i / 2] = two(g[0], 0.f);
+        } else {
+            w[i / 2] = two(apart(w[i / 2]).x, f[0]);
+            b[i / 2] = two(apart(b[i / 2]).x, g[0]);
+        }
     }
     const int64_t step = (int64_t)gridDim.x * LANES;
     const int64_t row0 = (int64_t)blockIdx.x * LANES + threadIdx.x / TR;
     auto slot = [&](int stage, int i) {
         return reinterpret_cast<V*>(ring) + (stage * NV + i) * THREADS + threadIdx.x;
     };
+    V x[NV];
     auto fetch = [&](int64_t row, int stage) {
         if (row < a.M) {
-            const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+            const T* from = static_cast<const T*>(a.x) + row * a.ldx;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * TR + tid) * VEC;
-                if (c < a.N) copy_async(slot(stage, i), x + c);
+                const int c = column(i * VEC);
+                if (c >= a.N) continue;
+                if constexpr (RING) copy_async(slot(stage, i), from + c);
+                else x[i] = *reinterpret_cast<const V*>(from + c);
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (RING) asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int k = 0; k < STAGES - 1; ++k) fetch(row0 + k * step, k);
+    if constexpr (RING) {
+        for (int k = 0; k < STAGES - 1; ++k) fetch(row0 + k * step, k);
+    } else {
+        fetch(row0, 0);
+    }
     const float inv = 1.f / (float)a.N;
     int stage = 0;
     for (int64_t row = row0; row < a.M; row += step) {
-        Two v[NV][P], t = two(0.f, 0.f);
-        asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 2) : "memory");
+        Two v[P], t = two(0.f, 0.f);
+        if constexpr (RING) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 2) : "memory");
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if ((i * TR + tid) * VEC >= a.N) continue;
-            to_pairs<T, VEC>(*slot(stage, i), v[i]);
+            for (int i = 0; i < NV; ++i) {
+                if (column(i * VEC) >= a.N) continue;
+                Two part[VEC / 2 > 0 ? VEC / 2 : 1];
+                to_pairs<T, VEC>(*slot(stage, i), part);
 #pragma unroll
-            for (int j = 0; j < P; ++j) t = add2(t, v[i][j]);
+                for (int j = 0; j < VEC / 2; ++j) {
+                    v[i * VEC / 2 + j] = part[j];
+                    t = add2(t, part[j]);
+                }
+            }
+            fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+            if (++stage == STAGES) stage = 0;
+        } else {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                v[k] = two(column(2 * k) < a.N ? to_f32(x[2 * k].v[0]) : 0.f,
+                           column(2 * k + 1) < a.N ? to_f32(x[2 * k + 1].v[0]) : 0.f);
+                t = add2(t, v[k]);
+            }
+            fetch(row + step, 0);
         }
-        fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-        if (++stage == STAGES) stage = 0;
         float s[1] = {sum2(t)};
         row_sum<WARPS, 1>(s, slots[0]);
         const float mean = s[0] / (float)a.N;
         const Two off = two(-mean, -mean);
         t = two(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if ((i * TR + tid) * VEC >= a.N) continue;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                v[i][j] = add2(v[i][j], off);
-                t = fma2(v[i][j], v[i][j], t);
-            }
+        for (int k = 0; k < P; ++k) {
+            if (column(2 * k) >= a.N) continue;
+            v[k] = add2(v[k], off);
+            if (VEC == 1 && column(2 * k + 1) >= a.N) v[k] = two(apart(v[k]).x, 0.f);
+            t = fma2(v[k], v[k], t);
         }
         s[0] = sum2(t);
         row_sum<WARPS, 1>(s, slots[1]);
@@ -311,15 +341,23 @@ __global__ void __launch_bounds__(32 * WARPS * LANES) norm_walk_kernel(const Nor
         const Two by = two(rstd, rstd);
         T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TR + tid) * VEC;
-            if (c >= a.N) continue;
+        for (int k = 0; k < P; ++k) v[k] = fma2(mul2(v[k], by), w[k], b[k]);
 #pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = fma2(mul2(v[i][j], by), w[i][j], b[i][j]);
-            *reinterpret_cast<V*>(y + c) = from_pairs<T, VEC>(v[i]);
+        for (int i = 0; i < NV; ++i) {
+            const int c = column(i * VEC);
+            if (c >= a.N) continue;
+            if constexpr (VEC > 1) {
+                Two part[VEC / 2];
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) part[j] = v[i * VEC / 2 + j];
+                *reinterpret_cast<V*>(y + c) = from_pairs<T, VEC>(part);
+            } else {
+                const float2 f = apart(v[i / 2]);
+                y[c] = from_f32<T>(i % 2 ? f.y : f.x);
+            }
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Rows too long for the registers of a block: x is read three times (from L2
@@ -376,7 +414,8 @@ constexpr int kGradWarps = 16;  // on an SM
 
 // Rows on their way to a thread, the one that it works on included. With 16-bit
 // rows of 2048, 128 threads and four blocks on an SM that is 96 KB in flight.
-template <typename T> constexpr int kNormStages = sizeof(T) == 2 ? 4 : 3;
+template <typename T, int WARPS>
+constexpr int kNormStages = sizeof(T) == 2 ? (WARPS == 32 ? 3 : 4) : WARPS == 32 ? 1 : 3;
 
 // A block of WARPS x LANES warps: LANES rows side by side, each on WARPS warps
 // (LANES > 1 only with one warp a row). Thread tid of a row owns the columns
@@ -389,8 +428,8 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
     norm_grad_kernel(const NormGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int TR = 32 * WARPS, NV = kOwn / VEC, THREADS = TR * LANES;
-    constexpr int BYTES = VEC * (int)sizeof(T), STAGES = kNormStages<T>;
-    constexpr bool RING = BYTES == 16;
+    constexpr int BYTES = VEC * (int)sizeof(T), STAGES = kNormStages<T, WARPS>;
+    constexpr bool RING = BYTES == 16 && STAGES > 1;
     using V = Pack<T, VEC>;
     extern __shared__ __align__(16) uint8_t ring[];  // STAGES x (x, dy) x NV x THREADS vectors
     __shared__ float slots[2][2 * WARPS];
@@ -648,11 +687,14 @@ int norm_dispatch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
     };
     auto walk = [&](auto warps, auto lanes) {
         constexpr int WARPS = decltype(warps)::value, LANES = decltype(lanes)::value;
-        constexpr int THREADS = 32 * WARPS * LANES, SMEM = kWalkStages * kOwn * sizeof(T) * THREADS;
-        auto kern = norm_walk_kernel<T, W, WARPS, LANES>;
+        constexpr int THREADS = 32 * WARPS * LANES;
+        constexpr int SMEM = VEC > 1 ? kWalkStages * kOwn * (int)sizeof(T) * THREADS : 0;
+        auto kern = norm_walk_kernel<T, W, WARPS, LANES, VEC>;
         const int rc = allow_smem(kern, SMEM, dev);
         if (rc != kOk) return rc;
-        const int64_t rows = (a.M + LANES - 1) / LANES, most = dev.sm_count * (24 / (WARPS * LANES));
+        constexpr int WALK_WARPS = 24;  // on an SM
+        const int64_t rows = (a.M + LANES - 1) / LANES;
+        const int64_t most = dev.sm_count * (WALK_WARPS / (WARPS * LANES));
         return launch_dependent(kern, dim3((unsigned)(rows < most ? rows : most)), dim3(THREADS),
                                 SMEM, s, a);
     };
@@ -665,13 +707,12 @@ int norm_dispatch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
     // vectors of a thread: 8 at most by 16 bytes, 32 single elements
     constexpr int MOST = VEC == 1 ? 32 : 8;
     const int64_t vecs = (a.N + VEC - 1) / VEC;
-    if constexpr (VEC > 1) {
-        if (a.M * a.N >= (int64_t)dev.sm_count * 16384) {  // eight rows or more for each block
-            if (a.N <= 32 * kOwn) NORM_WALK(1, 4);
-            if (a.N <= 64 * kOwn) NORM_WALK(2, 1);
-            if (a.N <= 128 * kOwn) NORM_WALK(4, 1);
-            if (a.N <= 256 * kOwn) NORM_WALK(8, 1);
-        }
+    if (a.M * a.N >= (int64_t)dev.sm_count * 16384) {  // some rows for each block
+        if (a.N <= 32 * kOwn) NORM_WALK(1, 4);
+        if (a.N <= 64 * kOwn) NORM_WALK(2, 1);
+        if (a.N <= 128 * kOwn) NORM_WALK(4, 1);
+        if (a.N <= 256 * kOwn) NORM_WALK(8, 1);
+
     }
     if (vecs <= 32) NORM_RUN(1, 1, 128);
     if (vecs <= 128 * (MOST / 4)) NORM_RUN(4, MOST / 4, 128);
@@ -699,16 +740,16 @@ struct GradPlan {
     int warps, lanes, blocks;
 };
 GradPlan grad_plan(int64_t M, int64_t N, int sm_count) {
-    GradPlan g{16, 1, 0};
-    if (N > 32 * 16 * kOwn) return g;
-    for (int w : {1, 2, 4, 8, 16})
+    GradPlan g{32, 1, 0};
+    if (N > 32 * 32 * kOwn) return g;
+    for (int w : {1, 2, 4, 8, 16, 32})
         if (N <= 32 * w * kOwn) {
             g.warps = w;
             break;
         }
     g.lanes = g.warps == 1 ? 4 : 1;
     const int64_t rows = (M + g.lanes - 1) / g.lanes;
-    const int64_t most = (int64_t)sm_count * (kGradWarps / (g.warps * g.lanes));
+    const int64_t most = (int64_t)sm_count * (g.warps == 32 ? 1 : kGradWarps / (g.warps * g.lanes));
     g.blocks = (int)(rows < most ? rows : most);
     return g;
 }
@@ -717,7 +758,8 @@ constexpr int kLongShares = 32;
 template <typename T, typename W, int WARPS, int LANES, int VEC>
 int run_norm_grad(const NormGradArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int THREADS = 32 * WARPS * LANES;
-    constexpr int SMEM = VEC * sizeof(T) == 16 ? kNormStages<T> * 2 * kOwn * (int)sizeof(T) * THREADS
+    constexpr int STAGES = kNormStages<T, WARPS>;
+    constexpr int SMEM = VEC * sizeof(T) == 16 && STAGES > 1 ? STAGES * 2 * kOwn * (int)sizeof(T) * THREADS
                                               : 0;
     auto kern = norm_grad_kernel<T, W, WARPS, LANES, VEC>;
     const int rc = allow_smem(kern, SMEM, dev);
@@ -749,7 +791,8 @@ int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const Device
             case 2: NORM_GRAD_RUN(2, 1); break;
             case 4: NORM_GRAD_RUN(4, 1); break;
             case 8: NORM_GRAD_RUN(8, 1); break;
-            default: NORM_GRAD_RUN(16, 1); break;
+            case 16: NORM_GRAD_RUN(16, 1); break;
+            default: NORM_GRAD_RUN(32, 1); break;
         }
 #undef NORM_GRAD_RUN
     } else if (a.M > 0) {
