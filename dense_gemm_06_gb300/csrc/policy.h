@@ -6,6 +6,7 @@
 // shape and split of its last round.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <numeric>
 
@@ -409,7 +410,7 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
 // run at once, else 128. The forward pass of at most 128 rows is bound by reading
 // W, so its tiles divide the columns evenly over whole rounds of the SMs (32000
 // columns on 152 SMs: 2 rounds of 112).
-constexpr int64_t kXentMaxVocab = 1 << 24;
+constexpr int64_t kXentMaxVocab = 1 << 24, kXentMaxRows = 1 << 29;
 constexpr int64_t kXentMaxDepth = 1 << 20;  // K of gemm_xent_grad
 struct XentShape {
     int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
@@ -455,11 +456,11 @@ inline XentSumPlan plan_xent_sum(int64_t M, int64_t K, int64_t n, int sm_count) 
 
 // Rows of gemm_xent that run together: a whole number of tiles whose partial
 // maxima and sums (16 bytes for every row and tile of 32 columns or more) stay
-// within 256 MB.
+// within 256 MB, or 256 of them.
 inline int64_t xent_panel_rows(int64_t M, int64_t N, int tile_n) {
     const int64_t per_row = (N + tile_n - 1) / tile_n * 16;
     const int64_t rows = (256ll << 20) / per_row / 256 * 256;
-    return rows < 256 ? 256 : (rows < M ? rows : M);
+    return std::min(std::max<int64_t>(rows, 256), M);
 }
 
 // Columns of the vocabulary that gemm_xent_grad holds G of at one time: all of

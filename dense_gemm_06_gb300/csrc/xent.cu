@@ -349,6 +349,7 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
     int rc = check_inputs(M, N, K, X, ldx, W, ldw, target, dtype);
     if (rc != kOk || M == 0) return rc;
     if (!loss || !aligned_to(loss, 4) || !aligned_to(lse, 4)) return kInvalidArg;
+    if (M > kXentMaxRows) return kUnsupported;
     DeviceInfo* dev = nullptr;
     cudaMemPool_t pool = nullptr;
     rc = current_device_info(&dev, &pool);
@@ -445,6 +446,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     if (M > 0 && K > 0 && (dX || dW) &&
         (!lse || !aligned_to(lse, 4) || !aligned_to(dloss, 4)))
         return kInvalidArg;
+    if (M > kXentMaxRows) return kUnsupported;
     if (K == 0 || (!dX && !dW) || (M == 0 && !dW)) return kOk;
     DeviceInfo* dev = nullptr;
     cudaMemPool_t pool = nullptr;

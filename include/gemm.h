@@ -378,11 +378,12 @@ int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
  * and lse are DEVICE arrays of M floats; lse may be NULL, and is written for every
  * row. Types: the 16-bit dtypes (the result's type is not used; GEMM_F32 is
  * GEMM_ERR_UNSUPPORTED). Logits and sums are fp32; infinite or NaN logits make
- * their row's lse NaN. N is 1 .. 2^24 (more: GEMM_ERR_UNSUPPORTED). The rows' results
- * do not depend on each other. Scratch: 16 bytes for each row and 32 to 256
- * columns, for as many rows at a time as stay within 256 MB, and copies of X or W
- * where their rows are not 16-byte aligned. M zero is a no-op, K zero gives
- * lse = log N. Otherwise ownership, asynchrony and status codes are gemm()'s.
+ * their row's lse NaN. N is 1 .. 2^24, M at most 2^29 (more: GEMM_ERR_UNSUPPORTED).
+ * The rows' results do not depend on each other. Scratch: 16 bytes for each row and
+ * 32 to 256 columns, for as many rows at a time as stay within 256 MB (256 at
+ * least), and copies of X or W where their rows are not 16-byte aligned. M zero is a
+ * no-op, K zero gives lse = log N. Otherwise ownership, asynchrony and status codes
+ * are gemm()'s.
  */
 int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
               const void *W, int64_t ldw, const int32_t *target, float *loss, float *lse,
@@ -474,8 +475,8 @@ int embed_rows(int64_t M, int64_t V, int64_t K, const int32_t *ids, const void *
  * lddt >= K). With beta = 1 only the rows that a token names are touched (an
  * embedding tied to gemm_xent's W adds to its dW this way); else the whole table is
  * written. ids as in embed_rows; dy of rows that do not count may hold anything.
- * Sums are fp32 in an order that M alone fixes, rounded once. Scratch: 16 bytes a
- * token, and 2 K floats for each 16 tokens (at most 8192 times). Otherwise as
+ * Sums are fp32 in an order that M alone fixes, rounded once. Scratch: 32 bytes a
+ * token, and 2 K floats for each 32 tokens (at most 8192 times). Otherwise as
  * embed_rows.
  */
 int embed_rows_grad(int64_t M, int64_t V, int64_t K, const int32_t *ids, const void *dy,

@@ -108,6 +108,8 @@ def test_invalid_arguments_are_refused_on_the_host(call, kw):
 @pytest.mark.parametrize("call,kw", [
     (xent, dict(dtype=lg.GEMM_F32)), (xent_grad, dict(dtype=lg.GEMM_F32)),
     (xent, dict(N=(1 << 24) + 1)), (xent_grad, dict(N=(1 << 24) + 1)),
+    (xent, dict(M=(1 << 29) + 1)), (xent_grad, dict(M=(1 << 29) + 1)),
+    (xent_grad, dict(K=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21, lddx=1 << 21, lddw=1 << 21)),
     (balance, dict(E=1025, ldl=1025)), (balance_grad, dict(E=1025, ldl=1025, lddl=1025))])
 def test_what_is_not_supported(call, kw):
     assert call(**kw) == UNSUPPORTED
