@@ -7,6 +7,8 @@
     python -m dense_gemm_06_gb300.profile_case --case every
     python -m dense_gemm_06_gb300.profile_case --case grouped --reps 3   (or grouped_decode,
                                                                     grouped_k, lora, lora_decode)
+    python -m dense_gemm_06_gb300.profile_case --case xent --reps 3      (or xent_decode, layernorm,
+                                                                    embed, balance)
     python -m dense_gemm_06_gb300.profile_case --case bf16 --vendor --reps 2
     python -m dense_gemm_06_gb300.profile_case --case f16skinny --dtype 3 --bm 0 --vendor --reps 2
 
@@ -15,7 +17,8 @@ launch list that covers all of them): the tcgen05 GEMM at its small and
 ragged shapes (with the operand repack), the TMA-fed FFMA kernel with its
 K-slice tail and fixup, its stream-K variant, the cp.async FFMA kernel, the
 transpose pre-pass, the K = 0 kernels of gemm, gemm_ex and gemm_noalloc,
-gemm_noalloc's repack and the three row-softmax kernels.
+gemm_noalloc's repack, the three row-softmax kernels, the ragged products, and
+the cross entropy, layer norm, embedding and router kernels with their gradients.
 
 Inputs are the seeded synthetic operands of the benchmark (datagen), resident
 on the device before the first launch; each repetition is one gemm() call on
@@ -122,7 +125,135 @@ def run_every():
     lg.check(lg.gemm_grouped(2, 100, 65, 133, off, A, 133, W, 133, 65 * 133, 0, Y, 65,
                              lg.GEMM_F16_F32), "gemm_grouped")
     print("every: gemm_grouped with its repack, misaligned fp16", flush=True)
+    # cross entropy: pairs; one CTA, shared depth of dX, scaled; unaligned; no depth
+    for M, N, K, bf16, f32, pad in ((600, 40000, 256, True, True, 0), (70, 1000, 256, False, False, 0),
+                                    (300, 1999, 129, True, False, 1), (300, 1000, 0, True, True, 0)):
+        run_xent(M, N, K, bf16, f32, pad)()
+        print(f"every: gemm_xent, gemm_xent_grad {M} x {N} x {K}", flush=True)
+    for M, N, dtype in ((1, 512, lg.GEMM_F32), (300, 2048, lg.GEMM_BF16_F32),
+                        (5000, 1024, lg.GEMM_F16_F16), (20000, 1001, lg.GEMM_BF16_BF16),
+                        (40, 20000, lg.GEMM_BF16_F32), (40, 70001, lg.GEMM_F32)):
+        run_norm(M, N, dtype)()
+        print(f"every: layernorm_rows, layernorm_rows_grad {M} x {N}", flush=True)
+    for M, V, K, dtype in ((1, 1000, 64, lg.GEMM_BF16_BF16), (9000, 500, 256, lg.GEMM_F16_F32),
+                           (9000, 500, 131, lg.GEMM_BF16_BF16)):
+        run_embed(M, V, K, dtype)()
+        print(f"every: embed_rows, embed_rows_grad {M} of {V} x {K}", flush=True)
+    for T, E, top in ((1, 8, 2), (4096, 64, 6), (300, 1000, 4)):
+        run_balance(T, E, top)()
+        print(f"every: router_balance, router_balance_grad {T} x {E}", flush=True)
     lg.check(lg.gemm_check_device_error(), "device error word")
+
+
+def _normal(*shape, seed=1):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _types(dtype):
+    import torch
+    t = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+    import dense_gemm_06_gb300 as lg
+    return t[lg.IN_TYPE[dtype]], t[lg.OUT_TYPE[dtype]]
+
+
+def run_xent(M, N, K, bf16=True, f32=True, pad=0):
+    """A call of gemm_xent and gemm_xent_grad, one in eight rows not counting."""
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+    dtype = {(True, True): lg.GEMM_BF16_F32, (True, False): lg.GEMM_BF16_BF16,
+             (False, True): lg.GEMM_F16_F32, (False, False): lg.GEMM_F16_F16}[bf16, f32]
+    it, ot = _types(dtype)
+    ld = K + pad
+    x, w = _normal(M, ld).to(it), (_normal(N, ld, seed=2) * max(K, 1) ** -0.5).to(it)
+    target = torch.arange(M, device="cuda", dtype=torch.int32) * 97 % N
+    target[::8] = -1
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    dx, dw = torch.empty(M, K, dtype=it, device="cuda"), torch.empty(N, K, dtype=ot, device="cuda")
+
+    def call():
+        lg.check(lg.gemm_xent(M, N, K, x, ld, w, ld, target, loss, lse, dtype), "gemm_xent")
+        lg.check(lg.gemm_xent_grad(M, N, K, x, ld, w, ld, target, lse, None, dx, K, dw, K, dtype,
+                                   alpha=1.0 / M), "gemm_xent_grad")
+    return call
+
+
+def run_norm(M, N, dtype):
+    """A call of layernorm_rows and layernorm_rows_grad."""
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+    it, wt = _types(dtype)
+    x, dy, w, b = (_normal(M, N).to(it), _normal(M, N, seed=2).to(it), _normal(N).to(wt),
+                   _normal(N, seed=2).to(wt))
+    y, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+
+    def call():
+        lg.check(lg.layernorm_rows(M, N, x, N, w, b, 1e-5, y, N, mean, rstd, dtype), "layernorm")
+        lg.check(lg.layernorm_rows_grad(M, N, x, N, w, mean, rstd, dy, N, y, N, dw, db, dtype),
+                 "layernorm_rows_grad")
+    return call
+
+
+def run_embed(M, V, K, dtype):
+    """A call of embed_rows and embed_rows_grad, a third of the tokens one number."""
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+    it, ot = _types(dtype)
+    ids = (torch.arange(M, device="cuda") * 7919 % V).int()
+    ids[::3] = V // 2
+    table, dy = _normal(V, K).to(it), _normal(M, K).to(it)
+    y, dtable = torch.empty(M, K, dtype=ot, device="cuda"), torch.empty(V, K, dtype=ot, device="cuda")
+
+    def call():
+        lg.check(lg.embed_rows(M, V, K, ids, table, K, y, K, dtype), "embed_rows")
+        lg.check(lg.embed_rows_grad(M, V, K, ids, dy, K, dtable, K, dtype), "embed_rows_grad")
+    return call
+
+
+def run_balance(T, E, top):
+    """A call of router_balance and router_balance_grad on fp32 logits."""
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+    logits = _normal(T, E)
+    expert = logits.topk(top, dim=1).indices.int().contiguous()
+    counts, offsets = (torch.empty(E + 1, dtype=torch.int32, device="cuda") for _ in range(2))
+    prob, loss, dl = torch.empty(E, device="cuda"), torch.empty(1, device="cuda"), logits.clone()
+
+    def call():
+        lg.check(lg.router_balance(T, E, top, logits, E, expert, counts, offsets, prob, loss,
+                                   lg.GEMM_F32), "router_balance")
+        lg.check(lg.router_balance_grad(T, E, top, logits, E, expert, counts, None, dl, E,
+                                        lg.GEMM_F32), "router_balance_grad")
+    return call
+
+
+# the operators around the products, forward and backward
+MODEL = {"xent": lambda: run_xent(4096, 32000, 2048),
+         "xent_decode": lambda: run_xent(16, 32000, 2048),
+         "layernorm": lambda: run_norm(16384, 4096, 2),
+         "embed": lambda: run_embed(32768, 32000, 2048, 4),
+         "balance": lambda: run_balance(65536, 128, 8)}
+
+
+def run_model(case, reps):
+    import torch
+
+    import dense_gemm_06_gb300 as lg
+    call = MODEL[case]()
+    for r in range(reps):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        call()
+        e1.record()
+        torch.cuda.synchronize()
+        print(f"{case} rep {r}: {e0.elapsed_time(e1):.4f} ms, forward and backward")
+    lg.check(lg.gemm_check_device_error(), "device error words")
 
 
 # groups, rows, N, K of the ragged products (lora: adapters, rows, N, K; rank 32)
@@ -193,12 +324,12 @@ def main(argv=None):
         run_every()
         return
     if "--case" in argv and argv[argv.index("--case") + 1:][:1] and \
-            argv[argv.index("--case") + 1] in RAGGED:
+            argv[argv.index("--case") + 1] in {**RAGGED, **MODEL}:
         ap = argparse.ArgumentParser()
-        ap.add_argument("--case", choices=sorted(RAGGED))
+        ap.add_argument("--case", choices=sorted({**RAGGED, **MODEL}))
         ap.add_argument("--reps", type=int, default=3)
         a = ap.parse_args(argv)
-        run_ragged(a.case, a.reps)
+        (run_ragged if a.case in RAGGED else run_model)(a.case, a.reps)
         return
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", choices=sorted(CASES) + ["every"], required=True)
