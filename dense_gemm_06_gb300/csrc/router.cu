@@ -9,9 +9,9 @@
 // Both are bound by memory for many rows and by latency for few. A row sits on 8
 // or 32 lanes of a warp, so the softmax and the inner product are reductions over
 // those, and several rows are in flight in a warp. The forward pass keeps each
-// lane's sum of p over its rows in registers; a block's sums and counts are added
-// by a second kernel in the order of the blocks (counts are whole numbers, sums
-// do not depend on timing).
+// lane's sum of p over its rows in registers; the blocks of a cluster add theirs in
+// the order of their ranks, and where there are several clusters a second kernel adds
+// the clusters' (counts are whole numbers, sums do not depend on timing).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -72,22 +72,119 @@ __device__ __forceinline__ void softmax_row(float (&v)[NE]) {
     for (int i = 0; i < NE; ++i) v[i] *= s;
 }
 
+// Expert i of the NE that a lane holds: groups of four side by side.
+template <int LANES>
+__device__ __forceinline__ int expert_of(int sub, int i) {
+    return (sub + LANES * (i / 4)) * 4 + i % 4;
+}
+
+// A lane's logits of a row, -inf past the last expert (and for no row); four at a
+// time where E and every row's address allow it.
+template <typename T, int LANES, int NE>
+__device__ __forceinline__ void load_row(const T* row, bool in, int E, int sub, bool fours,
+                                         float (&v)[NE]) {
+    if (fours) {
+#pragma unroll
+        for (int i = 0; i < NE; i += 4) {
+            const int e = expert_of<LANES>(sub, i);
+            Piece<4 * sizeof(T)> p;
+            if (in && e < E) p = *reinterpret_cast<const Piece<4 * sizeof(T)>*>(row + e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    v[i + j] = __uint_as_float(p.w[j]);
+                } else {
+                    const uint16_t h = (uint16_t)(p.w[j / 2] >> (j % 2 * 16));
+                    v[i + j] = to_f32(*reinterpret_cast<const T*>(&h));
+                }
+                if (!in || e >= E) v[i + j] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = expert_of<LANES>(sub, i);
+            v[i] = in && e < E ? to_f32(row[e]) : -INFINITY;
+        }
+    }
+}
+
 struct BalanceArgs {
     int64_t T;
     int E, top;
     const void* logits;
     int64_t ldl;
+    bool fours;
     const int32_t* expert;
-    float* part_p;      // blocks x E sums of p
-    int32_t* part_n;    // blocks x (E + 1) counts, the last the rows that count
+    int32_t* counts;
+    int32_t* offsets;   // or null
+    float* prob;
+    float* loss;
+    float* part_p;      // clusters x E sums of p
+    int32_t* part_n;    // clusters x (E + 1) counts, the last the rows that count
     ErrWord* err;
 };
 
-// A row on LANES lanes, expert sub + LANES i in lane sub; a warp takes 32 / LANES
-// rows at a time, ROWS times over with their reads in flight together.
-constexpr int kWarps = 8;
-template <typename T, int LANES, int NE, int ROWS>
-__global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs a) {
+// Writes the results from the experts' counts and sums of p (in shared memory) of n
+// rows that count: a thread takes 1024 / THREADS experts in a row. The whole block
+// calls it; the sums are added in one order whatever the timing.
+template <int THREADS>
+__device__ __forceinline__ void write_balance(const BalanceArgs& a, int n, const float* p,
+                                              const int32_t* c) {
+    constexpr int PER = kMaxExperts / THREADS, WARPS = THREADS / 32;
+    __shared__ int32_t warp_c[WARPS];
+    __shared__ float warp_f[WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e0 = threadIdx.x * PER, m = n > 0 ? n : 1;
+    int32_t upto[PER], all = 0;
+    float term = 0.f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        upto[j] = all;
+        if (e0 + j >= a.E) continue;
+        const int32_t own = c[e0 + j];
+        const float mean = p[e0 + j] / (float)m;
+        a.counts[e0 + j] = own;
+        a.prob[e0 + j] = mean;
+        term += (float)((double)own / ((double)a.top * m)) * mean;
+        all += own;
+        upto[j] = all;
+    }
+    int32_t before = all;  // of the warp's threads up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t add = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += add;
+    }
+    term = sum_lanes<32>(term);
+    if (lane == 31) warp_c[warp] = before;
+    if (lane == 0) warp_f[warp] = term;
+    __syncthreads();
+    if (a.offsets) {
+        before += __reduce_add_sync(0xffffffffu, lane < warp ? warp_c[lane] : 0) - all;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (e0 + j < a.E) a.offsets[e0 + j + 1] = before + upto[j];
+        if (threadIdx.x == 0) a.offsets[0] = 0;
+    }
+    if (warp == 0) {
+        term = sum_lanes<32>(lane < WARPS ? warp_f[lane] : 0.f);
+        if (lane == 0) {
+            *a.loss = (float)a.E * term;
+            a.counts[a.E] = n;
+        }
+    }
+}
+
+// A row on LANES lanes, four experts in a row on each; a warp takes 32 / LANES rows at a time, ROWS times over with their reads in flight together. The blocks of
+// a cluster (CL) add up their sums in the order of their ranks; a cluster that is
+// alone writes the results, else each leaves one part.
+constexpr int kWarps = 8, kCluster = 8;
+// Blocks on an SM, by the probabilities that a lane holds.
+constexpr int resident(int held) { return held <= 20 ? 4 : held <= 24 ? 3 : 2; }
+template <typename T, int LANES, int NE, int ROWS, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(32 * kWarps, resident(NE * ROWS))
+    balance_kernel(const BalanceArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int SIDE = 32 / LANES;  // rows of a warp side by side
     extern __shared__ int32_t counts[];  // E + 1, then kWarps x E sums
@@ -112,10 +209,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs 
             const int64_t t = w0 + side + r * step;
             const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
             // read whether the row counts or not, so that one latency covers both
-#pragma unroll
-            for (int i = 0; i < NE; ++i)
-                v[r][i] = t < a.T && sub + LANES * i < a.E ? to_f32(row[sub + LANES * i])
-                                                           : -INFINITY;
+            load_row<T, LANES>(row, t < a.T, a.E, sub, a.fours, v[r]);
             first[r] = t < a.T && sub < a.top ? a.expert[t * a.top + sub] : -1;
         }
 #pragma unroll
@@ -139,55 +233,75 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const BalanceArgs 
 #pragma unroll
         for (int o = LANES; o < 32; o *= 2)
             total[i] += __shfl_xor_sync(0xffffffffu, total[i], o);
-        if (side == 0 && sub + LANES * i < a.E) sums[warp * a.E + sub + LANES * i] = total[i];
+        const int e = expert_of<LANES>(sub, i);
+        if (side == 0 && e < a.E) sums[warp * a.E + e] = total[i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e <= a.E; e += 32 * kWarps) {
-        a.part_n[(int64_t)blockIdx.x * (a.E + 1) + e] = counts[e];
-        if (e == a.E) continue;
+    for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) {
         float s = 0.f;
         for (int w = 0; w < kWarps; ++w) s += sums[w * a.E + e];
-        a.part_p[(int64_t)blockIdx.x * a.E + e] = s;
+        sums[e] = s;
+    }
+    if constexpr (CL == 1) {
+        __syncthreads();
+        write_balance<32 * kWarps>(a, counts[a.E], sums, counts);
+    } else {
+        gemm_ptx::cluster_sync_all();
+        const int rank = (int)gemm_ptx::cluster_ctarank();
+        const bool alone = gridDim.x == CL;
+        // alone: all of them into the second and third warp's place; else a share each
+        const int e0 = alone ? (rank == 0 ? 0 : a.E + 1) : (a.E + 1) * rank / CL;
+        const int e1 = alone ? a.E + 1 : (a.E + 1) * (rank + 1) / CL;
+        float* all_p = alone ? sums + a.E : a.part_p + (int64_t)(blockIdx.x / CL) * a.E;
+        int32_t* all_n = alone ? reinterpret_cast<int32_t*>(sums + 2 * a.E)
+                               : a.part_n + (int64_t)(blockIdx.x / CL) * (a.E + 1);
+        for (int e = e0 + threadIdx.x; e < e1; e += 32 * kWarps) {
+            float p[CL];
+            int32_t n[CL];
+#pragma unroll
+            for (int r = 0; r < CL; ++r) {
+                p[r] = e < a.E ? ld_cluster(&sums[e], r) : 0.f;
+                n[r] = ld_cluster(&counts[e], r);
+            }
+#pragma unroll
+            for (int r = 1; r < CL; ++r) {
+                p[0] += p[r];
+                n[0] += n[r];
+            }
+            if (e < a.E) all_p[e] = p[0];
+            all_n[e] = n[0];
+        }
+        gemm_ptx::cluster_sync_all();  // no block leaves while its sums are read
+        if (alone && rank == 0) write_balance<32 * kWarps>(a, all_n[a.E], all_p, all_n);
     }
 }
 
-// One cluster of JOIN blocks (one where there is little to add up): each adds up
-// its share of the parts, the first one the shares, and writes the limits and the
-// loss. `shares` threads an expert (a power of two), each a share of the block's
-// parts, whose reads are in flight together.
-template <int JOIN>
-__global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(1024)
-    balance_join_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_n,
-                        int parts, int E, int top, int shares, int32_t* __restrict__ counts,
-                        int32_t* __restrict__ offsets, float* __restrict__ prob,
-                        float* __restrict__ loss) {
+// Adds up the parts that several clusters left: `shares` threads an expert (a power of
+// two), each with its share of the parts, whose reads are in flight together.
+__global__ void __launch_bounds__(1024)
+    balance_join_kernel(const BalanceArgs a, int parts, int shares) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int AHEAD = 8;
     __shared__ float p[1024];
-    __shared__ int32_t c[1024], warp_n[32], warp_c[32];
-    __shared__ float warp_f[32];
-    __shared__ int32_t block_n;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = JOIN == 1 ? 0 : (int)gemm_ptx::cluster_ctarank();
+    __shared__ int32_t c[1024], warp_n[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.E;
     gemm_ptx::pdl_wait();
-    const int b0 = (int)((int64_t)parts * rank / JOIN);
-    const int b1 = (int)((int64_t)parts * (rank + 1) / JOIN);
     int n = 0;  // rows that count
-    for (int b = b0 + threadIdx.x; b < b1; b += 1024) n += part_n[(int64_t)b * (E + 1) + E];
+    for (int b = threadIdx.x; b < parts; b += 1024) n += a.part_n[(int64_t)b * (E + 1) + E];
     // an expert's shares lie a whole number of experts apart
     const int wide = 1024 / shares;
     const int e = threadIdx.x % wide, share = threadIdx.x / wide;
     float s = 0.f;
     int32_t k = 0;
     if (e < E)
-        for (int b = b0 + share; b < b1; b += AHEAD * shares) {
+        for (int b = share; b < parts; b += AHEAD * shares) {
             float ps[AHEAD];
             int32_t ns[AHEAD];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int64_t at = b + j * shares;
-                ps[j] = at < b1 ? part_p[at * E + e] : 0.f;
-                ns[j] = at < b1 ? part_n[at * (E + 1) + e] : 0;
+                ps[j] = at < parts ? a.part_p[at * E + e] : 0.f;
+                ns[j] = at < parts ? a.part_n[at * (E + 1) + e] : 0;
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
@@ -208,65 +322,7 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(1024)
         __syncthreads();
     }
     n = __reduce_add_sync(0xffffffffu, warp_n[lane]);
-    const bool mine = threadIdx.x < E;
-    int32_t own = c[threadIdx.x];
-    s = p[threadIdx.x];
-    if constexpr (JOIN > 1) {
-        if (threadIdx.x == 0) block_n = n;
-        gemm_ptx::cluster_sync_all();
-        if (rank == 0) {
-            int32_t rn[JOIN], rc[JOIN];
-            float rp[JOIN];
-#pragma unroll
-            for (int r = 0; r < JOIN; ++r) {
-                rn[r] = ld_cluster(&block_n, r);
-                rp[r] = ld_cluster(&p[threadIdx.x], r);
-                rc[r] = ld_cluster(&c[threadIdx.x], r);
-            }
-            n = own = 0;
-            s = 0.f;
-#pragma unroll
-            for (int r = 0; r < JOIN; ++r) {
-                n += rn[r];
-                own += rc[r];
-                s += rp[r];
-            }
-        }
-        gemm_ptx::cluster_sync_all();  // no block leaves while its sums are read
-        if (rank != 0) return;
-    }
-    if (!mine) own = 0;
-    const int m = n > 0 ? n : 1;
-    float term = 0.f;
-    if (mine) {
-        const float mean = s / (float)m;
-        counts[threadIdx.x] = own;
-        prob[threadIdx.x] = mean;
-        term = (float)((double)own / ((double)top * m)) * mean;
-    }
-    // the limits: a sum up to each expert; the loss: a sum in a fixed order
-    int32_t upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int32_t add = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += add;
-    }
-    term = sum_lanes<32>(term);
-    if (lane == 31) warp_c[warp] = upto;
-    if (lane == 0) warp_f[warp] = term;
-    __syncthreads();
-    if (offsets) {
-        const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_c[lane] : 0);
-        if (mine) offsets[threadIdx.x + 1] = before + upto;
-        if (threadIdx.x == 0) offsets[0] = 0;
-    }
-    if (warp == 0) {
-        term = sum_lanes<32>(warp_f[lane]);
-        if (lane == 0) {
-            *loss = (float)E * term;
-            counts[E] = n;
-        }
-    }
+    write_balance<1024>(a, n, p, c);
 }
 
 struct BalanceGradArgs {
@@ -274,6 +330,7 @@ struct BalanceGradArgs {
     int E, top;
     const void* logits;
     int64_t ldl;
+    bool fours;
     const int32_t* expert;
     const int32_t* counts;
     const float* dloss;  // null: 1
@@ -284,34 +341,38 @@ struct BalanceGradArgs {
 
 constexpr int kGradWarps = 8;
 template <typename T, typename O, int LANES, int NE, int ROWS>
-__global__ void __launch_bounds__(32 * kGradWarps) balance_grad_kernel(const BalanceGradArgs a) {
+__global__ void __launch_bounds__(32 * kGradWarps, NE * (ROWS + 1) <= 48 ? 3 : 2)
+    balance_grad_kernel(const BalanceGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int SIDE = 32 / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane % LANES, side = lane / LANES;
     gemm_ptx::pdl_wait();
-    const int n = a.counts[a.E];
-    const float by = n > 0 ? 1.f / (float)n : 0.f;
-    const float each = by / (float)a.top;
-    float f[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        f[i] = sub + LANES * i < a.E ? (float)a.counts[sub + LANES * i] * each : 0.f;
-    const float d = a.alpha * (a.dloss ? *a.dloss : 1.f) * (float)a.E * by;
     const int64_t step = (int64_t)gridDim.x * kGradWarps * SIDE;
-    for (int64_t w0 = ((int64_t)blockIdx.x * kGradWarps + warp) * SIDE; w0 < a.T; w0 += ROWS * step) {
-        float v[ROWS][NE];
-        bool in[ROWS];
+    int64_t w0 = ((int64_t)blockIdx.x * kGradWarps + warp) * SIDE;
+    float v[ROWS][NE];
+    bool in[ROWS];
+    auto load = [&] {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int64_t t = w0 + side + r * step;
             const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
             in[r] = t < a.T && a.expert[t * a.top] >= 0;
-#pragma unroll
-            for (int i = 0; i < NE; ++i)
-                v[r][i] = t < a.T && sub + LANES * i < a.E ? to_f32(row[sub + LANES * i])
-                                                           : -INFINITY;
+            load_row<T, LANES>(row, t < a.T, a.E, sub, a.fours, v[r]);
         }
+    };
+    load();  // beside the counts
+    const int n = a.counts[a.E];
+    const float by = n > 0 ? 1.f / (float)n : 0.f;
+    const float each = by / (float)a.top;
+    float f[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = expert_of<LANES>(sub, i);
+        f[i] = e < a.E ? (float)a.counts[e] * each : 0.f;
+    }
+    const float d = a.alpha * (a.dloss ? *a.dloss : 1.f) * (float)a.E * by;
+    for (; w0 < a.T; w0 += ROWS * step, load()) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int64_t t = w0 + side + r * step;
@@ -323,11 +384,26 @@ __global__ void __launch_bounds__(32 * kGradWarps) balance_grad_kernel(const Bal
             if (t >= a.T) continue;
             O* row = static_cast<O*>(a.dlogits) + t * a.ldd;
 #pragma unroll
+            for (int i = 0; i < NE; ++i) v[r][i] = in[r] ? d * v[r][i] * (f[i] - inner) : 0.f;
+            if (a.fours && a.beta == 0.f) {
+#pragma unroll
+                for (int i = 0; i < NE; i += 4) {
+                    const int e = expert_of<LANES>(sub, i);
+                    if (e >= a.E) continue;
+                    alignas(16) O o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = from_f32<O>(v[r][i + j]);
+                    *reinterpret_cast<Piece<4 * sizeof(O)>*>(row + e) =
+                        *reinterpret_cast<Piece<4 * sizeof(O)>*>(o);
+                }
+                continue;
+            }
+#pragma unroll
             for (int i = 0; i < NE; ++i) {
-                const int e = sub + LANES * i;
+                const int e = expert_of<LANES>(sub, i);
                 if (e >= a.E) continue;
-                const float g = in[r] ? d * v[r][i] * (f[i] - inner) : 0.f;
-                row[e] = from_f32<O>(a.beta != 0.f ? fmaf(a.beta, to_f32(row[e]), g) : g);
+                row[e] = from_f32<O>(a.beta != 0.f ? fmaf(a.beta, to_f32(row[e]), v[r][i])
+                                                   : v[r][i]);
             }
         }
         __syncwarp();
@@ -337,6 +413,11 @@ __global__ void __launch_bounds__(32 * kGradWarps) balance_grad_kernel(const Bal
 bool rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int es) {
     return p && aligned_to(p, es) && ld >= cols &&
            (__int128)(rows - 1) * ld + cols <= (__int128)(INT64_MAX / es);
+}
+
+// Every row begins on, and is a whole number of, four elements.
+bool in_fours(const void* p, int64_t E, int64_t ld, int es) {
+    return aligned_to(p, 4 * es) && E % 4 == 0 && ld % 4 == 0;
 }
 
 // Calls f with integral constants LANES, NE (numbers of a lane) and ROWS. Eight
@@ -389,42 +470,51 @@ int balance(int64_t T, int64_t E, int64_t top, const void* logits, int64_t ldl,
                            prob, loss};
     rc = check_device_pointers(ptrs, 6, dev->device);
     if (rc != kOk) return rc;
-    const int each = kWarps * (E <= 256 ? 4 : 1);  // rows of a block at a time
-    int64_t blocks = (T + each - 1) / each;
-    const int64_t most = (int64_t)dev->sm_count * 3;
-    if (blocks > most) blocks = most;
+    // Rows of a block at a time. Two rounds are a block's, up to two for each of its
+    // blocks a cluster's, which saves the second kernel (us: 48 rows of E = 64 5.4 by a
+    // block, 5.7 by a cluster; 200 rows of E = 160 5.3 by a cluster, 6.1 by blocks and a
+    // join, 1024 rows, four rounds, 7.8 and 6.6). Many rows are those of as many blocks
+    // as run at once (an eighth less: clusters do not fill the SMs evenly), as many
+    // rounds each.
+    const int64_t each = kWarps * (E <= 256 ? 4 : 1), rounds = (T + each - 1) / each;
+    const size_t smem = (size_t)(E + 1 + kWarps * E) * 4;
     Scratch scratch{pool, s, dev->device};
-    BalanceArgs a{T, (int)E, (int)top, logits, ldl, expert, nullptr, nullptr, dev->err_word};
-    if (blocks > 0) {
-        char* mem = static_cast<char*>(scratch.get((size_t)(blocks * (2 * E + 1) * 4)));
-        if (!mem) return kCuda;
-        a.part_p = reinterpret_cast<float*>(mem);
-        a.part_n = reinterpret_cast<int32_t*>(mem + blocks * E * 4);
-        const size_t smem = (size_t)(E + 1 + kWarps * E) * 4;
-        const dim3 grid((unsigned)blocks), block(32 * kWarps);
-        rc = with_lanes((int)E, [&](auto lanes, auto ne, auto rows) {
-            constexpr int LANES = decltype(lanes)::value;
-            constexpr int NE = decltype(ne)::value, ROWS = decltype(rows)::value;
-            auto run = [&](auto t) {
-                using L = decltype(t);
-                return launch_dependent(balance_kernel<L, LANES, NE, ROWS>, grid, block, smem, s,
-                                        a);
-            };
-            if (dtype == GEMM_F32) return run(float{});
-            if (dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16) return run(__nv_bfloat16{});
-            return run(__half{});
-        });
-    }
-    if (rc == kOk) {
+    const bool fours = in_fours(logits, E, ldl, dtype == GEMM_F32 ? 4 : 2);
+    BalanceArgs a{T,      (int)E,  (int)top, logits, ldl,     fours,   expert,
+                  counts, offsets, prob,     loss,   nullptr, nullptr, dev->err_word};
+    rc = with_lanes((int)E, [&](auto lanes, auto ne, auto rows) {
+        constexpr int LANES = decltype(lanes)::value;
+        constexpr int NE = decltype(ne)::value, ROWS = decltype(rows)::value;
+        const bool single = rounds <= 2;
+        const int64_t most =
+            (int64_t)dev->sm_count * resident(NE * ROWS) * 7 / 8 / kCluster * kCluster;
+        int64_t blocks = single ? 1 : kCluster;
+        if (rounds > kCluster * 2) {
+            const int64_t turns = (rounds + most - 1) / most;
+            blocks = ((rounds + turns - 1) / turns + kCluster - 1) / kCluster * kCluster;
+        }
+        const int clusters = (int)(blocks / kCluster);
+        if (clusters > 1) {
+            char* mem = static_cast<char*>(scratch.get((size_t)(clusters * (2 * E + 1) * 4)));
+            if (!mem) return (int)kCuda;
+            a.part_p = reinterpret_cast<float*>(mem);
+            a.part_n = reinterpret_cast<int32_t*>(mem + clusters * E * 4);
+        }
+        auto run = [&](auto t) {
+            using L = decltype(t);
+            return launch_dependent(single ? balance_kernel<L, LANES, NE, ROWS, 1>
+                                           : balance_kernel<L, LANES, NE, ROWS, kCluster>,
+                                    dim3((unsigned)blocks), dim3(32 * kWarps), smem, s, a);
+        };
+        const int r = dtype == GEMM_F32 ? run(float{})
+                      : dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16 ? run(__nv_bfloat16{})
+                                                                          : run(__half{});
+        if (r != kOk || clusters < 2) return r;
         int shares = 1;
         while (shares * 2 * E <= 1024) shares *= 2;
-        // more than one round of reads for each thread: eight blocks share them
-        const bool wide = blocks > 8 * shares;
-        rc = launch_dependent(wide ? balance_join_kernel<8> : balance_join_kernel<1>,
-                              dim3(wide ? 8 : 1), dim3(1024), 0, s, (const float*)a.part_p,
-                              (const int32_t*)a.part_n, (int)blocks, (int)E, (int)top, shares,
-                              counts, offsets, prob, loss);
-    }
+        return launch_dependent(balance_join_kernel, dim3(1), dim3(1024), 0, s, a, clusters,
+                                shares);
+    });
     scratch.release();
     return rc;
 }
@@ -444,7 +534,9 @@ int balance_grad(int64_t T, int64_t E, int64_t top, const void* logits, int64_t 
     const void* ptrs[5] = {logits, expert, counts, dloss, dlogits};
     rc = check_device_pointers(ptrs, 5, dev->device);
     if (rc != kOk) return rc;
-    const BalanceGradArgs a{T, (int)E, (int)top, logits, ldl, expert, counts, dloss, alpha, beta,
+    const bool fours = in_fours(logits, E, ldl, dtype == GEMM_F32 ? 4 : 2) &&
+                       in_fours(dlogits, E, ldd, os);
+    const BalanceGradArgs a{T, (int)E, (int)top, logits, ldl, fours, expert, counts, dloss, alpha, beta,
                             dlogits, ldd};
     const int each = kGradWarps * (E <= 256 ? 4 : 1);  // rows of a block at a time
     int64_t blocks = (T + each - 1) / each;
