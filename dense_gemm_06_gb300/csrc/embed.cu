@@ -16,6 +16,11 @@
 // Sums: the sorted list is cut into chunks of equal length, so that a frequent
 // token's rows are shared by many blocks. A run that crosses chunks leaves one
 // partial sum in each, which a last kernel adds in the order of the chunks.
+//
+// 8192 tokens of 32000 x 2048, bf16 to fp32, us: forward 11.5; sort 4, merge 8, list
+// of pieces 4, sums and fill 47.5 (6.2 TB/s), crossing runs 8.5, some of it beside its
+// neighbours: 82 together. (Filling a part of the rows beside the list of pieces and
+// the crossing runs instead left the whole as it was.)
 #include <cuda_runtime.h>
 
 #include <cstdint>

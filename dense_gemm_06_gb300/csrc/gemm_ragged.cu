@@ -418,9 +418,9 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     if (rc != kOk) return rc;
 
     EpiParams ep = epi_params(epi);
-    if (scale) ep.active = 1;  // a factor in device memory, on alpha
     const RaggedShape shape =
         plan_grouped_k(G, M, N, dev->sm_count, ragged_out(ep, dtype), K / G);
+    if (scale) ep.active = 1;  // a factor in device memory, on alpha
     const bool bf16 = is_bf16(dtype);
     RaggedParams rp;
     std::memset(&rp, 0, sizeof(rp));

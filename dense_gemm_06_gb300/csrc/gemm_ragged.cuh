@@ -68,7 +68,7 @@ struct RaggedParams {
     // gemm_lora
     const int32_t* adapter;  // adapter number of each row
     const float* scale;      // one factor per adapter, or null (depth: null, or one factor
-                             // on alpha: gemm_xent_grad's scaling back of fp16 sums)
+                             // on alpha: what gemm_xent_grad divided by)
     const void* x;           // kRagShrinkRows: X and LA, row pitches ldx and ldla
     const void* lora_a;
     int64_t ldx, ldla;
@@ -771,11 +771,12 @@ __global__ void __launch_bounds__(kRowsThreads)
 // with it. With p.split > 0 (CG == 1) a cluster of 2^split CTAs shares
 // each unit: every CTA sums its share of the k-blocks, and the partial sums
 // meet in the shared memory of the CTA that owns the row, in rank order.
-// EPI: the launch has a fused epilogue. A template argument where fp32 sums are
-// folded (else always true): the 128 sums leave the plain kernel no registers
-// for code that it does not run (511 us against 477 us, 64 weight gradients of
-// 2816 x 2048).
-template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, bool EPI>
+// EPI: whether the launch has a fused epilogue, or only a factor in device memory. A
+// template argument where fp32 sums are folded (else always kEpiAny): the 128 sums
+// leave the plain kernel no registers for code that it does not run (511 us against
+// 477 us, 64 weight gradients of 2816 x 2048).
+enum { kEpiNone = 0, kEpiAny = 1, kEpiScale = 2 };
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, int EPI>
 __global__ void __launch_bounds__(RTHREADS, 1)
     ragged_kernel(const __grid_constant__ RaggedParams p) {
     constexpr bool NARROW = MODE == kRagShrink && P_MN;
@@ -1262,7 +1263,7 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             const int l = q * 32 + lane;  // TMEM lane
             const int f = un.feat0 + (int)rank * 128 + l;
             const int n_rows = min(un.width, un.row_end - un.row0);
-            const bool epi = EPI && MODE != kRagShrink && p.epi.active;
+            const bool epi = EPI == kEpiAny && MODE != kRagShrink && p.epi.active;
             const bool f_ok = f < p.feats;
             float bias = 0.f;
             if (epi && p.epi.bias && f_ok)
@@ -1342,6 +1343,11 @@ __global__ void __launch_bounds__(RTHREADS, 1)
                 }
                 OutT* dst = c_col + (int64_t)(c * 32) * p.ldc;
                 const int row = un.row0 + c * 32;
+                if constexpr (EPI == kEpiScale) {
+                    const float by = *p.scale;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= by;
+                }
                 if constexpr (MODE == kRagLora) {
                     if (by_hand && f_ok) {
 #pragma unroll
@@ -1690,12 +1696,19 @@ __global__ void __launch_bounds__(RTHREADS, 1)
 
 // units: work units (an upper bound where only the device knows their number);
 // the grid holds as many clusters as fit the GPU at once, at most one per unit.
-template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, bool EPI = true>
+template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, int EPI = kEpiAny>
 int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev,
                           cudaStream_t stream) {
-    if constexpr (EPI && std::is_same_v<OutT, float> && MODE != kRagShrink)
+    if constexpr (EPI == kEpiAny && std::is_same_v<OutT, float> && MODE != kRagShrink) {
+        if constexpr (MODE == kRagDepth)
+            if (rp.scale && rp.epi.alpha == 1.f && rp.epi.beta == 0.f && !rp.epi.bias &&
+                rp.epi.act == 0)
+                return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, kEpiScale>(rp, units, dev,
+                                                                                    stream);
         if (!rp.epi.active)
-            return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, false>(rp, units, dev, stream);
+            return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, kEpiNone>(rp, units, dev,
+                                                                               stream);
+    }
     auto kern = ragged_kernel<CG, MODE, P_MN, BF16, OutT, EPI>;
     static std::mutex mu;
     static uint64_t configured = 0;  // bit per device

@@ -412,6 +412,11 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
 // columns on 152 SMs: 2 rounds of 112).
 constexpr int64_t kXentMaxVocab = 1 << 24, kXentMaxRows = 1 << 29;
 constexpr int64_t kXentMaxDepth = 1 << 20;  // K of gemm_xent_grad
+// gemm_xent_grad: a 16-bit dW of at most so many rows of X (in whole tiles) that one
+// accumulator takes them runs on the kernel that stores by TMA, deeper ones on
+// gemm_grouped_k's (bf16, 32000 x 2048, us: 1 row 74 and 110, 300 rows 111 and 138,
+// 1000 rows 184 and 177; 64000 x 4096 from 2048 rows 1260 and 1183).
+constexpr int64_t kXentTableRows = 704;
 struct XentShape {
     int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
     int tile_n;

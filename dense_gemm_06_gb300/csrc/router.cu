@@ -11,7 +11,9 @@
 // those, and several rows are in flight in a warp. The forward pass keeps each
 // lane's sum of p over its rows in registers; the blocks of a cluster add theirs in
 // the order of their ranks, and where there are several clusters a second kernel adds
-// the clusters' (counts are whole numbers, sums do not depend on timing).
+// the clusters' (counts are whole numbers, sums do not depend on timing). 32768 rows
+// of 160, fp32, us: forward 9 and 6.5 for the join, gradient 10.7; 48 rows of 64: 4.3.
+// Both kernels are chains of latencies: a load, two reductions, expf, a barrier.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -13,18 +13,22 @@
 // are never stored, only 1/16 of their bytes.
 //
 // Backward: piece by piece of the vocabulary the same kernel computes the logits
-// again and writes G as 16-bit numbers; the dense kernel of gemm() multiplies it
-// with the piece's rows of W (dX, summed over the pieces in fp32) and with X (the
-// piece's rows of dW, complete). G takes at most 512 MB, or 4096 columns.
+// again and writes G as 16-bit numbers, which are multiplied with the piece's rows of
+// W (dX, summed over the pieces in fp32, on gemm()'s kernel or, where its tiles are
+// few, in shares of the depth) and with X (the piece's rows of dW, complete). G takes
+// at most 512 MB, or 4096 columns.
 //
 // Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
 // relative 2^-9 (bf16) is below the rounding of a 16-bit result. An fp32 dW would
 // show it, so for that G is two numbers, hi + lo (2^-17 of g), and X is multiplied
 // with both in one product of twice the depth, on gemm_grouped_k's kernel, which
-// adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384). fp16 has the exponents
-// for that only near 1: G is scaled by a power of two that brings the largest
-// |alpha dloss| to 2^12, its small probabilities then reach down to 2^-36 of it, and
-// the products are scaled back in fp32 before they are rounded.
+// adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384).
+// G is divided by the largest |alpha dloss|, which the products are multiplied with
+// again in fp32 before they are rounded: a mean's 1 / n, rounded to 16 bits, would
+// put the same error into every term (0.2 % of dX in bf16), and fp16 has exponents
+// only near 1 (there the largest is 2^12, and probabilities reach down to 2^-36).
+// That costs the scale's launch and dX an fp32 pass (4096 x 32000 x 2048: 14 of
+// 1310 us).
 //
 // Rows whose target does not count are zero in G, and zero in the copy of X that
 // dW is multiplied from (0 times an infinity would be NaN).
@@ -144,11 +148,12 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// scale[0]: the power of two that brings the largest finite |alpha dloss_t| of
-// the rows that count into [2^12, 2^13); scale[1]: its inverse. One block.
+// scale[0]: what brings the largest finite |alpha dloss_t| of the rows that count to
+// `top`; scale[1]: its inverse. One block.
 __global__ void __launch_bounds__(1024)
     xent_scale_kernel(int M, const int32_t* __restrict__ target, int vocab,
-                      const float* __restrict__ dloss, float alpha, float* __restrict__ scale) {
+                      const float* __restrict__ dloss, float alpha, float to,
+                      float* __restrict__ scale) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
     __shared__ float most[32];
@@ -163,13 +168,13 @@ __global__ void __launch_bounds__(1024)
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int i = 1; i < 32; ++i) top = fmaxf(top, most[i]);
-    int e = top > 0.f ? 12 - ilogbf(top) : 0;
-    e = min(max(e, -100), 100);
-    scale[0] = ldexpf(1.f, e);
-    scale[1] = ldexpf(1.f, -e);
+    if (top == 0.f) top = to;
+    top = fminf(fmaxf(top, 0x1p-100f), 0x1p100f);
+    scale[0] = to / top;
+    scale[1] = top / to;
 }
 
-// dX = scale * (the sum of `parts` matrices, part_rows rows apart), rounded once;
+// dX = *scale * (the sum of `parts` matrices, part_rows rows apart), rounded once;
 // rows x cols. A warp takes 32 groups of 8 columns of two rows at a time, and stores
 // them in 16-byte pieces whatever dX's alignment.
 template <typename T>
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(256)
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
     constexpr int ROWS = 2, G = 8;
-    const float by = scale ? *scale : 1.f;
+    const float by = *scale;
     const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * G;
     const int64_t warps = (int64_t)gridDim.x * 8;
     for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS; r0 < rows;
@@ -310,8 +315,8 @@ bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void
 // dX's part of a piece (n columns, in a vocabulary cut into pieces of `piece`) in
 // shares of the depth that are the same for every piece: sums (+)= G W.
 int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int64_t n,
-               const void* g, int64_t ldg, const void* W, int64_t ldw, float* sums, int64_t sum_rows, bool add,
-               bool bf16, const DeviceInfo& dev, cudaStream_t s) {
+               const void* g, int64_t ldg, const void* W, int64_t ldw, float* sums,
+               int64_t sum_rows, bool add, bool bf16, const DeviceInfo& dev, cudaStream_t s) {
     XentParams xp;
     xent_params(xp, M, K, 0, plan.shape, 0, nullptr, dev);
     xp.all_kb = (int)((n + XBK - 1) / XBK);
@@ -329,6 +334,25 @@ int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int
     return launch(xp, kXentSum, bf16, plan.shape, dev, s);
 }
 
+// A piece's rows of a 16-bit dW (n x K) = factor G^T X, `rows` deep; dW's rows lie as
+// TMA wants them.
+int launch_table(int64_t n, int64_t K, int64_t rows, const void* g, int64_t ldg, const void* X,
+                 int64_t ldx, void* dW, int64_t lddw, const float* factor, bool bf16,
+                 const DeviceInfo& dev, cudaStream_t s) {
+    const XentShape shape{2, 256};
+    XentParams xp;
+    xent_params(xp, n, K, rows, shape, 0, nullptr, dev);
+    xp.scale = factor;
+    if (!encode_tma_16(&xp.map_x, bf16, g, (uint64_t)ldg, (uint64_t)rows, (uint64_t)ldg, 0, 0, 64,
+                       XBK) ||
+        !encode_tma_16(&xp.map_w, bf16, X, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 0, 0, 64,
+                       XBK) ||
+        !encode_tma_16(&xp.map_g, bf16, dW, (uint64_t)K, (uint64_t)n, (uint64_t)lddw, 0, 0, 64,
+                       32))
+        return kCuda;
+    return launch(xp, kXentTable, bf16, shape, dev, s);
+}
+
 int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const DeviceInfo& dev,
            cudaStream_t s) {
     const int64_t units = (int64_t)xp.tiles_m * xp.tiles_n * (mode == kXentSum ? xp.splits : 1);
@@ -337,7 +361,11 @@ int launch(XentParams& xp, int mode, bool bf16, const XentShape& shape, const De
     const int rc = bf16 ? launch_xent_bf16(xp, mode, shape.cta_group, dev, s)
                         : launch_xent_f16(xp, mode, shape.cta_group, dev, s);
     dispatch_log("cross entropy %s %dx%d, %d k-blocks: %s, %d x %d tiles of %d columns",
-                 mode == kXentStats ? "logits" : mode == kXentSum ? "dX" : "gradient's logits", xp.M, xp.N, xp.num_kb,
+                 mode == kXentStats   ? "logits"
+                 : mode == kXentSum   ? "dX"
+                 : mode == kXentTable ? "dW"
+                                      : "gradient's logits",
+                 xp.M, xp.N, xp.num_kb,
                  shape.cta_group == 2 ? "CTA pairs" : "one CTA per tile", xp.tiles_m, xp.tiles_n,
                  xp.tile_n);
     return rc;
@@ -408,20 +436,20 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
     return rc;
 }
 
-// C = alpha A B^T + beta C on the dense kernel.
-int product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, int a_major,
-            const void* B, int64_t ldb, int b_major, void* C, int64_t ldc, int dtype, float beta,
-            const DeviceInfo& dev, cudaStream_t s) {
-    Problem p{M, N, K, A, lda, a_major == GEMM_MAJOR_K, B, ldb, b_major == GEMM_MAJOR_K, C, ldc,
-              dtype, EpiParams{}};
-    if (beta != 0.f) p.epi = EpiParams{1, 1.f, beta, nullptr, 0, GEMM_ACT_NONE};
+// dX's part of a piece on the dense kernel: sum (+)= G W, fp32.
+int product(int64_t M, int64_t K, int64_t n, const void* g, int64_t ldg, const void* W,
+            int64_t ldw, float* sum, int64_t lds, bool add, bool bf16, const DeviceInfo& dev,
+            cudaStream_t s) {
+    const int dtype = bf16 ? GEMM_BF16_F32 : GEMM_F16_F32;
+    Problem p{M, K, n, g, ldg, true, W, ldw, false, sum, lds, dtype, EpiParams{}};
+    if (add) p.epi = EpiParams{1, 1.f, 1.f, nullptr, 0, GEMM_ACT_NONE};
     return launch_gemm_tc(p, dev,
-                          resolve_tc_options(M, N, K, A, lda, a_major, B, ldb, b_major, C, ldc,
-                                             GEMM_MAJOR_MN, dtype),
+                          resolve_tc_options(M, K, n, g, ldg, GEMM_MAJOR_K, W, ldw, GEMM_MAJOR_MN,
+                                             sum, lds, GEMM_MAJOR_MN, dtype),
                           s);
 }
 
-// dW = beta dW + scale G^T X on the product over the rows of one group, {0, depth}
+// dW = beta dW + *scale G^T X on the product over the rows of one group, {0, depth}
 // in `limits`: it adds up fp32 sums in parts of the depth (the tensor core's cut-off
 // additions would show in an fp32 dW), and takes the factor from device memory.
 int product_rows(int64_t M, int64_t N, int64_t depth, const void* A, int64_t lda, const void* B,
@@ -465,7 +493,6 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     if (rc != kOk) return rc;
 
     const int parts = dW && we == 4 ? 2 : 1;  // numbers that hold an entry of G
-    const bool scaled = !bf16;
     const int64_t piece = xent_piece_cols(up(M, 256), N, parts);
     const XentShape shape = plan_xent(M, piece, dev->sm_count, false);  // of every piece
     const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
@@ -473,21 +500,20 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     // dX by shares of the depth where its tiles are few, else through gemm()'s kernel
     const XentSumPlan plan = plan_xent_sum(M, K, piece, dev->sm_count);
     const bool split_dx = dX && plan.splits > 1;
-    const bool sum_dx = dX && (pieces > 1 || scaled || split_dx);
     const int64_t ldg = up(piece, 256), ldk = up(K, 8);
     Parts at;
     const int64_t g_at = at.add(ldg * rows * parts * 2);
     const bool copy_x = dW || !tma_ready(X, ldx);
     const int64_t x_at = copy_x ? at.add(ldk * rows * parts * 2) : -1;
     const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * ldk * 2);
-    const int64_t dx_at = sum_dx ? at.add(plan.splits * M * up(K, 4) * 4) : -1;
-    const int64_t scale_at = scaled ? at.add(8) : -1;
+    const int64_t dx_at = dX ? at.add(plan.splits * M * up(K, 4) * 4) : -1;
+    const int64_t scale_at = at.add(8);
     const int64_t limits_at = at.add(8);
     Scratch scratch{pool, s, dev->device};
     char* mem = static_cast<char*>(scratch.get((size_t)at.bytes));
     if (!mem) return kCuda;
-    float* scale = scaled ? reinterpret_cast<float*>(mem + scale_at) : nullptr;
-    float* dx_sum = sum_dx ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
+    float* scale = reinterpret_cast<float*>(mem + scale_at);
+    float* dx_sum = dX ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
     int32_t* limits = reinterpret_cast<int32_t*>(mem + limits_at);
     char* g = mem + g_at;
 
@@ -505,11 +531,9 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
         ldxc = ldk;
     }
     if (rc == kOk && w_at >= 0) rc = repack_one(W, ldw, N, K, mem + w_at, *dev, s);
-    if (rc == kOk && scaled)
+    if (rc == kOk)
         rc = launch_dependent(xent_scale_kernel, dim3(1), dim3(1024), 0, s, (int)M, target, (int)N,
-                              dloss, alpha, scale);
-    const int f32 = bf16 ? GEMM_BF16_F32 : GEMM_F16_F32;
-    const int same = bf16 ? GEMM_BF16_BF16 : GEMM_F16_F16;
+                              dloss, alpha, bf16 ? 1.f : 4096.f, scale);
     for (int64_t v0 = 0; v0 < N && rc == kOk; v0 += piece) {
         const int64_t n = N - v0 < piece ? N - v0 : piece;
         const void* wp = static_cast<const uint16_t*>(W) + v0 * ldw;
@@ -529,24 +553,20 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
         }
         rc = launch(xp, parts == 2 ? kXentGrad2 : kXentGrad, bf16, shape, *dev, s);
         if (rc == kOk && split_dx)
-            rc = launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, bf16, *dev, s);
+            rc = launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, bf16, *dev,
+                            s);
         else if (rc == kOk && dX)
-            rc = sum_dx ? product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dx_sum,
-                                  up(K, 4), f32, v0 > 0 ? 1.f : 0.f, *dev, s)
-                        : product(M, K, n, g, ldg, GEMM_MAJOR_K, wp, ldw, GEMM_MAJOR_MN, dX, lddx,
-                                  same, 0.f, *dev, s);
+            rc = product(M, K, n, g, ldg, wp, ldw, dx_sum, up(K, 4), v0 > 0, bf16, *dev, s);
         if (rc != kOk || !dW) continue;
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
-        const int64_t depth = (int64_t)rows * parts;
-        rc = parts == 2 || scaled
-                 ? product_rows(n, K, depth, g, ldg, xc, ldxc, dst, lddw, dtype, beta,
-                                scaled ? scale + 1 : nullptr, limits, s)
-                 : product(n, K, depth, g, ldg, GEMM_MAJOR_MN, xc, ldxc, GEMM_MAJOR_MN, dst, lddw,
-                           dtype, beta, *dev, s);
+        rc = we == 2 && beta == 0.f && tma_ready(dW, lddw) && rows <= kXentTableRows
+                 ? launch_table(n, K, rows, g, ldg, xc, ldxc, dst, lddw, scale + 1, bf16, *dev, s)
+                 : product_rows(n, K, (int64_t)rows * parts, g, ldg, xc, ldxc, dst, lddw, dtype,
+                                beta, scale + 1, limits, s);
     }
-    if (rc == kOk && sum_dx)
+    if (rc == kOk && dX)
         rc = finish(dx_sum, up(K, 4), split_dx ? plan.used(piece) : 1, M, dX, lddx, M, K,
-                    scaled ? scale + 1 : nullptr, bf16, *dev, s);
+                    scale + 1, bf16, *dev, s);
     scratch.release();
     return rc;
 }

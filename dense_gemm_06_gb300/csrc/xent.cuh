@@ -10,7 +10,11 @@
 //   kSum    dX = G W where its tiles are few: the depth (the piece's columns of
 //           the vocabulary) is shared by several CTAs or pairs a tile, each of
 //           which leaves an fp32 part (1531 rows of 1037 from 50001 columns: 220 us
-//           with a CTA for each of 108 whole tiles, 100 us so).
+//           with a CTA for each of 108 whole tiles, 100 us so);
+//   kTable  a 16-bit dW = factor G^T X of few rows, the factor read from device
+//           memory, stored by TMA from the boxes that G leaves through (32000 x 2048
+//           of 300 rows: 111 us with the logits, 138 on gemm_grouped_k's kernel, whose
+//           lanes store their own 2 bytes).
 //
 // The pipeline is the dense kernel's: warp 0 copies 64-deep blocks of X and W by
 // TMA into a ring, warp 1 issues the MMAs (a CTA pair on 256 x 256 tiles, or one
@@ -43,14 +47,16 @@
 
 namespace libgemm {
 
-enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2, kXentSum = 3 };
+enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2, kXentSum = 3, kXentTable = 4 };
 
 struct XentParams {
     // kSum: X is G (rows of the piece's columns), W its rows of W read N-major, M x N
     // the rows and columns of dX, num_kb the blocks of one share of the depth.
+    // kTable: X is G read M-major, W the rows of X read N-major, M x N the rows and
+    // columns of the piece's dW, num_kb the blocks of rows.
     CUtensorMap map_x;   // M x K: boxes of 64 x 128 (one CTA a tile: x_rows) rows
     CUtensorMap map_w;   // the piece's N x K: boxes of 64 x (tile_n / CG) rows
-    CUtensorMap map_g;   // kGrad, kGrad2: G, boxes of 64 columns x 32 rows
+    CUtensorMap map_g;   // kGrad, kGrad2: G, kTable: dW, boxes of 64 columns x 32 rows
     int M, N;            // rows, and columns of this piece of the vocabulary
     int num_kb;          // 64-deep blocks of K
     int part_kb;         // blocks whose sums one accumulator takes (see kXentFold)
@@ -72,7 +78,7 @@ struct XentParams {
     int add;             // kSum: add to what `sums` holds
     const float* lse;
     const float* dloss;  // null: ones
-    const float* scale;  // null: 1; a power of two that keeps fp16 numbers in range
+    const float* scale;  // a factor on alpha, or null
     float alpha;
     ErrWord* err;
     ErrWord gen;
@@ -294,8 +300,14 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                 const uint32_t at = base + stage * stage_bytes;
                 if (xent_elect()) {
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), bytes);
-                    tma_load_2d<CG>(at, &p.map_x, fb, (kb0 + kb) * XBK, x_row);
-                    if constexpr (MODE == kXentSum) {
+                    if constexpr (MODE == kXentTable) {
+                        for (int j = 0; j < XROWS / 64; ++j)  // boxes of 64 rows of dW
+                            tma_load_2d<CG>(at + j * 64 * XBK * 2, &p.map_x, fb, x_row + 64 * j,
+                                            kb * XBK);
+                    } else {
+                        tma_load_2d<CG>(at, &p.map_x, fb, (kb0 + kb) * XBK, x_row);
+                    }
+                    if constexpr (MODE == kXentSum || MODE == kXentTable) {
                         for (int j = 0; j < b_rows / 64; ++j)  // boxes of 64 columns
                             tma_load_2d<CG>(at + x_bytes + j * 64 * XBK * 2, &p.map_w, fb,
                                             w_row + 64 * j, (kb0 + kb) * XBK);
@@ -317,12 +329,14 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         // ---------------------------------------------------- MMA issuer --
         give_registers();
         if (rank == 0) {
-            // W is K-major, 32 bytes a step of 16 deep, or (kSum) N-major, 16 rows of 128
-            constexpr bool W_MN = MODE == kXentSum;
+            // X and W are K-major, 32 bytes a step of 16 deep, or (W of kSum, both of
+            // kTable) M- or N-major, 16 rows of 128
+            constexpr bool X_MN = MODE == kXentTable, W_MN = MODE == kXentSum || X_MN;
+            constexpr uint64_t X_STEP = X_MN ? 16 * 128 >> 4 : 32 >> 4;
             constexpr uint64_t W_STEP = W_MN ? 16 * 128 >> 4 : 32 >> 4;
-            const uint32_t idesc = make_idesc_f16(BF16, false, W_MN, (uint32_t)(XROWS * CG),
+            const uint32_t idesc = make_idesc_f16(BF16, X_MN, W_MN, (uint32_t)(XROWS * CG),
                                                   (uint32_t)p.tile_n);
-            const uint64_t x_desc0 = make_sdesc_sw128(base, 16, 1024);
+            const uint64_t x_desc0 = make_sdesc_sw128(base, X_MN ? 64 * XBK * 2 : 16, 1024);
             const uint64_t w_desc0 =
                 make_sdesc_sw128(base + x_bytes, W_MN ? 64 * XBK * 2 : 16, 1024);
             int stage = 0, acc = 0;
@@ -343,8 +357,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                         if (xent_elect()) {
 #pragma unroll
                             for (int j = 0; j < XBK / 16; ++j)
-                                mma_f16<CG>(d, xd + (uint64_t)(2 * j), wd + W_STEP * (uint64_t)j, idesc,
-                                            j > 0 ? 1u : add);
+                                mma_f16<CG>(d, xd + X_STEP * (uint64_t)j,
+                                            wd + W_STEP * (uint64_t)j, idesc, j > 0 ? 1u : add);
                             mma_commit<CG>(empty_bar(stage));
                         }
                         __syncwarp();
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             const int row = row0 + lane;
             int target = -1;
             float lse2 = 0.f, d = 0.f;
-            if (MODE != kXentSum && row < p.M) {
+            if (MODE != kXentSum && MODE != kXentTable && row < p.M) {
                 const int v = p.target[row];
                 if (v >= 0 && v < p.vocab) target = v;
                 if (v >= p.vocab) report_bad_value(p.err);
@@ -411,7 +425,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                     }
                 }
             }
-            const bool counts = target >= 0;
+            const bool counts = target >= 0 || MODE == kXentTable;
             const int rel = target - p.col0;  // the target's column in this piece
             // the parts of the depth before the last, added up
             const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -459,7 +473,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                     for (int i = 0; i < 32; ++i)
                         v[i] = __float_as_uint(parts[j * 64 + h * 32 + i] + __uint_as_float(v[i]));
                     const int first = col + h * 32;
-                    const int at = counts && rel < end ? rel - first : -1;  // the target's place in v
+                    // the target's place in v
+                    const int at = target >= 0 && rel < end ? rel - first : -1;
                     if constexpr (MODE == kXentSum) {
                         if (row < p.M) {
                             float* to = p.sums + (split * p.sum_rows + row) * p.sum_ld + first;
@@ -508,8 +523,10 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                         float g[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            g[i] = d * ex2(fmaf(__uint_as_float(v[i]), kLog2e, -lse2));
-                        if ((unsigned)at < 32u) {
+                            g[i] = MODE == kXentTable
+                                       ? alpha * __uint_as_float(v[i])
+                                       : d * ex2(fmaf(__uint_as_float(v[i]), kLog2e, -lse2));
+                        if (MODE != kXentTable && (unsigned)at < 32u) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (i == at)
@@ -547,7 +564,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                         if (h == 1) {
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) {
+                            // (G has room for whole tiles, dW has not)
+                            if (lane == 0 && (MODE != kXentTable || (row0 < p.M && col < p.N))) {
                                 tma_store_2d(&p.map_g, staging, col, row0);
                                 if constexpr (MODE == kXentGrad2)
                                     tma_store_2d(&p.map_g, staging + 32 * 128, col,
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             release(acc);
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if ((MODE == kXentGrad || MODE == kXentGrad2) && lane == 0) bulk_wait_all();
+        if (MODE != kXentStats && MODE != kXentSum && lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
         give_registers();
@@ -644,6 +662,7 @@ int launch_xent(XentParams& xp, int mode, int cg, const DeviceInfo& dev, cudaStr
     if (mode == kXentGrad2)
         return cg == 2 ? launch_xent_variant<kXentGrad2, 2, BF16>(xp, dev, s)
                        : launch_xent_variant<kXentGrad2, 1, BF16>(xp, dev, s);
+    if (mode == kXentTable) return launch_xent_variant<kXentTable, 2, BF16>(xp, dev, s);
     return cg == 2 ? launch_xent_variant<kXentSum, 2, BF16>(xp, dev, s)
                    : launch_xent_variant<kXentSum, 1, BF16>(xp, dev, s);
 }

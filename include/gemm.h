@@ -404,15 +404,14 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  *
  * The logits are computed again, a piece of the vocabulary at a time. G is held as
  * 16-bit numbers, for an fp32 dW as two that leave 2^-17 (bf16) or 2^-22 (fp16) of
- * it; fp16 numbers are scaled by a power of two that brings the largest
- * |alpha * dloss[t]| into [2^12, 2^13), so that G reaches down to 2^-36 of that.
- * Probabilities below 2^-126 count as zero.
+ * it, divided by the largest |alpha * dloss[t]| (fp16: 2^-12 of that, so that G
+ * reaches down to 2^-36 of it), which is put back in fp32: a factor that all rows
+ * share is not rounded. Probabilities below 2^-126 count as zero.
  * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, or
- * 4096 columns), a copy of X (two for an fp32 dW), and one or a few fp32 dX where
- * the vocabulary takes more than one piece, the type is fp16 or dX is small. An fp32
- * dW with beta = 1 is added to as gemm_grouped_k's C. With M zero dW = beta * dW; K
- * zero is a no-op. K is at most 2^20 (more: GEMM_ERR_UNSUPPORTED). Otherwise as
- * gemm_xent.
+ * 4096 columns), a copy of X (two for an fp32 dW), and an fp32 dX (a few where dX is
+ * small). An fp32 dW with beta = 1 is added to as gemm_grouped_k's C. With M zero
+ * dW = beta * dW; K zero is a no-op. K is at most 2^20 (more: GEMM_ERR_UNSUPPORTED).
+ * Otherwise as gemm_xent.
  */
 int gemm_xent_grad(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                    const void *W, int64_t ldw, const int32_t *target, const float *lse,

@@ -116,6 +116,16 @@ def test_formula(T, E, top, dtype):
     compare(T, E, top, dtype)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,E,top", [
+    # one block, one cluster, several: 32 rows of a block at a time, 8 where E > 256
+    (64, 64, 6), (65, 64, 6), (512, 160, 6), (513, 160, 6), (16, 300, 3), (17, 300, 3),
+    (128, 1000, 4), (129, 1000, 4), (4000, 1022, 5), (20000, 256, 8),
+])
+def test_blocks_and_clusters(T, E, top, dtype):
+    compare(T, E, top, dtype)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, H32])
 @pytest.mark.parametrize("pads,shifts", [((1, 0), (0, 0)), ((0, 3), (1, 0)), ((5, 2), (3, 1))])
 def test_pitches(pads, shifts, dtype):

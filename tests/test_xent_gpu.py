@@ -172,6 +172,39 @@ def test_small_and_large_gradients(dtype, alpha):
     compare(150, 600, 64, dtype, alpha=alpha)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M", [64, 1536])  # dW on either of its kernels
+def test_a_common_factor_leaves_no_bias(M, dtype):
+    """A mean over 3 M tokens: 1 / (3 M) rounded to 16 bits is off by as much as half a
+    step (bf16 2^-9, fp16 2^-12), in every term alike. The projection of the result on
+    the formula's averages the independent roundings of K M = 32768 numbers and more
+    (half a step of bf16 each, 2^-8: below 2^-8 / sqrt(3 * 32768) = 1.3e-5 of standard
+    deviation), so 2^-13 is nine of them.
+
+    To that comes what the target's own entry leaves: it is 1 - p of the factor, and
+    rounds to 1, p off, where p is below half a step under 1 (bf16 2^-9, fp16 2^-12),
+    else it is at most that half step off. For small p these have one sign and do not
+    average out: the mean over the rows of min(p, half a step), twice for rows whose
+    other terms are not small beside it. The factor's own rounding would be 2^-9
+    (bf16), of which that mean has to stay well below."""
+    N, K = 5000, 512
+    X, W, target, _ = inputs(M, N, K, dtype, out=0.0)
+    dloss = torch.full((M,), 1.0 / (3 * M), device="cuda")
+    _, lse = forward(X, W, target, dtype)
+    e = Exact(X, W, target, dloss, 1.0, lse)
+    dX, dW = backward(X, W, target, lse, dloss, dtype)
+    left = float(torch.exp(-e.loss).clamp(max=torch.finfo(IN[dtype]).eps / 4).mean())
+    assert dtype not in (BF, BF32) or 2.0 ** -13 + 2 * left < 2.0 ** -10
+    for got, (ref, _) in zip((dX, dW), e.grads(dtype, parts_of(dtype))):
+        off = (got.double() * ref).sum() / ref.square().sum() - 1
+        assert abs(float(off)) < 2.0 ** -13 + 2 * left
+    check()
+
+
+def test_a_16_bit_table_in_pieces():
+    compare(640, 430001, 24, BF)  # two pieces: G of 2^28 numbers is 419430 columns
+
+
 @pytest.mark.parametrize("dtype", [BF32, H16])
 def test_large_logits(dtype):
     compare(200, 700, 256, dtype, scale=60.0)  # logits of hundreds: exp alone would overflow
