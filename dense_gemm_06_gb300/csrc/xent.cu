@@ -30,8 +30,12 @@
 // That costs the scale's launch and dX an fp32 pass (4096 x 32000 x 2048: 14 of
 // 1310 us).
 //
-// Rows whose target does not count are zero in G, and zero in the copy of X that
-// dW is multiplied from (0 times an infinity would be NaN).
+// Rows whose target does not count (prompts, padding) take no part: a first kernel
+// lists the others, which are copied side by side, and G's kernel, dW's product and
+// the shared dX work on as many tiles as these fill, a number that stays on the device
+// (1531 rows of 1037, fp16, vocabulary 50001, 918 of them counting: 490 us with the
+// forward pass, 557 with all of them). The last tile's rows past them are zero in G and
+// in the copy of X (0 times an infinity would be NaN).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -118,28 +122,86 @@ __global__ void xent_uniform_kernel(int M, int vocab, const int32_t* target, flo
     }
 }
 
-// The rows of X that count, in rows of TMA's alignment; the others, and those
-// from M to `rows`, zero. With copies == 2 the same again below. A warp per row.
-// limits: {0, rows * copies}, the depth of dW's product.
-__global__ void __launch_bounds__(256)
-    xent_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, int M, int64_t K,
-                     const int32_t* __restrict__ target, int vocab, uint16_t* __restrict__ out,
-                     int64_t ldo, int rows, int copies, int32_t* __restrict__ limits) {
+// One block: the rows of a gradient that count, in their order (order[j], and place[t]
+// the j of row t or -1); scale[0]: what brings the largest finite |alpha dloss_t| of
+// them to `to`; scale[1]: its inverse.
+__global__ void __launch_bounds__(1024)
+    xent_order_kernel(int M, const int32_t* __restrict__ target, int vocab,
+                      const float* __restrict__ dloss, float alpha, float to, int tile, int copies,
+                      int32_t* __restrict__ order, int32_t* __restrict__ place,
+                      XentInfo* __restrict__ info, float* __restrict__ scale, ErrWord* err) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        limits[0] = 0;
-        limits[1] = rows * copies;
+    constexpr int PER = 8;  // rows of a thread
+    __shared__ float most[32];
+    __shared__ int found[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float top = 0.f;
+    int count = 0;
+    for (int base = 0; base < M; base += 1024 * PER) {
+        const int t0 = base + threadIdx.x * PER;
+        int v[PER];
+        uint32_t kept = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = t0 + i < M ? target[t0 + i] : -1;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (v[i] >= vocab) report_bad_value(err);
+            if (v[i] < 0 || v[i] >= vocab) continue;
+            kept |= 1u << i;
+            const float d = fabsf(dloss ? alpha * dloss[t0 + i] : alpha);
+            if (d < INFINITY) top = fmaxf(top, d);
+        }
+        int upto = __popc(kept);
+        for (int o = 1; o < 32; o *= 2) {
+            const int n = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += n;
+        }
+        if (lane == 31) found[warp] = upto;
+        __syncthreads();
+        const int n = found[lane];
+        int j = count + upto - __popc(kept) +
+                __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+        count += __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (t0 + i >= M) continue;
+            const bool in = kept >> i & 1;
+            place[t0 + i] = in ? j : -1;
+            if (in) order[j++] = t0 + i;
+        }
+        __syncthreads();
     }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) most[warp] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, most[i]);
+    if (top == 0.f) top = to;
+    top = fminf(fmaxf(top, 0x1p-100f), 0x1p100f);
+    scale[0] = to / top;
+    scale[1] = top / to;
+    const int used = count > 0 ? (count + tile - 1) / tile * tile : tile;
+    *info = XentInfo{{0, used * copies}, count, used};
+}
+
+// The rows of X that count, one after the other in rows of TMA's alignment, then zeros
+// up to whole tiles; with copies == 2 the same again below. A warp per row.
+__global__ void __launch_bounds__(256)
+    xent_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t K,
+                     const int32_t* __restrict__ order, const XentInfo* __restrict__ info,
+                     uint16_t* __restrict__ out, int64_t ldo, int copies) {
+    gemm_ptx::pdl_launch_dependents();
+    gemm_ptx::pdl_wait();
+    const int count = info->count, used = info->used;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
     for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-         r < (int64_t)rows * copies; r += warps) {
-        const int64_t t = r % rows;
+         r < (int64_t)used * copies; r += warps) {
+        const int j = (int)(r < used ? r : r - used);
         uint16_t* dst = out + r * ldo;
-        const int v = t < M ? target[t] : -1;
-        if (v >= 0 && v < vocab) {
-            repack16_row(X + t * ldx, dst, K, lane);
+        if (j < count) {
+            repack16_row(X + order[j] * ldx, dst, K, lane);
             for (int64_t c = K + lane; c < ldo; c += 32) dst[c] = 0;
         } else {
             for (int64_t c = lane * 8; c < ldo; c += 256)
@@ -148,40 +210,14 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// scale[0]: what brings the largest finite |alpha dloss_t| of the rows that count to
-// `top`; scale[1]: its inverse. One block.
-__global__ void __launch_bounds__(1024)
-    xent_scale_kernel(int M, const int32_t* __restrict__ target, int vocab,
-                      const float* __restrict__ dloss, float alpha, float to,
-                      float* __restrict__ scale) {
-    gemm_ptx::pdl_launch_dependents();
-    gemm_ptx::pdl_wait();
-    __shared__ float most[32];
-    float top = 0.f;
-    for (int r = threadIdx.x; r < M; r += blockDim.x) {
-        const int t = target[r];
-        const float d = fabsf(dloss ? alpha * dloss[r] : alpha);
-        if (t >= 0 && t < vocab && d < INFINITY) top = fmaxf(top, d);
-    }
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = top;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, most[i]);
-    if (top == 0.f) top = to;
-    top = fminf(fmaxf(top, 0x1p-100f), 0x1p100f);
-    scale[0] = to / top;
-    scale[1] = top / to;
-}
-
-// dX = *scale * (the sum of `parts` matrices, part_rows rows apart), rounded once;
-// rows x cols. A warp takes 32 groups of 8 columns of two rows at a time, and stores
+// Row t of dX = *scale * (the sum of row place[t] of `parts` matrices, part_rows rows
+// apart), rounded once, or zero; rows x cols. A warp takes 32 groups of 8 columns of two rows at a time, and stores
 // them in 16-byte pieces whatever dX's alignment.
 template <typename T>
 __global__ void __launch_bounds__(256)
     xent_finish_kernel(const float* __restrict__ sum, int64_t lds, int parts, int64_t part_rows,
                        T* __restrict__ out, int64_t ldo, int64_t rows, int cols,
-                       const float* __restrict__ scale) {
+                       const int32_t* __restrict__ place, const float* __restrict__ scale) {
     gemm_ptx::pdl_launch_dependents();
     gemm_ptx::pdl_wait();
     constexpr int ROWS = 2, G = 8;
@@ -191,14 +227,18 @@ __global__ void __launch_bounds__(256)
     for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS; r0 < rows;
          r0 += warps * ROWS) {
         float v[ROWS][G] = {};
-        const float* from = sum + r0 * lds + c;
+        int at[ROWS];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) at[j] = r0 + j < rows ? place[r0 + j] : -1;
+        const float* from = sum + c;
         for (int p = 0; p < parts; ++p, from += part_rows * lds)
 #pragma unroll
             for (int j = 0; j < ROWS; ++j)
 #pragma unroll
                 for (int q = 0; q < G; q += 4) {
-                    if (r0 + j >= rows || c + q >= lds) continue;  // lds % 4 == 0
-                    const float4 f = *reinterpret_cast<const float4*>(from + j * lds + q);
+                    if (at[j] < 0 || c + q >= lds) continue;  // lds % 4 == 0
+                    const float4 f =
+                        *reinterpret_cast<const float4*>(from + (int64_t)at[j] * lds + q);
                     v[j][q] += f.x, v[j][q + 1] += f.y, v[j][q + 2] += f.z, v[j][q + 3] += f.w;
                 }
 #pragma unroll
@@ -212,15 +252,15 @@ __global__ void __launch_bounds__(256)
 }
 
 int finish(const float* sum, int64_t lds, int parts, int64_t part_rows, void* out, int64_t ldo,
-           int64_t rows, int64_t cols, const float* scale, bool bf16, const DeviceInfo& dev,
-           cudaStream_t s) {
+           int64_t rows, int64_t cols, const int32_t* place, const float* scale, bool bf16,
+           const DeviceInfo& dev, cudaStream_t s) {
     const int64_t across = (cols + 255) / 256;  // warps for a row
     const int64_t turns = (rows + 15) / 16, most = (dev.sm_count * 8 + across - 1) / across;
     const dim3 grid((unsigned)(turns < most ? turns : most), (unsigned)across);
     auto run = [&](auto t) {
         using T = decltype(t);
         return launch_dependent(xent_finish_kernel<T>, grid, dim3(256), 0, s, sum, lds, parts,
-                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, scale);
+                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, place, scale);
     };
     return bf16 ? run(__nv_bfloat16{}) : run(__half{});
 }
@@ -316,7 +356,8 @@ bool xent_maps(XentParams& xp, bool bf16, const void* X, int64_t ldx, const void
 // shares of the depth that are the same for every piece: sums (+)= G W.
 int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int64_t n,
                const void* g, int64_t ldg, const void* W, int64_t ldw, float* sums,
-               int64_t sum_rows, bool add, bool bf16, const DeviceInfo& dev, cudaStream_t s) {
+               int64_t sum_rows, bool add, const XentInfo* info, bool bf16,
+               const DeviceInfo& dev, cudaStream_t s) {
     XentParams xp;
     xent_params(xp, M, K, 0, plan.shape, 0, nullptr, dev);
     xp.all_kb = (int)((n + XBK - 1) / XBK);
@@ -327,6 +368,7 @@ int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int
     xp.sum_ld = up(K, 4);
     xp.sum_rows = sum_rows;
     xp.add = add ? 1 : 0;
+    xp.info = info;
     if (!encode_tma_16(&xp.map_x, bf16, g, (uint64_t)n, (uint64_t)M, (uint64_t)ldg, 0, 0, XBK,
                        plan.shape.cta_group == 2 ? XROWS : (uint32_t)xp.x_rows) ||
         !encode_tma_16(&xp.map_w, bf16, W, (uint64_t)K, (uint64_t)n, (uint64_t)ldw, 0, 0, 64, XBK))
@@ -337,12 +379,13 @@ int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int
 // A piece's rows of a 16-bit dW (n x K) = factor G^T X, `rows` deep; dW's rows lie as
 // TMA wants them.
 int launch_table(int64_t n, int64_t K, int64_t rows, const void* g, int64_t ldg, const void* X,
-                 int64_t ldx, void* dW, int64_t lddw, const float* factor, bool bf16,
-                 const DeviceInfo& dev, cudaStream_t s) {
+                 int64_t ldx, void* dW, int64_t lddw, const float* factor, const XentInfo* info,
+                 bool bf16, const DeviceInfo& dev, cudaStream_t s) {
     const XentShape shape{2, 256};
     XentParams xp;
     xent_params(xp, n, K, rows, shape, 0, nullptr, dev);
     xp.scale = factor;
+    xp.info = info;
     if (!encode_tma_16(&xp.map_x, bf16, g, (uint64_t)ldg, (uint64_t)rows, (uint64_t)ldg, 0, 0, 64,
                        XBK) ||
         !encode_tma_16(&xp.map_w, bf16, X, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 0, 0, 64,
@@ -436,7 +479,9 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
     return rc;
 }
 
-// dX's part of a piece on the dense kernel: sum (+)= G W, fp32.
+// dX's part of a piece on the dense kernel: sum (+)= G W, fp32, of all M rows: those
+// past the ones that count hold anything, and nothing reads their sums. (launch_sum
+// would leave them out, but adds up in parts: 298 us and 307, 4096 x 2048 from 32000.)
 int product(int64_t M, int64_t K, int64_t n, const void* g, int64_t ldg, const void* W,
             int64_t ldw, float* sum, int64_t lds, bool add, bool bf16, const DeviceInfo& dev,
             cudaStream_t s) {
@@ -499,74 +544,70 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const int64_t pieces = (N + piece - 1) / piece;
     // dX by shares of the depth where its tiles are few, else through gemm()'s kernel
     const XentSumPlan plan = plan_xent_sum(M, K, piece, dev->sm_count);
-    const bool split_dx = dX && plan.splits > 1;
     const int64_t ldg = up(piece, 256), ldk = up(K, 8);
     Parts at;
     const int64_t g_at = at.add(ldg * rows * parts * 2);
-    const bool copy_x = dW || !tma_ready(X, ldx);
-    const int64_t x_at = copy_x ? at.add(ldk * rows * parts * 2) : -1;
+    const int64_t x_at = at.add(ldk * rows * parts * 2);
     const int64_t w_at = tma_ready(W, ldw) ? -1 : at.add(N * ldk * 2);
     const int64_t dx_at = dX ? at.add(plan.splits * M * up(K, 4) * 4) : -1;
-    const int64_t scale_at = at.add(8);
-    const int64_t limits_at = at.add(8);
+    const int64_t order_at = at.add(M * 4), place_at = at.add(M * 4);
+    const int64_t scale_at = at.add(8), info_at = at.add(sizeof(XentInfo));
     Scratch scratch{pool, s, dev->device};
     char* mem = static_cast<char*>(scratch.get((size_t)at.bytes));
     if (!mem) return kCuda;
-    float* scale = reinterpret_cast<float*>(mem + scale_at);
     float* dx_sum = dX ? reinterpret_cast<float*>(mem + dx_at) : nullptr;
-    int32_t* limits = reinterpret_cast<int32_t*>(mem + limits_at);
-    char* g = mem + g_at;
+    int32_t* order = reinterpret_cast<int32_t*>(mem + order_at);
+    int32_t* place = reinterpret_cast<int32_t*>(mem + place_at);
+    float* scale = reinterpret_cast<float*>(mem + scale_at);
+    XentInfo* info = reinterpret_cast<XentInfo*>(mem + info_at);
+    char *g = mem + g_at, *xc = mem + x_at;
 
-    const void* xc = X;  // rows that count, aligned
-    int64_t ldxc = ldx;
-    if (copy_x) {
-        const int64_t blocks = ((int64_t)rows * parts + 7) / 8;
-        rc = launch_dependent(xent_rows_kernel,
-                              dim3((unsigned)(blocks < dev->sm_count * 8 ? blocks
-                                                                         : dev->sm_count * 8)),
-                              dim3(256), 0, s, static_cast<const uint16_t*>(X), ldx, (int)M, K,
-                              target, (int)N, reinterpret_cast<uint16_t*>(mem + x_at), ldk, rows,
-                              parts, limits);
-        xc = mem + x_at;
-        ldxc = ldk;
+    rc = launch_dependent(xent_order_kernel, dim3(1), dim3(1024), 0, s, (int)M, target, (int)N,
+                          dloss, alpha, bf16 ? 1.f : 4096.f, XROWS * shape.cta_group, parts, order,
+                          place, info, scale, dev->err_word);
+    if (rc == kOk) {
+        const int64_t blocks = ((int64_t)rows * parts + 7) / 8, most = dev->sm_count * 8;
+        rc = launch_dependent(xent_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                              dim3(256), 0, s, static_cast<const uint16_t*>(X), ldx, K,
+                              (const int32_t*)order, (const XentInfo*)info,
+                              reinterpret_cast<uint16_t*>(xc), ldk, parts);
     }
     if (rc == kOk && w_at >= 0) rc = repack_one(W, ldw, N, K, mem + w_at, *dev, s);
-    if (rc == kOk)
-        rc = launch_dependent(xent_scale_kernel, dim3(1), dim3(1024), 0, s, (int)M, target, (int)N,
-                              dloss, alpha, bf16 ? 1.f : 4096.f, scale);
     for (int64_t v0 = 0; v0 < N && rc == kOk; v0 += piece) {
         const int64_t n = N - v0 < piece ? N - v0 : piece;
         const void* wp = static_cast<const uint16_t*>(W) + v0 * ldw;
         XentParams xp;
         xent_params(xp, M, n, K, shape, N, target, *dev);
         xp.col0 = (int)v0;
-        xp.lo_row = rows;
+        xp.order = order;
+        xp.info = info;
         xp.lse = lse;
         xp.dloss = dloss;
         xp.alpha = alpha;
         xp.scale = scale;
-        if (!xent_maps(xp, bf16, xc, ldxc, wp, ldw, K, shape) ||
+        if (!xent_maps(xp, bf16, xc, ldk, wp, ldw, K, shape) ||
             !encode_tma_16(&xp.map_g, bf16, g, (uint64_t)ldg, (uint64_t)rows * parts,
                            (uint64_t)ldg, 0, 0, 64, 32)) {
             rc = kCuda;
             break;
         }
         rc = launch(xp, parts == 2 ? kXentGrad2 : kXentGrad, bf16, shape, *dev, s);
-        if (rc == kOk && split_dx)
-            rc = launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, bf16, *dev,
-                            s);
-        else if (rc == kOk && dX)
-            rc = product(M, K, n, g, ldg, wp, ldw, dx_sum, up(K, 4), v0 > 0, bf16, *dev, s);
+        if (rc == kOk && dX)
+            rc = plan.splits > 1
+                     ? launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, info,
+                                  bf16, *dev, s)
+                     : product(M, K, n, g, ldg, wp, ldw, dx_sum, up(K, 4), v0 > 0, bf16, *dev, s);
         if (rc != kOk || !dW) continue;
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
         rc = we == 2 && beta == 0.f && tma_ready(dW, lddw) && rows <= kXentTableRows
-                 ? launch_table(n, K, rows, g, ldg, xc, ldxc, dst, lddw, scale + 1, bf16, *dev, s)
-                 : product_rows(n, K, (int64_t)rows * parts, g, ldg, xc, ldxc, dst, lddw, dtype,
-                                beta, scale + 1, limits, s);
+                 ? launch_table(n, K, rows, g, ldg, xc, ldk, dst, lddw, scale + 1, info, bf16,
+                                *dev, s)
+                 : product_rows(n, K, (int64_t)rows * parts, g, ldg, xc, ldk, dst, lddw, dtype,
+                                beta, scale + 1, info->limits, s);
     }
     if (rc == kOk && dX)
-        rc = finish(dx_sum, up(K, 4), split_dx ? plan.used(piece) : 1, M, dX, lddx, M, K,
-                    scale + 1, bf16, *dev, s);
+        rc = finish(dx_sum, up(K, 4), plan.used(piece), M, dX, lddx, M, K, place, scale + 1, bf16,
+                    *dev, s);
     scratch.release();
     return rc;
 }

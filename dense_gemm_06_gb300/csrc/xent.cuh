@@ -49,6 +49,14 @@ namespace libgemm {
 
 enum XentMode { kXentStats = 0, kXentGrad = 1, kXentGrad2 = 2, kXentSum = 3, kXentTable = 4 };
 
+// The rows of a gradient that count, found on the device.
+struct XentInfo {
+    int32_t limits[2];  // of dW's depth: 0, and the rows in use of all copies of X
+    int32_t count;      // rows that count
+    int32_t used;       // the same in whole tiles, one at least: the second copies of X
+                        // and G begin there
+};
+
 struct XentParams {
     // kSum: X is G (rows of the piece's columns), W its rows of W read N-major, M x N
     // the rows and columns of dX, num_kb the blocks of one share of the depth.
@@ -67,8 +75,11 @@ struct XentParams {
     int band;            // tile rows of a raster band
     int col0;            // the piece's first vocabulary number
     int vocab;           // the whole vocabulary: targets at or past it do not count
-    int lo_row;          // kGrad2: the row of G where the second numbers begin
     const int32_t* target;
+    // All but kStats: only the rows that count take part, side by side. The kernel's row
+    // j is row order[j] of the caller's; `info` says how many.
+    const int32_t* order;
+    const XentInfo* info;
     float2* part;        // kStats: (maximum, sum) of each row, half tile by half tile
     int64_t part_ld;     // rows of a half tile in `part`
     float* picked;       // kStats: each row's target logit
@@ -210,15 +221,32 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Tiles in raster order: bands of `band` tile rows, column after column, every
 // other band backwards, so that the tiles running at one time share X and W in L2.
-__device__ __forceinline__ int2 xent_tile(int t, const XentParams& p) {
+__device__ __forceinline__ int2 xent_tile(int t, int tiles_m, const XentParams& p) {
     const int band_tiles = p.band * p.tiles_n;
     const int band = t / band_tiles;
     const int within = t - band * band_tiles;
-    const int rows = min(p.band, p.tiles_m - band * p.band);
+    const int rows = min(p.band, tiles_m - band * p.band);
     int tn = within / rows;
     const int tm = band * p.band + (within - tn * rows);
     if (band & 1) tn = p.tiles_n - 1 - tn;
     return make_int2(tm, tn);
+}
+
+// What there is to do. All but kStats read it from the device: after pdl_wait().
+struct XentWork {
+    int tiles_m, tiles, total, num_kb;
+};
+template <int MODE, int CG>
+__device__ __forceinline__ XentWork xent_work(const XentParams& p) {
+    XentWork w{p.tiles_m, 0, 0, p.num_kb};
+    if constexpr (MODE != kXentStats) {
+        const int used = p.info->used;
+        if constexpr (MODE == kXentTable) w.num_kb = used / XBK;
+        else w.tiles_m = min(p.tiles_m, (used + XROWS * CG - 1) / (XROWS * CG));
+    }
+    w.tiles = w.tiles_m * p.tiles_n;
+    w.total = MODE == kXentSum ? w.tiles * p.splits : w.tiles;
+    return w;
 }
 
 template <int MODE, int CG, bool BF16>
@@ -247,12 +275,10 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
     const int cluster = CG == 2 ? (int)cluster_id_x() : (int)blockIdx.x;
     const int nclusters = CG == 2 ? (int)num_clusters_x() : (int)gridDim.x;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int total = MODE == kXentSum ? tiles * p.splits : tiles;
     constexpr int ACC_COLS = CG == 2 ? 256 : 128;  // TMEM columns of an accumulator
     // depth blocks of a unit (kSum: the last share may be shorter)
-    auto blocks_of = [&](int split) {
-        return MODE == kXentSum ? min(p.num_kb, p.all_kb - split * p.num_kb) : p.num_kb;
+    auto blocks_of = [&](int split, const XentWork& w) {
+        return MODE == kXentSum ? min(p.num_kb, p.all_kb - split * p.num_kb) : w.num_kb;
     };
 
     if (threadIdx.x == 0) {
@@ -284,16 +310,17 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         // ------------------------------------------------ TMA producer --
         give_registers();
         pdl_wait();
+        const XentWork work = xent_work<MODE, CG>(p);
         int stage = 0;
         uint32_t phase = 0;
         const int b_rows = p.tile_n / CG;
         const uint32_t bytes = (uint32_t)(CG * (x_bytes + b_rows * XBK * 2));
-        for (int t = cluster; t < total && !aborted; t += nclusters) {
-            const int split = MODE == kXentSum ? t / tiles : 0;
-            const int2 tile = xent_tile(MODE == kXentSum ? t - split * tiles : t, p);
+        for (int t = cluster; t < work.total && !aborted; t += nclusters) {
+            const int split = MODE == kXentSum ? t / work.tiles : 0;
+            const int2 tile = xent_tile(t - split * work.tiles, work.tiles_m, p);
             const int x_row = (tile.x * CG + (int)rank) * XROWS;
             const int w_row = tile.y * p.tile_n + (int)rank * b_rows;
-            const int kb0 = split * p.num_kb, kbs = blocks_of(split);
+            const int kb0 = split * p.num_kb, kbs = blocks_of(split, work);
             for (int kb = 0; kb < kbs; ++kb) {
                 if (!xent_wait(empty_bar(stage), phase ^ 1u, p)) { aborted = true; break; }
                 const uint32_t fb = CG == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
@@ -329,6 +356,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         // ---------------------------------------------------- MMA issuer --
         give_registers();
         if (rank == 0) {
+            if constexpr (MODE != kXentStats) pdl_wait();
+            const XentWork work = xent_work<MODE, CG>(p);
             // X and W are K-major, 32 bytes a step of 16 deep, or (W of kSum, both of
             // kTable) M- or N-major, 16 rows of 128
             constexpr bool X_MN = MODE == kXentTable, W_MN = MODE == kXentSum || X_MN;
@@ -341,8 +370,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                 make_sdesc_sw128(base + x_bytes, W_MN ? 64 * XBK * 2 : 16, 1024);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            for (int t = cluster; t < total && !aborted; t += nclusters) {
-                const int kbs = blocks_of(MODE == kXentSum ? t / tiles : 0);
+            for (int t = cluster; t < work.total && !aborted; t += nclusters) {
+                const int kbs = blocks_of(MODE == kXentSum ? t / work.tiles : 0, work);
                 for (int kb = 0; kb < kbs && !aborted;) {
                     if (!xent_wait(acce_bar(acc), acc_phase ^ 1u, p)) { aborted = true; break; }
                     tc_fence_after_sync();
@@ -403,26 +432,30 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
             }
         };
         pdl_wait();
+        const XentWork work = xent_work<MODE, CG>(p);
         float alpha = p.alpha;
         if (MODE != kXentStats && p.scale) alpha *= *p.scale;
         if (p.fault_inject == 1 && !xent_wait_inline(never_bar, 0u, p)) aborted = true;
-        for (int t = cluster; t < total && !aborted; t += nclusters) {
-            const int split = MODE == kXentSum ? t / tiles : 0;
-            const int2 tile = xent_tile(MODE == kXentSum ? t - split * tiles : t, p);
-            const int kbs = blocks_of(split);
+        for (int t = cluster; t < work.total && !aborted; t += nclusters) {
+            const int split = MODE == kXentSum ? t / work.tiles : 0;
+            const int2 tile = xent_tile(t - split * work.tiles, work.tiles_m, p);
+            const int kbs = blocks_of(split, work);
             const int row0 = (tile.x * CG + (int)rank) * XROWS + q * 32;
             const int row = row0 + lane;
             int target = -1;
             float lse2 = 0.f, d = 0.f;
-            if (MODE != kXentSum && MODE != kXentTable && row < p.M) {
-                const int v = p.target[row];
-                if (v >= 0 && v < p.vocab) target = v;
-                if (v >= p.vocab) report_bad_value(p.err);
-                if constexpr (MODE != kXentStats) {
-                    if (target >= 0) {
-                        lse2 = p.lse[row] * kLog2e;
-                        d = p.dloss ? alpha * p.dloss[row] : alpha;
-                    }
+            if constexpr (MODE == kXentStats) {
+                if (row < p.M) {
+                    const int v = p.target[row];
+                    if (v >= 0 && v < p.vocab) target = v;
+                    if (v >= p.vocab) report_bad_value(p.err);
+                }
+            } else if constexpr (MODE != kXentSum && MODE != kXentTable) {
+                if (row < p.info->count) {
+                    const int from = p.order[row];
+                    target = p.target[from];
+                    lse2 = p.lse[from] * kLog2e;
+                    d = p.dloss ? alpha * p.dloss[from] : alpha;
                 }
             }
             const bool counts = target >= 0 || MODE == kXentTable;
@@ -569,7 +602,7 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                                 tma_store_2d(&p.map_g, staging, col, row0);
                                 if constexpr (MODE == kXentGrad2)
                                     tma_store_2d(&p.map_g, staging + 32 * 128, col,
-                                                 p.lo_row + row0);
+                                                 p.info->used + row0);
                                 bulk_commit_group();
                             }
                         }

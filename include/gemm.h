@@ -396,7 +396,7 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  *     dX = G * W,   dW = beta * dW + G^T * X
  *
  * with G zero for rows that do not count; of them nothing but target is used (X,
- * lse and dloss may hold anything there). dloss is a DEVICE array of M floats, or
+ * lse and dloss may hold anything there), and most of their operations are left out. dloss is a DEVICE array of M floats, or
  * NULL for ones (the mean of M tokens: alpha = 1 / M). dX is M x K (lddx >= K) of
  * the operands' type, dW is N x K (lddw >= K) of the dtype's result type: fp32 for
  * master gradients, which beta = 1 accumulates over micro-batches, or 16-bit.
@@ -408,8 +408,8 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  * reaches down to 2^-36 of it), which is put back in fp32: a factor that all rows
  * share is not rounded. Probabilities below 2^-126 count as zero.
  * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, or
- * 4096 columns), a copy of X (two for an fp32 dW), and an fp32 dX (a few where dX is
- * small). An fp32 dW with beta = 1 is added to as gemm_grouped_k's C. With M zero
+ * 4096 columns), a copy of X (two for an fp32 dW), 8 bytes a row, and an fp32 dX (a
+ * few where dX is small). An fp32 dW with beta = 1 is added to as gemm_grouped_k's C. With M zero
  * dW = beta * dW; K zero is a no-op. K is at most 2^20 (more: GEMM_ERR_UNSUPPORTED).
  * Otherwise as gemm_xent.
  */

@@ -256,6 +256,34 @@ def test_rows_that_do_not_count_hold_anything():
     check()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K,out", [
+    # fewer tiles than rows; more rows than are listed at a time; one accumulator's
+    # depth for dW; dX on the dense kernel; odd sizes
+    (3000, 400, 72, 0.97), (9000, 300, 64, 0.5), (20000, 130, 32, 0.9), (640, 5000, 128, 0.6),
+    (9000, 300, 512, 0.8), (8193, 77, 33, 0.99),
+])
+def test_few_rows_count(M, N, K, out, dtype):
+    compare(M, N, K, dtype, out=out)
+
+
+@pytest.mark.parametrize("dtype", [BF32, H16])
+@pytest.mark.parametrize("row", [0, 8191, 8192, 8999])
+def test_one_row_counts(row, dtype):
+    X, W, target, dloss = inputs(9000, 300, 64, dtype, out=2.0)
+    target[row] = 7
+    loss, lse = forward(X, W, target, dtype)
+    dX, dW = backward(X, W, target, lse, dloss, dtype)
+    only = slice(row, row + 1)
+    (rx, lx), (rw, lw) = Exact(X[only], W, target[only], dloss[only], 1.0,
+                               lse[only]).grads(dtype, parts_of(dtype))
+    within(dX[only], rx, lx, "dX")
+    within(dW, rw, lw, "dW")
+    dX[row] = 0
+    assert bool((dX == 0).all())
+    check()
+
+
 @pytest.mark.parametrize("dtype", [BF, BF32, H16])
 def test_no_row_counts(dtype):
     X, W, target, dloss = inputs(140, 300, 64, dtype, out=2.0)
