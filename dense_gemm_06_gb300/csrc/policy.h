@@ -405,11 +405,12 @@ inline LoraShape plan_lora(int64_t M, int64_t N, int64_t num_kb, int64_t listed,
 
 // gemm_xent, gemm_xent_grad: tiles of the logits (M rows, N columns of a piece of
 // the vocabulary). CTA pairs on 256 x 256, but single CTAs on 128 rows where at
-// most 128 rows make half of a pair's tile padding, or where pairs would leave
-// more than half of the SMs idle; these take 64 columns if all tiles then still
-// run at once, else 128. The forward pass of at most 128 rows is bound by reading
-// W, so its tiles divide the columns evenly over whole rounds of the SMs (32000
-// columns on 152 SMs: 2 rounds of 112).
+// most 128 rows make half of a pair's tile padding, or where their 128 x 128 tiles
+// all run at once (K = 2048, us: 300 x 6000 13.2 and 17.2 by pairs, 2000 x 1000 12.7
+// and 16.5; past that 1000 x 2500 19.4 and 16.6); these take 64 columns if all tiles
+// then still run at once, else 128. The forward pass of at most 128 rows is bound by
+// reading W, so its tiles divide the columns evenly over whole rounds of the SMs (100
+// rows of 1024 from 50000 22.8 us, 23.9 with 128 columns each).
 constexpr int64_t kXentMaxVocab = 1 << 24, kXentMaxRows = 1 << 29;
 constexpr int64_t kXentMaxDepth = 1 << 20;  // K of gemm_xent_grad
 // gemm_xent_grad: a 16-bit dW of at most so many rows of X (in whole tiles) that one
@@ -422,8 +423,7 @@ struct XentShape {
     int tile_n;
 };
 inline XentShape plan_xent(int64_t M, int64_t N, int sm_count, bool forward) {
-    const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
-    if (M > 128 && pairs * 4 >= sm_count) return XentShape{2, 256};
+    if (M > 128 && ((M + 127) / 128) * ((N + 127) / 128) > sm_count) return XentShape{2, 256};
     if (forward && M <= 128) {
         const int64_t rounds = (N + 128 * (int64_t)sm_count - 1) / (128 * (int64_t)sm_count);
         const int64_t each = (N + rounds * sm_count - 1) / (rounds * sm_count);
@@ -469,12 +469,13 @@ inline int64_t xent_panel_rows(int64_t M, int64_t N, int tile_n) {
 }
 
 // Columns of the vocabulary that gemm_xent_grad holds G of at one time: all of
-// them if `parts` numbers of 16 bits for each of `rows` rows stay within 512 MB,
-// else pieces of equal width (in whole tiles) that do, of 4096 columns at least:
-// every piece adds its part of dX to an fp32 sum, which a narrow one would spend
-// its time on.
-inline int64_t xent_piece_cols(int64_t rows, int64_t N, int parts) {
-    int64_t most = (512ll << 20) / (rows * 2 * parts) / 256 * 256;
+// them if each of the numbers of 16 bits that an entry takes stays within 512 MB for
+// `rows` rows, else pieces of equal width (in whole tiles) that do, of 4096 columns at
+// least: every piece adds its part of dX to an fp32 sum, which a narrow one would
+// spend its time on (8192 rows of 1024 from 131072, fp32 dW, us: 6585 by 2 x 512 MB,
+// 7000 by 2 x 256, 6573 by 2 x 1024).
+inline int64_t xent_piece_cols(int64_t rows, int64_t N) {
+    int64_t most = (512ll << 20) / (rows * 2) / 256 * 256;
     if (most < 4096) most = 4096;
     if (N <= most) return N;
     const int64_t pieces = (N + most - 1) / most;

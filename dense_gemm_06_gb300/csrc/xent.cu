@@ -16,7 +16,7 @@
 // again and writes G as 16-bit numbers, which are multiplied with the piece's rows of
 // W (dX, summed over the pieces in fp32, on gemm()'s kernel or, where its tiles are
 // few, in shares of the depth) and with X (the piece's rows of dW, complete). G takes
-// at most 512 MB, or 4096 columns.
+// at most 512 MB for each of its numbers, or 4096 columns.
 //
 // Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
 // relative 2^-9 (bf16) is below the rounding of a 16-bit result. An fp32 dW would
@@ -538,7 +538,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     if (rc != kOk) return rc;
 
     const int parts = dW && we == 4 ? 2 : 1;  // numbers that hold an entry of G
-    const int64_t piece = xent_piece_cols(up(M, 256), N, parts);
+    const int64_t piece = xent_piece_cols(up(M, 256), N);
     const XentShape shape = plan_xent(M, piece, dev->sm_count, false);  // of every piece
     const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
     const int64_t pieces = (N + piece - 1) / piece;

@@ -407,8 +407,8 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  * it, divided by the largest |alpha * dloss[t]| (fp16: 2^-12 of that, so that G
  * reaches down to 2^-36 of it), which is put back in fp32: a factor that all rows
  * share is not rounded. Probabilities below 2^-126 count as zero.
- * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, or
- * 4096 columns), a copy of X (two for an fp32 dW), 8 bytes a row, and an fp32 dX (a
+ * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, 1 GB
+ * for an fp32 dW, or 4096 columns), a copy of X (two for an fp32 dW), 8 bytes a row, and an fp32 dX (a
  * few where dX is small). An fp32 dW with beta = 1 is added to as gemm_grouped_k's C. With M zero
  * dW = beta * dW; K zero is a no-op. K is at most 2^20 (more: GEMM_ERR_UNSUPPORTED).
  * Otherwise as gemm_xent.

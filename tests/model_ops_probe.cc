@@ -4,7 +4,7 @@
 //
 //   xent  M N sm_count forward     -> "cta_group tile_n"
 //   panel M N tile_n               -> "rows"
-//   piece rows N parts             -> "columns"
+//   piece rows N                   -> "columns"
 //   sum   M K n sm_count last      -> "cta_group tile_n splits used each used_of_last"
 //   chunk M                        -> "tokens"
 #include <cstdio>
@@ -23,7 +23,7 @@ int main(int argc, char** argv) {
     } else if (std::strcmp(argv[1], "panel") == 0) {
         std::printf("%lld\n", (long long)xent_panel_rows(arg(2), arg(3), (int)arg(4)));
     } else if (std::strcmp(argv[1], "piece") == 0) {
-        std::printf("%lld\n", (long long)xent_piece_cols(arg(2), arg(3), (int)arg(4)));
+        std::printf("%lld\n", (long long)xent_piece_cols(arg(2), arg(3)));
     } else if (std::strcmp(argv[1], "sum") == 0) {
         const XentSumPlan p = plan_xent_sum(arg(2), arg(3), arg(4), (int)arg(5));
         const long long each = p.each(arg(4)), kb = (arg(6) + 63) / 64;

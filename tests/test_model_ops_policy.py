@@ -34,9 +34,9 @@ def probe(tmp_path_factory):
     # 128 rows and fewer: even tiles over whole rounds of the SMs, or 128 columns
     (5, 32000, 1, (1, 112)), (128, 131072, 1, (1, 128)), (1, 1000, 1, (1, 32)),
     (1, 152 * 128, 1, (1, 128)), (1, 152 * 128 + 1, 1, (1, 80)), (5, 32000, 0, (1, 128)),
-    # too few pair tiles for half of the SMs
+    # tiles of 128 x 128 that run at once: 8 x 19 of them do, 8 x 20 do not
     (300, 1000, 1, (1, 64)), (300, 1000, 0, (1, 64)), (1000, 2304, 0, (1, 128)),
-    (1000, 2305, 0, (2, 256)), (1000, 2432, 1, (2, 256)),
+    (1000, 2432, 1, (1, 128)), (1000, 2433, 1, (2, 256)), (1000, 2433, 0, (2, 256)),
 ])
 def test_tiles_of_the_logits(probe, M, N, forward, want):
     assert probe("xent", M, N, SMS, forward) == want
@@ -56,16 +56,16 @@ def test_panels_keep_their_partial_sums_in_256_mb(probe):
 
 
 def test_pieces_of_the_vocabulary(probe):
-    assert probe("piece", 4096, 32000, 1) == (32000,)        # 256 MB of G
-    assert probe("piece", 8192, 131072, 2) == (16384,)       # eight of 512 MB
-    assert probe("piece", 8192, 32769, 1) == (16640,)        # two of equal width
-    assert probe("piece", 1 << 20, 50000, 1) == (4096,)      # many rows: 4096 columns
+    assert probe("piece", 4096, 32000) == (32000,)           # 256 MB of G
+    assert probe("piece", 8192, 131072) == (32768,)          # four of 512 MB
+    assert probe("piece", 8192, 32769) == (16640,)           # two of equal width
+    assert probe("piece", 1 << 20, 50000) == (4096,)         # many rows: 4096 columns
     rng = random.Random(2)
     for _ in range(200):
-        rows, N, parts = rng.randint(1, 10 ** 6) * 128, rng.randint(1, 300000), rng.choice([1, 2])
-        cols, = probe("piece", rows, N, parts)
+        rows, N = rng.randint(1, 10 ** 6) * 128, rng.randint(1, 300000)
+        cols, = probe("piece", rows, N)
         assert 1 <= cols <= N + 255 and (cols == N or cols % 256 == 0)
-        assert cols <= 4096 or rows * 2 * parts * cols <= 512 << 20
+        assert cols <= 4096 or rows * 2 * cols <= 512 << 20
 
 
 @pytest.mark.parametrize("M,K,n,want", [
