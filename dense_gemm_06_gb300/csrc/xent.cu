@@ -19,7 +19,7 @@
 // at most 512 MB for each of its numbers, or 4096 columns.
 //
 // Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
-// relative 2^-9 (bf16) is below the rounding of a 16-bit result. An fp32 dW would
+// relative 2^-8 (bf16) is that of a 16-bit result itself. An fp32 dW would
 // show it, so for that G is two numbers, hi + lo (2^-17 of g), and X is multiplied
 // with both in one product of twice the depth, on gemm_grouped_k's kernel, which
 // adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384).
