@@ -1730,7 +1730,7 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
         if (!(configured & bit)) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      RCfg<MODE == kRagShrink && P_MN>::SMEM_BYTES) != cudaSuccess)
-                return kCuda;
+                return refused();
             int n = dev.sm_count / 2;
             if (CG == 2) {
                 cfg.gridDim = dim3(2 * n);

@@ -786,7 +786,7 @@ int launch_variant(TcParams& tp, const DeviceInfo& dev, cudaStream_t stream) {
         if (!(configured & bit)) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C_::SMEM_BYTES) != cudaSuccess)
-                return kCuda;
+                return refused();
             int n = dev.sm_count / CLUSTER;
             if (CLUSTER > 1) {
                 cudaLaunchConfig_t cfg = {};
@@ -821,7 +821,7 @@ int launch_variant(TcParams& tp, const DeviceInfo& dev, cudaStream_t stream) {
         cfg.numAttrs = 2;
     }
     cfg.stream = stream;
-    if (cudaLaunchKernelEx(&cfg, kern, tp) != cudaSuccess) return kCuda;
+    if (cudaLaunchKernelEx(&cfg, kern, tp) != cudaSuccess) return refused();
     note_launch();
     return kOk;
 }

@@ -230,5 +230,12 @@ enum : int {
     kTimeout = -4,
 };
 
+// The status of a call that the CUDA runtime refused. Its error is taken back: left
+// behind, the next check of the runtime in this process, the caller's own among them,
+// would report it.
+inline int refused() {
+    cudaGetLastError();
+    return kCuda;
+}
 
 }  // namespace libgemm

@@ -441,8 +441,10 @@ bool configure_once(Kern kern, std::atomic<uint64_t>& done, int device, int smem
     const uint64_t bit = 1ull << (device & 63);
     if (done.load() & bit) return true;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) !=
-        cudaSuccess)
+        cudaSuccess) {
+        cudaGetLastError();
         return false;
+    }
     done.fetch_or(bit);
     return true;
 }

@@ -653,11 +653,11 @@ int launch_xent_variant(XentParams& xp, const DeviceInfo& dev, cudaStream_t stre
         if (!(configured & bit)) {
             // the epilogue's registers come out of what the block is launched with
             cudaFuncAttributes fa;
-            if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != XREGS)
-                return kCuda;
+            if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return refused();
+            if (fa.numRegs != XREGS) return kCuda;
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
                 cudaSuccess)
-                return kCuda;
+                return refused();
             int n = dev.sm_count / CG;
             if (CG > 1) {
                 int fit = 0;
@@ -679,7 +679,7 @@ int launch_xent_variant(XentParams& xp, const DeviceInfo& dev, cudaStream_t stre
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 2;
     cfg.stream = stream;
-    if (cudaLaunchKernelEx(&cfg, kern, xp) != cudaSuccess) return kCuda;
+    if (cudaLaunchKernelEx(&cfg, kern, xp) != cudaSuccess) return refused();
     note_launch();
     return kOk;
 }
