@@ -433,8 +433,8 @@ inline XentShape plan_xent(int64_t M, int64_t N, int sm_count, bool forward) {
 }
 
 // gemm_xent_grad: how dX (M x K, the depth the `n` columns of a piece of the
-// vocabulary) runs when its tiles alone would leave SMs idle: so many shares of the
-// depth (splits; 1: gemm()'s kernel), of at least 512 columns, that the rounds of
+// vocabulary) runs: where its tiles alone would leave half of the SMs idle, so many
+// shares of the depth (splits), of at least 512 columns, that the rounds of
 // units times the length of one is least, and the fewest such (each leaves an fp32
 // part of dX to add up). Tiles as in plan_xent; at most 128 rows are bound by
 // reading W.

@@ -14,15 +14,19 @@
 //
 // Backward: piece by piece of the vocabulary the same kernel computes the logits
 // again and writes G as 16-bit numbers, which are multiplied with the piece's rows of
-// W (dX, summed over the pieces in fp32, on gemm()'s kernel or, where its tiles are
-// few, in shares of the depth) and with X (the piece's rows of dW, complete). G takes
-// at most 512 MB for each of its numbers, or 4096 columns.
+// W (dX, summed over the pieces in fp32, in shares of the depth where its tiles are
+// few) and with X (the piece's rows of dW, complete). G takes at most 512 MB for each
+// of its numbers, or 4096 columns. dX's product adds up its sums every 704 of depth: on
+// one accumulator for all of it, gemm()'s way, dX came out 8e-4 too small from 131072
+// columns, 2e-4 from 32000 (the means of rows whose terms have one sign; fp16's own
+// rounding, of either sign, is 2e-4). The time differs by -6 to 8 % with the fill of the
+// last round (bf16 from 32000, dX alone, us: 4096 x 2048 657 and 650 by gemm()'s kernel,
+// 4096 x 1280 539 and 497, 1024 x 1280 189 and 202).
 //
 // Rounding. G is 16-bit because the tensor cores take 16-bit operands: its
 // relative 2^-8 (bf16) is that of a 16-bit result itself. An fp32 dW would
 // show it, so for that G is two numbers, hi + lo (2^-17 of g), and X is multiplied
-// with both in one product of twice the depth, on gemm_grouped_k's kernel, which
-// adds up its sums every 704 of depth (gemm()'s is 2e-5 off at a depth of 16384).
+// with both in one product of twice the depth, on gemm_grouped_k's kernel.
 // G is divided by the largest |alpha dloss|, which the products are multiplied with
 // again in fp32 before they are rounded: a mean's 1 / n, rounded to 16 bits, would
 // put the same error into every term (0.2 % of dX in bf16), and fp16 has exponents
@@ -31,11 +35,11 @@
 // 1310 us).
 //
 // Rows whose target does not count (prompts, padding) take no part: a first kernel
-// lists the others, which are copied side by side, and G's kernel, dW's product and
-// the shared dX work on as many tiles as these fill, a number that stays on the device
-// (1531 rows of 1037, fp16, vocabulary 50001, 918 of them counting: 490 us with the
-// forward pass, 557 with all of them). The last tile's rows past them are zero in G and
-// in the copy of X (0 times an infinity would be NaN).
+// lists the others, which are copied side by side, and G's kernel and both products
+// work on as many tiles as these fill, a number that stays on the device (8192 rows of
+// 2048 from 32000, bf16, dX alone: 1286 us, 1015 with 30 % left out, 352 with 80 %). The
+// last tile's rows past them are zero in G and in the copy of X (0 times an infinity
+// would be NaN).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -479,21 +483,6 @@ int forward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const v
     return rc;
 }
 
-// dX's part of a piece on the dense kernel: sum (+)= G W, fp32, of all M rows: those
-// past the ones that count hold anything, and nothing reads their sums. (launch_sum
-// would leave them out, but adds up in parts: 298 us and 307, 4096 x 2048 from 32000.)
-int product(int64_t M, int64_t K, int64_t n, const void* g, int64_t ldg, const void* W,
-            int64_t ldw, float* sum, int64_t lds, bool add, bool bf16, const DeviceInfo& dev,
-            cudaStream_t s) {
-    const int dtype = bf16 ? GEMM_BF16_F32 : GEMM_F16_F32;
-    Problem p{M, K, n, g, ldg, true, W, ldw, false, sum, lds, dtype, EpiParams{}};
-    if (add) p.epi = EpiParams{1, 1.f, 1.f, nullptr, 0, GEMM_ACT_NONE};
-    return launch_gemm_tc(p, dev,
-                          resolve_tc_options(M, K, n, g, ldg, GEMM_MAJOR_K, W, ldw, GEMM_MAJOR_MN,
-                                             sum, lds, GEMM_MAJOR_MN, dtype),
-                          s);
-}
-
 // dW = beta dW + *scale G^T X on the product over the rows of one group, {0, depth}
 // in `limits`: it adds up fp32 sums in parts of the depth (the tensor core's cut-off
 // additions would show in an fp32 dW), and takes the factor from device memory.
@@ -542,7 +531,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
     const XentShape shape = plan_xent(M, piece, dev->sm_count, false);  // of every piece
     const int rows = (int)up(M, XROWS * shape.cta_group);        // that the tiles cover
     const int64_t pieces = (N + piece - 1) / piece;
-    // dX by shares of the depth where its tiles are few, else through gemm()'s kernel
+    // dX: in shares of the depth where its tiles are few
     const XentSumPlan plan = plan_xent_sum(M, K, piece, dev->sm_count);
     const int64_t ldg = up(piece, 256), ldk = up(K, 8);
     Parts at;
@@ -593,10 +582,8 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
         }
         rc = launch(xp, parts == 2 ? kXentGrad2 : kXentGrad, bf16, shape, *dev, s);
         if (rc == kOk && dX)
-            rc = plan.splits > 1
-                     ? launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, info,
-                                  bf16, *dev, s)
-                     : product(M, K, n, g, ldg, wp, ldw, dx_sum, up(K, 4), v0 > 0, bf16, *dev, s);
+            rc = launch_sum(plan, M, K, piece, n, g, ldg, wp, ldw, dx_sum, M, v0 > 0, info, bf16,
+                            *dev, s);
         if (rc != kOk || !dW) continue;
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
         rc = we == 2 && beta == 0.f && tma_ready(dW, lddw) && rows <= kXentTableRows

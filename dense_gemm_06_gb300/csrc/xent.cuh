@@ -7,9 +7,9 @@
 //           products dX = G W and dW = G^T X (16-bit results);
 //   kGrad2  the same as two 16-bit numbers, hi = rn(g) and lo = rn(g - hi), for
 //           an fp32 dW;
-//   kSum    dX = G W where its tiles are few: the depth (the piece's columns of
-//           the vocabulary) is shared by several CTAs or pairs a tile, each of
-//           which leaves an fp32 part (1531 rows of 1037 from 50001 columns: 220 us
+//   kSum    dX = G W in fp32; where its tiles are few, the depth (the piece's columns
+//           of the vocabulary) is shared by several CTAs or pairs a tile, each of
+//           which leaves a part (1531 rows of 1037 from 50001 columns: 220 us
 //           with a CTA for each of 108 whole tiles, 100 us so);
 //   kTable  a 16-bit dW = factor G^T X of few rows, the factor read from device
 //           memory, stored by TMA from the boxes that G leaves through (32000 x 2048
@@ -25,7 +25,7 @@
 //
 // The tensor core cuts off what an addition shifts below its last bits, so a long
 // sum of products drifts towards zero by about half a step for every 16 of depth:
-// losses of K = 2048 were off by 6e-6 of themselves. So an accumulator takes at
+// losses of K = 2048 were off by 6e-6 of themselves, dX from 131072 columns by 8e-4. So an accumulator takes at
 // most kXentFold blocks of depth, and the epilogue warps add up those parts in
 // registers, rounded to nearest (128 numbers a thread; the warps that only issue
 // copies and MMAs hand over registers for them).  With K = 2048
