@@ -439,6 +439,7 @@ int grouped_k(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets
     rp.stridec = stridec;
     rp.epi = ep;
     rp.scale = scale;
+    rp.fold = scale && K > kXentFoldRows;
     map_c(rp, dtype, C, G, stridec, M, N, ldc);
     const int64_t units = G * rp.tiles_f * rp.tiles_r;
     if ((int64_t)rp.tiles_f * rp.tiles_r > INT32_MAX / G ||

@@ -69,6 +69,7 @@ struct RaggedParams {
     const int32_t* adapter;  // adapter number of each row
     const float* scale;      // one factor per adapter, or null (depth: null, or one factor
                              // on alpha: what gemm_xent_grad divided by)
+    int fold;                // depth, 16-bit results: the sums in parts, as fp32 ones
     const void* x;           // kRagShrinkRows: X and LA, row pitches ldx and ldla
     const void* lora_a;
     int64_t ldx, ldla;
@@ -774,8 +775,9 @@ __global__ void __launch_bounds__(kRowsThreads)
 // EPI: whether the launch has a fused epilogue, or only a factor in device memory. A
 // template argument where fp32 sums are folded (else always kEpiAny): the 128 sums
 // leave the plain kernel no registers for code that it does not run (511 us against
-// 477 us, 64 weight gradients of 2816 x 2048).
-enum { kEpiNone = 0, kEpiAny = 1, kEpiScale = 2 };
+// 477 us, 64 weight gradients of 2816 x 2048). kEpiFold: a fused epilogue of 16-bit
+// results whose sums are folded like fp32 ones (gemm_xent_grad's dW).
+enum { kEpiNone = 0, kEpiAny = 1, kEpiScale = 2, kEpiFold = 3 };
 template <int CG, int MODE, bool P_MN, bool BF16, typename OutT, int EPI>
 __global__ void __launch_bounds__(RTHREADS, 1)
     ragged_kernel(const __grid_constant__ RaggedParams p) {
@@ -786,7 +788,8 @@ __global__ void __launch_bounds__(RTHREADS, 1)
     constexpr bool Q_MN = MODE == kRagDepth;
     // T in fp16 may need the second accumulator (see T_SMALL)
     constexpr bool SMALL_T = MODE == kRagLora && !BF16;
-    constexpr bool FOLD = std::is_same_v<OutT, float> && MODE != kRagShrink;
+    constexpr bool FOLD =
+        (std::is_same_v<OutT, float> || EPI == kEpiFold) && MODE != kRagShrink;
     constexpr int CHUNKS = CG == 2 ? 4 : 2;  // of 32 rows that an epilogue warp stores
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -1263,7 +1266,8 @@ __global__ void __launch_bounds__(RTHREADS, 1)
             const int l = q * 32 + lane;  // TMEM lane
             const int f = un.feat0 + (int)rank * 128 + l;
             const int n_rows = min(un.width, un.row_end - un.row0);
-            const bool epi = EPI == kEpiAny && MODE != kRagShrink && p.epi.active;
+            const bool epi =
+                (EPI == kEpiAny || EPI == kEpiFold) && MODE != kRagShrink && p.epi.active;
             const bool f_ok = f < p.feats;
             float bias = 0.f;
             if (epi && p.epi.bias && f_ok)
@@ -1709,6 +1713,10 @@ int launch_ragged_variant(RaggedParams& rp, int64_t units, const DeviceInfo& dev
             return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, kEpiNone>(rp, units, dev,
                                                                                stream);
     }
+    if constexpr (EPI == kEpiAny && !std::is_same_v<OutT, float> && MODE == kRagDepth)
+        if (rp.fold)
+            return launch_ragged_variant<CG, MODE, P_MN, BF16, OutT, kEpiFold>(rp, units, dev,
+                                                                               stream);
     auto kern = ragged_kernel<CG, MODE, P_MN, BF16, OutT, EPI>;
     static std::mutex mu;
     static uint64_t configured = 0;  // bit per device

@@ -418,6 +418,12 @@ constexpr int64_t kXentMaxDepth = 1 << 20;  // K of gemm_xent_grad
 // gemm_grouped_k's (bf16, 32000 x 2048, us: 1 row 74 and 110, 300 rows 111 and 138,
 // 1000 rows 184 and 177; 64000 x 4096 from 2048 rows 1260 and 1183).
 constexpr int64_t kXentTableRows = 704;
+// And one of more rows than this on that kernel's form that folds its sums every 704 of
+// depth as fp32 ones are. One accumulator's additions cut off 6.4e-9 of a steady sum
+// for each row of depth: 5e-5 at 8192 (fp16's own rounding is at most 2.4e-4), 4e-4 at
+// 65536, 1.3e-3 at 200000. Folding costs 2 to 6 % from 8192 rows on (bf16, 32000 x 2048,
+// beta 0, us: 32768 rows 5330 and 5128), 15 to 20 % of few.
+constexpr int64_t kXentFoldRows = 8192;
 struct XentShape {
     int cta_group;  // 1: a CTA per 128 rows, 2: a CTA pair per 256 rows
     int tile_n;

@@ -55,3 +55,31 @@ def test_dx_of_a_deep_vocabulary_does_not_drift(M, gone, dtype, lim):
     ref = p @ W.double()
     off = float((dX.double() * ref).sum() / ref.square().sum()) - 1
     assert abs(off) < lim
+
+
+@pytest.mark.parametrize("dtype,lim", [(lg.GEMM_F16_F16, 2.0 ** -15),
+                                       (lg.GEMM_BF16_BF16, 2.0 ** -14)])
+@pytest.mark.parametrize("M,K,beta", [(8193, 512, 0.0), (65536, 512, 0.0), (65536, 509, 0.0),
+                                      (65536, 512, 1.0), (200000, 512, 0.0)])
+def test_a_16_bit_dw_of_many_rows_does_not_drift(M, K, beta, dtype, lim):
+    """The same of dW over the rows, for every token but the target: X has positive columns,
+    so a token's sum of p_t X_t grows steadily. Allowed: 44 2^-23 for an accumulator,
+    285 2^-24 for the additions of 200000 rows' parts, 46 2^-24 for the exponentials
+    (lse below 7.5), 2.5e-5; the roundings average over 1023 K results, and G's over the
+    rows too, 2^-9 / sqrt(3 * 8193) = 1.2e-5 of a token's sum in bf16, and over tokens."""
+    N, t = 1024, IN[dtype]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = (torch.randn(M, K, generator=g, device="cuda") * 0.2
+         + torch.rand(K, generator=g, device="cuda") + 0.5).to(t)
+    W = (torch.randn(N, K, generator=g, device="cuda") * 0.5 * K ** -0.5).to(t)
+    target = torch.zeros(M, dtype=torch.int32, device="cuda")
+    lse, dW = torch.empty(M, device="cuda"), torch.zeros(N, K, dtype=t, device="cuda")
+    lg.check(lg.gemm_xent(M, N, K, X, K, W, K, target, torch.empty_like(lse), lse, dtype))
+    assert float(lse.max()) < 7.5
+    lg.check(lg.gemm_xent_grad(M, N, K, X, K, W, K, target, lse, None, None, K, dW, K, dtype,
+                               alpha=N / M, beta=beta))
+    check()
+    p = torch.exp_((X.double() @ W.double().T).sub_(lse.double()[:, None]))
+    ref = (p.T @ X.double())[1:] * (N / M)
+    off = float((dW[1:].double() * ref).sum() / ref.square().sum()) - 1
+    assert abs(off) < lim
