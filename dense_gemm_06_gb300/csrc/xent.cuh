@@ -356,7 +356,9 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
         // ---------------------------------------------------- MMA issuer --
         give_registers();
         if (rank == 0) {
-            if constexpr (MODE != kXentStats) pdl_wait();
+            // the limit of the waits below begins when the kernel before this one on the
+            // stream has ended, however long that takes beside this one's start
+            pdl_wait();
             const XentWork work = xent_work<MODE, CG>(p);
             // X and W are K-major, 32 bytes a step of 16 deep, or (W of kSum, both of
             // kTable) M- or N-major, 16 rows of 128
