@@ -2,8 +2,7 @@
 program would run it on gemm_lora, gemm_grouped and gemm_grouped_k:
 
     x  = lora(tokens)                     a shared projection, an adapter per request
-    route: logits = x R^T, the top k of their softmax; rows sorted by expert on the GPU,
-           the experts' limits and the balance loss from router_balance
+    route: logits = x R^T, the top k of their softmax; rows sorted by expert on the GPU
     h  = relu(x W1_e^T), y = h W2_e^T     gemm_grouped, twice
     out = sum over a token's experts of weight * y
 
@@ -12,9 +11,10 @@ micro-batches (beta = 1) as fp32:
 
     dW2_e += dy^T h   dh = dy W2_e   dW1_e += (dh masked)^T x   dx = (dh masked) W1_e
 
-Nothing of it copies the experts' sizes to the host: router_balance counts the
-rows of each expert and sums the counts up to the limits, on the stream that the
-products run on, so block() can be captured into a graph.
+Nothing of it copies the experts' sizes to the host: the limits are searched
+for in the sorted experts of the rows, on the stream that the products run on
+(torch.bincount would read its input's range back), so block() can be captured
+into a graph.
 
     python -m dense_gemm_06_gb300.experts_demo [--tokens T] [--experts E] [--top K]
         [--hidden D] [--inner F] [--requests Q] [--rank R]
@@ -69,36 +69,19 @@ def experts_weight_grad(dy, x, offsets, into):
                                BF_F32, beta=1.0))
 
 
-def routing(x, router, top, kept=None):
-    """The choice of `top` experts for every token (`kept`: of those that are True,
-    the others' rows come after the last group): logits, their softmax p, the choice
-    (token by token, -1 where none), the experts' counts, the limits of their rows and
-    the balance loss; and for each row, by expert, its token, expert, weight and
-    whether it counts."""
-    import torch
-    (m, k), e, dev = x.shape, router.shape[0], x.device
-    logits, p = torch.empty(m, e, device=dev), torch.empty(m, e, device=dev)
-    lg.check(lg.gemm(m, e, k, x, k, K_MAJOR, router, k, K_MAJOR, logits, e, MN_MAJOR, BF_F32))
-    lg.check(lg.softmax_rows(m, e, logits, e, p, e))
-    weight, expert = p.topk(top, dim=1)
-    choice = expert.int()
-    if kept is not None:
-        choice = torch.where(kept[:, None], choice, -1)
-        expert = torch.where(kept[:, None], expert, e)
-    counts, offsets = (torch.empty(e + 1, dtype=torch.int32, device=dev) for _ in range(2))
-    prob, balance = torch.empty(e, device=dev), torch.empty(1, device=dev)
-    lg.check(lg.router_balance(m, e, top, logits, e, choice, counts, offsets, prob, balance,
-                               lg.GEMM_F32))
-    by_expert, order = expert.flatten().sort(stable=True)
-    return dict(logits=logits, p=p, choice=choice, counts=counts, offsets=offsets, prob=prob,
-                balance=balance, token=order // top, expert=by_expert.clamp(max=e - 1),
-                weight=weight.flatten()[order], counts_row=by_expert < e)
-
-
 def route(x, router, top):
     """(expert limits, token of each row, weight of each row), rows by expert."""
-    r = routing(x, router, top)
-    return r["offsets"], r["token"], r["weight"]
+    import torch
+    logits = torch.empty(x.shape[0], router.shape[0], device=x.device)
+    lg.check(lg.gemm(x.shape[0], router.shape[0], x.shape[1], x, x.shape[1], K_MAJOR, router,
+                     x.shape[1], K_MAJOR, logits, router.shape[0], MN_MAJOR, BF_F32))
+    lg.check(lg.softmax_rows(x.shape[0], router.shape[0], logits, router.shape[0], logits,
+                             router.shape[0]))
+    weight, expert = logits.topk(top, dim=1)
+    by_expert, order = expert.flatten().sort(stable=True)
+    offsets = torch.searchsorted(by_expert, torch.arange(router.shape[0] + 1, device=x.device),
+                                 out_int32=True)
+    return offsets, order // top, weight.flatten()[order]
 
 
 def make(tokens, n_experts, hidden, inner, requests, rank, seed=0):

@@ -73,6 +73,29 @@ def norm_grad(saved, dy):
     return dx, dw, db
 
 
+def routing(x, router, top, kept):
+    """The choice of `top` experts for every token that is `kept` (the others' rows come
+    after the last group): logits, their softmax p, the choice (token by token, -1
+    where none), the experts' counts, the limits of their rows and the balance loss; and
+    for each row, by expert, its token, expert, weight and whether it counts."""
+    import torch
+    (m, k), e, dev = x.shape, router.shape[0], x.device
+    logits, p = torch.empty(m, e, device=dev), torch.empty(m, e, device=dev)
+    lg.check(lg.gemm(m, e, k, x, k, K_MAJOR, router, k, K_MAJOR, logits, e, MN_MAJOR, BF_F32))
+    lg.check(lg.softmax_rows(m, e, logits, e, p, e))
+    weight, expert = p.topk(top, dim=1)
+    choice = torch.where(kept[:, None], expert.int(), -1)
+    expert = torch.where(kept[:, None], expert, e)
+    counts, offsets = (torch.empty(e + 1, dtype=torch.int32, device=dev) for _ in range(2))
+    prob, balance = torch.empty(e, device=dev), torch.empty(1, device=dev)
+    lg.check(lg.router_balance(m, e, top, logits, e, choice, counts, offsets, prob, balance,
+                               lg.GEMM_F32))
+    by_expert, order = expert.flatten().sort(stable=True)
+    return dict(logits=logits, p=p, choice=choice, counts=counts, offsets=offsets, prob=prob,
+                balance=balance, token=order // top, expert=by_expert.clamp(max=e - 1),
+                weight=weight.flatten()[order], counts_row=by_expert < e)
+
+
 def step(s, top, timed=lambda name, f: f()):
     """Losses and gradients of one step; everything is enqueued on the current stream."""
     import torch
@@ -88,7 +111,7 @@ def step(s, top, timed=lambda name, f: f()):
     x = timed("lora projection", lambda: ex.lora(n1, s["w"], s["adapter"], s["la"], s["lb"],
                                                  s["scale"]))
     kept = s["ids"] >= 0
-    a = timed("routing", lambda: ex.routing(x, s["router"], top, kept))
+    a = timed("routing", lambda: routing(x, s["router"], top, kept))
     xs = x[a["token"]]
     h = timed("experts up", lambda: ex.experts(xs, s["w1"], a["offsets"], lg.GEMM_ACT_RELU))
     y = timed("experts down", lambda: ex.experts(h, s["w2"], a["offsets"]))
