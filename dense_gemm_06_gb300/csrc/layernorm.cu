@@ -417,7 +417,7 @@ constexpr int kGradWarps = 16;  // on an SM
 // Rows on their way to a thread, the one that it works on included. With 16-bit
 // rows of 2048, 128 threads and four blocks on an SM that is 96 KB in flight.
 template <typename T, int WARPS>
-constexpr int kNormStages = sizeof(T) == 2 ? (WARPS == 32 ? 3 : 4) : WARPS == 32 ? 1 : 3;
+constexpr int kNormStages = sizeof(T) == 2 && WARPS < 32 ? 4 : 3;
 
 // A block of WARPS x LANES warps: LANES rows side by side, each on WARPS warps
 // (LANES > 1 only with one warp a row). Thread tid of a row owns the columns
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(32 * WARPS * LANES)
     norm_grad_kernel(const NormGradArgs a) {
     gemm_ptx::pdl_launch_dependents();
     constexpr int TR = 32 * WARPS, NV = kOwn / VEC, THREADS = TR * LANES;
-    constexpr int BYTES = VEC * (int)sizeof(T), STAGES = kNormStages<T, WARPS>;
-    constexpr bool RING = BYTES == 16 && STAGES > 1;
+    constexpr int STAGES = kNormStages<T, WARPS>;
+    constexpr bool RING = VEC > 1;
     using V = Pack<T, VEC>;
     extern __shared__ __align__(16) uint8_t ring[];  // STAGES x (x, dy) x NV x THREADS vectors
     __shared__ float slots[2][2 * WARPS];
@@ -739,15 +739,17 @@ int norm_forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
 }
 
 // The backward kernel's blocks (its sums' parts) for rows of N columns: 0 where
-// the rows are too long for it (2048 rows of 12000, bf16: 80.6 us by 32 warps a row,
-// 132 by the kernels of long rows). 16 warps on an SM: 19.5 us for 8192 rows of 2048,
+// the rows are too long for it. 32 warps a row leave a thread 64 registers, which
+// pays only for 16-bit rows read in vectors (2048 rows, us, by them and by the kernels
+// of long rows: 12000 bf16 87 and 141; 12001 bf16, single elements, 167 and 141, fp16 244
+// and 137, though 16383 bf16 187 and 198; 12000 fp32 297 and 161). 16 warps on an SM: 19.5 us for 8192 rows of 2048,
 // 5.2 TB/s.
 struct GradPlan {
     int warps, lanes, blocks;
 };
-GradPlan grad_plan(int64_t M, int64_t N, int sm_count) {
+GradPlan grad_plan(int64_t M, int64_t N, bool vec16, int sm_count) {
     GradPlan g{32, 1, 0};
-    if (N > 32 * 32 * kOwn) return g;
+    if (N > (vec16 ? 32 : 16) * 32 * kOwn) return g;
     for (int w : {1, 2, 4, 8, 16, 32})
         if (N <= 32 * w * kOwn) {
             g.warps = w;
@@ -765,8 +767,7 @@ template <typename T, typename W, int WARPS, int LANES, int VEC>
 int run_norm_grad(const NormGradArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int THREADS = 32 * WARPS * LANES;
     constexpr int STAGES = kNormStages<T, WARPS>;
-    constexpr int SMEM = VEC * sizeof(T) == 16 && STAGES > 1 ? STAGES * 2 * kOwn * (int)sizeof(T) * THREADS
-                                              : 0;
+    constexpr int SMEM = VEC > 1 ? STAGES * 2 * kOwn * (int)sizeof(T) * THREADS : 0;
     auto kern = norm_grad_kernel<T, W, WARPS, LANES, VEC>;
     const int rc = allow_smem(kern, SMEM, dev);
     if (rc != kOk) return rc;
@@ -778,16 +779,16 @@ int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const Device
                   cudaMemPool_t pool, cudaStream_t s) {
     const bool sums = dweight || dbias;
     int rc = kOk;
-    const GradPlan g = grad_plan(a.M, a.N, dev.sm_count);
+    const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.dy, a.lddy, sizeof(T)) &&
+                     (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) &&
+                     a.N % (16 / sizeof(T)) == 0 && aligned_to(a.weight, 16);
+    const GradPlan g = grad_plan(a.M, a.N, vec && sizeof(T) == 2, dev.sm_count);
     const int parts = g.blocks > 0 ? g.blocks : (int)(a.M < kLongShares ? a.M : kLongShares);
     Scratch scratch{pool, s, dev.device};
     if (sums && a.M > 0) {
         a.part = static_cast<float*>(scratch.get((size_t)parts * 2 * a.N * 4));
         if (!a.part) return kCuda;
     }
-    const bool vec = vec_ready(a.x, a.ldx, sizeof(T)) && vec_ready(a.dy, a.lddy, sizeof(T)) &&
-                     (!a.dx || vec_ready(a.dx, a.lddx, sizeof(T))) &&
-                     a.N % (16 / sizeof(T)) == 0 && aligned_to(a.weight, 16);
     if (a.M > 0 && g.blocks > 0) {
 #define NORM_GRAD_RUN(WARPS, LANES)                                                        \
     rc = vec ? run_norm_grad<T, W, WARPS, LANES, 16 / (int)sizeof(T)>(a, g.blocks, dev, s) \
@@ -798,7 +799,10 @@ int norm_backward(NormGradArgs a, W* dweight, W* dbias, float beta, const Device
             case 4: NORM_GRAD_RUN(4, 1); break;
             case 8: NORM_GRAD_RUN(8, 1); break;
             case 16: NORM_GRAD_RUN(16, 1); break;
-            default: NORM_GRAD_RUN(32, 1); break;
+            default:
+                if constexpr (sizeof(T) == 2)
+                    rc = run_norm_grad<T, W, 32, 1, 8>(a, g.blocks, dev, s);
+                break;
         }
 #undef NORM_GRAD_RUN
     } else if (a.M > 0) {
