@@ -670,7 +670,8 @@ int embed_grad(int64_t M, int64_t V, int64_t K, const int32_t* ids, const void* 
     char* mem = nullptr;
     if (M > 0) {
         const int64_t part = up((int64_t)a.chunks * 2 * a.kp * 4, 256);
-        mem = static_cast<char*>(scratch.get((size_t)(4 * list + part + 8 + (int64_t)a.chunks * 4)));
+        const int64_t bytes = 4 * list + part + 8 + (int64_t)a.chunks * 4;
+        mem = static_cast<char*>(scratch.get((size_t)bytes));
         if (!mem) return kCuda;
         uint64_t* in = reinterpret_cast<uint64_t*>(mem);
         uint64_t* out = reinterpret_cast<uint64_t*>(mem + list);

@@ -742,8 +742,8 @@ int norm_forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
 // the rows are too long for it. 32 warps a row leave a thread 64 registers, which
 // pays only for 16-bit rows read in vectors (2048 rows, us, by them and by the kernels
 // of long rows: 12000 bf16 87 and 141; 12001 bf16, single elements, 167 and 141, fp16 244
-// and 137, though 16383 bf16 187 and 198; 12000 fp32 297 and 161). 16 warps on an SM: 19.5 us for 8192 rows of 2048,
-// 5.2 TB/s.
+// and 137, though 16383 bf16 187 and 198; 12000 fp32 297 and 161). 16 warps on an SM:
+// 19.5 us for 8192 rows of 2048, 5.2 TB/s.
 struct GradPlan {
     int warps, lanes, blocks;
 };

@@ -178,9 +178,10 @@ __device__ __forceinline__ void write_balance(const BalanceArgs& a, int n, const
     }
 }
 
-// A row on LANES lanes, four experts in a row on each; a warp takes 32 / LANES rows at a time, ROWS times over with their reads in flight together. The blocks of
-// a cluster (CL) add up their sums in the order of their ranks; a cluster that is
-// alone writes the results, else each leaves one part.
+// A row on LANES lanes, four experts in a row on each; a warp takes 32 / LANES rows at
+// a time, ROWS times over with their reads in flight together. The blocks of a cluster
+// (CL) add up their sums in the order of their ranks; a cluster that is alone writes the
+// results, else each leaves one part.
 constexpr int kWarps = 8, kCluster = 8;
 // Blocks on an SM, by the probabilities that a lane holds.
 constexpr int resident(int held) { return held <= 20 ? 4 : held <= 24 ? 3 : 2; }
@@ -538,8 +539,8 @@ int balance_grad(int64_t T, int64_t E, int64_t top, const void* logits, int64_t 
     if (rc != kOk) return rc;
     const bool fours = in_fours(logits, E, ldl, dtype == GEMM_F32 ? 4 : 2) &&
                        in_fours(dlogits, E, ldd, os);
-    const BalanceGradArgs a{T, (int)E, (int)top, logits, ldl, fours, expert, counts, dloss, alpha, beta,
-                            dlogits, ldd};
+    const BalanceGradArgs a{T,      (int)E, (int)top, logits, ldl,  fours,   expert,
+                            counts, dloss,  alpha,    beta,   dlogits, ldd};
     const int each = kGradWarps * (E <= 256 ? 4 : 1);  // rows of a block at a time
     int64_t blocks = (T + each - 1) / each;
     const int64_t most = (int64_t)dev->sm_count * 8;
@@ -547,24 +548,16 @@ int balance_grad(int64_t T, int64_t E, int64_t top, const void* logits, int64_t 
     return with_lanes((int)E, [&](auto lanes, auto ne, auto rows) {
         constexpr int LANES = decltype(lanes)::value;
         constexpr int NE = decltype(ne)::value, ROWS = decltype(rows)::value;
-        const dim3 grid((unsigned)blocks), block(32 * kGradWarps);
+        auto run = [&](auto t, auto o) {
+            return launch_dependent(balance_grad_kernel<decltype(t), decltype(o), LANES, NE, ROWS>,
+                                    dim3((unsigned)blocks), dim3(32 * kGradWarps), 0, s, a);
+        };
         switch (dtype) {
-            case GEMM_F32:
-                return launch_dependent(balance_grad_kernel<float, float, LANES, NE, ROWS>, grid, block,
-                                        0, s, a);
-            case GEMM_F16_F32:
-                return launch_dependent(balance_grad_kernel<__half, float, LANES, NE, ROWS>, grid, block,
-                                        0, s, a);
-            case GEMM_BF16_F32:
-                return launch_dependent(balance_grad_kernel<__nv_bfloat16, float, LANES, NE, ROWS>, grid,
-                                        block, 0, s, a);
-            case GEMM_F16_F16:
-                return launch_dependent(balance_grad_kernel<__half, __half, LANES, NE, ROWS>, grid, block,
-                                        0, s, a);
-            default:
-                return launch_dependent(
-                    balance_grad_kernel<__nv_bfloat16, __nv_bfloat16, LANES, NE, ROWS>, grid, block, 0, s,
-                    a);
+            case GEMM_F32: return run(float{}, float{});
+            case GEMM_F16_F32: return run(__half{}, float{});
+            case GEMM_BF16_F32: return run(__nv_bfloat16{}, float{});
+            case GEMM_F16_F16: return run(__half{}, __half{});
+            default: return run(__nv_bfloat16{}, __nv_bfloat16{});
         }
     });
 }

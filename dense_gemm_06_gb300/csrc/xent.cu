@@ -8,9 +8,10 @@
 //   dX     = G W,                     dW = beta dW + G^T X
 //
 // Forward: the kernel of xent.cuh leaves a (maximum, sum of exponentials) pair
-// for every row and 128 columns (a half tile), which a second kernel joins:
-// exp(m_i - m) s_i summed over the pairs, the online softmax identity. The logits
-// are never stored, only 1/16 of their bytes.
+// for every row and half tile (128 columns by CTA pairs, 16 to 64 by single CTAs),
+// which a second kernel joins: exp(m_i - m) s_i summed over the pairs, the online
+// softmax identity. The logits are never stored, only 8 bytes for each pair: 1/64 of
+// fp32 logits by CTA pairs.
 //
 // Backward: piece by piece of the vocabulary the same kernel computes the logits
 // again and writes G as 16-bit numbers, which are multiplied with the piece's rows of
@@ -215,8 +216,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // Row t of dX = *scale * (the sum of row place[t] of `parts` matrices, part_rows rows
-// apart), rounded once, or zero; rows x cols. A warp takes 32 groups of 8 columns of two rows at a time, and stores
-// them in 16-byte pieces whatever dX's alignment.
+// apart), rounded once, or zero; rows x cols. A warp takes 32 groups of 8 columns of
+// two rows at a time, and stores them in 16-byte pieces whatever dX's alignment.
 template <typename T>
 __global__ void __launch_bounds__(256)
     xent_finish_kernel(const float* __restrict__ sum, int64_t lds, int parts, int64_t part_rows,
@@ -264,7 +265,8 @@ int finish(const float* sum, int64_t lds, int parts, int64_t part_rows, void* ou
     auto run = [&](auto t) {
         using T = decltype(t);
         return launch_dependent(xent_finish_kernel<T>, grid, dim3(256), 0, s, sum, lds, parts,
-                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, place, scale);
+                                part_rows, static_cast<T*>(out), ldo, rows, (int)cols, place,
+                                scale);
     };
     return bf16 ? run(__nv_bfloat16{}) : run(__half{});
 }

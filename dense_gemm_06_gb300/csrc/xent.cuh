@@ -24,13 +24,13 @@
 // and per element one maximum, one fma, one ex2 and one addition.
 //
 // The tensor core cuts off what an addition shifts below its last bits, so a long
-// sum of products drifts towards zero by about half a step for every 16 of depth:
-// losses of K = 2048 were off by 6e-6 of themselves, dX from 131072 columns by 8e-4. So an accumulator takes at
-// most kXentFold blocks of depth, and the epilogue warps add up those parts in
-// registers, rounded to nearest (128 numbers a thread; the warps that only issue
-// copies and MMAs hand over registers for them).  With K = 2048
-// these take about 1,100 of the 8,192 cycles that a tile's MMAs take, and they
-// run beside the next tile's MMAs: the tensor pipe bounds the kernel.
+// sum of products drifts towards zero by half a step to a step for every 16 of depth:
+// losses of K = 2048 were off by 6e-6 of themselves, dX from 131072 columns by 8e-4.
+// So an accumulator takes at most kXentFold blocks of depth, and the epilogue warps
+// add up those parts in registers, rounded to nearest (128 numbers a thread; the warps
+// that only issue copies and MMAs hand over registers for them). With K = 2048 these
+// take about 1,100 of the 8,192 cycles that a tile's MMAs take, and they run beside the
+// next tile's MMAs: the tensor pipe bounds the kernel.
 #pragma once
 
 #include <cuda.h>
@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(XTHREADS, 1) xent_kernel(const __grid_constant
                                                    : 0u;
                                 }
                             }
-                            const uint32_t dst = my_row + (uint32_t)(((h * 4 + u) ^ (lane & 7)) * 16);
+                            const uint32_t dst =
+                                my_row + (uint32_t)(((h * 4 + u) ^ (lane & 7)) * 16);
                             xent_sts128(dst, hi[0], hi[1], hi[2], hi[3]);
                             if constexpr (MODE == kXentGrad2)
                                 xent_sts128(dst + 32 * 128, lo[0], lo[1], lo[2], lo[3]);

@@ -126,8 +126,9 @@ def run_every():
                              lg.GEMM_F16_F32), "gemm_grouped")
     print("every: gemm_grouped with its repack, misaligned fp16", flush=True)
     # cross entropy: pairs; one CTA, shared depth of dX, scaled; unaligned; no depth
-    for M, N, K, bf16, f32, pad in ((600, 40000, 256, True, True, 0), (70, 1000, 256, False, False, 0),
-                                    (300, 1999, 129, True, False, 1), (300, 1000, 0, True, True, 0)):
+    for M, N, K, bf16, f32, pad in (
+            (600, 40000, 256, True, True, 0), (70, 1000, 256, False, False, 0),
+            (300, 1999, 129, True, False, 1), (300, 1000, 0, True, True, 0)):
         run_xent(M, N, K, bf16, f32, pad)()
         print(f"every: gemm_xent, gemm_xent_grad {M} x {N} x {K}", flush=True)
     for M, N, dtype in ((1, 512, lg.GEMM_F32), (300, 2048, lg.GEMM_BF16_F32),
@@ -207,7 +208,7 @@ def run_embed(M, V, K, dtype):
     ids = (torch.arange(M, device="cuda") * 7919 % V).int()
     ids[::3] = V // 2
     table, dy = _normal(V, K).to(it), _normal(M, K).to(it)
-    y, dtable = torch.empty(M, K, dtype=ot, device="cuda"), torch.empty(V, K, dtype=ot, device="cuda")
+    y, dtable = (torch.empty(n, K, dtype=ot, device="cuda") for n in (M, V))
 
     def call():
         lg.check(lg.embed_rows(M, V, K, ids, table, K, y, K, dtype), "embed_rows")

@@ -377,8 +377,10 @@ int gemm_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
  * negative, and gemm_check_device_error() then reports GEMM_ERR_INVALID_ARG. loss
  * and lse are DEVICE arrays of M floats; lse may be NULL, and is written for every
  * row. Types: the 16-bit dtypes (the result's type is not used; GEMM_F32 is
- * GEMM_ERR_UNSUPPORTED). Logits and sums are fp32; infinite or NaN logits make
- * their row's lse NaN. N is 1 .. 2^24, M at most 2^29 (more: GEMM_ERR_UNSUPPORTED).
+ * GEMM_ERR_UNSUPPORTED). Logits and sums are fp32. A logit of minus infinity has
+ * probability zero (a row of nothing else has lse minus infinity); one of plus
+ * infinity, or NaN, makes its row's lse NaN. N is 1 .. 2^24, M at most 2^29 (more:
+ * GEMM_ERR_UNSUPPORTED).
  * The rows' results do not depend on each other. Scratch: 16 bytes for each row and
  * 32 to 256 columns, for as many rows at a time as stay within 256 MB (256 at
  * least), and copies of X or W where their rows are not 16-byte aligned. M zero is a
@@ -396,11 +398,13 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  *     dX = G * W,   dW = beta * dW + G^T * X
  *
  * with G zero for rows that do not count; of them nothing but target is used (X,
- * lse and dloss may hold anything there), and most of their operations are left out. dloss is a DEVICE array of M floats, or
- * NULL for ones (the mean of M tokens: alpha = 1 / M). dX is M x K (lddx >= K) of
- * the operands' type, dW is N x K (lddw >= K) of the dtype's result type: fp32 for
- * master gradients, which beta = 1 accumulates over micro-batches, or 16-bit.
- * Either may be NULL. dX and dW overlap neither each other nor X and W.
+ * lse and dloss may hold anything there), and most of their operations are left out.
+ * dloss is a DEVICE array of M floats, or NULL for ones (the mean of M tokens: alpha =
+ * 1 / M). dX is M x K (lddx >= K) of the operands' type, dW is N x K (lddw >= K) of the
+ * dtype's result type: fp32 for master gradients, which beta = 1 accumulates over
+ * micro-batches, or 16-bit. Either may be NULL. dX and dW overlap neither each other
+ * nor X and W. An infinity in W makes dX NaN, also where its word's probability is
+ * zero, as G * W says.
  *
  * The logits are computed again, a piece of the vocabulary at a time. G is held as
  * 16-bit numbers, for an fp32 dW as two that leave 2^-17 (bf16) or 2^-22 (fp16) of
@@ -408,10 +412,10 @@ int gemm_xent(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
  * reaches down to 2^-36 of it), which is put back in fp32: a factor that all rows
  * share is not rounded. Probabilities below 2^-126 count as zero.
  * Sums are fp32, each result is rounded once. Scratch: G of a piece (512 MB, 1 GB
- * for an fp32 dW, or 4096 columns), a copy of X (two for an fp32 dW), 8 bytes a row, and an fp32 dX (a
- * few where dX is small). An fp32 dW with beta = 1 is added to as gemm_grouped_k's C. With M zero
- * dW = beta * dW; K zero is a no-op. K is at most 2^20 (more: GEMM_ERR_UNSUPPORTED).
- * Otherwise as gemm_xent.
+ * for an fp32 dW, or 4096 columns), a copy of X (two for an fp32 dW), 8 bytes a row,
+ * and an fp32 dX (a few where dX is small). An fp32 dW with beta = 1 is added to as
+ * gemm_grouped_k's C. With M zero dW = beta * dW; K zero is a no-op. K is at most 2^20
+ * (more: GEMM_ERR_UNSUPPORTED). Otherwise as gemm_xent.
  */
 int gemm_xent_grad(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                    const void *W, int64_t ldw, const int32_t *target, const float *lse,
@@ -474,7 +478,7 @@ int embed_rows(int64_t M, int64_t V, int64_t K, const int32_t *ids, const void *
  * lddt >= K). With beta = 1 only the rows that a token names are touched (an
  * embedding tied to gemm_xent's W adds to its dW this way); else the whole table is
  * written. ids as in embed_rows; dy of rows that do not count may hold anything.
- * Sums are fp32 in an order that M alone fixes, rounded once. Scratch: 32 bytes a
+ * Sums are fp32 in an order that ids alone fix, rounded once. Scratch: 32 bytes a
  * token, and 2 K floats for each 32 tokens (at most 8192 times). Otherwise as
  * embed_rows.
  */

@@ -52,14 +52,16 @@ CALLS = {
     "xent_grad fp32": xent_grad(3000, 9000, 512, 512, BF32, 1.0),
     "xent_grad dense": xent_grad(4096, 9000, 2048, 2048, BF),
     "xent_grad odd": xent_grad(300, 3000, 63, 63, lg.GEMM_F16_F32),
-    "xent_grad no rows": lambda: lg.gemm_xent_grad(0, 9, 8, P, 8, P, 8, P, P, P, P, 8, P, 8, BF, **S),
+    "xent_grad no rows": lambda: lg.gemm_xent_grad(0, 9, 8, P, 8, P, 8, P, P, P, P, 8, P, 8, BF,
+                                                   **S),
     "norm few": lambda: lg.layernorm_rows(3, 64, P, 64, P, P, 1e-5, P, 64, P, P, BF32, **S),
     "norm many": lambda: lg.layernorm_rows(9000, 2048, P, 2048, P, P, 1e-5, P, 2048, P, P, BF, **S),
-    "norm long": lambda: lg.layernorm_rows(3, 70001, P, 70001, P, P, 1e-5, P, 70001, P, P, F32, **S),
+    "norm long": lambda: lg.layernorm_rows(3, 70001, P, 70001, P, P, 1e-5, P, 70001, P, P, F32,
+                                           **S),
     "norm_grad": lambda: lg.layernorm_rows_grad(900, 2048, P, 2048, P, P, P, P, 2048, P, 2048, P, P,
                                                 F32, **S),
-    "norm_grad long": lambda: lg.layernorm_rows_grad(90, 20000, P, 20000, P, P, P, P, 20000, P, 20000,
-                                                     P, P, BF, **S),
+    "norm_grad long": lambda: lg.layernorm_rows_grad(90, 20000, P, 20000, P, P, P, P, 20000, P,
+                                                     20000, P, P, BF, **S),
     "embed": lambda: lg.embed_rows(90, 300, 64, P, P, 64, P, 64, BF, **S),
     "embed_grad": lambda: lg.embed_rows_grad(9000, 300, 64, P, P, 64, P, 64, BF32, **S),
     "balance few": lambda: lg.router_balance(9, 64, 2, P, 64, P, P, P, P, P, F32, **S),
@@ -73,7 +75,8 @@ CALLS = {
     "grouped": lambda: lg.gemm_grouped(4, 500, 200, 64, P, P, 64, P, 64, 12800, 0, P, 200, BF, **S),
     "grouped_k": grouped_k(BF), "grouped_k fp32": grouped_k(BF32),
     "lora": lambda: lg.gemm_lora(300, 200, 64, 3, 8, P, 64, P, 64, 0, P, P, P, P, P, 200, BF, **S),
-    "lora few": lambda: lg.gemm_lora(3, 200, 64, 3, 8, P, 64, P, 64, 0, P, P, P, P, P, 200, H16, **S),
+    "lora few": lambda: lg.gemm_lora(3, 200, 64, 3, 8, P, 64, P, 64, 0, P, P, P, P, P, 200, H16,
+                                     **S),
 }
 
 

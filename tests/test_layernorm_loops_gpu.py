@@ -28,7 +28,8 @@ def test_more_than_32_rows_a_block(M, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF32, H16, F32])
-@pytest.mark.parametrize("M,N", [(700, 8200), (700, 9001), (310, 16384), (310, 16383), (5200, 8200)])
+@pytest.mark.parametrize("M,N", [(700, 8200), (700, 9001), (310, 16384), (310, 16383),
+                                 (5200, 8200)])
 def test_32_warps_a_row(M, N, dtype):
     both(M, N, dtype)
     both(M, N, dtype, pads=(1, 0, 3), shifts=(0, 1, 0))

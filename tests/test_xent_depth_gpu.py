@@ -40,8 +40,8 @@ def test_dx_of_a_deep_vocabulary_does_not_drift(M, gone, dtype, lim):
     W += torch.rand(K, generator=g, device="cuda") * 0.4 + 0.1
     W[0] = 0
     W = W.to(IN[dtype])
-    X -= (X.double() @ W.double().mean(0) / W.double().mean(0).square().sum())[:, None].to(X.dtype) \
-        * W.double().mean(0).to(X.dtype)  # the common part of a row's logits out of the way
+    mean = W.double().mean(0)  # the common part of a row's logits out of the way:
+    X -= (X.double() @ mean / mean.square().sum())[:, None].to(X.dtype) * mean.to(X.dtype)
     target = torch.zeros(M, dtype=torch.int32, device="cuda")
     target[torch.rand(M, generator=g, device="cuda") < gone] = -1
     lse, dX = torch.empty(M, device="cuda"), torch.empty_like(X)
