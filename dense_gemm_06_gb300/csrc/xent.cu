@@ -383,7 +383,8 @@ int launch_sum(const XentSumPlan& plan, int64_t M, int64_t K, int64_t piece, int
 }
 
 // A piece's rows of a 16-bit dW (n x K) = factor G^T X, `rows` deep; dW's rows lie as
-// TMA wants them.
+// TMA wants them, and end on 16 bytes: a box that crosses the end of a row in the middle
+// of 16 bytes may be stored up to their end.
 int launch_table(int64_t n, int64_t K, int64_t rows, const void* g, int64_t ldg, const void* X,
                  int64_t ldx, void* dW, int64_t lddw, const float* factor, const XentInfo* info,
                  bool bf16, const DeviceInfo& dev, cudaStream_t s) {
@@ -588,7 +589,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const 
                             *dev, s);
         if (rc != kOk || !dW) continue;
         void* dst = static_cast<char*>(dW) + v0 * lddw * we;
-        rc = we == 2 && beta == 0.f && tma_ready(dW, lddw) && rows <= kXentTableRows
+        rc = we == 2 && beta == 0.f && tma_ready(dW, lddw) && K % 8 == 0 && rows <= kXentTableRows
                  ? launch_table(n, K, rows, g, ldg, xc, ldk, dst, lddw, scale + 1, info, bf16,
                                 *dev, s)
                  : product_rows(n, K, (int64_t)rows * parts, g, ldg, xc, ldk, dst, lddw, dtype,
