@@ -125,15 +125,18 @@ def run_every():
     lg.check(lg.gemm_grouped(2, 100, 65, 133, off, A, 133, W, 133, 65 * 133, 0, Y, 65,
                              lg.GEMM_F16_F32), "gemm_grouped")
     print("every: gemm_grouped with its repack, misaligned fp16", flush=True)
-    # cross entropy: pairs; one CTA, shared depth of dX, scaled; unaligned; no depth
+    # cross entropy: pairs; one CTA, shared depth of dX, scaled; unaligned; no depth; a
+    # 16-bit dW of many rows
     for M, N, K, bf16, f32, pad in (
             (600, 40000, 256, True, True, 0), (70, 1000, 256, False, False, 0),
-            (300, 1999, 129, True, False, 1), (300, 1000, 0, True, True, 0)):
+            (300, 1999, 129, True, False, 1), (300, 1000, 0, True, True, 0),
+            (16384, 1000, 256, True, False, 0)):
         run_xent(M, N, K, bf16, f32, pad)()
         print(f"every: gemm_xent, gemm_xent_grad {M} x {N} x {K}", flush=True)
     for M, N, dtype in ((1, 512, lg.GEMM_F32), (300, 2048, lg.GEMM_BF16_F32),
                         (5000, 1024, lg.GEMM_F16_F16), (20000, 1001, lg.GEMM_BF16_BF16),
-                        (40, 20000, lg.GEMM_BF16_F32), (40, 70001, lg.GEMM_F32)):
+                        (40, 9000, lg.GEMM_BF16_F32), (40, 20000, lg.GEMM_BF16_F32),
+                        (40, 70001, lg.GEMM_F32)):
         run_norm(M, N, dtype)()
         print(f"every: layernorm_rows, layernorm_rows_grad {M} x {N}", flush=True)
     for M, V, K, dtype in ((1, 1000, 64, lg.GEMM_BF16_BF16), (9000, 500, 256, lg.GEMM_F16_F32),
